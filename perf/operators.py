@@ -9,7 +9,7 @@ import torch
 
 own = False
 
-LOW, HIGH = -100, 120   # exponents a scale may take
+LOW, HIGH = -40, 60   # exponents a scale may take
 
 
 # ---- the cases ----
