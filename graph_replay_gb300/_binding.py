@@ -64,6 +64,31 @@ class dec_stats(ctypes.Structure):
                 ("kv_bytes", ctypes.c_int64)]
 
 
+class dec_kv8_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_void_p), ("rows", ctypes.c_int32),
+                ("pages_per_row", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32),
+                ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("scale_block", ctypes.c_int32),
+                ("device", ctypes.c_int32)]
+
+
+class dec_kv8_batch(ctypes.Structure):
+    _fields_ = [("q_start", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("err", ctypes.c_void_p),
+                ("total", ctypes.c_int32), ("max_new", ctypes.c_int32)]
+
+
+class dec_kv8_new(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_stride", ctypes.c_int64),
+                ("v_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class dec_kv8_attn(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("out", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("dtype", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+                ("window", ctypes.c_int32), ("sinks", ctypes.c_int32), ("scale", ctypes.c_double),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 # every symbol the header declares: (name, restype, argtypes)
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -90,6 +115,12 @@ _SIG = [
     ("dec_kv_ptr", ctypes.c_int, [_P, _I32, _I32, ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_size_t)]),
     ("dec_attention", ctypes.c_int, [_P, _I32, _P, _P, _P]),
     ("dec_attention_static", ctypes.c_int, [_P, _I32, _P, _P, _P]),
+    ("dec_kv8_append", ctypes.c_int, [ctypes.POINTER(dec_kv8_cache), ctypes.POINTER(dec_kv8_batch),
+                                      ctypes.POINTER(dec_kv8_new), _P]),
+    ("dec_kv8_attend", ctypes.c_int, [ctypes.POINTER(dec_kv8_cache), ctypes.POINTER(dec_kv8_batch),
+                                      ctypes.POINTER(dec_kv8_attn), _P]),
+    ("dec_kv8_workspace", ctypes.c_int, [ctypes.POINTER(dec_kv8_cache), ctypes.POINTER(dec_kv8_batch),
+                                         ctypes.POINTER(dec_kv8_attn), ctypes.POINTER(ctypes.c_size_t)]),
     ("dec_logits_ptr", ctypes.c_int, [_P, ctypes.POINTER(_P)]),
     ("dec_stream", ctypes.c_int, [_P, ctypes.POINTER(_P)]),
     ("dec_stats_get", ctypes.c_int, [_P, ctypes.POINTER(dec_stats)]),
@@ -260,6 +291,20 @@ def dec_attention(h, layer: int, qkv_ptr, pos_ptr, out_ptr) -> int:
 
 def dec_attention_static(h, layer: int, qkv_ptr, pos_ptr, out_ptr) -> int:
     return lib().dec_attention_static(h, layer, qkv_ptr, pos_ptr, out_ptr)
+
+
+def dec_kv8_append(cache: dec_kv8_cache, batch: dec_kv8_batch, new: dec_kv8_new, stream) -> None:
+    check(None, lib().dec_kv8_append(cache, batch, new, stream))
+
+
+def dec_kv8_attend(cache: dec_kv8_cache, batch: dec_kv8_batch, attn: dec_kv8_attn, stream) -> None:
+    check(None, lib().dec_kv8_attend(cache, batch, attn, stream))
+
+
+def dec_kv8_workspace(cache: dec_kv8_cache, batch: dec_kv8_batch, attn: dec_kv8_attn) -> int:
+    n = ctypes.c_size_t()
+    check(None, lib().dec_kv8_workspace(cache, batch, attn, ctypes.byref(n)))
+    return n.value
 
 
 def dec_logits_ptr(h) -> int:

@@ -29,7 +29,7 @@ using namespace gd;
 
 namespace {
 
-thread_local std::string g_init_msg;   // message of the last failed dec_init on this thread
+thread_local std::string g_init_msg;   // message of the last failed call without a handle on this thread
 
 constexpr int ST_READY = 0, ST_NEEDS_RESET = 1, ST_POISONED = 2;
 constexpr int MAX_ROWS = 8;
@@ -1369,6 +1369,7 @@ int engine_fail(dec_handle* h, int code, const char* msg) {
     return fail(h, code, "%s", msg);
 }
 int engine_device(const dec_handle* h) { return h->cfg.device; }
+void set_call_message(const char* msg) { g_init_msg = msg; }
 
 }  // namespace gd
 
@@ -1397,7 +1398,7 @@ int dec_set_timeout(dec_handle* h, int64_t wait_timeout_ms) {
     return DEC_OK;
 }
 
-// With a NULL handle: the message of the last failed dec_init on this thread.
+// With a NULL handle: the message of the last failed call without a handle (dec_init, dec_kv8_*) on this thread.
 const char* dec_last_error(const dec_handle* h) { return h ? h->msg.c_str() : g_init_msg.c_str(); }
 
 const char* dec_status_str(int s) {

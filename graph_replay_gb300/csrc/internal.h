@@ -270,6 +270,41 @@ void prefill_free(PrefillState* s);
 cudaError_t prefill_run(PrefillState* s, const int* tokens, int n, int pos0, int row, const int* pages, float* x_last,
                         cudaStream_t st);
 
+// ---------------- the 8-bit K/V cache (kv8*.cu) ----------------
+struct Kv8Cache {              // a dec_kv8_cache that passed its checks
+    uint8_t *k, *v;            // [num_pages, Hkv, page, hd] e4m3
+    uint8_t *ks, *vs;          // [num_pages, Hkv, page / block] exponent + 127
+    const int* pages;          // [rows, ppr] or null: row r owns pages r * ppr ..
+    int rows, ppr, page, num_pages, Hkv, hd, block;
+};
+struct Kv8Batch {
+    const int* q_start;        // [rows + 1] or null: one token a row
+    const int* kv_len;         // [rows]
+    int total, max_new;
+    unsigned* err;
+};
+struct Kv8Append {
+    Kv8Cache c;
+    Kv8Batch b;
+    const void *k, *v;         // [total, Hkv, hd], token strides below (elements)
+    long long k_stride, v_stride;
+    int dtype;                 // W_F32 / W_BF16
+};
+struct Kv8Attend {
+    Kv8Cache c;
+    Kv8Batch b;
+    const void* q;             // [total, Hq, hd]
+    void* out;                 // [total, Hq, hd]
+    long long q_stride, out_stride;
+    int dtype, Hq;
+    int window, sinks;         // window INT_MAX: every position up to the token's own
+    float scale;
+    float* ws;                 // kv8_attend_floats() floats
+};
+cudaError_t kv8_append_launch(const Kv8Append& p, cudaStream_t s);
+cudaError_t kv8_attend_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
+size_t kv8_attend_floats(const Kv8Attend& p, int num_sms);
+
 }  // namespace gd
 
 struct dec_handle;
@@ -281,5 +316,7 @@ void engine_attention_scratch(const dec_handle* h, size_t* part_floats, size_t* 
 int engine_gate(dec_handle* h);
 int engine_fail(dec_handle* h, int code, const char* msg);
 int engine_device(const dec_handle* h);
+// the message that dec_last_error(NULL) gives on this thread
+void set_call_message(const char* msg);
 
 }  // namespace gd

@@ -1,0 +1,117 @@
+"""The 8-bit K/V cache on torch tensors: e4m3 values with a power-of-two scale
+for each block of positions and K/V head (graphdec.h, "The 8-bit K/V cache").
+
+    cache = KV8Cache.empty(rows, cap, n_kv_heads, head_dim)
+    cache.append(k, v, kv_len)                     # one new token for each row
+    out = cache.attend(q, kv_len, window=4096, sinks=4)
+
+Both calls launch on torch's current stream and return at once; nothing reads
+back to the host.  ``check`` does, and raises if a call met an entry of
+``kv_len``, ``q_start`` or the page table that is out of range.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+
+from . import _binding as B
+
+_DT = {torch.float32: B.DEC_DTYPE_F32, torch.bfloat16: B.DEC_DTYPE_BF16}
+
+
+class KV8Cache:
+    """k, v: uint8 or float8_e4m3fn [num_pages, n_kv_heads, page_size, head_dim];
+    k_scale, v_scale: uint8 or float8_e8m0fnu [num_pages, n_kv_heads, page_size / scale_block];
+    page_table: int32 [rows, pages_per_row], or None: `rows` rows of equally many pages, in order."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 page_table: Optional[torch.Tensor] = None, rows: int = 0):
+        for t in (k, v, k_scale, v_scale) + (() if page_table is None else (page_table,)):
+            if not t.is_cuda or not t.is_contiguous() or t.device != k.device:
+                raise ValueError("KV8Cache: contiguous CUDA tensors on one device")
+        if k.dim() != 4 or k.shape != v.shape or k.dtype not in (torch.uint8, torch.float8_e4m3fn) or v.dtype != k.dtype:
+            raise ValueError("KV8Cache: k and v are e4m3 bytes [num_pages, n_kv_heads, page_size, head_dim]")
+        pages, heads, page, dim = k.shape
+        if (k_scale.dim() != 3 or k_scale.shape != v_scale.shape or k_scale.element_size() != 1
+                or v_scale.element_size() != 1 or k_scale.shape[:2] != k.shape[:2] or k_scale.shape[2] < 1
+                or page % k_scale.shape[2]):
+            raise ValueError("KV8Cache: scales are bytes [num_pages, n_kv_heads, page_size / scale_block]")
+        if page_table is None:
+            if rows < 1 or pages % rows:
+                raise ValueError("KV8Cache: without a page table, rows must divide num_pages")
+            per_row = pages // rows
+        else:
+            if page_table.dim() != 2 or page_table.dtype != torch.int32:
+                raise ValueError("KV8Cache: page_table is int32 [rows, pages_per_row]")
+            rows, per_row = page_table.shape
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self.rows, self.cap, self.n_kv_heads, self.head_dim = rows, per_row * page, heads, dim
+        self.page_size, self.scale_block = page, page // k_scale.shape[2]
+        self.device = k.device
+        self._err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self._c = B.dec_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                  None if page_table is None else page_table.data_ptr(), rows, per_row, page, pages,
+                                  heads, dim, self.scale_block, k.device.index)
+
+    @classmethod
+    def empty(cls, rows: int, cap: int, n_kv_heads: int, head_dim: int, scale_block: int = 64,
+              device="cuda") -> "KV8Cache":
+        """An empty contiguous cache of `cap` positions (a multiple of scale_block) for each row."""
+        k = torch.zeros(rows, n_kv_heads, cap, head_dim, dtype=torch.uint8, device=device)
+        s = torch.full((rows, n_kv_heads, cap // scale_block), 127, dtype=torch.uint8, device=device)
+        return cls(k, torch.zeros_like(k), s, s.clone(), rows=rows)
+
+    def _batch(self, kv_len, q_start, total, max_new):
+        for t in (kv_len,) if q_start is None else (kv_len, q_start):
+            if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous():
+                raise ValueError("KV8Cache: kv_len and q_start are contiguous int32 tensors on the cache's device")
+        if kv_len.numel() != self.rows or (q_start is not None and q_start.numel() != self.rows + 1):
+            raise ValueError("KV8Cache: kv_len has rows entries, q_start rows + 1")
+        return B.dec_kv8_batch(None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(),
+                               self._err.data_ptr(), total, max_new)
+
+    def _tokens(self, what, t, heads):
+        if (t.dim() != 3 or t.dtype not in _DT or t.device != self.device or t.shape[2] != self.head_dim
+                or (heads and t.shape[1] != heads) or t.stride(2) != 1 or t.stride(1) != self.head_dim):
+            raise ValueError(f"KV8Cache: {what} is f32 or bf16 [tokens, heads, head_dim], heads side by side, on the "
+                             "cache's device")
+        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor, q_start: Optional[torch.Tensor] = None,
+               max_new: int = 1) -> None:
+        """Store new K and V [tokens, n_kv_heads, head_dim].  kv_len [rows] counts each row's positions, these
+        tokens included; q_start [rows + 1] gives each row its packed tokens (None: one each), at most max_new."""
+        if k.shape != v.shape or k.dtype != v.dtype:
+            raise ValueError("KV8Cache: k and v have one shape and type")
+        ks, vs = self._tokens("k", k, self.n_kv_heads), self._tokens("v", v, self.n_kv_heads)
+        b = self._batch(kv_len, q_start, k.shape[0], max_new)
+        n = B.dec_kv8_new(k.data_ptr(), v.data_ptr(), ks, vs, _DT[k.dtype], 0)
+        B.dec_kv8_append(self._c, b, n, torch.cuda.current_stream(self.device).cuda_stream)
+
+    def attend(self, q: torch.Tensor, kv_len: torch.Tensor, q_start: Optional[torch.Tensor] = None, max_new: int = 1,
+               window: int = 0, sinks: int = 0, scale: float = 0.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+        """Attention of q [tokens, n_heads, head_dim] over the cache, causal; with a window each token sees its last
+        `window` positions (its own among them) and the first `sinks`.  scale 0: 1 / sqrt(head_dim).  Returns `out`
+        (allocated like q if None); packed tokens that belong to no row are not written."""
+        qs = self._tokens("q", q, 0)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        elif out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("KV8Cache: out has q's shape and type")
+        os_ = self._tokens("out", out, 0)
+        b = self._batch(kv_len, q_start, q.shape[0], max_new)
+        a = B.dec_kv8_attn(q.data_ptr(), out.data_ptr(), qs, os_, _DT[q.dtype], q.shape[1], window, sinks, scale, None, 0)
+        need = B.dec_kv8_workspace(self._c, b, a)
+        if need:   # from torch's allocator on this stream: calls on other streams, and graphs, have their own
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            a.workspace, a.workspace_bytes = ws.data_ptr(), need
+        B.dec_kv8_attend(self._c, b, a, torch.cuda.current_stream(self.device).cuda_stream)
+        return out
+
+    def check(self) -> None:
+        """Wait for the calls so far and raise DecError if one met an entry out of range since the last check."""
+        bits = int(self._err.item())
+        if bits:
+            self._err.zero_()
+            raise B.DecError(B.DEC_E_DEVICE_FAULT, f"8-bit K/V cache: an entry out of range (error word 0x{bits:x})")

@@ -17,7 +17,8 @@
  *   - Every call returns an int status (dec_status); DEC_OK == 0.  After a
  *     failure, dec_last_error() returns a NUL-terminated message owned by the
  *     handle (valid until the next call on that handle); dec_last_error(NULL)
- *     gives the message of the last failed dec_init on the calling thread.
+ *     gives the message of the last failed call without a handle (dec_init,
+ *     dec_kv8_*) on the calling thread.
  *   - Pointers marked "device" are CUDA device addresses on the handle's GPU;
  *     "host" pointers are ordinary (pageable or pinned) host memory.  The
  *     library never frees memory it did not allocate.
@@ -435,6 +436,106 @@ int dec_attention(dec_handle *h, int32_t layer, const float *qkv, const int32_t 
  * for the life of the process; a cudaDeviceReset invalidates it together with
  * every handle); make that first call before any stream capture. */
 int dec_attention_static(dec_handle *h, int32_t layer, const float *qkv, const int32_t *pos, float *out);
+
+/* ---- The 8-bit K/V cache ----
+ * K and V of a batch of sequences in e4m3 (one byte a value: half of bf16's
+ * bytes to hold and to read), with one power-of-two scale for each block of
+ * scale_block consecutive positions of one K/V head.  A stored byte x8 in a
+ * block with scale byte s stands for x8 * 2^(s - 127); scale bytes that
+ * dec_kv8_append writes lie in [87, 187].
+ *
+ * These calls stand beside dec_attention for callers who keep their own cache.
+ * They take no handle, only launch kernels on the caller's stream (NULL: the
+ * legacy default stream), neither wait nor allocate, and may be recorded into
+ * a graph; lengths, page table and token ranges are read from device memory
+ * when the kernels run, so one recorded graph serves every step.  The current
+ * device is put back before they return.  Messages: dec_last_error(NULL).
+ *
+ * Layout: the pools are [num_pages, n_kv_heads, page_size, head_dim] like the
+ * paged K/V of a capture; position j of row r lies in page
+ * pages[r * pages_per_row + j / page_size] at j % page_size (pages = NULL: in
+ * page r * pages_per_row + j / page_size, the contiguous layout).  Rows may
+ * share pages that no append writes to.  K is stored as the caller gives it
+ * (rotated by RoPE already).
+ *   head_dim     64 or 128           scale_block  16, 32, 64 or 128
+ *   page_size    a multiple of scale_block
+ *   rows         1 .. 1024; pages_per_row * page_size <= 2^30 */
+typedef struct dec_kv8_cache {
+    void *k, *v;                 /* device, 16-byte aligned: e4m3 pools */
+    uint8_t *k_scale, *v_scale;  /* device: [num_pages, n_kv_heads, page_size / scale_block] */
+    const int32_t *pages;        /* device [rows, pages_per_row], or NULL */
+    int32_t rows, pages_per_row, page_size, num_pages, n_kv_heads, head_dim, scale_block;
+    int32_t device;              /* CUDA device ordinal of all of it */
+} dec_kv8_cache;
+
+/* Which tokens a call works on.  Tokens of all rows are packed: row r has the
+ * n = q_start[r + 1] - q_start[r] tokens from q_start[r] on, at the positions
+ * kv_len[r] - n .. kv_len[r] - 1.  Rows may have none.  A token whose position
+ * is negative (kv_len[r] < n: an idle row of a padded batch has kv_len 0) is
+ * not stored and sees nothing.  Packed tokens that belong to no row are left
+ * as they are.
+ * A row with q_start or kv_len out of range (not 0 <= q_start[r] <= q_start[r+1]
+ * <= total, more than max_new tokens, kv_len outside [0, pages_per_row *
+ * page_size]) sets DEC_FAULT_POS in *err and is skipped whole; a page id that
+ * is needed and outside [0, num_pages) sets DEC_FAULT_SLOT_MAP, and the page
+ * counts as holding nothing. */
+typedef struct dec_kv8_batch {
+    const int32_t *q_start;      /* device [rows + 1], or NULL: one token for each row */
+    const int32_t *kv_len;       /* device [rows]: positions of each row, this call's tokens included */
+    uint32_t *err;               /* device: DEC_FAULT_* bits are added, never cleared */
+    int32_t total;               /* packed tokens */
+    int32_t max_new;             /* the most tokens of one row (sizes the launch) */
+} dec_kv8_batch;
+
+/* New K and V: [total, n_kv_heads, head_dim], heads side by side, tokens any
+ * stride apart (elements; a multiple of 16 bytes): views into a packed QKV
+ * matrix need no copy. */
+typedef struct dec_kv8_new {
+    const void *k, *v;           /* device, 16-byte aligned */
+    int64_t k_stride, v_stride;
+    int32_t dtype;               /* dec_dtype of k and v */
+    int32_t reserved;            /* 0 */
+} dec_kv8_new;
+
+/* Store the batch's new K and V.  Each block that new tokens enter takes the
+ * least exponent e with max |x| <= 448 * 2^e over its new finite values (at
+ * least -40; at least the block's own if it holds earlier positions of the
+ * row), and x is stored as e4m3(x * 2^-e), round to nearest even.  If e grew,
+ * the block's earlier positions are rounded again at the new exponent.  NaN,
+ * infinities and values over 448 * 2^60 are stored as NaN.  Positions behind
+ * the row's end are left as they are; storing a position again (a rejected
+ * draft) replaces it.  Two rows must not store into the same block in a call.
+ * Results do not depend on scheduling. */
+int dec_kv8_append(const dec_kv8_cache *cache, const dec_kv8_batch *batch, const dec_kv8_new *tokens, void *stream);
+
+/* Attention of the batch's tokens over the cache (their own K and V stored
+ * before): out = sum_j softmax_j(scale * q . k_j) v_j over the positions j that
+ * the token at position i sees: j <= i and, with a window, j > i - window or
+ * j < sinks.  A token that sees nothing gets zeros.  Query head a reads K/V
+ * head a / (n_heads / n_kv_heads).  What a token does not see never reaches its
+ * result, whatever bits it holds; a NaN that it sees does.  Scores, weights and
+ * sums are held in fp32; with fp32 q the products are exact to about 2^-20, with
+ * bf16 q the softmax weights are rounded to f16 (2^-11), finer than the result.
+ * Results do not depend on scheduling. */
+typedef struct dec_kv8_attn {
+    const void *q;               /* device [total, n_heads, head_dim], 16-byte aligned */
+    void *out;                   /* device, the same shape and type; may not overlap q */
+    int64_t q_stride, out_stride;   /* elements between tokens; a multiple of 16 bytes */
+    int32_t dtype;               /* dec_dtype of q and out */
+    int32_t n_heads;             /* n_heads / n_kv_heads <= 128 */
+    int32_t window;              /* 0: none */
+    int32_t sinks;               /* first positions that stay visible (with a window) */
+    double scale;                /* 0: 1 / sqrt(head_dim) */
+    void *workspace;             /* device, 16-byte aligned, dec_kv8_workspace bytes; its contents mean nothing
+                                    between calls, but calls that may overlap on the GPU need one each */
+    size_t workspace_bytes;
+} dec_kv8_attn;
+
+int dec_kv8_attend(const dec_kv8_cache *cache, const dec_kv8_batch *batch, const dec_kv8_attn *attn, void *stream);
+
+/* Bytes of workspace that dec_kv8_attend needs for these arguments (*bytes,
+ * host; may be 0).  Reads sizes only: the same for every content. */
+int dec_kv8_workspace(const dec_kv8_cache *cache, const dec_kv8_batch *batch, const dec_kv8_attn *attn, size_t *bytes);
 
 /* Device address of the logits [rows, vocab] fp32 of the last step. */
 int dec_logits_ptr(dec_handle *h, float **ptr);
