@@ -47,9 +47,10 @@ __global__ void k_kv8_attend(const Kv8Attend p) {
 
 }  // namespace
 
-size_t kv8_attend_floats(const Kv8Attend&, int) { return 0; }
+size_t kv8_attend_floats(const Kv8Attend& p, int num_sms) { return kv8_decode_takes(p) ? kv8_decode_floats(p, num_sms) : 0; }
 
-cudaError_t kv8_attend_launch(const Kv8Attend& p, int, cudaStream_t s) {
+cudaError_t kv8_attend_launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
+    if (kv8_decode_takes(p)) return kv8_decode_launch(p, num_sms, s);
     const int blocks = (p.b.total * p.Hq + 3) / 4;
     if (p.dtype == W_BF16) k_kv8_attend<__nv_bfloat16><<<blocks, 128, 0, s>>>(p);
     else k_kv8_attend<float><<<blocks, 128, 0, s>>>(p);

@@ -1,0 +1,594 @@
+// kv8_decode.cu -- attention over the 8-bit K/V cache for single tokens (and for
+// the few tokens of a draft): up to 16 query rows (tokens x the query heads of a
+// K/V head) against one K/V head of one sequence.
+//
+// Bound: the bytes of the visible K and V, each read once.  Everything else has
+// to hide behind that stream, so
+//   * K and V go from global memory straight into registers, in the order in
+//     which the tensor core wants them.  Both products keep the cache as the A
+//     operand of mma.m16n8k16 (S^T = K Q^T, O^T = V^T P^T), so the few query
+//     rows fill the N = 8 side and no accumulator row is wasted.  The sum over
+//     dims may run in any order: lane (g, t) of a warp reads 16 consecutive
+//     bytes of key g and uses them as its operand words, q is laid out to match;
+//     for V a lane reads a run of dims of its four keys and pairs the keys' bytes
+//     with byte permutes.  No shared memory, no transposing load;
+//   * e4m3 converts to f16 exactly and in pairs; the scales stay outside the
+//     products: K's exponent multiplies the 16-key score tile, V's is added to
+//     the exponent of the weights.  M is the running maximum of
+//     score * log2(e) + V's exponent: the weight of the largest contribution
+//     is 1 whatever the scales are, and the sum of the softmax gets
+//     weight * 2^-(V's exponent);
+//   * q enters as two f16 parts (22 bits; exact for bf16, whose second part is
+//     not multiplied); with fp32 q the weights enter as two f16 parts too;
+//   * the maximum is kept within a factor 2^8 of the true one (weights are
+//     scaled by 2^6, f16 holds 2^14), so a 16-key step needs one vote and
+//     almost never a reduction or a rescaling;
+//   * work: the visible 64-key tiles of all rows and K/V heads, in one line, cut
+//     into equal pieces: one for each resident CTA, whatever the lengths are.
+//     Windows make gaps in a row's tiles that are never touched.  A (row, head)
+//     that is cut leaves partial results, which a second kernel joins in order.
+#include <limits.h>
+#include "kv8.cuh"
+
+namespace gd {
+
+namespace {
+
+constexpr int KD_THREADS = 128, KD_WARPS = 4;
+constexpr int KD_TILE = 64;           // positions of a unit of work: 16 for each warp
+constexpr float KD_SLACK = 8.f;       // how far the maximum may lag (log2)
+constexpr float KD_SHIFT = 6.f;       // weights carry 2^6
+constexpr int KD_MAX_ROWS = 1024;       // as the C ABI allows
+
+// The tiles of a row: its first `sink` tiles, then `gap` tiles that no token
+// sees, then the rest; n of them are visible to one of its tokens.
+struct KdTiles {
+    int n, sink, gap;
+};
+__device__ __forceinline__ KdTiles kd_tiles(const Kv8Row& row, int window, int sinks) {
+    if (row.n == 0) return KdTiles{0, 0, 0};
+    const int end = (row.len + KD_TILE - 1) / KD_TILE;
+    const int first = max(row.len - row.n, 0);
+    const int low = (int)max((long long)first - window + 1, 0ll) / KD_TILE;   // the first token's window begins here
+    const int sink = (min(sinks, row.len) + KD_TILE - 1) / KD_TILE;
+    if (sink >= low) return KdTiles{max(end, 1), end, 0};   // a row without positions has one tile with nothing in it
+    return KdTiles{sink + end - low, sink, low - sink};
+}
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// where the pieces of work lie: pre[r] = tiles of the rows before r
+struct KdPlan {
+    int pre[KD_MAX_ROWS + 1];
+    int warp_sum[KD_WARPS];
+};
+__device__ __forceinline__ void kd_plan(const Kv8Attend& p, KdPlan& s) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = p.c.rows, cap = p.c.ppr * p.c.page;
+    const int per = (rows + KD_THREADS - 1) / KD_THREADS, r0 = min(tid * per, rows), r1 = min(r0 + per, rows);
+    int sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        Kv8Row row;
+        s.pre[r] = sum;
+        if (kv8_row(p.b, cap, r, &row)) sum += kd_tiles(row, p.window, p.sinks).n;
+    }
+    int inc = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+    }
+    if (lane == 31) s.warp_sum[warp] = inc;
+    __syncthreads();
+    int before = inc - sum;
+    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
+    for (int r = r0; r < r1; ++r) s.pre[r] += before;
+    if (tid == KD_THREADS - 1) s.pre[rows] = before + sum;
+    __syncthreads();
+}
+// of n pieces, piece c takes the units [begin(c), begin(c + 1)); a piece has at
+// least two tiles where the grid allows it, so short rows are not cut to crumbs
+__device__ __forceinline__ int kd_pieces(long long units, int grid) {
+    return (int)min((long long)grid, max((units + 1) / 2, 1ll));
+}
+__device__ __forceinline__ long long kd_begin(long long units, int pieces, int c) { return units * c / pieces; }
+__device__ __forceinline__ int kd_piece_of(long long units, int pieces, long long u) {
+    int c = (int)(u * pieces / units);
+    while (c + 1 < pieces && kd_begin(units, pieces, c + 1) <= u) ++c;
+    while (c > 0 && kd_begin(units, pieces, c) > u) --c;
+    return c;
+}
+template <int HD, int MT>
+__host__ __device__ constexpr int kd_slot_floats() { return MT * 8 * (HD + 2); }   // O, then M, then l of each query row
+
+// the 16 positions of one step as they came from memory
+template <int HD>
+struct KdStep {
+    uint4 k[2][HD / 64];   // keys g, g + 8: 16 dims from 16 t + 64 j
+    uint32_t v[4][HD / 32];   // keys 2t, 2t + 1, 2t + 8, 2t + 9: HD / 8 dims from g * HD / 8
+    int ke, ve;            // scale bytes
+};
+
+// MT: query rows / 8 (up).  FINE: fp32 q -- second f16 parts of q and of the weights.
+template <int HD, int MT, bool FINE>
+__global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(const Kv8Attend p) {
+    using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
+    constexpr int NK = HD / 16;   // 16-dim steps of S, 16-dim tiles of O
+    constexpr int PARTS = FINE ? 2 : 1;
+    __shared__ KdPlan plan;
+    __shared__ __align__(16) float o_s[KD_WARPS][MT * 8][HD];   // read and written as vectors
+    __shared__ float m_s[KD_WARPS][MT * 8], l_s[KD_WARPS][MT * 8];
+    __shared__ __align__(16) uint4 q_s[PARTS][MT][NK / 2][32];   // f16 parts of q, by step and lane
+    __shared__ float fac_s[MT * 8];
+    __shared__ uint32_t nan_s[KD_WARPS][HD];
+    pdl_wait();
+    pdl_trigger();
+    const Kv8Cache& c = p.c;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int G = p.Hq / c.Hkv, cap = c.ppr * c.page, nb = c.page / c.block;
+    kd_plan(p, plan);
+    const long long units = (long long)plan.pre[c.rows] * c.Hkv;
+    const int pieces = kd_pieces(units, gridDim.x);
+    if ((int)blockIdx.x >= pieces) return;
+    const long long u_end = kd_begin(units, pieces, blockIdx.x + 1);
+    const long long u_begin = kd_begin(units, pieces, blockIdx.x);
+
+    for (long long u = u_begin; u < u_end;) {
+        // the row of unit u: the last r with pre[r] * Hkv <= u
+        int r = 0;
+        {
+            int hi = c.rows;
+            while (r + 1 < hi) {
+                const int mid = (r + hi) >> 1;
+                if ((long long)plan.pre[mid] * c.Hkv <= u) r = mid;
+                else hi = mid;
+            }
+        }
+        Kv8Row row;
+        kv8_row(p.b, cap, r, &row);
+        const KdTiles tl = kd_tiles(row, p.window, p.sinks);
+        const long long u_row = (long long)plan.pre[r] * c.Hkv;
+        const int h = (int)((u - u_row) / tl.n), i0 = (int)((u - u_row) % tl.n);
+        const int i1 = (int)min((long long)tl.n, i0 + (u_end - u));
+        const int nq = row.n * G, p0 = row.len - row.n;   // query rows, the first token's position
+
+        const int end = min(row.len, p0 + row.n);
+        const int low = (int)max((long long)max(p0, 0) - p.window + 1, 0ll);   // no token of the row sees [sinks, low)
+        auto key0 = [&](int i) { return (i < tl.sink ? i : i + tl.gap) * KD_TILE + warp * 16; };
+        auto wanted = [&](int kb) { return kb < end && (kb + 15 >= low || kb < p.sinks); };
+        int page_ids = 0;   // lane L: the page of this warp's step in tile (i & ~31) + L, or -1
+        auto fetch_pages = [&](int i) {
+            const int ii = (i & ~31) + lane;
+            page_ids = -1;
+            if (ii >= i0 && ii < i1) {
+                const int kb = key0(ii);
+                if (wanted(kb)) page_ids = kv8_page(c, p.b.err, r, kb / c.page);
+            }
+        };
+        auto load = [&](int i, KdStep<HD>& s) -> bool {
+            if ((i & 31) == 0 || i == i0) fetch_pages(i);
+            const int page = __shfl_sync(0xffffffffu, page_ids, i & 31);
+            if (page < 0) return false;
+            const int kb = key0(i), off = kb % c.page;
+            const size_t head = (size_t)page * c.Hkv + h;
+            const uint8_t* kp = c.k + (head * c.page + off) * HD + g * HD + t * 16;
+            const uint8_t* vp = c.v + (head * c.page + off) * HD + 2 * t * HD + g * (HD / 8);
+#pragma unroll
+            for (int j = 0; j < HD / 64; ++j) {
+                s.k[0][j] = ld_stream16(kp + j * 64);
+                s.k[1][j] = ld_stream16(kp + 8 * HD + j * 64);
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const uint8_t* vx = vp + ((x & 1) + (x >> 1) * 8) * HD;
+                if constexpr (HD == 128) {
+                    const uint4 w = ld_stream16(vx);
+                    s.v[x][0] = w.x; s.v[x][1] = w.y; s.v[x][2] = w.z; s.v[x][3] = w.w;
+                } else {
+                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(vx));
+                    s.v[x][0] = w.x; s.v[x][1] = w.y;
+                }
+            }
+            s.ke = c.ks[head * nb + off / c.block];
+            s.ve = c.vs[head * nb + off / c.block];
+            return true;
+        };
+        KdStep<HD> s0, s1;
+        bool have0 = load(i0, s0), have1 = false;   // in flight while q is laid out
+
+        // q as B operand: warp a lays out the query rows a * 8 + g of this K/V head
+        float fac[MT][2];   // scale * log2(e) / q's power of two, of query rows 2t and 2t + 1
+        int pos[MT][2];     // their positions (-1: no such row, or before the sequence)
+        if (warp < MT) {
+            const int m = warp * 8 + g;
+            float x[NK * 4];
+            float top = 0.f;
+            if (m < nq) {
+                const T* src = static_cast<const T*>(p.q) + (row.t0 + m / G) * p.q_stride + (h * G + m % G) * HD + t * 16;
+#pragma unroll
+                for (int j = 0; j < HD / 64; ++j)
+#pragma unroll
+                    for (int v = 0; v < 16; v += Elem<T>::VEC) {
+                        float f[Elem<T>::VEC];
+                        Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(src + j * 64 + v)), f);
+#pragma unroll
+                        for (int e = 0; e < Elem<T>::VEC; ++e) x[j * 16 + v + e] = f[e];
+                    }
+            } else {
+#pragma unroll
+                for (int e = 0; e < NK * 4; ++e) x[e] = 0.f;
+            }
+#pragma unroll
+            for (int e = 0; e < NK * 4; ++e) top = fmaxf(top, fabsf(x[e]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            // a power of two that brings the row's largest value to [2^14, 2^15)
+            const int ex = min(max(268 - (int)(__float_as_uint(top) >> 23), 1), 254);
+            const float up = __int_as_float(ex << 23);
+#pragma unroll
+            for (int k = 0; k < NK; k += 2) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    const float x0 = x[k * 4 + b * 2] * up, x1 = x[k * 4 + b * 2 + 1] * up;
+                    hi[b] = pack_f16x2(x0, x1);
+                    const float2 f = unpack_f16x2(hi[b]);
+                    lo[b] = pack_f16x2(x0 - f.x, x1 - f.y);
+                }
+                q_s[0][warp][k / 2][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                if constexpr (FINE) q_s[1][warp][k / 2][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
+            if (t == 0) fac_s[m] = p.scale * KV8_LOG2E / up;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+                const int mq = a * 8 + 2 * t + b;
+                fac[a][b] = fac_s[mq];
+                pos[a][b] = mq < nq ? p0 + mq / G : -1;
+            }
+
+        float o[MT][NK][4], M[MT][2], l[MT][2];
+#pragma unroll
+        for (int a = 0; a < MT; ++a) {
+#pragma unroll
+            for (int k = 0; k < NK; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[a][k][e] = 0.f;
+            M[a][0] = M[a][1] = -INFINITY;
+            l[a][0] = l[a][1] = 0.f;
+        }
+
+        auto compute = [&](int i, KdStep<HD>& s) {
+            const int kb = key0(i);
+            // S^T: rows keys g, g + 8; columns query rows 2t, 2t + 1
+            float sc[MT][4];
+#pragma unroll
+            for (int a = 0; a < MT; ++a) sc[a][0] = sc[a][1] = sc[a][2] = sc[a][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < HD / 64; ++j) {
+                const uint32_t w0[4] = {s.k[0][j].x, s.k[0][j].y, s.k[0][j].z, s.k[0][j].w};
+                const uint32_t w1[4] = {s.k[1][j].x, s.k[1][j].y, s.k[1][j].z, s.k[1][j].w};
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+                    e4m3x4_to_f16(w0[e], a0, a2);
+                    e4m3x4_to_f16(w1[e], a1, a3);
+                    e4m3x4_to_f16(w0[e + 1], c0, c2);
+                    e4m3x4_to_f16(w1[e + 1], c1, c3);
+#pragma unroll
+                    for (int a = 0; a < MT; ++a)
+#pragma unroll
+                        for (int f = 0; f < PARTS; ++f) {
+                            const uint4 q = q_s[f][a][(j * 4 + e) / 2][lane];
+                            mma_f16(sc[a], a0, a1, a2, a3, q.x, q.y);
+                            mma_f16(sc[a], c0, c1, c2, c3, q.z, q.w);
+                        }
+                }
+            }
+            const float kf = pow2i(s.ke - 127), ve = (float)(s.ve - 127), vinv = pow2i(127 - s.ve);
+            // positions every token of the row sees need no mask
+            const bool all = kb + 15 <= p0 && (kb + 15 < p.sinks || kb > row.len - 1 - p.window);
+            bool grew = false;
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int b = e & 1, j = kb + g + (e >> 1) * 8;
+                    sc[a][e] = fmaf(sc[a][e], fac[a][b] * kf, ve);
+                    if (!all && !(pos[a][b] >= 0 && kv8_sees(pos[a][b], j, p.window, p.sinks))) sc[a][e] = -INFINITY;
+                    grew |= sc[a][e] > M[a][b] + KD_SLACK;
+                }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        float m = fmaxf(sc[a][b], sc[a][b + 2]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                        m = fmaxf(m, M[a][b]);
+                        const float f = M[a][b] == m ? 1.f : kv8_exp2(M[a][b] - m);   // -inf: 0
+                        M[a][b] = m;
+                        l[a][b] *= f;
+#pragma unroll
+                        for (int k = 0; k < NK; ++k) {
+                            o[a][k][b] *= f;
+                            o[a][k][b + 2] *= f;
+                        }
+                    }
+            }
+            uint32_t ph[MT][2], pl[FINE ? MT : 1][2];
+#pragma unroll
+            for (int a = 0; a < MT; ++a) {
+                float w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float m = M[a][e & 1];
+                    w[e] = kv8_exp2(sc[a][e] - (m == -INFINITY ? 0.f : m) + KD_SHIFT);
+                    l[a][e & 1] += w[e] * vinv;
+                }
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const uint32_t hi = pack_f16x2(w[2 * b], w[2 * b + 1]);
+                    ph[a][b] = transpose8x8(hi);
+                    if constexpr (FINE) {
+                        const float2 f = unpack_f16x2(hi);
+                        pl[a][b] = transpose8x8(pack_f16x2(w[2 * b] - f.x, w[2 * b + 1] - f.y));
+                    }
+                }
+            }
+            // V of positions that not every token sees: their bytes may be anything, and 0 * NaN is not 0
+            uint32_t seen_nan[4] = {0, 0, 0, 0};   // bytes of visible NaN, where some tokens see them and some do not
+            if (!all) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int j = kb + 2 * t + (x & 1) + (x >> 1) * 8;
+                    bool any = false;
+                    for (int n = max(-p0, 0); n < row.n; ++n) any |= kv8_sees(p0 + n, j, p.window, p.sinks);
+                    if (!any)
+#pragma unroll
+                        for (int d = 0; d < HD / 32; ++d) s.v[x][d] = 0u;
+                    else if (row.n > 1)
+#pragma unroll
+                        for (int d = 0; d < HD / 32; ++d)
+                            seen_nan[x] |= ((s.v[x][d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                }
+            }
+            if (__any_sync(0xffffffffu, seen_nan[0] | seen_nan[1] | seen_nan[2] | seen_nan[3])) {
+                // rare: take the NaN bytes out of the product; the columns of the tokens that see them become NaN.
+                // nan_s: which of the 16 keys hold a NaN, by dim
+                for (int d = lane; d < HD; d += 32) nan_s[warp][d] = 0u;
+                __syncwarp();
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int d = 0; d < HD / 32; ++d) {
+                        uint32_t at = ((s.v[x][d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                        s.v[x][d] &= ~((at >> 7) * 0xFFu);
+                        while (at) {
+                            const int bit = __ffs(at) - 1;
+                            at &= at - 1;
+                            atomicOr(&nan_s[warp][g * (HD / 8) + 4 * d + bit / 8], 1u << (2 * t + (x & 1) + (x >> 1) * 8));
+                        }
+                    }
+                __syncwarp();
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t sees = 0u;   // keys that this query row sees
+                        for (int j = 0; j < 16; ++j)
+                            if (pos[a][b] >= 0 && kv8_sees(pos[a][b], kb + j, p.window, p.sinks)) sees |= 1u << j;
+#pragma unroll
+                        for (int k = 0; k < NK; ++k)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if (nan_s[warp][g * (HD / 8) + 2 * k + e] & sees) o[a][k][b + 2 * e] = __int_as_float(0x7FFFFFFF);
+                    }
+            }
+#pragma unroll
+            for (int d = 0; d < HD / 32; ++d) {
+                // words of four keys, four dims each -> pairs of keys for dims 0, 1 and 2, 3
+                const uint32_t x01 = __byte_perm(s.v[0][d], s.v[1][d], 0x5140), x23 = __byte_perm(s.v[0][d], s.v[1][d], 0x7362);
+                const uint32_t y01 = __byte_perm(s.v[2][d], s.v[3][d], 0x5140), y23 = __byte_perm(s.v[2][d], s.v[3][d], 0x7362);
+                uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
+                e4m3x4_to_f16(x01, a0, a1);
+                e4m3x4_to_f16(y01, a2, a3);
+                e4m3x4_to_f16(x23, c0, c1);
+                e4m3x4_to_f16(y23, c2, c3);
+#pragma unroll
+                for (int a = 0; a < MT; ++a) {
+                    mma_f16(o[a][2 * d], a0, a1, a2, a3, ph[a][0], ph[a][1]);
+                    mma_f16(o[a][2 * d + 1], c0, c1, c2, c3, ph[a][0], ph[a][1]);
+                    if constexpr (FINE) {
+                        mma_f16(o[a][2 * d], a0, a1, a2, a3, pl[a][0], pl[a][1]);
+                        mma_f16(o[a][2 * d + 1], c0, c1, c2, c3, pl[a][0], pl[a][1]);
+                    }
+                }
+            }
+        };
+
+        {
+            for (int i = i0; i < i1; i += 2) {
+                if (i + 1 < i1) have1 = load(i + 1, s1);
+                if (have0) compute(i, s0);
+                if (i + 1 >= i1) break;
+                if (i + 2 < i1) have0 = load(i + 2, s0);
+                if (have1) compute(i + 1, s1);
+            }
+        }
+
+        // join the four warps: the largest maximum, then sums in warp order
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[a][b] += __shfl_xor_sync(0xffffffffu, l[a][b], x);
+                if (g == 0) {
+                    m_s[warp][a * 8 + 2 * t + b] = M[a][b];
+                    l_s[warp][a * 8 + 2 * t + b] = l[a][b];
+                }
+            }
+#pragma unroll
+        for (int a = 0; a < MT; ++a)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                for (int k = 0; k < NK; ++k)   // dims g * HD / 8 + 2 k, + 1
+                    *reinterpret_cast<float2*>(&o_s[warp][a * 8 + 2 * t + b][g * (HD / 8) + 2 * k]) =
+                        make_float2(o[a][k][b], o[a][k][b + 2]);
+        __syncthreads();
+        const bool whole = i0 == 0 && i1 == tl.n;
+        float* slot = p.ws + ((size_t)blockIdx.x * 2 + (u == u_begin ? 0 : 1)) * kd_slot_floats<HD, MT>();
+        for (int x = tid; x < MT * 8 * (HD / 4); x += KD_THREADS) {
+            const int m = x / (HD / 4), d = (x % (HD / 4)) * 4;
+            if (m >= nq) continue;   // no such query row
+            float top = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < KD_WARPS; ++w) top = fmaxf(top, m_s[w][m]);
+            float sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int w = 0; w < KD_WARPS; ++w) {
+                const float f = m_s[w][m] == -INFINITY ? 0.f : kv8_exp2(m_s[w][m] - top);
+                const float4 v = *reinterpret_cast<const float4*>(&o_s[w][m][d]);
+                if (m_s[w][m] == -INFINITY && l_s[w][m] == 0.f) continue;   // nothing seen by this warp
+                sum += l_s[w][m] * f;
+                y[0] += v.x * f; y[1] += v.y * f; y[2] += v.z * f; y[3] += v.w * f;
+            }
+            if (whole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                T* dst = static_cast<T*>(p.out) + (row.t0 + m / G) * p.out_stride + (h * G + m % G) * HD + d;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Elem<T>::round_store(y[e] * inv, dst + e);
+            } else {
+                *reinterpret_cast<float4*>(slot + m * HD + d) = make_float4(y[0], y[1], y[2], y[3]);
+                if (d == 0) {
+                    slot[MT * 8 * HD + m] = top;
+                    slot[MT * 8 * (HD + 1) + m] = sum;
+                }
+            }
+        }
+        __syncthreads();   // the shared buffers are free again
+        u += i1 - i0;
+    }
+}
+
+// the rows and heads that were cut: grid (rows, Hkv * query rows), HD / 4 lanes used by a block of KD_THREADS
+template <int HD, int MT, bool FINE>
+__global__ void __launch_bounds__(KD_THREADS) k_kv8_join(const Kv8Attend p, int grid) {
+    using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
+    __shared__ KdPlan plan;
+    __shared__ float part_s[KD_THREADS / (HD / 4)][HD / 4][6];
+    pdl_wait();
+    pdl_trigger();
+    const Kv8Cache& c = p.c;
+    const int G = p.Hq / c.Hkv, r = blockIdx.x, h = blockIdx.y / (MT * 8), m = blockIdx.y % (MT * 8);
+    kd_plan(p, plan);
+    Kv8Row row;
+    if (!kv8_row(p.b, c.ppr * c.page, r, &row) || m >= row.n * G) return;
+    const long long units = (long long)plan.pre[c.rows] * c.Hkv;
+    const int pieces = kd_pieces(units, grid), n = plan.pre[r + 1] - plan.pre[r];
+    const long long u0 = (long long)plan.pre[r] * c.Hkv + (long long)h * n, u1 = u0 + n;
+    const int c0 = kd_piece_of(units, pieces, u0), c1 = kd_piece_of(units, pieces, u1 - 1);
+    if (c0 == c1) return;   // not cut
+    constexpr int LANES = HD / 4, PARTS = KD_THREADS / LANES;
+    const int part = threadIdx.x / LANES, d = (threadIdx.x % LANES) * 4;
+    float top = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int q = c0 + part; q <= c1; q += PARTS) {
+        const int which = q == c0 && kd_begin(units, pieces, q) != u0 ? 1 : 0;
+        const float* slot = p.ws + ((size_t)q * 2 + which) * kd_slot_floats<HD, MT>();
+        const float mm = slot[MT * 8 * HD + m], ll = slot[MT * 8 * (HD + 1) + m];
+        const float4 v = *reinterpret_cast<const float4*>(slot + m * HD + d);
+        if (mm == -INFINITY && ll == 0.f) continue;
+        const float big = fmaxf(top, mm);
+        const float f = top == -INFINITY ? 0.f : kv8_exp2(top - big), e = mm == -INFINITY ? 0.f : kv8_exp2(mm - big);
+        top = big;
+        sum = sum * f + ll * e;
+        y[0] = y[0] * f + v.x * e; y[1] = y[1] * f + v.y * e; y[2] = y[2] * f + v.z * e; y[3] = y[3] * f + v.w * e;
+    }
+    float* ps = part_s[part][threadIdx.x % LANES];
+    ps[0] = top; ps[1] = sum; ps[2] = y[0]; ps[3] = y[1]; ps[4] = y[2]; ps[5] = y[3];
+    __syncthreads();
+    if (part) return;
+    for (int w = 1; w < PARTS; ++w) {
+        const float* o = part_s[w][threadIdx.x];
+        if (o[0] == -INFINITY && o[1] == 0.f) continue;
+        const float big = fmaxf(top, o[0]);
+        const float f = top == -INFINITY ? 0.f : kv8_exp2(top - big), e = o[0] == -INFINITY ? 0.f : kv8_exp2(o[0] - big);
+        top = big;
+        sum = sum * f + o[1] * e;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = y[k] * f + o[2 + k] * e;
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    T* dst = static_cast<T*>(p.out) + (row.t0 + m / G) * p.out_stride + (h * G + m % G) * HD + d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Elem<T>::round_store(y[e] * inv, dst + e);
+}
+
+int decode_sets(const Kv8Attend& p) { return (p.b.max_new * (p.Hq / p.c.Hkv) + 7) / 8; }
+
+// one CTA for each place on the GPU, but no more than there can be tiles
+int decode_grid(const Kv8Attend& p, int num_sms) {
+    const long long tiles = (long long)p.c.rows * p.c.Hkv * (((long long)p.c.ppr * p.c.page + KD_TILE - 1) / KD_TILE);
+    const long long most = (long long)num_sms * (decode_sets(p) == 1 ? 3 : 2);
+    return (int)(tiles < most ? tiles : most);
+}
+
+template <int HD, int MT, bool FINE>
+cudaError_t launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
+    const int grid = decode_grid(p, num_sms);
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(KD_THREADS);
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_decode<HD, MT, FINE>, p);
+    if (e != cudaSuccess || p.c.ppr * (long long)p.c.page <= KD_TILE) return e;   // one tile a head: nothing is cut
+    cfg.gridDim = dim3(p.c.rows, p.c.Hkv * MT * 8);
+    return cudaLaunchKernelEx(&cfg, k_kv8_join<HD, MT, FINE>, p, grid);
+}
+
+}  // namespace
+
+bool kv8_decode_takes(const Kv8Attend& p) { return decode_sets(p) <= 2; }
+
+size_t kv8_decode_floats(const Kv8Attend& p, int num_sms) {
+    return (size_t)decode_grid(p, num_sms) * 2 * decode_sets(p) * 8 * (p.c.hd + 2);
+}
+
+cudaError_t kv8_decode_launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
+    const bool two = decode_sets(p) == 2, fine = p.dtype == W_F32;
+    if (p.c.hd == 128) {
+        if (fine) return two ? launch<128, 2, true>(p, num_sms, s) : launch<128, 1, true>(p, num_sms, s);
+        return two ? launch<128, 2, false>(p, num_sms, s) : launch<128, 1, false>(p, num_sms, s);
+    }
+    if (fine) return two ? launch<64, 2, true>(p, num_sms, s) : launch<64, 1, true>(p, num_sms, s);
+    return two ? launch<64, 2, false>(p, num_sms, s) : launch<64, 1, false>(p, num_sms, s);
+}
+
+}  // namespace gd
