@@ -299,15 +299,16 @@ struct Kv8Attend {
     int dtype, Hq;
     int window, sinks;         // window INT_MAX: every position up to the token's own
     float scale;
-    float* ws;                 // kv8_attend_floats() floats
+    float* ws;                 // kv8_decode_floats() or kv8_prompt_floats() floats
 };
 cudaError_t kv8_append_launch(const Kv8Append& p, cudaStream_t s);
-cudaError_t kv8_attend_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
-size_t kv8_attend_floats(const Kv8Attend& p, int num_sms);
 // up to 16 query rows (tokens x query heads of a K/V head) of a sequence (kv8_decode.cu)
 bool kv8_decode_takes(const Kv8Attend& p);
 cudaError_t kv8_decode_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
-size_t kv8_decode_floats(const Kv8Attend& p, int num_sms);
+size_t kv8_decode_floats(const Kv8Attend& p, int num_sms);   // of workspace
+// any number of query rows (kv8_prompt.cu)
+cudaError_t kv8_prompt_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
+size_t kv8_prompt_floats(const Kv8Attend& p, int num_sms);
 
 }  // namespace gd
 

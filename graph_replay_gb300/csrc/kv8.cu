@@ -102,6 +102,7 @@ int check_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const d
     if ((rc = check_dtype(a->dtype, &p->dtype)) != DEC_OK) return rc;
     if (a->n_heads < 1 || a->n_heads % p->c.Hkv) return refuse(DEC_E_INVALID, "n_kv_heads must divide n_heads");
     if (a->n_heads / p->c.Hkv > 128) return refuse(DEC_E_UNSUPPORTED, "n_heads / n_kv_heads: at most 128");
+    if ((int64_t)p->b.max_new * a->n_heads > (1 << 30)) return refuse(DEC_E_UNSUPPORTED, "max_new * n_heads: at most 2^30");
     if (a->window < 0 || a->sinks < 0) return refuse(DEC_E_INVALID, "window and sinks must be >= 0");
     if (!(a->scale >= 0.0) || !std::isfinite((float)a->scale))
         return refuse(DEC_E_INVALID, "scale must be finite and >= 0");
@@ -116,6 +117,10 @@ int check_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const d
     p->sinks = a->window ? a->sinks : 0;
     p->scale = a->scale > 0.0 ? (float)a->scale : (float)(1.0 / std::sqrt((double)p->c.hd));
     return DEC_OK;
+}
+
+size_t attend_bytes(const Kv8Attend& p, int sms) {
+    return sizeof(float) * (kv8_decode_takes(p) ? kv8_decode_floats(p, sms) : kv8_prompt_floats(p, sms));
 }
 
 int sms_of(int device, int* n) {
@@ -160,7 +165,7 @@ int dec_kv8_workspace(const dec_kv8_cache* cache, const dec_kv8_batch* batch, co
     int rc, sms;
     if ((rc = check_attend(cache, batch, attn, &p)) != DEC_OK) return rc;
     if ((rc = sms_of(cache->device, &sms)) != DEC_OK) return rc;
-    *bytes = kv8_attend_floats(p, sms) * sizeof(float);
+    *bytes = attend_bytes(p, sms);
     return DEC_OK;
 }
 
@@ -170,7 +175,7 @@ int dec_kv8_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const
     if ((rc = check_attend(cache, batch, attn, &p)) != DEC_OK) return rc;
     if (p.b.total == 0) return DEC_OK;
     if ((rc = sms_of(cache->device, &sms)) != DEC_OK) return rc;
-    const size_t need = kv8_attend_floats(p, sms) * sizeof(float);
+    const size_t need = attend_bytes(p, sms);
     if (need && (!attn->workspace || attn->workspace_bytes < need))
         return refuse(DEC_E_OOM, "workspace of %zu bytes is smaller than the %zu needed",
                       attn->workspace ? attn->workspace_bytes : (size_t)0, need);
@@ -178,7 +183,8 @@ int dec_kv8_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const
     p.ws = (float*)attn->workspace;
     OnDevice on(cache->device);
     if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
-    return launched(kv8_attend_launch(p, sms, (cudaStream_t)stream), "dec_kv8_attend");
+    const cudaStream_t s = (cudaStream_t)stream;
+    return launched(kv8_decode_takes(p) ? kv8_decode_launch(p, sms, s) : kv8_prompt_launch(p, sms, s), "dec_kv8_attend");
 }
 
 }  // extern "C"

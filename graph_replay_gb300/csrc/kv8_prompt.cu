@@ -1,0 +1,739 @@
+// kv8_prompt.cu -- attention over the 8-bit K/V cache for prompts and chunks
+// (more than 16 query rows of a K/V head) on the 5th-generation tensor cores.
+//
+// The query rows of a K/V head are (token, query head of the group), tokens
+// first: a tile of 128 holds all G heads of 128 / G tokens, so the heads share
+// every K/V tile and little of a tile lies above the causal diagonal.  Any G
+// works: a tile may begin inside a token.  Per 128 positions:
+//   convert   four warps read the e4m3 bytes (the pages' own order), turn them
+//             into f16 -- exact -- and store them as 128-byte-swizzled operand
+//             tiles in a ring; V's NaN become 0 there (see below)
+//   S = Q K^T tcgen05.mma kind::f16, A = Q, B = K, D in TMEM
+//   softmax   a thread owns a row: scores times K's scale, V's exponent added
+//             (weights are relative to the largest weight * V scale, the sum
+//             divides V's exponent out again), running maximum kept within 2^8,
+//             weights as f16 back into TMEM over the scores they came from
+//   O += P V  A = P from TMEM, B = V read MN-major
+// With bf16 q a CTA works on two query tiles in turn: while one is in softmax
+// the tensor core works for the other (TMEM: two S of 128 columns, two O).
+// With fp32 q, q and the weights enter as two f16 parts each; a CTA then has
+// one query tile, two S and P in columns of its own.
+//
+// What bounds it: 4 * 128 * 128 * HD operations a tile pair on the tensor
+// cores against 128 exponentials a row and the conversion's shared-memory
+// stores.
+//
+// Few tiles and many positions: the positions of a tile are split over several
+// CTAs (a host rule on sizes) and joined by a second kernel in split order.
+//
+// NaN: 0 * NaN is NaN inside an MMA, so a NaN in V that one row of a tile sees
+// would reach the rows that do not.  Therefore V's NaN never enter the product;
+// a tile that held one is marked, and at the end each row looks through the
+// marked tiles for NaN that it sees.  Positions that nobody sees are stored as
+// zeros.  Masked scores are replaced, never multiplied.
+#include <limits.h>
+#include "kv8.cuh"
+#include "mma_helpers.cuh"
+
+namespace gd {
+
+namespace {
+
+constexpr int KP_ROWS = 128;              // query rows of a tile: TMEM lanes
+constexpr int KP_KEYS = 128;              // positions of a tile
+constexpr int KP_THREADS = 13 * 32;       // 8 softmax warps, 4 converting warps, 1 MMA warp
+constexpr int KP_CONV_WARP = 8, KP_MMA_WARP = 12;
+constexpr int KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a tile
+constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
+constexpr int KP_META = 8;                // tiles whose scales are held
+constexpr int KP_MARKS = 32;              // words of marks: tile i has bit i % (32 * KP_MARKS)
+
+template <int HD, bool FINE>
+struct KpLayout {
+    static constexpr int NQ = FINE ? 1 : 2, PARTS = FINE ? 2 : 1;
+    static constexpr int TILE = HD / 64 * KP_PANEL;            // bytes of an f16 operand tile
+    static constexpr int SLOTS = HD == 128 ? 4 : 6;            // K and V tiles in turn
+    static constexpr int Q = 0, KV = NQ * PARTS * TILE, BYTES = KV + SLOTS * TILE;
+    // TMEM columns
+    [[maybe_unused]] static constexpr int S0 = 0, S1 = 128, O0 = 256, NEXT = 256 + HD;   // NEXT (FINE): P hi 64, P lo 64
+};
+template <int HD, bool FINE>
+constexpr int kp_smem() { return KpLayout<HD, FINE>::BYTES + 1024; }
+
+// byte offset of 16-byte chunk c of row r in a panel (128-byte swizzle)
+__device__ __forceinline__ uint32_t kp_sw(int r, int c) {
+    return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
+}
+__device__ __forceinline__ uint64_t kp_desc(uint32_t saddr, uint32_t lbo) {
+    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, f16 A and B, fp32 D
+constexpr uint32_t kp_idesc(int N, bool b_mn) {
+    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(KP_ROWS >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "r"((uint32_t)acc)
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+                 "r"((uint32_t)acc)
+                 : "memory");
+}
+__device__ __forceinline__ void kp_commit(uint64_t* bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
+__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
+
+// what 16 positions of a tile contribute besides their bytes
+struct __align__(16) KpMeta {
+    float kf, ve, vinv, pad;   // 2^K exponent, V's exponent (-inf: nothing there), 2^-V exponent
+};
+
+// what turns a product into a score (log2); never 0, which would make NaN of a masked -inf
+__device__ __forceinline__ float kp_mul(float fac, float kf) { return fmaxf(fac * kf, 1.17549435e-38f); }
+
+// the tiles of a CTA's rows: `sink` first ones, `gap` that no row sees, the rest
+struct KpTiles {
+    int n, sink, gap, end, low;   // tiles; first position behind; first position of the earliest window
+};
+__device__ __forceinline__ KpTiles kp_tiles(int pmin, int pmax, int window, int sinks) {
+    KpTiles t{};
+    t.end = max(pmax + 1, 0);
+    t.low = (int)max((long long)max(pmin, 0) - window + 1, 0ll);
+    const int end = (t.end + KP_KEYS - 1) / KP_KEYS, low = t.low / KP_KEYS;
+    const int sink = (min(sinks, t.end) + KP_KEYS - 1) / KP_KEYS;
+    if (sink >= low) {
+        t.n = t.sink = end;
+    } else {
+        t.n = sink + end - low;
+        t.sink = sink;
+        t.gap = low - sink;
+    }
+    return t;
+}
+
+// grid (Hkv * query tiles, rows * splits)
+template <int HD, bool FINE>
+__global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p, int splits) {
+    using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
+    using LY = KpLayout<HD, FINE>;
+    constexpr int NQ = LY::NQ, PARTS = LY::PARTS, SLOTS = LY::SLOTS;
+    extern __shared__ __align__(1024) unsigned char kp_raw[];
+    unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(kp_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ __align__(8) uint64_t kv_full[SLOTS], kv_empty[SLOTS], s_full[2], p_full[2], pv_done[2], meta_full[KP_META], all_done;
+    __shared__ KpMeta meta[KP_META][KP_KEYS / 16];
+    __shared__ float fac_s[NQ * KP_ROWS];
+    __shared__ uint32_t marks[KP_MARKS];
+    __shared__ uint32_t tmem;
+    __shared__ int aborted, marked;
+
+    pdl_wait();
+    pdl_trigger();
+    const Kv8Cache& c = p.c;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.Hq / c.Hkv, h = (gridDim.x - 1 - blockIdx.x) % c.Hkv, r = blockIdx.y / splits, sp = blockIdx.y % splits;
+    Kv8Row row;
+    if (!kv8_row(p.b, c.ppr * c.page, r, &row)) return;
+    const long long rows_q = (long long)row.n * G;
+    // tiles with the most positions first
+    const long long base = (long long)((gridDim.x - 1 - blockIdx.x) / c.Hkv) * (NQ * KP_ROWS);
+    if (base >= rows_q) return;
+    const int nact = NQ == 2 && base + KP_ROWS < rows_q ? 2 : 1;   // query tiles in use
+    const int p0 = row.len - row.n;
+    const int tok0 = (int)(base / G), tok1 = (int)((min(base + NQ * KP_ROWS, rows_q) - 1) / G);
+    const KpTiles tl = kp_tiles(p0 + tok0, p0 + tok1, p.window, p.sinks);
+    const int i0 = (int)((long long)tl.n * sp / splits), i1 = (int)((long long)tl.n * (sp + 1) / splits);
+    const int ntiles = i1 - i0;
+    auto key0 = [&](int i) { return (i < tl.sink ? i : i + tl.gap) * KP_KEYS; };
+
+    // ---- setup: Q as f16 tiles, each row brought to [2^14, 2^15) by a power of two ----
+    if (ntiles > 0) {
+        constexpr int LPR = HD / 8;   // lanes of a row, 8 dims each
+        for (int x = tid; x < NQ * KP_ROWS * LPR; x += KP_THREADS) {   // a whole warp keeps whole rows: KP_THREADS % LPR == 0
+            const int m = x / LPR, ch = x % LPR;
+            float v[8];
+            if (base + m < rows_q) {
+                const int tk = (int)((base + m) / G), hq = h * G + (int)((base + m) % G);
+                const T* src = static_cast<const T*>(p.q) + (row.t0 + tk) * p.q_stride + hq * HD + ch * 8;
+                if constexpr (FINE) {
+                    const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
+                    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+                } else {
+                    Elem<__nv_bfloat16>::unpack(__ldg(reinterpret_cast<const uint4*>(src)), v);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = 0.f;
+            }
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+            const unsigned grp = LPR == 16 ? 0xFFFFu << (lane & 16) : 0xFFu << (lane & 24);
+#pragma unroll
+            for (int o = 1; o < LPR; o <<= 1) top = fmaxf(top, __shfl_xor_sync(grp, top, o));
+            const int ex = min(max(268 - (int)(__float_as_uint(top) >> 23), 1), 254);
+            const float up = __int_as_float(ex << 23);
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float a = v[2 * e] * up, b = v[2 * e + 1] * up;
+                hi[e] = pack_h2(a, b);
+                const float2 f = unpack_h2(hi[e]);
+                lo[e] = pack_h2(a - f.x, b - f.y);
+            }
+            unsigned char* q = sm + LY::Q + (m / KP_ROWS) * LY::TILE + (ch / 8) * KP_PANEL + kp_sw(m % KP_ROWS, ch % 8);
+            *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (FINE) *reinterpret_cast<uint4*>(q + LY::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (ch == 0) fac_s[m] = p.scale * KV8_LOG2E / up;
+        }
+    }
+    if (warp == KP_MMA_WARP) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    if (tid == 0) {
+        for (int s = 0; s < SLOTS; ++s) {
+            mbar_init(&kv_full[s], 128);
+            mbar_init(&kv_empty[s], 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(&s_full[x], 1);
+            mbar_init(&p_full[x], 128);
+            mbar_init(&pv_done[x], 1);
+        }
+        for (int x = 0; x < KP_META; ++x) mbar_init(&meta_full[x], 1);
+        mbar_init(&all_done, 1);
+        aborted = 0;
+        marked = 0;
+        mbar_fence_init();
+    }
+    if (tid < KP_MARKS) marks[tid] = 0u;
+    fence_proxy_async_smem();   // Q's generic writes before the tensor core reads them
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t dt = tmem;
+    volatile int* ab = &aborted;
+    auto give_up = [&]() {
+        *ab = 1;
+        atomicOr(p.b.err, FAULT_WAIT);
+    };
+
+    const int x = warp / 4, m = (warp & 3) * 32 + lane;   // softmax warps: query tile and row
+    const long long mq = base + x * KP_ROWS + m;
+    const bool live = x < nact && mq < rows_q;
+    const int tk = (int)((live ? mq : base) / G), hq = h * G + (int)((live ? mq : base) % G), pos = live ? p0 + tk : -1;
+    const uint32_t lrow = dt + ((uint32_t)((warp & 3) * 32) << 16);
+    const uint32_t ocol = LY::O0 + (uint32_t)HD * x;
+    float M = -INFINITY, l = 0.f;
+    bool ok = true;
+
+    if (warp >= KP_CONV_WARP && warp < KP_MMA_WARP) {
+        // ---- K and V tiles: global e4m3 -> f16 operand tiles ----
+        constexpr int LOADS = HD / 16;                 // 16-byte loads of a thread: keys quad + 32 u, panel v
+        const int ct = tid - KP_CONV_WARP * 32, quad = ct >> 2, q4 = ct & 3;
+        // lane g < 8: the pool row of the tile's positions 16 g .. 16 g + 15, or -1
+        auto rows_of = [&](int i) -> long long {
+            long long at = -1;
+            const int kb = key0(i) + 16 * (lane & 7);
+            if (kb < tl.end && (kb + 15 >= tl.low || kb < p.sinks)) {
+                const int page = kv8_page(c, p.b.err, r, kb / c.page);
+                if (page >= 0) at = ((long long)page * c.Hkv + h) * c.page + kb % c.page;
+            }
+            return at;
+        };
+        auto load = [&](const uint8_t* pool, long long at, uint4 (&v)[LOADS]) {
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) {
+                const int key = quad + 32 * (u % 4), panel = u / 4;
+                const long long b = __shfl_sync(0xffffffffu, at, key >> 4);
+                v[u] = make_uint4(0u, 0u, 0u, 0u);
+                if (b >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(pool + (b + (key & 15)) * HD + panel * 64 + q4 * 16));
+            }
+        };
+        auto store = [&](unsigned char* tile, const uint4 (&v)[LOADS]) {
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) {
+                const int key = quad + 32 * (u % 4), panel = u / 4;
+                uint32_t a[4], b[4];
+                e4m3x4_to_f16(v[u].x, a[0], a[1]);
+                e4m3x4_to_f16(v[u].y, a[2], a[3]);
+                e4m3x4_to_f16(v[u].z, b[0], b[1]);
+                e4m3x4_to_f16(v[u].w, b[2], b[3]);
+                unsigned char* d = tile + panel * KP_PANEL;
+                *reinterpret_cast<uint4*>(d + kp_sw(key, 2 * q4)) = make_uint4(a[0], a[1], a[2], a[3]);
+                *reinterpret_cast<uint4*>(d + kp_sw(key, 2 * q4 + 1)) = make_uint4(b[0], b[1], b[2], b[3]);
+            }
+        };
+        auto put = [&](int s, const uint4 (&v)[LOADS]) -> bool {   // slot number s, counted over the whole loop
+            const bool go = s < SLOTS || (!*ab && mbar_wait(&kv_empty[s % SLOTS], (uint32_t)(s / SLOTS - 1) & 1u));
+            if (!__all_sync(0xffffffffu, go)) {
+                give_up();
+                return false;
+            }
+            store(sm + LY::KV + (s % SLOTS) * LY::TILE, v);
+            fence_proxy_async_smem();
+            mbar_arrive(&kv_full[s % SLOTS]);
+            return true;
+        };
+        uint4 kv[LOADS], vv[LOADS];
+        long long at = ntiles > 0 ? rows_of(i0) : -1;
+        if (ntiles > 0) load(c.k, at, kv);
+        for (int j = 0; j < ntiles; ++j) {
+            load(c.v, at, vv);
+            if (ct < 8) {
+                KpMeta m{1.f, -INFINITY, 0.f, 0.f};
+                if (at >= 0) {
+                    const long long sc = at / c.page * (c.page / c.block) + at % c.page / c.block;
+                    const int ve = (int)c.vs[sc] - 127;
+                    m = KpMeta{pow2i((int)c.ks[sc] - 127), (float)ve, pow2i(-ve), 0.f};
+                }
+                meta[j % KP_META][ct] = m;   // its last reader, the softmax of tile j - KP_META, is done: the ring is shorter
+            }
+            if (warp == KP_CONV_WARP) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&meta_full[j % KP_META]);
+            }
+            if (!put(2 * j, kv)) break;
+            if (j + 1 < ntiles) {
+                at = rows_of(i0 + j + 1);
+                load(c.k, at, kv);
+            }
+            // V's NaN stay out of the product; those at positions that a row of the CTA sees are marked
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) bad |= nan_bytes(vv[u].x) | nan_bytes(vv[u].y) | nan_bytes(vv[u].z) | nan_bytes(vv[u].w);
+            if (bad) {
+                bool seen = false;
+#pragma unroll
+                for (int u = 0; u < LOADS; ++u) {
+                    const uint32_t n[4] = {nan_bytes(vv[u].x), nan_bytes(vv[u].y), nan_bytes(vv[u].z), nan_bytes(vv[u].w)};
+                    const int key = key0(i0 + j) + quad + 32 * (u % 4);
+                    if ((n[0] | n[1] | n[2] | n[3]) && key < tl.end && (key >= tl.low || key < p.sinks)) seen = true;
+                    vv[u].x &= ~((n[0] >> 7) * 0xFFu);
+                    vv[u].y &= ~((n[1] >> 7) * 0xFFu);
+                    vv[u].z &= ~((n[2] >> 7) * 0xFFu);
+                    vv[u].w &= ~((n[3] >> 7) * 0xFFu);
+                }
+                if (seen) {
+                    atomicOr(&marks[(i0 + j) / 32 % KP_MARKS], 1u << ((i0 + j) & 31));
+                    marked = 1;
+                }
+            }
+            if (!put(2 * j + 1, vv)) break;
+        }
+    } else if (warp == KP_MMA_WARP) {
+        // ---- MMA issuer ----
+        if (lane == 0 && ntiles > 0) {
+            constexpr uint32_t id_s = kp_idesc(KP_KEYS, false), id_o = kp_idesc(HD, true);
+            const uint32_t ring = smem_u32(sm + LY::KV), qs = smem_u32(sm + LY::Q);
+            auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+                if (!*ab && mbar_wait(bar, parity)) {
+                    fence_after();
+                    return true;
+                }
+                give_up();
+                return false;
+            };
+            auto qk = [&](int x, uint32_t scol, int j) {   // S of query tile x and tile j
+                const uint32_t kt = ring + (uint32_t)((2 * j) % SLOTS * LY::TILE);
+#pragma unroll
+                for (int kk = 0; kk < HD / 16; ++kk) {
+                    const uint32_t o = (uint32_t)(kk / 4) * KP_PANEL + 32u * (kk % 4);
+#pragma unroll
+                    for (int f = 0; f < PARTS; ++f)
+                        mma_ss(dt + scol, kp_desc(qs + (uint32_t)(x * LY::TILE + f * LY::TILE) + o, 16), kp_desc(kt + o, 16), id_s,
+                               kk > 0 || f > 0);
+                }
+            };
+            auto pv = [&](uint32_t pcol, uint32_t ocol, int j) {
+                const uint32_t vt = ring + (uint32_t)((2 * j + 1) % SLOTS * LY::TILE);
+#pragma unroll
+                for (int kk = 0; kk < KP_KEYS / 16; ++kk)
+#pragma unroll
+                    for (int f = 0; f < PARTS; ++f)
+                        mma_ts(dt + ocol, dt + pcol + (uint32_t)(f * 64 + kk * 8), kp_desc(vt + 2048u * kk, KP_PANEL), id_o,
+                               j > 0 || kk > 0 || f > 0);
+            };
+            auto full = [&](int s) { return wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
+            if constexpr (!FINE) {
+                ok = full(0);
+                if (ok) {
+                    for (int x = 0; x < nact; ++x) {
+                        qk(x, LY::S0 + 128u * x, 0);
+                        kp_commit(&s_full[x]);
+                    }
+                    kp_commit(&kv_empty[0]);
+                }
+                for (int j = 0; j < ntiles && ok; ++j) {
+                    ok = full(2 * j + 1);
+                    for (int x = 0; x < nact && ok; ++x) {
+                        if (!(ok = wait(&p_full[x], (uint32_t)j & 1u))) break;
+                        pv(LY::S0 + 128u * x, LY::O0 + (uint32_t)HD * x, j);
+                        kp_commit(&pv_done[x]);
+                        if (x == nact - 1) kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
+                        if (j + 1 < ntiles) {
+                            if (x == 0 && !(ok = full(2 * j + 2))) break;
+                            qk(x, LY::S0 + 128u * x, j + 1);
+                            kp_commit(&s_full[x]);
+                            if (x == nact - 1) kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
+                        }
+                    }
+                }
+            } else {
+                ok = full(0);
+                if (ok) {
+                    qk(0, LY::S0, 0);
+                    kp_commit(&s_full[0]);
+                    kp_commit(&kv_empty[0]);
+                }
+                for (int j = 0; j < ntiles && ok; ++j) {
+                    if (j + 1 < ntiles) {   // the other S: its scores were read before P of tile j - 1 was full
+                        if (!(ok = full(2 * j + 2))) break;
+                        qk(0, (j + 1) & 1 ? LY::S1 : LY::S0, j + 1);
+                        kp_commit(&s_full[(j + 1) & 1]);
+                        kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
+                    }
+                    if (!(ok = full(2 * j + 1)) || !(ok = wait(&p_full[0], (uint32_t)j & 1u))) break;
+                    pv(LY::NEXT, LY::O0, j);
+                    kp_commit(&pv_done[0]);
+                    kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
+                }
+            }
+            // every MMA issued has finished before TMEM is released (also after a give-up)
+            kp_commit(&all_done);
+            if (!mbar_wait(&all_done, 0u)) give_up();
+        }
+        __syncwarp();
+    } else if (x < nact) {
+        // ---- softmax: warp w reads TMEM lanes 32 (w % 4) + lane, the rows of query tile w / 4 ----
+        const float fac = ntiles > 0 ? fac_s[x * KP_ROWS + m] : 0.f;
+        // the positions of this query tile's rows
+        const int xmin = p0 + (int)((base + x * KP_ROWS) / G);
+        const int xmax = p0 + (int)((min(base + (x + 1) * KP_ROWS, rows_q) - 1) / G);
+        const int lo = (int)max((long long)pos - p.window + 1, 0ll);   // this row sees [lo, pos] and [0, sinks)
+        for (int j = 0; j < ntiles; ++j) {
+            const int k0 = key0(i0 + j);
+            const int sb = FINE ? j & 1 : x;
+            ok = __all_sync(0xffffffffu, !*ab && mbar_wait(&s_full[sb], (uint32_t)(FINE ? j >> 1 : j) & 1u) &&
+                                             mbar_wait(&meta_full[j % KP_META], (uint32_t)(j / KP_META) & 1u));
+            if (!ok) {
+                give_up();
+                break;
+            }
+            fence_after();
+            const uint32_t scol = sb ? LY::S1 : LY::S0;
+            const KpMeta* mt = meta[j % KP_META];
+            // every row of the query tile sees every position: no mask
+            const bool all = xmin >= 0 && k0 + KP_KEYS - 1 <= xmin && (k0 > xmax - p.window || k0 + KP_KEYS - 1 < p.sinks);
+            auto mask = [&](uint32_t (&s)[32], int cc) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    const int key = k0 + cc + e;
+                    if (!(key <= pos && (key >= lo || key < p.sinks))) s[e] = 0xFF800000u;
+                }
+            };
+            uint32_t s[2][32];
+            float top = -INFINITY;
+            tm_ld32(lrow + scol, s[0]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                wait_ld();
+                if (q < 3) tm_ld32(lrow + scol + 32 * (q + 1), s[(q + 1) & 1]);
+                uint32_t(&v)[32] = s[q & 1];
+                if (!all) mask(v, 32 * q);
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    float t = __uint_as_float(v[16 * b]);
+#pragma unroll
+                    for (int e = 1; e < 16; ++e) t = fmaxf(t, __uint_as_float(v[16 * b + e]));
+                    const KpMeta k = mt[2 * q + b];
+                    top = fmaxf(top, fmaf(t, kp_mul(fac, k.kf), k.ve));
+                }
+            }
+            float alpha = 1.f;
+            if (top > M + KP_SLACK) {
+                alpha = M == -INFINITY ? 1.f : kv8_exp2(M - top);   // nothing has been summed yet: nothing to scale
+                M = top;
+                l *= alpha;
+            }
+            if (j > 0) {
+                // P and O of the last tile have been used
+                const bool scale_o = __any_sync(0xffffffffu, alpha != 1.f);
+                if (FINE || scale_o) {
+                    ok = __all_sync(0xffffffffu, !*ab && mbar_wait(&pv_done[x], (uint32_t)(j - 1) & 1u));
+                    if (!ok) {
+                        give_up();
+                        break;
+                    }
+                    fence_after();
+                }
+                if (scale_o)
+#pragma unroll
+                    for (int cc = 0; cc < HD; cc += 32) {
+                        tm_ld32(lrow + ocol + cc, s[0]);
+                        wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) s[0][e] = __float_as_uint(__uint_as_float(s[0][e]) * alpha);
+                        tm_st32(lrow + ocol + cc, s[0]);
+                    }
+            }
+            const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
+            tm_ld32(lrow + scol, s[0]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                wait_ld();
+                if (q < 3) tm_ld32(lrow + scol + 32 * (q + 1), s[(q + 1) & 1]);
+                uint32_t(&v)[32] = s[q & 1];
+                if (!all) mask(v, 32 * q);
+                uint32_t hi[16], low[16];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const KpMeta k = mt[2 * q + b];
+                    const float mul = kp_mul(fac, k.kf), add = k.ve - sub;
+                    float sum = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        const float w0 = kv8_exp2(fmaf(__uint_as_float(v[16 * b + e]), mul, add));
+                        const float w1 = kv8_exp2(fmaf(__uint_as_float(v[16 * b + e + 1]), mul, add));
+                        sum += w0 + w1;
+                        const int d = 8 * b + e / 2;
+                        hi[d] = pack_h2(w0, w1);
+                        if constexpr (FINE) {
+                            const float2 f = unpack_h2(hi[d]);
+                            low[d] = pack_h2(w0 - f.x, w1 - f.y);
+                        }
+                    }
+                    l = fmaf(sum, k.vinv, l);
+                }
+                // bf16 q: P lies over scores that this thread has read (columns 16 q .. of chunks <= q)
+                if constexpr (FINE) {
+                    tm_st16(lrow + LY::NEXT + 16 * q, hi);
+                    tm_st16(lrow + LY::NEXT + 64 + 16 * q, low);
+                } else {
+                    tm_st16(lrow + scol + 16 * q, hi);
+                }
+            }
+            wait_st();
+            fence_before();
+            mbar_arrive(&p_full[x]);
+        }
+        if (ok && ntiles > 0) {
+            ok = __all_sync(0xffffffffu, !*ab && mbar_wait(&pv_done[x], (uint32_t)(ntiles - 1) & 1u));
+            if (!ok) give_up();
+            fence_after();
+        }
+    }
+    __syncthreads();   // every tile has been converted: the marks are complete
+    if (x < nact) {
+        // NaN in V that this row sees: bits by dim
+        uint32_t nan[HD / 32];
+#pragma unroll
+        for (int d = 0; d < HD / 32; ++d) nan[d] = 0u;
+        if (ok && marked) {
+            for (int j = i0; j < i1; ++j) {
+                if (!(marks[j / 32 % KP_MARKS] >> (j & 31) & 1u)) continue;
+                const int k0 = key0(j);
+                for (int key = k0; key < min(k0 + KP_KEYS, pos + 1); ++key) {
+                    if (!kv8_sees(pos, key, p.window, p.sinks)) continue;
+                    const int id = c.pages ? c.pages[(size_t)r * c.ppr + key / c.page] : r * c.ppr + key / c.page;
+                    if ((unsigned)id >= (unsigned)c.num_pages) continue;
+                    const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                        c.v + (((size_t)id * c.Hkv + h) * c.page + key % c.page) * HD);
+#pragma unroll
+                    for (int d = 0; d < HD / 32; ++d)
+                        for (int e = 0; e < 8; ++e) {
+                            const uint32_t n = nan_bytes(__ldg(v + 8 * d + e)) >> 7;   // bits 0, 8, 16, 24
+                            nan[d] |= ((n & 1u) | (n >> 7 & 2u) | (n >> 14 & 4u) | (n >> 21 & 8u)) << (4 * e);
+                        }
+                }
+            }
+        }
+        // the result, or this split's part of it
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq;
+        const size_t all_rows = (size_t)p.b.total * p.Hq;
+        T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD;
+        float* part = p.ws + (sp * all_rows + qrow) * HD;
+        if (ok) {
+#pragma unroll
+            for (int cc = 0; cc < HD; cc += 32) {
+                uint32_t o[32];
+                if (ntiles > 0) {
+                    tm_ld32(lrow + ocol + cc, o);
+                    wait_ld();
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) o[e] = 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 32; ++e)
+                    if (nan[cc / 32] >> e & 1u) o[e] = 0x7FFFFFFFu;
+                if (!live) continue;
+                if (splits > 1) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4*>(part + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                } else if constexpr (FINE) {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<float4*>(dst + cc + e) =
+                            make_float4(l == 0.f ? 0.f : __uint_as_float(o[e]) * inv, l == 0.f ? 0.f : __uint_as_float(o[e + 1]) * inv,
+                                        l == 0.f ? 0.f : __uint_as_float(o[e + 2]) * inv, l == 0.f ? 0.f : __uint_as_float(o[e + 3]) * inv);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            w[k] = l == 0.f ? 0u
+                                            : pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                        *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            if (splits > 1 && live) {
+                float* ml = p.ws + (size_t)splits * all_rows * HD + (sp * all_rows + qrow) * 2;
+                ml[0] = M;
+                ml[1] = l;
+            }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == KP_MMA_WARP) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(dt) : "memory");
+    }
+}
+
+// one warp for each token and query head: the splits' parts in split order.  grid (query rows / 8, rows)
+template <int HD, bool FINE>
+__global__ void __launch_bounds__(256) k_kv8_prompt_join(const Kv8Attend p, int splits) {
+    using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
+    pdl_wait();
+    pdl_trigger();
+    const int r = blockIdx.y, lane = threadIdx.x & 31;
+    const long long m = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    Kv8Row row;
+    if (!kv8_row(p.b, p.c.ppr * p.c.page, r, &row) || m >= (long long)row.n * p.Hq) return;
+    const size_t all_rows = (size_t)p.b.total * p.Hq, qrow = (size_t)row.t0 * p.Hq + m;
+    const float* ml = p.ws + (size_t)splits * all_rows * HD;
+    constexpr int D = HD / 32;
+    float M = -INFINITY, l = 0.f, o[D];
+#pragma unroll
+    for (int d = 0; d < D; ++d) o[d] = 0.f;
+    for (int s = 0; s < splits; ++s) M = fmaxf(M, ml[(s * all_rows + qrow) * 2]);
+    for (int s = 0; s < splits; ++s) {
+        const float ms = ml[(s * all_rows + qrow) * 2], ls = ml[(s * all_rows + qrow) * 2 + 1];
+        if (ms == -INFINITY && ls == 0.f) continue;   // nothing seen in this split
+        const float f = ms == -INFINITY ? 0.f : kv8_exp2(ms - M);
+        l += ls * f;
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[d] = fmaf(p.ws[(s * all_rows + qrow) * HD + lane * D + d], f, o[d]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    T* dst = static_cast<T*>(p.out) + (row.t0 + m / p.Hq) * p.out_stride + m % p.Hq * HD + lane * D;
+#pragma unroll
+    for (int d = 0; d < D; ++d) Elem<T>::round_store(o[d] * inv, dst + d);
+}
+
+long long prompt_tiles(const Kv8Attend& p) {   // query tiles (of one CTA) of the longest row
+    const int per = (p.dtype == W_F32 ? 1 : 2) * KP_ROWS;
+    return ((long long)p.b.max_new * (p.Hq / p.c.Hkv) + per - 1) / per;
+}
+
+// Splits of a query tile's positions: as many as bring the CTAs to the SMs'
+// count, each with at least 4 tiles of the most positions that a tile may see
+int prompt_splits(const Kv8Attend& p, int num_sms) {
+    const long long ctas = prompt_tiles(p) * p.c.Hkv * p.c.rows;
+    long long keys = (long long)p.c.ppr * p.c.page;
+    const long long win = (long long)p.window + p.sinks + 2 * KP_KEYS + p.b.max_new;
+    if (win < keys) keys = win;
+    long long s = num_sms / ctas;
+    if (s > keys / (4 * KP_KEYS)) s = keys / (4 * KP_KEYS);
+    if (s > 32) s = 32;
+    return s < 1 ? 1 : (int)s;
+}
+
+template <int HD, bool FINE>
+cudaError_t launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
+    const int splits = prompt_splits(p, num_sms);
+    cudaError_t e = cudaFuncSetAttribute((const void*)&k_kv8_prompt<HD, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         kp_smem<HD, FINE>());
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(prompt_tiles(p) * p.c.Hkv), p.c.rows * splits);
+    cfg.blockDim = dim3(KP_THREADS);
+    cfg.dynamicSmemBytes = kp_smem<HD, FINE>();
+    cfg.stream = s;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, k_kv8_prompt<HD, FINE>, p, splits);
+    if (e != cudaSuccess || splits == 1) return e;
+    cfg.gridDim = dim3((unsigned)(((long long)p.b.max_new * p.Hq + 7) / 8), p.c.rows);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
+    return cudaLaunchKernelEx(&cfg, k_kv8_prompt_join<HD, FINE>, p, splits);
+}
+
+}  // namespace
+
+size_t kv8_prompt_floats(const Kv8Attend& p, int num_sms) {
+    const int splits = prompt_splits(p, num_sms);
+    return splits == 1 ? 0 : (size_t)splits * p.b.total * p.Hq * (p.c.hd + 2);
+}
+
+cudaError_t kv8_prompt_launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
+    const bool fine = p.dtype == W_F32;
+    if (p.c.hd == 128) return fine ? launch<128, true>(p, num_sms, s) : launch<128, false>(p, num_sms, s);
+    return fine ? launch<64, true>(p, num_sms, s) : launch<64, false>(p, num_sms, s);
+}
+
+}  // namespace gd
