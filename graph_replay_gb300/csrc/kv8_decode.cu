@@ -4,14 +4,18 @@
 //
 // Bound: the bytes of the visible K and V, each read once.  Everything else has
 // to hide behind that stream, so
-//   * K and V go from global memory straight into registers, in the order in
-//     which the tensor core wants them.  Both products keep the cache as the A
-//     operand of mma.m16n8k16 (S^T = K Q^T, O^T = V^T P^T), so the few query
-//     rows fill the N = 8 side and no accumulator row is wasted.  The sum over
-//     dims may run in any order: lane (g, t) of a warp reads 16 consecutive
-//     bytes of key g and uses them as its operand words, q is laid out to match;
-//     for V a lane reads a run of dims of its four keys and pairs the keys' bytes
-//     with byte permutes.  No shared memory, no transposing load;
+//   * each warp copies its own 16-key steps into a ring in shared memory (cp.async,
+//     three steps ahead, seven at 64 dims), so most of an SM's shared memory is
+//     in flight, whatever registers the arithmetic needs.  No barrier joins the
+//     warps inside the loop;
+//   * both products keep the cache as the A operand of mma.m16n8k16
+//     (S^T = K Q^T, O^T = V^T P^T), so the few query rows fill the N = 8 side and
+//     no accumulator row is wasted.  The sum over dims may run in any order: lane
+//     (g, t) of a warp takes consecutive bytes of key g as its operand words, q is
+//     laid out to match; for V a lane takes a run of dims of its four keys and
+//     pairs the keys' bytes with byte permutes.  No transposing load; 16-byte
+//     chunks are permuted within the rows so that both reads are free of bank
+//     conflicts;
 //   * e4m3 converts to f16 exactly and in pairs; the scales stay outside the
 //     products: K's exponent multiplies the 16-key score tile, V's is added to
 //     the exponent of the weights.  M is the running maximum of
@@ -117,12 +121,27 @@ __device__ __forceinline__ int kd_piece_of(long long units, int pieces, long lon
 template <int HD, int MT>
 __host__ __device__ constexpr int kd_slot_floats() { return MT * 8 * (HD + 2); }   // O, then M, then l of each query row
 
-// the 16 positions of one step as they came from memory
+// A step is 16 positions: K, then V, 16 rows of HD bytes each in lines of 128.
+// Chunk x (16 bytes) of row `key` lies at kd_at: chunks are permuted so that the
+// rows that a quarter warp reads at once lie in different banks.
 template <int HD>
-struct KdStep {
-    uint4 k[2][HD / 64];   // keys g, g + 8: 16 dims from 16 t + 64 j
-    uint32_t v[4][HD / 32];   // keys 2t, 2t + 1, 2t + 8, 2t + 9: HD / 8 dims from g * HD / 8
-    int ke, ve;            // scale bytes
+__device__ __forceinline__ uint32_t kd_at(int key, int x) {
+    if constexpr (HD == 128) return (uint32_t)(key * 128 + ((x ^ (key & 7)) << 4));
+    else return (uint32_t)((key >> 1) * 128 + (((((key & 1) << 2) | x) ^ ((key & 6))) << 4));
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// dynamic shared memory: the rings; when the loop is done the warps' results lie over them
+template <int HD, int MT>
+struct KdShared {
+    static constexpr int STEP = 2 * 16 * HD, STAGES = 512 / HD;   // 16 KB a warp
+    static constexpr int RING = KD_WARPS * STAGES * STEP, OUT = KD_WARPS * MT * 8 * HD * (int)sizeof(float);
+    static constexpr int BYTES = RING > OUT ? RING : OUT;
 };
 
 // MT: query rows / 8 (up).  FINE: fp32 q -- second f16 parts of q and of the weights.
@@ -130,15 +149,17 @@ template <int HD, int MT, bool FINE>
 __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(const Kv8Attend p) {
     using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
     constexpr int NK = HD / 16;   // 16-dim steps of S, 16-dim tiles of O
-    constexpr int PARTS = FINE ? 2 : 1;
+    constexpr int PARTS = FINE ? 2 : 1, STAGES = KdShared<HD, MT>::STAGES;
     __shared__ KdPlan plan;
-    __shared__ __align__(16) float o_s[KD_WARPS][MT * 8][HD];   // read and written as vectors
+    extern __shared__ __align__(128) unsigned char kd_raw[];
+    float(*o_s)[MT * 8][HD] = reinterpret_cast<float(*)[MT * 8][HD]>(kd_raw);
+    const unsigned char* ring_p = kd_raw + (threadIdx.x >> 5) * (STAGES * KdShared<HD, MT>::STEP);
+    const uint32_t ring = smem_u32(ring_p);
     __shared__ float m_s[KD_WARPS][MT * 8], l_s[KD_WARPS][MT * 8];
     __shared__ __align__(16) uint4 q_s[PARTS][MT][NK / 2][32];   // f16 parts of q, by step and lane
     __shared__ float fac_s[MT * 8];
     __shared__ uint32_t nan_s[KD_WARPS][HD];
     pdl_wait();
-    pdl_trigger();
     const Kv8Cache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int G = p.Hq / c.Hkv, cap = c.ppr * c.page, nb = c.page / c.block;
@@ -172,45 +193,44 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
         const int low = (int)max((long long)max(p0, 0) - p.window + 1, 0ll);   // no token of the row sees [sinks, low)
         auto key0 = [&](int i) { return (i < tl.sink ? i : i + tl.gap) * KD_TILE + warp * 16; };
         auto wanted = [&](int kb) { return kb < end && (kb + 15 >= low || kb < p.sinks); };
-        int page_ids = 0;   // lane L: the page of this warp's step in tile (i & ~31) + L, or -1
-        auto fetch_pages = [&](int i) {
+        // This warp's steps of 32 tiles, a tile for each lane: the page (-1: no step) and, packed, V's
+        // and K's scale bytes.  The copies run ahead of the arithmetic: it may still need the 32 before.
+        int pages = -1, scales = -1, scales_before = -1;
+        auto next32 = [&](int i) {
             const int ii = (i & ~31) + lane;
-            page_ids = -1;
-            if (ii >= i0 && ii < i1) {
-                const int kb = key0(ii);
-                if (wanted(kb)) page_ids = kv8_page(c, p.b.err, r, kb / c.page);
-            }
+            scales_before = scales;
+            pages = scales = -1;
+            if (ii < i0 || ii >= i1) return;
+            const int kb = key0(ii);
+            if (!wanted(kb)) return;
+            pages = kv8_page(c, p.b.err, r, kb / c.page);
+            if (pages < 0) return;
+            const size_t at = ((size_t)pages * c.Hkv + h) * nb + kb % c.page / c.block;
+            scales = (int)c.ks[at] | (int)c.vs[at] << 8;
         };
-        auto load = [&](int i, KdStep<HD>& s) -> bool {
-            if ((i & 31) == 0 || i == i0) fetch_pages(i);
-            const int page = __shfl_sync(0xffffffffu, page_ids, i & 31);
-            if (page < 0) return false;
-            const int kb = key0(i), off = kb % c.page;
-            const size_t head = (size_t)page * c.Hkv + h;
-            const uint8_t* kp = c.k + (head * c.page + off) * HD + g * HD + t * 16;
-            const uint8_t* vp = c.v + (head * c.page + off) * HD + 2 * t * HD + g * (HD / 8);
+        int ahead = i0;   // the next tile to copy
+        // one more step into the ring; one group a call, also for nothing
+        auto copy_next = [&]() {
+            const int i = ahead++;
+            if (i < i1) {
+                if ((i & 31) == 0 || i == i0) next32(i);
+                const int page = __shfl_sync(0xffffffffu, pages, i & 31);
+                if (page >= 0) {
+                    const size_t at = (((size_t)page * c.Hkv + h) * c.page + key0(i) % c.page) * HD;
+                    const uint32_t dst = ring + (uint32_t)((i % STAGES) * KdShared<HD, MT>::STEP);
 #pragma unroll
-            for (int j = 0; j < HD / 64; ++j) {
-                s.k[0][j] = ld_stream16(kp + j * 64);
-                s.k[1][j] = ld_stream16(kp + 8 * HD + j * 64);
-            }
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-                const uint8_t* vx = vp + ((x & 1) + (x >> 1) * 8) * HD;
-                if constexpr (HD == 128) {
-                    const uint4 w = ld_stream16(vx);
-                    s.v[x][0] = w.x; s.v[x][1] = w.y; s.v[x][2] = w.z; s.v[x][3] = w.w;
-                } else {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(vx));
-                    s.v[x][0] = w.x; s.v[x][1] = w.y;
+                    for (int u = 0; u < HD / 32; ++u) {
+                        const int x = lane + 32 * u;
+                        const uint32_t d = dst + kd_at<HD>(x / (HD / 16), x % (HD / 16));
+                        copy16(d, c.k + at + (size_t)x * 16);
+                        copy16(d + 16 * HD, c.v + at + (size_t)x * 16);
+                    }
                 }
             }
-            s.ke = c.ks[head * nb + off / c.block];
-            s.ve = c.vs[head * nb + off / c.block];
-            return true;
+            copy_commit();
         };
-        KdStep<HD> s0, s1;
-        bool have0 = load(i0, s0), have1 = false;   // in flight while q is laid out
+#pragma unroll
+        for (int x = 0; x < STAGES - 1; ++x) copy_next();   // in flight while q is laid out
 
         // q as B operand: warp a lays out the query rows a * 8 + g of this K/V head
         float fac[MT][2];   // scale * log2(e) / q's power of two, of query rows 2t and 2t + 1
@@ -220,13 +240,13 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
             float x[NK * 4];
             float top = 0.f;
             if (m < nq) {
-                const T* src = static_cast<const T*>(p.q) + (row.t0 + m / G) * p.q_stride + (h * G + m % G) * HD + t * 16;
+                const T* src = static_cast<const T*>(p.q) + (row.t0 + m / G) * p.q_stride + (h * G + m % G) * HD + t * (HD / 4);
 #pragma unroll
                 for (int j = 0; j < HD / 64; ++j)
 #pragma unroll
                     for (int v = 0; v < 16; v += Elem<T>::VEC) {
                         float f[Elem<T>::VEC];
-                        Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(src + j * 64 + v)), f);
+                        Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(src + j * 16 + v)), f);
 #pragma unroll
                         for (int e = 0; e < Elem<T>::VEC; ++e) x[j * 16 + v + e] = f[e];
                     }
@@ -277,16 +297,18 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
             l[a][0] = l[a][1] = 0.f;
         }
 
-        auto compute = [&](int i, KdStep<HD>& s) {
+        auto compute = [&](int i, int scale_bytes) {
             const int kb = key0(i);
+            const unsigned char* step = ring_p + (i % STAGES) * KdShared<HD, MT>::STEP;
             // S^T: rows keys g, g + 8; columns query rows 2t, 2t + 1
             float sc[MT][4];
 #pragma unroll
             for (int a = 0; a < MT; ++a) sc[a][0] = sc[a][1] = sc[a][2] = sc[a][3] = 0.f;
 #pragma unroll
             for (int j = 0; j < HD / 64; ++j) {
-                const uint32_t w0[4] = {s.k[0][j].x, s.k[0][j].y, s.k[0][j].z, s.k[0][j].w};
-                const uint32_t w1[4] = {s.k[1][j].x, s.k[1][j].y, s.k[1][j].z, s.k[1][j].w};
+                const uint4 k0 = *reinterpret_cast<const uint4*>(step + kd_at<HD>(g, t * (HD / 64) + j));
+                const uint4 k1 = *reinterpret_cast<const uint4*>(step + kd_at<HD>(g + 8, t * (HD / 64) + j));
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
                 for (int e = 0; e < 4; e += 2) {
                     uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
@@ -304,7 +326,8 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
                         }
                 }
             }
-            const float kf = pow2i(s.ke - 127), ve = (float)(s.ve - 127), vinv = pow2i(127 - s.ve);
+            const int e_k = (scale_bytes & 255) - 127, e_v = (scale_bytes >> 8) - 127;
+            const float kf = pow2i(e_k), ve = (float)e_v, vinv = pow2i(-e_v);
             // positions every token of the row sees need no mask
             const bool all = kb + 15 <= p0 && (kb + 15 < p.sinks || kb > row.len - 1 - p.window);
             bool grew = false;
@@ -357,6 +380,18 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
                 }
             }
             // V of positions that not every token sees: their bytes may be anything, and 0 * NaN is not 0
+            uint32_t v[4][HD / 32];   // keys 2t, 2t + 1, 2t + 8, 2t + 9: dims g * HD / 8 ..
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int key = 2 * t + (x & 1) + (x >> 1) * 8;
+                if constexpr (HD == 128) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(step + 16 * HD + kd_at<HD>(key, g));
+                    v[x][0] = w.x; v[x][1] = w.y; v[x][2] = w.z; v[x][3] = w.w;
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(step + 16 * HD + kd_at<HD>(key, g >> 1) + (g & 1) * 8);
+                    v[x][0] = w.x; v[x][1] = w.y;
+                }
+            }
             uint32_t seen_nan[4] = {0, 0, 0, 0};   // bytes of visible NaN, where some tokens see them and some do not
             if (!all) {
 #pragma unroll
@@ -366,11 +401,11 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
                     for (int n = max(-p0, 0); n < row.n; ++n) any |= kv8_sees(p0 + n, j, p.window, p.sinks);
                     if (!any)
 #pragma unroll
-                        for (int d = 0; d < HD / 32; ++d) s.v[x][d] = 0u;
+                        for (int d = 0; d < HD / 32; ++d) v[x][d] = 0u;
                     else if (row.n > 1)
 #pragma unroll
                         for (int d = 0; d < HD / 32; ++d)
-                            seen_nan[x] |= ((s.v[x][d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                            seen_nan[x] |= ((v[x][d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
                 }
             }
             if (__any_sync(0xffffffffu, seen_nan[0] | seen_nan[1] | seen_nan[2] | seen_nan[3])) {
@@ -382,8 +417,8 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
                 for (int x = 0; x < 4; ++x)
 #pragma unroll
                     for (int d = 0; d < HD / 32; ++d) {
-                        uint32_t at = ((s.v[x][d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                        s.v[x][d] &= ~((at >> 7) * 0xFFu);
+                        uint32_t at = ((v[x][d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                        v[x][d] &= ~((at >> 7) * 0xFFu);
                         while (at) {
                             const int bit = __ffs(at) - 1;
                             at &= at - 1;
@@ -408,8 +443,8 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
 #pragma unroll
             for (int d = 0; d < HD / 32; ++d) {
                 // words of four keys, four dims each -> pairs of keys for dims 0, 1 and 2, 3
-                const uint32_t x01 = __byte_perm(s.v[0][d], s.v[1][d], 0x5140), x23 = __byte_perm(s.v[0][d], s.v[1][d], 0x7362);
-                const uint32_t y01 = __byte_perm(s.v[2][d], s.v[3][d], 0x5140), y23 = __byte_perm(s.v[2][d], s.v[3][d], 0x7362);
+                const uint32_t x01 = __byte_perm(v[0][d], v[1][d], 0x5140), x23 = __byte_perm(v[0][d], v[1][d], 0x7362);
+                const uint32_t y01 = __byte_perm(v[2][d], v[3][d], 0x5140), y23 = __byte_perm(v[2][d], v[3][d], 0x7362);
                 uint32_t a0, a1, a2, a3, c0, c1, c2, c3;
                 e4m3x4_to_f16(x01, a0, a1);
                 e4m3x4_to_f16(y01, a2, a3);
@@ -427,15 +462,16 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
             }
         };
 
-        {
-            for (int i = i0; i < i1; i += 2) {
-                if (i + 1 < i1) have1 = load(i + 1, s1);
-                if (have0) compute(i, s0);
-                if (i + 1 >= i1) break;
-                if (i + 2 < i1) have0 = load(i + 2, s0);
-                if (have1) compute(i + 1, s1);
-            }
+        for (int i = i0; i < i1; ++i) {
+            copy_next();
+            copy_wait<STAGES - 1>();   // tile i's group is complete
+            __syncwarp();                 // for every lane's copies
+            const int sb = __shfl_sync(0xffffffffu, (i >> 5) == (min(ahead, i1) - 1) >> 5 ? scales : scales_before, i & 31);
+            if (sb >= 0) compute(i, sb);
+            __syncwarp();                 // the stage may be overwritten
         }
+        copy_wait<0>();
+        __syncthreads();   // every warp is done with its ring
 
         // join the four warps: the largest maximum, then sums in warp order
 #pragma unroll
@@ -491,6 +527,8 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
         __syncthreads();   // the shared buffers are free again
         u += i1 - i0;
     }
+    // not earlier: the next kernel's blocks would take places that this grid, which is one wave, counts on
+    pdl_trigger();
 }
 
 // the rows and heads that were cut: grid (rows, Hkv * query rows), HD / 4 lanes used by a block of KD_THREADS
@@ -500,7 +538,6 @@ __global__ void __launch_bounds__(KD_THREADS) k_kv8_join(const Kv8Attend p, int 
     __shared__ KdPlan plan;
     __shared__ float part_s[KD_THREADS / (HD / 4)][HD / 4][6];
     pdl_wait();
-    pdl_trigger();
     const Kv8Cache& c = p.c;
     const int G = p.Hq / c.Hkv, r = blockIdx.x, h = blockIdx.y / (MT * 8), m = blockIdx.y % (MT * 8);
     kd_plan(p, plan);
@@ -564,12 +601,16 @@ cudaError_t launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(KD_THREADS);
+    cfg.dynamicSmemBytes = KdShared<HD, MT>::BYTES;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, k_kv8_decode<HD, MT, FINE>, p);
+    cudaError_t e = cudaFuncSetAttribute((const void*)&k_kv8_decode<HD, MT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         KdShared<HD, MT>::BYTES);
+    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_kv8_decode<HD, MT, FINE>, p);
     if (e != cudaSuccess || p.c.ppr * (long long)p.c.page <= KD_TILE) return e;   // one tile a head: nothing is cut
     cfg.gridDim = dim3(p.c.rows, p.c.Hkv * MT * 8);
+    cfg.dynamicSmemBytes = 0;
     return cudaLaunchKernelEx(&cfg, k_kv8_join<HD, MT, FINE>, p, grid);
 }
 

@@ -41,7 +41,9 @@ namespace {
 
 constexpr int KP_ROWS = 128;              // query rows of a tile: TMEM lanes
 constexpr int KP_KEYS = 128;              // positions of a tile
-constexpr int KP_THREADS = 13 * 32;       // 8 softmax warps, 4 converting warps, 1 MMA warp
+constexpr int KP_THREADS = 16 * 32;       // 8 softmax warps, 4 converting warps, 1 MMA warp, 3 that only pad
+// registers a thread by role (setmaxnreg): of 512 threads x 128 at launch, 2 x 176 + 104 + 56 = 4 x 128
+constexpr int KP_REGS_SOFTMAX = 176, KP_REGS_CONV = 104, KP_REGS_MMA = 56;
 constexpr int KP_CONV_WARP = 8, KP_MMA_WARP = 12;
 constexpr int KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a tile
 constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
@@ -102,15 +104,12 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&r)[32]) {
           "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(a));
 }
-__device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&r)[32]) {
+__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-        "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-        "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-        "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(a));
 }
 __device__ __forceinline__ void tm_st16(uint32_t a, const uint32_t (&r)[16]) {
     asm volatile(
@@ -131,6 +130,35 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7
 struct __align__(16) KpMeta {
     float kf, ve, vinv, pad;   // 2^K exponent, V's exponent (-inf: nothing there), 2^-V exponent
 };
+
+// every warp of the CTA, each from its own role
+__device__ __forceinline__ void cta_meet() { asm volatile("bar.sync 0;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+// two fp32 at once
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 
 // what turns a product into a score (log2); never 0, which would make NaN of a masked -inf
 __device__ __forceinline__ float kp_mul(float fac, float kf) { return fmaxf(fac * kf, 1.17549435e-38f); }
@@ -171,7 +199,6 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     __shared__ int aborted, marked;
 
     pdl_wait();
-    pdl_trigger();
     const Kv8Cache& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.Hq / c.Hkv, h = (gridDim.x - 1 - blockIdx.x) % c.Hkv, r = blockIdx.y / splits, sp = blockIdx.y % splits;
@@ -262,17 +289,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         atomicOr(p.b.err, FAULT_WAIT);
     };
 
-    const int x = warp / 4, m = (warp & 3) * 32 + lane;   // softmax warps: query tile and row
-    const long long mq = base + x * KP_ROWS + m;
-    const bool live = x < nact && mq < rows_q;
-    const int tk = (int)((live ? mq : base) / G), hq = h * G + (int)((live ? mq : base) % G), pos = live ? p0 + tk : -1;
-    const uint32_t lrow = dt + ((uint32_t)((warp & 3) * 32) << 16);
-    const uint32_t ocol = LY::O0 + (uint32_t)HD * x;
-    float M = -INFINITY, l = 0.f;
-    bool ok = true;
-
     if (warp >= KP_CONV_WARP && warp < KP_MMA_WARP) {
         // ---- K and V tiles: global e4m3 -> f16 operand tiles ----
+        regs_down<KP_REGS_CONV>();
         constexpr int LOADS = HD / 16;                 // 16-byte loads of a thread: keys quad + 32 u, panel v
         const int ct = tid - KP_CONV_WARP * 32, quad = ct >> 2, q4 = ct & 3;
         // lane g < 8: the pool row of the tile's positions 16 g .. 16 g + 15, or -1
@@ -365,9 +384,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             }
             if (!put(2 * j + 1, vv)) break;
         }
-    } else if (warp == KP_MMA_WARP) {
+        cta_meet();
+    } else if (warp >= KP_MMA_WARP) {
         // ---- MMA issuer ----
-        if (lane == 0 && ntiles > 0) {
+        regs_down<KP_REGS_MMA>();
+        if (warp == KP_MMA_WARP && lane == 0 && ntiles > 0) {
             constexpr uint32_t id_s = kp_idesc(KP_KEYS, false), id_o = kp_idesc(HD, true);
             const uint32_t ring = smem_u32(sm + LY::KV), qs = smem_u32(sm + LY::Q);
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -400,7 +421,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             };
             auto full = [&](int s) { return wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
             if constexpr (!FINE) {
-                ok = full(0);
+                bool ok = full(0);
                 if (ok) {
                     for (int x = 0; x < nact; ++x) {
                         qk(x, LY::S0 + 128u * x, 0);
@@ -424,7 +445,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     }
                 }
             } else {
-                ok = full(0);
+                bool ok = full(0);
                 if (ok) {
                     qk(0, LY::S0, 0);
                     kp_commit(&s_full[0]);
@@ -448,14 +469,24 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             if (!mbar_wait(&all_done, 0u)) give_up();
         }
         __syncwarp();
-    } else if (x < nact) {
+        cta_meet();
+    } else {
         // ---- softmax: warp w reads TMEM lanes 32 (w % 4) + lane, the rows of query tile w / 4 ----
-        const float fac = ntiles > 0 ? fac_s[x * KP_ROWS + m] : 0.f;
+        regs_up<KP_REGS_SOFTMAX>();
+        const int x = warp / 4, m = (warp & 3) * 32 + lane;   // query tile and row
+        const long long mq = base + x * KP_ROWS + m;
+        const bool live = x < nact && mq < rows_q;
+        const int tk = (int)((live ? mq : base) / G), hq = h * G + (int)((live ? mq : base) % G), pos = live ? p0 + tk : -1;
+        const uint32_t lrow = dt + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t ocol = LY::O0 + (uint32_t)HD * x;
+        float M = -INFINITY, l = 0.f;
+        bool ok = true;
+        const float fac = ntiles > 0 && x < NQ ? fac_s[x * KP_ROWS + m] : 0.f;
         // the positions of this query tile's rows
         const int xmin = p0 + (int)((base + x * KP_ROWS) / G);
         const int xmax = p0 + (int)((min(base + (x + 1) * KP_ROWS, rows_q) - 1) / G);
         const int lo = (int)max((long long)pos - p.window + 1, 0ll);   // this row sees [lo, pos] and [0, sinks)
-        for (int j = 0; j < ntiles; ++j) {
+        for (int j = 0; j < (x < nact ? ntiles : 0); ++j) {
             const int k0 = key0(i0 + j);
             const int sb = FINE ? j & 1 : x;
             ok = __all_sync(0xffffffffu, !*ab && mbar_wait(&s_full[sb], (uint32_t)(FINE ? j >> 1 : j) & 1u) &&
@@ -465,35 +496,37 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 break;
             }
             fence_after();
-            const uint32_t scol = sb ? LY::S1 : LY::S0;
+            const uint32_t scol = lrow + (sb ? LY::S1 : LY::S0);
             const KpMeta* mt = meta[j % KP_META];
-            // every row of the query tile sees every position: no mask
-            const bool all = xmin >= 0 && k0 + KP_KEYS - 1 <= xmin && (k0 > xmax - p.window || k0 + KP_KEYS - 1 < p.sinks);
-            auto mask = [&](uint32_t (&s)[32], int cc) {
+            uint32_t s[4][32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    const int key = k0 + cc + e;
-                    if (!(key <= pos && (key >= lo || key < p.sinks))) s[e] = 0xFF800000u;
+            for (int q = 0; q < 4; ++q) tm_ld32(scol + 32 * q, s[q]);
+            wait_ld();
+            // some row of the query tile does not see some position
+            if (!(xmin >= 0 && k0 + KP_KEYS - 1 <= xmin && (k0 > xmax - p.window || k0 + KP_KEYS - 1 < p.sinks))) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    // bit e: position k0 + 32 q + e is one that this row sees
+                    auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+                    const int kq = k0 + 32 * q;
+                    const uint32_t see = below(pos + 1 - kq) & (~below(lo - kq) | below(p.sinks - kq));
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) s[q][e] = see >> e & 1u ? s[q][e] : 0xFF800000u;
                 }
-            };
-            uint32_t s[2][32];
+            }
             float top = -INFINITY;
-            tm_ld32(lrow + scol, s[0]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                wait_ld();
-                if (q < 3) tm_ld32(lrow + scol + 32 * (q + 1), s[(q + 1) & 1]);
-                uint32_t(&v)[32] = s[q & 1];
-                if (!all) mask(v, 32 * q);
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    float t = __uint_as_float(v[16 * b]);
-#pragma unroll
-                    for (int e = 1; e < 16; ++e) t = fmaxf(t, __uint_as_float(v[16 * b + e]));
+                    const uint32_t* v = s[q] + 16 * b;
+                    auto f = [&](int e) { return __uint_as_float(v[e]); };
+                    const float t0 = max3(f(0), f(1), f(2)), t1 = max3(f(3), f(4), f(5)), t2 = max3(f(6), f(7), f(8));
+                    const float t3 = max3(f(9), f(10), f(11)), t4 = max3(f(12), f(13), f(14));
+                    const float t = fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15)));
                     const KpMeta k = mt[2 * q + b];
                     top = fmaxf(top, fmaf(t, kp_mul(fac, k.kf), k.ve));
                 }
-            }
             float alpha = 1.f;
             if (top > M + KP_SLACK) {
                 alpha = M == -INFINITY ? 1.f : kv8_exp2(M - top);   // nothing has been summed yet: nothing to scale
@@ -512,34 +545,35 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     fence_after();
                 }
                 if (scale_o)
-#pragma unroll
-                    for (int cc = 0; cc < HD; cc += 32) {
-                        tm_ld32(lrow + ocol + cc, s[0]);
+#pragma unroll 1
+                    for (int cc = 0; cc < HD; cc += 16) {
+                        uint32_t o[16];
+                        tm_ld16(lrow + ocol + cc, o);
                         wait_ld();
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) s[0][e] = __float_as_uint(__uint_as_float(s[0][e]) * alpha);
-                        tm_st32(lrow + ocol + cc, s[0]);
+                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                        tm_st16(lrow + ocol + cc, o);
                     }
             }
             const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
-            tm_ld32(lrow + scol, s[0]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                wait_ld();
-                if (q < 3) tm_ld32(lrow + scol + 32 * (q + 1), s[(q + 1) & 1]);
-                uint32_t(&v)[32] = s[q & 1];
-                if (!all) mask(v, 32 * q);
                 uint32_t hi[16], low[16];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
                     const KpMeta k = mt[2 * q + b];
                     const float mul = kp_mul(fac, k.kf), add = k.ve - sub;
-                    float sum = 0.f;
+                    const uint64_t mul2 = pair(mul, mul), plus2 = pair(add, add);
+                    uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
-                        const float w0 = kv8_exp2(fmaf(__uint_as_float(v[16 * b + e]), mul, add));
-                        const float w1 = kv8_exp2(fmaf(__uint_as_float(v[16 * b + e + 1]), mul, add));
-                        sum += w0 + w1;
+                        const uint64_t t = fma2(pair(__uint_as_float(s[q][16 * b + e]), __uint_as_float(s[q][16 * b + e + 1])), mul2, plus2);
+                        float w0, w1;
+                        unpair(t, w0, w1);
+                        w0 = kv8_exp2(w0);
+                        w1 = kv8_exp2(w1);
+                        if (e & 2) sum1 = add2(sum1, pair(w0, w1));
+                        else sum0 = add2(sum0, pair(w0, w1));
                         const int d = 8 * b + e / 2;
                         hi[d] = pack_h2(w0, w1);
                         if constexpr (FINE) {
@@ -547,98 +581,100 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                             low[d] = pack_h2(w0 - f.x, w1 - f.y);
                         }
                     }
-                    l = fmaf(sum, k.vinv, l);
+                    float a0, a1;
+                    unpair(add2(sum0, sum1), a0, a1);
+                    l = fmaf(a0 + a1, k.vinv, l);
                 }
-                // bf16 q: P lies over scores that this thread has read (columns 16 q .. of chunks <= q)
+                // bf16 q: P lies over the scores, which this thread holds in registers
                 if constexpr (FINE) {
                     tm_st16(lrow + LY::NEXT + 16 * q, hi);
                     tm_st16(lrow + LY::NEXT + 64 + 16 * q, low);
                 } else {
-                    tm_st16(lrow + scol + 16 * q, hi);
+                    tm_st16(scol + 16 * q, hi);
                 }
             }
             wait_st();
             fence_before();
             mbar_arrive(&p_full[x]);
         }
-        if (ok && ntiles > 0) {
+        if (x < nact && ok && ntiles > 0) {
             ok = __all_sync(0xffffffffu, !*ab && mbar_wait(&pv_done[x], (uint32_t)(ntiles - 1) & 1u));
             if (!ok) give_up();
             fence_after();
         }
-    }
-    __syncthreads();   // every tile has been converted: the marks are complete
-    if (x < nact) {
-        // NaN in V that this row sees: bits by dim
-        uint32_t nan[HD / 32];
+        cta_meet();   // every tile has been converted: the marks are complete
+        if (x < nact) {
+            // NaN in V that this row sees: bits by dim
+            uint32_t nan[HD / 32];
 #pragma unroll
-        for (int d = 0; d < HD / 32; ++d) nan[d] = 0u;
-        if (ok && marked) {
-            for (int j = i0; j < i1; ++j) {
-                if (!(marks[j / 32 % KP_MARKS] >> (j & 31) & 1u)) continue;
-                const int k0 = key0(j);
-                for (int key = k0; key < min(k0 + KP_KEYS, pos + 1); ++key) {
-                    if (!kv8_sees(pos, key, p.window, p.sinks)) continue;
-                    const int id = c.pages ? c.pages[(size_t)r * c.ppr + key / c.page] : r * c.ppr + key / c.page;
-                    if ((unsigned)id >= (unsigned)c.num_pages) continue;
-                    const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                        c.v + (((size_t)id * c.Hkv + h) * c.page + key % c.page) * HD);
+            for (int d = 0; d < HD / 32; ++d) nan[d] = 0u;
+            if (ok && marked) {
+                for (int j = i0; j < i1; ++j) {
+                    if (!(marks[j / 32 % KP_MARKS] >> (j & 31) & 1u)) continue;
+                    const int k0 = key0(j);
+                    for (int key = k0; key < min(k0 + KP_KEYS, pos + 1); ++key) {
+                        if (!kv8_sees(pos, key, p.window, p.sinks)) continue;
+                        const int id = c.pages ? c.pages[(size_t)r * c.ppr + key / c.page] : r * c.ppr + key / c.page;
+                        if ((unsigned)id >= (unsigned)c.num_pages) continue;
+                        const uint32_t* v = reinterpret_cast<const uint32_t*>(
+                            c.v + (((size_t)id * c.Hkv + h) * c.page + key % c.page) * HD);
 #pragma unroll
-                    for (int d = 0; d < HD / 32; ++d)
-                        for (int e = 0; e < 8; ++e) {
-                            const uint32_t n = nan_bytes(__ldg(v + 8 * d + e)) >> 7;   // bits 0, 8, 16, 24
-                            nan[d] |= ((n & 1u) | (n >> 7 & 2u) | (n >> 14 & 4u) | (n >> 21 & 8u)) << (4 * e);
-                        }
-                }
-            }
-        }
-        // the result, or this split's part of it
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq;
-        const size_t all_rows = (size_t)p.b.total * p.Hq;
-        T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD;
-        float* part = p.ws + (sp * all_rows + qrow) * HD;
-        if (ok) {
-#pragma unroll
-            for (int cc = 0; cc < HD; cc += 32) {
-                uint32_t o[32];
-                if (ntiles > 0) {
-                    tm_ld32(lrow + ocol + cc, o);
-                    wait_ld();
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = 0u;
-                }
-#pragma unroll
-                for (int e = 0; e < 32; ++e)
-                    if (nan[cc / 32] >> e & 1u) o[e] = 0x7FFFFFFFu;
-                if (!live) continue;
-                if (splits > 1) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4*>(part + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                } else if constexpr (FINE) {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<float4*>(dst + cc + e) =
-                            make_float4(l == 0.f ? 0.f : __uint_as_float(o[e]) * inv, l == 0.f ? 0.f : __uint_as_float(o[e + 1]) * inv,
-                                        l == 0.f ? 0.f : __uint_as_float(o[e + 2]) * inv, l == 0.f ? 0.f : __uint_as_float(o[e + 3]) * inv);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 32; e += 8) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            w[k] = l == 0.f ? 0u
-                                            : pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-                        *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        for (int d = 0; d < HD / 32; ++d)
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t n = nan_bytes(__ldg(v + 8 * d + e)) >> 7;   // bits 0, 8, 16, 24
+                                nan[d] |= ((n & 1u) | (n >> 7 & 2u) | (n >> 14 & 4u) | (n >> 21 & 8u)) << (4 * e);
+                            }
                     }
                 }
             }
-            if (splits > 1 && live) {
-                float* ml = p.ws + (size_t)splits * all_rows * HD + (sp * all_rows + qrow) * 2;
-                ml[0] = M;
-                ml[1] = l;
+            // the result, or this split's part of it
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq;
+            const size_t all_rows = (size_t)p.b.total * p.Hq;
+            T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD;
+            float* part = p.ws + (sp * all_rows + qrow) * HD;
+            if (ok) {
+#pragma unroll
+                for (int cc = 0; cc < HD; cc += 32) {
+                    uint32_t o[32];
+                    if (ntiles > 0) {
+                        tm_ld32(lrow + ocol + cc, o);
+                        wait_ld();
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = 0u;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (nan[cc / 32] >> e & 1u) o[e] = 0x7FFFFFFFu;
+                    if (!live) continue;
+                    if (splits > 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<uint4*>(part + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    } else if constexpr (FINE) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4*>(dst + cc + e) =
+                                make_float4(l == 0.f ? 0.f : __uint_as_float(o[e]) * inv, l == 0.f ? 0.f : __uint_as_float(o[e + 1]) * inv,
+                                            l == 0.f ? 0.f : __uint_as_float(o[e + 2]) * inv, l == 0.f ? 0.f : __uint_as_float(o[e + 3]) * inv);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                w[k] = l == 0.f ? 0u
+                                                : pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
+                            *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    }
+                }
+                if (splits > 1 && live) {
+                    float* ml = p.ws + (size_t)splits * all_rows * HD + (sp * all_rows + qrow) * 2;
+                    ml[0] = M;
+                    ml[1] = l;
+                }
             }
         }
     }
@@ -655,7 +691,6 @@ template <int HD, bool FINE>
 __global__ void __launch_bounds__(256) k_kv8_prompt_join(const Kv8Attend p, int splits) {
     using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
     pdl_wait();
-    pdl_trigger();
     const int r = blockIdx.y, lane = threadIdx.x & 31;
     const long long m = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     Kv8Row row;
