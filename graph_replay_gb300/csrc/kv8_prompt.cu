@@ -32,6 +32,7 @@
 // marked tiles for NaN that it sees.  Positions that nobody sees are stored as
 // zeros.  Masked scores are replaced, never multiplied.
 #include <limits.h>
+#include <type_traits>
 #include "kv8.cuh"
 #include "mma_helpers.cuh"
 
@@ -66,28 +67,32 @@ constexpr int kp_smem() { return KpLayout<HD, FINE>::BYTES + 1024; }
 __device__ __forceinline__ uint32_t kp_sw(int r, int c) {
     return (uint32_t)((r >> 3) * 1024 + (r & 7) * 128 + ((c ^ (r & 7)) << 4));
 }
-__device__ __forceinline__ uint64_t kp_desc(uint32_t saddr, uint32_t lbo) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
+// shared-memory descriptor of 128-byte-swizzled tiles: the low word holds the address and the stride
+// between panels (both in 16 bytes), the high word is the same for all
+__device__ __forceinline__ uint32_t kp_desc(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16; }
+constexpr uint32_t KP_DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
 // kind::f16, f16 A and B, fp32 D
 constexpr uint32_t kp_idesc(int N, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(KP_ROWS >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                 "r"((uint32_t)acc)
+// One thread issues every MMA, so what it computes for each lies on the tensor core's path: with addresses and
+// descriptors computed in that thread's branch an MMA of 64 cycles took 290.  So the whole warp runs the issuing
+// code, every lane has the operands, and each MMA or commit elects the lane that issues it
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred e, p;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
+                 " elect.sync _|e, 0xffffffff;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d), "r"(a),
+                 "r"(b), "r"(KP_DESC_HI), "r"(idesc), "r"(acc)
                  : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
-    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                 " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
-                 "r"((uint32_t)acc)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred e, p;\n .reg .b64 y;\n setp.ne.u32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
+                 " elect.sync _|e, 0xffffffff;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d), "r"(a),
+                 "r"(b), "r"(KP_DESC_HI), "r"(idesc), "r"(acc)
                  : "memory");
 }
 __device__ __forceinline__ void kp_commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+                 " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
                  : "memory");
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -158,6 +163,20 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
+}
+
+// A whole warp waits; one lane polls: 32 lanes' polls would take shared memory from the tensor core.
+// False: another role has given up, or this wait has (FAULT_WAIT)
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* aborted, unsigned* err) {
+    bool go = true;
+    if ((threadIdx.x & 31) == 0) {
+        go = !*aborted && mbar_wait(bar, parity);
+        if (!go) {
+            *aborted = 1;
+            atomicOr(err, FAULT_WAIT);
+        }
+    }
+    return __all_sync(0xffffffffu, go);
 }
 
 // what turns a product into a score (log2); never 0, which would make NaN of a masked -inf
@@ -288,7 +307,6 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         *ab = 1;
         atomicOr(p.b.err, FAULT_WAIT);
     };
-
     if (warp >= KP_CONV_WARP && warp < KP_MMA_WARP) {
         // ---- K and V tiles: global e4m3 -> f16 operand tiles ----
         regs_down<KP_REGS_CONV>();
@@ -328,11 +346,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             }
         };
         auto put = [&](int s, const uint4 (&v)[LOADS]) -> bool {   // slot number s, counted over the whole loop
-            const bool go = s < SLOTS || (!*ab && mbar_wait(&kv_empty[s % SLOTS], (uint32_t)(s / SLOTS - 1) & 1u));
-            if (!__all_sync(0xffffffffu, go)) {
-                give_up();
-                return false;
-            }
+            if (s >= SLOTS && !warp_wait(&kv_empty[s % SLOTS], (uint32_t)(s / SLOTS - 1) & 1u, ab, p.b.err)) return false;
             store(sm + LY::KV + (s % SLOTS) * LY::TILE, v);
             fence_proxy_async_smem();
             mbar_arrive(&kv_full[s % SLOTS]);
@@ -388,85 +402,95 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     } else if (warp >= KP_MMA_WARP) {
         // ---- MMA issuer ----
         regs_down<KP_REGS_MMA>();
-        if (warp == KP_MMA_WARP && lane == 0 && ntiles > 0) {
-            constexpr uint32_t id_s = kp_idesc(KP_KEYS, false), id_o = kp_idesc(HD, true);
-            const uint32_t ring = smem_u32(sm + LY::KV), qs = smem_u32(sm + LY::Q);
+        if (warp == KP_MMA_WARP && ntiles > 0) {
+            constexpr uint32_t id_s = kp_idesc(KP_KEYS, false), id_o = kp_idesc(HD, true), STEP = LY::TILE >> 4;
+            const uint32_t dtu = __shfl_sync(0xffffffffu, dt, 0);
+            const int nt = __shfl_sync(0xffffffffu, ntiles, 0);
+            const uint32_t qd = kp_desc(smem_u32(sm + LY::Q), 16), kd = kp_desc(smem_u32(sm + LY::KV), 16),
+                           vd = kp_desc(smem_u32(sm + LY::KV), KP_PANEL);
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-                if (!*ab && mbar_wait(bar, parity)) {
-                    fence_after();
-                    return true;
-                }
-                give_up();
-                return false;
+                const bool there = warp_wait(bar, parity, ab, p.b.err);
+                fence_after();
+                return there;
             };
-            auto qk = [&](int x, uint32_t scol, int j) {   // S of query tile x and tile j
-                const uint32_t kt = ring + (uint32_t)((2 * j) % SLOTS * LY::TILE);
+            auto qk = [&](auto tile, uint32_t scol, int j) {   // S of a query tile and tile j
+                const uint32_t kt = kd + (uint32_t)((2 * j) % SLOTS) * STEP, qt = qd + decltype(tile)::value * STEP;
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t o = (uint32_t)(kk / 4) * KP_PANEL + 32u * (kk % 4);
-#pragma unroll
-                    for (int f = 0; f < PARTS; ++f)
-                        mma_ss(dt + scol, kp_desc(qs + (uint32_t)(x * LY::TILE + f * LY::TILE) + o, 16), kp_desc(kt + o, 16), id_s,
-                               kk > 0 || f > 0);
+                    const uint32_t o = (uint32_t)(kk / 4 * KP_PANEL + 32 * (kk % 4)) >> 4;
+                    mma_ss(scol, qt + o, kt + o, id_s, kk > 0);
+                    if constexpr (FINE) mma_ss(scol, qt + STEP + o, kt + o, id_s, 1);
                 }
             };
             auto pv = [&](uint32_t pcol, uint32_t ocol, int j) {
-                const uint32_t vt = ring + (uint32_t)((2 * j + 1) % SLOTS * LY::TILE);
+                const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * STEP;
 #pragma unroll
-                for (int kk = 0; kk < KP_KEYS / 16; ++kk)
-#pragma unroll
-                    for (int f = 0; f < PARTS; ++f)
-                        mma_ts(dt + ocol, dt + pcol + (uint32_t)(f * 64 + kk * 8), kp_desc(vt + 2048u * kk, KP_PANEL), id_o,
-                               j > 0 || kk > 0 || f > 0);
+                for (int kk = 0; kk < KP_KEYS / 16; ++kk) {
+                    mma_ts(ocol, pcol + kk * 8, vt + 128 * kk, id_o, kk > 0 ? 1u : (uint32_t)(j > 0));
+                    if constexpr (FINE) mma_ts(ocol, pcol + 64 + kk * 8, vt + 128 * kk, id_o, 1);
+                }
             };
             auto full = [&](int s) { return wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
+            constexpr std::integral_constant<int, 0> A{};
+            bool ok = full(0);
             if constexpr (!FINE) {
-                bool ok = full(0);
+                constexpr std::integral_constant<int, 1> B{};
+                const bool two = nact == 2;
+                const uint32_t sa = dtu + LY::S0, sb = dtu + LY::S1, oa = dtu + LY::O0, ob = dtu + LY::O0 + HD;
                 if (ok) {
-                    for (int x = 0; x < nact; ++x) {
-                        qk(x, LY::S0 + 128u * x, 0);
-                        kp_commit(&s_full[x]);
+                    qk(A, sa, 0);
+                    kp_commit(&s_full[0]);
+                    if (two) {
+                        qk(B, sb, 0);
+                        kp_commit(&s_full[1]);
                     }
                     kp_commit(&kv_empty[0]);
                 }
-                for (int j = 0; j < ntiles && ok; ++j) {
-                    ok = full(2 * j + 1);
-                    for (int x = 0; x < nact && ok; ++x) {
-                        if (!(ok = wait(&p_full[x], (uint32_t)j & 1u))) break;
-                        pv(LY::S0 + 128u * x, LY::O0 + (uint32_t)HD * x, j);
-                        kp_commit(&pv_done[x]);
-                        if (x == nact - 1) kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
-                        if (j + 1 < ntiles) {
-                            if (x == 0 && !(ok = full(2 * j + 2))) break;
-                            qk(x, LY::S0 + 128u * x, j + 1);
-                            kp_commit(&s_full[x]);
-                            if (x == nact - 1) kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
-                        }
+                for (int j = 0; j < nt && ok; ++j) {
+                    const bool more = j + 1 < nt;
+                    if (!(ok = full(2 * j + 1) && wait(&p_full[0], (uint32_t)j & 1u))) break;
+                    pv(sa, oa, j);
+                    kp_commit(&pv_done[0]);
+                    if (!two) kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
+                    if (more) {
+                        if (!(ok = full(2 * j + 2))) break;
+                        qk(A, sa, j + 1);
+                        kp_commit(&s_full[0]);
+                        if (!two) kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
+                    }
+                    if (!two) continue;
+                    if (!(ok = wait(&p_full[1], (uint32_t)j & 1u))) break;
+                    pv(sb, ob, j);
+                    kp_commit(&pv_done[1]);
+                    kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
+                    if (more) {
+                        qk(B, sb, j + 1);
+                        kp_commit(&s_full[1]);
+                        kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
                     }
                 }
             } else {
-                bool ok = full(0);
                 if (ok) {
-                    qk(0, LY::S0, 0);
+                    qk(A, dtu + LY::S0, 0);
                     kp_commit(&s_full[0]);
                     kp_commit(&kv_empty[0]);
                 }
-                for (int j = 0; j < ntiles && ok; ++j) {
-                    if (j + 1 < ntiles) {   // the other S: its scores were read before P of tile j - 1 was full
+                for (int j = 0; j < nt && ok; ++j) {
+                    if (j + 1 < nt) {   // the other S: its scores were read before P of tile j - 1 was full
                         if (!(ok = full(2 * j + 2))) break;
-                        qk(0, (j + 1) & 1 ? LY::S1 : LY::S0, j + 1);
+                        qk(A, dtu + ((j + 1) & 1 ? LY::S1 : LY::S0), j + 1);
                         kp_commit(&s_full[(j + 1) & 1]);
                         kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
                     }
-                    if (!(ok = full(2 * j + 1)) || !(ok = wait(&p_full[0], (uint32_t)j & 1u))) break;
-                    pv(LY::NEXT, LY::O0, j);
+                    if (!(ok = full(2 * j + 1) && wait(&p_full[0], (uint32_t)j & 1u))) break;
+                    pv(dtu + LY::NEXT, dtu + LY::O0, j);
                     kp_commit(&pv_done[0]);
                     kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
                 }
             }
             // every MMA issued has finished before TMEM is released (also after a give-up)
             kp_commit(&all_done);
-            if (!mbar_wait(&all_done, 0u)) give_up();
+            if (lane == 0 && !mbar_wait(&all_done, 0u)) give_up();
         }
         __syncwarp();
         cta_meet();
@@ -489,12 +513,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         for (int j = 0; j < (x < nact ? ntiles : 0); ++j) {
             const int k0 = key0(i0 + j);
             const int sb = FINE ? j & 1 : x;
-            ok = __all_sync(0xffffffffu, !*ab && mbar_wait(&s_full[sb], (uint32_t)(FINE ? j >> 1 : j) & 1u) &&
-                                             mbar_wait(&meta_full[j % KP_META], (uint32_t)(j / KP_META) & 1u));
-            if (!ok) {
-                give_up();
-                break;
-            }
+            ok = warp_wait(&s_full[sb], (uint32_t)(FINE ? j >> 1 : j) & 1u, ab, p.b.err) &&
+                 warp_wait(&meta_full[j % KP_META], (uint32_t)(j / KP_META) & 1u, ab, p.b.err);
+            if (!ok) break;
             fence_after();
             const uint32_t scol = lrow + (sb ? LY::S1 : LY::S0);
             const KpMeta* mt = meta[j % KP_META];
@@ -537,11 +558,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 // P and O of the last tile have been used
                 const bool scale_o = __any_sync(0xffffffffu, alpha != 1.f);
                 if (FINE || scale_o) {
-                    ok = __all_sync(0xffffffffu, !*ab && mbar_wait(&pv_done[x], (uint32_t)(j - 1) & 1u));
-                    if (!ok) {
-                        give_up();
-                        break;
-                    }
+                    if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
                     fence_after();
                 }
                 if (scale_o)
@@ -598,8 +615,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             mbar_arrive(&p_full[x]);
         }
         if (x < nact && ok && ntiles > 0) {
-            ok = __all_sync(0xffffffffu, !*ab && mbar_wait(&pv_done[x], (uint32_t)(ntiles - 1) & 1u));
-            if (!ok) give_up();
+            ok = warp_wait(&pv_done[x], (uint32_t)(ntiles - 1) & 1u, ab, p.b.err);
             fence_after();
         }
         cta_meet();   // every tile has been converted: the marks are complete
