@@ -43,8 +43,8 @@ namespace {
 constexpr int KP_ROWS = 128;              // query rows of a tile: TMEM lanes
 constexpr int KP_KEYS = 128;              // positions of a tile
 constexpr int KP_THREADS = 16 * 32;       // 8 softmax warps, 4 converting warps, 1 MMA warp, 3 that only pad
-// registers a thread by role (setmaxnreg): of 512 threads x 128 at launch, 2 x 176 + 104 + 56 = 4 x 128
-constexpr int KP_REGS_SOFTMAX = 176, KP_REGS_CONV = 104, KP_REGS_MMA = 56;
+// registers a thread by role (setmaxnreg): of 512 threads x 128 at launch, 2 x 152 + 112 + 96 = 4 x 128
+constexpr int KP_REGS_SOFTMAX = 152, KP_REGS_CONV = 112, KP_REGS_MMA = 96;
 constexpr int KP_CONV_WARP = 8, KP_MMA_WARP = 12;
 constexpr int KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a tile
 constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
@@ -168,6 +168,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // A whole warp waits; one lane polls: 32 lanes' polls would take shared memory from the tensor core.
 // False: another role has given up, or this wait has (FAULT_WAIT)
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* aborted, unsigned* err) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;   // mostly it is done already
     bool go = true;
     if ((threadIdx.x & 31) == 0) {
         go = !*aborted && mbar_wait(bar, parity);
@@ -312,21 +313,32 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         regs_down<KP_REGS_CONV>();
         constexpr int LOADS = HD / 16;                 // 16-byte loads of a thread: keys quad + 32 u, panel v
         const int ct = tid - KP_CONV_WARP * 32, quad = ct >> 2, q4 = ct & 3;
-        // lane g < 8: the pool row of the tile's positions 16 g .. 16 g + 15, or -1
-        auto rows_of = [&](int i) -> long long {
-            long long at = -1;
+        // Four tiles at a time, lane 8 i + g knows of the 16 positions g of tile i: their first pool row (-1: none)
+        // and scale bytes.  Both are read a batch ahead -- the page ids first, the scales two tiles later -- so that
+        // no tile waits for them
+        const int nb = c.page / c.block;
+        long long at = -1, at_next = -1, scale_at = 0;
+        int scales = 0, scales_next = 0;   // K's byte, V's << 8
+        auto pages_ahead = [&](int j) {    // the batch that begins with tile j of this CTA
+            const int i = i0 + j + (lane >> 3);
+            at_next = -1;
+            if (i >= i1) return;
             const int kb = key0(i) + 16 * (lane & 7);
-            if (kb < tl.end && (kb + 15 >= tl.low || kb < p.sinks)) {
-                const int page = kv8_page(c, p.b.err, r, kb / c.page);
-                if (page >= 0) at = ((long long)page * c.Hkv + h) * c.page + kb % c.page;
-            }
-            return at;
+            if (kb >= tl.end || (kb + 15 < tl.low && kb >= p.sinks)) return;
+            const int slot = kb / c.page, off = kb - slot * c.page, page = kv8_page(c, p.b.err, r, slot);
+            if (page < 0) return;
+            const long long head = (long long)page * c.Hkv + h;
+            at_next = head * c.page + off;
+            scale_at = head * nb + off / c.block;
         };
-        auto load = [&](const uint8_t* pool, long long at, uint4 (&v)[LOADS]) {
+        auto scales_ahead = [&]() {
+            if (at_next >= 0) scales_next = (int)c.ks[scale_at] | (int)c.vs[scale_at] << 8;
+        };
+        auto load = [&](const uint8_t* pool, int j, long long rows, uint4 (&v)[LOADS]) {   // tile j, in rows' batch
 #pragma unroll
             for (int u = 0; u < LOADS; ++u) {
                 const int key = quad + 32 * (u % 4), panel = u / 4;
-                const long long b = __shfl_sync(0xffffffffu, at, key >> 4);
+                const long long b = __shfl_sync(0xffffffffu, rows, (j & 3) * 8 + (key >> 4));
                 v[u] = make_uint4(0u, 0u, 0u, 0u);
                 if (b >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(pool + (b + (key & 15)) * HD + panel * 64 + q4 * 16));
             }
@@ -353,28 +365,32 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             return true;
         };
         uint4 kv[LOADS], vv[LOADS];
-        long long at = ntiles > 0 ? rows_of(i0) : -1;
-        if (ntiles > 0) load(c.k, at, kv);
+        if (ntiles > 0) {
+            pages_ahead(0);
+            scales_ahead();
+            at = at_next;
+            scales = scales_next;
+            load(c.k, 0, at, kv);
+            load(c.v, 0, at, vv);
+        }
         for (int j = 0; j < ntiles; ++j) {
-            load(c.v, at, vv);
-            if (ct < 8) {
-                KpMeta m{1.f, -INFINITY, 0.f, 0.f};
-                if (at >= 0) {
-                    const long long sc = at / c.page * (c.page / c.block) + at % c.page / c.block;
-                    const int ve = (int)c.vs[sc] - 127;
-                    m = KpMeta{pow2i((int)c.ks[sc] - 127), (float)ve, pow2i(-ve), 0.f};
-                }
-                meta[j % KP_META][ct] = m;   // its last reader, the softmax of tile j - KP_META, is done: the ring is shorter
-            }
+            if ((j & 3) == 0) pages_ahead(j + 4);
+            if ((j & 3) == 2) scales_ahead();
             if (warp == KP_CONV_WARP) {
+                if (lane >> 3 == (j & 3)) {
+                    const int ve = (scales >> 8) - 127;
+                    // the last reader of this entry, the softmax of tile j - KP_META, is done: the ring is shorter
+                    meta[j % KP_META][lane & 7] = at >= 0 ? KpMeta{pow2i((scales & 255) - 127), (float)ve, pow2i(-ve), 0.f}
+                                                          : KpMeta{1.f, -INFINITY, 0.f, 0.f};
+                }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&meta_full[j % KP_META]);
             }
+            // tile j + 1 may lie in the next batch
+            const bool turn = (j & 3) == 3;
+            const long long rows1 = turn ? at_next : at;
             if (!put(2 * j, kv)) break;
-            if (j + 1 < ntiles) {
-                at = rows_of(i0 + j + 1);
-                load(c.k, at, kv);
-            }
+            if (j + 1 < ntiles) load(c.k, j + 1, rows1, kv);
             // V's NaN stay out of the product; those at positions that a row of the CTA sees are marked
             uint32_t bad = 0u;
 #pragma unroll
@@ -397,6 +413,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 }
             }
             if (!put(2 * j + 1, vv)) break;
+            if (j + 1 < ntiles) load(c.v, j + 1, rows1, vv);
+            if (turn) {
+                at = at_next;
+                scales = scales_next;
+            }
         }
         cta_meet();
     } else if (warp >= KP_MMA_WARP) {
@@ -519,49 +540,87 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             fence_after();
             const uint32_t scol = lrow + (sb ? LY::S1 : LY::S0);
             const KpMeta* mt = meta[j % KP_META];
-            uint32_t s[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tm_ld32(scol + 32 * q, s[q]);
-            wait_ld();
+            // P of fp32 q has columns of its own: free once the last tile's P V is done
+            if (FINE && j > 0) {
+                if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
+                fence_after();
+            }
             // some row of the query tile does not see some position
-            if (!(xmin >= 0 && k0 + KP_KEYS - 1 <= xmin && (k0 > xmax - p.window || k0 + KP_KEYS - 1 < p.sinks))) {
+            const bool masked = !(xmin >= 0 && k0 + KP_KEYS - 1 <= xmin && (k0 > xmax - p.window || k0 + KP_KEYS - 1 < p.sinks));
+            uint32_t pk[FINE ? 1 : KP_KEYS / 2];   // bf16 q: P, packed, until the maximum is known to hold
+            float part;
+            // Weights and maximum in one pass, with the maximum of the tiles before.  Where a row's grew by more
+            // than the slack (the first tile, and rarely after), the pass is made again with the new one
+            while (true) {
+                const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
+                float top = -INFINITY;
+                uint32_t s[2][32];
+                part = 0.f;
+                tm_ld32(scol, s[0]);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    // bit e: position k0 + 32 q + e is one that this row sees
-                    auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
-                    const int kq = k0 + 32 * q;
-                    const uint32_t see = below(pos + 1 - kq) & (~below(lo - kq) | below(p.sinks - kq));
+                    wait_ld();
+                    if (q < 3) tm_ld32(scol + 32 * (q + 1), s[(q + 1) & 1]);
+                    uint32_t(&v)[32] = s[q & 1];
+                    if (masked) {
+                        // bit e: position k0 + 32 q + e is one that this row sees
+                        auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+                        const int kq = k0 + 32 * q;
+                        const uint32_t see = below(pos + 1 - kq) & (~below(lo - kq) | below(p.sinks - kq));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) s[q][e] = see >> e & 1u ? s[q][e] : 0xFF800000u;
-                }
-            }
-            float top = -INFINITY;
+                        for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : 0xFF800000u;
+                    }
+                    uint32_t hi[FINE ? 16 : 1], low[FINE ? 16 : 1];
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+                    for (int b = 0; b < 2; ++b) {
+                        const KpMeta k = mt[2 * q + b];
+                        const float mul = kp_mul(fac, k.kf), add = k.ve - sub;
+                        auto f = [&](int e) { return __uint_as_float(v[16 * b + e]); };
+                        const float t0 = max3(f(0), f(1), f(2)), t1 = max3(f(3), f(4), f(5)), t2 = max3(f(6), f(7), f(8));
+                        const float t3 = max3(f(9), f(10), f(11)), t4 = max3(f(12), f(13), f(14));
+                        top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), mul, k.ve));
+                        const uint64_t mul2 = pair(mul, mul), plus2 = pair(add, add);
+                        uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint32_t* v = s[q] + 16 * b;
-                    auto f = [&](int e) { return __uint_as_float(v[e]); };
-                    const float t0 = max3(f(0), f(1), f(2)), t1 = max3(f(3), f(4), f(5)), t2 = max3(f(6), f(7), f(8));
-                    const float t3 = max3(f(9), f(10), f(11)), t4 = max3(f(12), f(13), f(14));
-                    const float t = fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15)));
-                    const KpMeta k = mt[2 * q + b];
-                    top = fmaxf(top, fmaf(t, kp_mul(fac, k.kf), k.ve));
+                        for (int e = 0; e < 16; e += 2) {
+                            float w0, w1;
+                            unpair(fma2(pair(f(e), f(e + 1)), mul2, plus2), w0, w1);
+                            w0 = kv8_exp2(w0);
+                            w1 = kv8_exp2(w1);
+                            if (e & 2) sum1 = add2(sum1, pair(w0, w1));
+                            else sum0 = add2(sum0, pair(w0, w1));
+                            const int d = 8 * b + e / 2;
+                            const uint32_t h2 = pack_h2(w0, w1);
+                            if constexpr (FINE) {
+                                const float2 g = unpack_h2(h2);
+                                hi[d] = h2;
+                                low[d] = pack_h2(w0 - g.x, w1 - g.y);
+                            } else {
+                                pk[16 * q + d] = h2;
+                            }
+                        }
+                        float a0, a1;
+                        unpair(add2(sum0, sum1), a0, a1);
+                        part = fmaf(a0 + a1, k.vinv, part);
+                    }
+                    if constexpr (FINE) {
+                        tm_st16(lrow + LY::NEXT + 16 * q, hi);
+                        tm_st16(lrow + LY::NEXT + 64 + 16 * q, low);
+                    }
                 }
-            float alpha = 1.f;
-            if (top > M + KP_SLACK) {
-                alpha = M == -INFINITY ? 1.f : kv8_exp2(M - top);   // nothing has been summed yet: nothing to scale
-                M = top;
-                l *= alpha;
-            }
-            if (j > 0) {
-                // P and O of the last tile have been used
-                const bool scale_o = __any_sync(0xffffffffu, alpha != 1.f);
-                if (FINE || scale_o) {
-                    if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
-                    fence_after();
+                const bool grew = top > M + KP_SLACK;
+                if (!__any_sync(0xffffffffu, grew)) break;
+                float alpha = 1.f;
+                if (grew) {
+                    if (M != -INFINITY) alpha = kv8_exp2(M - top);   // else nothing has been summed yet
+                    M = top;
+                    l *= alpha;
                 }
-                if (scale_o)
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    if (!FINE) {   // O must be at rest
+                        if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
+                        fence_after();
+                    }
 #pragma unroll 1
                     for (int cc = 0; cc < HD; cc += 16) {
                         uint32_t o[16];
@@ -571,44 +630,13 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                         for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                         tm_st16(lrow + ocol + cc, o);
                     }
+                }
             }
-            const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
+            if (!ok) break;
+            l += part;
+            if constexpr (!FINE) {   // P lies over the scores
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t hi[16], low[16];
-#pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const KpMeta k = mt[2 * q + b];
-                    const float mul = kp_mul(fac, k.kf), add = k.ve - sub;
-                    const uint64_t mul2 = pair(mul, mul), plus2 = pair(add, add);
-                    uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-                    for (int e = 0; e < 16; e += 2) {
-                        const uint64_t t = fma2(pair(__uint_as_float(s[q][16 * b + e]), __uint_as_float(s[q][16 * b + e + 1])), mul2, plus2);
-                        float w0, w1;
-                        unpair(t, w0, w1);
-                        w0 = kv8_exp2(w0);
-                        w1 = kv8_exp2(w1);
-                        if (e & 2) sum1 = add2(sum1, pair(w0, w1));
-                        else sum0 = add2(sum0, pair(w0, w1));
-                        const int d = 8 * b + e / 2;
-                        hi[d] = pack_h2(w0, w1);
-                        if constexpr (FINE) {
-                            const float2 f = unpack_h2(hi[d]);
-                            low[d] = pack_h2(w0 - f.x, w1 - f.y);
-                        }
-                    }
-                    float a0, a1;
-                    unpair(add2(sum0, sum1), a0, a1);
-                    l = fmaf(a0 + a1, k.vinv, l);
-                }
-                // bf16 q: P lies over the scores, which this thread holds in registers
-                if constexpr (FINE) {
-                    tm_st16(lrow + LY::NEXT + 16 * q, hi);
-                    tm_st16(lrow + LY::NEXT + 64 + 16 * q, low);
-                } else {
-                    tm_st16(scol + 16 * q, hi);
-                }
+                for (int q = 0; q < 4; ++q) tm_st16(scol + 16 * q, reinterpret_cast<const uint32_t(&)[16]>(pk[16 * q]));
             }
             wait_st();
             fence_before();
