@@ -42,10 +42,10 @@ namespace {
 
 constexpr int KP_ROWS = 128;              // query rows of a tile: TMEM lanes
 constexpr int KP_KEYS = 128;              // positions of a tile
-constexpr int KP_THREADS = 16 * 32;       // 8 softmax warps, 4 converting warps, 1 MMA warp, 3 that only pad
-// registers a thread by role (setmaxnreg): of 512 threads x 128 at launch, 2 x 152 + 112 + 96 = 4 x 128
-constexpr int KP_REGS_SOFTMAX = 152, KP_REGS_CONV = 112, KP_REGS_MMA = 96;
-constexpr int KP_CONV_WARP = 8, KP_MMA_WARP = 12;
+// 16 softmax warps, 4 that convert K, 4 that convert V, 1 MMA warp and 3 that only pad its warpgroup
+constexpr int KP_K_WARP = 16, KP_V_WARP = 20, KP_MMA_WARP = 24, KP_THREADS = 28 * 32;
+// registers a thread by role (setmaxnreg): 896 threads x 72 at launch = 512 x 72 + 256 x 80 + 128 x 56
+constexpr int KP_REGS_CONV = 80, KP_REGS_MMA = 56;
 constexpr int KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a tile
 constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
 constexpr int KP_META = 8;                // tiles whose scales are held
@@ -54,6 +54,7 @@ constexpr int KP_MARKS = 32;              // words of marks: tile i has bit i % 
 template <int HD, bool FINE>
 struct KpLayout {
     static constexpr int NQ = FINE ? 1 : 2, PARTS = FINE ? 2 : 1;
+    static constexpr int TPR = 4 / NQ, COLS = KP_KEYS / TPR;   // softmax threads of a row, and their positions
     static constexpr int TILE = HD / 64 * KP_PANEL;            // bytes of an f16 operand tile
     static constexpr int SLOTS = HD == 128 ? 4 : 6;            // K and V tiles in turn
     static constexpr int Q = 0, KV = NQ * PARTS * TILE, BYTES = KV + SLOTS * TILE;
@@ -165,16 +166,30 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return r;
 }
 
-// A whole warp waits; one lane polls: 32 lanes' polls would take shared memory from the tensor core.
-// False: another role has given up, or this wait has (FAULT_WAIT)
+// Whether the phase with this parity completes within about KP_WAIT_NS (the thread sleeps meanwhile)
+constexpr uint32_t KP_WAIT_NS = 20000;
+__device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(KP_WAIT_NS)
+        : "memory");
+    return ok != 0;
+}
+// A whole warp waits, bounded (about two seconds; FAULT_WAIT then).  One lane polls, and sleeps between polls: spinning
+// warps took 40 % of the issue slots from the working ones.  False: this wait has given up, or another role has
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* aborted, unsigned* err) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;   // mostly it is done already
     bool go = true;
     if ((threadIdx.x & 31) == 0) {
-        go = !*aborted && mbar_wait(bar, parity);
-        if (!go) {
+        const long long t0 = clock64();
+        while (!sleep_wait(bar, parity)) {
+            if (!*aborted && clock64() - t0 < 4000000000ll) continue;
+            go = false;
             *aborted = 1;
             atomicOr(err, FAULT_WAIT);
+            break;
         }
     }
     return __all_sync(0xffffffffu, go);
@@ -214,6 +229,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     __shared__ __align__(8) uint64_t kv_full[SLOTS], kv_empty[SLOTS], s_full[2], p_full[2], pv_done[2], meta_full[KP_META], all_done;
     __shared__ KpMeta meta[KP_META][KP_KEYS / 16];
     __shared__ float fac_s[NQ * KP_ROWS];
+    // what the threads of a row tell one another: maxima (by tile parity), whether to stop, sums
+    __shared__ float row_s[2][LY::TPR][NQ * KP_ROWS], sum_s[LY::TPR][NQ * KP_ROWS];
+    __shared__ int stop_s[2][LY::TPR][NQ * 4];
     __shared__ uint32_t marks[KP_MARKS];
     __shared__ uint32_t tmem;
     __shared__ int aborted, marked;
@@ -239,7 +257,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     // ---- setup: Q as f16 tiles, each row brought to [2^14, 2^15) by a power of two ----
     if (ntiles > 0) {
         constexpr int LPR = HD / 8;   // lanes of a row, 8 dims each
-        for (int x = tid; x < NQ * KP_ROWS * LPR; x += KP_THREADS) {   // a whole warp keeps whole rows: KP_THREADS % LPR == 0
+        for (int x = tid; x < NQ * KP_ROWS * LPR; x += KP_THREADS) {   // a whole warp keeps whole rows: KP_THREADS % 32 == 0
             const int m = x / LPR, ch = x % LPR;
             float v[8];
             if (base + m < rows_q) {
@@ -288,7 +306,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 128);
+            mbar_init(&p_full[x], 128 * LY::TPR);
             mbar_init(&pv_done[x], 1);
         }
         for (int x = 0; x < KP_META; ++x) mbar_init(&meta_full[x], 1);
@@ -308,117 +326,115 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         *ab = 1;
         atomicOr(p.b.err, FAULT_WAIT);
     };
-    if (warp >= KP_CONV_WARP && warp < KP_MMA_WARP) {
-        // ---- K and V tiles: global e4m3 -> f16 operand tiles ----
-        regs_down<KP_REGS_CONV>();
+    if (warp >= KP_K_WARP && warp < KP_MMA_WARP) {
+        // ---- K or V tiles: global e4m3 -> f16 operand tiles ----
+        regs_up<KP_REGS_CONV>();
         constexpr int LOADS = HD / 16;                 // 16-byte loads of a thread: keys quad + 32 u, panel v
-        const int ct = tid - KP_CONV_WARP * 32, quad = ct >> 2, q4 = ct & 3;
-        // Four tiles at a time, lane 8 i + g knows of the 16 positions g of tile i: their first pool row (-1: none)
-        // and scale bytes.  Both are read a batch ahead -- the page ids first, the scales two tiles later -- so that
-        // no tile waits for them
-        const int nb = c.page / c.block;
-        long long at = -1, at_next = -1, scale_at = 0;
-        int scales = 0, scales_next = 0;   // K's byte, V's << 8
-        auto pages_ahead = [&](int j) {    // the batch that begins with tile j of this CTA
-            const int i = i0 + j + (lane >> 3);
-            at_next = -1;
-            if (i >= i1) return;
-            const int kb = key0(i) + 16 * (lane & 7);
-            if (kb >= tl.end || (kb + 15 < tl.low && kb >= p.sinks)) return;
-            const int slot = kb / c.page, off = kb - slot * c.page, page = kv8_page(c, p.b.err, r, slot);
-            if (page < 0) return;
-            const long long head = (long long)page * c.Hkv + h;
-            at_next = head * c.page + off;
-            scale_at = head * nb + off / c.block;
-        };
-        auto scales_ahead = [&]() {
-            if (at_next >= 0) scales_next = (int)c.ks[scale_at] | (int)c.vs[scale_at] << 8;
-        };
-        auto load = [&](const uint8_t* pool, int j, long long rows, uint4 (&v)[LOADS]) {   // tile j, in rows' batch
+        auto convert = [&](auto is_v) {
+            constexpr bool V = decltype(is_v)::value;
+            const uint8_t* pool = V ? c.v : c.k;
+            const int ct = tid & 127, quad = ct >> 2, q4 = ct & 3;
+            const size_t in_group = (size_t)(quad & 15) * HD + q4 * 16;
+            // Four tiles at a time, lane 8 i + g knows of the 16 positions g of tile i: where they begin in the pool, in
+            // 16 rows (-1: nowhere), and their scale bytes.  Both are read a batch ahead -- the page ids first, the
+            // scales two tiles later -- so that no tile waits for them
+            const int nb = c.page / c.block;
+            int at = -1, at_next = -1, scales = 0, scales_next = 0;   // K's byte, V's << 8
+            long long scale_at = 0;
+            auto pages_ahead = [&](int j) {    // the batch that begins with tile j of this CTA
+                const int i = i0 + j + (lane >> 3);
+                at_next = -1;
+                if (i >= i1) return;
+                const int kb = key0(i) + 16 * (lane & 7);
+                if (kb >= tl.end || (kb + 15 < tl.low && kb >= p.sinks)) return;
+                const int slot = kb / c.page, off = kb - slot * c.page, page = kv8_page(c, p.b.err, r, slot);
+                if (page < 0) return;
+                const long long head = (long long)page * c.Hkv + h;
+                at_next = (int)((head * c.page + off) / 16);
+                if (!V) scale_at = head * nb + off / c.block;
+            };
+            auto scales_ahead = [&]() {
+                if (!V && at_next >= 0) scales_next = (int)c.ks[scale_at] | (int)c.vs[scale_at] << 8;
+            };
+            uint4 v[LOADS];
+            auto load = [&](int j, int rows) {   // tile j, in rows' batch
 #pragma unroll
-            for (int u = 0; u < LOADS; ++u) {
-                const int key = quad + 32 * (u % 4), panel = u / 4;
-                const long long b = __shfl_sync(0xffffffffu, rows, (j & 3) * 8 + (key >> 4));
-                v[u] = make_uint4(0u, 0u, 0u, 0u);
-                if (b >= 0) v[u] = __ldg(reinterpret_cast<const uint4*>(pool + (b + (key & 15)) * HD + panel * 64 + q4 * 16));
-            }
-        };
-        auto store = [&](unsigned char* tile, const uint4 (&v)[LOADS]) {
+                for (int u = 0; u < 4; ++u) {    // keys quad + 32 u
+                    const int b = __shfl_sync(0xffffffffu, rows, (j & 3) * 8 + 2 * u + (quad >> 4));
+                    const uint4* src = reinterpret_cast<const uint4*>(pool + (size_t)b * (16 * HD) + in_group);
 #pragma unroll
-            for (int u = 0; u < LOADS; ++u) {
-                const int key = quad + 32 * (u % 4), panel = u / 4;
-                uint32_t a[4], b[4];
-                e4m3x4_to_f16(v[u].x, a[0], a[1]);
-                e4m3x4_to_f16(v[u].y, a[2], a[3]);
-                e4m3x4_to_f16(v[u].z, b[0], b[1]);
-                e4m3x4_to_f16(v[u].w, b[2], b[3]);
-                unsigned char* d = tile + panel * KP_PANEL;
-                *reinterpret_cast<uint4*>(d + kp_sw(key, 2 * q4)) = make_uint4(a[0], a[1], a[2], a[3]);
-                *reinterpret_cast<uint4*>(d + kp_sw(key, 2 * q4 + 1)) = make_uint4(b[0], b[1], b[2], b[3]);
-            }
-        };
-        auto put = [&](int s, const uint4 (&v)[LOADS]) -> bool {   // slot number s, counted over the whole loop
-            if (s >= SLOTS && !warp_wait(&kv_empty[s % SLOTS], (uint32_t)(s / SLOTS - 1) & 1u, ab, p.b.err)) return false;
-            store(sm + LY::KV + (s % SLOTS) * LY::TILE, v);
-            fence_proxy_async_smem();
-            mbar_arrive(&kv_full[s % SLOTS]);
-            return true;
-        };
-        uint4 kv[LOADS], vv[LOADS];
-        if (ntiles > 0) {
-            pages_ahead(0);
-            scales_ahead();
-            at = at_next;
-            scales = scales_next;
-            load(c.k, 0, at, kv);
-            load(c.v, 0, at, vv);
-        }
-        for (int j = 0; j < ntiles; ++j) {
-            if ((j & 3) == 0) pages_ahead(j + 4);
-            if ((j & 3) == 2) scales_ahead();
-            if (warp == KP_CONV_WARP) {
-                if (lane >> 3 == (j & 3)) {
-                    const int ve = (scales >> 8) - 127;
-                    // the last reader of this entry, the softmax of tile j - KP_META, is done: the ring is shorter
-                    meta[j % KP_META][lane & 7] = at >= 0 ? KpMeta{pow2i((scales & 255) - 127), (float)ve, pow2i(-ve), 0.f}
-                                                          : KpMeta{1.f, -INFINITY, 0.f, 0.f};
+                    for (int n = 0; n < HD / 64; ++n) v[n * 4 + u] = b >= 0 ? __ldg(src + 4 * n) : make_uint4(0u, 0u, 0u, 0u);
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&meta_full[j % KP_META]);
-            }
-            // tile j + 1 may lie in the next batch
-            const bool turn = (j & 3) == 3;
-            const long long rows1 = turn ? at_next : at;
-            if (!put(2 * j, kv)) break;
-            if (j + 1 < ntiles) load(c.k, j + 1, rows1, kv);
-            // V's NaN stay out of the product; those at positions that a row of the CTA sees are marked
-            uint32_t bad = 0u;
-#pragma unroll
-            for (int u = 0; u < LOADS; ++u) bad |= nan_bytes(vv[u].x) | nan_bytes(vv[u].y) | nan_bytes(vv[u].z) | nan_bytes(vv[u].w);
-            if (bad) {
-                bool seen = false;
-#pragma unroll
-                for (int u = 0; u < LOADS; ++u) {
-                    const uint32_t n[4] = {nan_bytes(vv[u].x), nan_bytes(vv[u].y), nan_bytes(vv[u].z), nan_bytes(vv[u].w)};
-                    const int key = key0(i0 + j) + quad + 32 * (u % 4);
-                    if ((n[0] | n[1] | n[2] | n[3]) && key < tl.end && (key >= tl.low || key < p.sinks)) seen = true;
-                    vv[u].x &= ~((n[0] >> 7) * 0xFFu);
-                    vv[u].y &= ~((n[1] >> 7) * 0xFFu);
-                    vv[u].z &= ~((n[2] >> 7) * 0xFFu);
-                    vv[u].w &= ~((n[3] >> 7) * 0xFFu);
-                }
-                if (seen) {
-                    atomicOr(&marks[(i0 + j) / 32 % KP_MARKS], 1u << ((i0 + j) & 31));
-                    marked = 1;
-                }
-            }
-            if (!put(2 * j + 1, vv)) break;
-            if (j + 1 < ntiles) load(c.v, j + 1, rows1, vv);
-            if (turn) {
+            };
+            if (ntiles > 0) {
+                pages_ahead(0);
+                scales_ahead();
                 at = at_next;
                 scales = scales_next;
+                load(0, at);
             }
-        }
+            for (int j = 0; j < ntiles; ++j) {
+                if ((j & 3) == 0) pages_ahead(j + 4);
+                if ((j & 3) == 2) scales_ahead();
+                if (!V && warp == KP_K_WARP) {
+                    if (lane >> 3 == (j & 3)) {
+                        const int ve = (scales >> 8) - 127;
+                        // the last reader of this entry, the softmax of tile j - KP_META, is done: the ring is shorter
+                        meta[j % KP_META][lane & 7] = at >= 0 ? KpMeta{pow2i((scales & 255) - 127), (float)ve, pow2i(-ve), 0.f}
+                                                              : KpMeta{1.f, -INFINITY, 0.f, 0.f};
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&meta_full[j % KP_META]);
+                }
+                if (V) {
+                    // V's NaN stay out of the product; those at positions that a row of the CTA sees are marked
+                    uint32_t bad = 0u;
+#pragma unroll
+                    for (int u = 0; u < LOADS; ++u) bad |= nan_bytes(v[u].x) | nan_bytes(v[u].y) | nan_bytes(v[u].z) | nan_bytes(v[u].w);
+                    if (bad) {
+                        bool seen = false;
+#pragma unroll
+                        for (int u = 0; u < LOADS; ++u) {
+                            const uint32_t n[4] = {nan_bytes(v[u].x), nan_bytes(v[u].y), nan_bytes(v[u].z), nan_bytes(v[u].w)};
+                            const int key = key0(i0 + j) + quad + 32 * (u % 4);
+                            if ((n[0] | n[1] | n[2] | n[3]) && key < tl.end && (key >= tl.low || key < p.sinks)) seen = true;
+                            v[u].x &= ~((n[0] >> 7) * 0xFFu);
+                            v[u].y &= ~((n[1] >> 7) * 0xFFu);
+                            v[u].z &= ~((n[2] >> 7) * 0xFFu);
+                            v[u].w &= ~((n[3] >> 7) * 0xFFu);
+                        }
+                        if (seen) {
+                            atomicOr(&marks[(i0 + j) / 32 % KP_MARKS], 1u << ((i0 + j) & 31));
+                            marked = 1;
+                        }
+                    }
+                }
+                const int s = 2 * j + (V ? 1 : 0);   // slot number, K and V in turn
+                if (s >= SLOTS && !warp_wait(&kv_empty[s % SLOTS], (uint32_t)(s / SLOTS - 1) & 1u, ab, p.b.err)) break;
+                unsigned char* tile = sm + LY::KV + (s % SLOTS) * LY::TILE;
+#pragma unroll
+                for (int u = 0; u < LOADS; ++u) {
+                    uint32_t a[4], b[4];
+                    e4m3x4_to_f16(v[u].x, a[0], a[1]);
+                    e4m3x4_to_f16(v[u].y, a[2], a[3]);
+                    e4m3x4_to_f16(v[u].z, b[0], b[1]);
+                    e4m3x4_to_f16(v[u].w, b[2], b[3]);
+                    unsigned char* d = tile + u / 4 * KP_PANEL;
+                    *reinterpret_cast<uint4*>(d + kp_sw(quad + 32 * (u % 4), 2 * q4)) = make_uint4(a[0], a[1], a[2], a[3]);
+                    *reinterpret_cast<uint4*>(d + kp_sw(quad + 32 * (u % 4), 2 * q4 + 1)) = make_uint4(b[0], b[1], b[2], b[3]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&kv_full[s % SLOTS]);
+                const bool turn = (j & 3) == 3;   // tile j + 1 lies in the next batch
+                if (turn) {
+                    at = at_next;
+                    scales = scales_next;
+                }
+                if (j + 1 < ntiles) load(j + 1, at);
+            }
+        };
+        if (warp < KP_V_WARP) convert(std::false_type{});
+        else convert(std::true_type{});
         cta_meet();
     } else if (warp >= KP_MMA_WARP) {
         // ---- MMA issuer ----
@@ -443,11 +459,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     if constexpr (FINE) mma_ss(scol, qt + STEP + o, kt + o, id_s, 1);
                 }
             };
-            auto pv = [&](uint32_t pcol, uint32_t ocol, int j) {
+            auto pv = [&](uint32_t pcol, uint32_t ocol, int j) {   // bf16 q: the second half of P lies 64 columns on
                 const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * STEP;
 #pragma unroll
                 for (int kk = 0; kk < KP_KEYS / 16; ++kk) {
-                    mma_ts(ocol, pcol + kk * 8, vt + 128 * kk, id_o, kk > 0 ? 1u : (uint32_t)(j > 0));
+                    mma_ts(ocol, pcol + kk * 8 + (!FINE && kk >= 4 ? 32 : 0), vt + 128 * kk, id_o, kk > 0 ? 1u : (uint32_t)(j > 0));
                     if constexpr (FINE) mma_ts(ocol, pcol + 64 + kk * 8, vt + 128 * kk, id_o, 1);
                 }
             };
@@ -516,127 +532,137 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         __syncwarp();
         cta_meet();
     } else {
-        // ---- softmax: warp w reads TMEM lanes 32 (w % 4) + lane, the rows of query tile w / 4 ----
-        regs_up<KP_REGS_SOFTMAX>();
-        const int x = warp / 4, m = (warp & 3) * 32 + lane;   // query tile and row
+        // ---- softmax: warp w reads TMEM lanes 32 (w % 4) + lane.  TPR threads, in as many warps, share a row of
+        // query tile x; each takes COLS positions of a tile and HD / TPR columns of O ----
+        constexpr int TPR = LY::TPR, COLS = LY::COLS, CH = COLS / 32;
+        const int x = warp / (4 * TPR), part = warp / 4 % TPR, m = (warp & 3) * 32 + lane;
         const long long mq = base + x * KP_ROWS + m;
         const bool live = x < nact && mq < rows_q;
         const int tk = (int)((live ? mq : base) / G), hq = h * G + (int)((live ? mq : base) % G), pos = live ? p0 + tk : -1;
         const uint32_t lrow = dt + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ocol = LY::O0 + (uint32_t)HD * x;
+        const uint32_t ocol = lrow + LY::O0 + (uint32_t)(HD * x + HD / TPR * part);
         float M = -INFINITY, l = 0.f;
         bool ok = true;
-        const float fac = ntiles > 0 && x < NQ ? fac_s[x * KP_ROWS + m] : 0.f;
+        const float fac = ntiles > 0 ? fac_s[x * KP_ROWS + m] : 0.f;
         // the positions of this query tile's rows
         const int xmin = p0 + (int)((base + x * KP_ROWS) / G);
         const int xmax = p0 + (int)((min(base + (x + 1) * KP_ROWS, rows_q) - 1) / G);
         const int lo = (int)max((long long)pos - p.window + 1, 0ll);   // this row sees [lo, pos] and [0, sinks)
+        auto row_meet = [&]() { named_sync(1 + x * 4 + (warp & 3), 32 * TPR); };
         for (int j = 0; j < (x < nact ? ntiles : 0); ++j) {
-            const int k0 = key0(i0 + j);
+            const int k0 = key0(i0 + j) + part * COLS;
             const int sb = FINE ? j & 1 : x;
-            ok = warp_wait(&s_full[sb], (uint32_t)(FINE ? j >> 1 : j) & 1u, ab, p.b.err) &&
+            ok = ok && warp_wait(&s_full[sb], (uint32_t)(FINE ? j >> 1 : j) & 1u, ab, p.b.err) &&
                  warp_wait(&meta_full[j % KP_META], (uint32_t)(j / KP_META) & 1u, ab, p.b.err);
-            if (!ok) break;
-            fence_after();
-            const uint32_t scol = lrow + (sb ? LY::S1 : LY::S0);
-            const KpMeta* mt = meta[j % KP_META];
             // P of fp32 q has columns of its own: free once the last tile's P V is done
-            if (FINE && j > 0) {
-                if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
-                fence_after();
-            }
-            // some row of the query tile does not see some position
-            const bool masked = !(xmin >= 0 && k0 + KP_KEYS - 1 <= xmin && (k0 > xmax - p.window || k0 + KP_KEYS - 1 < p.sinks));
-            uint32_t pk[FINE ? 1 : KP_KEYS / 2];   // bf16 q: P, packed, until the maximum is known to hold
-            float part;
-            // Weights and maximum in one pass, with the maximum of the tiles before.  Where a row's grew by more
-            // than the slack (the first tile, and rarely after), the pass is made again with the new one
-            while (true) {
-                const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
-                float top = -INFINITY;
-                uint32_t s[2][32];
-                part = 0.f;
-                tm_ld32(scol, s[0]);
+            if (FINE && j > 0) ok = ok && warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err);
+            fence_after();
+            const uint32_t scol = lrow + (sb ? LY::S1 : LY::S0) + part * COLS;
+            const KpMeta* mt = meta[j % KP_META] + part * (COLS / 16);
+            // some row of the query tile does not see some of these positions
+            const bool masked = !(xmin >= 0 && k0 + COLS - 1 <= xmin && (k0 > xmax - p.window || k0 + COLS - 1 < p.sinks));
+            auto mask = [&](uint32_t (&v)[32], int q) {
+                // bit e: position k0 + 32 q + e is one that this row sees
+                auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+                const int kq = k0 + 32 * q;
+                const uint32_t see = below(pos + 1 - kq) & (~below(lo - kq) | below(p.sinks - kq));
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : 0xFF800000u;
+            };
+            uint32_t v[32];
+            float top = -INFINITY;
+            if (ok) {
+#pragma unroll
+                for (int q = 0; q < CH; ++q) {
+                    tm_ld32(scol + 32 * q, v);
                     wait_ld();
-                    if (q < 3) tm_ld32(scol + 32 * (q + 1), s[(q + 1) & 1]);
-                    uint32_t(&v)[32] = s[q & 1];
-                    if (masked) {
-                        // bit e: position k0 + 32 q + e is one that this row sees
-                        auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
-                        const int kq = k0 + 32 * q;
-                        const uint32_t see = below(pos + 1 - kq) & (~below(lo - kq) | below(p.sinks - kq));
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : 0xFF800000u;
-                    }
-                    uint32_t hi[FINE ? 16 : 1], low[FINE ? 16 : 1];
+                    if (masked) mask(v, q);
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        const KpMeta k = mt[2 * q + b];
-                        const float mul = kp_mul(fac, k.kf), add = k.ve - sub;
                         auto f = [&](int e) { return __uint_as_float(v[16 * b + e]); };
                         const float t0 = max3(f(0), f(1), f(2)), t1 = max3(f(3), f(4), f(5)), t2 = max3(f(6), f(7), f(8));
                         const float t3 = max3(f(9), f(10), f(11)), t4 = max3(f(12), f(13), f(14));
-                        top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), mul, k.ve));
-                        const uint64_t mul2 = pair(mul, mul), plus2 = pair(add, add);
-                        uint64_t sum0 = 0, sum1 = 0;
-#pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            float w0, w1;
-                            unpair(fma2(pair(f(e), f(e + 1)), mul2, plus2), w0, w1);
-                            w0 = kv8_exp2(w0);
-                            w1 = kv8_exp2(w1);
-                            if (e & 2) sum1 = add2(sum1, pair(w0, w1));
-                            else sum0 = add2(sum0, pair(w0, w1));
-                            const int d = 8 * b + e / 2;
-                            const uint32_t h2 = pack_h2(w0, w1);
-                            if constexpr (FINE) {
-                                const float2 g = unpack_h2(h2);
-                                hi[d] = h2;
-                                low[d] = pack_h2(w0 - g.x, w1 - g.y);
-                            } else {
-                                pk[16 * q + d] = h2;
-                            }
-                        }
-                        float a0, a1;
-                        unpair(add2(sum0, sum1), a0, a1);
-                        part = fmaf(a0 + a1, k.vinv, part);
-                    }
-                    if constexpr (FINE) {
-                        tm_st16(lrow + LY::NEXT + 16 * q, hi);
-                        tm_st16(lrow + LY::NEXT + 64 + 16 * q, low);
-                    }
-                }
-                const bool grew = top > M + KP_SLACK;
-                if (!__any_sync(0xffffffffu, grew)) break;
-                float alpha = 1.f;
-                if (grew) {
-                    if (M != -INFINITY) alpha = kv8_exp2(M - top);   // else nothing has been summed yet
-                    M = top;
-                    l *= alpha;
-                }
-                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    if (!FINE) {   // O must be at rest
-                        if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
-                        fence_after();
-                    }
-#pragma unroll 1
-                    for (int cc = 0; cc < HD; cc += 16) {
-                        uint32_t o[16];
-                        tm_ld16(lrow + ocol + cc, o);
-                        wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tm_st16(lrow + ocol + cc, o);
+                        const KpMeta k = mt[2 * q + b];
+                        top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), kp_mul(fac, k.kf), k.ve));
                     }
                 }
             }
-            if (!ok) break;
-            l += part;
-            if constexpr (!FINE) {   // P lies over the scores
+            // The row's maximum (the buffer of two tiles ago has been read by all).  The warps of a row leave the
+            // loop together: none may wait for one that has given up
+            row_s[j & 1][part][x * KP_ROWS + m] = top;
+            if (lane == 0) stop_s[j & 1][part][x * 4 + (warp & 3)] = !ok;
+            row_meet();
+            int stop = 0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) tm_st16(scol + 16 * q, reinterpret_cast<const uint32_t(&)[16]>(pk[16 * q]));
+            for (int q = 0; q < TPR; ++q) stop |= stop_s[j & 1][q][x * 4 + (warp & 3)];
+            if (__any_sync(0xffffffffu, stop)) {
+                ok = false;
+                break;
+            }
+#pragma unroll
+            for (int q = 0; q < TPR; ++q) top = fmaxf(top, row_s[j & 1][q][x * KP_ROWS + m]);
+            float alpha = 1.f;
+            if (top > M + KP_SLACK) {
+                if (M != -INFINITY) alpha = kv8_exp2(M - top);   // else nothing has been summed yet
+                M = top;
+                l *= alpha;
+            }
+            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                if (!FINE) {   // O must be at rest
+                    ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err);
+                    if (!ok) continue;   // and stop with the others
+                    fence_after();
+                }
+#pragma unroll 1
+                for (int cc = 0; cc < HD / TPR; cc += 16) {
+                    uint32_t o[16];
+                    tm_ld16(ocol + cc, o);
+                    wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tm_st16(ocol + cc, o);
+                }
+            }
+            const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
+#pragma unroll
+            for (int q = 0; q < CH; ++q) {
+                if (CH > 1) {
+                    tm_ld32(scol + 32 * q, v);
+                    wait_ld();
+                    if (masked) mask(v, q);
+                }
+                uint32_t hi[16], low[FINE ? 16 : 1];
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const KpMeta k = mt[2 * q + b];
+                    const float mul = kp_mul(fac, k.kf), add = k.ve - sub;
+                    const uint64_t mul2 = pair(mul, mul), plus2 = pair(add, add);
+                    uint64_t sum0 = 0, sum1 = 0;
+#pragma unroll
+                    for (int e = 0; e < 16; e += 2) {
+                        float w0, w1;
+                        unpair(fma2(pair(__uint_as_float(v[16 * b + e]), __uint_as_float(v[16 * b + e + 1])), mul2, plus2), w0, w1);
+                        w0 = kv8_exp2(w0);
+                        w1 = kv8_exp2(w1);
+                        if (e & 2) sum1 = add2(sum1, pair(w0, w1));
+                        else sum0 = add2(sum0, pair(w0, w1));
+                        const int d = 8 * b + e / 2;
+                        hi[d] = pack_h2(w0, w1);
+                        if constexpr (FINE) {
+                            const float2 g = unpack_h2(hi[d]);
+                            low[d] = pack_h2(w0 - g.x, w1 - g.y);
+                        }
+                    }
+                    float a0, a1;
+                    unpair(add2(sum0, sum1), a0, a1);
+                    l = fmaf(a0 + a1, k.vinv, l);
+                }
+                if constexpr (FINE) {
+                    tm_st16(lrow + LY::NEXT + part * 16, hi);
+                    tm_st16(lrow + LY::NEXT + 64 + part * 16, low);
+                } else {
+                    tm_st16(scol + 16 * q, hi);   // over scores that this thread has read
+                }
             }
             wait_st();
             fence_before();
@@ -646,13 +672,19 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             ok = warp_wait(&pv_done[x], (uint32_t)(ntiles - 1) & 1u, ab, p.b.err);
             fence_after();
         }
+        if (x < nact) sum_s[part][x * KP_ROWS + m] = l;
         cta_meet();   // every tile has been converted: the marks are complete
-        if (x < nact) {
-            // NaN in V that this row sees: bits by dim
-            uint32_t nan[HD / 32];
+        if (x < nact && ok) {
+            constexpr int OC = HD / TPR, NW = (OC + 31) / 32;
+            const int c0 = OC * part;   // this thread's columns
+            l = 0.f;
 #pragma unroll
-            for (int d = 0; d < HD / 32; ++d) nan[d] = 0u;
-            if (ok && marked) {
+            for (int q = 0; q < TPR; ++q) l += sum_s[q][x * KP_ROWS + m];
+            // NaN in V that this row sees: a bit for each column
+            uint32_t nan[NW];
+#pragma unroll
+            for (int d = 0; d < NW; ++d) nan[d] = 0u;
+            if (marked) {
                 for (int j = i0; j < i1; ++j) {
                     if (!(marks[j / 32 % KP_MARKS] >> (j & 31) & 1u)) continue;
                     const int k0 = key0(j);
@@ -661,10 +693,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                         const int id = c.pages ? c.pages[(size_t)r * c.ppr + key / c.page] : r * c.ppr + key / c.page;
                         if ((unsigned)id >= (unsigned)c.num_pages) continue;
                         const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                            c.v + (((size_t)id * c.Hkv + h) * c.page + key % c.page) * HD);
+                            c.v + (((size_t)id * c.Hkv + h) * c.page + key % c.page) * HD + c0);
 #pragma unroll
-                        for (int d = 0; d < HD / 32; ++d)
-                            for (int e = 0; e < 8; ++e) {
+                        for (int d = 0; d < NW; ++d)
+                            for (int e = 0; e < (OC < 32 ? OC : 32) / 4; ++e) {
                                 const uint32_t n = nan_bytes(__ldg(v + 8 * d + e)) >> 7;   // bits 0, 8, 16, 24
                                 nan[d] |= ((n & 1u) | (n >> 7 & 2u) | (n >> 14 & 4u) | (n >> 21 & 8u)) << (4 * e);
                             }
@@ -673,52 +705,46 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             }
             // the result, or this split's part of it
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq;
-            const size_t all_rows = (size_t)p.b.total * p.Hq;
-            T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD;
-            float* part = p.ws + (sp * all_rows + qrow) * HD;
-            if (ok) {
+            const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq, all_rows = (size_t)p.b.total * p.Hq;
+            T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD + c0;
+            float* piece = p.ws + (sp * all_rows + qrow) * HD + c0;
 #pragma unroll
-                for (int cc = 0; cc < HD; cc += 32) {
-                    uint32_t o[32];
-                    if (ntiles > 0) {
-                        tm_ld32(lrow + ocol + cc, o);
-                        wait_ld();
-                    } else {
+            for (int cc = 0; cc < OC; cc += 16) {
+                uint32_t o[16];
+                if (ntiles > 0) {
+                    tm_ld16(ocol + cc, o);
+                    wait_ld();
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0u;
-                    }
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (nan[cc / 32] >> e & 1u) o[e] = 0x7FFFFFFFu;
-                    if (!live) continue;
-                    if (splits > 1) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<uint4*>(part + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    } else if constexpr (FINE) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4*>(dst + cc + e) =
-                                make_float4(l == 0.f ? 0.f : __uint_as_float(o[e]) * inv, l == 0.f ? 0.f : __uint_as_float(o[e + 1]) * inv,
-                                            l == 0.f ? 0.f : __uint_as_float(o[e + 2]) * inv, l == 0.f ? 0.f : __uint_as_float(o[e + 3]) * inv);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                w[k] = l == 0.f ? 0u
-                                                : pack_bf16x2(__uint_as_float(o[e + 2 * k]) * inv, __uint_as_float(o[e + 2 * k + 1]) * inv);
-                            *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    }
+                    for (int e = 0; e < 16; ++e) o[e] = 0u;
                 }
-                if (splits > 1 && live) {
-                    float* ml = p.ws + (size_t)splits * all_rows * HD + (sp * all_rows + qrow) * 2;
-                    ml[0] = M;
-                    ml[1] = l;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (nan[cc / 32] >> (cc % 32 + e) & 1u) o[e] = 0x7FFFFFFFu;
+                if (!live) continue;
+                if (splits > 1) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4)
+                        *reinterpret_cast<uint4*>(piece + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+                    continue;
                 }
+                float y[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;   // nothing seen: O is undefined
+                if constexpr (FINE) {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(dst + cc + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 16; e += 8)
+                        *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
+                                                                             pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+                }
+            }
+            if (splits > 1 && live && part == 0) {
+                float* ml = p.ws + (size_t)splits * all_rows * HD + (sp * all_rows + qrow) * 2;
+                ml[0] = M;
+                ml[1] = l;
             }
         }
     }
