@@ -41,25 +41,25 @@ namespace gd {
 namespace {
 
 constexpr int KP_ROWS = 128;              // query rows of a tile: TMEM lanes
-constexpr int KP_KEYS = 128;              // positions of a tile
-// 16 softmax warps, 4 that convert K, 4 that convert V, 1 MMA warp and 3 that only pad its warpgroup
-constexpr int KP_K_WARP = 16, KP_V_WARP = 20, KP_MMA_WARP = 24, KP_THREADS = 28 * 32;
-// registers a thread by role (setmaxnreg): 896 threads x 72 at launch = 512 x 72 + 256 x 80 + 128 x 56
-constexpr int KP_REGS_CONV = 80, KP_REGS_MMA = 56;
-constexpr int KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a tile
+constexpr int KP_KEYS = 64;               // positions of a tile
+// 8 softmax warps, 4 that convert K, 4 that convert V, 1 MMA warp and 3 that only pad its warpgroup
+constexpr int KP_K_WARP = 8, KP_V_WARP = 12, KP_MMA_WARP = 16, KP_THREADS = 20 * 32;
+// registers a thread by role (setmaxnreg): 640 threads x 96 at launch = 256 x 128 + 256 x 80 + 128 x 64
+constexpr int KP_REGS_SOFTMAX = 128, KP_REGS_CONV = 80, KP_REGS_MMA = 64;
+constexpr int KP_QPANEL = KP_ROWS * 128, KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a query tile, of a K or V tile
 constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
 constexpr int KP_META = 8;                // tiles whose scales are held
+constexpr int KP_GROUPS = KP_KEYS / 16, KP_BATCH = 32 / KP_GROUPS;   // 16-position groups of a tile; tiles that a warp's lanes know of
 constexpr int KP_MARKS = 32;              // words of marks: tile i has bit i % (32 * KP_MARKS)
 
 template <int HD, bool FINE>
 struct KpLayout {
-    static constexpr int NQ = FINE ? 1 : 2, PARTS = FINE ? 2 : 1;
-    static constexpr int TPR = 4 / NQ, COLS = KP_KEYS / TPR;   // softmax threads of a row, and their positions
-    static constexpr int TILE = HD / 64 * KP_PANEL;            // bytes of an f16 operand tile
-    static constexpr int SLOTS = HD == 128 ? 4 : 6;            // K and V tiles in turn
-    static constexpr int Q = 0, KV = NQ * PARTS * TILE, BYTES = KV + SLOTS * TILE;
-    // TMEM columns
-    [[maybe_unused]] static constexpr int S0 = 0, S1 = 128, O0 = 256, NEXT = 256 + HD;   // NEXT (FINE): P hi 64, P lo 64
+    static constexpr int PARTS = FINE ? 2 : 1;
+    static constexpr int QTILE = HD / 64 * KP_QPANEL, TILE = HD / 64 * KP_PANEL;   // bytes of f16 operand tiles
+    static constexpr int SLOTS = HD == 128 && FINE ? 4 : 8;                         // K and V tiles in turn
+    static constexpr int Q = 0, KV = 2 * PARTS * QTILE, BYTES = KV + SLOTS * TILE;
+    // TMEM columns: S of query tile x, buffer b at 128 x + 64 b (P lies over it), O of query tile x at 256 + HD x
+    static constexpr int O = 256;
 };
 template <int HD, bool FINE>
 constexpr int kp_smem() { return KpLayout<HD, FINE>::BYTES + 1024; }
@@ -223,15 +223,12 @@ template <int HD, bool FINE>
 __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p, int splits) {
     using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
     using LY = KpLayout<HD, FINE>;
-    constexpr int NQ = LY::NQ, PARTS = LY::PARTS, SLOTS = LY::SLOTS;
+    constexpr int NQ = 2, SLOTS = LY::SLOTS;
     extern __shared__ __align__(1024) unsigned char kp_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(kp_raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ __align__(8) uint64_t kv_full[SLOTS], kv_empty[SLOTS], s_full[2], p_full[2], pv_done[2], meta_full[KP_META], all_done;
-    __shared__ KpMeta meta[KP_META][KP_KEYS / 16];
+    __shared__ __align__(8) uint64_t kv_full[SLOTS], kv_empty[SLOTS], s_full[4], p_full[2], pv_done[2], meta_full[KP_META], all_done;
+    __shared__ KpMeta meta[KP_META][KP_GROUPS];
     __shared__ float fac_s[NQ * KP_ROWS];
-    // what the threads of a row tell one another: maxima (by tile parity), whether to stop, sums
-    __shared__ float row_s[2][LY::TPR][NQ * KP_ROWS], sum_s[LY::TPR][NQ * KP_ROWS];
-    __shared__ int stop_s[2][LY::TPR][NQ * 4];
     __shared__ uint32_t marks[KP_MARKS];
     __shared__ uint32_t tmem;
     __shared__ int aborted, marked;
@@ -246,7 +243,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     // tiles with the most positions first
     const long long base = (long long)((gridDim.x - 1 - blockIdx.x) / c.Hkv) * (NQ * KP_ROWS);
     if (base >= rows_q) return;
-    const int nact = NQ == 2 && base + KP_ROWS < rows_q ? 2 : 1;   // query tiles in use
+    const int nact = base + KP_ROWS < rows_q ? 2 : 1;   // query tiles in use
     const int p0 = row.len - row.n;
     const int tok0 = (int)(base / G), tok1 = (int)((min(base + NQ * KP_ROWS, rows_q) - 1) / G);
     const KpTiles tl = kp_tiles(p0 + tok0, p0 + tok1, p.window, p.sinks);
@@ -289,9 +286,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 const float2 f = unpack_h2(hi[e]);
                 lo[e] = pack_h2(a - f.x, b - f.y);
             }
-            unsigned char* q = sm + LY::Q + (m / KP_ROWS) * LY::TILE + (ch / 8) * KP_PANEL + kp_sw(m % KP_ROWS, ch % 8);
+            unsigned char* q = sm + LY::Q + (m / KP_ROWS) * (LY::PARTS * LY::QTILE) + (ch / 8) * KP_QPANEL + kp_sw(m % KP_ROWS, ch % 8);
             *reinterpret_cast<uint4*>(q) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            if constexpr (FINE) *reinterpret_cast<uint4*>(q + LY::TILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if constexpr (FINE) *reinterpret_cast<uint4*>(q + LY::QTILE) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             if (ch == 0) fac_s[m] = p.scale * KV8_LOG2E / up;
         }
     }
@@ -305,8 +302,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             mbar_init(&kv_empty[s], 1);
         }
         for (int x = 0; x < 2; ++x) {
-            mbar_init(&s_full[x], 1);
-            mbar_init(&p_full[x], 128 * LY::TPR);
+            mbar_init(&s_full[2 * x], 1);
+            mbar_init(&s_full[2 * x + 1], 1);
+            mbar_init(&p_full[x], 128);
             mbar_init(&pv_done[x], 1);
         }
         for (int x = 0; x < KP_META; ++x) mbar_init(&meta_full[x], 1);
@@ -328,24 +326,24 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     };
     if (warp >= KP_K_WARP && warp < KP_MMA_WARP) {
         // ---- K or V tiles: global e4m3 -> f16 operand tiles ----
-        regs_up<KP_REGS_CONV>();
-        constexpr int LOADS = HD / 16;                 // 16-byte loads of a thread: keys quad + 32 u, panel v
+        regs_down<KP_REGS_CONV>();
+        constexpr int KU = KP_KEYS / 32, LOADS = KU * (HD / 64);   // 16-byte loads of a thread: keys quad + 32 u of each panel
         auto convert = [&](auto is_v) {
             constexpr bool V = decltype(is_v)::value;
             const uint8_t* pool = V ? c.v : c.k;
             const int ct = tid & 127, quad = ct >> 2, q4 = ct & 3;
             const size_t in_group = (size_t)(quad & 15) * HD + q4 * 16;
-            // Four tiles at a time, lane 8 i + g knows of the 16 positions g of tile i: where they begin in the pool, in
+            // KP_BATCH tiles at a time, lane KP_GROUPS i + g knows of the 16 positions g of tile i: where they begin in the pool, in
             // 16 rows (-1: nowhere), and their scale bytes.  Both are read a batch ahead -- the page ids first, the
             // scales two tiles later -- so that no tile waits for them
             const int nb = c.page / c.block;
             int at = -1, at_next = -1, scales = 0, scales_next = 0;   // K's byte, V's << 8
             long long scale_at = 0;
             auto pages_ahead = [&](int j) {    // the batch that begins with tile j of this CTA
-                const int i = i0 + j + (lane >> 3);
+                const int i = i0 + j + lane / KP_GROUPS;
                 at_next = -1;
                 if (i >= i1) return;
-                const int kb = key0(i) + 16 * (lane & 7);
+                const int kb = key0(i) + 16 * (lane % KP_GROUPS);
                 if (kb >= tl.end || (kb + 15 < tl.low && kb >= p.sinks)) return;
                 const int slot = kb / c.page, off = kb - slot * c.page, page = kv8_page(c, p.b.err, r, slot);
                 if (page < 0) return;
@@ -359,11 +357,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             uint4 v[LOADS];
             auto load = [&](int j, int rows) {   // tile j, in rows' batch
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {    // keys quad + 32 u
-                    const int b = __shfl_sync(0xffffffffu, rows, (j & 3) * 8 + 2 * u + (quad >> 4));
+                for (int u = 0; u < KU; ++u) {
+                    const int b = __shfl_sync(0xffffffffu, rows, j % KP_BATCH * KP_GROUPS + 2 * u + (quad >> 4));
                     const uint4* src = reinterpret_cast<const uint4*>(pool + (size_t)b * (16 * HD) + in_group);
 #pragma unroll
-                    for (int n = 0; n < HD / 64; ++n) v[n * 4 + u] = b >= 0 ? __ldg(src + 4 * n) : make_uint4(0u, 0u, 0u, 0u);
+                    for (int n = 0; n < HD / 64; ++n) v[n * KU + u] = b >= 0 ? __ldg(src + 4 * n) : make_uint4(0u, 0u, 0u, 0u);
                 }
             };
             if (ntiles > 0) {
@@ -374,13 +372,13 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 load(0, at);
             }
             for (int j = 0; j < ntiles; ++j) {
-                if ((j & 3) == 0) pages_ahead(j + 4);
-                if ((j & 3) == 2) scales_ahead();
+                if (j % KP_BATCH == 0) pages_ahead(j + KP_BATCH);
+                if (j % KP_BATCH == 2) scales_ahead();
                 if (!V && warp == KP_K_WARP) {
-                    if (lane >> 3 == (j & 3)) {
+                    if (lane / KP_GROUPS == j % KP_BATCH) {
                         const int ve = (scales >> 8) - 127;
                         // the last reader of this entry, the softmax of tile j - KP_META, is done: the ring is shorter
-                        meta[j % KP_META][lane & 7] = at >= 0 ? KpMeta{pow2i((scales & 255) - 127), (float)ve, pow2i(-ve), 0.f}
+                        meta[j % KP_META][lane % KP_GROUPS] = at >= 0 ? KpMeta{pow2i((scales & 255) - 127), (float)ve, pow2i(-ve), 0.f}
                                                               : KpMeta{1.f, -INFINITY, 0.f, 0.f};
                     }
                     __syncwarp();
@@ -396,7 +394,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
 #pragma unroll
                         for (int u = 0; u < LOADS; ++u) {
                             const uint32_t n[4] = {nan_bytes(v[u].x), nan_bytes(v[u].y), nan_bytes(v[u].z), nan_bytes(v[u].w)};
-                            const int key = key0(i0 + j) + quad + 32 * (u % 4);
+                            const int key = key0(i0 + j) + quad + 32 * (u % KU);
                             if ((n[0] | n[1] | n[2] | n[3]) && key < tl.end && (key >= tl.low || key < p.sinks)) seen = true;
                             v[u].x &= ~((n[0] >> 7) * 0xFFu);
                             v[u].y &= ~((n[1] >> 7) * 0xFFu);
@@ -419,13 +417,13 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     e4m3x4_to_f16(v[u].y, a[2], a[3]);
                     e4m3x4_to_f16(v[u].z, b[0], b[1]);
                     e4m3x4_to_f16(v[u].w, b[2], b[3]);
-                    unsigned char* d = tile + u / 4 * KP_PANEL;
-                    *reinterpret_cast<uint4*>(d + kp_sw(quad + 32 * (u % 4), 2 * q4)) = make_uint4(a[0], a[1], a[2], a[3]);
-                    *reinterpret_cast<uint4*>(d + kp_sw(quad + 32 * (u % 4), 2 * q4 + 1)) = make_uint4(b[0], b[1], b[2], b[3]);
+                    unsigned char* d = tile + u / KU * KP_PANEL;
+                    *reinterpret_cast<uint4*>(d + kp_sw(quad + 32 * (u % KU), 2 * q4)) = make_uint4(a[0], a[1], a[2], a[3]);
+                    *reinterpret_cast<uint4*>(d + kp_sw(quad + 32 * (u % KU), 2 * q4 + 1)) = make_uint4(b[0], b[1], b[2], b[3]);
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(&kv_full[s % SLOTS]);
-                const bool turn = (j & 3) == 3;   // tile j + 1 lies in the next batch
+                const bool turn = j % KP_BATCH == KP_BATCH - 1;   // tile j + 1 lies in the next batch
                 if (turn) {
                     at = at_next;
                     scales = scales_next;
@@ -440,7 +438,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         // ---- MMA issuer ----
         regs_down<KP_REGS_MMA>();
         if (warp == KP_MMA_WARP && ntiles > 0) {
-            constexpr uint32_t id_s = kp_idesc(KP_KEYS, false), id_o = kp_idesc(HD, true), STEP = LY::TILE >> 4;
+            constexpr uint32_t id_s = kp_idesc(KP_KEYS, false), id_o = kp_idesc(HD, true);
             const uint32_t dtu = __shfl_sync(0xffffffffu, dt, 0);
             const int nt = __shfl_sync(0xffffffffu, ntiles, 0);
             const uint32_t qd = kp_desc(smem_u32(sm + LY::Q), 16), kd = kp_desc(smem_u32(sm + LY::KV), 16),
@@ -450,80 +448,53 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 fence_after();
                 return there;
             };
-            auto qk = [&](auto tile, uint32_t scol, int j) {   // S of a query tile and tile j
-                const uint32_t kt = kd + (uint32_t)((2 * j) % SLOTS) * STEP, qt = qd + decltype(tile)::value * STEP;
+            auto qk = [&](auto tile, int j) {   // S of query tile x and tile j, into buffer j & 1
+                constexpr int x = decltype(tile)::value;
+                const uint32_t kt = kd + (uint32_t)((2 * j) % SLOTS) * (LY::TILE >> 4), qt = qd + x * (LY::PARTS * LY::QTILE >> 4);
+                const uint32_t scol = dtu + 128 * x + 64 * (j & 1);
 #pragma unroll
                 for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t o = (uint32_t)(kk / 4 * KP_PANEL + 32 * (kk % 4)) >> 4;
-                    mma_ss(scol, qt + o, kt + o, id_s, kk > 0);
-                    if constexpr (FINE) mma_ss(scol, qt + STEP + o, kt + o, id_s, 1);
+                    const uint32_t qo = (uint32_t)(kk / 4 * KP_QPANEL + 32 * (kk % 4)) >> 4, ko = (uint32_t)(kk / 4 * KP_PANEL + 32 * (kk % 4)) >> 4;
+                    mma_ss(scol, qt + qo, kt + ko, id_s, kk > 0);
+                    if constexpr (FINE) mma_ss(scol, qt + (LY::QTILE >> 4) + qo, kt + ko, id_s, 1);
                 }
+                kp_commit(&s_full[2 * x + (j & 1)]);
             };
-            auto pv = [&](uint32_t pcol, uint32_t ocol, int j) {   // bf16 q: the second half of P lies 64 columns on
-                const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * STEP;
+            auto pv = [&](auto tile, int j) {
+                constexpr int x = decltype(tile)::value;
+                const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * (LY::TILE >> 4);
+                const uint32_t pcol = dtu + 128 * x + 64 * (j & 1), ocol = dtu + LY::O + HD * x;
 #pragma unroll
                 for (int kk = 0; kk < KP_KEYS / 16; ++kk) {
-                    mma_ts(ocol, pcol + kk * 8 + (!FINE && kk >= 4 ? 32 : 0), vt + 128 * kk, id_o, kk > 0 ? 1u : (uint32_t)(j > 0));
-                    if constexpr (FINE) mma_ts(ocol, pcol + 64 + kk * 8, vt + 128 * kk, id_o, 1);
+                    mma_ts(ocol, pcol + kk * 8, vt + 128 * kk, id_o, kk > 0 ? 1u : (uint32_t)(j > 0));
+                    if constexpr (FINE) mma_ts(ocol, pcol + 32 + kk * 8, vt + 128 * kk, id_o, 1);
                 }
+                kp_commit(&pv_done[x]);
             };
             auto full = [&](int s) { return wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
             constexpr std::integral_constant<int, 0> A{};
+            constexpr std::integral_constant<int, 1> B{};
+            const bool two = nact == 2;
             bool ok = full(0);
-            if constexpr (!FINE) {
-                constexpr std::integral_constant<int, 1> B{};
-                const bool two = nact == 2;
-                const uint32_t sa = dtu + LY::S0, sb = dtu + LY::S1, oa = dtu + LY::O0, ob = dtu + LY::O0 + HD;
-                if (ok) {
-                    qk(A, sa, 0);
-                    kp_commit(&s_full[0]);
-                    if (two) {
-                        qk(B, sb, 0);
-                        kp_commit(&s_full[1]);
-                    }
-                    kp_commit(&kv_empty[0]);
+            if (ok) {
+                qk(A, 0);
+                if (two) qk(B, 0);
+                kp_commit(&kv_empty[0]);
+            }
+            for (int j = 0; j < nt && ok; ++j) {
+                if (j + 1 < nt) {   // the other buffers: their P have been multiplied, in order
+                    if (!(ok = full(2 * j + 2))) break;
+                    qk(A, j + 1);
+                    if (two) qk(B, j + 1);
+                    kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
                 }
-                for (int j = 0; j < nt && ok; ++j) {
-                    const bool more = j + 1 < nt;
-                    if (!(ok = full(2 * j + 1) && wait(&p_full[0], (uint32_t)j & 1u))) break;
-                    pv(sa, oa, j);
-                    kp_commit(&pv_done[0]);
-                    if (!two) kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
-                    if (more) {
-                        if (!(ok = full(2 * j + 2))) break;
-                        qk(A, sa, j + 1);
-                        kp_commit(&s_full[0]);
-                        if (!two) kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
-                    }
-                    if (!two) continue;
+                if (!(ok = full(2 * j + 1) && wait(&p_full[0], (uint32_t)j & 1u))) break;
+                pv(A, j);
+                if (two) {
                     if (!(ok = wait(&p_full[1], (uint32_t)j & 1u))) break;
-                    pv(sb, ob, j);
-                    kp_commit(&pv_done[1]);
-                    kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
-                    if (more) {
-                        qk(B, sb, j + 1);
-                        kp_commit(&s_full[1]);
-                        kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
-                    }
+                    pv(B, j);
                 }
-            } else {
-                if (ok) {
-                    qk(A, dtu + LY::S0, 0);
-                    kp_commit(&s_full[0]);
-                    kp_commit(&kv_empty[0]);
-                }
-                for (int j = 0; j < nt && ok; ++j) {
-                    if (j + 1 < nt) {   // the other S: its scores were read before P of tile j - 1 was full
-                        if (!(ok = full(2 * j + 2))) break;
-                        qk(A, dtu + ((j + 1) & 1 ? LY::S1 : LY::S0), j + 1);
-                        kp_commit(&s_full[(j + 1) & 1]);
-                        kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
-                    }
-                    if (!(ok = full(2 * j + 1) && wait(&p_full[0], (uint32_t)j & 1u))) break;
-                    pv(dtu + LY::NEXT, dtu + LY::O0, j);
-                    kp_commit(&pv_done[0]);
-                    kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
-                }
+                kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
             }
             // every MMA issued has finished before TMEM is released (also after a give-up)
             kp_commit(&all_done);
@@ -532,15 +503,14 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         __syncwarp();
         cta_meet();
     } else {
-        // ---- softmax: warp w reads TMEM lanes 32 (w % 4) + lane.  TPR threads, in as many warps, share a row of
-        // query tile x; each takes COLS positions of a tile and HD / TPR columns of O ----
-        constexpr int TPR = LY::TPR, COLS = LY::COLS, CH = COLS / 32;
-        const int x = warp / (4 * TPR), part = warp / 4 % TPR, m = (warp & 3) * 32 + lane;
+        // ---- softmax: warp w reads TMEM lanes 32 (w % 4) + lane, the rows of query tile w / 4 ----
+        regs_up<KP_REGS_SOFTMAX>();
+        const int x = warp / 4, m = (warp & 3) * 32 + lane;
         const long long mq = base + x * KP_ROWS + m;
         const bool live = x < nact && mq < rows_q;
         const int tk = (int)((live ? mq : base) / G), hq = h * G + (int)((live ? mq : base) % G), pos = live ? p0 + tk : -1;
         const uint32_t lrow = dt + ((uint32_t)((warp & 3) * 32) << 16);
-        const uint32_t ocol = lrow + LY::O0 + (uint32_t)(HD * x + HD / TPR * part);
+        const uint32_t ocol = lrow + LY::O + (uint32_t)(HD * x);
         float M = -INFINITY, l = 0.f;
         bool ok = true;
         const float fac = ntiles > 0 ? fac_s[x * KP_ROWS + m] : 0.f;
@@ -548,73 +518,52 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         const int xmin = p0 + (int)((base + x * KP_ROWS) / G);
         const int xmax = p0 + (int)((min(base + (x + 1) * KP_ROWS, rows_q) - 1) / G);
         const int lo = (int)max((long long)pos - p.window + 1, 0ll);   // this row sees [lo, pos] and [0, sinks)
-        auto row_meet = [&]() { named_sync(1 + x * 4 + (warp & 3), 32 * TPR); };
         for (int j = 0; j < (x < nact ? ntiles : 0); ++j) {
-            const int k0 = key0(i0 + j) + part * COLS;
-            const int sb = FINE ? j & 1 : x;
-            ok = ok && warp_wait(&s_full[sb], (uint32_t)(FINE ? j >> 1 : j) & 1u, ab, p.b.err) &&
+            const int k0 = key0(i0 + j);
+            ok = warp_wait(&s_full[2 * x + (j & 1)], (uint32_t)(j >> 1) & 1u, ab, p.b.err) &&
                  warp_wait(&meta_full[j % KP_META], (uint32_t)(j / KP_META) & 1u, ab, p.b.err);
-            // P of fp32 q has columns of its own: free once the last tile's P V is done
-            if (FINE && j > 0) ok = ok && warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err);
+            if (!ok) break;
             fence_after();
-            const uint32_t scol = lrow + (sb ? LY::S1 : LY::S0) + part * COLS;
-            const KpMeta* mt = meta[j % KP_META] + part * (COLS / 16);
+            const uint32_t scol = lrow + 128 * x + 64 * (j & 1);
+            const KpMeta* mt = meta[j % KP_META];
+            uint32_t v[2][32];
+            tm_ld32(scol, v[0]);
+            tm_ld32(scol + 32, v[1]);
+            wait_ld();
             // some row of the query tile does not see some of these positions
-            const bool masked = !(xmin >= 0 && k0 + COLS - 1 <= xmin && (k0 > xmax - p.window || k0 + COLS - 1 < p.sinks));
-            auto mask = [&](uint32_t (&v)[32], int q) {
-                // bit e: position k0 + 32 q + e is one that this row sees
-                auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
-                const int kq = k0 + 32 * q;
-                const uint32_t see = below(pos + 1 - kq) & (~below(lo - kq) | below(p.sinks - kq));
+            if (!(xmin >= 0 && k0 + KP_KEYS - 1 <= xmin && (k0 > xmax - p.window || k0 + KP_KEYS - 1 < p.sinks))) {
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = see >> e & 1u ? v[e] : 0xFF800000u;
-            };
-            uint32_t v[32];
-            float top = -INFINITY;
-            if (ok) {
+                for (int q = 0; q < 2; ++q) {
+                    // bit e: position k0 + 32 q + e is one that this row sees
+                    auto below = [&](int n) { return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u; };
+                    const int kq = k0 + 32 * q;
+                    const uint32_t see = below(pos + 1 - kq) & (~below(lo - kq) | below(p.sinks - kq));
 #pragma unroll
-                for (int q = 0; q < CH; ++q) {
-                    tm_ld32(scol + 32 * q, v);
-                    wait_ld();
-                    if (masked) mask(v, q);
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        auto f = [&](int e) { return __uint_as_float(v[16 * b + e]); };
-                        const float t0 = max3(f(0), f(1), f(2)), t1 = max3(f(3), f(4), f(5)), t2 = max3(f(6), f(7), f(8));
-                        const float t3 = max3(f(9), f(10), f(11)), t4 = max3(f(12), f(13), f(14));
-                        const KpMeta k = mt[2 * q + b];
-                        top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), kp_mul(fac, k.kf), k.ve));
-                    }
+                    for (int e = 0; e < 32; ++e) v[q][e] = see >> e & 1u ? v[q][e] : 0xFF800000u;
                 }
             }
-            // The row's maximum (the buffer of two tiles ago has been read by all).  The warps of a row leave the
-            // loop together: none may wait for one that has given up
-            row_s[j & 1][part][x * KP_ROWS + m] = top;
-            if (lane == 0) stop_s[j & 1][part][x * 4 + (warp & 3)] = !ok;
-            row_meet();
-            int stop = 0;
+            float top = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < TPR; ++q) stop |= stop_s[j & 1][q][x * 4 + (warp & 3)];
-            if (__any_sync(0xffffffffu, stop)) {
-                ok = false;
-                break;
+            for (int b = 0; b < KP_GROUPS; ++b) {
+                auto f = [&](int e) { return __uint_as_float(v[b / 2][b % 2 * 16 + e]); };
+                const float t0 = max3(f(0), f(1), f(2)), t1 = max3(f(3), f(4), f(5)), t2 = max3(f(6), f(7), f(8));
+                const float t3 = max3(f(9), f(10), f(11)), t4 = max3(f(12), f(13), f(14));
+                const KpMeta k = mt[b];
+                top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), kp_mul(fac, k.kf), k.ve));
             }
-#pragma unroll
-            for (int q = 0; q < TPR; ++q) top = fmaxf(top, row_s[j & 1][q][x * KP_ROWS + m]);
             float alpha = 1.f;
+            bool rested = j == 0;   // P V of tile j - 1 is done
             if (top > M + KP_SLACK) {
                 if (M != -INFINITY) alpha = kv8_exp2(M - top);   // else nothing has been summed yet
                 M = top;
                 l *= alpha;
             }
             if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                if (!FINE) {   // O must be at rest
-                    ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err);
-                    if (!ok) continue;   // and stop with the others
-                    fence_after();
-                }
+                if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
+                rested = true;
+                fence_after();
 #pragma unroll 1
-                for (int cc = 0; cc < HD / TPR; cc += 16) {
+                for (int cc = 0; cc < HD; cc += 16) {
                     uint32_t o[16];
                     tm_ld16(ocol + cc, o);
                     wait_ld();
@@ -625,12 +574,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             }
             const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
 #pragma unroll
-            for (int q = 0; q < CH; ++q) {
-                if (CH > 1) {
-                    tm_ld32(scol + 32 * q, v);
-                    wait_ld();
-                    if (masked) mask(v, q);
-                }
+            for (int q = 0; q < 2; ++q) {
                 uint32_t hi[16], low[FINE ? 16 : 1];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
@@ -641,7 +585,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         float w0, w1;
-                        unpair(fma2(pair(__uint_as_float(v[16 * b + e]), __uint_as_float(v[16 * b + e + 1])), mul2, plus2), w0, w1);
+                        unpair(fma2(pair(__uint_as_float(v[q][16 * b + e]), __uint_as_float(v[q][16 * b + e + 1])), mul2, plus2), w0, w1);
                         w0 = kv8_exp2(w0);
                         w1 = kv8_exp2(w1);
                         if (e & 2) sum1 = add2(sum1, pair(w0, w1));
@@ -657,14 +601,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     unpair(add2(sum0, sum1), a0, a1);
                     l = fmaf(a0 + a1, k.vinv, l);
                 }
-                if constexpr (FINE) {
-                    tm_st16(lrow + LY::NEXT + part * 16, hi);
-                    tm_st16(lrow + LY::NEXT + 64 + part * 16, low);
-                } else {
-                    tm_st16(scol + 16 * q, hi);   // over scores that this thread has read
-                }
+                tm_st16(scol + 16 * q, hi);   // over the scores, which this thread holds
+                if constexpr (FINE) tm_st16(scol + 32 + 16 * q, low);
             }
             wait_st();
+            // every tile's P V is waited for once: a parity tells a phase only from the one before it
+            if (!rested && !(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
             fence_before();
             mbar_arrive(&p_full[x]);
         }
@@ -672,18 +614,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             ok = warp_wait(&pv_done[x], (uint32_t)(ntiles - 1) & 1u, ab, p.b.err);
             fence_after();
         }
-        if (x < nact) sum_s[part][x * KP_ROWS + m] = l;
         cta_meet();   // every tile has been converted: the marks are complete
         if (x < nact && ok) {
-            constexpr int OC = HD / TPR, NW = (OC + 31) / 32;
-            const int c0 = OC * part;   // this thread's columns
-            l = 0.f;
-#pragma unroll
-            for (int q = 0; q < TPR; ++q) l += sum_s[q][x * KP_ROWS + m];
             // NaN in V that this row sees: a bit for each column
-            uint32_t nan[NW];
+            uint32_t nan[HD / 32];
 #pragma unroll
-            for (int d = 0; d < NW; ++d) nan[d] = 0u;
+            for (int d = 0; d < HD / 32; ++d) nan[d] = 0u;
             if (marked) {
                 for (int j = i0; j < i1; ++j) {
                     if (!(marks[j / 32 % KP_MARKS] >> (j & 31) & 1u)) continue;
@@ -692,12 +628,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                         if (!kv8_sees(pos, key, p.window, p.sinks)) continue;
                         const int id = c.pages ? c.pages[(size_t)r * c.ppr + key / c.page] : r * c.ppr + key / c.page;
                         if ((unsigned)id >= (unsigned)c.num_pages) continue;
-                        const uint32_t* v = reinterpret_cast<const uint32_t*>(
-                            c.v + (((size_t)id * c.Hkv + h) * c.page + key % c.page) * HD + c0);
+                        const uint32_t* w = reinterpret_cast<const uint32_t*>(
+                            c.v + (((size_t)id * c.Hkv + h) * c.page + key % c.page) * HD);
 #pragma unroll
-                        for (int d = 0; d < NW; ++d)
-                            for (int e = 0; e < (OC < 32 ? OC : 32) / 4; ++e) {
-                                const uint32_t n = nan_bytes(__ldg(v + 8 * d + e)) >> 7;   // bits 0, 8, 16, 24
+                        for (int d = 0; d < HD / 32; ++d)
+                            for (int e = 0; e < 8; ++e) {
+                                const uint32_t n = nan_bytes(__ldg(w + 8 * d + e)) >> 7;   // bits 0, 8, 16, 24
                                 nan[d] |= ((n & 1u) | (n >> 7 & 2u) | (n >> 14 & 4u) | (n >> 21 & 8u)) << (4 * e);
                             }
                     }
@@ -706,10 +642,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             // the result, or this split's part of it
             const float inv = l == 0.f ? 0.f : 1.f / l;
             const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq, all_rows = (size_t)p.b.total * p.Hq;
-            T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD + c0;
-            float* piece = p.ws + (sp * all_rows + qrow) * HD + c0;
+            T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD;
+            float* piece = p.ws + (sp * all_rows + qrow) * HD;
 #pragma unroll
-            for (int cc = 0; cc < OC; cc += 16) {
+            for (int cc = 0; cc < HD; cc += 16) {
                 uint32_t o[16];
                 if (ntiles > 0) {
                     tm_ld16(ocol + cc, o);
@@ -741,7 +677,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                                                                              pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
                 }
             }
-            if (splits > 1 && live && part == 0) {
+            if (splits > 1 && live) {
                 float* ml = p.ws + (size_t)splits * all_rows * HD + (sp * all_rows + qrow) * 2;
                 ml[0] = M;
                 ml[1] = l;
@@ -787,19 +723,19 @@ __global__ void __launch_bounds__(256) k_kv8_prompt_join(const Kv8Attend p, int 
 }
 
 long long prompt_tiles(const Kv8Attend& p) {   // query tiles (of one CTA) of the longest row
-    const int per = (p.dtype == W_F32 ? 1 : 2) * KP_ROWS;
+    const int per = 2 * KP_ROWS;
     return ((long long)p.b.max_new * (p.Hq / p.c.Hkv) + per - 1) / per;
 }
 
 // Splits of a query tile's positions: as many as bring the CTAs to the SMs'
-// count, each with at least 4 tiles of the most positions that a tile may see
+// count, each with at least 8 tiles of the most positions that a tile may see
 int prompt_splits(const Kv8Attend& p, int num_sms) {
     const long long ctas = prompt_tiles(p) * p.c.Hkv * p.c.rows;
     long long keys = (long long)p.c.ppr * p.c.page;
     const long long win = (long long)p.window + p.sinks + 2 * KP_KEYS + p.b.max_new;
     if (win < keys) keys = win;
     long long s = num_sms / ctas;
-    if (s > keys / (4 * KP_KEYS)) s = keys / (4 * KP_KEYS);
+    if (s > keys / (8 * KP_KEYS)) s = keys / (8 * KP_KEYS);
     if (s > 32) s = 32;
     return s < 1 ? 1 : (int)s;
 }
