@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <atomic>
 #include "graphdec.h"
 
 namespace gd {
@@ -271,6 +272,21 @@ cudaError_t prefill_run(PrefillState* s, const int* tokens, int n, int pos0, int
                         cudaStream_t st);
 
 // ---------------- the 8-bit K/V cache (kv8*.cu) ----------------
+constexpr int KV8_MAX_ROWS = 1024;
+// what a kernel needs to be told once on each device (a race only tells it twice)
+struct OncePerDevice {
+    std::atomic<unsigned long long> done{0};
+    template <typename F>
+    cudaError_t run(F f) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+        if ((e = f()) == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
 struct Kv8Cache {              // a dec_kv8_cache that passed its checks
     uint8_t *k, *v;            // [num_pages, Hkv, page, hd] e4m3
     uint8_t *ks, *vs;          // [num_pages, Hkv, page / block] exponent + 127
@@ -299,6 +315,7 @@ struct Kv8Attend {
     int dtype, Hq;
     int window, sinks;         // window INT_MAX: every position up to the token's own
     float scale;
+    int* counters;             // [rows, Hkv], zero between calls
     float* ws;                 // kv8_decode_floats() or kv8_prompt_floats() floats
 };
 cudaError_t kv8_append_launch(const Kv8Append& p, cudaStream_t s);

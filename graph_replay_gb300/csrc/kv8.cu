@@ -15,7 +15,6 @@ using namespace gd;
 
 namespace {
 
-constexpr int KV8_MAX_ROWS = 1024;
 constexpr int64_t KV8_MAX_CAP = 1 << 30;
 
 int refuse(int code, const char* fmt, ...) {
@@ -119,8 +118,10 @@ int check_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const d
     return DEC_OK;
 }
 
+// the counters, then the floats
+size_t counter_bytes(const Kv8Cache& c) { return ((size_t)c.rows * c.Hkv * sizeof(int) + 255) / 256 * 256; }
 size_t attend_bytes(const Kv8Attend& p, int sms) {
-    return sizeof(float) * (kv8_decode_takes(p) ? kv8_decode_floats(p, sms) : kv8_prompt_floats(p, sms));
+    return counter_bytes(p.c) + sizeof(float) * (kv8_decode_takes(p) ? kv8_decode_floats(p, sms) : kv8_prompt_floats(p, sms));
 }
 
 int sms_of(int device, int* n) {
@@ -176,11 +177,12 @@ int dec_kv8_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const
     if (p.b.total == 0) return DEC_OK;
     if ((rc = sms_of(cache->device, &sms)) != DEC_OK) return rc;
     const size_t need = attend_bytes(p, sms);
-    if (need && (!attn->workspace || attn->workspace_bytes < need))
+    if (!attn->workspace || attn->workspace_bytes < need)
         return refuse(DEC_E_OOM, "workspace of %zu bytes is smaller than the %zu needed",
                       attn->workspace ? attn->workspace_bytes : (size_t)0, need);
     if (!aligned16(attn->workspace)) return refuse(DEC_E_INVALID, "workspace must be 16-byte aligned");
-    p.ws = (float*)attn->workspace;
+    p.counters = (int*)attn->workspace;
+    p.ws = (float*)((char*)attn->workspace + counter_bytes(p.c));
     OnDevice on(cache->device);
     if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
     const cudaStream_t s = (cudaStream_t)stream;

@@ -27,36 +27,40 @@
 //   * the maximum is kept within a factor 2^8 of the true one (weights are
 //     scaled by 2^6, f16 holds 2^14), so a 16-key step needs one vote and
 //     almost never a reduction or a rescaling;
-//   * work: the visible 64-key tiles of all rows and K/V heads, in one line, cut
-//     into equal pieces: one for each resident CTA, whatever the lengths are.
-//     Windows make gaps in a row's tiles that are never touched.  A (row, head)
-//     that is cut leaves partial results, which a second kernel joins in order.
+//   * work: the visible 16-key steps of each row and K/V head (windows make gaps
+//     that are never touched).  Where the SMs suffice, each (row, head) is cut into
+//     pieces of its own, of at least two steps a warp, so short rows are not cut.
+//     Otherwise all steps, in one line, are cut into equal pieces, one for each SM,
+//     whatever the lengths are.  A
+//     (row, head) that is cut leaves partial results in the workspace; the CTA that
+//     finishes it last joins them, in the order of the pieces, and sets its counter
+//     back to 0.
 #include <limits.h>
+#include <type_traits>
 #include "kv8.cuh"
+#include "mma_helpers.cuh"
 
 namespace gd {
 
 namespace {
 
-constexpr int KD_THREADS = 128, KD_WARPS = 4;
-constexpr int KD_TILE = 64;           // positions of a unit of work: 16 for each warp
+constexpr int KD_STEP = 16;           // positions of a step: the unit of work
 constexpr float KD_SLACK = 8.f;       // how far the maximum may lag (log2)
 constexpr float KD_SHIFT = 6.f;       // weights carry 2^6
-constexpr int KD_MAX_ROWS = 1024;       // as the C ABI allows
 
-// The tiles of a row: its first `sink` tiles, then `gap` tiles that no token
-// sees, then the rest; n of them are visible to one of its tokens.
-struct KdTiles {
+// The steps of a row: its first `sink` steps, then `gap` that no token sees,
+// then the rest; n of them are visible to one of its tokens.
+struct KdSteps {
     int n, sink, gap;
 };
-__device__ __forceinline__ KdTiles kd_tiles(const Kv8Row& row, int window, int sinks) {
-    if (row.n == 0) return KdTiles{0, 0, 0};
-    const int end = (row.len + KD_TILE - 1) / KD_TILE;
+__device__ __forceinline__ KdSteps kd_steps(const Kv8Row& row, int window, int sinks) {
+    if (row.n == 0) return KdSteps{0, 0, 0};
+    const int end = (row.len + KD_STEP - 1) / KD_STEP;
     const int first = max(row.len - row.n, 0);
-    const int low = (int)max((long long)first - window + 1, 0ll) / KD_TILE;   // the first token's window begins here
-    const int sink = (min(sinks, row.len) + KD_TILE - 1) / KD_TILE;
-    if (sink >= low) return KdTiles{max(end, 1), end, 0};   // a row without positions has one tile with nothing in it
-    return KdTiles{sink + end - low, sink, low - sink};
+    const int low = (int)max((long long)first - window + 1, 0ll) / KD_STEP;   // the first token's window begins here
+    const int sink = (min(sinks, row.len) + KD_STEP - 1) / KD_STEP;
+    if (sink >= low) return KdSteps{max(end, 1), end, 0};   // a row without positions has one step with nothing in it
+    return KdSteps{sink + end - low, sink, low - sink};
 }
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -78,45 +82,82 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-// where the pieces of work lie: pre[r] = tiles of the rows before r
-struct KdPlan {
-    int pre[KD_MAX_ROWS + 1];
-    int warp_sum[KD_WARPS];
-};
-__device__ __forceinline__ void kd_plan(const Kv8Attend& p, KdPlan& s) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = p.c.rows, cap = p.c.ppr * p.c.page;
-    const int per = (rows + KD_THREADS - 1) / KD_THREADS, r0 = min(tid * per, rows), r1 = min(r0 + per, rows);
-    int sum = 0;
-    for (int r = r0; r < r1; ++r) {
-        Kv8Row row;
-        s.pre[r] = sum;
-        if (kv8_row(p.b, cap, r, &row)) sum += kd_tiles(row, p.window, p.sinks).n;
+// a / b for a >= 0: most numbers here fit 32 bits, and a 64-bit division costs a short call half a microsecond
+__device__ __forceinline__ long long quotient(long long a, int b) {
+    return (a >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+// The work cut into pieces.  own: pieces of one (row, head) each; else the line of units in pieces of q or q + 1
+struct KdCut {
+    bool own;
+    int pieces, rem;
+    long long units, q;
+    __device__ __forceinline__ long long begin(int c) const { return q * c + min(c, rem); }
+    __device__ __forceinline__ int piece_of(long long u) const {
+        const long long lead = (q + 1) * rem;   // q < 2^31: a piece is a part of one SM's work
+        return u < lead ? (int)quotient(u, (int)q + 1) : rem + (int)quotient(u - lead, (int)q);
     }
-    int inc = sum;
+};
+// sum of v over the threads before this one; *all: over all threads.  s: W entries
+template <int W>
+__device__ __forceinline__ long long sum_before(long long v, long long* s, long long* all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    long long inc = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += x;
     }
-    if (lane == 31) s.warp_sum[warp] = inc;
+    if (lane == 31) s[warp] = inc;
     __syncthreads();
-    int before = inc - sum;
-    for (int w = 0; w < warp; ++w) before += s.warp_sum[w];
-    for (int r = r0; r < r1; ++r) s.pre[r] += before;
-    if (tid == KD_THREADS - 1) s.pre[rows] = before + sum;
+    long long before = inc - v, total = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+        if (w < warp) before += s[w];
+        total += s[w];
+    }
+    *all = total;
+    return before;
+}
+// pre[r], cuts[r]: steps, and pieces of a head (own), of the rows before r
+template <int W>
+__device__ __forceinline__ KdCut kd_plan(const Kv8Attend& p, int grid, long long* pre, int* cuts, long long (*sums)[W]) {
+    const int tid = threadIdx.x, rows = p.c.rows, cap = p.c.ppr * p.c.page;
+    const int per = (rows + 32 * W - 1) / (32 * W), r0 = min(tid * per, rows), r1 = min(r0 + per, rows);
+    long long sum = 0;
+    for (int r = r0; r < r1; ++r) {
+        Kv8Row row;
+        pre[r] = kv8_row(p.b, cap, r, &row) ? kd_steps(row, p.window, p.sinks).n : 0;
+        sum += pre[r];
+    }
+    KdCut cut;
+    long long all, all_cuts, before = sum_before<W>(sum, sums[0], &all);
+    cut.units = all * p.c.Hkv;
+    // steps of a row's own pieces: an eighth of the SMs may stay without work for them
+    const int least = (int)max(2ll * W, quotient(cut.units * 9 + 8 * grid - 1, 8 * grid));
+    long long mine = 0;
+    for (int r = r0; r < r1; ++r) {
+        const int n = (int)pre[r];
+        pre[r] = before;
+        before += n;
+        cuts[r] = (n + least - 1) / least;
+        mine += cuts[r];
+    }
+    long long at = sum_before<W>(mine, sums[1], &all_cuts);
+    for (int r = r0; r < r1; ++r) {
+        const int n = cuts[r];
+        cuts[r] = (int)at;
+        at += n;
+    }
+    if (tid == 0) {
+        pre[rows] = all;
+        cuts[rows] = (int)all_cuts;
+    }
     __syncthreads();
-}
-// of n pieces, piece c takes the units [begin(c), begin(c + 1)); a piece has at
-// least two tiles where the grid allows it, so short rows are not cut to crumbs
-__device__ __forceinline__ int kd_pieces(long long units, int grid) {
-    return (int)min((long long)grid, max((units + 1) / 2, 1ll));
-}
-__device__ __forceinline__ long long kd_begin(long long units, int pieces, int c) { return units * c / pieces; }
-__device__ __forceinline__ int kd_piece_of(long long units, int pieces, long long u) {
-    int c = (int)(u * pieces / units);
-    while (c + 1 < pieces && kd_begin(units, pieces, c + 1) <= u) ++c;
-    while (c > 0 && kd_begin(units, pieces, c) > u) --c;
-    return c;
+    cut.own = all_cuts * p.c.Hkv <= grid;
+    cut.pieces = cut.own ? (int)all_cuts * p.c.Hkv : grid;
+    cut.q = quotient(cut.units, grid);   // at least 1 where it is used: more units than pieces
+    cut.rem = (int)(cut.units - cut.q * grid);
+    return cut;
 }
 template <int HD, int MT>
 __host__ __device__ constexpr int kd_slot_floats() { return MT * 8 * (HD + 2); }   // O, then M, then l of each query row
@@ -139,81 +180,99 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // dynamic shared memory: the rings; when the loop is done the warps' results lie over them
 template <int HD, int MT>
 struct KdShared {
-    static constexpr int STEP = 2 * 16 * HD, STAGES = 512 / HD;   // 16 KB a warp
-    static constexpr int RING = KD_WARPS * STAGES * STEP, OUT = KD_WARPS * MT * 8 * HD * (int)sizeof(float);
+    static constexpr int W = MT == 1 ? 12 : 8;            // warps: what the registers allow, one CTA on an SM
+    static constexpr int STEP = 2 * KD_STEP * HD, STAGES = 512 / HD;   // 16 KB a warp
+    static constexpr int RING = W * STAGES * STEP, OUT = W * MT * 8 * HD * (int)sizeof(float);
     static constexpr int BYTES = RING > OUT ? RING : OUT;
 };
 
 // MT: query rows / 8 (up).  FINE: fp32 q -- second f16 parts of q and of the weights.
 template <int HD, int MT, bool FINE>
-__global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(const Kv8Attend p) {
+__global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(const Kv8Attend p) {
     using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
     constexpr int NK = HD / 16;   // 16-dim steps of S, 16-dim tiles of O
-    constexpr int PARTS = FINE ? 2 : 1, STAGES = KdShared<HD, MT>::STAGES;
-    __shared__ KdPlan plan;
+    constexpr int PARTS = FINE ? 2 : 1, STAGES = KdShared<HD, MT>::STAGES, W = KdShared<HD, MT>::W;
     extern __shared__ __align__(128) unsigned char kd_raw[];
     float(*o_s)[MT * 8][HD] = reinterpret_cast<float(*)[MT * 8][HD]>(kd_raw);
     const unsigned char* ring_p = kd_raw + (threadIdx.x >> 5) * (STAGES * KdShared<HD, MT>::STEP);
     const uint32_t ring = smem_u32(ring_p);
-    __shared__ float m_s[KD_WARPS][MT * 8], l_s[KD_WARPS][MT * 8];
+    __shared__ long long pre[KV8_MAX_ROWS + 1], sums[2][W];
+    __shared__ int cuts[KV8_MAX_ROWS + 1], last_s;
+    __shared__ float m_s[W][MT * 8], l_s[W][MT * 8];
     __shared__ __align__(16) uint4 q_s[PARTS][MT][NK / 2][32];   // f16 parts of q, by step and lane
     __shared__ float fac_s[MT * 8];
-    __shared__ uint32_t nan_s[KD_WARPS][HD];
+    __shared__ uint32_t nan_s[W][HD];
     pdl_wait();
     const Kv8Cache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int G = p.Hq / c.Hkv, cap = c.ppr * c.page, nb = c.page / c.block;
-    kd_plan(p, plan);
-    const long long units = (long long)plan.pre[c.rows] * c.Hkv;
-    const int pieces = kd_pieces(units, gridDim.x);
-    if ((int)blockIdx.x >= pieces) return;
-    const long long u_end = kd_begin(units, pieces, blockIdx.x + 1);
-    const long long u_begin = kd_begin(units, pieces, blockIdx.x);
+    const KdCut cut = kd_plan<W>(p, gridDim.x, pre, cuts, sums);
+    if ((int)blockIdx.x >= cut.pieces) return;
+    // the last r with at[r] * Hkv <= u
+    auto row_of = [&](const auto* at, long long u) {
+        int r = 0, hi = c.rows;
+        while (r + 1 < hi) {
+            const int mid = (r + hi) >> 1;
+            if ((long long)at[mid] * c.Hkv <= u) r = mid;
+            else hi = mid;
+        }
+        return r;
+    };
+    const long long u_begin = cut.own ? 0 : cut.begin(blockIdx.x), u_end = cut.own ? 1 : cut.begin(blockIdx.x + 1);
 
     for (long long u = u_begin; u < u_end;) {
-        // the row of unit u: the last r with pre[r] * Hkv <= u
-        int r = 0;
-        {
-            int hi = c.rows;
-            while (r + 1 < hi) {
-                const int mid = (r + hi) >> 1;
-                if ((long long)plan.pre[mid] * c.Hkv <= u) r = mid;
-                else hi = mid;
-            }
-        }
+        // steps [i0, i1) of row r and K/V head h; a head that is cut has the pieces c0 .. c1
+        const int r = cut.own ? row_of(cuts, blockIdx.x) : row_of(pre, u);
         Kv8Row row;
         kv8_row(p.b, cap, r, &row);
-        const KdTiles tl = kd_tiles(row, p.window, p.sinks);
-        const long long u_row = (long long)plan.pre[r] * c.Hkv;
-        const int h = (int)((u - u_row) / tl.n), i0 = (int)((u - u_row) % tl.n);
-        const int i1 = (int)min((long long)tl.n, i0 + (u_end - u));
+        const KdSteps tl = kd_steps(row, p.window, p.sinks);
+        int h, i0, i1, c0, c1;
+        if (cut.own) {
+            const int n = cuts[r + 1] - cuts[r], at = blockIdx.x - cuts[r] * c.Hkv;
+            h = at / n;
+            c0 = cuts[r] * c.Hkv + h * n;
+            c1 = c0 + n - 1;
+            i0 = (int)quotient((long long)tl.n * (at - h * n), n);
+            i1 = (int)quotient((long long)tl.n * (at - h * n + 1), n);
+        } else {
+            const long long u_row = pre[r] * c.Hkv;
+            h = (int)quotient(u - u_row, tl.n);
+            i0 = (int)(u - u_row - (long long)h * tl.n);
+            i1 = (int)min((long long)tl.n, i0 + (u_end - u));
+            c0 = cut.piece_of(u - i0);
+            c1 = cut.piece_of(u - i0 + tl.n - 1);
+        }
         const int nq = row.n * G, p0 = row.len - row.n;   // query rows, the first token's position
 
         const int end = min(row.len, p0 + row.n);
         const int low = (int)max((long long)max(p0, 0) - p.window + 1, 0ll);   // no token of the row sees [sinks, low)
-        auto key0 = [&](int i) { return (i < tl.sink ? i : i + tl.gap) * KD_TILE + warp * 16; };
+        // this warp's steps: i0 + warp + k * W, k < mine
+        const int mine = max((i1 - i0 - warp + W - 1) / W, 0);
+        auto key0 = [&](int k) {
+            const int i = i0 + warp + k * W;
+            return (i < tl.sink ? i : i + tl.gap) * KD_STEP;
+        };
         auto wanted = [&](int kb) { return kb < end && (kb + 15 >= low || kb < p.sinks); };
-        // This warp's steps of 32 tiles, a tile for each lane: the page (-1: no step) and, packed, V's
-        // and K's scale bytes.  The copies run ahead of the arithmetic: it may still need the 32 before.
+        // 32 of them, one for each lane: the page (-1: no step) and, packed, V's and K's scale
+        // bytes.  The copies run ahead of the arithmetic: it may still need the 32 before.
         int pages = -1, scales = -1, scales_before = -1;
-        auto next32 = [&](int i) {
-            const int ii = (i & ~31) + lane;
+        auto next32 = [&](int k) {
             scales_before = scales;
             pages = scales = -1;
-            if (ii < i0 || ii >= i1) return;
-            const int kb = key0(ii);
+            if (k + lane >= mine) return;
+            const int kb = key0(k + lane);
             if (!wanted(kb)) return;
             pages = kv8_page(c, p.b.err, r, kb / c.page);
             if (pages < 0) return;
             const size_t at = ((size_t)pages * c.Hkv + h) * nb + kb % c.page / c.block;
             scales = (int)c.ks[at] | (int)c.vs[at] << 8;
         };
-        int ahead = i0;   // the next tile to copy
+        int ahead = 0;   // the next step to copy
         // one more step into the ring; one group a call, also for nothing
         auto copy_next = [&]() {
             const int i = ahead++;
-            if (i < i1) {
-                if ((i & 31) == 0 || i == i0) next32(i);
+            if (i < mine) {
+                if ((i & 31) == 0) next32(i);
                 const int page = __shfl_sync(0xffffffffu, pages, i & 31);
                 if (page >= 0) {
                     const size_t at = (((size_t)page * c.Hkv + h) * c.page + key0(i) % c.page) * HD;
@@ -462,13 +521,13 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
             }
         };
 
-        for (int i = i0; i < i1; ++i) {
+        for (int i = 0; i < mine; ++i) {
             copy_next();
-            copy_wait<STAGES - 1>();   // tile i's group is complete
-            __syncwarp();                 // for every lane's copies
-            const int sb = __shfl_sync(0xffffffffu, (i >> 5) == (min(ahead, i1) - 1) >> 5 ? scales : scales_before, i & 31);
+            copy_wait<STAGES - 1>();   // step i's group is complete
+            __syncwarp();              // for every lane's copies
+            const int sb = __shfl_sync(0xffffffffu, i >> 5 == (min(ahead, mine) - 1) >> 5 ? scales : scales_before, i & 31);
             if (sb >= 0) compute(i, sb);
-            __syncwarp();                 // the stage may be overwritten
+            __syncwarp();              // the stage may be overwritten
         }
         copy_wait<0>();
         __syncthreads();   // every warp is done with its ring
@@ -495,16 +554,22 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
                         make_float2(o[a][k][b], o[a][k][b + 2]);
         __syncthreads();
         const bool whole = i0 == 0 && i1 == tl.n;
-        float* slot = p.ws + ((size_t)blockIdx.x * 2 + (u == u_begin ? 0 : 1)) * kd_slot_floats<HD, MT>();
-        for (int x = tid; x < MT * 8 * (HD / 4); x += KD_THREADS) {
+        float* slots = p.ws;
+        float* slot = slots + ((size_t)blockIdx.x * 2 + (u == u_begin ? 0 : 1)) * kd_slot_floats<HD, MT>();
+        auto put = [&](int m, int d, float sum, const float (&y)[4]) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;   // nothing seen: zeros
+            T* dst = static_cast<T*>(p.out) + (row.t0 + m / G) * p.out_stride + (h * G + m % G) * HD + d;
+            if constexpr (FINE) *reinterpret_cast<float4*>(dst) = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+            else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv));
+        };
+        for (int x = tid; x < nq * (HD / 4); x += 32 * W) {
             const int m = x / (HD / 4), d = (x % (HD / 4)) * 4;
-            if (m >= nq) continue;   // no such query row
             float top = -INFINITY;
 #pragma unroll
-            for (int w = 0; w < KD_WARPS; ++w) top = fmaxf(top, m_s[w][m]);
+            for (int w = 0; w < W; ++w) top = fmaxf(top, m_s[w][m]);
             float sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < KD_WARPS; ++w) {
+            for (int w = 0; w < W; ++w) {
                 const float f = m_s[w][m] == -INFINITY ? 0.f : kv8_exp2(m_s[w][m] - top);
                 const float4 v = *reinterpret_cast<const float4*>(&o_s[w][m][d]);
                 if (m_s[w][m] == -INFINITY && l_s[w][m] == 0.f) continue;   // nothing seen by this warp
@@ -512,10 +577,7 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
                 y[0] += v.x * f; y[1] += v.y * f; y[2] += v.z * f; y[3] += v.w * f;
             }
             if (whole) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                T* dst = static_cast<T*>(p.out) + (row.t0 + m / G) * p.out_stride + (h * G + m % G) * HD + d;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) Elem<T>::round_store(y[e] * inv, dst + e);
+                put(m, d, sum, y);
             } else {
                 *reinterpret_cast<float4*>(slot + m * HD + d) = make_float4(y[0], y[1], y[2], y[3]);
                 if (d == 0) {
@@ -524,94 +586,80 @@ __global__ void __launch_bounds__(KD_THREADS, MT == 1 ? 3 : 2) k_kv8_decode(cons
                 }
             }
         }
+        if (!whole) {
+            // the last CTA of this row and head joins the pieces' parts, in their order
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) last_s = atomicAdd(p.counters + r * c.Hkv + h, 1) == c1 - c0;
+            __syncthreads();
+            if (last_s) {
+                __threadfence();
+                const bool second = !cut.own && cut.begin(c0) != u - i0;   // piece c0 had other work before
+                for (int x = tid; x < nq * (HD / 4); x += 32 * W) {
+                    const int m = x / (HD / 4), d = (x % (HD / 4)) * 4;
+                    float top = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
+                    constexpr int B = 8;   // parts read at once
+                    for (int q0 = c0; q0 <= c1; q0 += B) {
+                        float mm[B], ll[B];
+                        float4 v[B];
+#pragma unroll
+                        for (int k = 0; k < B; ++k) {
+                            const int q = min(q0 + k, c1);
+                            const float* part = slots + ((size_t)q * 2 + (q == c0 && second ? 1 : 0)) * kd_slot_floats<HD, MT>();
+                            mm[k] = __ldcg(part + MT * 8 * HD + m);
+                            ll[k] = __ldcg(part + MT * 8 * (HD + 1) + m);
+                            v[k] = __ldcg(reinterpret_cast<const float4*>(part + m * HD + d));
+                        }
+#pragma unroll
+                        for (int k = 0; k < B; ++k) {
+                            if (q0 + k > c1 || (mm[k] == -INFINITY && ll[k] == 0.f)) continue;
+                            const float big = fmaxf(top, mm[k]);
+                            const float f = top == -INFINITY ? 0.f : kv8_exp2(top - big), e = mm[k] == -INFINITY ? 0.f : kv8_exp2(mm[k] - big);
+                            top = big;
+                            sum = sum * f + ll[k] * e;
+                            y[0] = y[0] * f + v[k].x * e; y[1] = y[1] * f + v[k].y * e;
+                            y[2] = y[2] * f + v[k].z * e; y[3] = y[3] * f + v[k].w * e;
+                        }
+                    }
+                    put(m, d, sum, y);
+                }
+                if (tid == 0) p.counters[r * c.Hkv + h] = 0;   // for the next call
+            }
+        }
         __syncthreads();   // the shared buffers are free again
-        u += i1 - i0;
+        u += cut.own ? 1 : i1 - i0;
     }
     // not earlier: the next kernel's blocks would take places that this grid, which is one wave, counts on
     pdl_trigger();
 }
 
-// the rows and heads that were cut: grid (rows, Hkv * query rows), HD / 4 lanes used by a block of KD_THREADS
-template <int HD, int MT, bool FINE>
-__global__ void __launch_bounds__(KD_THREADS) k_kv8_join(const Kv8Attend p, int grid) {
-    using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
-    __shared__ KdPlan plan;
-    __shared__ float part_s[KD_THREADS / (HD / 4)][HD / 4][6];
-    pdl_wait();
-    const Kv8Cache& c = p.c;
-    const int G = p.Hq / c.Hkv, r = blockIdx.x, h = blockIdx.y / (MT * 8), m = blockIdx.y % (MT * 8);
-    kd_plan(p, plan);
-    Kv8Row row;
-    if (!kv8_row(p.b, c.ppr * c.page, r, &row) || m >= row.n * G) return;
-    const long long units = (long long)plan.pre[c.rows] * c.Hkv;
-    const int pieces = kd_pieces(units, grid), n = plan.pre[r + 1] - plan.pre[r];
-    const long long u0 = (long long)plan.pre[r] * c.Hkv + (long long)h * n, u1 = u0 + n;
-    const int c0 = kd_piece_of(units, pieces, u0), c1 = kd_piece_of(units, pieces, u1 - 1);
-    if (c0 == c1) return;   // not cut
-    constexpr int LANES = HD / 4, PARTS = KD_THREADS / LANES;
-    const int part = threadIdx.x / LANES, d = (threadIdx.x % LANES) * 4;
-    float top = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int q = c0 + part; q <= c1; q += PARTS) {
-        const int which = q == c0 && kd_begin(units, pieces, q) != u0 ? 1 : 0;
-        const float* slot = p.ws + ((size_t)q * 2 + which) * kd_slot_floats<HD, MT>();
-        const float mm = slot[MT * 8 * HD + m], ll = slot[MT * 8 * (HD + 1) + m];
-        const float4 v = *reinterpret_cast<const float4*>(slot + m * HD + d);
-        if (mm == -INFINITY && ll == 0.f) continue;
-        const float big = fmaxf(top, mm);
-        const float f = top == -INFINITY ? 0.f : kv8_exp2(top - big), e = mm == -INFINITY ? 0.f : kv8_exp2(mm - big);
-        top = big;
-        sum = sum * f + ll * e;
-        y[0] = y[0] * f + v.x * e; y[1] = y[1] * f + v.y * e; y[2] = y[2] * f + v.z * e; y[3] = y[3] * f + v.w * e;
-    }
-    float* ps = part_s[part][threadIdx.x % LANES];
-    ps[0] = top; ps[1] = sum; ps[2] = y[0]; ps[3] = y[1]; ps[4] = y[2]; ps[5] = y[3];
-    __syncthreads();
-    if (part) return;
-    for (int w = 1; w < PARTS; ++w) {
-        const float* o = part_s[w][threadIdx.x];
-        if (o[0] == -INFINITY && o[1] == 0.f) continue;
-        const float big = fmaxf(top, o[0]);
-        const float f = top == -INFINITY ? 0.f : kv8_exp2(top - big), e = o[0] == -INFINITY ? 0.f : kv8_exp2(o[0] - big);
-        top = big;
-        sum = sum * f + o[1] * e;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = y[k] * f + o[2 + k] * e;
-    }
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    T* dst = static_cast<T*>(p.out) + (row.t0 + m / G) * p.out_stride + (h * G + m % G) * HD + d;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) Elem<T>::round_store(y[e] * inv, dst + e);
-}
-
 int decode_sets(const Kv8Attend& p) { return (p.b.max_new * (p.Hq / p.c.Hkv) + 7) / 8; }
 
-// one CTA for each place on the GPU, but no more than there can be tiles
+// one CTA for each SM, but no more than there can be steps
 int decode_grid(const Kv8Attend& p, int num_sms) {
-    const long long tiles = (long long)p.c.rows * p.c.Hkv * (((long long)p.c.ppr * p.c.page + KD_TILE - 1) / KD_TILE);
-    const long long most = (long long)num_sms * (decode_sets(p) == 1 ? 3 : 2);
-    return (int)(tiles < most ? tiles : most);
+    const long long steps = (long long)p.c.rows * p.c.Hkv * (((long long)p.c.ppr * p.c.page + KD_STEP - 1) / KD_STEP);
+    return (int)(steps < num_sms ? steps : num_sms);
 }
 
 template <int HD, int MT, bool FINE>
 cudaError_t launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
-    const int grid = decode_grid(p, num_sms);
+    using S = KdShared<HD, MT>;
+    static OncePerDevice raised;
+    cudaError_t e = raised.run([] {
+        return cudaFuncSetAttribute((const void*)&k_kv8_decode<HD, MT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::BYTES);
+    });
+    if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(KD_THREADS);
-    cfg.dynamicSmemBytes = KdShared<HD, MT>::BYTES;
+    cfg.gridDim = dim3(decode_grid(p, num_sms));
+    cfg.blockDim = dim3(32 * S::W);
+    cfg.dynamicSmemBytes = S::BYTES;
     cfg.stream = s;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaFuncSetAttribute((const void*)&k_kv8_decode<HD, MT, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         KdShared<HD, MT>::BYTES);
-    if (e == cudaSuccess) e = cudaLaunchKernelEx(&cfg, k_kv8_decode<HD, MT, FINE>, p);
-    if (e != cudaSuccess || p.c.ppr * (long long)p.c.page <= KD_TILE) return e;   // one tile a head: nothing is cut
-    cfg.gridDim = dim3(p.c.rows, p.c.Hkv * MT * 8);
-    cfg.dynamicSmemBytes = 0;
-    return cudaLaunchKernelEx(&cfg, k_kv8_join<HD, MT, FINE>, p, grid);
+    return cudaLaunchKernelEx(&cfg, k_kv8_decode<HD, MT, FINE>, p);
 }
 
 }  // namespace

@@ -743,8 +743,10 @@ int prompt_splits(const Kv8Attend& p, int num_sms) {
 template <int HD, bool FINE>
 cudaError_t launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
     const int splits = prompt_splits(p, num_sms);
-    cudaError_t e = cudaFuncSetAttribute((const void*)&k_kv8_prompt<HD, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         kp_smem<HD, FINE>());
+    static OncePerDevice raised;
+    cudaError_t e = raised.run([] {
+        return cudaFuncSetAttribute((const void*)&k_kv8_prompt<HD, FINE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kp_smem<HD, FINE>());
+    });
     if (e != cudaSuccess) return e;
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

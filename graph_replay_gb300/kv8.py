@@ -17,6 +17,7 @@ import torch
 
 from . import _binding as B
 
+_raw_stream = torch._C._cuda_getCurrentRawStream   # of a device: what torch.cuda.current_stream wraps, without the wrapper
 _DT = {torch.float32: B.DEC_DTYPE_F32, torch.bfloat16: B.DEC_DTYPE_BF16}
 
 
@@ -49,6 +50,7 @@ class KV8Cache:
         self.rows, self.cap, self.n_kv_heads, self.head_dim = rows, per_row * page, heads, dim
         self.page_size, self.scale_block = page, page // k_scale.shape[2]
         self.device = k.device
+        self._need, self._ws = {}, {}
         self._err = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._c = B.dec_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   None if page_table is None else page_table.data_ptr(), rows, per_row, page, pages,
@@ -87,26 +89,56 @@ class KV8Cache:
         ks, vs = self._tokens("k", k, self.n_kv_heads), self._tokens("v", v, self.n_kv_heads)
         b = self._batch(kv_len, q_start, k.shape[0], max_new)
         n = B.dec_kv8_new(k.data_ptr(), v.data_ptr(), ks, vs, _DT[k.dtype], 0)
-        B.dec_kv8_append(self._c, b, n, torch.cuda.current_stream(self.device).cuda_stream)
+        B.dec_kv8_append(self._c, b, n, _raw_stream(self._c.device))
+
+    def workspace_bytes(self, tokens: int, n_heads: int, max_new: int = 1, window: int = 0, sinks: int = 0,
+                        dtype: torch.dtype = torch.bfloat16) -> int:
+        """Bytes of workspace that attend needs for these sizes."""
+        key = (tokens, n_heads, max_new, window, sinks, dtype)
+        need = self._need.get(key)
+        if need is None:
+            b = B.dec_kv8_batch(self._c.pages or self._c.k, self._c.k, self._c.k, tokens, max_new)   # addresses are not read
+            a = B.dec_kv8_attn(self._c.k, self._c.k, n_heads * self.head_dim, n_heads * self.head_dim, _DT[dtype], n_heads,
+                               window, sinks, 0.0, None, 0)
+            need = self._need[key] = B.dec_kv8_workspace(self._c, b, a)
+        return need
+
+    def _workspace(self, stream: int, need: int) -> torch.Tensor:
+        # One for each stream, zeroed once: calls on a stream follow one another, and each leaves it as it found it.  A
+        # recorded graph gets its own, from its pool, and zeroes the counters when it runs
+        if torch.cuda.is_current_stream_capturing():
+            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+            ws[:-(-self.rows * self.n_kv_heads * 4 // 256) * 256].zero_()
+            return ws
+        ws = self._ws.get(stream)
+        if ws is None or ws.numel() < need:
+            ws = self._ws[stream] = torch.zeros(need, dtype=torch.uint8, device=self.device)
+        return ws
 
     def attend(self, q: torch.Tensor, kv_len: torch.Tensor, q_start: Optional[torch.Tensor] = None, max_new: int = 1,
-               window: int = 0, sinks: int = 0, scale: float = 0.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+               window: int = 0, sinks: int = 0, scale: float = 0.0, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
         """Attention of q [tokens, n_heads, head_dim] over the cache, causal; with a window each token sees its last
         `window` positions (its own among them) and the first `sinks`.  scale 0: 1 / sqrt(head_dim).  Returns `out`
-        (allocated like q if None); packed tokens that belong to no row are not written."""
+        (allocated like q if None); packed tokens that belong to no row are not written.  `workspace`: uint8, zeroed
+        before its first use, of workspace_bytes(...); None: the cache keeps one for each stream, and a graph that
+        records the call one of its own."""
         qs = self._tokens("q", q, 0)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         elif out.shape != q.shape or out.dtype != q.dtype:
             raise ValueError("KV8Cache: out has q's shape and type")
         os_ = self._tokens("out", out, 0)
-        b = self._batch(kv_len, q_start, q.shape[0], max_new)
-        a = B.dec_kv8_attn(q.data_ptr(), out.data_ptr(), qs, os_, _DT[q.dtype], q.shape[1], window, sinks, scale, None, 0)
-        need = B.dec_kv8_workspace(self._c, b, a)
-        if need:   # from torch's allocator on this stream: calls on other streams, and graphs, have their own
-            ws = torch.empty(need, dtype=torch.uint8, device=self.device)
-            a.workspace, a.workspace_bytes = ws.data_ptr(), need
-        B.dec_kv8_attend(self._c, b, a, torch.cuda.current_stream(self.device).cuda_stream)
+        tokens, heads, _ = q.shape
+        b = self._batch(kv_len, q_start, tokens, max_new)
+        stream = _raw_stream(self._c.device)
+        if workspace is None:
+            workspace = self._workspace(stream, self.workspace_bytes(tokens, heads, max_new, window, sinks, q.dtype))
+        elif workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError("KV8Cache: the workspace is contiguous and on the cache's device")
+        a = B.dec_kv8_attn(q.data_ptr(), out.data_ptr(), qs, os_, _DT[q.dtype], heads, window, sinks, scale,
+                           workspace.data_ptr(), workspace.numel() * workspace.element_size())
+        B.dec_kv8_attend(self._c, b, a, stream)
         return out
 
     def check(self) -> None:

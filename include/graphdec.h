@@ -526,15 +526,16 @@ typedef struct dec_kv8_attn {
     int32_t window;              /* 0: none */
     int32_t sinks;               /* first positions that stay visible (with a window) */
     double scale;                /* 0: 1 / sqrt(head_dim) */
-    void *workspace;             /* device, 16-byte aligned, dec_kv8_workspace bytes; its contents mean nothing
-                                    between calls, but calls that may overlap on the GPU need one each */
+    void *workspace;             /* device, 16-byte aligned, dec_kv8_workspace bytes.  Zero-filled by the caller before
+                                    its first use; every call leaves it ready for the next one on the same cache, of
+                                    any size that it holds.  Calls that may overlap on the GPU need one each */
     size_t workspace_bytes;
 } dec_kv8_attn;
 
 int dec_kv8_attend(const dec_kv8_cache *cache, const dec_kv8_batch *batch, const dec_kv8_attn *attn, void *stream);
 
 /* Bytes of workspace that dec_kv8_attend needs for these arguments (*bytes,
- * host; may be 0).  Reads sizes only: the same for every content. */
+ * host).  Reads sizes only: the same for every content. */
 int dec_kv8_workspace(const dec_kv8_cache *cache, const dec_kv8_batch *batch, const dec_kv8_attn *attn, size_t *bytes);
 
 /* Device address of the logits [rows, vocab] fp32 of the last step. */
