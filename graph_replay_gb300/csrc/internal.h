@@ -287,11 +287,24 @@ struct OncePerDevice {
         return e;
     }
 };
+// n / d for 0 <= n < 2^31 without a division: mul = ceil(2^(31 + shift) / d), shift = ceil(log2 d)
+struct FastDiv {
+    unsigned d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(unsigned d_) : d(d_), shift(0) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (unsigned)(((1ull << (31 + shift)) + d - 1) / d);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int of(int n) const { return (int)(__umulhi((unsigned)n << 1, mul) >> shift); }
+#endif
+};
 struct Kv8Cache {              // a dec_kv8_cache that passed its checks
     uint8_t *k, *v;            // [num_pages, Hkv, page, hd] e4m3
     uint8_t *ks, *vs;          // [num_pages, Hkv, page / block] exponent + 127
     const int* pages;          // [rows, ppr] or null: row r owns pages r * ppr ..
-    int rows, ppr, page, num_pages, Hkv, hd, block;
+    int rows, ppr, page, num_pages, Hkv, hd, block, block_log2;
+    FastDiv by_page;
 };
 struct Kv8Batch {
     const int* q_start;        // [rows + 1] or null: one token a row

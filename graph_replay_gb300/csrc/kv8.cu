@@ -61,7 +61,9 @@ int check_cache(const dec_kv8_cache* c, Kv8Cache* out) {
         return refuse(DEC_E_INVALID, "without a page table num_pages must be at least rows * pages_per_row");
     if (c->device < 0) return refuse(DEC_E_INVALID, "device must be >= 0");
     *out = Kv8Cache{(uint8_t*)c->k, (uint8_t*)c->v, c->k_scale, c->v_scale, c->pages, c->rows, c->pages_per_row,
-                    c->page_size, c->num_pages, c->n_kv_heads, c->head_dim, c->scale_block};
+                    c->page_size, c->num_pages, c->n_kv_heads, c->head_dim, c->scale_block,
+                    c->scale_block == 16 ? 4 : c->scale_block == 32 ? 5 : c->scale_block == 64 ? 6 : 7,
+                    FastDiv((unsigned)c->page_size)};
     return DEC_OK;
 }
 

@@ -83,8 +83,9 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
 }
 
 // a / b for a >= 0: most numbers here fit 32 bits, and a 64-bit division costs a short call half a microsecond
+__device__ __noinline__ long long quotient64(long long a, int b) { return a / b; }
 __device__ __forceinline__ long long quotient(long long a, int b) {
-    return (a >> 32) ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+    return (a >> 32) ? quotient64(a, b) : (long long)((uint32_t)a / (uint32_t)b);
 }
 // The work cut into pieces.  own: pieces of one (row, head) each; else the line of units in pieces of q or q + 1
 struct KdCut {
@@ -97,64 +98,75 @@ struct KdCut {
         return u < lead ? (int)quotient(u, (int)q + 1) : rem + (int)quotient(u - lead, (int)q);
     }
 };
-// sum of v over the threads before this one; *all: over all threads.  s: W entries
-template <int W>
-__device__ __forceinline__ long long sum_before(long long v, long long* s, long long* all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    long long inc = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
+// The plan is made by every warp for itself, 32 rows at a time and a row for each lane: no shared memory, no
+// barrier, and one trip to memory where there are at most 32 rows
+struct KdRows {
+    const Kv8Attend& p;
+    const int lane, cap;
+    int at = -1, n = 0;   // the 32 rows held: 32 * at .., steps of row 32 * at + lane
+    Kv8Row row{0, 0, 0};  // and what it is
+    __device__ __forceinline__ KdRows(const Kv8Attend& p_) : p(p_), lane(threadIdx.x & 31), cap(p_.c.ppr * p_.c.page) {}
+    __device__ __forceinline__ int steps(int chunk) {
+        if (chunk != at) {
+            const int r = 32 * chunk + lane;
+            n = r < p.c.rows && kv8_row(p.b, cap, r, &row) ? kd_steps(row, p.window, p.sinks).n : 0;
+            at = chunk;
+        }
+        return n;
     }
-    if (lane == 31) s[warp] = inc;
-    __syncthreads();
-    long long before = inc - v, total = 0;
+    __device__ __forceinline__ int chunks() const { return (p.c.rows + 31) / 32; }
+};
+// a row's pieces: least > 0: cuts of at least that many steps; 0: its steps
+__device__ __forceinline__ uint32_t kd_weight(int n, int least) { return least ? (uint32_t)((n + least - 1) / least) : (uint32_t)n; }
+// Row and place of item u on the line of all heads' weights: the weight of the rows before (of one head) and of the row
+struct KdPlace {
+    int r;
+    Kv8Row row;
+    long long before;
+    uint32_t weight;
+};
+__device__ __forceinline__ KdPlace kd_find(KdRows& rows, long long u, int least) {
+    const int Hkv = rows.p.c.Hkv;
+    long long before = 0;
+    for (int k = 0; k < rows.chunks(); ++k) {
+        const uint32_t w = kd_weight(rows.steps(k), least);
+        uint32_t inc = w;   // 32 rows of at most 2^26 steps
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-        if (w < warp) before += s[w];
-        total += s[w];
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(0xffffffffu, inc, o);
+            if (rows.lane >= o) inc += x;
+        }
+        const unsigned past = __ballot_sync(0xffffffffu, (before + inc) * Hkv > u);
+        if (past) {   // the first row that ends behind u
+            const int l = __ffs(past) - 1;
+            const uint32_t wl = __shfl_sync(0xffffffffu, w, l);
+            const Kv8Row row{__shfl_sync(0xffffffffu, rows.row.t0, l), __shfl_sync(0xffffffffu, rows.row.n, l),
+                             __shfl_sync(0xffffffffu, rows.row.len, l)};
+            return KdPlace{32 * k + l, row, before + __shfl_sync(0xffffffffu, inc, l) - wl, wl};
+        }
+        before += __shfl_sync(0xffffffffu, inc, 31);
     }
-    *all = total;
-    return before;
+    return KdPlace{-1, Kv8Row{0, 0, 0}, 0, 0};   // the lengths have changed under the kernel: nothing is left to do
 }
-// pre[r], cuts[r]: steps, and pieces of a head (own), of the rows before r
 template <int W>
-__device__ __forceinline__ KdCut kd_plan(const Kv8Attend& p, int grid, long long* pre, int* cuts, long long (*sums)[W]) {
-    const int tid = threadIdx.x, rows = p.c.rows, cap = p.c.ppr * p.c.page;
-    const int per = (rows + 32 * W - 1) / (32 * W), r0 = min(tid * per, rows), r1 = min(r0 + per, rows);
-    long long sum = 0;
-    for (int r = r0; r < r1; ++r) {
-        Kv8Row row;
-        pre[r] = kv8_row(p.b, cap, r, &row) ? kd_steps(row, p.window, p.sinks).n : 0;
-        sum += pre[r];
-    }
+__device__ __forceinline__ KdCut kd_plan(KdRows& rows, int grid, int* least) {
+    const int Hkv = rows.p.c.Hkv;
+    long long all = 0, all_cuts = 0;
+    for (int k = 0; k < rows.chunks(); ++k) all += __reduce_add_sync(0xffffffffu, (uint32_t)rows.steps(k));
     KdCut cut;
-    long long all, all_cuts, before = sum_before<W>(sum, sums[0], &all);
-    cut.units = all * p.c.Hkv;
-    // steps of a row's own pieces: an eighth of the SMs may stay without work for them
-    const int least = (int)max(2ll * W, quotient(cut.units * 9 + 8 * grid - 1, 8 * grid));
-    long long mine = 0;
-    for (int r = r0; r < r1; ++r) {
-        const int n = (int)pre[r];
-        pre[r] = before;
-        before += n;
-        cuts[r] = (n + least - 1) / least;
-        mine += cuts[r];
+    cut.units = all * Hkv;
+    // Own pieces: the places that stay without work cost more the longer the pieces are, a piece that goes on in a
+    // second head costs some 4 us.  So an eighth may idle up to 512 steps a place, three up to 96, none beyond
+    // (16 rows x 4 heads x 257 steps: 22.9 us with own pieces, 26.2 without; 32 x 8 x ~1350: 306 against 221)
+    all_cuts = grid + 1;
+    for (int spare = 9; spare <= 11 && all_cuts * Hkv > grid; spare += 2) {
+        if (cut.units > (spare == 9 ? 512ll : 96ll) * grid) break;
+        *least = (int)max(2ll * W, quotient(cut.units * spare + 8 * grid - 1, 8 * grid));
+        all_cuts = 0;
+        for (int k = 0; k < rows.chunks(); ++k) all_cuts += __reduce_add_sync(0xffffffffu, kd_weight(rows.steps(k), *least));
     }
-    long long at = sum_before<W>(mine, sums[1], &all_cuts);
-    for (int r = r0; r < r1; ++r) {
-        const int n = cuts[r];
-        cuts[r] = (int)at;
-        at += n;
-    }
-    if (tid == 0) {
-        pre[rows] = all;
-        cuts[rows] = (int)all_cuts;
-    }
-    __syncthreads();
-    cut.own = all_cuts * p.c.Hkv <= grid;
-    cut.pieces = cut.own ? (int)all_cuts * p.c.Hkv : grid;
+    cut.own = all_cuts * Hkv <= grid;
+    cut.pieces = cut.own ? (int)all_cuts * Hkv : grid;
     cut.q = quotient(cut.units, grid);   // at least 1 where it is used: more units than pieces
     cut.rem = (int)(cut.units - cut.q * grid);
     return cut;
@@ -180,7 +192,7 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // dynamic shared memory: the rings; when the loop is done the warps' results lie over them
 template <int HD, int MT>
 struct KdShared {
-    static constexpr int W = MT == 1 ? 12 : 8;            // warps: what the registers allow, one CTA on an SM
+    static constexpr int W = MT == 1 ? 6 : 4, CTAS = 2;   // warps of a CTA, CTAs on an SM: one's ends hide behind the other's stream
     static constexpr int STEP = 2 * KD_STEP * HD, STAGES = 512 / HD;   // 16 KB a warp
     static constexpr int RING = W * STAGES * STEP, OUT = W * MT * 8 * HD * (int)sizeof(float);
     static constexpr int BYTES = RING > OUT ? RING : OUT;
@@ -188,7 +200,7 @@ struct KdShared {
 
 // MT: query rows / 8 (up).  FINE: fp32 q -- second f16 parts of q and of the weights.
 template <int HD, int MT, bool FINE>
-__global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(const Kv8Attend p) {
+__global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CTAS) k_kv8_decode(const Kv8Attend p) {
     using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
     constexpr int NK = HD / 16;   // 16-dim steps of S, 16-dim tiles of O
     constexpr int PARTS = FINE ? 2 : 1, STAGES = KdShared<HD, MT>::STAGES, W = KdShared<HD, MT>::W;
@@ -196,8 +208,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
     float(*o_s)[MT * 8][HD] = reinterpret_cast<float(*)[MT * 8][HD]>(kd_raw);
     const unsigned char* ring_p = kd_raw + (threadIdx.x >> 5) * (STAGES * KdShared<HD, MT>::STEP);
     const uint32_t ring = smem_u32(ring_p);
-    __shared__ long long pre[KV8_MAX_ROWS + 1], sums[2][W];
-    __shared__ int cuts[KV8_MAX_ROWS + 1], last_s;
+    __shared__ int last_s;
     __shared__ float m_s[W][MT * 8], l_s[W][MT * 8];
     __shared__ __align__(16) uint4 q_s[PARTS][MT][NK / 2][32];   // f16 parts of q, by step and lane
     __shared__ float fac_s[MT * 8];
@@ -205,39 +216,31 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
     pdl_wait();
     const Kv8Cache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int G = p.Hq / c.Hkv, cap = c.ppr * c.page, nb = c.page / c.block;
-    const KdCut cut = kd_plan<W>(p, gridDim.x, pre, cuts, sums);
+    const int G = p.Hq / c.Hkv, nb = c.page >> c.block_log2;
+    KdRows rows(p);
+    int least = 1;
+    const KdCut cut = kd_plan<W>(rows, gridDim.x, &least);
     if ((int)blockIdx.x >= cut.pieces) return;
-    // the last r with at[r] * Hkv <= u
-    auto row_of = [&](const auto* at, long long u) {
-        int r = 0, hi = c.rows;
-        while (r + 1 < hi) {
-            const int mid = (r + hi) >> 1;
-            if ((long long)at[mid] * c.Hkv <= u) r = mid;
-            else hi = mid;
-        }
-        return r;
-    };
-    const long long u_begin = cut.own ? 0 : cut.begin(blockIdx.x), u_end = cut.own ? 1 : cut.begin(blockIdx.x + 1);
+    const long long u_begin = cut.own ? blockIdx.x : cut.begin(blockIdx.x);
+    const long long u_end = cut.own ? u_begin + 1 : cut.begin(blockIdx.x + 1);
 
     for (long long u = u_begin; u < u_end;) {
         // steps [i0, i1) of row r and K/V head h; a head that is cut has the pieces c0 .. c1
-        const int r = cut.own ? row_of(cuts, blockIdx.x) : row_of(pre, u);
-        Kv8Row row;
-        kv8_row(p.b, cap, r, &row);
+        const KdPlace at = kd_find(rows, u, cut.own ? least : 0);
+        const int r = at.r;
+        if (r < 0) break;
+        const Kv8Row row = at.row;
         const KdSteps tl = kd_steps(row, p.window, p.sinks);
-        int h, i0, i1, c0, c1;
+        const long long in_row = u - at.before * c.Hkv;
+        const int h = (int)quotient(in_row, (int)at.weight), in_head = (int)(in_row - (long long)h * at.weight);
+        int i0, i1, c0, c1;
         if (cut.own) {
-            const int n = cuts[r + 1] - cuts[r], at = blockIdx.x - cuts[r] * c.Hkv;
-            h = at / n;
-            c0 = cuts[r] * c.Hkv + h * n;
-            c1 = c0 + n - 1;
-            i0 = (int)quotient((long long)tl.n * (at - h * n), n);
-            i1 = (int)quotient((long long)tl.n * (at - h * n + 1), n);
+            c0 = blockIdx.x - in_head;
+            c1 = c0 + (int)at.weight - 1;
+            i0 = (int)quotient((long long)tl.n * in_head, (int)at.weight);
+            i1 = (int)quotient((long long)tl.n * (in_head + 1), (int)at.weight);
         } else {
-            const long long u_row = pre[r] * c.Hkv;
-            h = (int)quotient(u - u_row, tl.n);
-            i0 = (int)(u - u_row - (long long)h * tl.n);
+            i0 = in_head;
             i1 = (int)min((long long)tl.n, i0 + (u_end - u));
             c0 = cut.piece_of(u - i0);
             c1 = cut.piece_of(u - i0 + tl.n - 1);
@@ -253,19 +256,24 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
             return (i < tl.sink ? i : i + tl.gap) * KD_STEP;
         };
         auto wanted = [&](int kb) { return kb < end && (kb + 15 >= low || kb < p.sinks); };
-        // 32 of them, one for each lane: the page (-1: no step) and, packed, V's and K's scale
-        // bytes.  The copies run ahead of the arithmetic: it may still need the 32 before.
-        int pages = -1, scales = -1, scales_before = -1;
+        // 32 of them, one for each lane: where in the pools, in 16 rows (-1: no step), and the scale bytes.  The copies
+        // run ahead of the arithmetic: it may still need the 32 before.
+        int place = -1, place_before = -1, ke = 0, ke_before = 0, ve = 0, ve_before = 0;
         auto next32 = [&](int k) {
-            scales_before = scales;
-            pages = scales = -1;
+            place_before = place;
+            ke_before = ke;
+            ve_before = ve;
+            place = -1;
             if (k + lane >= mine) return;
             const int kb = key0(k + lane);
             if (!wanted(kb)) return;
-            pages = kv8_page(c, p.b.err, r, kb / c.page);
-            if (pages < 0) return;
-            const size_t at = ((size_t)pages * c.Hkv + h) * nb + kb % c.page / c.block;
-            scales = (int)c.ks[at] | (int)c.vs[at] << 8;
+            const int slot = c.by_page.of(kb), off = kb - slot * c.page, page = kv8_page(c, p.b.err, r, slot);
+            if (page < 0) return;
+            const long long head = (long long)page * c.Hkv + h;
+            place = (int)((head * c.page + off) >> 4);
+            const long long at = head * nb + (off >> c.block_log2);
+            ke = c.ks[at];   // not looked at before the step is computed: nothing waits for them here
+            ve = c.vs[at];
         };
         int ahead = 0;   // the next step to copy
         // one more step into the ring; one group a call, also for nothing
@@ -273,9 +281,9 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
             const int i = ahead++;
             if (i < mine) {
                 if ((i & 31) == 0) next32(i);
-                const int page = __shfl_sync(0xffffffffu, pages, i & 31);
-                if (page >= 0) {
-                    const size_t at = (((size_t)page * c.Hkv + h) * c.page + key0(i) % c.page) * HD;
+                const int there = __shfl_sync(0xffffffffu, place, i & 31);
+                if (there >= 0) {
+                    const size_t at = (size_t)there * (16 * HD);
                     const uint32_t dst = ring + (uint32_t)((i % STAGES) * KdShared<HD, MT>::STEP);
 #pragma unroll
                     for (int u = 0; u < HD / 32; ++u) {
@@ -288,52 +296,55 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
             }
             copy_commit();
         };
+        // q on its way before the first page id is waited for.  The sets of 8 query rows and the pairs of 16 dims are laid
+        // out by different warps; each needs all of a row for its power of two
+        constexpr int QW = HD / 4 / Elem<T>::VEC;   // 16-byte words of a lane's dims
+        constexpr int PAIRS = NK / 2, ITEMS = MT * PAIRS;
+        auto load_q = [&](int a, uint4 (&qw)[QW]) {
+            const int m = a * 8 + g;
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (row.t0 + m / G) * p.q_stride +
+                                                              (h * G + m % G) * HD + t * (HD / 4));
+#pragma unroll
+            for (int v = 0; v < QW; ++v) qw[v] = m < nq ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
+        };
+        uint4 qw[QW];
+        if (warp < ITEMS) load_q(warp / PAIRS, qw);
 #pragma unroll
         for (int x = 0; x < STAGES - 1; ++x) copy_next();   // in flight while q is laid out
 
-        // q as B operand: warp a lays out the query rows a * 8 + g of this K/V head
+        // q as B operand: lane (g, t) holds 16 dims' worth of query row g of a set
         float fac[MT][2];   // scale * log2(e) / q's power of two, of query rows 2t and 2t + 1
         int pos[MT][2];     // their positions (-1: no such row, or before the sequence)
-        if (warp < MT) {
-            const int m = warp * 8 + g;
-            float x[NK * 4];
-            float top = 0.f;
-            if (m < nq) {
-                const T* src = static_cast<const T*>(p.q) + (row.t0 + m / G) * p.q_stride + (h * G + m % G) * HD + t * (HD / 4);
+        for (int item = warp; item < ITEMS; item += W) {
+            const int a = item / PAIRS, pr = item % PAIRS;
+            if (item != warp) load_q(a, qw);
+            float top = 0.f, mine4[8];   // this pair's 8 values of the lane
 #pragma unroll
-                for (int j = 0; j < HD / 64; ++j)
+            for (int v = 0; v < QW; ++v) {
+                float f[Elem<T>::VEC];
+                Elem<T>::unpack(qw[v], f);
 #pragma unroll
-                    for (int v = 0; v < 16; v += Elem<T>::VEC) {
-                        float f[Elem<T>::VEC];
-                        Elem<T>::unpack(__ldg(reinterpret_cast<const uint4*>(src + j * 16 + v)), f);
-#pragma unroll
-                        for (int e = 0; e < Elem<T>::VEC; ++e) x[j * 16 + v + e] = f[e];
-                    }
-            } else {
-#pragma unroll
-                for (int e = 0; e < NK * 4; ++e) x[e] = 0.f;
+                for (int e = 0; e < Elem<T>::VEC; ++e) {
+                    top = fmaxf(top, fabsf(f[e]));
+                    if ((v * Elem<T>::VEC + e) / 8 == pr) mine4[(v * Elem<T>::VEC + e) % 8] = f[e];
+                }
             }
-#pragma unroll
-            for (int e = 0; e < NK * 4; ++e) top = fmaxf(top, fabsf(x[e]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
             // a power of two that brings the row's largest value to [2^14, 2^15)
             const int ex = min(max(268 - (int)(__float_as_uint(top) >> 23), 1), 254);
             const float up = __int_as_float(ex << 23);
+            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int k = 0; k < NK; k += 2) {
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const float x0 = x[k * 4 + b * 2] * up, x1 = x[k * 4 + b * 2 + 1] * up;
-                    hi[b] = pack_f16x2(x0, x1);
-                    const float2 f = unpack_f16x2(hi[b]);
-                    lo[b] = pack_f16x2(x0 - f.x, x1 - f.y);
-                }
-                q_s[0][warp][k / 2][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                if constexpr (FINE) q_s[1][warp][k / 2][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            for (int b = 0; b < 4; ++b) {
+                const float x0 = mine4[2 * b] * up, x1 = mine4[2 * b + 1] * up;
+                hi[b] = pack_f16x2(x0, x1);
+                const float2 f = unpack_f16x2(hi[b]);
+                lo[b] = pack_f16x2(x0 - f.x, x1 - f.y);
             }
-            if (t == 0) fac_s[m] = p.scale * KV8_LOG2E / up;
+            q_s[0][a][pr][lane] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            if constexpr (FINE) q_s[1][a][pr][lane] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            if (pr == 0 && t == 0) fac_s[a * 8 + g] = p.scale * KV8_LOG2E / up;
         }
         __syncthreads();
 #pragma unroll
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
             l[a][0] = l[a][1] = 0.f;
         }
 
-        auto compute = [&](int i, int scale_bytes) {
+        auto compute = [&](int i, int e_k, int e_v) {
             const int kb = key0(i);
             const unsigned char* step = ring_p + (i % STAGES) * KdShared<HD, MT>::STEP;
             // S^T: rows keys g, g + 8; columns query rows 2t, 2t + 1
@@ -385,8 +396,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
                         }
                 }
             }
-            const int e_k = (scale_bytes & 255) - 127, e_v = (scale_bytes >> 8) - 127;
-            const float kf = pow2i(e_k), ve = (float)e_v, vinv = pow2i(-e_v);
+            const float kf = pow2i(e_k), vexp = (float)e_v, vinv = pow2i(-e_v);
             // positions every token of the row sees need no mask
             const bool all = kb + 15 <= p0 && (kb + 15 < p.sinks || kb > row.len - 1 - p.window);
             bool grew = false;
@@ -395,7 +405,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int b = e & 1, j = kb + g + (e >> 1) * 8;
-                    sc[a][e] = fmaf(sc[a][e], fac[a][b] * kf, ve);
+                    sc[a][e] = fmaf(sc[a][e], fac[a][b] * kf, vexp);
                     if (!all && !(pos[a][b] >= 0 && kv8_sees(pos[a][b], j, p.window, p.sinks))) sc[a][e] = -INFINITY;
                     grew |= sc[a][e] > M[a][b] + KD_SLACK;
                 }
@@ -525,8 +535,11 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
             copy_next();
             copy_wait<STAGES - 1>();   // step i's group is complete
             __syncwarp();              // for every lane's copies
-            const int sb = __shfl_sync(0xffffffffu, i >> 5 == (min(ahead, mine) - 1) >> 5 ? scales : scales_before, i & 31);
-            if (sb >= 0) compute(i, sb);
+            const bool now = i >> 5 == (min(ahead, mine) - 1) >> 5;   // of the 32 held, or of the 32 before
+            const int there = __shfl_sync(0xffffffffu, now ? place : place_before, i & 31);
+            const int e_k = __shfl_sync(0xffffffffu, now ? ke : ke_before, i & 31) - 127;
+            const int e_v = __shfl_sync(0xffffffffu, now ? ve : ve_before, i & 31) - 127;
+            if (there >= 0) compute(i, e_k, e_v);
             __syncwarp();              // the stage may be overwritten
         }
         copy_wait<0>();
@@ -588,40 +601,51 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
         }
         if (!whole) {
             // the last CTA of this row and head joins the pieces' parts, in their order
-            __threadfence();
             __syncthreads();
-            if (tid == 0) last_s = atomicAdd(p.counters + r * c.Hkv + h, 1) == c1 - c0;
+            if (tid == 0) {
+                __threadfence();   // the CTA's parts, before its arrival is counted
+                last_s = atomicAdd(p.counters + r * c.Hkv + h, 1) == c1 - c0;
+                __threadfence();
+            }
             __syncthreads();
             if (last_s) {
-                __threadfence();
                 const bool second = !cut.own && cut.begin(c0) != u - i0;   // piece c0 had other work before
-                for (int x = tid; x < nq * (HD / 4); x += 32 * W) {
-                    const int m = x / (HD / 4), d = (x % (HD / 4)) * 4;
-                    float top = -INFINITY, sum = 0.f, y[4] = {0.f, 0.f, 0.f, 0.f};
-                    constexpr int B = 8;   // parts read at once
+                for (int x = tid; x < nq * (HD / 8); x += 32 * W) {
+                    const int m = x / (HD / 8), d = (x % (HD / 8)) * 8;
+                    float top = -INFINITY, sum = 0.f, y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = 0.f;
+                    constexpr int B = 6;   // parts read at once
                     for (int q0 = c0; q0 <= c1; q0 += B) {
-                        float mm[B], ll[B];
-                        float4 v[B];
+                        float mm[B], ll[B], big = top;
+                        float4 v[B][2];
 #pragma unroll
                         for (int k = 0; k < B; ++k) {
                             const int q = min(q0 + k, c1);
                             const float* part = slots + ((size_t)q * 2 + (q == c0 && second ? 1 : 0)) * kd_slot_floats<HD, MT>();
                             mm[k] = __ldcg(part + MT * 8 * HD + m);
                             ll[k] = __ldcg(part + MT * 8 * (HD + 1) + m);
-                            v[k] = __ldcg(reinterpret_cast<const float4*>(part + m * HD + d));
+                            v[k][0] = __ldcg(reinterpret_cast<const float4*>(part + m * HD + d));
+                            v[k][1] = __ldcg(reinterpret_cast<const float4*>(part + m * HD + d) + 1);
                         }
 #pragma unroll
+                        for (int k = 0; k < B; ++k) big = fmaxf(big, mm[k]);
+                        const float f = top == -INFINITY ? 0.f : kv8_exp2(top - big);
+                        sum *= f;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] *= f;
+                        top = big;
+#pragma unroll
                         for (int k = 0; k < B; ++k) {
-                            if (q0 + k > c1 || (mm[k] == -INFINITY && ll[k] == 0.f)) continue;
-                            const float big = fmaxf(top, mm[k]);
-                            const float f = top == -INFINITY ? 0.f : kv8_exp2(top - big), e = mm[k] == -INFINITY ? 0.f : kv8_exp2(mm[k] - big);
-                            top = big;
-                            sum = sum * f + ll[k] * e;
-                            y[0] = y[0] * f + v[k].x * e; y[1] = y[1] * f + v[k].y * e;
-                            y[2] = y[2] * f + v[k].z * e; y[3] = y[3] * f + v[k].w * e;
+                            if (q0 + k > c1 || (mm[k] == -INFINITY && ll[k] == 0.f)) continue;   // nothing seen there
+                            const float e = mm[k] == -INFINITY ? 0.f : kv8_exp2(mm[k] - big);
+                            sum += ll[k] * e;
+                            y[0] += v[k][0].x * e; y[1] += v[k][0].y * e; y[2] += v[k][0].z * e; y[3] += v[k][0].w * e;
+                            y[4] += v[k][1].x * e; y[5] += v[k][1].y * e; y[6] += v[k][1].z * e; y[7] += v[k][1].w * e;
                         }
                     }
-                    put(m, d, sum, y);
+                    put(m, d, sum, reinterpret_cast<const float(&)[4]>(y[0]));
+                    put(m, d + 4, sum, reinterpret_cast<const float(&)[4]>(y[4]));
                 }
                 if (tid == 0) p.counters[r * c.Hkv + h] = 0;   // for the next call
             }
@@ -635,10 +659,11 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, 1) k_kv8_decode(cons
 
 int decode_sets(const Kv8Attend& p) { return (p.b.max_new * (p.Hq / p.c.Hkv) + 7) / 8; }
 
-// one CTA for each SM, but no more than there can be steps
+// one CTA for each place on the GPU, but no more than there can be steps
 int decode_grid(const Kv8Attend& p, int num_sms) {
     const long long steps = (long long)p.c.rows * p.c.Hkv * (((long long)p.c.ppr * p.c.page + KD_STEP - 1) / KD_STEP);
-    return (int)(steps < num_sms ? steps : num_sms);
+    const int most = num_sms * KdShared<128, 1>::CTAS;
+    return (int)(steps < most ? steps : most);
 }
 
 template <int HD, int MT, bool FINE>
