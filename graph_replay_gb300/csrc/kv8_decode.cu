@@ -521,11 +521,22 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
                 e4m3x4_to_f16(y23, c2, c3);
 #pragma unroll
                 for (int a = 0; a < MT; ++a) {
-                    mma_f16(o[a][2 * d], a0, a1, a2, a3, ph[a][0], ph[a][1]);
-                    mma_f16(o[a][2 * d + 1], c0, c1, c2, c3, ph[a][0], ph[a][1]);
                     if constexpr (FINE) {
-                        mma_f16(o[a][2 * d], a0, a1, a2, a3, pl[a][0], pl[a][1]);
-                        mma_f16(o[a][2 * d + 1], c0, c1, c2, c3, pl[a][0], pl[a][1]);
+                        // the tensor core cuts what it adds to its accumulator off, towards 0: over hundreds of
+                        // steps that shows in fp32 (7e-6 after 450), so the steps are added up outside, rounded
+                        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+                        mma_f16(x, a0, a1, a2, a3, ph[a][0], ph[a][1]);
+                        mma_f16(y, c0, c1, c2, c3, ph[a][0], ph[a][1]);
+                        mma_f16(x, a0, a1, a2, a3, pl[a][0], pl[a][1]);
+                        mma_f16(y, c0, c1, c2, c3, pl[a][0], pl[a][1]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            o[a][2 * d][e] += x[e];
+                            o[a][2 * d + 1][e] += y[e];
+                        }
+                    } else {
+                        mma_f16(o[a][2 * d], a0, a1, a2, a3, ph[a][0], ph[a][1]);
+                        mma_f16(o[a][2 * d + 1], c0, c1, c2, c3, ph[a][0], ph[a][1]);
                     }
                 }
             }

@@ -48,6 +48,7 @@ constexpr int KP_K_WARP = 8, KP_V_WARP = 12, KP_MMA_WARP = 16, KP_THREADS = 20 *
 constexpr int KP_REGS_SOFTMAX = 128, KP_REGS_CONV = 80, KP_REGS_MMA = 64;
 constexpr int KP_QPANEL = KP_ROWS * 128, KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a query tile, of a K or V tile
 constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
+constexpr int KP_FOLD = 16;               // fp32 q: tiles between two folds of O into memory
 constexpr int KP_META = 8;                // tiles whose scales are held
 constexpr int KP_GROUPS = KP_KEYS / 16, KP_BATCH = 32 / KP_GROUPS;   // 16-position groups of a tile; tiles that a warp's lanes know of
 constexpr int KP_MARKS = 32;              // words of marks: tile i has bit i % (32 * KP_MARKS)
@@ -197,6 +198,11 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
 
 // what turns a product into a score (log2); never 0, which would make NaN of a masked -inf
 __device__ __forceinline__ float kp_mul(float fac, float kf) { return fmaxf(fac * kf, 1.17549435e-38f); }
+
+// floats of the splits' parts (O, then M and l of each), up to a multiple of 16 bytes
+__host__ __device__ __forceinline__ size_t kp_part_floats(int splits, size_t all_rows, int hd) {
+    return splits == 1 ? 0 : (splits * all_rows * (hd + 2) + 3) / 4 * 4;
+}
 
 // the tiles of a CTA's rows: `sink` first ones, `gap` that no row sees, the rest
 struct KpTiles {
@@ -466,7 +472,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 const uint32_t pcol = dtu + 128 * x + 64 * (j & 1), ocol = dtu + LY::O + HD * x;
 #pragma unroll
                 for (int kk = 0; kk < KP_KEYS / 16; ++kk) {
-                    mma_ts(ocol, pcol + kk * 8, vt + 128 * kk, id_o, kk > 0 ? 1u : (uint32_t)(j > 0));
+                    mma_ts(ocol, pcol + kk * 8, vt + 128 * kk, id_o, kk > 0 ? 1u : (uint32_t)(FINE ? j % KP_FOLD > 0 : j > 0));
                     if constexpr (FINE) mma_ts(ocol, pcol + 32 + kk * 8, vt + 128 * kk, id_o, 1);
                 }
                 kp_commit(&pv_done[x]);
@@ -518,8 +524,49 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         const int xmin = p0 + (int)((base + x * KP_ROWS) / G);
         const int xmax = p0 + (int)((min(base + (x + 1) * KP_ROWS, rows_q) - 1) / G);
         const int lo = (int)max((long long)pos - p.window + 1, 0ll);   // this row sees [lo, pos] and [0, sinks)
+        const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq, all_rows = (size_t)p.b.total * p.Hq;
+        T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD;   // the result, or this split's part of it
+        float* piece = p.ws + (sp * all_rows + qrow) * HD;
+        // fp32 q: the tensor core cuts what it adds to its accumulator off, towards 0, and that shows after hundreds of
+        // additions (7e-6 after 450).  So O is folded into memory every KP_FOLD tiles, in rounded sums: 16 bytes of
+        // each row side by side, the rows of a CTA together (in the result's own rows a fold took 8 us)
+        const size_t fold_tile = ((size_t)((long long)row.t0 * G / (NQ * KP_ROWS)) + r + (size_t)(base / (NQ * KP_ROWS))) * c.Hkv + h;
+        float4* fold = reinterpret_cast<float4*>(p.ws + kp_part_floats(splits, all_rows, HD)) +
+                       (fold_tile * splits + sp) * (NQ * KP_ROWS * HD / 4) + x * (KP_ROWS * HD / 4) + m;   // + KP_ROWS * (column / 4)
+        float M_fold = -INFINITY;   // the maximum that the folded sums refer to
+        auto fold_o = [&](int cc) {   // columns cc .. cc + 63
+            float4 was[16];
+            const bool some = live && M_fold != -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) was[e] = some ? fold[KP_ROWS * (cc / 4 + e)] : make_float4(0.f, 0.f, 0.f, 0.f);
+            const float f = M_fold == -INFINITY || M_fold == M ? 1.f : kv8_exp2(M_fold - M);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t o[32];
+                tm_ld32(ocol + cc + 32 * q, o);
+                wait_ld();
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float4 w = was[8 * q + e];
+                    if (live && M != -INFINITY)
+                        fold[KP_ROWS * (cc / 4 + 8 * q + e)] =
+                            make_float4(fmaf(w.x, f, __uint_as_float(o[4 * e])), fmaf(w.y, f, __uint_as_float(o[4 * e + 1])),
+                                        fmaf(w.z, f, __uint_as_float(o[4 * e + 2])), fmaf(w.w, f, __uint_as_float(o[4 * e + 3])));
+                }
+            }
+        };
         for (int j = 0; j < (x < nact ? ntiles : 0); ++j) {
             const int k0 = key0(i0 + j);
+            bool rested = j == 0;   // P V of tile j - 1 is done
+            const bool folds = FINE && j > 0 && j % KP_FOLD == 0;
+            if (folds) {   // the next P V starts O anew, after P of this tile is full
+                if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
+                rested = true;
+                fence_after();
+#pragma unroll
+                for (int cc = 0; cc < HD; cc += 64) fold_o(cc);
+                M_fold = M;
+            }
             ok = warp_wait(&s_full[2 * x + (j & 1)], (uint32_t)(j >> 1) & 1u, ab, p.b.err) &&
                  warp_wait(&meta_full[j % KP_META], (uint32_t)(j / KP_META) & 1u, ab, p.b.err);
             if (!ok) break;
@@ -552,13 +599,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), kp_mul(fac, k.kf), k.ve));
             }
             float alpha = 1.f;
-            bool rested = j == 0;   // P V of tile j - 1 is done
             if (top > M + KP_SLACK) {
                 if (M != -INFINITY) alpha = kv8_exp2(M - top);   // else nothing has been summed yet
                 M = top;
                 l *= alpha;
             }
-            if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+            if (j > 0 && !folds && __any_sync(0xffffffffu, alpha != 1.f)) {
                 if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
                 rested = true;
                 fence_after();
@@ -639,17 +685,24 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     }
                 }
             }
-            // the result, or this split's part of it
             const float inv = l == 0.f ? 0.f : 1.f / l;
-            const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq, all_rows = (size_t)p.b.total * p.Hq;
-            T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD;
-            float* piece = p.ws + (sp * all_rows + qrow) * HD;
 #pragma unroll
             for (int cc = 0; cc < HD; cc += 16) {
                 uint32_t o[16];
                 if (ntiles > 0) {
                     tm_ld16(ocol + cc, o);
                     wait_ld();
+                    if (FINE && live && M_fold != -INFINITY) {   // and what is folded
+                        const float f = kv8_exp2(M_fold - M);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float4 w = fold[KP_ROWS * (cc / 4 + e)];
+                            o[4 * e] = __float_as_uint(fmaf(w.x, f, __uint_as_float(o[4 * e])));
+                            o[4 * e + 1] = __float_as_uint(fmaf(w.y, f, __uint_as_float(o[4 * e + 1])));
+                            o[4 * e + 2] = __float_as_uint(fmaf(w.z, f, __uint_as_float(o[4 * e + 2])));
+                            o[4 * e + 3] = __float_as_uint(fmaf(w.w, f, __uint_as_float(o[4 * e + 3])));
+                        }
+                    }
                 } else {
 #pragma unroll
                     for (int e = 0; e < 16; ++e) o[e] = 0u;
@@ -729,11 +782,12 @@ long long prompt_tiles(const Kv8Attend& p) {   // query tiles (of one CTA) of th
 
 // Splits of a query tile's positions: as many as bring the CTAs to the SMs'
 // count, each with at least 8 tiles of the most positions that a tile may see
+long long prompt_keys(const Kv8Attend& p) {   // the most positions that the rows of a CTA may see, and two tiles
+    const long long keys = (long long)p.c.ppr * p.c.page, win = (long long)p.window + p.sinks + p.b.max_new;
+    return (win < keys ? win : keys) + 2 * KP_KEYS;
+}
 int prompt_splits(const Kv8Attend& p, int num_sms) {
-    const long long ctas = prompt_tiles(p) * p.c.Hkv * p.c.rows;
-    long long keys = (long long)p.c.ppr * p.c.page;
-    const long long win = (long long)p.window + p.sinks + 2 * KP_KEYS + p.b.max_new;
-    if (win < keys) keys = win;
+    const long long ctas = prompt_tiles(p) * p.c.Hkv * p.c.rows, keys = prompt_keys(p);
     long long s = num_sms / ctas;
     if (s > keys / (8 * KP_KEYS)) s = keys / (8 * KP_KEYS);
     if (s > 32) s = 32;
@@ -770,7 +824,13 @@ cudaError_t launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
 
 size_t kv8_prompt_floats(const Kv8Attend& p, int num_sms) {
     const int splits = prompt_splits(p, num_sms);
-    return splits == 1 ? 0 : (size_t)splits * p.b.total * p.Hq * (p.c.hd + 2);
+    size_t n = kp_part_floats(splits, (size_t)p.b.total * p.Hq, p.c.hd);
+    // fp32 q and more tiles than O takes unfolded: a fold for each query tile of each row
+    if (p.dtype == W_F32 && (prompt_keys(p) / KP_KEYS + 2 + splits - 1) / splits > KP_FOLD) {
+        const size_t tiles = (size_t)p.b.total * (p.Hq / p.c.Hkv) / (2 * KP_ROWS) + p.c.rows + 1;
+        n += tiles * p.c.Hkv * splits * (2 * KP_ROWS) * p.c.hd;
+    }
+    return n;
 }
 
 cudaError_t kv8_prompt_launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
