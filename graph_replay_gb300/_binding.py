@@ -29,6 +29,7 @@ DEC_FAULT_WAIT = 0x10
 
 DEC_DTYPE_F32 = 0
 DEC_DTYPE_BF16 = 1
+DEC_DTYPE_E4M3 = 2
 DEC_KV_CONTIGUOUS = 0
 DEC_KV_PAGED = 1
 DEC_STRATEGY_GRAPH = 0
@@ -110,6 +111,9 @@ _SIG = [
     ("dec_logprobs", ctypes.c_int, [_P, _I32, _P, _P]),
     ("dec_set_strategy", ctypes.c_int, [_P, _I32]),
     ("dec_set_kv_sweep", ctypes.c_int, [_P, _I32]),
+    ("dec_set_window", ctypes.c_int, [_P, _I32, _I32]),
+    ("dec_kv_scale_ptr", ctypes.c_int, [_P, _I32, _I32, ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_size_t),
+                                        ctypes.POINTER(_I32)]),
     ("dec_set_eager", ctypes.c_int, [_P, _I32]),
     ("dec_reset_state", ctypes.c_int, [_P]),
     ("dec_kv_ptr", ctypes.c_int, [_P, _I32, _I32, ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_size_t)]),
@@ -268,6 +272,16 @@ def dec_set_strategy(h, strategy: int) -> None:
 
 def dec_set_kv_sweep(h, sweep: int) -> None:
     check(h, lib().dec_set_kv_sweep(h, sweep))
+
+
+def dec_set_window(h, window: int, sinks: int) -> None:
+    check(h, lib().dec_set_window(h, window, sinks))
+
+
+def dec_kv_scale_ptr(h, layer, which):
+    p, n, b = ctypes.c_void_p(), ctypes.c_size_t(), ctypes.c_int32()
+    check(h, lib().dec_kv_scale_ptr(h, layer, which, ctypes.byref(p), ctypes.byref(n), ctypes.byref(b)))
+    return p.value, n.value, b.value
 
 
 def dec_set_eager(h, eager: bool) -> None:

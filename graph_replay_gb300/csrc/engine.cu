@@ -53,12 +53,35 @@ struct StatusBlock {
 
 size_t align_up(size_t v) { return (v + ALIGN - 1) / ALIGN * ALIGN; }
 
-int es_of(int dtype) { return dtype == DEC_DTYPE_BF16 ? 2 : 4; }
+int es_of(int dtype) { return dtype == DEC_DTYPE_BF16 ? 2 : dtype == DEC_DTYPE_E4M3 ? 1 : 4; }
+
+// an e4m3 store: positions that share a scale, 0 if there is none for the layout
+int kv8_block(int layout, int page, int cap) {
+    const int n = layout == DEC_KV_PAGED ? page : cap;
+    for (int b : {64, 32, 16})
+        if (n % b == 0) return b;
+    return 0;
+}
+constexpr int KV8_SMS = 192;   // SMs that the scratch of the e4m3 attention is sized for: dec_workspace_size asks no device
+// its arguments as far as its scratch goes
+Kv8Attend kv8_shape(const dec_config& c, int cap, int R) {
+    Kv8Attend t{};
+    t.c.rows = R;
+    t.c.Hkv = c.n_kv_heads;
+    t.c.hd = c.head_dim;
+    t.c.ppr = 1;
+    t.c.page = cap;
+    t.b.max_new = 1;
+    t.b.total = R;
+    t.Hq = c.n_heads;
+    t.dtype = W_F32;
+    return t;
+}
 
 // Offsets of every buffer of a capture inside one workspace.
 struct WsLayout {
     size_t status, slots, slot_map, counters, trace, ptabs, tmaps, gbar, dbg, x, qkv, attn, gu, logits, part, gpart,
-        gcnt, chain, sampler, rope, kv, kv_layer, total;
+        gcnt, chain, sampler, rope, kv, kv_layer, kvs, kvs_layer, q_rot, kv8_counters, kv8_ws, total;
 };
 
 // kernels recorded per step: embedding, 5 per layer, head
@@ -108,6 +131,15 @@ bool compute_layout(const dec_config& c, int cap, int R, int layout, int page, i
         L->kv_layer = align_up((size_t)npages * Hkv * page * hd * es);
     else
         L->kv_layer = align_up((size_t)R * Hkv * cap * hd * es);
+    // e4m3 store: rotated q, the attention's counters and scratch, and the scales
+    const bool kv8 = c.kv_dtype == DEC_DTYPE_E4M3;
+    const int block = kv8 ? kv8_block(layout, page, cap) : 0;
+    L->q_rot = take(kv8 ? (size_t)R * Hq * hd * 4 : 0);
+    L->kv8_counters = take(kv8 ? (size_t)R * Hkv * sizeof(int) : 0);
+    L->kv8_ws = take(kv8 ? kv8_decode_floats(kv8_shape(c, cap, R), KV8_SMS) * sizeof(float) : 0);
+    L->kvs_layer = kv8 && block ? align_up(L->kv_layer / (hd * block) + 1) : 0;
+    L->kvs = take(0);
+    o += 2 * (size_t)c.n_layers * L->kvs_layer;
     L->kv = take(0);
     o += 2 * (size_t)c.n_layers * L->kv_layer;
     L->total = o;
@@ -126,6 +158,7 @@ struct dec_handle {
     bool eager = false;
     int strategy = DEC_STRATEGY_GRAPH;
     int kv_sweep = DEC_SWEEP_CAP;
+    int window = 0, sinks = 0;     // dec_set_window
     PersistPlan persist;
 
     // weights by role
@@ -154,6 +187,7 @@ struct dec_handle {
     float* d_part = nullptr;
     float2* d_rope = nullptr;
     std::vector<void*> K, V;
+    std::vector<void*> KS, VS;     // e4m3 store: the scales
 
     // pinned host staging
     int32_t* h_slots = nullptr;
@@ -256,8 +290,8 @@ int validate_config(const dec_config* c, dec_handle* h) {
     if (c->vocab < 1) return fail(h, DEC_E_INVALID, "vocab must be >= 1");
     if (c->weight_dtype != DEC_DTYPE_F32 && c->weight_dtype != DEC_DTYPE_BF16)
         return fail(h, DEC_E_INVALID, "weight_dtype must be DEC_DTYPE_F32 or DEC_DTYPE_BF16");
-    if (c->kv_dtype != DEC_DTYPE_F32 && c->kv_dtype != DEC_DTYPE_BF16)
-        return fail(h, DEC_E_INVALID, "kv_dtype must be DEC_DTYPE_F32 or DEC_DTYPE_BF16");
+    if (c->kv_dtype != DEC_DTYPE_F32 && c->kv_dtype != DEC_DTYPE_BF16 && c->kv_dtype != DEC_DTYPE_E4M3)
+        return fail(h, DEC_E_INVALID, "kv_dtype must be DEC_DTYPE_F32, DEC_DTYPE_BF16 or DEC_DTYPE_E4M3");
     if (!(c->rms_eps >= 0.0) || !std::isfinite(c->rms_eps)) return fail(h, DEC_E_INVALID, "rms_eps must be finite and >= 0");
     if (!(c->rope_theta > 0.0) || !std::isfinite(c->rope_theta)) return fail(h, DEC_E_INVALID, "rope_theta must be finite and > 0");
     if (c->device < 0) return fail(h, DEC_E_INVALID, "device must be >= 0");
@@ -265,6 +299,8 @@ int validate_config(const dec_config* c, dec_handle* h) {
     const int hd = c->head_dim;
     if (hd != 16 && hd != 32 && hd != 64 && hd != 128)
         return fail(h, DEC_E_UNSUPPORTED, "head_dim %d unsupported (16, 32, 64 or 128)", hd);
+    if (c->kv_dtype == DEC_DTYPE_E4M3 && hd != 64 && hd != 128)
+        return fail(h, DEC_E_UNSUPPORTED, "an e4m3 K/V store needs head_dim 64 or 128, not %d", hd);
     const int G = c->n_heads / c->n_kv_heads;
     if (G != 1 && G != 2 && G != 4 && G != 8)
         return fail(h, DEC_E_UNSUPPORTED, "n_heads / n_kv_heads = %d unsupported (1, 2, 4 or 8)", G);
@@ -312,11 +348,21 @@ std::vector<float2> rope_table(int cap, int hd, double theta) {
 }
 
 cudaError_t launch_attn(const AttnPlan& a, cudaStream_t s, bool pdl) {
+    if (a.kv8) return attn_kv8_launch(a, s, pdl);
     if (a.prewrite) {
         cudaError_t e = kv_write_launch(a, s, pdl);
         if (e != cudaSuccess) return e;
     }
     return a.mma ? attn_mma_launch(a, s, pdl) : attn_launch(a, s, pdl);
+}
+
+// layer l's e4m3 store as the kernels take it
+Kv8Cache kv8_cache(const dec_handle* h, int l) {
+    const bool paged = h->layout == DEC_KV_PAGED;
+    const int page = paged ? h->page : h->cap, block = kv8_block(h->layout, h->page, h->cap);
+    return Kv8Cache{(uint8_t*)h->K[l], (uint8_t*)h->V[l], (uint8_t*)h->KS[l], (uint8_t*)h->VS[l], h->d_slot_map, h->rows,
+                    paged ? h->ppr : 1, page, paged ? h->npages : h->rows, h->cfg.n_kv_heads, h->cfg.head_dim, block,
+                    kv8_log2(block), FastDiv((unsigned)page)};
 }
 
 // launch the whole step (the sequence the graph records)
@@ -358,7 +404,14 @@ cudaError_t zero_state(dec_handle* h) {
     for (int l = 0; l < h->cfg.n_layers; ++l) {
         if ((e = cudaMemsetAsync(h->K[l], 0, h->lay.kv_layer, h->stream)) != cudaSuccess) return e;
         if ((e = cudaMemsetAsync(h->V[l], 0, h->lay.kv_layer, h->stream)) != cudaSuccess) return e;
+        if (!h->lay.kvs_layer) continue;
+        // zeros at scale 1
+        if ((e = cudaMemsetAsync(h->KS[l], 127, h->lay.kvs_layer, h->stream)) != cudaSuccess) return e;
+        if ((e = cudaMemsetAsync(h->VS[l], 127, h->lay.kvs_layer, h->stream)) != cudaSuccess) return e;
     }
+    if (h->lay.kvs_layer && (e = cudaMemsetAsync(h->ws + h->lay.kv8_counters, 0, sizeof(int) * h->rows * h->cfg.n_kv_heads,
+                                                 h->stream)) != cudaSuccess)
+        return e;
     if ((e = cudaMemsetAsync(h->d_status, 0, sizeof(StatusBlock), h->stream)) != cudaSuccess) return e;
     if ((e = cudaMemsetAsync(h->ws + h->lay.gbar, 0, ((size_t)h->kernels + 3) * sizeof(unsigned), h->stream)) !=
         cudaSuccess)
@@ -483,6 +536,7 @@ int dec_workspace_size(const dec_config* cfg, int32_t cap, int32_t rows, int32_t
     if (validate_config(cfg, nullptr) != DEC_OK) return DEC_E_INVALID;
     if (cap < 1 || rows < 1 || rows > MAX_ROWS) return DEC_E_INVALID;
     if (kv_layout == DEC_KV_PAGED && (page_size < 1 || cap % page_size || num_pages < 1)) return DEC_E_INVALID;
+    if (cfg->kv_dtype == DEC_DTYPE_E4M3 && !kv8_block(kv_layout, page_size, cap)) return DEC_E_INVALID;
     WsLayout L;
     compute_layout(*cfg, cap, rows, kv_layout, page_size, num_pages, &L);
     *bytes = L.total;
@@ -506,6 +560,13 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
         if ((int64_t)num_pages * page_size > INT32_MAX) return fail(h, DEC_E_UNSUPPORTED, "pool too large");
     }
     if ((int64_t)cap * c.head_dim > INT32_MAX) return fail(h, DEC_E_UNSUPPORTED, "cap too large");
+    const bool kv8 = c.kv_dtype == DEC_DTYPE_E4M3;
+    if (kv8 && !kv8_block(kv_layout, page_size, cap))
+        return fail(h, DEC_E_UNSUPPORTED, "an e4m3 K/V store needs %s a multiple of 16",
+                    kv_layout == DEC_KV_PAGED ? "pages of" : "a cap that is");
+    if (kv8 && h->strategy == DEC_STRATEGY_PERSISTENT)
+        return fail(h, DEC_E_UNSUPPORTED, "an e4m3 K/V store needs DEC_STRATEGY_GRAPH");
+    if (h->window && !kv8) return fail(h, DEC_E_UNSUPPORTED, "a window needs an e4m3 K/V store");
     if (!h->embed) return fail(h, DEC_E_INVALID, "weight EMBED is unbound");
     if (!h->final_norm) return fail(h, DEC_E_INVALID, "weight FINAL_NORM is unbound");
     if (!h->lm_head) return fail(h, DEC_E_INVALID, "weight LM_HEAD is unbound");
@@ -562,9 +623,13 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
     h->d_rope = (float2*)(h->ws + L.rope);
     h->K.resize(c.n_layers);
     h->V.resize(c.n_layers);
+    h->KS.resize(c.n_layers);
+    h->VS.resize(c.n_layers);
     for (int l = 0; l < c.n_layers; ++l) {
         h->K[l] = h->ws + L.kv + (size_t)(2 * l) * L.kv_layer;
         h->V[l] = h->ws + L.kv + (size_t)(2 * l + 1) * L.kv_layer;
+        h->KS[l] = kv8 ? h->ws + L.kvs + (size_t)(2 * l) * L.kvs_layer : nullptr;
+        h->VS[l] = kv8 ? h->ws + L.kvs + (size_t)(2 * l + 1) * L.kvs_layer : nullptr;
     }
 
     if ((e = cudaHostAlloc((void**)&h->h_slots, 3 * sizeof(int32_t) * rows, cudaHostAllocDefault)) != cudaSuccess)
@@ -709,7 +774,20 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
     }
     const char* att_env = getenv("GRAPHDEC_ATTN");   // "simd" selects the CUDA-core attention kernel
     const bool allow_mma = !(att_env && strcmp(att_env, "simd") == 0);
+    for (int l = 0; kv8 && l < c.n_layers; ++l) {
+        AttnPlan& ap = h->attn[l];
+        ap.kv8 = true;
+        ap.cache = kv8_cache(h, l);
+        ap.q_rot = (float*)(h->ws + L.q_rot);
+        ap.kv8_counters = (int*)(h->ws + L.kv8_counters);
+        ap.kv8_ws = (float*)(h->ws + L.kv8_ws);
+        ap.window = h->window;
+        ap.sinks = h->sinks;
+        ap.num_sms = h->num_sms < KV8_SMS ? h->num_sms : KV8_SMS;
+        ap.prewrite = rows >= 2;   // every row's K/V lands before any row's attention
+    }
     for (auto& ap : h->attn) {
+        if (ap.kv8) continue;
         if (allow_mma && attn_mma_supported(ap.kvtype, hd, Hq / Hkv, ap.paged, ap.p.page_size)) {
             if ((e = attn_mma_plan(&ap, h->num_sms)) != cudaSuccess)
                 return fail(h, DEC_E_UNSUPPORTED, "no attention kernel for head_dim=%d group=%d cap=%d (%s)", hd,
@@ -731,7 +809,7 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
                         Hq / Hkv, cap, cudaGetErrorString(e));
     }
     h->kernels = kernels_per_step(c.n_layers);
-    h->extra_kernels = ((!h->attn.empty() && h->attn[0].prewrite) ? c.n_layers : 0) + (h->sampler_on ? 1 : 0);
+    h->extra_kernels = ((!h->attn.empty() && (h->attn[0].prewrite || kv8)) ? c.n_layers : 0) + (h->sampler_on ? 1 : 0);
     if ((e = cudaMemsetAsync(h->d_trace, 0, sizeof(unsigned long long), h->stream)) != cudaSuccess)
         return cuda_fail(h, e, "trace clear");
     if (h->strategy == DEC_STRATEGY_PERSISTENT) {
@@ -965,7 +1043,7 @@ int dec_prefill(dec_handle* h, const int32_t* pages, const int32_t* tokens, int3
     if (h->state == ST_NEEDS_RESET) return fail(h, DEC_E_NEEDS_RESET, "an earlier step failed; call dec_reset_state");
     if (h->layout != DEC_KV_PAGED || h->rows < 2 || h->strategy != DEC_STRATEGY_GRAPH || h->attn.empty() ||
         !h->attn[0].prewrite)
-        return fail(h, DEC_E_UNSUPPORTED, "multi-token prefill needs a paged graph capture of 2..8 rows with bf16 K/V");
+        return fail(h, DEC_E_UNSUPPORTED, "multi-token prefill needs a paged graph capture of 2..8 rows with bf16 or e4m3 K/V");
     if (!pages || !tokens) return fail(h, DEC_E_INVALID, "pages and tokens are required");
     if (n < 1 || pos0 < 0 || (int64_t)pos0 + n > h->cap)
         return fail(h, DEC_E_RANGE, "positions [%d, %d) outside [0, %d)", pos0, pos0 + n, h->cap);
@@ -1020,8 +1098,8 @@ int dec_prefill_block(dec_handle* h, int32_t row, const int32_t* pages, const in
     if (rc) return rc;
     if (h->state == ST_NEEDS_RESET) return fail(h, DEC_E_NEEDS_RESET, "an earlier step failed; call dec_reset_state");
     const dec_config& c = h->cfg;
-    if (c.weight_dtype != DEC_DTYPE_BF16 || c.kv_dtype != DEC_DTYPE_BF16)
-        return fail(h, DEC_E_UNSUPPORTED, "the block prefill needs bf16 weights and K/V");
+    if (c.weight_dtype != DEC_DTYPE_BF16 || c.kv_dtype == DEC_DTYPE_F32)
+        return fail(h, DEC_E_UNSUPPORTED, "the block prefill needs bf16 weights and bf16 or e4m3 K/V");
     PrefillArgs a{};
     a.L = c.n_layers; a.d = c.d_model; a.Hq = c.n_heads; a.Hkv = c.n_kv_heads; a.hd = c.head_dim;
     a.F = c.ffn_hidden; a.cap = h->cap; a.eps = (float)c.rms_eps;
@@ -1029,6 +1107,12 @@ int dec_prefill_block(dec_handle* h, int32_t row, const int32_t* pages, const in
     a.lw = reinterpret_cast<const void* const*>(h->lw.data());
     a.K = h->K.data();
     a.V = h->V.data();
+    a.kv8 = c.kv_dtype == DEC_DTYPE_E4M3;
+    a.KS = h->KS.data();
+    a.VS = h->VS.data();
+    a.block = a.kv8 ? kv8_block(h->layout, h->page, h->cap) : 0;
+    a.window = h->window;
+    a.sinks = h->sinks;
     a.paged = h->layout == DEC_KV_PAGED;
     a.page = h->page;
     a.ppr = h->ppr;
@@ -1145,6 +1229,32 @@ int dec_set_kv_sweep(dec_handle* h, int32_t sweep) {
     if (h->captured) return fail(h, DEC_E_STATE, "the K/V sweep is chosen before dec_capture");
     if (sweep != DEC_SWEEP_CAP && sweep != DEC_SWEEP_POS) return fail(h, DEC_E_INVALID, "unknown K/V sweep %d", sweep);
     h->kv_sweep = sweep;
+    return DEC_OK;
+}
+
+int dec_set_window(dec_handle* h, int32_t window, int32_t sinks) {
+    int rc = gate(h, false);
+    if (rc) return rc;
+    if (h->captured) return fail(h, DEC_E_STATE, "the window is chosen before dec_capture");
+    if (window < 0 || sinks < 0) return fail(h, DEC_E_INVALID, "window and sinks must be >= 0");
+    h->window = window;
+    h->sinks = window ? sinks : 0;
+    return DEC_OK;
+}
+
+int dec_kv_scale_ptr(dec_handle* h, int32_t layer, int32_t which, void** ptr, size_t* bytes, int32_t* block) {
+    int rc = gate(h, true);
+    if (rc) return rc;
+    if (h->cfg.kv_dtype != DEC_DTYPE_E4M3) return fail(h, DEC_E_STATE, "the K/V store is not e4m3: it has no scales");
+    if (layer < 0 || layer >= h->cfg.n_layers || (which != 0 && which != 1) || !ptr)
+        return fail(h, DEC_E_INVALID, "dec_kv_scale_ptr: bad layer/which/ptr");
+    const int b = kv8_block(h->layout, h->page, h->cap);
+    *ptr = which ? h->VS[layer] : h->KS[layer];
+    if (bytes) {
+        const size_t positions = h->layout == DEC_KV_PAGED ? (size_t)h->npages * h->page : (size_t)h->rows * h->cap;
+        *bytes = positions / b * h->cfg.n_kv_heads;
+    }
+    if (block) *block = b;
     return DEC_OK;
 }
 
@@ -1359,6 +1469,10 @@ int engine_run_attention(dec_handle* h, int32_t layer, const float* qkv, const i
 
 // split scratch one layer's attention needs: partial floats and counters
 void engine_attention_scratch(const dec_handle* h, size_t* part_floats, size_t* counters) {
+    if (h->cfg.kv_dtype == DEC_DTYPE_E4M3) {   // its scratch is the handle's own
+        *part_floats = *counters = SIZE_MAX;
+        return;
+    }
     *part_floats = attn_part_floats(h->rows, h->cfg.n_heads, h->cfg.head_dim, h->attn.empty() ? 0 : h->attn[0].p.nsplit);
     *counters = (size_t)h->rows * h->cfg.n_kv_heads;
 }

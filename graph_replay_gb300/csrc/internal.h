@@ -85,6 +85,89 @@ size_t gemv_box_part_floats(int R, int K, int N);
 constexpr size_t GEMV_TC_CNT_WORDS = 1024;
 cudaError_t gemv_launch(const GemvPlan& plan, cudaStream_t s, bool pdl);
 
+// ---------------- the 8-bit K/V cache (kv8*.cu) ----------------
+constexpr int KV8_MAX_ROWS = 1024;
+// what a kernel needs to be told once on each device (a race only tells it twice)
+struct OncePerDevice {
+    std::atomic<unsigned long long> done{0};
+    template <typename F>
+    cudaError_t run(F f) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = 1ull << (dev & 63);
+        if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+        if ((e = f()) == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
+// n / d for 0 <= n < 2^31 without a division: mul = ceil(2^(31 + shift) / d), shift = ceil(log2 d)
+struct FastDiv {
+    unsigned d, mul, shift;
+    FastDiv() = default;
+    explicit FastDiv(unsigned d_) : d(d_), shift(0) {
+        while ((1ull << shift) < d) ++shift;
+        mul = (unsigned)(((1ull << (31 + shift)) + d - 1) / d);
+    }
+#ifdef __CUDACC__
+    __device__ __forceinline__ int of(int n) const { return (int)(__umulhi((unsigned)n << 1, mul) >> shift); }
+#endif
+};
+struct Kv8Cache {              // a dec_kv8_cache that passed its checks
+    uint8_t *k, *v;            // [num_pages, Hkv, page, hd] e4m3
+    uint8_t *ks, *vs;          // [num_pages, Hkv, page / block] exponent + 127
+    const int* pages;          // [rows, ppr] or null: row r owns pages r * ppr ..
+    int rows, ppr, page, num_pages, Hkv, hd, block, block_log2;
+    FastDiv by_page;
+};
+inline int kv8_log2(int block) { return block == 16 ? 4 : block == 32 ? 5 : block == 64 ? 6 : 7; }
+struct Kv8Batch {
+    const int* q_start;        // [rows + 1] or null: one token a row
+    const int* kv_len;         // [rows], or null: one row of len_add positions with all tokens
+    int total, max_new;
+    unsigned* err;
+    int len_add;               // added to kv_len: 1 where it is the position of a row's one token
+};
+struct Kv8Append {
+    Kv8Cache c;
+    Kv8Batch b;
+    const void *k, *v;         // [total, Hkv, hd], token strides below (elements)
+    long long k_stride, v_stride;
+    int dtype;                 // W_F32 / W_BF16
+};
+struct Kv8Attend {
+    Kv8Cache c;
+    Kv8Batch b;
+    const void* q;             // [total, Hq, hd]
+    void* out;                 // [total, Hq, hd]
+    long long q_stride, out_stride;
+    int dtype, Hq;
+    int window, sinks;         // window INT_MAX: every position up to the token's own
+    float scale;
+    int* counters;             // [rows, Hkv], zero between calls
+    float* ws;                 // kv8_decode_floats() or kv8_prompt_floats() floats
+};
+// a decode step's q, K and V (kv8_step.cu)
+struct Kv8Step {
+    Kv8Cache c;
+    const float* qkv;          // [R, qkv_stride]: q, k, v of every row, before RoPE
+    int qkv_stride, Hq, R, cap;
+    const int* pos;            // [R] Pos slot
+    const int* write_map;      // [R] WriteMap slot (paged) or null
+    const float2* rope;        // [cap, hd / 2]
+    float* q_out;              // [R, Hq * hd]: q after RoPE
+    unsigned* err;
+};
+cudaError_t kv8_step_launch(const Kv8Step& p, cudaStream_t s, bool pdl);
+cudaError_t kv8_append_launch(const Kv8Append& p, cudaStream_t s);
+// up to 16 query rows (tokens x query heads of a K/V head) of a sequence (kv8_decode.cu)
+bool kv8_decode_takes(const Kv8Attend& p);
+cudaError_t kv8_decode_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
+size_t kv8_decode_floats(const Kv8Attend& p, int num_sms);   // of workspace
+// any number of query rows (kv8_prompt.cu)
+cudaError_t kv8_prompt_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
+size_t kv8_prompt_floats(const Kv8Attend& p, int num_sms);
+
 // ---------------- split-KV masked decode attention ----------------
 struct AttnParams {
     const float* qkv;      // [R, qkv_stride]: q [Hq*hd], k [Hkv*hd], v [Hkv*hd] (fp32, pre-RoPE)
@@ -121,12 +204,20 @@ struct AttnPlan {
     bool mma = false;              // tensor-core kernel (attn_mma.cu)
     void* mma_params = nullptr;    // its parameter block (tensor maps + p), owned by the plan
     bool prewrite = false;         // launch k_kv_write before the attention (p.kv_prewritten = 1)
+    bool kv8 = false;              // e4m3 store: kv8_step.cu, then kv8_decode.cu, with what stands below
+    Kv8Cache cache{};
+    float* q_rot = nullptr;        // [R, Hq * hd]
+    int* kv8_counters = nullptr;
+    float* kv8_ws = nullptr;
+    int window = 0, sinks = 0, num_sms = 0;
 };
 
 // RoPE of every row's k at Pos, rounding and store of k, v (bf16 store) at the
 // row's position or WriteMap slot, before the attention of any row reads them
 cudaError_t kv_write_launch(const AttnPlan& plan, cudaStream_t s, bool pdl);
 
+// the attention of an e4m3 store: two launches
+cudaError_t attn_kv8_launch(const AttnPlan& plan, cudaStream_t s, bool pdl);
 // choose split_len / nsplit; returns cudaErrorInvalidValue for unsupported head_dim / group
 cudaError_t attn_plan(AttnPlan* plan, int num_sms);
 cudaError_t attn_launch(const AttnPlan& plan, cudaStream_t s, bool pdl);
@@ -253,6 +344,9 @@ struct PrefillArgs {
     const void* const* lw;      // host array [L * 9] of device pointers: attn_norm, q, k, v, o, ffn_norm, gate, up, down
     void* const* K;             // host array [L] of device pointers: K store of each layer
     void* const* V;             // host array [L]: V store
+    bool kv8;                   // e4m3 store, with scales and perhaps a window; else bf16
+    void* const *KS, *const *VS;   // host arrays [L]: scales of each layer
+    int block, window, sinks;
     bool paged;
     int page, ppr;              // paged: tokens per page, pages per sequence
     int rows, num_pages;        // contiguous: the capture's rows; paged: the pool's pages
@@ -270,75 +364,6 @@ void prefill_free(PrefillState* s);
 // positions written; the last token's hidden state (fp32 [d]) to x_last (device)
 cudaError_t prefill_run(PrefillState* s, const int* tokens, int n, int pos0, int row, const int* pages, float* x_last,
                         cudaStream_t st);
-
-// ---------------- the 8-bit K/V cache (kv8*.cu) ----------------
-constexpr int KV8_MAX_ROWS = 1024;
-// what a kernel needs to be told once on each device (a race only tells it twice)
-struct OncePerDevice {
-    std::atomic<unsigned long long> done{0};
-    template <typename F>
-    cudaError_t run(F f) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        const unsigned long long bit = 1ull << (dev & 63);
-        if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
-        if ((e = f()) == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
-        return e;
-    }
-};
-// n / d for 0 <= n < 2^31 without a division: mul = ceil(2^(31 + shift) / d), shift = ceil(log2 d)
-struct FastDiv {
-    unsigned d, mul, shift;
-    FastDiv() = default;
-    explicit FastDiv(unsigned d_) : d(d_), shift(0) {
-        while ((1ull << shift) < d) ++shift;
-        mul = (unsigned)(((1ull << (31 + shift)) + d - 1) / d);
-    }
-#ifdef __CUDACC__
-    __device__ __forceinline__ int of(int n) const { return (int)(__umulhi((unsigned)n << 1, mul) >> shift); }
-#endif
-};
-struct Kv8Cache {              // a dec_kv8_cache that passed its checks
-    uint8_t *k, *v;            // [num_pages, Hkv, page, hd] e4m3
-    uint8_t *ks, *vs;          // [num_pages, Hkv, page / block] exponent + 127
-    const int* pages;          // [rows, ppr] or null: row r owns pages r * ppr ..
-    int rows, ppr, page, num_pages, Hkv, hd, block, block_log2;
-    FastDiv by_page;
-};
-struct Kv8Batch {
-    const int* q_start;        // [rows + 1] or null: one token a row
-    const int* kv_len;         // [rows]
-    int total, max_new;
-    unsigned* err;
-};
-struct Kv8Append {
-    Kv8Cache c;
-    Kv8Batch b;
-    const void *k, *v;         // [total, Hkv, hd], token strides below (elements)
-    long long k_stride, v_stride;
-    int dtype;                 // W_F32 / W_BF16
-};
-struct Kv8Attend {
-    Kv8Cache c;
-    Kv8Batch b;
-    const void* q;             // [total, Hq, hd]
-    void* out;                 // [total, Hq, hd]
-    long long q_stride, out_stride;
-    int dtype, Hq;
-    int window, sinks;         // window INT_MAX: every position up to the token's own
-    float scale;
-    int* counters;             // [rows, Hkv], zero between calls
-    float* ws;                 // kv8_decode_floats() or kv8_prompt_floats() floats
-};
-cudaError_t kv8_append_launch(const Kv8Append& p, cudaStream_t s);
-// up to 16 query rows (tokens x query heads of a K/V head) of a sequence (kv8_decode.cu)
-bool kv8_decode_takes(const Kv8Attend& p);
-cudaError_t kv8_decode_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
-size_t kv8_decode_floats(const Kv8Attend& p, int num_sms);   // of workspace
-// any number of query rows (kv8_prompt.cu)
-cudaError_t kv8_prompt_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
-size_t kv8_prompt_floats(const Kv8Attend& p, int num_sms);
 
 }  // namespace gd
 

@@ -62,8 +62,7 @@ int check_cache(const dec_kv8_cache* c, Kv8Cache* out) {
     if (c->device < 0) return refuse(DEC_E_INVALID, "device must be >= 0");
     *out = Kv8Cache{(uint8_t*)c->k, (uint8_t*)c->v, c->k_scale, c->v_scale, c->pages, c->rows, c->pages_per_row,
                     c->page_size, c->num_pages, c->n_kv_heads, c->head_dim, c->scale_block,
-                    c->scale_block == 16 ? 4 : c->scale_block == 32 ? 5 : c->scale_block == 64 ? 6 : 7,
-                    FastDiv((unsigned)c->page_size)};
+                    kv8_log2(c->scale_block), FastDiv((unsigned)c->page_size)};
     return DEC_OK;
 }
 
@@ -74,7 +73,7 @@ int check_batch(const dec_kv8_batch* b, const Kv8Cache& c, Kv8Batch* out) {
     if (!b->q_start && (b->total != c.rows || b->max_new != 1))
         return refuse(DEC_E_INVALID, "without q_start each row has one token: total = rows, max_new = 1");
     if (b->max_new > (1 << 24)) return refuse(DEC_E_UNSUPPORTED, "max_new = %d: at most 2^24", b->max_new);
-    *out = Kv8Batch{b->q_start, b->kv_len, b->total, b->max_new, b->err};
+    *out = Kv8Batch{b->q_start, b->kv_len, b->total, b->max_new, b->err, 0};
     return DEC_OK;
 }
 

@@ -23,9 +23,13 @@ struct Kv8Row {
 };
 // false: the row's entries are out of range (FAULT_POS); nothing of it is touched
 __device__ __forceinline__ bool kv8_row(const Kv8Batch& b, int cap, int r, Kv8Row* out) {
+    if (!b.kv_len) {   // one row, by the launch
+        *out = Kv8Row{0, b.total, b.len_add};
+        return true;
+    }
     const int t0 = b.q_start ? b.q_start[r] : r;
     const int t1 = b.q_start ? b.q_start[r + 1] : r + 1;
-    const int len = b.kv_len[r];
+    const int len = (int)((unsigned)b.kv_len[r] + (unsigned)b.len_add);
     if (t0 < 0 || t1 < t0 || t1 > b.total || t1 - t0 > b.max_new || len < 0 || len > cap) {
         atomicOr(b.err, FAULT_POS);
         return false;
@@ -70,6 +74,15 @@ __device__ __forceinline__ uint32_t f32_to_e4m3x4(float a, float b, float c, flo
         : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
 }
+constexpr int KV8_EXP_MIN = -40, KV8_EXP_MAX = 60;
+
+// least e with top <= 448 * 2^e; 448 = 1.75 * 2^8
+__device__ __forceinline__ int kv8_exponent(float top) {
+    const uint32_t b = __float_as_uint(top);
+    const int e = (int)(b >> 23) - 135 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return min(max(e, KV8_EXP_MIN), KV8_EXP_MAX);
+}
+
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 // 2^x by the hardware's base-2 exponential

@@ -19,16 +19,7 @@ namespace gd {
 
 namespace {
 
-constexpr int KV8_EXP_MIN = -40, KV8_EXP_MAX = 60;
-
 __device__ __forceinline__ bool finite_f(float x) { return fabsf(x) <= 3.402823466e38f; }
-
-// least e with top <= 448 * 2^e; 448 = 1.75 * 2^8
-__device__ __forceinline__ int kv8_exponent(float top) {
-    const uint32_t b = __float_as_uint(top);
-    const int e = (int)(b >> 23) - 135 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return min(max(e, KV8_EXP_MIN), KV8_EXP_MAX);
-}
 
 // 8 values as they came from memory, until they are needed: half the registers for bf16
 template <typename T>

@@ -21,6 +21,7 @@
 // significant bits, fp32 accumulation); everything else is fp32, and K/V are
 // rounded to the KV dtype (bf16) when stored, as in a decode step.
 #include <cuda.h>
+#include <limits.h>
 #include <math.h>
 #include <vector>
 
@@ -157,8 +158,9 @@ __device__ __forceinline__ size_t kv_off(const PfKv& kv, int g, int pos) {
 // Four consecutive dims per thread and step (16-byte loads), every load of a
 // step issued before its arithmetic; the partial sums, the RoPE table and the
 // page table are read-only here (non-coherent loads).
+// kvout (e4m3 store): k and v of each token side by side in fp32, for dec_kv8_append's kernel, and the store untouched.
 __global__ void k_pf_qkv(const float* part, int splits, int ntp, int Hq, int nt, int pos0, const float2* rope,
-                         float* qout, PfKv kv) {
+                         float* qout, PfKv kv, float* kvout) {
     const int t = blockIdx.x;
     if (t >= nt) return;
     const int hd = kv.hd, h2 = hd / 2, qd = Hq * hd, kvd = kv.Hkv * hd, N = qd + 2 * kvd;
@@ -194,6 +196,10 @@ __global__ void k_pf_qkv(const float* part, int splits, int ntp, int Hq, int nt,
                 float* qo = qout + (size_t)t * qd + hh * hd + e;
                 *reinterpret_cast<float4*>(qo) = make_float4(r0[0], r0[1], r0[2], r0[3]);
                 *reinterpret_cast<float4*>(qo + h2) = make_float4(r1[0], r1[1], r1[2], r1[3]);
+            } else if (kvout) {
+                float* ko = kvout + (size_t)t * 2 * kvd + (hh - Hq) * hd + e;
+                *reinterpret_cast<float4*>(ko) = make_float4(r0[0], r0[1], r0[2], r0[3]);
+                *reinterpret_cast<float4*>(ko + h2) = make_float4(r1[0], r1[1], r1[2], r1[3]);
             } else {
                 __nv_bfloat16* ko = kv.K + kv_off(kv, hh - Hq, pos) + e;
                 *reinterpret_cast<uint2*>(ko) = make_uint2(pack_bf16x2(r0[0], r0[1]), pack_bf16x2(r0[2], r0[3]));
@@ -204,7 +210,10 @@ __global__ void k_pf_qkv(const float* part, int splits, int ntp, int Hq, int nt,
             float4 v = __ldg(reinterpret_cast<const float4*>(pp + qd + kvd + j));
             for (int s = 1; s < splits; ++s)
                 v = f4add(v, __ldg(reinterpret_cast<const float4*>(pp + (size_t)s * ntp * N + qd + kvd + j)));
-            *reinterpret_cast<uint2*>(kv.V + kv_off(kv, g, pos) + e) =
+            if (kvout)
+                *reinterpret_cast<float4*>(kvout + (size_t)t * 2 * kvd + kvd + j) = v;
+            else
+                *reinterpret_cast<uint2*>(kv.V + kv_off(kv, g, pos) + e) =
                 make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
         }
     }
@@ -626,6 +635,13 @@ __global__ void k_pf_zero_rows(__nv_bfloat16* hb, int K, int nt) {
     for (int k = threadIdx.x * 4; k < K; k += blockDim.x * 4) put_hilo4(hb, K, t, k, make_float4(0.f, 0.f, 0.f, 0.f));
 }
 
+// attention results (fp32) as the O projection's hi/lo rows
+__global__ void k_pf_hilo(const float* o, int K, __nv_bfloat16* hb) {
+    const int t = blockIdx.x;
+    for (int k = threadIdx.x * 4; k < K; k += blockDim.x * 4)
+        put_hilo4(hb, K, t, k, __ldg(reinterpret_cast<const float4*>(o + (size_t)t * K + k)));
+}
+
 typedef CUresult (*PfEncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -698,6 +714,9 @@ struct PrefillState {
     int* pages = nullptr;
     std::vector<PfProj> proj;   // per layer: qkv, o, gate/up, down
     size_t part_floats = 0;
+    float *kv = nullptr, *o = nullptr;   // e4m3 store: a pass's k and v, and its attention results (fp32)
+    int* kv8_counters = nullptr;         // and the attention's counters and scratch
+    float* kv8_ws = nullptr;
     CUtensorMap* kvmaps = nullptr;   // device [L][K, V]: the attention's TMA maps of the K/V stores
 };
 
@@ -724,10 +743,10 @@ bool prefill_supported(const PrefillArgs& a) {
     const int qd = a.Hq * a.hd;
     if (a.hd != 64 && a.hd != 128) return false;
     const int G = a.Hq / a.Hkv;
-    if (G != 2 && G != 4) return false;
+    if (!a.kv8 && G != 2 && G != 4) return false;
     if (a.d % PF_BK || qd % PF_BK || a.F % PF_BK) return false;
     if (a.d > 4 * PF_NT * PF_RN) return false;   // the norm kernel's row in registers
-    if (a.paged && (a.page < 8 || 64 % a.page)) return false;   // whole 8-row swizzle atoms per page box
+    if (!a.kv8 && a.paged && (a.page < 8 || 64 % a.page)) return false;   // whole 8-row swizzle atoms per page box
     return true;
 }
 
@@ -741,6 +760,10 @@ void prefill_free(PrefillState* s) {
     cudaFree(s->tok);
     cudaFree(s->pages);
     cudaFree(s->kvmaps);
+    cudaFree(s->kv);
+    cudaFree(s->o);
+    cudaFree(s->kv8_counters);
+    cudaFree(s->kv8_ws);
     delete s;
 }
 
@@ -753,6 +776,41 @@ static const void* pf_attn_fn(int hd, int G) {
         if (G == 2) return (const void*)&k_pf_attn_tc<64, 2>;
     }
     return nullptr;
+}
+
+// layer l's e4m3 store as the one row that a prefill works on: `row` of the contiguous store, or the pages
+static Kv8Attend pf_kv8(const PrefillState* s, int l, int row, int nt, int len) {
+    const PrefillArgs& a = s->a;
+    Kv8Attend t{};
+    const size_t first = a.paged ? 0 : (size_t)row * a.Hkv * a.cap;   // pool rows before it
+    const int page = a.paged ? a.page : a.cap;
+    t.c = Kv8Cache{(uint8_t*)a.K[l] + first * a.hd, (uint8_t*)a.V[l] + first * a.hd, (uint8_t*)a.KS[l] + first / a.block,
+                   (uint8_t*)a.VS[l] + first / a.block, a.paged ? s->pages : nullptr, 1, a.paged ? a.ppr : 1, page,
+                   a.paged ? a.num_pages : 1, a.Hkv, a.hd, a.block, kv8_log2(a.block), FastDiv((unsigned)page)};
+    t.b = Kv8Batch{nullptr, nullptr, nt, nt, a.err, len};
+    t.q = s->q;
+    t.out = s->o;
+    t.q_stride = t.out_stride = (long long)a.Hq * a.hd;
+    t.dtype = W_F32;
+    t.Hq = a.Hq;
+    t.window = a.window ? a.window : INT_MAX;
+    t.sinks = a.window ? a.sinks : 0;
+    t.scale = (float)(1.0 / sqrt((double)a.hd));
+    t.counters = s->kv8_counters;
+    t.ws = s->kv8_ws;
+    return t;
+}
+static cudaError_t pf_attend_kv8(const PrefillState* s, int l, int row, int nt, int p0, cudaStream_t st) {
+    const PrefillArgs& a = s->a;
+    const int kvd = a.Hkv * a.hd;
+    const Kv8Attend t = pf_kv8(s, l, row, nt, p0 + nt);
+    Kv8Append n{t.c, t.b, s->kv, s->kv + kvd, 2 * kvd, 2 * kvd, W_F32};
+    cudaError_t e = kv8_append_launch(n, st);
+    if (e != cudaSuccess) return e;
+    e = kv8_decode_takes(t) ? kv8_decode_launch(t, s->num_sms, st) : kv8_prompt_launch(t, s->num_sms, st);
+    if (e != cudaSuccess) return e;
+    k_pf_hilo<<<nt, PF_NT, 0, st>>>(s->o, a.Hq * a.hd, s->hb);
+    return cudaGetLastError();
 }
 
 cudaError_t prefill_create(const PrefillArgs& a, int num_sms, PrefillState** out) {
@@ -776,6 +834,23 @@ cudaError_t prefill_create(const PrefillArgs& a, int num_sms, PrefillState** out
         cudaGetLastError();
         prefill_free(s);
         return e;
+    }
+    if (a.kv8) {
+        size_t most = 1;
+        for (int nt = 1; nt <= PF_PASS; ++nt) {
+            const Kv8Attend t = pf_kv8(s, 0, 0, nt, a.cap);
+            const size_t n = kv8_decode_takes(t) ? kv8_decode_floats(t, num_sms) : kv8_prompt_floats(t, num_sms);
+            most = n > most ? n : most;
+        }
+        if ((e = cudaMalloc(&s->kv, sizeof(float) * PF_PASS * 2 * kvd)) != cudaSuccess ||
+            (e = cudaMalloc(&s->o, sizeof(float) * PF_PASS * qd)) != cudaSuccess ||
+            (e = cudaMalloc(&s->kv8_ws, sizeof(float) * most)) != cudaSuccess ||
+            (e = cudaMalloc(&s->kv8_counters, sizeof(int) * a.Hkv)) != cudaSuccess ||
+            (e = cudaMemset(s->kv8_counters, 0, sizeof(int) * a.Hkv)) != cudaSuccess) {
+            cudaGetLastError();
+            prefill_free(s);
+            return e;
+        }
     }
     // tensor maps: every layer's weights, and the hi/lo activation rows for K = d, qd, F
     CUtensorMap hd_map, hq_map, hf_map;
@@ -845,7 +920,7 @@ cudaError_t prefill_create(const PrefillArgs& a, int num_sms, PrefillState** out
         s->proj[4 * l + 3].add = true;
     }
     // the attention's K/V tensor maps, one pair per layer
-    {
+    if (!a.kv8) {
         std::vector<CUtensorMap> km((size_t)2 * a.L);
         const long long kvrows = a.paged ? (long long)a.num_pages * a.Hkv * a.page : (long long)a.rows * a.Hkv * a.cap;
         const int box = a.paged ? a.page : PA_KT;
@@ -861,8 +936,8 @@ cudaError_t prefill_create(const PrefillArgs& a, int num_sms, PrefillState** out
         }
     }
     if ((e = cudaFuncSetAttribute(k_pf_gemm, cudaFuncAttributeMaxDynamicSharedMemorySize, PF_SMEM)) != cudaSuccess ||
-        (e = cudaFuncSetAttribute(pf_attn_fn(a.hd, a.Hq / a.Hkv), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  pf_attn_tc_smem(a.hd))) != cudaSuccess) {
+        (!a.kv8 && (e = cudaFuncSetAttribute(pf_attn_fn(a.hd, a.Hq / a.Hkv), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  pf_attn_tc_smem(a.hd))) != cudaSuccess)) {
         prefill_free(s);
         return e;
     }
@@ -894,8 +969,8 @@ cudaError_t prefill_run(PrefillState* s, const int* tokens, int n, int pos0, int
     if (a.paged &&
         (e = cudaMemcpyAsync(s->pages, pages, sizeof(int) * a.ppr, cudaMemcpyHostToDevice, st)) != cudaSuccess)
         return e;
-    const void* attn = pf_attn_fn(a.hd, G);
-    if (!attn) return cudaErrorInvalidValue;
+    const void* attn = a.kv8 ? nullptr : pf_attn_fn(a.hd, G);
+    if (!attn && !a.kv8) return cudaErrorInvalidValue;
     const float scale = (float)(1.0 / sqrt((double)a.hd));
     for (int c0 = 0; c0 < n; c0 += PF_PASS) {
         int nt = n - c0 < PF_PASS ? n - c0 : PF_PASS;
@@ -907,12 +982,14 @@ cudaError_t prefill_run(PrefillState* s, const int* tokens, int n, int pos0, int
         for (int l = 0; l < a.L; ++l) {
             const void* const* w = a.lw + (size_t)l * 9;
             PfKv kv{static_cast<__nv_bfloat16*>(a.K[l]), static_cast<__nv_bfloat16*>(a.V[l]),
-                    a.paged ? s->pages : nullptr, row, a.Hkv, a.hd, a.cap, a.page};
+                    a.paged ? s->pages : nullptr, row, a.Hkv, a.hd, a.cap, a.page};   // e4m3: its heads and dims only
             int sp = 1;
             if ((e = pf_gemm_launch(s, s->proj[4 * l + 0], nb, &sp, st)) != cudaSuccess) return e;
-            k_pf_qkv<<<nt, PF_NT, 0, st>>>(s->part, sp, ntp, a.Hq, nt, p0, a.rope, s->q, kv);
+            k_pf_qkv<<<nt, PF_NT, 0, st>>>(s->part, sp, ntp, a.Hq, nt, p0, a.rope, s->q, kv, s->kv);
             if (nt < ntp) k_pf_zero_rows<<<ntp - nt, PF_NT, 0, st>>>(s->hb, qd, nt);
-            {
+            if (a.kv8) {
+                if ((e = pf_attend_kv8(s, l, row, nt, p0, st)) != cudaSuccess) return e;
+            } else {
                 unsigned* errp = a.err;
                 const CUtensorMap* kvm = s->kvmaps + 2 * l;
                 void* args[] = {&s->q,   const_cast<int*>(&a.Hq), &nt,   &p0, const_cast<float*>(&scale),

@@ -19,7 +19,7 @@ from . import _binding as B
 _ROLE = {"attn_norm": B.DEC_W_ATTN_NORM, "wq": B.DEC_W_Q, "wk": B.DEC_W_K, "wv": B.DEC_W_V, "wo": B.DEC_W_O,
          "ffn_norm": B.DEC_W_FFN_NORM, "wg": B.DEC_W_GATE, "wu": B.DEC_W_UP, "wd": B.DEC_W_DOWN}
 _DT = {torch.float32: B.DEC_DTYPE_F32, torch.bfloat16: B.DEC_DTYPE_BF16}
-_DTN = {"f32": B.DEC_DTYPE_F32, "bf16": B.DEC_DTYPE_BF16}
+_DTN = {"f32": B.DEC_DTYPE_F32, "bf16": B.DEC_DTYPE_BF16, "e4m3": B.DEC_DTYPE_E4M3}   # e4m3: K/V only
 
 
 @dataclass
@@ -62,7 +62,7 @@ class Decoder:
     def __init__(self, cfg: B.dec_config, weights: dict, cap: int, rows: int = 1, kv_layout: str = "contiguous",
                  page_size: int = 16, num_pages: int = 0, stream: Optional[torch.cuda.Stream] = None,
                  lib_workspace: bool = False, strategy: str = "graph", sampler: Optional[dict] = None,
-                 kv_sweep: str = "cap"):
+                 kv_sweep: str = "cap", window: int = 0, sinks: int = 0):
         self.cfg = cfg
         self.rows, self.cap = rows, cap
         self.layout = B.DEC_KV_PAGED if kv_layout == "paged" else B.DEC_KV_CONTIGUOUS
@@ -75,6 +75,8 @@ class Decoder:
             B.dec_set_strategy(self.h, B.DEC_STRATEGY_PERSISTENT if strategy == "persistent" else B.DEC_STRATEGY_GRAPH)
             # "cap": the constant-shape sweep of [0, cap); "pos": stop at the tile holding pos (same results)
             B.dec_set_kv_sweep(self.h, B.DEC_SWEEP_POS if kv_sweep == "pos" else B.DEC_SWEEP_CAP)
+            if window or sinks:   # e4m3 K/V: each token sees its last `window` positions and the first `sinks`
+                B.dec_set_window(self.h, window, sinks)
             if sampler is not None:   # records the sampling kernel after the head
                 B.check(self.h, B.dec_set_sampler(self.h, make_sampler(**sampler)))
             self.ws = None
@@ -219,10 +221,20 @@ class Decoder:
             shape = (self.num_pages, c.n_kv_heads, self.page_size, c.head_dim)
         else:
             shape = (self.rows, c.n_kv_heads, self.cap, c.head_dim)
+        if c.kv_dtype == B.DEC_DTYPE_E4M3:
+            return torch.as_tensor(_DevArray(ptr, shape, "|u1"), device=f"cuda:{c.device}").view(torch.float8_e4m3fn)
         if c.kv_dtype == B.DEC_DTYPE_BF16:
             t = torch.as_tensor(_DevArray(ptr, shape, "<i2"), device=f"cuda:{c.device}")
             return t.view(torch.bfloat16)
         return torch.as_tensor(_DevArray(ptr, shape, "<f4"), device=f"cuda:{c.device}")
+
+    def kv_scale(self, layer: int, which: int) -> torch.Tensor:
+        """Zero-copy view of the scales of an e4m3 K (0) or V (1) store: exponent + 127,
+        [rows or num_pages, n_kv_heads, blocks of positions]."""
+        ptr, nbytes, block = B.dec_kv_scale_ptr(self.h, layer, which)
+        n = self.page_size if self.layout == B.DEC_KV_PAGED else self.cap
+        rows = self.num_pages if self.layout == B.DEC_KV_PAGED else self.rows
+        return torch.as_tensor(_DevArray(ptr, (rows, self.cfg.n_kv_heads, n // block), "|u1"), device=f"cuda:{self.cfg.device}")
 
     def logits_device(self) -> torch.Tensor:
         ptr = B.dec_logits_ptr(self.h)

@@ -69,7 +69,9 @@ typedef enum dec_status {
 #define DEC_FAULT_SLOT_MAP  0x8u  /* a SlotMap entry outside [0, num_pages) */
 #define DEC_FAULT_WAIT      0x10u /* an in-kernel wait on another CTA or on a copy gave up (bounded poll) */
 
-typedef enum dec_dtype { DEC_DTYPE_F32 = 0, DEC_DTYPE_BF16 = 1 } dec_dtype;
+/* E4M3 is a K/V store's type only: one byte a value with a power-of-two scale for
+ * each block of positions and head, see "The 8-bit K/V cache" below. */
+typedef enum dec_dtype { DEC_DTYPE_F32 = 0, DEC_DTYPE_BF16 = 1, DEC_DTYPE_E4M3 = 2 } dec_dtype;
 
 /* KV layouts ("Execution", section "A constant-shape decode graph"):
  *   CONTIGUOUS: per layer K and V of shape [rows, n_kv_heads, cap, head_dim];
@@ -104,6 +106,7 @@ typedef enum dec_strategy { DEC_STRATEGY_GRAPH = 0, DEC_STRATEGY_PERSISTENT = 1 
  *        ("Execution", "A constant-shape decode graph": attention always
  *        sweeps [cap]; a mask computed from Slot::Pos against an iota hides
  *        the positions after pos) -- the default;
+ *        (an e4m3 store's attention reads what the token sees, under either)
  *   POS  the same captured graph and grid, but each split stops loading K/V
  *        tiles after the one holding pos (a split that starts after pos loads
  *        none).  The tiles it skips are fully masked, and the kernel already
@@ -124,7 +127,9 @@ typedef struct dec_config {
     int32_t ffn_hidden;     /* SwiGLU hidden width */
     int32_t vocab;
     int32_t weight_dtype;   /* dec_dtype of every weight (matrices, embeddings, norm gains) */
-    int32_t kv_dtype;       /* dec_dtype of the stored K/V */
+    int32_t kv_dtype;       /* dec_dtype of the stored K/V; E4M3: head_dim 64 or 128, DEC_STRATEGY_GRAPH,
+                             * a cap (contiguous) or pages that are multiples of 16, new K/V stored by
+                             * dec_kv8_append's rules; only positions that a token sees are read */
     int32_t device;         /* CUDA device ordinal */
     double rms_eps;
     double rope_theta;
@@ -293,9 +298,11 @@ int dec_chain(dec_handle *h, int32_t n_steps, const int32_t *tokens, const int32
  *   pos0        first position; pos0 + n <= cap (DEC_E_RANGE otherwise)
  *   logits_out  host [vocab] fp32 logits after the last token, or NULL
  *   id_out      host, the greedy id after the last token, or NULL
- * Needs a paged graph capture of 2..8 rows with bf16 K/V (DEC_E_UNSUPPORTED
- * otherwise).  Per token the arithmetic equals a decode step of that token, so
- * the chunking does not change any result. */
+ * Needs a paged graph capture of 2..8 rows with bf16 or e4m3 K/V
+ * (DEC_E_UNSUPPORTED otherwise).  Per token the arithmetic equals a decode step
+ * of that token, so the chunking does not change any result -- except that with
+ * e4m3 K/V a chunk's later tokens may have raised the scale of a block, and so
+ * rounded its earlier tokens again, before the earlier ones attend to them. */
 int dec_prefill(dec_handle *h, const int32_t *pages, const int32_t *tokens, int32_t n, int32_t pos0,
                 float *logits_out, int32_t *id_out);
 
@@ -308,7 +315,7 @@ int dec_prefill(dec_handle *h, const int32_t *pages, const int32_t *tokens, int3
  * (tcgen05.mma, bf16 weights, activations as bf16 hi + lo parts, fp32
  * accumulation), attention is causal over every position up to each token
  * (online softmax, fp32), and every layer's K/V of the n positions is written
- * into the sequence's store (rounded to bf16).  The last token's hidden state
+ * into the sequence's store (rounded to bf16, or by dec_kv8_append's rules).  The last token's hidden state
  * then goes through the captured step's final RMSNorm, LM head and argmax.
  *   row         contiguous K/V: the capture row whose store holds the
  *               sequence (0 .. rows-1); ignored for paged K/V
@@ -319,10 +326,10 @@ int dec_prefill(dec_handle *h, const int32_t *pages, const int32_t *tokens, int3
  *   logits_out  host [vocab] fp32 logits after the last token, or NULL
  *   id_out      host, the greedy id after the last token, or NULL
  * Positions before pos0 must already hold the sequence's K/V (from steps or an
- * earlier prefill).  Any capture with bf16 weights and K/V whose shape has
- * head_dim 64 or 128, n_heads / n_kv_heads of 2 or 4, d_model, n_heads *
- * head_dim and ffn_hidden multiples of 64, d_model <= 8192 and (paged
- * K/V) pages of at least 8 tokens (DEC_E_UNSUPPORTED otherwise).  The
+ * earlier prefill).  Any capture with bf16 weights and bf16 or e4m3 K/V whose
+ * shape has head_dim 64 or 128, d_model, n_heads * head_dim and ffn_hidden
+ * multiples of 64, d_model <= 8192 and with bf16 K/V n_heads / n_kv_heads of 2
+ * or 4 and (paged) pages of at least 8 tokens (DEC_E_UNSUPPORTED otherwise).  The
  * first call allocates the block's device buffers (cudaMalloc, kept until
  * dec_destroy); the call is synchronous (bounded wait) and must not be
  * captured.  Results agree with stepping the tokens one at a time within the
@@ -376,10 +383,17 @@ int dec_set_strategy(dec_handle *h, int32_t strategy);
 
 /* Choose the K/V sweep (dec_kv_sweep) of the coming dec_capture; DEC_E_STATE
  * after capture, DEC_E_INVALID for an unknown value.  Default DEC_SWEEP_CAP.
- * DEC_SWEEP_POS needs the GRAPH strategy and the tensor-core attention kernel
- * (bf16 K/V, head_dim 64 or 128): dec_capture returns DEC_E_UNSUPPORTED
+ * DEC_SWEEP_POS needs the GRAPH strategy and a tensor-core attention kernel
+ * (bf16 or e4m3 K/V, head_dim 64 or 128): dec_capture returns DEC_E_UNSUPPORTED
  * otherwise.  It also applies to dec_attention on the same handle. */
 int dec_set_kv_sweep(dec_handle *h, int32_t sweep);
+
+/* Attention within a window for the coming dec_capture (DEC_E_STATE after it):
+ * a token at position i sees j <= i with j > i - window or j < sinks; window 0
+ * (the default): every j <= i.  DEC_E_INVALID for negative values.  Needs an
+ * e4m3 K/V store (dec_capture returns DEC_E_UNSUPPORTED otherwise).  Also
+ * applies to dec_attention, dec_prefill and dec_prefill_block on the handle. */
+int dec_set_window(dec_handle *h, int32_t window, int32_t sinks);
 
 /* 1: later steps launch the recorded kernel sequence directly on the stream
  * instead of replaying the graph (same kernels, same arguments); 0: replay. */
@@ -399,6 +413,14 @@ int dec_reset_state(dec_handle *h);
  * dec_destroy); *bytes (host, optional) its size.  DEC_E_STATE before
  * dec_capture, DEC_E_INVALID for a bad layer or which. */
 int dec_kv_ptr(dec_handle *h, int32_t layer, int32_t which, void **ptr, size_t *bytes);
+
+/* E4M3 store: device address and byte size (optional) of the scales of one
+ * layer's K (which = 0) or V (which = 1), one byte for each block of *block
+ * positions (optional) and head: [rows or num_pages, n_kv_heads, positions /
+ * block], exponent + 127.  block is 64, 32 or 16, the largest that divides the
+ * cap (contiguous) or the page.  Like dec_kv_ptr otherwise; DEC_E_STATE for
+ * another K/V type. */
+int dec_kv_scale_ptr(dec_handle *h, int32_t layer, int32_t which, void **ptr, size_t *bytes, int32_t *block);
 
 /* One layer's decode attention as a standalone operation, on the caller's
  * buffers ("Execution", section "A constant-shape decode graph"): rotates q and
@@ -428,7 +450,8 @@ int dec_attention(dec_handle *h, int32_t layer, const float *qkv, const int32_t 
  * this entry point.
  * Limits: the array holds 2^19 fp32 partials and 1024 counters (about 2 MiB); a
  * shape that needs more (rows * n_heads * splits * (head_dim + 4) floats)
- * returns DEC_E_UNSUPPORTED and leaves the handle usable.  Every GPU that loads
+ * returns DEC_E_UNSUPPORTED and leaves the handle usable, as does an e4m3
+ * store (its attention has scratch in the capture's workspace).  Every GPU that loads
  * the library keeps the array until the process exits.  All calls on a device
  * share the array (it keeps the last call's contents; the counters are cleared
  * on entry), so calls that overlap on the GPU race: serialise them.  The first
@@ -573,7 +596,8 @@ int dec_launch_kernel(dec_handle *h, int32_t index, int32_t pdl, int64_t *bytes)
  * recorded kernel stamp the device's global nanosecond timer at: its earliest
  * CTA entry, the latest CTA to pass the wait on the previous kernel, its
  * earliest CTA exit and its latest CTA exit; enable = 0 stops recording.
- * Stamps accumulate (min / max) over the steps run while enabled. */
+ * Stamps accumulate (min / max) over the steps run while enabled.  The
+ * attention of an e4m3 K/V store does not stamp. */
 int dec_trace(dec_handle *h, int32_t enable);
 
 /* Copy 4 stamps per kernel for the first n_kernels kernels of the step

@@ -114,3 +114,30 @@ def test_attention_definition_small_cases():
     assert out[:, 0, 0].tolist() == [0.0, 0.5, 1.5]
     out, _, _ = R.attend(q, k, v, torch.tensor([0, 2, 3]), window=1, sinks=1)
     assert out[:, 0, 0].tolist() == [0.0, 1.0, 1.5]
+
+
+# ---- captures with an e4m3 store: what is refused without a device ----
+
+def config(**kw):
+    from graph_replay_gb300 import make_config
+    base = dict(n_layers=2, d_model=128, n_heads=4, n_kv_heads=2, head_dim=64, ffn_hidden=256, vocab=512, weight_dtype="bf16",
+                kv_dtype="e4m3")
+    base.update(kw)
+    return make_config(**base)
+
+
+@pytest.mark.parametrize("kw, code, word", [(dict(head_dim=32), 2, "e4m3"), (dict(weight_dtype="e4m3"), 1, "weight_dtype"), (dict(kv_dtype=3), 1, "kv_dtype")])
+def test_store_types(B, kw, code, word):
+    h = ctypes.c_void_p()
+    assert B.lib().dec_init(ctypes.byref(config(**kw)), ctypes.byref(h)) == code and word in B.last_error(None)
+
+
+def test_store_size(B):
+    cap, rows = 8192, 4
+    one, two = (B.dec_workspace_size(config(kv_dtype=t), cap, rows, B.DEC_KV_CONTIGUOUS) for t in ("e4m3", "bf16"))
+    values = 2 * 2 * rows * 2 * cap * 64          # K and V, layers, rows, heads, positions, dims
+    assert 0.85 * values <= two - one <= values   # a byte less a value; the scales and the attention's scratch come on top
+    with pytest.raises(B.DecError):
+        B.dec_workspace_size(config(), 8200, 1, B.DEC_KV_CONTIGUOUS)     # not a multiple of 16
+    with pytest.raises(B.DecError):
+        B.dec_workspace_size(config(), 64, 1, B.DEC_KV_PAGED, 8, 64)
