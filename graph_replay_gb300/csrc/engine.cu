@@ -73,7 +73,7 @@ Kv8Attend kv8_shape(const dec_config& c, int cap, int R) {
     t.c.page = cap;
     t.b.max_new = 1;
     t.b.total = R;
-    t.Hq = c.n_heads;
+    t.heads(c.n_heads);
     t.dtype = W_F32;
     return t;
 }

@@ -142,6 +142,13 @@ struct Kv8Attend {
     void* out;                 // [total, Hq, hd]
     long long q_stride, out_stride;
     int dtype, Hq;
+    int G;                     // query heads of a K/V head
+    FastDiv by_group;
+    void heads(int n) {
+        Hq = n;
+        G = n / c.Hkv;
+        by_group = FastDiv((unsigned)G);
+    }
     int window, sinks;         // window INT_MAX: every position up to the token's own
     float scale;
     int* counters;             // [rows, Hkv], zero between calls

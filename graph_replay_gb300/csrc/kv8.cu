@@ -112,7 +112,7 @@ int check_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const d
     p->out = a->out;
     p->q_stride = a->q_stride;
     p->out_stride = a->out_stride;
-    p->Hq = a->n_heads;
+    p->heads(a->n_heads);
     p->window = a->window ? a->window : INT_MAX;
     p->sinks = a->window ? a->sinks : 0;
     p->scale = a->scale > 0.0 ? (float)a->scale : (float)(1.0 / std::sqrt((double)p->c.hd));

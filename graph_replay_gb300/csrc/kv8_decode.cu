@@ -216,7 +216,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
     pdl_wait();
     const Kv8Cache& c = p.c;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-    const int G = p.Hq / c.Hkv, nb = c.page >> c.block_log2;
+    const int G = p.G, nb = c.page >> c.block_log2;
     KdRows rows(p);
     int least = 1;
     const KdCut cut = kd_plan<W>(rows, gridDim.x, &least);
@@ -302,8 +302,9 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
         constexpr int PAIRS = NK / 2, ITEMS = MT * PAIRS;
         auto load_q = [&](int a, uint4 (&qw)[QW]) {
             const int m = a * 8 + g;
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (row.t0 + m / G) * p.q_stride +
-                                                              (h * G + m % G) * HD + t * (HD / 4));
+            const int n = p.by_group.of(m);
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (row.t0 + n) * p.q_stride +
+                                                              (h * G + m - n * G) * HD + t * (HD / 4));
 #pragma unroll
             for (int v = 0; v < QW; ++v) qw[v] = m < nq ? __ldg(src + v) : make_uint4(0u, 0u, 0u, 0u);
         };
@@ -353,7 +354,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             for (int b = 0; b < 2; ++b) {
                 const int mq = a * 8 + 2 * t + b;
                 fac[a][b] = fac_s[mq];
-                pos[a][b] = mq < nq ? p0 + mq / G : -1;
+                pos[a][b] = mq < nq ? p0 + p.by_group.of(mq) : -1;
             }
 
         float o[MT][NK][4], M[MT][2], l[MT][2];
@@ -582,7 +583,8 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
         float* slot = slots + ((size_t)blockIdx.x * 2 + (u == u_begin ? 0 : 1)) * kd_slot_floats<HD, MT>();
         auto put = [&](int m, int d, float sum, const float (&y)[4]) {
             const float inv = sum == 0.f ? 0.f : 1.f / sum;   // nothing seen: zeros
-            T* dst = static_cast<T*>(p.out) + (row.t0 + m / G) * p.out_stride + (h * G + m % G) * HD + d;
+            const int n = p.by_group.of(m);
+            T* dst = static_cast<T*>(p.out) + (row.t0 + n) * p.out_stride + (h * G + m - n * G) * HD + d;
             if constexpr (FINE) *reinterpret_cast<float4*>(dst) = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
             else *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(y[0] * inv, y[1] * inv), pack_bf16x2(y[2] * inv, y[3] * inv));
         };
@@ -668,7 +670,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
     pdl_trigger();
 }
 
-int decode_sets(const Kv8Attend& p) { return (p.b.max_new * (p.Hq / p.c.Hkv) + 7) / 8; }
+int decode_sets(const Kv8Attend& p) { return (p.b.max_new * p.G + 7) / 8; }
 
 // one CTA for each place on the GPU, but no more than there can be steps
 int decode_grid(const Kv8Attend& p, int num_sms) {

@@ -242,16 +242,16 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     pdl_wait();
     const Kv8Cache& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = p.Hq / c.Hkv, h = (gridDim.x - 1 - blockIdx.x) % c.Hkv, r = blockIdx.y / splits, sp = blockIdx.y % splits;
+    const int G = p.G, h = (gridDim.x - 1 - blockIdx.x) % c.Hkv, r = blockIdx.y / splits, sp = blockIdx.y % splits;
     Kv8Row row;
     if (!kv8_row(p.b, c.ppr * c.page, r, &row)) return;
-    const long long rows_q = (long long)row.n * G;
+    const int rows_q = row.n * G;   // max_new * n_heads <= 2^30
     // tiles with the most positions first
-    const long long base = (long long)((gridDim.x - 1 - blockIdx.x) / c.Hkv) * (NQ * KP_ROWS);
+    const int base = (int)((gridDim.x - 1 - blockIdx.x) / c.Hkv) * (NQ * KP_ROWS);
     if (base >= rows_q) return;
     const int nact = base + KP_ROWS < rows_q ? 2 : 1;   // query tiles in use
     const int p0 = row.len - row.n;
-    const int tok0 = (int)(base / G), tok1 = (int)((min(base + NQ * KP_ROWS, rows_q) - 1) / G);
+    const int tok0 = p.by_group.of(base), tok1 = p.by_group.of(min(base + NQ * KP_ROWS, rows_q) - 1);
     const KpTiles tl = kp_tiles(p0 + tok0, p0 + tok1, p.window, p.sinks);
     const int i0 = (int)((long long)tl.n * sp / splits), i1 = (int)((long long)tl.n * (sp + 1) / splits);
     const int ntiles = i1 - i0;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             const int m = x / LPR, ch = x % LPR;
             float v[8];
             if (base + m < rows_q) {
-                const int tk = (int)((base + m) / G), hq = h * G + (int)((base + m) % G);
+                const int tk = p.by_group.of(base + m), hq = h * G + base + m - tk * G;
                 const T* src = static_cast<const T*>(p.q) + (row.t0 + tk) * p.q_stride + hq * HD + ch * 8;
                 if constexpr (FINE) {
                     const float4 a = __ldg(reinterpret_cast<const float4*>(src)), b = __ldg(reinterpret_cast<const float4*>(src) + 1);
@@ -512,17 +512,17 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         // ---- softmax: warp w reads TMEM lanes 32 (w % 4) + lane, the rows of query tile w / 4 ----
         regs_up<KP_REGS_SOFTMAX>();
         const int x = warp / 4, m = (warp & 3) * 32 + lane;
-        const long long mq = base + x * KP_ROWS + m;
+        const int mq = base + x * KP_ROWS + m;
         const bool live = x < nact && mq < rows_q;
-        const int tk = (int)((live ? mq : base) / G), hq = h * G + (int)((live ? mq : base) % G), pos = live ? p0 + tk : -1;
+        const int any = live ? mq : base, tk = p.by_group.of(any), hq = h * G + any - tk * G, pos = live ? p0 + tk : -1;
         const uint32_t lrow = dt + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t ocol = lrow + LY::O + (uint32_t)(HD * x);
         float M = -INFINITY, l = 0.f;
         bool ok = true;
         const float fac = ntiles > 0 ? fac_s[x * KP_ROWS + m] : 0.f;
         // the positions of this query tile's rows
-        const int xmin = p0 + (int)((base + x * KP_ROWS) / G);
-        const int xmax = p0 + (int)((min(base + (x + 1) * KP_ROWS, rows_q) - 1) / G);
+        const int xmin = p0 + p.by_group.of(base + x * KP_ROWS);
+        const int xmax = p0 + p.by_group.of(min(base + (x + 1) * KP_ROWS, rows_q) - 1);
         const int lo = (int)max((long long)pos - p.window + 1, 0ll);   // this row sees [lo, pos] and [0, sinks)
         const size_t qrow = (size_t)(row.t0 + tk) * p.Hq + hq, all_rows = (size_t)p.b.total * p.Hq;
         T* dst = static_cast<T*>(p.out) + (row.t0 + tk) * p.out_stride + hq * HD;   // the result, or this split's part of it
@@ -777,7 +777,7 @@ __global__ void __launch_bounds__(256) k_kv8_prompt_join(const Kv8Attend p, int 
 
 long long prompt_tiles(const Kv8Attend& p) {   // query tiles (of one CTA) of the longest row
     const int per = 2 * KP_ROWS;
-    return ((long long)p.b.max_new * (p.Hq / p.c.Hkv) + per - 1) / per;
+    return ((long long)p.b.max_new * p.G + per - 1) / per;
 }
 
 // Splits of a query tile's positions: as many as bring the CTAs to the SMs'
@@ -827,7 +827,7 @@ size_t kv8_prompt_floats(const Kv8Attend& p, int num_sms) {
     size_t n = kp_part_floats(splits, (size_t)p.b.total * p.Hq, p.c.hd);
     // fp32 q and more tiles than O takes unfolded: a fold for each query tile of each row
     if (p.dtype == W_F32 && (prompt_keys(p) / KP_KEYS + 2 + splits - 1) / splits > KP_FOLD) {
-        const size_t tiles = (size_t)p.b.total * (p.Hq / p.c.Hkv) / (2 * KP_ROWS) + p.c.rows + 1;
+        const size_t tiles = (size_t)p.b.total * p.G / (2 * KP_ROWS) + p.c.rows + 1;
         n += tiles * p.c.Hkv * splits * (2 * KP_ROWS) * p.c.hd;
     }
     return n;

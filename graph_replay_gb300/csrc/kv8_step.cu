@@ -125,7 +125,7 @@ cudaError_t attn_kv8_launch(const AttnPlan& a, cudaStream_t s, bool pdl) {
     t.out = p.out;
     t.q_stride = t.out_stride = (long long)p.Hq * p.hd;
     t.dtype = W_F32;
-    t.Hq = p.Hq;
+    t.heads(p.Hq);
     t.window = a.window ? a.window : INT_MAX;
     t.sinks = a.window ? a.sinks : 0;
     t.scale = p.scale;

@@ -792,7 +792,7 @@ static Kv8Attend pf_kv8(const PrefillState* s, int l, int row, int nt, int len) 
     t.out = s->o;
     t.q_stride = t.out_stride = (long long)a.Hq * a.hd;
     t.dtype = W_F32;
-    t.Hq = a.Hq;
+    t.heads(a.Hq);
     t.window = a.window ? a.window : INT_MAX;
     t.sinks = a.window ? a.sinks : 0;
     t.scale = (float)(1.0 / sqrt((double)a.hd));
