@@ -623,18 +623,23 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             __syncthreads();
             if (last_s) {
                 const bool second = !cut.own && cut.begin(c0) != u - i0;   // piece c0 had other work before
-                for (int x = tid; x < nq * (HD / 8); x += 32 * W) {
-                    const int m = x / (HD / 8), d = (x % (HD / 8)) * 8;
+                // 8 columns of a query row are an item; where there are fewer items than threads, several threads share
+                // an item's parts, a run of them each
+                const int items = nq * (HD / 8), teams = max(32 * W / items, 1), run = (c1 - c0 + teams) / teams;
+                float* shared = reinterpret_cast<float*>(kd_raw);   // [teams][items][12]: the warps' results are not needed any more
+                for (int x = tid; x < items * teams; x += 32 * W) {
+                    const int team = x / items, item = x - team * items, m = item / (HD / 8), d = (item % (HD / 8)) * 8;
+                    const int from = c0 + team * run, to = min(from + run - 1, c1);
                     float top = -INFINITY, sum = 0.f, y[8];
 #pragma unroll
                     for (int k = 0; k < 8; ++k) y[k] = 0.f;
                     constexpr int B = 6;   // parts read at once
-                    for (int q0 = c0; q0 <= c1; q0 += B) {
+                    for (int q0 = from; q0 <= to; q0 += B) {
                         float mm[B], ll[B], big = top;
                         float4 v[B][2];
 #pragma unroll
                         for (int k = 0; k < B; ++k) {
-                            const int q = min(q0 + k, c1);
+                            const int q = min(q0 + k, to);
                             const float* part = slots + ((size_t)q * 2 + (q == c0 && second ? 1 : 0)) * kd_slot_floats<HD, MT>();
                             mm[k] = __ldcg(part + MT * 8 * HD + m);
                             ll[k] = __ldcg(part + MT * 8 * (HD + 1) + m);
@@ -650,12 +655,32 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
                         top = big;
 #pragma unroll
                         for (int k = 0; k < B; ++k) {
-                            if (q0 + k > c1 || (mm[k] == -INFINITY && ll[k] == 0.f)) continue;   // nothing seen there
+                            if (q0 + k > to || (mm[k] == -INFINITY && ll[k] == 0.f)) continue;   // nothing seen there
                             const float e = mm[k] == -INFINITY ? 0.f : kv8_exp2(mm[k] - big);
                             sum += ll[k] * e;
                             y[0] += v[k][0].x * e; y[1] += v[k][0].y * e; y[2] += v[k][0].z * e; y[3] += v[k][0].w * e;
                             y[4] += v[k][1].x * e; y[5] += v[k][1].y * e; y[6] += v[k][1].z * e; y[7] += v[k][1].w * e;
                         }
+                    }
+                    float4* mine_s = reinterpret_cast<float4*>(shared + (team * items + item) * 12);
+                    mine_s[0] = make_float4(y[0], y[1], y[2], y[3]);
+                    mine_s[1] = make_float4(y[4], y[5], y[6], y[7]);
+                    mine_s[2] = make_float4(top, sum, 0.f, 0.f);
+                }
+                __syncthreads();
+                for (int x = tid; x < items; x += 32 * W) {
+                    const int m = x / (HD / 8), d = (x % (HD / 8)) * 8;
+                    float top = -INFINITY, sum = 0.f, y[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = 0.f;
+                    for (int w = 0; w < teams; ++w) top = fmaxf(top, shared[(w * items + x) * 12 + 8]);
+                    for (int w = 0; w < teams; ++w) {
+                        const float* o = shared + (w * items + x) * 12;
+                        if (o[8] == -INFINITY && o[9] == 0.f) continue;   // nothing seen there
+                        const float e = o[8] == -INFINITY ? 0.f : kv8_exp2(o[8] - top);
+                        sum += o[9] * e;
+#pragma unroll
+                        for (int k = 0; k < 8; ++k) y[k] += o[k] * e;
                     }
                     put(m, d, sum, reinterpret_cast<const float(&)[4]>(y[0]));
                     put(m, d + 4, sum, reinterpret_cast<const float(&)[4]>(y[4]));
