@@ -44,8 +44,8 @@ constexpr int KP_ROWS = 128;              // query rows of a tile: TMEM lanes
 constexpr int KP_KEYS = 64;               // positions of a tile
 // 8 softmax warps, 4 that convert K, 4 that convert V, 1 MMA warp and 3 that only pad its warpgroup
 constexpr int KP_K_WARP = 8, KP_V_WARP = 12, KP_MMA_WARP = 16, KP_THREADS = 20 * 32;
-// registers a thread by role (setmaxnreg): 640 threads x 96 at launch = 256 x 128 + 256 x 80 + 128 x 64
-constexpr int KP_REGS_SOFTMAX = 128, KP_REGS_CONV = 80, KP_REGS_MMA = 64;
+// registers a thread by role (setmaxnreg): 640 threads x 96 at launch = 256 x 120 + 256 x 88 + 128 x 64
+constexpr int KP_REGS_SOFTMAX = 120, KP_REGS_CONV = 88, KP_REGS_MMA = 64;
 constexpr int KP_QPANEL = KP_ROWS * 128, KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a query tile, of a K or V tile
 constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
 constexpr int KP_FOLD = 16;               // fp32 q: tiles between two folds of O into memory
@@ -224,9 +224,16 @@ __device__ __forceinline__ KpTiles kp_tiles(int pmin, int pmax, int window, int 
     return t;
 }
 
+// The parts that the tiles of a CTA's rows are split into, of at most `splits` CTAs: at least 8 tiles each, since a
+// CTA's beginning and end cost as much as two and the parts have to be joined
+__host__ __device__ __forceinline__ int kp_parts(int tiles, int splits) {
+    const int n = (tiles + 7) / 8;
+    return n < 1 ? 1 : n < splits ? n : splits;
+}
+
 // grid (Hkv * query tiles, rows * splits)
 template <int HD, bool FINE>
-__global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p, int splits) {
+__global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p, int most) {
     using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
     using LY = KpLayout<HD, FINE>;
     constexpr int NQ = 2, SLOTS = LY::SLOTS;
@@ -242,7 +249,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     pdl_wait();
     const Kv8Cache& c = p.c;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int G = p.G, h = (gridDim.x - 1 - blockIdx.x) % c.Hkv, r = blockIdx.y / splits, sp = blockIdx.y % splits;
+    const int G = p.G, h = (gridDim.x - 1 - blockIdx.x) % c.Hkv, r = blockIdx.y / most, sp = blockIdx.y % most;
     Kv8Row row;
     if (!kv8_row(p.b, c.ppr * c.page, r, &row)) return;
     const int rows_q = row.n * G;   // max_new * n_heads <= 2^30
@@ -253,6 +260,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     const int p0 = row.len - row.n;
     const int tok0 = p.by_group.of(base), tok1 = p.by_group.of(min(base + NQ * KP_ROWS, rows_q) - 1);
     const KpTiles tl = kp_tiles(p0 + tok0, p0 + tok1, p.window, p.sinks);
+    const int splits = kp_parts(tl.n, most);   // of this CTA's rows
+    if (sp >= splits) return;
     const int i0 = (int)((long long)tl.n * sp / splits), i1 = (int)((long long)tl.n * (sp + 1) / splits);
     const int ntiles = i1 - i0;
     auto key0 = [&](int i) { return (i < tl.sink ? i : i + tl.gap) * KP_KEYS; };
@@ -531,8 +540,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         // additions (7e-6 after 450).  So O is folded into memory every KP_FOLD tiles, in rounded sums: 16 bytes of
         // each row side by side, the rows of a CTA together (in the result's own rows a fold took 8 us)
         const size_t fold_tile = ((size_t)((long long)row.t0 * G / (NQ * KP_ROWS)) + r + (size_t)(base / (NQ * KP_ROWS))) * c.Hkv + h;
-        float4* fold = reinterpret_cast<float4*>(p.ws + kp_part_floats(splits, all_rows, HD)) +
-                       (fold_tile * splits + sp) * (NQ * KP_ROWS * HD / 4) + x * (KP_ROWS * HD / 4) + m;   // + KP_ROWS * (column / 4)
+        float4* fold = reinterpret_cast<float4*>(p.ws + kp_part_floats(most, all_rows, HD)) +
+                       (fold_tile * most + sp) * (NQ * KP_ROWS * HD / 4) + x * (KP_ROWS * HD / 4) + m;   // + KP_ROWS * (column / 4)
         float M_fold = -INFINITY;   // the maximum that the folded sums refer to
         auto fold_o = [&](int cc) {   // columns cc .. cc + 63
             float4 was[16];
@@ -589,14 +598,16 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     for (int e = 0; e < 32; ++e) v[q][e] = see >> e & 1u ? v[q][e] : 0xFF800000u;
                 }
             }
-            float top = -INFINITY;
+            float mul[KP_GROUPS], ve[KP_GROUPS], top = -INFINITY;
 #pragma unroll
             for (int b = 0; b < KP_GROUPS; ++b) {
                 auto f = [&](int e) { return __uint_as_float(v[b / 2][b % 2 * 16 + e]); };
                 const float t0 = max3(f(0), f(1), f(2)), t1 = max3(f(3), f(4), f(5)), t2 = max3(f(6), f(7), f(8));
                 const float t3 = max3(f(9), f(10), f(11)), t4 = max3(f(12), f(13), f(14));
-                const KpMeta k = mt[b];
-                top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), kp_mul(fac, k.kf), k.ve));
+                const float2 k = *reinterpret_cast<const float2*>(&mt[b]);
+                mul[b] = kp_mul(fac, k.x);
+                ve[b] = k.y;
+                top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), mul[b], ve[b]));
             }
             float alpha = 1.f;
             if (top > M + KP_SLACK) {
@@ -624,9 +635,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 uint32_t hi[16], low[FINE ? 16 : 1];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const KpMeta k = mt[2 * q + b];
-                    const float mul = kp_mul(fac, k.kf), add = k.ve - sub;
-                    const uint64_t mul2 = pair(mul, mul), plus2 = pair(add, add);
+                    const float mu = mul[2 * q + b], add = ve[2 * q + b] - sub;
+                    const uint64_t mul2 = pair(mu, mu), plus2 = pair(add, add);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
@@ -634,7 +644,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                         unpair(fma2(pair(__uint_as_float(v[q][16 * b + e]), __uint_as_float(v[q][16 * b + e + 1])), mul2, plus2), w0, w1);
                         w0 = kv8_exp2(w0);
                         w1 = kv8_exp2(w1);
-                        if (e & 2) sum1 = add2(sum1, pair(w0, w1));
+                        if (e == 0) sum0 = pair(w0, w1);
+                        else if (e == 2) sum1 = pair(w0, w1);
+                        else if (e & 2) sum1 = add2(sum1, pair(w0, w1));
                         else sum0 = add2(sum0, pair(w0, w1));
                         const int d = 8 * b + e / 2;
                         hi[d] = pack_h2(w0, w1);
@@ -645,7 +657,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     }
                     float a0, a1;
                     unpair(add2(sum0, sum1), a0, a1);
-                    l = fmaf(a0 + a1, k.vinv, l);
+                    l = fmaf(a0 + a1, mt[2 * q + b].vinv, l);
                 }
                 tm_st16(scol + 16 * q, hi);   // over the scores, which this thread holds
                 if constexpr (FINE) tm_st16(scol + 32 + 16 * q, low);
@@ -685,7 +697,13 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     }
                 }
             }
-            const float inv = l == 0.f ? 0.f : 1.f / l;
+            // Each thread has a row; memory wants rows side by side.  So a warp lays its 32 rows down in shared memory,
+            // which nobody needs any more (16-byte chunks permuted against bank conflicts), and writes them row by row:
+            // 16 bytes of 32 rows at a time cost some 2 us a CTA
+            const bool whole = splits == 1;
+            const float inv = !whole ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            const int bytes = whole ? HD * (int)sizeof(T) : HD * 4, log2_chunks = 31 - __clz(bytes / 16);   // 8, 16 or 32 a row
+            unsigned char* stage = sm + warp * (32 * HD * 4);
 #pragma unroll
             for (int cc = 0; cc < HD; cc += 16) {
                 uint32_t o[16];
@@ -708,30 +726,32 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     for (int e = 0; e < 16; ++e) o[e] = 0u;
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 16; ++e) {
                     if (nan[cc / 32] >> (cc % 32 + e) & 1u) o[e] = 0x7FFFFFFFu;
-                if (!live) continue;
-                if (splits > 1) {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4)
-                        *reinterpret_cast<uint4*>(piece + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-                    continue;
+                    o[e] = l == 0.f ? 0u : __float_as_uint(__uint_as_float(o[e]) * inv);   // nothing seen: O is undefined
                 }
-                float y[16];
+                auto lay = [&](int chunk, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+                    *reinterpret_cast<uint4*>(stage + lane * bytes + ((chunk ^ (lane & 7)) << 4)) = make_uint4(x, y, z, w);
+                };
+                if (FINE || !whole) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e) y[e] = l == 0.f ? 0.f : __uint_as_float(o[e]) * inv;   // nothing seen: O is undefined
-                if constexpr (FINE) {
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) *reinterpret_cast<float4*>(dst + cc + e) = make_float4(y[e], y[e + 1], y[e + 2], y[e + 3]);
+                    for (int e = 0; e < 16; e += 4) lay((cc + e) / 4, o[e], o[e + 1], o[e + 2], o[e + 3]);
                 } else {
+                    auto two = [&](int e) { return pack_bf16x2(__uint_as_float(o[e]), __uint_as_float(o[e + 1])); };
 #pragma unroll
-                    for (int e = 0; e < 16; e += 8)
-                        *reinterpret_cast<uint4*>(dst + cc + e) = make_uint4(pack_bf16x2(y[e], y[e + 1]), pack_bf16x2(y[e + 2], y[e + 3]),
-                                                                             pack_bf16x2(y[e + 4], y[e + 5]), pack_bf16x2(y[e + 6], y[e + 7]));
+                    for (int e = 0; e < 16; e += 8) lay((cc + e) / 8, two(e), two(e + 2), two(e + 4), two(e + 6));
                 }
             }
+            __syncwarp();
+            const unsigned long long to = live ? (unsigned long long)(whole ? (void*)dst : (void*)piece) : 0ull;
+            for (int k = 0; k < 1 << log2_chunks; ++k) {
+                const int i = k * 32 + lane, rr = i >> log2_chunks, chunk = i & ((1 << log2_chunks) - 1);
+                const uint4 v = *reinterpret_cast<const uint4*>(stage + rr * bytes + ((chunk ^ (rr & 7)) << 4));
+                const unsigned long long at = __shfl_sync(0xffffffffu, to, rr);
+                if (at) reinterpret_cast<uint4*>(at)[chunk] = v;
+            }
             if (splits > 1 && live) {
-                float* ml = p.ws + (size_t)splits * all_rows * HD + (sp * all_rows + qrow) * 2;
+                float* ml = p.ws + (size_t)most * all_rows * HD + (sp * all_rows + qrow) * 2;
                 ml[0] = M;
                 ml[1] = l;
             }
@@ -747,15 +767,20 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
 
 // one warp for each token and query head: the splits' parts in split order.  grid (query rows / 8, rows)
 template <int HD, bool FINE>
-__global__ void __launch_bounds__(256) k_kv8_prompt_join(const Kv8Attend p, int splits) {
+__global__ void __launch_bounds__(256) k_kv8_prompt_join(const Kv8Attend p, int most) {
     using T = typename std::conditional<FINE, float, __nv_bfloat16>::type;
     pdl_wait();
     const int r = blockIdx.y, lane = threadIdx.x & 31;
     const long long m = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
     Kv8Row row;
     if (!kv8_row(p.b, p.c.ppr * p.c.page, r, &row) || m >= (long long)row.n * p.Hq) return;
+    // the parts of the CTA that had this query row
+    const int tk = (int)(m / p.Hq), g = (int)(m % p.Hq) % p.G, base = (tk * p.G + g) / (2 * KP_ROWS) * (2 * KP_ROWS), p0 = row.len - row.n;
+    const KpTiles tl = kp_tiles(p0 + p.by_group.of(base), p0 + p.by_group.of(min(base + 2 * KP_ROWS, row.n * p.G) - 1), p.window, p.sinks);
+    const int splits = kp_parts(tl.n, most);
+    if (splits == 1) return;   // it wrote the result itself
     const size_t all_rows = (size_t)p.b.total * p.Hq, qrow = (size_t)row.t0 * p.Hq + m;
-    const float* ml = p.ws + (size_t)splits * all_rows * HD;
+    const float* ml = p.ws + (size_t)most * all_rows * HD;
     constexpr int D = HD / 32;
     float M = -INFINITY, l = 0.f, o[D];
 #pragma unroll
@@ -780,18 +805,17 @@ long long prompt_tiles(const Kv8Attend& p) {   // query tiles (of one CTA) of th
     return ((long long)p.b.max_new * p.G + per - 1) / per;
 }
 
-// Splits of a query tile's positions: as many as bring the CTAs to the SMs'
-// count, each with at least 8 tiles of the most positions that a tile may see
 long long prompt_keys(const Kv8Attend& p) {   // the most positions that the rows of a CTA may see, and two tiles
     const long long keys = (long long)p.c.ppr * p.c.page, win = (long long)p.window + p.sinks + p.b.max_new;
     return (win < keys ? win : keys) + 2 * KP_KEYS;
 }
+// The most parts: as many as bring the CTAs to one round of the SMs (a second round costs more than it saves: a prompt
+// of 1024 tokens, 128 CTAs of up to 16 tiles, takes 31 us whole and 50 us in parts of 8)
 int prompt_splits(const Kv8Attend& p, int num_sms) {
-    const long long ctas = prompt_tiles(p) * p.c.Hkv * p.c.rows, keys = prompt_keys(p);
-    long long s = num_sms / ctas;
-    if (s > keys / (8 * KP_KEYS)) s = keys / (8 * KP_KEYS);
-    if (s > 32) s = 32;
-    return s < 1 ? 1 : (int)s;
+    const long long ctas = prompt_tiles(p) * p.c.Hkv * p.c.rows, tiles = prompt_keys(p) / KP_KEYS;
+    long long n = num_sms / ctas;
+    if (n > 32) n = 32;
+    return n < 1 ? 1 : kp_parts((int)(tiles < (1 << 20) ? tiles : 1 << 20), (int)n);
 }
 
 template <int HD, bool FINE>
@@ -826,7 +850,9 @@ size_t kv8_prompt_floats(const Kv8Attend& p, int num_sms) {
     const int splits = prompt_splits(p, num_sms);
     size_t n = kp_part_floats(splits, (size_t)p.b.total * p.Hq, p.c.hd);
     // fp32 q and more tiles than O takes unfolded: a fold for each query tile of each row
-    if (p.dtype == W_F32 && (prompt_keys(p) / KP_KEYS + 2 + splits - 1) / splits > KP_FOLD) {
+    // (a part holds at most 8 tiles, or its share of all of them)
+    const long long tiles_most = prompt_keys(p) / KP_KEYS + 2;
+    if (p.dtype == W_F32 && (tiles_most + splits - 1) / splits + 1 > KP_FOLD) {
         const size_t tiles = (size_t)p.b.total * p.G / (2 * KP_ROWS) + p.c.rows + 1;
         n += tiles * p.c.Hkv * splits * (2 * KP_ROWS) * p.c.hd;
     }
