@@ -251,6 +251,11 @@ def test_faults_and_refusals():
         dec.reset_state()
         assert np.array_equal(dec.step([1, 2], [0, 0]).logits, good)
         dec.reset_state()
+    # the fixed array of dec_attention_static is not for this store; the handle stays usable
+    buf = torch.zeros(2, (HEADS + 2 * KV) * HD, device="cuda")
+    pos = torch.zeros(2, dtype=torch.int32, device="cuda")
+    assert B.dec_attention_static(dec.h, 0, buf.data_ptr(), pos.data_ptr(), buf.data_ptr()) == B.DEC_E_UNSUPPORTED
+    assert np.array_equal(dec.step([1, 2], [0, 0]).logits, good)
     with pytest.raises(B.DecError, match="before dec_capture"):
         B.dec_set_window(dec.h, 4, 0)
     dec.close()

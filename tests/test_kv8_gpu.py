@@ -352,6 +352,76 @@ def test_graphs_and_streams():
     cache.check()
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_recorded_prompts(dtype):
+    """A recorded append and prompt attention (split over positions and not) replayed at other lengths and contents."""
+    rows = [(1500, 40), (300, 33)]
+    K, V, table, q, kv_len, starts = build(rows, 8, 2, 64, 64, 64, 31, dtype, poison=False)
+    cache = gpu_cache(K, V, table)
+    g = torch.Generator().manual_seed(6)
+    k, v = (torch.randn(q.shape[0], 2, 64, generator=g).to(dtype) for _ in range(2))
+    lens, st, qs, ks, vs = kv_len.cuda(), starts.cuda(), q.cuda(), k.cuda(), v.cuda()
+    ws = torch.zeros(cache.workspace_bytes(q.shape[0], 8, 40, dtype=dtype), dtype=torch.uint8, device="cuda")
+    out = torch.zeros_like(qs)
+    gr, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(gr, stream=stream):
+        cache.append(ks, vs, lens, q_start=st, max_new=40)
+        cache.attend(qs, lens, q_start=st, max_new=40, out=out, workspace=ws)
+    for now in ([(1500, 40), (300, 33)], [(800, 17), (70, 20)], [(40, 40), (0, 0)], [(1500, 1), (33, 33)]):
+        starts = starts_of([n for _, n in now])
+        lens.copy_(torch.tensor([l for l, _ in now], dtype=torch.int32))
+        st.copy_(starts)
+        out.fill_(5.0)
+        gr.replay()
+        torch.cuda.synchronize()
+        for s, x in ((K, k), (V, v)):
+            for r, (l, n) in enumerate(now):
+                s.append(table[r], l - n, x[starts[r]:starts[r + 1]].double())
+        compare(out, now, K, V, table, q, 0, 0, dtype)
+        assert bool((out[int(starts[-1]):] == 5).all())
+    cache.check()
+
+
+@pytest.mark.parametrize("new", [1, 3, 40])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_bad_queries_keep_to_themselves(new, dtype):
+    """NaN and infinities in one token's q: its heads' results are NaN, the others' as without them."""
+    rows = [(100, new), (90, new)]
+    K, V, table, q, kv_len, starts = build(rows, 8, 2, 64, 16, 16, 13, dtype)
+    cache = gpu_cache(K, V, table)
+    good = cache.attend(q.cuda(), kv_len.cuda(), q_start=starts.cuda(), max_new=new)
+    for value in (math.nan, math.inf):
+        bad = q.clone()
+        bad[new - 1, 3, 7] = value
+        bad[new, 5] = 0.0            # a row of zeros: the mean of what it sees
+        out = cache.attend(bad.cuda(), kv_len.cuda(), q_start=starts.cuda(), max_new=new)
+        assert bool(torch.isnan(out[new - 1, 3]).all())
+        ok = torch.ones(out.shape[:2], dtype=torch.bool)
+        ok[new - 1, 3] = ok[new, 5] = False
+        assert torch.equal(out[ok.cuda()], good[ok.cuda()])
+        o, mass, score = R.attend(bad[new:new + 1].double(), K.values(table[1].long()), V.values(table[1].long()), torch.tensor([90 - new]))
+        lim = R.bound(mass, score, o, dtype, 64, 90)
+        assert bool(((out[new].double().cpu() - o[0]).abs() <= lim[0])[5].all())
+    cache.check()
+
+
+def test_many_rows_and_the_smallest():
+    """More rows than a warp has lanes, most of them idle; then one row of one position."""
+    g = torch.Generator().manual_seed(2)
+    n = 1024
+    lens = torch.where(torch.rand(n, generator=g) < 0.1, torch.randint(1, 200, (n,), generator=g), torch.zeros(n, dtype=torch.long))
+    lens[700], lens[1023] = 900, 1
+    rows = [(int(l), 1) for l in lens]
+    K, V, table, q, kv_len, _ = build(rows, 4, 2, 64, 64, 64, 3, F32, poison=False)
+    cache = gpu_cache(K, V, table)
+    out = cache.attend(q.cuda(), kv_len.cuda())
+    cache.check()
+    for r in [0, 31, 32, 700, 1022, 1023] + [r for r in range(n) if lens[r]][:40]:
+        compare(out[r:r + 1], [rows[r]], K, V, table[r:r + 1], q[r:r + 1], 0, 0, F32)
+    assert bool((out[(lens == 0).cuda()] == 0).all())
+
+
 @pytest.mark.parametrize("new", [1, 64])
 def test_repeats_bit_for_bit(new):
     rows = [(3000, new), (10 + new, new), (777, new)]
