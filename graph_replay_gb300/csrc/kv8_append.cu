@@ -11,8 +11,9 @@
 // One CTA takes one block of one head of K or of V, so a block's maximum needs
 // no memory between CTAs and every byte is written once.  A thread keeps its
 // values in registers between the maximum and the rounding: the input is read
-// once.  Bound: those reads and writes (141 MB in 27 us, 5.2 TB/s); for a single
-// token three dependent trips to memory (1.9 us).
+// once.  Bound: those reads and writes, and close behind them the issue of
+// instructions (141 MB in 26.9 us, 5.25 TB/s); for a single token three
+// dependent trips to memory (1.9 us).
 #include "kv8.cuh"
 
 namespace gd {
@@ -41,10 +42,45 @@ struct Raw8 {
     }
 };
 
+// largest magnitude, infinities among them; a NaN never wins fmaxf or __hmax2
+__device__ __forceinline__ float top_of(const Raw8<float>& v, float top) {
+    float x[8];
+    v.values(x);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[k]));
+    return top;
+}
+__device__ __forceinline__ float top_of(const Raw8<__nv_bfloat16>& v, float top) {   // two at a time
+    const __nv_bfloat162* x = reinterpret_cast<const __nv_bfloat162*>(&v.w[0]);
+    const __nv_bfloat162 m = __hmax2(__hmax2(__habs2(x[0]), __habs2(x[1])), __hmax2(__habs2(x[2]), __habs2(x[3])));
+    return fmaxf(top, fmaxf(__low2float(m), __high2float(m)));
+}
+// v * 2^-e.  bf16 has fp32's exponents, so two at a time are as exact: only what is far below e4m3's least step is lost
+__device__ __forceinline__ void scale(Raw8<float>& v, float inv, float (&f)[8]) {
+    v.values(f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) f[k] *= inv;
+}
+__device__ __forceinline__ void scale(Raw8<__nv_bfloat16>& v, float inv, float (&f)[8]) {
+    __nv_bfloat162* x = reinterpret_cast<__nv_bfloat162*>(&v.w[0]);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) x[k] = __hmul2(x[k], __float2bfloat162_rn(inv));
+    v.values(f);
+}
+// largest of the CTA's values; `tops` holds a slot for each warp and is free when the CTA enters
+__device__ __forceinline__ float cta_max(float top, float* tops) {
+    top = warp_max(top);
+    if ((threadIdx.x & 31) == 0) tops[threadIdx.x >> 5] = top;
+    __syncthreads();
+    top = 0.f;
+    for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, tops[w]);
+    return top;
+}
+
 // grid (blocks a row may touch, 2 * Hkv, rows); NCH: chunks of 8 values a thread may hold
 template <typename T, int NCH>
 __global__ void k_kv8_append(const Kv8Append p) {
-    __shared__ float tops[8];
+    __shared__ float tops[2][8];
     const int r = blockIdx.z, h = blockIdx.y >> 1, which = blockIdx.y & 1, tid = threadIdx.x;
     const Kv8Cache& c = p.c;
     Kv8Row row;
@@ -72,22 +108,29 @@ __global__ void k_kv8_append(const Kv8Append p) {
     const int held = lo - b0;   // earlier positions in the block
     const int had = held ? (int)*sc - 127 : -1000;
 
+    // The kernel's instructions set its time as much as its bytes do, so infinities, NaN and what the largest exponent
+    // cannot hold cost the other blocks one compare: the plain maximum tells whether the block has any but NaN
     float top = 0.f;
 #pragma unroll
     for (int u = 0; u < NCH; ++u)
-        if (tid + u * (int)blockDim.x < chunks) {
-            float x[8];
-            v[u].values(x);
+        if (tid + u * (int)blockDim.x < chunks) top = top_of(v[u], top);
+    const float all = top = cta_max(top, tops[0]);   // and every thread has read the old exponent
+    if (!finite_f(all)) {   // again, over the finite values
+        top = 0.f;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                if (finite_f(x[k])) top = fmaxf(top, fabsf(x[k]));
-        }
-    top = warp_max(top);
-    if ((tid & 31) == 0) tops[tid >> 5] = top;
-    __syncthreads();   // and every thread has read the old exponent
-    top = 0.f;
-    for (int w = 0; w < (int)blockDim.x / 32; ++w) top = fmaxf(top, tops[w]);
+        for (int u = 0; u < NCH; ++u)
+            if (tid + u * (int)blockDim.x < chunks) {
+                float x[8];
+                v[u].values(x);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (finite_f(x[k])) top = fmaxf(top, fabsf(x[k]));
+            }
+        top = cta_max(top, tops[1]);
+    }
     const int e = max(kv8_exponent(top), had);
+    // a caller's own scale bytes go beyond what append writes: 118 keeps the limit finite, 126 the factor normal
+    const bool beyond = all > 448.f * pow2i(min(e, 118)) || e > 126;
     if (tid == 0) *sc = (uint8_t)(e + 127);
     const float inv = pow2i(-min(e, 126));
 #pragma unroll
@@ -95,11 +138,13 @@ __global__ void k_kv8_append(const Kv8Append p) {
         const int i = tid + u * blockDim.x;
         if (i >= chunks) continue;
         float x[8];
-        v[u].values(x);
+        scale(v[u], inv, x);
+        if (beyond) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            x[k] *= inv;
-            if (!(fabsf(x[k]) <= 448.f)) x[k] = __int_as_float(0x7FFFFFFF);
+            for (int k = 0; k < 8; ++k) {
+                x[k] *= pow2i(min(126 - e, 0));
+                if (!(fabsf(x[k]) <= 448.f)) x[k] = __int_as_float(0x7FFFFFFF);
+            }
         }
         *reinterpret_cast<uint2*>(dst + (size_t)held * c.hd + (size_t)i * 8) =
             make_uint2(f32_to_e4m3x4(x[0], x[1], x[2], x[3]), f32_to_e4m3x4(x[4], x[5], x[6], x[7]));
@@ -122,7 +167,7 @@ cudaError_t launch(const Kv8Append& p, cudaStream_t s) {
     const int span = p.b.max_new < p.c.block ? p.b.max_new : p.c.block;   // tokens of one block
     const int chunks = span * (p.c.hd / 8);
     // Few threads with many loads each: a CTA waits most of its life, so what counts is the bytes that an SM's 2048
-    // threads have under way (4 prompts of up to 8191 bf16 tokens: 128 threads 27 us, 64 or 256 threads 30 us)
+    // threads have under way (4 prompts of up to 8191 bf16 tokens: 128 threads 30 us, 64 or 256 threads 33 us, before the maximum and the scaling took bf16 in pairs)
     const int threads = chunks <= 64 ? 64 : sizeof(T) == 2 ? 128 : 256;
     const dim3 grid((p.b.max_new + p.c.block - 2) / p.c.block + 1, 2 * p.c.Hkv, p.c.rows);
     if (chunks <= threads) k_kv8_append<T, 1><<<grid, threads, 0, s>>>(p);

@@ -465,7 +465,8 @@ int dec_attention_static(dec_handle *h, int32_t layer, const float *qkv, const i
  * bytes to hold and to read), with one power-of-two scale for each block of
  * scale_block consecutive positions of one K/V head.  A stored byte x8 in a
  * block with scale byte s stands for x8 * 2^(s - 127); scale bytes that
- * dec_kv8_append writes lie in [87, 187].
+ * dec_kv8_append writes lie in [87, 187]; a caller who fills a cache by other
+ * means keeps them in [1, 254].
  *
  * These calls stand beside dec_attention for callers who keep their own cache.
  * They take no handle, only launch kernels on the caller's stream (NULL: the
@@ -501,7 +502,8 @@ typedef struct dec_kv8_cache {
  * <= total, more than max_new tokens, kv_len outside [0, pages_per_row *
  * page_size]) sets DEC_FAULT_POS in *err and is skipped whole; a page id that
  * is needed and outside [0, num_pages) sets DEC_FAULT_SLOT_MAP, and the page
- * counts as holding nothing. */
+ * counts as holding nothing.  DEC_FAULT_WAIT: a copy or product never ended,
+ * and the call's results are not to be used. */
 typedef struct dec_kv8_batch {
     const int32_t *q_start;      /* device [rows + 1], or NULL: one token for each row */
     const int32_t *kv_len;       /* device [rows]: positions of each row, this call's tokens included */
