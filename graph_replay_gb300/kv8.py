@@ -11,6 +11,7 @@ back to the host.  ``check`` does, and raises if a call met an entry of
 """
 from __future__ import annotations
 
+import threading
 from typing import Optional
 
 import torch
@@ -50,7 +51,7 @@ class KV8Cache:
         self.rows, self.cap, self.n_kv_heads, self.head_dim = rows, per_row * page, heads, dim
         self.page_size, self.scale_block = page, page // k_scale.shape[2]
         self.device = k.device
-        self._need, self._ws = {}, {}
+        self._need, self._ws, self._lock = {}, {}, threading.Lock()
         self._err = torch.zeros(1, dtype=torch.int32, device=k.device)
         self._c = B.dec_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   None if page_table is None else page_table.data_ptr(), rows, per_row, page, pages,
@@ -74,11 +75,12 @@ class KV8Cache:
                                self._err.data_ptr(), total, max_new)
 
     def _tokens(self, what, t, heads):
-        if (t.dim() != 3 or t.dtype not in _DT or t.device != self.device or t.shape[2] != self.head_dim
-                or (heads and t.shape[1] != heads) or t.stride(2) != 1 or t.stride(1) != self.head_dim):
+        shape, stride = t.shape, t.stride()
+        if (len(shape) != 3 or t.dtype not in _DT or t.device != self.device or shape[2] != self.head_dim
+                or (heads and shape[1] != heads) or stride[2] != 1 or stride[1] != self.head_dim):
             raise ValueError(f"KV8Cache: {what} is f32 or bf16 [tokens, heads, head_dim], heads side by side, on the "
                              "cache's device")
-        return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+        return stride[0] if shape[0] > 1 else shape[1] * shape[2]
 
     def append(self, k: torch.Tensor, v: torch.Tensor, kv_len: torch.Tensor, q_start: Optional[torch.Tensor] = None,
                max_new: int = 1) -> None:
@@ -132,13 +134,14 @@ class KV8Cache:
         tokens, heads, _ = q.shape
         b = self._batch(kv_len, q_start, tokens, max_new)
         stream = _raw_stream(self._c.device)
-        if workspace is None:
-            workspace = self._workspace(stream, self.workspace_bytes(tokens, heads, max_new, window, sinks, q.dtype))
-        elif workspace.device != self.device or not workspace.is_contiguous():
+        if workspace is not None and (workspace.device != self.device or not workspace.is_contiguous()):
             raise ValueError("KV8Cache: the workspace is contiguous and on the cache's device")
-        a = B.dec_kv8_attn(q.data_ptr(), out.data_ptr(), qs, os_, _DT[q.dtype], heads, window, sinks, scale,
-                           workspace.data_ptr(), workspace.numel() * workspace.element_size())
-        B.dec_kv8_attend(self._c, b, a, stream)
+        with self._lock:   # a call may launch two kernels that hand on the workspace: another thread's come before or after
+            if workspace is None:
+                workspace = self._workspace(stream, self.workspace_bytes(tokens, heads, max_new, window, sinks, q.dtype))
+            a = B.dec_kv8_attn(q.data_ptr(), out.data_ptr(), qs, os_, _DT[q.dtype], heads, window, sinks, scale,
+                               workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            B.dec_kv8_attend(self._c, b, a, stream)
         return out
 
     def check(self) -> None:

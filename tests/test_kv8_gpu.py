@@ -259,6 +259,26 @@ def test_append_extremes(dtype):
     same_bytes(cache, K, V)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("byte", [188, 240, 253, 255])
+def test_append_to_a_block_of_larger_scale(byte, dtype):
+    """A caller's own scale bytes go beyond those that append writes: the block keeps its exponent, infinities are NaN."""
+    from graph_replay_gb300 import KV8Cache
+    c = KV8Cache.empty(1, 64, 1, 64, scale_block=16)
+    c.k_scale[:, :, 0] = byte
+    c.v_scale[:, :, 0] = byte
+    x = torch.zeros(2, 1, 64, dtype=dtype)
+    x[0, 0, :6] = torch.tensor([math.inf, -math.inf, math.nan, 1.0, 2.0 ** (byte - 127 - 3), -3.0 * 2.0 ** (byte - 127 - 9)])
+    c.append(x.cuda(), x.cuda(), torch.tensor([3], dtype=torch.int32, device="cuda"),
+             torch.tensor([0, 2], dtype=torch.int32, device="cuda"), max_new=2)
+    c.check()
+    for pool, scale in ((c.k, c.k_scale), (c.v, c.v_scale)):
+        assert int(scale[0, 0, 0]) == byte
+        got = pool[0, 0, 1].view(torch.float8_e4m3fn).float().cpu()
+        assert bool(got[:3].isnan().all())
+        assert got[3:6].tolist() == [0.0, 2.0 ** -3, -3.0 * 2.0 ** -9] and not got[6:].any()
+
+
 def test_append_from_a_packed_matrix_and_bad_entries():
     from graph_replay_gb300 import _binding as B
     rows = [(20, 3), (40, 2), (8, 8)]
@@ -350,6 +370,30 @@ def test_graphs_and_streams():
             s.append(table[r], l - 1, x[r:r + 1].double().cpu())
     compare(outs[0], [(100, 1), (1, 1), (1999, 1)], K, V, table, q, 0, 0, F32)
     cache.check()
+
+
+def test_threads_on_one_stream():
+    """Calls of several threads on one stream share the cache's workspace; splits and their join stay together."""
+    import threading
+    rows = [(3000, 16)]
+    K, V, table, q, kv_len, starts = build(rows, 8, 1, 128, 64, 64, 77, F32)
+    c = gpu_cache(K, V, table)
+    q, kv_len, starts = q.cuda(), kv_len.cuda(), starts.cuda()
+    qs = [q * (1 + i) for i in range(4)]
+    want = [c.attend(x, kv_len, starts, max_new=16) for x in qs]
+    torch.cuda.synchronize()
+    got = [[] for _ in qs]
+
+    def work(i):
+        for _ in range(50):
+            got[i].append(c.attend(qs[i], kv_len, starts, max_new=16))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    torch.cuda.synchronize()
+    c.check()
+    assert [len(g) for g in got] == [50] * 4
+    assert all(torch.equal(o, w) for g, w in zip(got, want) for o in g)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
