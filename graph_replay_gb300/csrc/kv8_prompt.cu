@@ -782,17 +782,19 @@ __global__ void __launch_bounds__(256) k_kv8_prompt_join(const Kv8Attend p, int 
     const size_t all_rows = (size_t)p.b.total * p.Hq, qrow = (size_t)row.t0 * p.Hq + m;
     const float* ml = p.ws + (size_t)most * all_rows * HD;
     constexpr int D = HD / 32;
-    float M = -INFINITY, l = 0.f, o[D];
+    // lane s knows of part s: its maximum, sum and weight.  A part that saw nothing is all zeros with weight 0
+    const float2 mine = lane < splits ? *reinterpret_cast<const float2*>(ml + (lane * all_rows + qrow) * 2) : make_float2(-INFINITY, 0.f);
+    const float M = warp_max(mine.x), weight = mine.x == -INFINITY ? 0.f : kv8_exp2(mine.x - M);
+    float l = 0.f, o[D];
 #pragma unroll
     for (int d = 0; d < D; ++d) o[d] = 0.f;
-    for (int s = 0; s < splits; ++s) M = fmaxf(M, ml[(s * all_rows + qrow) * 2]);
-    for (int s = 0; s < splits; ++s) {
-        const float ms = ml[(s * all_rows + qrow) * 2], ls = ml[(s * all_rows + qrow) * 2 + 1];
-        if (ms == -INFINITY && ls == 0.f) continue;   // nothing seen in this split
-        const float f = ms == -INFINITY ? 0.f : kv8_exp2(ms - M);
-        l += ls * f;
+    const float* part = p.ws + qrow * HD + lane * D;
+#pragma unroll 8
+    for (int s = 0; s < splits; ++s) {   // the parts' loads do not wait for one another
+        const float f = __shfl_sync(0xffffffffu, weight, s);
+        l = fmaf(__shfl_sync(0xffffffffu, mine.y, s), f, l);
 #pragma unroll
-        for (int d = 0; d < D; ++d) o[d] = fmaf(p.ws[(s * all_rows + qrow) * HD + lane * D + d], f, o[d]);
+        for (int d = 0; d < D; ++d) o[d] = fmaf(part[s * all_rows * HD + d], f, o[d]);
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
     T* dst = static_cast<T*>(p.out) + (row.t0 + m / p.Hq) * p.out_stride + m % p.Hq * HD + lane * D;
@@ -814,7 +816,7 @@ long long prompt_keys(const Kv8Attend& p) {   // the most positions that the row
 int prompt_splits(const Kv8Attend& p, int num_sms) {
     const long long ctas = prompt_tiles(p) * p.c.Hkv * p.c.rows, tiles = prompt_keys(p) / KP_KEYS;
     long long n = num_sms / ctas;
-    if (n > 32) n = 32;
+    if (n > 32) n = 32;   // the join's lanes
     return n < 1 ? 1 : kp_parts((int)(tiles < (1 << 20) ? tiles : 1 << 20), (int)n);
 }
 
