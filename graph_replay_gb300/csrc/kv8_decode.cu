@@ -28,13 +28,21 @@
 //     scaled by 2^6, f16 holds 2^14), so a 16-key step needs one vote and
 //     almost never a reduction or a rescaling;
 //   * work: the visible 16-key steps of each row and K/V head (windows make gaps
-//     that are never touched).  Where the SMs suffice, each (row, head) is cut into
-//     pieces of its own, of at least two steps a warp, so short rows are not cut.
-//     Otherwise all steps, in one line, are cut into equal pieces, one for each SM,
-//     whatever the lengths are.  A
-//     (row, head) that is cut leaves partial results in the workspace; the CTA that
-//     finishes it last joins them, in the order of the pieces, and sets its counter
-//     back to 0.
+//     that are never touched).  Where the places (two CTAs an SM) suffice, each
+//     (row, head) is cut into pieces of its own, of at least two steps a warp, so
+//     short rows are not cut.  Otherwise all steps, in one line, are cut into
+//     equal pieces, one for each place, whatever the lengths are.  A (row, head)
+//     that is cut leaves partial results in the workspace; the CTA that finishes
+//     it last joins them, in the order of the pieces, and sets its counter back
+//     to 0: one launch.
+//
+// Measured (128 dims): 32 bf16 rows of up to 32k positions 221 us, 6.4 TB/s or
+// 94 % of the measured copy rate; 8 fp32 rows x 8k 28.9 us and one row of 8191 12.7 us, where
+// the ends bind it: of the 7.3 us that one short row takes on the device, the launch,
+// the plan (a trip to the lengths), the first steps (page id, then bytes) and the
+// join's trip through memory are nearly all.  Two CTAs an SM hide one's ends
+// behind the other's stream: when it was changed, a single CTA of 12 warps took
+// 34.6 us for the 8 rows, three of 4 warps 31.
 #include <limits.h>
 #include <type_traits>
 #include "kv8.cuh"

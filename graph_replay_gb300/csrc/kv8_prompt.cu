@@ -4,27 +4,39 @@
 // The query rows of a K/V head are (token, query head of the group), tokens
 // first: a tile of 128 holds all G heads of 128 / G tokens, so the heads share
 // every K/V tile and little of a tile lies above the causal diagonal.  Any G
-// works: a tile may begin inside a token.  Per 128 positions:
-//   convert   four warps read the e4m3 bytes (the pages' own order), turn them
-//             into f16 -- exact -- and store them as 128-byte-swizzled operand
-//             tiles in a ring; V's NaN become 0 there (see below)
-//   S = Q K^T tcgen05.mma kind::f16, A = Q, B = K, D in TMEM
+// works: a tile may begin inside a token.  A CTA has two query tiles, and per 64
+// positions (the one K/V tile that both read):
+//   convert   four warps for K and four for V read the e4m3 bytes (the pages'
+//             own order) a tile ahead, turn them into f16 -- exact -- and store
+//             them as 128-byte-swizzled operand tiles in a ring; page ids and
+//             scales are read a batch of tiles earlier.  V's NaN become 0 (below)
+//   S = Q K^T tcgen05.mma kind::f16, A = Q, B = K, D in TMEM; two S buffers for
+//             each query tile, so the product runs a tile ahead of the softmax
 //   softmax   a thread owns a row: scores times K's scale, V's exponent added
 //             (weights are relative to the largest weight * V scale, the sum
 //             divides V's exponent out again), running maximum kept within 2^8,
 //             weights as f16 back into TMEM over the scores they came from
 //   O += P V  A = P from TMEM, B = V read MN-major
-// With bf16 q a CTA works on two query tiles in turn: while one is in softmax
-// the tensor core works for the other (TMEM: two S of 128 columns, two O).
-// With fp32 q, q and the weights enter as two f16 parts each; a CTA then has
-// one query tile, two S and P in columns of its own.
+// 64 positions rather than 128: with 128 there is room for one S a query tile,
+// and product and softmax wait for one another (8191 tokens: 682 -> 633 us with
+// the change, although S = Q K^T of 64 columns reads Q from shared memory twice as
+// often and takes 48 cycles where 32 would do).
+// With fp32 q, q and the weights enter as two f16 parts each; the parts of P lie
+// side by side over their scores.  The tensor core's accumulator cuts off what it
+// adds, so O is folded into memory in rounded sums every KP_FOLD tiles.
 //
-// What bounds it: 4 * 128 * 128 * HD operations a tile pair on the tensor
-// cores against 128 exponentials a row and the conversion's shared-memory
-// stores.
+// Bound, measured: 8191 tokens 602 us, 47 % of the measured bf16 rate; 2 x 64 fp32
+// tokens over 32k 103 us.  A K/V tile takes 2600 cycles, of which the tensor core needs
+// 1280 and the softmax warps about 1840; taking out either (no exponentials and no
+// maximum: 602 -> 604 us; half of the MMAs: 559; no loads and conversions: 578; all of
+// them: 464) shows that no rate binds it but the chain of a tile's steps: one
+// softmax warp's own latencies (2 of them a scheduler) and the hand-overs between
+// the roles.  What did not help: one arrival a warp instead of a thread, more
+// registers for either role, polling instead of sleeping.
 //
 // Few tiles and many positions: the positions of a tile are split over several
 // CTAs (a host rule on sizes) and joined by a second kernel in split order.
+// Results leave through shared memory, row by row.
 //
 // NaN: 0 * NaN is NaN inside an MMA, so a NaN in V that one row of a tile sees
 // would reach the rows that do not.  Therefore V's NaN never enter the product;
@@ -77,9 +89,9 @@ constexpr uint32_t KP_DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
 constexpr uint32_t kp_idesc(int N, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(KP_ROWS >> 4) << 24);
 }
-// One thread issues every MMA, so what it computes for each lies on the tensor core's path: with addresses and
-// descriptors computed in that thread's branch an MMA of 64 cycles took 290.  So the whole warp runs the issuing
-// code, every lane has the operands, and each MMA or commit elects the lane that issues it
+// One thread issues every MMA, so what it computes for each lies on the tensor core's path.  The whole warp runs the
+// issuing code, every lane has the operands, and each MMA or commit elects the lane that issues it: an MMA is then a
+// few instructions, with nothing moved between a lane's registers and the warp's
 __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n .reg .pred e, p;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
                  " elect.sync _|e, 0xffffffff;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d), "r"(a),
@@ -178,8 +190,8 @@ __device__ __forceinline__ bool sleep_wait(uint64_t* bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-// A whole warp waits, bounded (about two seconds; FAULT_WAIT then).  One lane polls, and sleeps between polls: spinning
-// warps took 40 % of the issue slots from the working ones.  False: this wait has given up, or another role has
+// A whole warp waits, bounded (about two seconds; FAULT_WAIT then).  One lane polls, and sleeps between polls: two
+// fifths of the instructions were those of spinning warps (they filled idle slots: the time hardly changed).  False: this wait has given up, or another role has
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* aborted, unsigned* err) {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;   // mostly it is done already
     bool go = true;
