@@ -54,7 +54,7 @@ namespace {
 
 constexpr int KP_ROWS = 128;              // query rows of a tile: TMEM lanes
 constexpr int KP_KEYS = 64;               // positions of a tile
-// 8 softmax warps, 4 that convert K, 4 that convert V, 1 MMA warp and 3 that only pad its warpgroup
+// 8 softmax warps, 4 that convert K, 4 that convert V, 2 that issue MMAs and 2 that only pad their warpgroup
 constexpr int KP_K_WARP = 8, KP_V_WARP = 12, KP_MMA_WARP = 16, KP_THREADS = 20 * 32;
 // registers a thread by role (setmaxnreg): 640 threads x 96 at launch = 256 x 120 + 256 x 88 + 128 x 64
 constexpr int KP_REGS_SOFTMAX = 120, KP_REGS_CONV = 88, KP_REGS_MMA = 64;
@@ -89,19 +89,30 @@ constexpr uint32_t KP_DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
 constexpr uint32_t kp_idesc(int N, bool b_mn) {
     return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(KP_ROWS >> 4) << 24);
 }
-// One thread issues every MMA, so what it computes for each lies on the tensor core's path.  The whole warp runs the
-// issuing code, every lane has the operands, and each MMA or commit elects the lane that issues it: an MMA is then a
-// few instructions, with nothing moved between a lane's registers and the warp's
-__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred e, p;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n"
-                 " elect.sync _|e, 0xffffffff;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n}\n" ::"r"(d), "r"(a),
-                 "r"(b), "r"(KP_DESC_HI), "r"(idesc), "r"(acc)
+// One thread issues every MMA of a query tile, so what it does for each lies on the tensor core's path.  The whole warp
+// runs the issuing code, every lane has the operands, and each run of four MMAs (four steps of 16) or commit elects the
+// lane that issues it.
+
+// D (+)= A B over 64 dims, both tiles in shared memory.  acc 0: D starts anew
+__device__ __forceinline__ void mma_ss4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred e, p, t;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n"
+                 " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n elect.sync _|e, 0xffffffff;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n add.u64 x, x, 2;\n add.u64 y, y, 2;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n add.u64 x, x, 2;\n add.u64 y, y, 2;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n add.u64 x, x, 2;\n add.u64 y, y, 2;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(KP_DESC_HI),
+                 "r"(idesc), "r"(acc)
                  : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile("{\n .reg .pred e, p;\n .reg .b64 y;\n setp.ne.u32 p, %5, 0;\n mov.b64 y, {%2, %3};\n"
-                 " elect.sync _|e, 0xffffffff;\n @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n}\n" ::"r"(d), "r"(a),
-                 "r"(b), "r"(KP_DESC_HI), "r"(idesc), "r"(acc)
+// D (+)= A B over 64 positions, A in TMEM (8 columns a step), B's rows 128 bytes apart
+__device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred e, p, t;\n .reg .b64 y;\n .reg .b32 a;\n setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n"
+                 " mov.b32 a, %1;\n mov.b64 y, {%2, %3};\n elect.sync _|e, 0xffffffff;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, p;\n add.u32 a, a, 8;\n add.u64 y, y, 128;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n add.u32 a, a, 8;\n add.u64 y, y, 128;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n add.u32 a, a, 8;\n add.u64 y, y, 128;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(KP_DESC_HI),
+                 "r"(idesc), "r"(acc)
                  : "memory");
 }
 __device__ __forceinline__ void kp_commit(uint64_t* bar) {
@@ -251,7 +262,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     constexpr int NQ = 2, SLOTS = LY::SLOTS;
     extern __shared__ __align__(1024) unsigned char kp_raw[];
     unsigned char* sm = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(kp_raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ __align__(8) uint64_t kv_full[SLOTS], kv_empty[SLOTS], s_full[4], p_full[2], pv_done[2], meta_full[KP_META], all_done;
+    __shared__ __align__(8) uint64_t kv_full[SLOTS], kv_empty[SLOTS], s_full[4], p_full[4], pv_done[4], meta_full[KP_META], all_done[2];
     __shared__ KpMeta meta[KP_META][KP_GROUPS];
     __shared__ float fac_s[NQ * KP_ROWS];
     __shared__ uint32_t marks[KP_MARKS];
@@ -326,16 +337,18 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
     if (tid == 0) {
         for (int s = 0; s < SLOTS; ++s) {
             mbar_init(&kv_full[s], 128);
-            mbar_init(&kv_empty[s], 1);
+            mbar_init(&kv_empty[s], nact);
         }
         for (int x = 0; x < 2; ++x) {
             mbar_init(&s_full[2 * x], 1);
             mbar_init(&s_full[2 * x + 1], 1);
-            mbar_init(&p_full[x], 128);
-            mbar_init(&pv_done[x], 1);
+            mbar_init(&p_full[2 * x], 128);
+            mbar_init(&p_full[2 * x + 1], 128);
+            mbar_init(&pv_done[2 * x], 1);
+            mbar_init(&pv_done[2 * x + 1], 1);
+            mbar_init(&all_done[x], 1);
         }
         for (int x = 0; x < KP_META; ++x) mbar_init(&meta_full[x], 1);
-        mbar_init(&all_done, 1);
         aborted = 0;
         marked = 0;
         mbar_fence_init();
@@ -462,70 +475,52 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         else convert(std::true_type{});
         cta_meet();
     } else if (warp >= KP_MMA_WARP) {
-        // ---- MMA issuer ----
+        // ---- MMA issuers: a warp for each query tile, so that one's waits do not hold up the other's products ----
         regs_down<KP_REGS_MMA>();
-        if (warp == KP_MMA_WARP && ntiles > 0) {
+        const int x = warp - KP_MMA_WARP;   // query tile
+        if (x < nact && ntiles > 0) {
             constexpr uint32_t id_s = kp_idesc(KP_KEYS, false), id_o = kp_idesc(HD, true);
-            const uint32_t dtu = __shfl_sync(0xffffffffu, dt, 0);
+            const uint32_t dtu = __shfl_sync(0xffffffffu, dt, 0), xu = __shfl_sync(0xffffffffu, (uint32_t)x, 0);
             const int nt = __shfl_sync(0xffffffffu, ntiles, 0);
-            const uint32_t qd = kp_desc(smem_u32(sm + LY::Q), 16), kd = kp_desc(smem_u32(sm + LY::KV), 16),
-                           vd = kp_desc(smem_u32(sm + LY::KV), KP_PANEL);
+            const uint32_t qd = kp_desc(smem_u32(sm + LY::Q), 16) + xu * (LY::PARTS * LY::QTILE >> 4);
+            const uint32_t kd = kp_desc(smem_u32(sm + LY::KV), 16), vd = kp_desc(smem_u32(sm + LY::KV), KP_PANEL);
+            const uint32_t sd = dtu + 128 * xu, od = dtu + LY::O + HD * xu;
             auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
                 const bool there = warp_wait(bar, parity, ab, p.b.err);
                 fence_after();
                 return there;
             };
-            auto qk = [&](auto tile, int j) {   // S of query tile x and tile j, into buffer j & 1
-                constexpr int x = decltype(tile)::value;
-                const uint32_t kt = kd + (uint32_t)((2 * j) % SLOTS) * (LY::TILE >> 4), qt = qd + x * (LY::PARTS * LY::QTILE >> 4);
-                const uint32_t scol = dtu + 128 * x + 64 * (j & 1);
+            auto qk = [&](int j) {   // S of tile j, into buffer j & 1
+                const uint32_t kt = kd + (uint32_t)((2 * j) % SLOTS) * (LY::TILE >> 4), scol = sd + 64 * (j & 1);
 #pragma unroll
-                for (int kk = 0; kk < HD / 16; ++kk) {
-                    const uint32_t qo = (uint32_t)(kk / 4 * KP_QPANEL + 32 * (kk % 4)) >> 4, ko = (uint32_t)(kk / 4 * KP_PANEL + 32 * (kk % 4)) >> 4;
-                    mma_ss(scol, qt + qo, kt + ko, id_s, kk > 0);
-                    if constexpr (FINE) mma_ss(scol, qt + (LY::QTILE >> 4) + qo, kt + ko, id_s, 1);
+                for (int n = 0; n < HD / 64; ++n) {
+                    mma_ss4(scol, qd + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, n > 0);
+                    if constexpr (FINE) mma_ss4(scol, qd + (LY::QTILE >> 4) + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, 1);
                 }
-                kp_commit(&s_full[2 * x + (j & 1)]);
+                kp_commit(&s_full[2 * xu + (j & 1)]);
+                kp_commit(&kv_empty[(2 * j) % SLOTS]);
             };
-            auto pv = [&](auto tile, int j) {
-                constexpr int x = decltype(tile)::value;
-                const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * (LY::TILE >> 4);
-                const uint32_t pcol = dtu + 128 * x + 64 * (j & 1), ocol = dtu + LY::O + HD * x;
-#pragma unroll
-                for (int kk = 0; kk < KP_KEYS / 16; ++kk) {
-                    mma_ts(ocol, pcol + kk * 8, vt + 128 * kk, id_o, kk > 0 ? 1u : (uint32_t)(FINE ? j % KP_FOLD > 0 : j > 0));
-                    if constexpr (FINE) mma_ts(ocol, pcol + 32 + kk * 8, vt + 128 * kk, id_o, 1);
-                }
-                kp_commit(&pv_done[x]);
+            auto pv = [&](int j) {
+                const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * (LY::TILE >> 4), pcol = sd + 64 * (j & 1);
+                mma_ts4(od, pcol, vt, id_o, (uint32_t)(FINE ? j % KP_FOLD > 0 : j > 0));
+                if constexpr (FINE) mma_ts4(od, pcol + 32, vt, id_o, 1);
+                kp_commit(&pv_done[2 * xu + (j & 1)]);
+                kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
             };
             auto full = [&](int s) { return wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
-            constexpr std::integral_constant<int, 0> A{};
-            constexpr std::integral_constant<int, 1> B{};
-            const bool two = nact == 2;
             bool ok = full(0);
-            if (ok) {
-                qk(A, 0);
-                if (two) qk(B, 0);
-                kp_commit(&kv_empty[0]);
-            }
+            if (ok) qk(0);
             for (int j = 0; j < nt && ok; ++j) {
-                if (j + 1 < nt) {   // the other buffers: their P have been multiplied, in order
+                if (j + 1 < nt) {   // the other buffer: its P has been multiplied, in order
                     if (!(ok = full(2 * j + 2))) break;
-                    qk(A, j + 1);
-                    if (two) qk(B, j + 1);
-                    kp_commit(&kv_empty[(2 * j + 2) % SLOTS]);
+                    qk(j + 1);
                 }
-                if (!(ok = full(2 * j + 1) && wait(&p_full[0], (uint32_t)j & 1u))) break;
-                pv(A, j);
-                if (two) {
-                    if (!(ok = wait(&p_full[1], (uint32_t)j & 1u))) break;
-                    pv(B, j);
-                }
-                kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
+                if (!(ok = full(2 * j + 1) && wait(&p_full[2 * xu + (j & 1)], (uint32_t)(j >> 1) & 1u))) break;
+                pv(j);
             }
             // every MMA issued has finished before TMEM is released (also after a give-up)
-            kp_commit(&all_done);
-            if (lane == 0 && !mbar_wait(&all_done, 0u)) give_up();
+            kp_commit(&all_done[xu]);
+            if (lane == 0 && !mbar_wait(&all_done[xu], 0u)) give_up();
         }
         __syncwarp();
         cta_meet();
@@ -576,20 +571,25 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 }
             }
         };
+        auto pv_wait = [&](int j) { return warp_wait(&pv_done[2 * x + (j & 1)], (uint32_t)(j >> 1) & 1u, ab, p.b.err); };
         for (int j = 0; j < (x < nact ? ntiles : 0); ++j) {
             const int k0 = key0(i0 + j);
-            bool rested = j == 0;   // P V of tile j - 1 is done
             const bool folds = FINE && j > 0 && j % KP_FOLD == 0;
             if (folds) {   // the next P V starts O anew, after P of this tile is full
-                if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
-                rested = true;
+                if (!(ok = pv_wait(j - 1))) break;
                 fence_after();
 #pragma unroll
                 for (int cc = 0; cc < HD; cc += 64) fold_o(cc);
                 M_fold = M;
             }
-            ok = warp_wait(&s_full[2 * x + (j & 1)], (uint32_t)(j >> 1) & 1u, ab, p.b.err) &&
-                 warp_wait(&meta_full[j % KP_META], (uint32_t)(j / KP_META) & 1u, ab, p.b.err);
+            // Every phase of every barrier is waited for before the next can end, since a parity tells a phase only from
+            // the one before it.  s_full, p_full and pv_done have a barrier for each S buffer: S of tile j + 2 follows
+            // P V of tile j, which follows P of tile j; and here P V of tile j - 2 is waited for before P of tile j
+            uint64_t* const sb = &s_full[2 * x + (j & 1)];
+            uint64_t* const mb = &meta_full[j % KP_META];
+            const uint32_t sp_ = (uint32_t)(j >> 1) & 1u, mp = (uint32_t)(j / KP_META) & 1u;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(sb, sp_) && mbar_try_wait(mb, mp) && (j < 2 || mbar_try_wait(&pv_done[2 * x + (j & 1)], sp_ ^ 1u))))
+                ok = warp_wait(sb, sp_, ab, p.b.err) && warp_wait(mb, mp, ab, p.b.err) && (j < 2 || pv_wait(j - 2));
             if (!ok) break;
             fence_after();
             const uint32_t scol = lrow + 128 * x + 64 * (j & 1);
@@ -628,8 +628,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 l *= alpha;
             }
             if (j > 0 && !folds && __any_sync(0xffffffffu, alpha != 1.f)) {
-                if (!(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
-                rested = true;
+                if (!(ok = pv_wait(j - 1))) break;
                 fence_after();
 #pragma unroll 1
                 for (int cc = 0; cc < HD; cc += 16) {
@@ -675,13 +674,11 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 if constexpr (FINE) tm_st16(scol + 32 + 16 * q, low);
             }
             wait_st();
-            // every tile's P V is waited for once: a parity tells a phase only from the one before it
-            if (!rested && !(ok = warp_wait(&pv_done[x], (uint32_t)(j - 1) & 1u, ab, p.b.err))) break;
             fence_before();
-            mbar_arrive(&p_full[x]);
+            mbar_arrive(&p_full[2 * x + (j & 1)]);
         }
         if (x < nact && ok && ntiles > 0) {
-            ok = warp_wait(&pv_done[x], (uint32_t)(ntiles - 1) & 1u, ab, p.b.err);
+            ok = pv_wait(ntiles - 1);
             fence_after();
         }
         cta_meet();   // every tile has been converted: the marks are complete
