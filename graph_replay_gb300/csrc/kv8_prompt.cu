@@ -25,14 +25,19 @@
 // side by side over their scores.  The tensor core's accumulator cuts off what it
 // adds, so O is folded into memory in rounded sums every KP_FOLD tiles.
 //
-// Bound, measured: 8191 tokens 602 us, 47 % of the measured bf16 rate; 2 x 64 fp32
-// tokens over 32k 103 us.  A K/V tile takes 2600 cycles, of which the tensor core needs
-// 1280 and the softmax warps about 1840; taking out either (no exponentials and no
-// maximum: 602 -> 604 us; half of the MMAs: 559; no loads and conversions: 578; all of
-// them: 464) shows that no rate binds it but the chain of a tile's steps: one
-// softmax warp's own latencies (2 of them a scheduler) and the hand-overs between
-// the roles.  What did not help: one arrival a warp instead of a thread, more
-// registers for either role, polling instead of sleeping.
+// Each query tile has its own issuing warp: a wait costs its trip through a busy
+// shared memory (about 250 cycles) even where nothing is left to wait for, and
+// with one warp for both tiles those trips, not the products, filled its time
+// (8191 tokens: 602 -> 543 us; K's and V's waits as one: 539).
+//
+// Bound, measured: 8191 tokens 539 us, 53 % of the measured bf16 rate; 2 x 64 fp32
+// tokens over 32k 94 us.  A K/V tile takes about 2200 cycles, of which the tensor
+// core needs 1280 and a softmax warp 1700.  Leaving out half of the MMAs, the
+// exponentials and the maximum, or the loads and conversions, each brings some 20 us,
+// all of them 145: no rate binds it but the chain of a tile's steps -- P to S of the
+// tile after the next to P again -- and the hand-overs in it.  What did not help:
+// S two tiles ahead, right behind P V (564); 16 softmax warps, two threads a row
+// (572); one arrival a warp instead of a thread; other shares of the registers.
 //
 // Few tiles and many positions: the positions of a tile are split over several
 // CTAs (a host rule on sizes) and joined by a second kernel in split order.
@@ -498,25 +503,33 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     if constexpr (FINE) mma_ss4(scol, qd + (LY::QTILE >> 4) + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, 1);
                 }
                 kp_commit(&s_full[2 * xu + (j & 1)]);
-                kp_commit(&kv_empty[(2 * j) % SLOTS]);
             };
             auto pv = [&](int j) {
                 const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * (LY::TILE >> 4), pcol = sd + 64 * (j & 1);
                 mma_ts4(od, pcol, vt, id_o, (uint32_t)(FINE ? j % KP_FOLD > 0 : j > 0));
                 if constexpr (FINE) mma_ts4(od, pcol + 32, vt, id_o, 1);
-                kp_commit(&pv_done[2 * xu + (j & 1)]);
-                kp_commit(&kv_empty[(2 * j + 1) % SLOTS]);
             };
             auto full = [&](int s) { return wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
             bool ok = full(0);
-            if (ok) qk(0);
+            if (ok) {
+                qk(0);
+                kp_commit(&kv_empty[0]);
+            }
             for (int j = 0; j < nt && ok; ++j) {
-                if (j + 1 < nt) {   // the other buffer: its P has been multiplied, in order
-                    if (!(ok = full(2 * j + 2))) break;
-                    qk(j + 1);
+                const bool more = j + 1 < nt;
+                const int sv = 2 * j + 1, sk = more ? 2 * j + 2 : sv;
+                auto there = [&](int s) { return mbar_try_wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
+                // a wait costs a trip through a busy shared memory even where nothing is left to wait for: both at once
+                if (__all_sync(0xffffffffu, there(sv) & there(sk))) fence_after();
+                else if (!(ok = full(sv) && full(sk))) break;
+                if (more) {
+                    qk(j + 1);   // into the other buffer: its P has been multiplied, in order
+                    kp_commit(&kv_empty[sk % SLOTS]);
                 }
-                if (!(ok = full(2 * j + 1) && wait(&p_full[2 * xu + (j & 1)], (uint32_t)(j >> 1) & 1u))) break;
+                if (!(ok = wait(&p_full[2 * xu + (j & 1)], (uint32_t)(j >> 1) & 1u))) break;
                 pv(j);
+                if (j + 2 >= nt) kp_commit(&pv_done[2 * xu + (j == nt - 1)]);
+                kp_commit(&kv_empty[sv % SLOTS]);
             }
             // every MMA issued has finished before TMEM is released (also after a give-up)
             kp_commit(&all_done[xu]);
@@ -571,7 +584,15 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 }
             }
         };
-        auto pv_wait = [&](int j) { return warp_wait(&pv_done[2 * x + (j & 1)], (uint32_t)(j >> 1) & 1u, ab, p.b.err); };
+        // Every phase of every barrier of the loop is waited for before the next can end, since a parity tells a phase only
+        // from the one before it: s_full and p_full have a barrier for each S buffer, S of tile j + 2 follows P V of tile j,
+        // and that P of tile j
+        auto s_wait = [&](int j) { return warp_wait(&s_full[2 * x + (j & 1)], (uint32_t)(j >> 1) & 1u, ab, p.b.err); };
+        // P V of tile j (asked at tile j + 1, or behind the last) is done: S of tile j + 2 follows it on the tensor core, and
+        // does not wait for P of tile j + 1; the last two tiles have a barrier each
+        auto pv_wait = [&](int j) {
+            return j + 2 < ntiles ? s_wait(j + 2) : warp_wait(&pv_done[2 * x + (j == ntiles - 1)], 0u, ab, p.b.err);
+        };
         for (int j = 0; j < (x < nact ? ntiles : 0); ++j) {
             const int k0 = key0(i0 + j);
             const bool folds = FINE && j > 0 && j % KP_FOLD == 0;
@@ -582,14 +603,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 for (int cc = 0; cc < HD; cc += 64) fold_o(cc);
                 M_fold = M;
             }
-            // Every phase of every barrier is waited for before the next can end, since a parity tells a phase only from
-            // the one before it.  s_full, p_full and pv_done have a barrier for each S buffer: S of tile j + 2 follows
-            // P V of tile j, which follows P of tile j; and here P V of tile j - 2 is waited for before P of tile j
-            uint64_t* const sb = &s_full[2 * x + (j & 1)];
             uint64_t* const mb = &meta_full[j % KP_META];
-            const uint32_t sp_ = (uint32_t)(j >> 1) & 1u, mp = (uint32_t)(j / KP_META) & 1u;
-            if (!__all_sync(0xffffffffu, mbar_try_wait(sb, sp_) && mbar_try_wait(mb, mp) && (j < 2 || mbar_try_wait(&pv_done[2 * x + (j & 1)], sp_ ^ 1u))))
-                ok = warp_wait(sb, sp_, ab, p.b.err) && warp_wait(mb, mp, ab, p.b.err) && (j < 2 || pv_wait(j - 2));
+            const uint32_t mp = (uint32_t)(j / KP_META) & 1u;
+            if (!__all_sync(0xffffffffu, mbar_try_wait(&s_full[2 * x + (j & 1)], (uint32_t)(j >> 1) & 1u) & mbar_try_wait(mb, mp)))
+                ok = s_wait(j) && warp_wait(mb, mp, ab, p.b.err);
             if (!ok) break;
             fence_after();
             const uint32_t scol = lrow + 128 * x + 64 * (j & 1);
