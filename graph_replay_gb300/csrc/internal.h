@@ -150,6 +150,7 @@ struct Kv8Attend {
         by_group = FastDiv((unsigned)G);
     }
     int window, sinks;         // window INT_MAX: every position up to the token's own
+    int skip, take;            // kv8_decode: a launch's tokens of each row, [skip, skip + take); take 0: all
     float scale;
     int* counters;             // [rows, Hkv], zero between calls
     float* ws;                 // kv8_decode_floats() or kv8_prompt_floats() floats
@@ -167,8 +168,8 @@ struct Kv8Step {
 };
 cudaError_t kv8_step_launch(const Kv8Step& p, cudaStream_t s, bool pdl);
 cudaError_t kv8_append_launch(const Kv8Append& p, cudaStream_t s);
-// up to 16 query rows (tokens x query heads of a K/V head) of a sequence (kv8_decode.cu)
-bool kv8_decode_takes(const Kv8Attend& p);
+// up to 16 query rows (tokens x query heads of a K/V head) of a sequence, or a few times as many (kv8_decode.cu)
+bool kv8_decode_takes(const Kv8Attend& p, int num_sms);
 cudaError_t kv8_decode_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
 size_t kv8_decode_floats(const Kv8Attend& p, int num_sms);   // of workspace
 // any number of query rows (kv8_prompt.cu)

@@ -122,7 +122,7 @@ int check_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const d
 // the counters, then the floats
 size_t counter_bytes(const Kv8Cache& c) { return ((size_t)c.rows * c.Hkv * sizeof(int) + 255) / 256 * 256; }
 size_t attend_bytes(const Kv8Attend& p, int sms) {
-    return counter_bytes(p.c) + sizeof(float) * (kv8_decode_takes(p) ? kv8_decode_floats(p, sms) : kv8_prompt_floats(p, sms));
+    return counter_bytes(p.c) + sizeof(float) * (kv8_decode_takes(p, sms) ? kv8_decode_floats(p, sms) : kv8_prompt_floats(p, sms));
 }
 
 int sms_of(int device, int* n) {
@@ -187,7 +187,7 @@ int dec_kv8_attend(const dec_kv8_cache* cache, const dec_kv8_batch* batch, const
     OnDevice on(cache->device);
     if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
     const cudaStream_t s = (cudaStream_t)stream;
-    return launched(kv8_decode_takes(p) ? kv8_decode_launch(p, sms, s) : kv8_prompt_launch(p, sms, s), "dec_kv8_attend");
+    return launched(kv8_decode_takes(p, sms) ? kv8_decode_launch(p, sms, s) : kv8_prompt_launch(p, sms, s), "dec_kv8_attend");
 }
 
 }  // extern "C"

@@ -1,5 +1,5 @@
 // kv8_decode.cu -- attention over the 8-bit K/V cache for single tokens (and for
-// the few tokens of a draft): up to 16 query rows (tokens x the query heads of a
+// the few tokens of a draft): up to 16 query rows a launch (tokens x the query heads of a
 // K/V head) against one K/V head of one sequence.
 //
 // Bound: the bytes of the visible K and V, each read once.  Everything else has
@@ -55,6 +55,12 @@ namespace {
 constexpr int KD_STEP = 16;           // positions of a step: the unit of work
 constexpr float KD_SLACK = 8.f;       // how far the maximum may lag (log2)
 constexpr float KD_SHIFT = 6.f;       // weights carry 2^6
+
+// a row of which only the tokens [skip, skip + take) count: it ends behind them
+__device__ __forceinline__ Kv8Row kd_some(const Kv8Row& row, int skip, int take) {
+    const int n = min(max(row.n - skip, 0), take);
+    return Kv8Row{row.t0 + skip, n, max(row.len - max(row.n - skip - n, 0), 0)};
+}
 
 // The steps of a row: its first `sink` steps, then `gap` that no token sees,
 // then the rest; n of them are visible to one of its tokens.
@@ -117,7 +123,11 @@ struct KdRows {
     __device__ __forceinline__ int steps(int chunk) {
         if (chunk != at) {
             const int r = 32 * chunk + lane;
-            n = r < p.c.rows && kv8_row(p.b, cap, r, &row) ? kd_steps(row, p.window, p.sinks).n : 0;
+            n = 0;
+            if (r < p.c.rows && kv8_row(p.b, cap, r, &row)) {
+                if (p.take) row = kd_some(row, p.skip, p.take);
+                n = kd_steps(row, p.window, p.sinks).n;
+            }
             at = chunk;
         }
         return n;
@@ -703,7 +713,22 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
     pdl_trigger();
 }
 
-int decode_sets(const Kv8Attend& p) { return (p.b.max_new * p.G + 7) / 8; }
+// Tokens of a row that a launch takes, and the launches.  A prompt kernel's CTA has 256 query rows, so drafts of a large
+// batch leave most of it idle: there the stream of K and V, read two or three times, is shorter (4 query heads a K/V
+// head; 8 rows x 8k: 8 tokens 75 us in two launches, 106 by the prompt kernel; 16 rows x 32k: 8 tokens 271 and 645, 12
+// tokens 397 in three and 645).  Where few heads let the prompt kernel split the positions over the SMs it is as fast as
+// one launch here (one row x 8k: 8 tokens 23 us, 4 tokens 23.5), and for short caches a launch is what counts
+int decode_tokens(const Kv8Attend& p) { return p.b.max_new * p.G <= 16 ? p.b.max_new : 16 / p.G; }
+int decode_launches(const Kv8Attend& p, int num_sms) {
+    const int each = decode_tokens(p);
+    if (each == p.b.max_new) return 1;
+    if (each == 0 || p.b.max_new > 3 * each) return 0;
+    const long long cap = (long long)p.c.ppr * p.c.page, win = (long long)p.window + p.sinks + p.b.max_new;
+    const long long heads = (long long)p.c.rows * p.c.Hkv;
+    const int n = (p.b.max_new + each - 1) / each;
+    return (win < cap ? win : cap) >= 2048 && (n == 2 ? 3 : 2) * heads >= num_sms ? n : 0;
+}
+int decode_sets(const Kv8Attend& p) { return (decode_tokens(p) * p.G + 7) / 8; }
 
 // one CTA for each place on the GPU, but no more than there can be steps
 int decode_grid(const Kv8Attend& p, int num_sms) {
@@ -735,13 +760,21 @@ cudaError_t launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-bool kv8_decode_takes(const Kv8Attend& p) { return decode_sets(p) <= 2; }
+bool kv8_decode_takes(const Kv8Attend& p, int num_sms) { return decode_launches(p, num_sms) > 0; }
 
 size_t kv8_decode_floats(const Kv8Attend& p, int num_sms) {
     return (size_t)decode_grid(p, num_sms) * 2 * decode_sets(p) * 8 * (p.c.hd + 2);
 }
 
 cudaError_t kv8_decode_launch(const Kv8Attend& p, int num_sms, cudaStream_t s) {
+    const int each = decode_tokens(p);
+    if (!p.take && each < p.b.max_new) {
+        cudaError_t e = cudaSuccess;
+        Kv8Attend some = p;
+        some.take = each;
+        for (; some.skip < p.b.max_new && e == cudaSuccess; some.skip += each) e = kv8_decode_launch(some, num_sms, s);
+        return e;
+    }
     const bool two = decode_sets(p) == 2, fine = p.dtype == W_F32;
     if (p.c.hd == 128) {
         if (fine) return two ? launch<128, 2, true>(p, num_sms, s) : launch<128, 1, true>(p, num_sms, s);

@@ -807,7 +807,7 @@ static cudaError_t pf_attend_kv8(const PrefillState* s, int l, int row, int nt, 
     Kv8Append n{t.c, t.b, s->kv, s->kv + kvd, 2 * kvd, 2 * kvd, W_F32};
     cudaError_t e = kv8_append_launch(n, st);
     if (e != cudaSuccess) return e;
-    e = kv8_decode_takes(t) ? kv8_decode_launch(t, s->num_sms, st) : kv8_prompt_launch(t, s->num_sms, st);
+    e = kv8_decode_takes(t, s->num_sms) ? kv8_decode_launch(t, s->num_sms, st) : kv8_prompt_launch(t, s->num_sms, st);
     if (e != cudaSuccess) return e;
     k_pf_hilo<<<nt, PF_NT, 0, st>>>(s->o, a.Hq * a.hd, s->hb);
     return cudaGetLastError();
@@ -839,7 +839,7 @@ cudaError_t prefill_create(const PrefillArgs& a, int num_sms, PrefillState** out
         size_t most = 1;
         for (int nt = 1; nt <= PF_PASS; ++nt) {
             const Kv8Attend t = pf_kv8(s, 0, 0, nt, a.cap);
-            const size_t n = kv8_decode_takes(t) ? kv8_decode_floats(t, num_sms) : kv8_prompt_floats(t, num_sms);
+            const size_t n = kv8_decode_takes(t, num_sms) ? kv8_decode_floats(t, num_sms) : kv8_prompt_floats(t, num_sms);
             most = n > most ? n : most;
         }
         if ((e = cudaMalloc(&s->kv, sizeof(float) * PF_PASS * 2 * kvd)) != cudaSuccess ||

@@ -466,6 +466,19 @@ def test_many_rows_and_the_smallest():
     assert bool((out[(lens == 0).cuda()] == 0).all())
 
 
+@pytest.mark.parametrize("heads,new,window", [(8, 5, 0), (8, 12, 0), (6, 7, 2100), (10, 6, 0), (8, 13, 0)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_drafts_of_a_large_batch(heads, new, window, dtype):
+    """Drafts of more than 16 query rows, of unequal lengths, idle and short rows among them: 40 rows x 2 heads."""
+    rows = [(7 * r + 2050 if r % 11 == 0 else 13 * r + 1, max(new - r % 4, 1)) for r in range(40)]
+    rows[3], rows[8], rows[9], rows[20] = (0, new), (2, new), (4, 0), (new - 2, new)
+    K, V, table, q, kv_len, starts = build(rows, heads, 2, 64, 64, 32, 91, dtype)
+    c = gpu_cache(K, V, table)
+    out = c.attend(q.cuda(), kv_len.cuda(), starts.cuda(), max_new=new, window=window, sinks=3 if window else 0)
+    c.check()
+    compare(out, rows, K, V, table, q, window or None, 3 if window else 0, dtype)
+
+
 @pytest.mark.parametrize("new", [1, 64])
 def test_repeats_bit_for_bit(new):
     rows = [(3000, new), (10 + new, new), (777, new)]
