@@ -31,7 +31,7 @@
 // (8191 tokens: 602 -> 543 us; K's and V's waits as one: 539).
 //
 // Bound, measured: 8191 tokens 539 us, 53 % of the measured bf16 rate; 2 x 64 fp32
-// tokens over 32k 94 us.  A K/V tile takes about 2200 cycles, of which the tensor
+// tokens over 32k 100 us.  A K/V tile takes about 2200 cycles, of which the tensor
 // core needs 1280 and a softmax warp 1700.  Leaving out half of the MMAs, the
 // exponentials and the maximum, or the loads and conversions, each brings some 20 us,
 // all of them 145: no rate binds it but the chain of a tile's steps -- P to S of the
@@ -65,7 +65,9 @@ constexpr int KP_K_WARP = 8, KP_V_WARP = 12, KP_MMA_WARP = 16, KP_THREADS = 20 *
 constexpr int KP_REGS_SOFTMAX = 120, KP_REGS_CONV = 88, KP_REGS_MMA = 64;
 constexpr int KP_QPANEL = KP_ROWS * 128, KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a query tile, of a K or V tile
 constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
-constexpr int KP_FOLD = 16;               // fp32 q: tiles between two folds of O into memory
+// fp32 q: tiles between two folds of O into memory (64 tokens over 32k, relative error and time: 16 2.5e-6, 95 us; 8
+// 1.4e-6, 98; 6 1.1e-6, 100; 4 0.85e-6, 106.  fp32 sums in the plain order: 2.9e-6, but 0.9e-6 over 1000 positions)
+constexpr int KP_FOLD = 6;
 constexpr int KP_META = 8;                // tiles whose scales are held
 constexpr int KP_GROUPS = KP_KEYS / 16, KP_BATCH = 32 / KP_GROUPS;   // 16-position groups of a tile; tiles that a warp's lanes know of
 constexpr int KP_MARKS = 32;              // words of marks: tile i has bit i % (32 * KP_MARKS)
@@ -497,17 +499,19 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             };
             auto qk = [&](int j) {   // S of tile j, into buffer j & 1
                 const uint32_t kt = kd + (uint32_t)((2 * j) % SLOTS) * (LY::TILE >> 4), scol = sd + 64 * (j & 1);
+                // q's second parts first: the accumulator cuts off what is added, relative to what it holds, and that is little yet
+                if constexpr (FINE)
 #pragma unroll
-                for (int n = 0; n < HD / 64; ++n) {
-                    mma_ss4(scol, qd + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, n > 0);
-                    if constexpr (FINE) mma_ss4(scol, qd + (LY::QTILE >> 4) + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, 1);
-                }
+                    for (int n = 0; n < HD / 64; ++n)
+                        mma_ss4(scol, qd + (LY::QTILE >> 4) + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, n > 0);
+#pragma unroll
+                for (int n = 0; n < HD / 64; ++n) mma_ss4(scol, qd + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, FINE || n > 0);
                 kp_commit(&s_full[2 * xu + (j & 1)]);
             };
             auto pv = [&](int j) {
                 const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * (LY::TILE >> 4), pcol = sd + 64 * (j & 1);
-                mma_ts4(od, pcol, vt, id_o, (uint32_t)(FINE ? j % KP_FOLD > 0 : j > 0));
-                if constexpr (FINE) mma_ts4(od, pcol + 32, vt, id_o, 1);
+                if constexpr (FINE) mma_ts4(od, pcol + 32, vt, id_o, (uint32_t)(j % KP_FOLD > 0));
+                mma_ts4(od, pcol, vt, id_o, FINE ? 1u : (uint32_t)(j > 0));
             };
             auto full = [&](int s) { return wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
             bool ok = full(0);
@@ -563,11 +567,12 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         float4* fold = reinterpret_cast<float4*>(p.ws + kp_part_floats(most, all_rows, HD)) +
                        (fold_tile * most + sp) * (NQ * KP_ROWS * HD / 4) + x * (KP_ROWS * HD / 4) + m;   // + KP_ROWS * (column / 4)
         float M_fold = -INFINITY;   // the maximum that the folded sums refer to
-        auto fold_o = [&](int cc) {   // columns cc .. cc + 63
-            float4 was[16];
+        auto fold_before = [&](int cc, float4 (&was)[16]) {   // columns cc .. cc + 63
             const bool some = live && M_fold != -INFINITY;
 #pragma unroll
             for (int e = 0; e < 16; ++e) was[e] = some ? fold[KP_ROWS * (cc / 4 + e)] : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        auto fold_o = [&](int cc, const float4 (&was)[16]) {
             const float f = M_fold == -INFINITY || M_fold == M ? 1.f : kv8_exp2(M_fold - M);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
@@ -597,10 +602,15 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             const int k0 = key0(i0 + j);
             const bool folds = FINE && j > 0 && j % KP_FOLD == 0;
             if (folds) {   // the next P V starts O anew, after P of this tile is full
+                float4 was[16];
+                fold_before(0, was);   // on their way during the wait
                 if (!(ok = pv_wait(j - 1))) break;
                 fence_after();
 #pragma unroll
-                for (int cc = 0; cc < HD; cc += 64) fold_o(cc);
+                for (int cc = 0; cc < HD; cc += 64) {
+                    if (cc) fold_before(cc, was);
+                    fold_o(cc, was);
+                }
                 M_fold = M;
             }
             uint64_t* const mb = &meta_full[j % KP_META];
