@@ -36,7 +36,7 @@
 // exponentials and the maximum, or the loads and conversions, each brings some 20 us,
 // all of them 145: no rate binds it but the chain of a tile's steps -- P to S of the
 // tile after the next to P again -- and the hand-overs in it.  What did not help:
-// S two tiles ahead, right behind P V (564); 16 softmax warps, two threads a row
+// S two tiles ahead, right behind P V (544); 16 softmax warps, two threads a row
 // (572); one arrival a warp instead of a thread; other shares of the registers.
 //
 // Few tiles and many positions: the positions of a tile are split over several
