@@ -6,38 +6,50 @@
 // every K/V tile and little of a tile lies above the causal diagonal.  Any G
 // works: a tile may begin inside a token.  A CTA has two query tiles, and per 64
 // positions (the one K/V tile that both read):
-//   convert   four warps for K and four for V read the e4m3 bytes (the pages'
-//             own order) a tile ahead, turn them into f16 -- exact -- and store
-//             them as 128-byte-swizzled operand tiles in a ring; page ids and
-//             scales are read a batch of tiles earlier.  V's NaN become 0 (below)
+//   convert   four warps for the even tiles and four for the odd read the e4m3
+//             bytes (the pages' own order) two tiles ahead, turn K into f16 and V
+//             times its scale into bf16 -- both exact -- and store them as
+//             128-byte-swizzled operand tiles in a ring; page ids and scales are
+//             read a batch of tiles earlier.  V's NaN become 0 (below)
 //   S = Q K^T tcgen05.mma kind::f16, A = Q, B = K, D in TMEM; two S buffers for
 //             each query tile, so the product runs a tile ahead of the softmax
-//   softmax   a thread owns a row: scores times K's scale, V's exponent added
-//             (weights are relative to the largest weight * V scale, the sum
-//             divides V's exponent out again), running maximum kept within 2^8,
-//             weights as f16 back into TMEM over the scores they came from
-//   O += P V  A = P from TMEM, B = V read MN-major
+//   softmax   a thread owns a row: scores times K's scale, running maximum kept
+//             within 2^8, weights as two bf16 parts (16 bits and more, with fp32's
+//             range) back into TMEM over the scores they came from
+//   O += P V  A = P from TMEM, B = V read MN-major, in bf16
+// The largest weight may belong to a position whose V is 0 in a dim, and V's scales
+// may lie far apart, so small weights have to keep their digits: f16 holds 20 bits
+// below the largest, bf16 what fp32 does.  It has 8 bits where f16 has 11, hence two
+// parts for a weight, and that is what bf16 prompts pay for it (8191 tokens: one
+// f16 part 540 us, two bf16 parts 620; the second product itself costs 15 of them).
 // 64 positions rather than 128: with 128 there is room for one S a query tile,
 // and product and softmax wait for one another (8191 tokens: 682 -> 633 us with
 // the change, although S = Q K^T of 64 columns reads Q from shared memory twice as
 // often and takes 48 cycles where 32 would do).
-// With fp32 q, q and the weights enter as two f16 parts each; the parts of P lie
-// side by side over their scores.  The tensor core's accumulator cuts off what it
-// adds, so O is folded into memory in rounded sums every KP_FOLD tiles.
+// With fp32 q, q enters as two f16 parts and the weights as three bf16 parts (two:
+// relative error 2.6e-6, three: 1.2e-6).  Two parts of P lie side by side over their
+// scores, the third in TMEM (64 dims) or in shared memory (128: TMEM is full).  The
+// tensor core's accumulator cuts off what it adds, so O is folded into memory in
+// rounded sums every KP_FOLD tiles.
 //
 // Each query tile has its own issuing warp: a wait costs its trip through a busy
 // shared memory (about 250 cycles) even where nothing is left to wait for, and
 // with one warp for both tiles those trips, not the products, filled its time
 // (8191 tokens: 602 -> 543 us; K's and V's waits as one: 539).
 //
-// Bound, measured: 8191 tokens 539 us, 53 % of the measured bf16 rate; 2 x 64 fp32
-// tokens over 32k 100 us.  A K/V tile takes about 2200 cycles, of which the tensor
-// core needs 1280 and a softmax warp 1700.  Leaving out half of the MMAs, the
-// exponentials and the maximum, or the loads and conversions, each brings some 20 us,
-// all of them 145: no rate binds it but the chain of a tile's steps -- P to S of the
-// tile after the next to P again -- and the hand-overs in it.  What did not help:
-// S two tiles ahead, right behind P V (544); 16 softmax warps, two threads a row
-// (572); one arrival a warp instead of a thread; other shares of the registers.
+// Bound, measured: 8191 tokens 620 us, 46 % of the measured bf16 rate; 2 x 64 fp32
+// tokens over 32k 109 us.  The chain of a tile's steps binds it -- P to S of the
+// tile after the next to P again -- and the hand-overs in it.  With one f16 part a
+// weight (540 us) a K/V tile took about 2200 cycles, of which the tensor core needed
+// 1280 (now 1790) and a softmax warp 1700.  Leaving out half of the MMAs, the
+// exponentials and the maximum, or the loads and conversions, brought some 20 us
+// each, all of them 145.  What did not help then: S two tiles ahead, right behind
+// P V (544); 16 softmax warps, two threads a row (572); one arrival a warp instead
+// of a thread; other shares of the registers.
+// V's conversion is eight instructions for two values where f16 took one.  With K
+// and V in four warps each, V's warps, which also wait for their loads, could not
+// follow the tiles (800 us); with a tile's K and V in the same warps, every other
+// tile each, they do.
 //
 // Few tiles and many positions: the positions of a tile are split over several
 // CTAs (a host rule on sizes) and joined by a second kernel in split order.
@@ -59,14 +71,14 @@ namespace {
 
 constexpr int KP_ROWS = 128;              // query rows of a tile: TMEM lanes
 constexpr int KP_KEYS = 64;               // positions of a tile
-// 8 softmax warps, 4 that convert K, 4 that convert V, 2 that issue MMAs and 2 that only pad their warpgroup
-constexpr int KP_K_WARP = 8, KP_V_WARP = 12, KP_MMA_WARP = 16, KP_THREADS = 20 * 32;
+// 8 softmax warps, 8 that convert K and V, 2 that issue MMAs and 2 that only pad their warpgroup
+constexpr int KP_CONV_WARP = 8, KP_MMA_WARP = 16, KP_THREADS = 20 * 32;
 // registers a thread by role (setmaxnreg): 640 threads x 96 at launch = 256 x 120 + 256 x 88 + 128 x 64
 constexpr int KP_REGS_SOFTMAX = 120, KP_REGS_CONV = 88, KP_REGS_MMA = 64;
 constexpr int KP_QPANEL = KP_ROWS * 128, KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a query tile, of a K or V tile
-constexpr float KP_SLACK = 8.f, KP_SHIFT = 6.f;   // log2: maximum may lag, weights carry 2^6
-// fp32 q: tiles between two folds of O into memory (64 tokens over 32k, relative error and time: 16 2.5e-6, 95 us; 8
-// 1.4e-6, 98; 6 1.1e-6, 100; 4 0.85e-6, 106.  fp32 sums in the plain order: 2.9e-6, but 0.9e-6 over 1000 positions)
+constexpr float KP_SLACK = 8.f, KP_SHIFT = -8.f;   // log2: maximum may lag; weights carry 2^-8, so none is above 1
+// fp32 q: tiles between two folds of O into memory (64 tokens over 32k, relative error and time: 12 2.2e-6, 101 us; 8
+// 1.6e-6, 106; 6 1.2e-6, 109.  fp32 sums in the plain order: 2.9e-6, but 0.9e-6 over 2000 positions)
 constexpr int KP_FOLD = 6;
 constexpr int KP_META = 8;                // tiles whose scales are held
 constexpr int KP_GROUPS = KP_KEYS / 16, KP_BATCH = 32 / KP_GROUPS;   // 16-position groups of a tile; tiles that a warp's lanes know of
@@ -77,9 +89,13 @@ struct KpLayout {
     static constexpr int PARTS = FINE ? 2 : 1;
     static constexpr int QTILE = HD / 64 * KP_QPANEL, TILE = HD / 64 * KP_PANEL;   // bytes of f16 operand tiles
     static constexpr int SLOTS = HD == 128 && FINE ? 4 : 8;                         // K and V tiles in turn
-    static constexpr int Q = 0, KV = 2 * PARTS * QTILE, BYTES = KV + SLOTS * TILE;
-    // TMEM columns: S of query tile x, buffer b at 128 x + 64 b (P lies over it), O of query tile x at 256 + HD x
-    static constexpr int O = 256;
+    // fp32 q, the weights' third parts: TMEM has room for them beside 64 dims, else a tile in shared memory
+    static constexpr bool THIRD_TMEM = FINE && HD == 64, THIRD_SMEM = FINE && HD == 128;
+    static constexpr int PTILE = THIRD_SMEM ? KP_QPANEL : 0;
+    static constexpr int Q = 0, KV = 2 * PARTS * QTILE, P3 = KV + SLOTS * TILE, BYTES = P3 + 2 * PTILE;
+    // TMEM columns: S of query tile x, buffer b at 128 x + 64 b (P lies over it), O of query tile x at 256 + HD x, third
+    // parts at 384 + 64 x + 32 b
+    static constexpr int O = 256, THIRD = 384;
 };
 template <int HD, bool FINE>
 constexpr int kp_smem() { return KpLayout<HD, FINE>::BYTES + 1024; }
@@ -92,9 +108,9 @@ __device__ __forceinline__ uint32_t kp_sw(int r, int c) {
 // between panels (both in 16 bytes), the high word is the same for all
 __device__ __forceinline__ uint32_t kp_desc(uint32_t saddr, uint32_t lbo) { return ((saddr & 0x3FFFFu) >> 4) | (lbo >> 4) << 16; }
 constexpr uint32_t KP_DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
-// kind::f16, f16 A and B, fp32 D
-constexpr uint32_t kp_idesc(int N, bool b_mn) {
-    return (1u << 4) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(KP_ROWS >> 4) << 24);
+// kind::f16, fp32 D; Q K^T: f16 A and B, both K-major; P V: bf16 A and B, B MN-major
+constexpr uint32_t kp_idesc(int N, bool pv) {
+    return (1u << 4) | (pv ? 1u << 7 | 1u << 10 | 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(KP_ROWS >> 4) << 24);
 }
 // One thread issues every MMA of a query tile, so what it does for each lies on the tensor core's path.  The whole warp
 // runs the issuing code, every lane has the operands, and each run of four MMAs (four steps of 16) or commit elects the
@@ -119,6 +135,17 @@ __device__ __forceinline__ void mma_ts4(uint32_t d, uint32_t a, uint32_t b, uint
                  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n add.u32 a, a, 8;\n add.u64 y, y, 128;\n"
                  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n add.u32 a, a, 8;\n add.u64 y, y, 128;\n"
                  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(KP_DESC_HI),
+                 "r"(idesc), "r"(acc)
+                 : "memory");
+}
+// the same with A in shared memory
+__device__ __forceinline__ void mma_st4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile("{\n .reg .pred e, p, t;\n .reg .b64 x, y;\n setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n"
+                 " mov.b64 x, {%1, %3};\n mov.b64 y, {%2, %3};\n elect.sync _|e, 0xffffffff;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n add.u64 x, x, 2;\n add.u64 y, y, 128;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n add.u64 x, x, 2;\n add.u64 y, y, 128;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n add.u64 x, x, 2;\n add.u64 y, y, 128;\n"
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, t;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(KP_DESC_HI),
                  "r"(idesc), "r"(acc)
                  : "memory");
 }
@@ -161,11 +188,36 @@ __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
     return r;
 }
 __device__ __forceinline__ float2 unpack_h2(uint32_t w) { return __half22float2(*reinterpret_cast<__half2*>(&w)); }
+__device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// Four e4m3 values times 2^e as packed bf16 pairs, exact: 4 significant bits, fp32's exponents (e is at most 118, or 448
+// would become an infinity, and NaN times a weight of 0).  A byte s eeee mmm, moved to s 0000 eeee mmm 0000, is the bf16 of
+// its value times 2^-120, subnormals too.  2^(e + 120) passes the range, so it is two factors
+struct KpScale {
+    __nv_bfloat162 a, b;
+    __device__ __forceinline__ explicit KpScale(int e) {
+        const int n = min(e, 118) + 120, h = n >> 1;
+        a = __float2bfloat162_rn(pow2i(h));
+        b = __float2bfloat162_rn(pow2i(n - h));
+    }
+    __device__ __forceinline__ uint32_t two(uint32_t x) const {   // bytes in the high halves
+        const uint32_t w = (x & 0x7F007F00u) >> 4 | (x & 0x80008000u);
+        const __nv_bfloat162 y = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&w), a), b);
+        return *reinterpret_cast<const uint32_t*>(&y);
+    }
+    __device__ __forceinline__ void widen(uint32_t w, uint32_t& lo, uint32_t& hi) const {
+        lo = two(__byte_perm(w, 0u, 0x1404));
+        hi = two(__byte_perm(w, 0u, 0x3424));
+    }
+};
 __device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u; }
 
-// what 16 positions of a tile contribute besides their bytes
-struct __align__(16) KpMeta {
-    float kf, ve, vinv, pad;   // 2^K exponent, V's exponent (-inf: nothing there), 2^-V exponent
+// what the scores of 16 positions of a tile need
+struct __align__(8) KpMeta {
+    float kf, add;   // 2^K exponent; 0, or -inf where nothing is held
 };
 
 // every warp of the CTA, each from its own role
@@ -371,115 +423,129 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         *ab = 1;
         atomicOr(p.b.err, FAULT_WAIT);
     };
-    if (warp >= KP_K_WARP && warp < KP_MMA_WARP) {
-        // ---- K or V tiles: global e4m3 -> f16 operand tiles ----
+    if (warp >= KP_CONV_WARP && warp < KP_MMA_WARP) {
+        // ---- K and V tiles: global e4m3 -> operand tiles, K in f16, V times its scale in bf16 ----
         regs_down<KP_REGS_CONV>();
         constexpr int KU = KP_KEYS / 32, LOADS = KU * (HD / 64);   // 16-byte loads of a thread: keys quad + 32 u of each panel
-        auto convert = [&](auto is_v) {
-            constexpr bool V = decltype(is_v)::value;
-            const uint8_t* pool = V ? c.v : c.k;
-            const int ct = tid & 127, quad = ct >> 2, q4 = ct & 3;
-            const size_t in_group = (size_t)(quad & 15) * HD + q4 * 16;
-            // KP_BATCH tiles at a time, lane KP_GROUPS i + g knows of the 16 positions g of tile i: where they begin in the pool, in
-            // 16 rows (-1: nowhere), and their scale bytes.  Both are read a batch ahead -- the page ids first, the
-            // scales two tiles later -- so that no tile waits for them
-            const int nb = c.page / c.block;
-            int at = -1, at_next = -1, scales = 0, scales_next = 0;   // K's byte, V's << 8
-            long long scale_at = 0;
-            auto pages_ahead = [&](int j) {    // the batch that begins with tile j of this CTA
-                const int i = i0 + j + lane / KP_GROUPS;
-                at_next = -1;
-                if (i >= i1) return;
-                const int kb = key0(i) + 16 * (lane % KP_GROUPS);
-                if (kb >= tl.end || (kb + 15 < tl.low && kb >= p.sinks)) return;
-                const int slot = kb / c.page, off = kb - slot * c.page, page = kv8_page(c, p.b.err, r, slot);
-                if (page < 0) return;
-                const long long head = (long long)page * c.Hkv + h;
-                at_next = (int)((head * c.page + off) / 16);
-                if (!V) scale_at = head * nb + off / c.block;
-            };
-            auto scales_ahead = [&]() {
-                if (!V && at_next >= 0) scales_next = (int)c.ks[scale_at] | (int)c.vs[scale_at] << 8;
-            };
-            uint4 v[LOADS];
-            auto load = [&](int j, int rows) {   // tile j, in rows' batch
+        const int grp = (warp - KP_CONV_WARP) / 4, ct = tid & 127, quad = ct >> 2, q4 = ct & 3;   // four warps have the even tiles, four the odd
+        const size_t in_group = (size_t)(quad & 15) * HD + q4 * 16;
+        // KP_BATCH tiles at a time, lane KP_GROUPS i + g knows of the 16 positions g of tile i: where they begin in the pool, in
+        // 16 rows (-1: nowhere), and their scale bytes.  Both are read a batch ahead -- the page ids first, the
+        // scales two tiles later -- so that no tile waits for them
+        const int nb = c.page / c.block;
+        int at = -1, at_next = -1, scales = 0, scales_next = 0;   // K's byte, V's << 8
+        long long scale_at = 0;
+        auto pages_ahead = [&](int j) {    // the batch that begins with tile j of this CTA
+            const int i = i0 + j + lane / KP_GROUPS;
+            at_next = -1;
+            if (i >= i1) return;
+            const int kb = key0(i) + 16 * (lane % KP_GROUPS);
+            if (kb >= tl.end || (kb + 15 < tl.low && kb >= p.sinks)) return;
+            const int slot = kb / c.page, off = kb - slot * c.page, page = kv8_page(c, p.b.err, r, slot);
+            if (page < 0) return;
+            const long long head = (long long)page * c.Hkv + h;
+            at_next = (int)((head * c.page + off) / 16);
+            scale_at = head * nb + off / c.block;
+        };
+        auto scales_ahead = [&]() {
+            if (at_next >= 0) scales_next = (int)c.ks[scale_at] | (int)c.vs[scale_at] << 8;
+        };
+        uint4 k[LOADS], v[LOADS];
+        auto load = [&](int j) {   // tile j, in the batch of `at`
 #pragma unroll
-                for (int u = 0; u < KU; ++u) {
-                    const int b = __shfl_sync(0xffffffffu, rows, j % KP_BATCH * KP_GROUPS + 2 * u + (quad >> 4));
-                    const uint4* src = reinterpret_cast<const uint4*>(pool + (size_t)b * (16 * HD) + in_group);
+            for (int u = 0; u < KU; ++u) {
+                const int b = __shfl_sync(0xffffffffu, at, j % KP_BATCH * KP_GROUPS + 2 * u + (quad >> 4));
+                const size_t from = (size_t)b * (16 * HD) + in_group;
 #pragma unroll
-                    for (int n = 0; n < HD / 64; ++n) v[n * KU + u] = b >= 0 ? __ldg(src + 4 * n) : make_uint4(0u, 0u, 0u, 0u);
+                for (int n = 0; n < HD / 64; ++n) {
+                    k[n * KU + u] = b >= 0 ? __ldg(reinterpret_cast<const uint4*>(c.k + from) + 4 * n) : make_uint4(0u, 0u, 0u, 0u);
+                    v[n * KU + u] = b >= 0 ? __ldg(reinterpret_cast<const uint4*>(c.v + from) + 4 * n) : make_uint4(0u, 0u, 0u, 0u);
                 }
-            };
-            if (ntiles > 0) {
-                pages_ahead(0);
-                scales_ahead();
-                at = at_next;
-                scales = scales_next;
-                load(0, at);
-            }
-            for (int j = 0; j < ntiles; ++j) {
-                if (j % KP_BATCH == 0) pages_ahead(j + KP_BATCH);
-                if (j % KP_BATCH == 2) scales_ahead();
-                if (!V && warp == KP_K_WARP) {
-                    if (lane / KP_GROUPS == j % KP_BATCH) {
-                        const int ve = (scales >> 8) - 127;
-                        // the last reader of this entry, the softmax of tile j - KP_META, is done: the ring is shorter
-                        meta[j % KP_META][lane % KP_GROUPS] = at >= 0 ? KpMeta{pow2i((scales & 255) - 127), (float)ve, pow2i(-ve), 0.f}
-                                                              : KpMeta{1.f, -INFINITY, 0.f, 0.f};
-                    }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&meta_full[j % KP_META]);
-                }
-                if (V) {
-                    // V's NaN stay out of the product; those at positions that a row of the CTA sees are marked
-                    uint32_t bad = 0u;
-#pragma unroll
-                    for (int u = 0; u < LOADS; ++u) bad |= nan_bytes(v[u].x) | nan_bytes(v[u].y) | nan_bytes(v[u].z) | nan_bytes(v[u].w);
-                    if (bad) {
-                        bool seen = false;
-#pragma unroll
-                        for (int u = 0; u < LOADS; ++u) {
-                            const uint32_t n[4] = {nan_bytes(v[u].x), nan_bytes(v[u].y), nan_bytes(v[u].z), nan_bytes(v[u].w)};
-                            const int key = key0(i0 + j) + quad + 32 * (u % KU);
-                            if ((n[0] | n[1] | n[2] | n[3]) && key < tl.end && (key >= tl.low || key < p.sinks)) seen = true;
-                            v[u].x &= ~((n[0] >> 7) * 0xFFu);
-                            v[u].y &= ~((n[1] >> 7) * 0xFFu);
-                            v[u].z &= ~((n[2] >> 7) * 0xFFu);
-                            v[u].w &= ~((n[3] >> 7) * 0xFFu);
-                        }
-                        if (seen) {
-                            atomicOr(&marks[(i0 + j) / 32 % KP_MARKS], 1u << ((i0 + j) & 31));
-                            marked = 1;
-                        }
-                    }
-                }
-                const int s = 2 * j + (V ? 1 : 0);   // slot number, K and V in turn
-                if (s >= SLOTS && !warp_wait(&kv_empty[s % SLOTS], (uint32_t)(s / SLOTS - 1) & 1u, ab, p.b.err)) break;
-                unsigned char* tile = sm + LY::KV + (s % SLOTS) * LY::TILE;
-#pragma unroll
-                for (int u = 0; u < LOADS; ++u) {
-                    uint32_t a[4], b[4];
-                    e4m3x4_to_f16(v[u].x, a[0], a[1]);
-                    e4m3x4_to_f16(v[u].y, a[2], a[3]);
-                    e4m3x4_to_f16(v[u].z, b[0], b[1]);
-                    e4m3x4_to_f16(v[u].w, b[2], b[3]);
-                    unsigned char* d = tile + u / KU * KP_PANEL;
-                    *reinterpret_cast<uint4*>(d + kp_sw(quad + 32 * (u % KU), 2 * q4)) = make_uint4(a[0], a[1], a[2], a[3]);
-                    *reinterpret_cast<uint4*>(d + kp_sw(quad + 32 * (u % KU), 2 * q4 + 1)) = make_uint4(b[0], b[1], b[2], b[3]);
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&kv_full[s % SLOTS]);
-                const bool turn = j % KP_BATCH == KP_BATCH - 1;   // tile j + 1 lies in the next batch
-                if (turn) {
-                    at = at_next;
-                    scales = scales_next;
-                }
-                if (j + 1 < ntiles) load(j + 1, at);
             }
         };
-        if (warp < KP_V_WARP) convert(std::false_type{});
-        else convert(std::true_type{});
+        auto slot = [&](int s) -> unsigned char* {   // null: the wait for it gave up
+            if (s >= SLOTS && !warp_wait(&kv_empty[s % SLOTS], (uint32_t)(s / SLOTS - 1) & 1u, ab, p.b.err)) return nullptr;
+            return sm + LY::KV + (s % SLOTS) * LY::TILE;
+        };
+        auto put = [&](unsigned char* tile, int u, int half, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+            *reinterpret_cast<uint4*>(tile + u / KU * KP_PANEL + kp_sw(quad + 32 * (u % KU), 2 * q4 + half)) = make_uint4(x, y, z, w);
+        };
+        if (ntiles > grp) {
+            pages_ahead(0);
+            scales_ahead();
+            at = at_next;
+            scales = scales_next;
+            load(grp);
+        }
+        for (int j = grp; j < ntiles; j += 2) {
+            const int in_batch = j % KP_BATCH;
+            if (in_batch == grp) pages_ahead(j - grp + KP_BATCH);
+            if (in_batch == 2 + grp) scales_ahead();
+            unsigned char* tile = slot(2 * j);   // K and V tiles in turn
+            if (!tile) break;
+            if (ct < 32) {   // the last reader of this entry, the softmax of tile j - KP_META, is done: the ring is shorter
+                if (lane / KP_GROUPS == in_batch)
+                    meta[j % KP_META][lane % KP_GROUPS] = at >= 0 ? KpMeta{pow2i((scales & 255) - 127), 0.f} : KpMeta{1.f, -INFINITY};
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&meta_full[j % KP_META]);
+            }
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) {
+                uint32_t a[4], b[4];
+                e4m3x4_to_f16(k[u].x, a[0], a[1]);
+                e4m3x4_to_f16(k[u].y, a[2], a[3]);
+                e4m3x4_to_f16(k[u].z, b[0], b[1]);
+                e4m3x4_to_f16(k[u].w, b[2], b[3]);
+                put(tile, u, 0, a[0], a[1], a[2], a[3]);
+                put(tile, u, 1, b[0], b[1], b[2], b[3]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&kv_full[2 * j % SLOTS]);
+            // V's NaN stay out of the product; those at positions that a row of the CTA sees are marked
+            uint32_t bad = 0u;
+#pragma unroll
+            for (int u = 0; u < LOADS; ++u) bad |= nan_bytes(v[u].x) | nan_bytes(v[u].y) | nan_bytes(v[u].z) | nan_bytes(v[u].w);
+            if (bad) {
+                bool seen = false;
+#pragma unroll
+                for (int u = 0; u < LOADS; ++u) {
+                    const uint32_t n[4] = {nan_bytes(v[u].x), nan_bytes(v[u].y), nan_bytes(v[u].z), nan_bytes(v[u].w)};
+                    const int key = key0(i0 + j) + quad + 32 * (u % KU);
+                    if ((n[0] | n[1] | n[2] | n[3]) && key < tl.end && (key >= tl.low || key < p.sinks)) seen = true;
+                    v[u].x &= ~((n[0] >> 7) * 0xFFu);
+                    v[u].y &= ~((n[1] >> 7) * 0xFFu);
+                    v[u].z &= ~((n[2] >> 7) * 0xFFu);
+                    v[u].w &= ~((n[3] >> 7) * 0xFFu);
+                }
+                if (seen) {
+                    atomicOr(&marks[(i0 + j) / 32 % KP_MARKS], 1u << ((i0 + j) & 31));
+                    marked = 1;
+                }
+            }
+            if (!(tile = slot(2 * j + 1))) break;
+#pragma unroll
+            for (int u = 0; u < KU; ++u) {
+                const KpScale s((__shfl_sync(0xffffffffu, scales, in_batch * KP_GROUPS + 2 * u + (quad >> 4)) >> 8) - 127);
+#pragma unroll
+                for (int n = 0; n < HD / 64; ++n) {
+                    uint32_t a[4], b[4];
+                    const uint4 w = v[n * KU + u];
+                    s.widen(w.x, a[0], a[1]);
+                    s.widen(w.y, a[2], a[3]);
+                    s.widen(w.z, b[0], b[1]);
+                    s.widen(w.w, b[2], b[3]);
+                    put(tile, n * KU + u, 0, a[0], a[1], a[2], a[3]);
+                    put(tile, n * KU + u, 1, b[0], b[1], b[2], b[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&kv_full[(2 * j + 1) % SLOTS]);
+            if (in_batch == KP_BATCH - 2 + grp) {   // tile j + 2 lies in the next batch
+                at = at_next;
+                scales = scales_next;
+            }
+            if (j + 2 < ntiles) load(j + 2);
+        }
         cta_meet();
     } else if (warp >= KP_MMA_WARP) {
         // ---- MMA issuers: a warp for each query tile, so that one's waits do not hold up the other's products ----
@@ -500,18 +566,22 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             auto qk = [&](int j) {   // S of tile j, into buffer j & 1
                 const uint32_t kt = kd + (uint32_t)((2 * j) % SLOTS) * (LY::TILE >> 4), scol = sd + 64 * (j & 1);
                 // q's second parts first: the accumulator cuts off what is added, relative to what it holds, and that is little yet
-                if constexpr (FINE)
+                if constexpr (FINE) {
 #pragma unroll
                     for (int n = 0; n < HD / 64; ++n)
                         mma_ss4(scol, qd + (LY::QTILE >> 4) + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, n > 0);
+                }
 #pragma unroll
                 for (int n = 0; n < HD / 64; ++n) mma_ss4(scol, qd + n * (KP_QPANEL >> 4), kt + n * (KP_PANEL >> 4), id_s, FINE || n > 0);
                 kp_commit(&s_full[2 * xu + (j & 1)]);
             };
             auto pv = [&](int j) {
                 const uint32_t vt = vd + (uint32_t)((2 * j + 1) % SLOTS) * (LY::TILE >> 4), pcol = sd + 64 * (j & 1);
-                if constexpr (FINE) mma_ts4(od, pcol + 32, vt, id_o, (uint32_t)(j % KP_FOLD > 0));
-                mma_ts4(od, pcol, vt, id_o, FINE ? 1u : (uint32_t)(j > 0));
+                const uint32_t acc = (FINE ? j % KP_FOLD : j) > 0;
+                if constexpr (LY::THIRD_TMEM) mma_ts4(od, dtu + LY::THIRD + 64 * xu + 32 * (j & 1), vt, id_o, acc);
+                if constexpr (LY::THIRD_SMEM) mma_st4(od, kp_desc(smem_u32(sm + LY::P3), 16) + xu * (LY::PTILE >> 4), vt, id_o, acc);
+                mma_ts4(od, pcol + 32, vt, id_o, FINE ? 1u : acc);
+                mma_ts4(od, pcol, vt, id_o, 1u);
             };
             auto full = [&](int s) { return wait(&kv_full[s % SLOTS], (uint32_t)(s / SLOTS) & 1u); };
             bool ok = full(0);
@@ -637,7 +707,7 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                     for (int e = 0; e < 32; ++e) v[q][e] = see >> e & 1u ? v[q][e] : 0xFF800000u;
                 }
             }
-            float mul[KP_GROUPS], ve[KP_GROUPS], top = -INFINITY;
+            float mul[KP_GROUPS], add[KP_GROUPS], top = -INFINITY;
 #pragma unroll
             for (int b = 0; b < KP_GROUPS; ++b) {
                 auto f = [&](int e) { return __uint_as_float(v[b / 2][b % 2 * 16 + e]); };
@@ -645,8 +715,8 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 const float t3 = max3(f(9), f(10), f(11)), t4 = max3(f(12), f(13), f(14));
                 const float2 k = *reinterpret_cast<const float2*>(&mt[b]);
                 mul[b] = kp_mul(fac, k.x);
-                ve[b] = k.y;
-                top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), mul[b], ve[b]));
+                add[b] = k.y;
+                top = fmaxf(top, fmaf(fmaxf(max3(t0, t1, t2), max3(t3, t4, f(15))), mul[b], add[b]));
             }
             float alpha = 1.f;
             if (top > M + KP_SLACK) {
@@ -654,8 +724,10 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 M = top;
                 l *= alpha;
             }
-            if (j > 0 && !folds && __any_sync(0xffffffffu, alpha != 1.f)) {
+            bool waited = j == 0 || folds;   // for P V of tile j - 1
+            if (!waited && __any_sync(0xffffffffu, alpha != 1.f)) {
                 if (!(ok = pv_wait(j - 1))) break;
+                waited = true;
                 fence_after();
 #pragma unroll 1
                 for (int cc = 0; cc < HD; cc += 16) {
@@ -668,13 +740,14 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 }
             }
             const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
+            const uint64_t minus2 = pair(-1.f, -1.f);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-                uint32_t hi[16], low[FINE ? 16 : 1];
+                uint32_t hi[16], low[16], third[FINE ? 16 : 1];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float mu = mul[2 * q + b], add = ve[2 * q + b] - sub;
-                    const uint64_t mul2 = pair(mu, mu), plus2 = pair(add, add);
+                    const float mu = mul[2 * q + b], plus = add[2 * q + b] - sub;
+                    const uint64_t mul2 = pair(mu, mu), plus2 = pair(plus, plus);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
@@ -687,19 +760,32 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                         else if (e & 2) sum1 = add2(sum1, pair(w0, w1));
                         else sum0 = add2(sum0, pair(w0, w1));
                         const int d = 8 * b + e / 2;
-                        hi[d] = pack_h2(w0, w1);
+                        hi[d] = pack_b2(w0, w1);
+                        float r0, r1;
+                        unpair(fma2(pair(__uint_as_float(hi[d] << 16), __uint_as_float(hi[d] & 0xFFFF0000u)), minus2, pair(w0, w1)), r0, r1);
+                        low[d] = pack_b2(r0, r1);
                         if constexpr (FINE) {
-                            const float2 g = unpack_h2(hi[d]);
-                            low[d] = pack_h2(w0 - g.x, w1 - g.y);
+                            unpair(fma2(pair(__uint_as_float(low[d] << 16), __uint_as_float(low[d] & 0xFFFF0000u)), minus2, pair(r0, r1)), r0, r1);
+                            third[d] = pack_b2(r0, r1);
                         }
                     }
                     float a0, a1;
                     unpair(add2(sum0, sum1), a0, a1);
-                    l = fmaf(a0 + a1, mt[2 * q + b].vinv, l);
+                    l += a0 + a1;
                 }
                 tm_st16(scol + 16 * q, hi);   // over the scores, which this thread holds
-                if constexpr (FINE) tm_st16(scol + 32 + 16 * q, low);
+                tm_st16(scol + 32 + 16 * q, low);
+                if constexpr (LY::THIRD_TMEM) tm_st16(lrow + LY::THIRD + 64 * x + 32 * (j & 1) + 16 * q, third);
+                if constexpr (LY::THIRD_SMEM) {
+                    if (q == 0 && !waited && !(ok = pv_wait(j - 1))) break;   // that read the third parts of its tile
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        *reinterpret_cast<uint4*>(sm + LY::P3 + x * LY::PTILE + kp_sw(m, 4 * q + e)) =
+                            make_uint4(third[4 * e], third[4 * e + 1], third[4 * e + 2], third[4 * e + 3]);
+                }
             }
+            if (!ok) break;
+            if constexpr (LY::THIRD_SMEM) fence_proxy_async_smem();
             wait_st();
             fence_before();
             mbar_arrive(&p_full[2 * x + (j & 1)]);

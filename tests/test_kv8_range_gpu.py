@@ -1,0 +1,113 @@
+"""Attention over the 8-bit K/V cache where softmax weights, and the scales of V's blocks, lie far apart: the definition
+in 64 bits holds relative to sum p |v| of each dim, however small the weights are beside the largest."""
+import math
+
+import pytest
+import torch
+
+from test_kv8_gpu import BF16, F32, build, compare, gpu_cache
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(rows, heads, kv_heads, dim, dtype, change, window=0, sinks=0):
+    K, V, table, q, kv_len, starts = build(rows, heads, kv_heads, dim, 64, 16, 17, dtype)
+    change(K, V, table, q)
+    cache = gpu_cache(K, V, table)
+    out = cache.attend(q.cuda(), kv_len.cuda(), starts.cuda(), max_new=max(n for _, n in rows), window=window, sinks=sinks)
+    cache.check()
+    compare(out, rows, K, V, table, q, window, sinks, dtype)
+
+
+SHAPES = [([(70, 40)], 64), ([(1500, 60), (300, 60)], 128), ([(900, 300)], 64)]
+IDS = ["chunk", "chunks", "prompt"]
+
+
+def dominant(at, gap, zero=True):
+    """Position `at` of each row scores `gap` nats above 0 for every query, the rest of its block 0; its V is zero."""
+    def change(K, V, table, q):
+        q[..., 0] = 8.0
+        for r in range(table.shape[0]):
+            page, off = table[r, at // 64].long(), at % 64
+            first = off // 16 * 16
+            K.x[page, :, first:first + 16] = 0.0
+            K.e[page, :, off // 16] = -2
+            # 8 * x * 2^-2 / sqrt(dim) = gap
+            K.x[page, :, off, 0] = float(torch.tensor(gap * math.sqrt(q.shape[2]) / 2).to(torch.float8_e4m3fn))
+            if zero:
+                V.x[page, :, off] = 0.0
+    return change
+
+
+@pytest.mark.parametrize("gap", [10, 14, 18, 22, 40, 60])
+@pytest.mark.parametrize("rows,dim", SHAPES, ids=IDS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_dominant_first_position_without_values(gap, rows, dim, dtype):
+    """What the others contribute is all there is: weights of e^-gap and below."""
+    attend(rows, 4, 2, dim, dtype, dominant(0, gap))
+
+
+@pytest.mark.parametrize("gap", [18, 40])
+@pytest.mark.parametrize("at", [17, 29])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_dominant_position_among_the_others(gap, at, dtype):
+    """The dominant position is neither the first of its row nor of its tile; with a window that leaves it as a sink."""
+    attend([(900, 50)], 8, 2, 64, dtype, dominant(at, gap))
+    attend([(900, 50)], 8, 2, 64, dtype, dominant(at, gap), window=400, sinks=30)
+
+
+@pytest.mark.parametrize("spread", [11, 17, 24, 40, 90])
+@pytest.mark.parametrize("rows,dim", SHAPES, ids=IDS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_outlier_channels(spread, rows, dim, dtype):
+    """Blocks of a V scale 2^spread above the others', whose tokens are zero in all dims but one."""
+    def change(K, V, table, q):
+        V.e[:] = -30
+        for b in (0, 2):   # of each page: two of its four blocks
+            V.e[:, :, b] = -30 + spread
+            here = V.x[:, :, 16 * b:16 * b + 16]
+            seen = ~torch.isnan(here)
+            seen[..., 5] = False
+            here[seen] = 0.0
+    attend(rows, 4, 2, dim, dtype, change)
+
+
+@pytest.mark.parametrize("spread", [17, 40, 90, 200])
+@pytest.mark.parametrize("rows,dim", SHAPES, ids=IDS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_outlier_channels_in_every_fifth_block(spread, rows, dim, dtype):
+    """As above, in an order that gives each warp of a kernel blocks of both kinds."""
+    def change(K, V, table, q):
+        K.e.clamp_(max=-6)
+        V.e[:] = -(spread // 2)
+        for r in range(table.shape[0]):
+            for b in range(0, 4 * table.shape[1], 5):
+                page = table[r, b // 4].long()
+                V.e[page, :, b % 4] += spread
+                here = V.x[page, :, 16 * (b % 4):16 * (b % 4) + 16]
+                seen = ~torch.isnan(here)
+                seen[..., 5] = False
+                here[seen] = 0.0
+    attend(rows, 4, 2, dim, dtype, change)
+
+
+@pytest.mark.parametrize("new", [1, 2, 40])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_every_byte_of_v(new, dtype):
+    """A token that sees one position gets its V: all finite e4m3 values, zeros and subnormals among them."""
+    from graph_replay_gb300 import KV8Cache
+    length = 256
+    values = torch.arange(256, dtype=torch.uint8)
+    values[0x7F], values[0xFF] = 0x7E, 0xFE
+    v = values[(torch.arange(length)[:, None] * 7 + torch.arange(64)[None] * 5) % 256].view(1, 1, length, 64).contiguous()
+    scale = torch.full((1, 1, length // 16), 127, dtype=torch.uint8)
+    cache = KV8Cache(torch.zeros_like(v).cuda(), v.cuda(), scale.cuda(), scale.clone().cuda(), rows=1)
+    for last in range(new, length + 1, new):
+        out = cache.attend(torch.ones(new, 4, 64, dtype=dtype, device="cuda"), torch.tensor([last], dtype=torch.int32, device="cuda"),
+                           torch.tensor([0, new], dtype=torch.int32, device="cuda"), max_new=new, window=1)
+        want = v[0, 0, last - new:last].view(torch.float8_e4m3fn).double()[:, None].expand(new, 4, 64)
+        # the weight and the sum are one number; its inverse and the products are rounded: four half steps of fp32.  A value
+        # has 4 significant bits, so bf16 gives it back
+        off = (out.double().cpu() - want).abs()
+        assert bool((off <= want.abs() * (4 * 2.0 ** -24 if dtype == F32 else 0.0)).all()), last
+    cache.check()
