@@ -17,16 +17,19 @@
 //     chunks are permuted within the rows so that both reads are free of bank
 //     conflicts;
 //   * e4m3 converts to f16 exactly and in pairs; the scales stay outside the
-//     products: K's exponent multiplies the 16-key score tile, V's is added to
-//     the exponent of the weights.  M is the running maximum of
-//     score * log2(e) + V's exponent: the weight of the largest contribution
-//     is 1 whatever the scales are, and the sum of the softmax gets
-//     weight * 2^-(V's exponent);
+//     products: K's exponent multiplies the 16-key score tile, V's the step's
+//     P V where it is added to the result in fp32;
 //   * q enters as two f16 parts (22 bits; exact for bf16, whose second part is
-//     not multiplied); with fp32 q the weights enter as two f16 parts too;
-//   * the maximum is kept within a factor 2^8 of the true one (weights are
-//     scaled by 2^6, f16 holds 2^14), so a 16-key step needs one vote and
-//     almost never a reduction or a rescaling;
+//     not multiplied), the weights as two f16 parts for either type;
+//   * the maximum is kept within a factor 2 of the true one (weights are scaled
+//     by 2^13, f16 holds 2^15), so a 16-key step needs a vote and almost never a
+//     reduction or a rescaling;
+//   * two f16 parts hold only some 27 bits below the largest weight, and the
+//     largest may belong to a position whose V is 0 in a dim.  A second vote finds
+//     a step with smaller weights; it is taken relative to its own largest, and
+//     where its 16 weights lie further apart than that it is computed again for
+//     the rest, by an instance of its own (as a loop around the product alone,
+//     where its registers add to the others, 32 rows x 32k take 6 us more);
 //   * work: the visible 16-key steps of each row and K/V head (windows make gaps
 //     that are never touched).  Where the places (two CTAs an SM) suffice, each
 //     (row, head) is cut into pieces of its own, of at least two steps a warp, so
@@ -36,11 +39,13 @@
 //     it last joins them, in the order of the pieces, and sets its counter back
 //     to 0: one launch.
 //
-// Measured (128 dims): 32 bf16 rows of up to 32k positions 221 us, 6.4 TB/s or
-// 94 % of the measured copy rate; 8 fp32 rows x 8k 28.9 us and one row of 8191 12.7 us, where
-// the ends bind it: of the 7.3 us that one short row takes on the device, the launch,
-// the plan (a trip to the lengths), the first steps (page id, then bytes) and the
-// join's trip through memory are nearly all.  Two CTAs an SM hide one's ends
+// Measured (128 dims): 32 bf16 rows of up to 32k positions 237 us, 6.0 TB/s or
+// 88 % of the measured copy rate (222 with weights of one f16 part and nothing for
+// the small ones; with queries twice and four times as long, whose scores lie
+// further apart, 254 and 414); 8 fp32 rows x 8k 30.7 us and one row of 8191
+// 13.5 us, where the ends bind it: of the 7.3 us that one short row takes on the
+// device, the launch, the plan (a trip to the lengths), the first steps (page id,
+// then bytes) and the join's trip through memory are nearly all.  Two CTAs an SM hide one's ends
 // behind the other's stream: when it was changed, a single CTA of 12 warps took
 // 34.6 us for the 8 rows, three of 4 warps 31.
 #include <limits.h>
@@ -53,8 +58,15 @@ namespace gd {
 namespace {
 
 constexpr int KD_STEP = 16;           // positions of a step: the unit of work
-constexpr float KD_SLACK = 8.f;       // how far the maximum may lag (log2)
-constexpr float KD_SHIFT = 6.f;       // weights carry 2^6
+constexpr float KD_SLACK = 1.f;       // how far the maximum may lag (log2)
+constexpr float KD_SHIFT = 13.f;      // weights carry 2^13
+// Two f16 parts hold a weight 2^(x + KD_SHIFT) to 11 bits from x = -27 on; where the second carries KD_LOW, as with fp32 q,
+// to 20 bits from x = -30 on.  A step with smaller weights is taken relative to its own largest, and what is smaller than
+// that by as much takes a product of its own.  Weights below 2^-KD_LAST of the largest are 0 in fp32
+template <bool FINE>
+constexpr int KD_DEEP = FINE ? 30 : 27;
+constexpr float KD_LOW = 0x1p12f, KD_LAST = 126.f;
+constexpr float KD_UNIT = 0x1p-14f;   // results are summed in this unit, so that no term is above V's own size
 
 // a row of which only the tokens [skip, skip + take) count: it ends behind them
 __device__ __forceinline__ Kv8Row kd_some(const Kv8Row& row, int skip, int take) {
@@ -386,13 +398,16 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             l[a][0] = l[a][1] = 0.f;
         }
 
-        auto compute = [&](int i, int e_k, int e_v) {
+        auto compute = [&](auto is_first, int i, int e_k, int e_v, int level) -> bool {
+            constexpr bool FIRST = decltype(is_first)::value;
             const int kb = key0(i);
             const unsigned char* step = ring_p + (i % STAGES) * KdShared<HD, MT>::STEP;
             // S^T: rows keys g, g + 8; columns query rows 2t, 2t + 1
-            float sc[MT][4];
+            float sc[MT][4], s1[MT][4];   // two chains of products are half as long as one
 #pragma unroll
-            for (int a = 0; a < MT; ++a) sc[a][0] = sc[a][1] = sc[a][2] = sc[a][3] = 0.f;
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[a][e] = s1[a][e] = 0.f;
 #pragma unroll
             for (int j = 0; j < HD / 64; ++j) {
                 const uint4 k0 = *reinterpret_cast<const uint4*>(step + kd_at<HD>(g, t * (HD / 64) + j));
@@ -411,11 +426,15 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
                         for (int f = 0; f < PARTS; ++f) {
                             const uint4 q = q_s[f][a][(j * 4 + e) / 2][lane];
                             mma_f16(sc[a], a0, a1, a2, a3, q.x, q.y);
-                            mma_f16(sc[a], c0, c1, c2, c3, q.z, q.w);
+                            mma_f16(s1[a], c0, c1, c2, c3, q.z, q.w);
                         }
                 }
             }
-            const float kf = pow2i(e_k), vexp = (float)e_v, vinv = pow2i(-e_v);
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[a][e] = __fadd_rn(sc[a][e], s1[a][e]);
+            const float kf = pow2i(e_k);
             // positions every token of the row sees need no mask
             const bool all = kb + 15 <= p0 && (kb + 15 < p.sinks || kb > row.len - 1 - p.window);
             bool grew = false;
@@ -424,11 +443,11 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int b = e & 1, j = kb + g + (e >> 1) * 8;
-                    sc[a][e] = fmaf(sc[a][e], fac[a][b] * kf, vexp);
+                    sc[a][e] = __fmul_rn(sc[a][e], __fmul_rn(fac[a][b], kf));
                     if (!all && !(pos[a][b] >= 0 && kv8_sees(pos[a][b], j, p.window, p.sinks))) sc[a][e] = -INFINITY;
                     grew |= sc[a][e] > M[a][b] + KD_SLACK;
                 }
-            if (__any_sync(0xffffffffu, grew)) {
+            if (FIRST && __any_sync(0xffffffffu, grew)) {
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
@@ -447,25 +466,40 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
                         }
                     }
             }
-            uint32_t ph[MT][2], pl[FINE ? MT : 1][2];
+            // weights, and what the product with them is worth for each query row
+            float w[MT][4], unit[MT][2];
+            bool deep = false, rest = false;
 #pragma unroll
-            for (int a = 0; a < MT; ++a) {
-                float w[4];
+            for (int a = 0; a < MT; ++a)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float m = M[a][e & 1];
-                    w[e] = kv8_exp2(sc[a][e] - (m == -INFINITY ? 0.f : m) + KD_SHIFT);
-                    l[a][e & 1] += w[e] * vinv;
+                    sc[a][e] = __fadd_rn(sc[a][e], m == -INFINITY ? 0.f : -m);   // log2 of the weight
+                    w[a][e] = kv8_exp2(sc[a][e] + KD_SHIFT);
+                    if constexpr (FIRST) l[a][e & 1] += w[a][e];
+                    deep |= sc[a][e] < -(float)KD_DEEP<FINE> && sc[a][e] > -KD_LAST;
+                    unit[a][e & 1] = pow2i(e_v) * KD_UNIT;
                 }
+            if (!FIRST || __any_sync(0xffffffffu, deep)) {
+                constexpr float SPAN = KD_DEEP<FINE>;
 #pragma unroll
-                for (int b = 0; b < 2; ++b) {
-                    const uint32_t hi = pack_f16x2(w[2 * b], w[2 * b + 1]);
-                    ph[a][b] = transpose8x8(hi);
-                    if constexpr (FINE) {
-                        const float2 f = unpack_f16x2(hi);
-                        pl[a][b] = transpose8x8(pack_f16x2(w[2 * b] - f.x, w[2 * b + 1] - f.y));
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        float m = fmaxf(sc[a][b], sc[a][b + 2]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                        const float top = fmaxf(floorf(m), -KD_LAST), floor = -SPAN * (level + 1);
+                        unit[a][b] *= pow2i((int)top) * pow2i(-KD_DEEP<FINE> * level);
+#pragma unroll
+                        for (int e = b; e < 4; e += 2) {
+                            const float x = __fadd_rn(sc[a][e], -top);
+                            w[a][e] = kv8_exp2(x + (KD_SHIFT + SPAN * level));
+                            if (x < floor || (!FIRST && x >= floor + SPAN)) w[a][e] = 0.f;
+                            rest |= x < floor && sc[a][e] > -KD_LAST;
+                        }
                     }
-                }
+                rest = __any_sync(0xffffffffu, rest);
             }
             // V of positions that not every token sees: their bytes may be anything, and 0 * NaN is not 0
             uint32_t v[4][HD / 32];   // keys 2t, 2t + 1, 2t + 8, 2t + 9: dims g * HD / 8 ..
@@ -528,6 +562,19 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
                                 if (nan_s[warp][g * (HD / 8) + 2 * k + e] & sees) o[a][k][b + 2 * e] = __int_as_float(0x7FFFFFFF);
                     }
             }
+            // O += P V.  The tensor core cuts what it adds to its accumulator off, towards 0: over hundreds of steps that
+            // shows in fp32 (7e-6 after 450), so the steps are added up outside, rounded, and V's exponent joins there
+            uint32_t ph[MT][2], pl[MT][2];   // the weights that f16 holds in full, in two parts
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int b = 0; b < 2; ++b) {
+                    const float w0 = w[a][2 * b], w1 = w[a][2 * b + 1];
+                    const uint32_t hi = pack_f16x2(w0, w1);
+                    const float2 f = unpack_f16x2(hi);
+                    ph[a][b] = transpose8x8(hi);
+                    pl[a][b] = transpose8x8(FINE ? pack_f16x2((w0 - f.x) * KD_LOW, (w1 - f.y) * KD_LOW) : pack_f16x2(w0 - f.x, w1 - f.y));
+                }
 #pragma unroll
             for (int d = 0; d < HD / 32; ++d) {
                 // words of four keys, four dims each -> pairs of keys for dims 0, 1 and 2, 3
@@ -540,25 +587,26 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
                 e4m3x4_to_f16(y23, c2, c3);
 #pragma unroll
                 for (int a = 0; a < MT; ++a) {
+                    float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16(x, a0, a1, a2, a3, pl[a][0], pl[a][1]);
+                    mma_f16(y, c0, c1, c2, c3, pl[a][0], pl[a][1]);
                     if constexpr (FINE) {
-                        // the tensor core cuts what it adds to its accumulator off, towards 0: over hundreds of
-                        // steps that shows in fp32 (7e-6 after 450), so the steps are added up outside, rounded
-                        float x[4] = {0.f, 0.f, 0.f, 0.f}, y[4] = {0.f, 0.f, 0.f, 0.f};
-                        mma_f16(x, a0, a1, a2, a3, ph[a][0], ph[a][1]);
-                        mma_f16(y, c0, c1, c2, c3, ph[a][0], ph[a][1]);
-                        mma_f16(x, a0, a1, a2, a3, pl[a][0], pl[a][1]);
-                        mma_f16(y, c0, c1, c2, c3, pl[a][0], pl[a][1]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            o[a][2 * d][e] += x[e];
-                            o[a][2 * d + 1][e] += y[e];
+                            x[e] *= 1.f / KD_LOW;
+                            y[e] *= 1.f / KD_LOW;
                         }
-                    } else {
-                        mma_f16(o[a][2 * d], a0, a1, a2, a3, ph[a][0], ph[a][1]);
-                        mma_f16(o[a][2 * d + 1], c0, c1, c2, c3, ph[a][0], ph[a][1]);
+                    }
+                    mma_f16(x, a0, a1, a2, a3, ph[a][0], ph[a][1]);
+                    mma_f16(y, c0, c1, c2, c3, ph[a][0], ph[a][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        o[a][2 * d][e] = fmaf(x[e], unit[a][e & 1], o[a][2 * d][e]);
+                        o[a][2 * d + 1][e] = fmaf(y[e], unit[a][e & 1], o[a][2 * d + 1][e]);
                     }
                 }
             }
+            return rest;
         };
 
         for (int i = 0; i < mine; ++i) {
@@ -569,13 +617,14 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             const int there = __shfl_sync(0xffffffffu, now ? place : place_before, i & 31);
             const int e_k = __shfl_sync(0xffffffffu, now ? ke : ke_before, i & 31) - 127;
             const int e_v = __shfl_sync(0xffffffffu, now ? ve : ve_before, i & 31) - 127;
-            if (there >= 0) compute(i, e_k, e_v);
+            if (there >= 0 && compute(std::true_type{}, i, e_k, e_v, 0))
+                for (int level = 1; compute(std::false_type{}, i, e_k, e_v, level); ++level) {}
             __syncwarp();              // the stage may be overwritten
         }
         copy_wait<0>();
         __syncthreads();   // every warp is done with its ring
 
-        // join the four warps: the largest maximum, then sums in warp order
+        // join the warps: the largest maximum, then sums in warp order
 #pragma unroll
         for (int a = 0; a < MT; ++a)
 #pragma unroll
@@ -600,7 +649,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
         float* slots = p.ws;
         float* slot = slots + ((size_t)blockIdx.x * 2 + (u == u_begin ? 0 : 1)) * kd_slot_floats<HD, MT>();
         auto put = [&](int m, int d, float sum, const float (&y)[4]) {
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;   // nothing seen: zeros
+            const float inv = sum == 0.f ? 0.f : 1.f / (sum * KD_UNIT);   // nothing seen: zeros
             const int n = p.by_group.of(m);
             T* dst = static_cast<T*>(p.out) + (row.t0 + n) * p.out_stride + (h * G + m - n * G) * HD + d;
             if constexpr (FINE) *reinterpret_cast<float4*>(dst) = make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);

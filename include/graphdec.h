@@ -540,8 +540,9 @@ int dec_kv8_append(const dec_kv8_cache *cache, const dec_kv8_batch *batch, const
  * head a / (n_heads / n_kv_heads).  What a token does not see never reaches its
  * result, whatever bits it holds; a NaN that it sees does.  Scores, weights and
  * sums are held in fp32; with fp32 q the products are exact to about 2^-20, with
- * bf16 q the softmax weights are rounded to f16 (2^-11), finer than the result.
- * Results do not depend on scheduling. */
+ * bf16 q the softmax weights to 2^-11 or finer, which is finer than the result.
+ * That holds for each weight by itself, however small beside the largest (fp32's
+ * range, about 2^-120).  Results do not depend on scheduling. */
 typedef struct dec_kv8_attn {
     const void *q;               /* device [total, n_heads, head_dim], 16-byte aligned */
     void *out;                   /* device, the same shape and type; may not overlap q */

@@ -19,8 +19,8 @@ def attend(rows, heads, kv_heads, dim, dtype, change, window=0, sinks=0):
     compare(out, rows, K, V, table, q, window, sinks, dtype)
 
 
-SHAPES = [([(70, 40)], 64), ([(1500, 60), (300, 60)], 128), ([(900, 300)], 64)]
-IDS = ["chunk", "chunks", "prompt"]
+SHAPES = [([(2500, 1), (700, 1)], 64), ([(900, 3)], 128), ([(70, 40)], 64), ([(1500, 60), (300, 60)], 128), ([(900, 300)], 64)]
+IDS = ["tokens", "draft", "chunk", "chunks", "prompt"]
 
 
 def dominant(at, gap, zero=True):
@@ -52,8 +52,10 @@ def test_dominant_first_position_without_values(gap, rows, dim, dtype):
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_dominant_position_among_the_others(gap, at, dtype):
     """The dominant position is neither the first of its row nor of its tile; with a window that leaves it as a sink."""
+    attend([(900, 1), (800, 1)], 8, 2, 64, dtype, dominant(at, gap))
     attend([(900, 50)], 8, 2, 64, dtype, dominant(at, gap))
     attend([(900, 50)], 8, 2, 64, dtype, dominant(at, gap), window=400, sinks=30)
+    attend([(900, 2)], 8, 2, 64, dtype, dominant(at, gap, zero=False), window=300, sinks=30)
 
 
 @pytest.mark.parametrize("spread", [11, 17, 24, 40, 90])
