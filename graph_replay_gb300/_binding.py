@@ -26,6 +26,7 @@ DEC_FAULT_POS = 0x2
 DEC_FAULT_WRITE_MAP = 0x4
 DEC_FAULT_SLOT_MAP = 0x8
 DEC_FAULT_WAIT = 0x10
+DEC_FAULT_SCALE = 0x20
 
 DEC_DTYPE_F32 = 0
 DEC_DTYPE_BF16 = 1

@@ -12,6 +12,7 @@ constexpr unsigned FAULT_POS = 0x2u;
 constexpr unsigned FAULT_WRITE_MAP = 0x4u;
 constexpr unsigned FAULT_SLOT_MAP = 0x8u;
 constexpr unsigned FAULT_WAIT = 0x10u;   // an in-kernel wait gave up (bounded spin)
+constexpr unsigned FAULT_SCALE = 0x20u;  // a scale byte of an 8-bit K/V block out of range
 
 // ---- programmatic dependent launch (griddepcontrol) ----
 // wait: block until the preceding kernel in the stream/graph has completed and

@@ -83,6 +83,9 @@ __device__ __forceinline__ int kv8_exponent(float top) {
     return min(max(e, KV8_EXP_MIN), KV8_EXP_MAX);
 }
 
+// scale bytes with which attention's sums stay in fp32's range (2^-100 .. 2^100); others are flagged (FAULT_SCALE)
+__device__ __forceinline__ bool kv8_scale_ok(int byte) { return (unsigned)(byte - 27) <= 200u; }
+
 // 2^e for -126 <= e <= 127
 __device__ __forceinline__ float pow2i(int e) { return __int_as_float((e + 127) << 23); }
 // 2^x by the hardware's base-2 exponential

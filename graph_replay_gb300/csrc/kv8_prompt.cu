@@ -193,8 +193,8 @@ __device__ __forceinline__ uint32_t pack_b2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-// Four e4m3 values times 2^e as packed bf16 pairs, exact: 4 significant bits, fp32's exponents (e is at most 118, or 448
-// would become an infinity, and NaN times a weight of 0).  A byte s eeee mmm, moved to s 0000 eeee mmm 0000, is the bf16 of
+// Four e4m3 values times 2^e as packed bf16 pairs, exact: 4 significant bits, fp32's exponents (an e above 118, which is
+// flagged, would make an infinity of 448, and NaN with a weight of 0).  A byte s eeee mmm, moved to s 0000 eeee mmm 0000, is the bf16 of
 // its value times 2^-120, subnormals too.  2^(e + 120) passes the range, so it is two factors
 struct KpScale {
     __nv_bfloat162 a, b;
@@ -450,6 +450,9 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
         auto scales_ahead = [&]() {
             if (at_next >= 0) scales_next = (int)c.ks[scale_at] | (int)c.vs[scale_at] << 8;
         };
+        auto check_scales = [&]() {   // of the batch held
+            if (at >= 0 && !(kv8_scale_ok(scales & 255) && kv8_scale_ok(scales >> 8))) atomicOr(p.b.err, FAULT_SCALE);
+        };
         uint4 k[LOADS], v[LOADS];
         auto load = [&](int j) {   // tile j, in the batch of `at`
 #pragma unroll
@@ -541,11 +544,13 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
             fence_proxy_async_smem();
             mbar_arrive(&kv_full[(2 * j + 1) % SLOTS]);
             if (in_batch == KP_BATCH - 2 + grp) {   // tile j + 2 lies in the next batch
+                check_scales();
                 at = at_next;
                 scales = scales_next;
             }
             if (j + 2 < ntiles) load(j + 2);
         }
+        check_scales();
         cta_meet();
     } else if (warp >= KP_MMA_WARP) {
         // ---- MMA issuers: a warp for each query tile, so that one's waits do not hold up the other's products ----

@@ -68,6 +68,7 @@ typedef enum dec_status {
 #define DEC_FAULT_WRITE_MAP 0x4u  /* WriteMap[r] outside [0, num_pages * page_size) */
 #define DEC_FAULT_SLOT_MAP  0x8u  /* a SlotMap entry outside [0, num_pages) */
 #define DEC_FAULT_WAIT      0x10u /* an in-kernel wait on another CTA or on a copy gave up (bounded poll) */
+#define DEC_FAULT_SCALE     0x20u /* a scale byte of an 8-bit K/V block outside [27, 227] */
 
 /* E4M3 is a K/V store's type only: one byte a value with a power-of-two scale for
  * each block of positions and head, see "The 8-bit K/V cache" below. */
@@ -466,7 +467,7 @@ int dec_attention_static(dec_handle *h, int32_t layer, const float *qkv, const i
  * scale_block consecutive positions of one K/V head.  A stored byte x8 in a
  * block with scale byte s stands for x8 * 2^(s - 127); scale bytes that
  * dec_kv8_append writes lie in [87, 187]; a caller who fills a cache by other
- * means keeps them in [1, 254].
+ * means keeps them in [27, 227] (2^-100 .. 2^100: the attention's sums are fp32).
  *
  * These calls stand beside dec_attention for callers who keep their own cache.
  * They take no handle, only launch kernels on the caller's stream (NULL: the
@@ -502,8 +503,9 @@ typedef struct dec_kv8_cache {
  * <= total, more than max_new tokens, kv_len outside [0, pages_per_row *
  * page_size]) sets DEC_FAULT_POS in *err and is skipped whole; a page id that
  * is needed and outside [0, num_pages) sets DEC_FAULT_SLOT_MAP, and the page
- * counts as holding nothing.  DEC_FAULT_WAIT: a copy or product never ended,
- * and the call's results are not to be used. */
+ * counts as holding nothing.  DEC_FAULT_SCALE: attention met a scale byte outside
+ * [27, 227]; the results of the row's tokens are not to be used.  DEC_FAULT_WAIT:
+ * a copy or product never ended, and the call's results are not to be used. */
 typedef struct dec_kv8_batch {
     const int32_t *q_start;      /* device [rows + 1], or NULL: one token for each row */
     const int32_t *kv_len;       /* device [rows]: positions of each row, this call's tokens included */

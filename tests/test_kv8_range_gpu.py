@@ -93,6 +93,22 @@ def test_outlier_channels_in_every_fifth_block(spread, rows, dim, dtype):
     attend(rows, 4, 2, dim, dtype, change)
 
 
+@pytest.mark.parametrize("e", [-100, 100])
+@pytest.mark.parametrize("rows,dim", SHAPES, ids=IDS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_scales_at_the_ends_of_their_range(e, rows, dim, dtype):
+    """Scale bytes 27 and 227 in V, and in K with queries that bring the scores back."""
+    K, V, table, q, kv_len, starts = build(rows, 4, 2, dim, 64, 16, 23, dtype)
+    V.e[:] = e
+    K.e[:] = e
+    q = (q * 2.0 ** (-6 - e)).to(dtype)
+    cache = gpu_cache(K, V, table)
+    out = cache.attend(q.cuda(), kv_len.cuda(), starts.cuda(), max_new=max(n for _, n in rows))
+    cache.check()
+    V.e[:] = 0
+    compare(out.double() * 2.0 ** -e, rows, K, V, table, q, 0, 0, dtype)
+
+
 @pytest.mark.parametrize("new", [1, 2, 40])
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_every_byte_of_v(new, dtype):
@@ -112,4 +128,33 @@ def test_every_byte_of_v(new, dtype):
         # has 4 significant bits, so bf16 gives it back
         off = (out.double().cpu() - want).abs()
         assert bool((off <= want.abs() * (4 * 2.0 ** -24 if dtype == F32 else 0.0)).all()), last
+    cache.check()
+
+
+@pytest.mark.parametrize("byte", [1, 26, 228, 254])
+@pytest.mark.parametrize("which", ["k_scale", "v_scale"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_scales_out_of_range(byte, which, new):
+    """They are flagged where a token reads their block, and other rows keep their results."""
+    from graph_replay_gb300 import _binding as B
+    rows = [(300, new), (300, new), (200, new)]
+    K, V, table, q, kv_len, starts = build(rows, 4, 2, 64, 64, 16, 29, F32)
+    cache = gpu_cache(K, V, table)
+    args = dict(q_start=starts.cuda(), max_new=new, window=100, sinks=3)
+    good = cache.attend(q.cuda(), kv_len.cuda(), **args)
+    for block, seen in ((6, False), (0, True), (17, True)):   # blocks of row 1: between the sinks and the window, and in them
+        scale = getattr(cache, which)
+        at = (table[1, block // 4].long(), 1, block % 4)
+        was = int(scale[at])
+        scale[at] = byte
+        out = cache.attend(q.cuda(), kv_len.cuda(), **args)
+        if seen:
+            with pytest.raises(B.DecError, match="0x20"):
+                cache.check()
+        else:
+            cache.check()
+            assert torch.equal(out, good)
+        assert torch.equal(out[:new], good[:new]) and torch.equal(out[2 * new:], good[2 * new:])
+        scale[at] = was
+    assert torch.equal(cache.attend(q.cuda(), kv_len.cuda(), **args), good)
     cache.check()
