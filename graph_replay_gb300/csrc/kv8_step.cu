@@ -4,8 +4,11 @@
 // dec_kv8_append.
 //
 // Several rows may write into the same block (a prompt's chunk steps as rows of
-// one sequence); its scale is one, so the first of those rows' CTAs writes for
-// all of them, in row order.  One CTA for each row and K or V head, and for
+// one sequence), at any positions in any order; its scale is one, so the first
+// of those rows' CTAs writes for all of them, as one append: the largest of all
+// their values gives the exponent, and what the block holds below the last of
+// their positions is rounded again if that grew.  Of rows that write the same
+// position the last one counts.  One CTA for each row and K or V head, and for
 // each query head; a thread for each dim.  A few kilobytes: what it costs is
 // its launch and two dependent trips to memory.
 #include <limits.h>
@@ -14,6 +17,8 @@
 namespace gd {
 
 namespace {
+
+constexpr int KV8_STEP_ROWS = 8;   // of a step, at most
 
 // grid (2 * Hkv + Hq, R), HD threads
 template <int HD>
@@ -47,6 +52,9 @@ __global__ void __launch_bounds__(HD) k_kv8_step(const Kv8Step p) {
         const int slot = p.write_map[row];
         return slot < 0 || slot >= (long long)c.num_pages * c.page ? -1ll : (long long)slot;
     };
+    long long to[KV8_STEP_ROWS];
+#pragma unroll
+    for (int i = 0; i < KV8_STEP_ROWS; ++i) to[i] = i < p.R ? target(i) : -1ll;
     const long long mine = target(r);
     if (mine < 0) {
         if (d == 0 && p.write_map) atomicOr(p.err, FAULT_WRITE_MAP);
@@ -54,53 +62,67 @@ __global__ void __launch_bounds__(HD) k_kv8_step(const Kv8Step p) {
         return;
     }
     const long long block = mine >> c.block_log2;
-    for (int row = 0; row < r; ++row) {
-        const long long t = target(row);
-        if (t >= 0 && t >> c.block_log2 == block) {   // that row's CTA writes for this one
-            pdl_trigger();
-            return;
-        }
+    bool own = true;
+#pragma unroll
+    for (int i = 0; i < KV8_STEP_ROWS; ++i) own &= !(i < r && to[i] >= 0 && to[i] >> c.block_log2 == block);
+    if (!own) {   // an earlier row's CTA writes for this one
+        pdl_trigger();
+        return;
     }
     // the block's first byte and its scale
     const long long page = mine / c.page;
     const int first = (int)(mine % c.page) >> c.block_log2 << c.block_log2;
     uint8_t* store = (is_v ? c.v : c.k) + (((size_t)page * c.Hkv + h) * c.page + first) * HD;
     uint8_t* scale = (is_v ? c.vs : c.ks) + ((size_t)page * c.Hkv + h) * (c.page >> c.block_log2) + (first >> c.block_log2);
-    int had = (int)*scale - 127;
-    for (int row = r; row < p.R; ++row) {
-        const long long t = target(row);
-        if (t < 0 || t >> c.block_log2 != block) continue;
-        const int held = (int)(t & (c.block - 1));   // earlier positions in the block
-        float x = value(row, is_v ? (p.Hq + c.Hkv + h) * HD : (p.Hq + h) * HD, !is_v);
-        float top = warp_max(fabsf(x) <= 3.402823466e38f ? fabsf(x) : 0.f);
-        __syncthreads();   // the last row's maxima have been read
-        if ((d & 31) == 0) tops[d >> 5] = top;
-        __syncthreads();
-        top = tops[0];
+    const int had = (int)*scale - 127;
+    float x[KV8_STEP_ROWS], top = 0.f;
+    int at[KV8_STEP_ROWS], last = 0;   // position in the block, -1: not a row of this block
+    unsigned long long written = 0;    // a block has at most 64 positions
 #pragma unroll
-        for (int w = 1; w < HD / 32; ++w) top = fmaxf(top, tops[w]);
-        int e = kv8_exponent(top);
-        if (held) e = max(e, had);
-        x *= pow2i(-min(e, 126));
-        if (!(fabsf(x) <= 448.f)) x = __int_as_float(0x7FFFFFFF);
-        store[(size_t)held * HD + d] = (uint8_t)f32_to_e4m3x4(x, 0.f, 0.f, 0.f);
-        if (held && e > had) {
-            const float f = pow2i(max(had - e, -60));
-            for (int j = 0; j < held; ++j) {   // each thread its own dim: no other thread's bytes
-                float y[4];
-                e4m3x4_to_f32(store[(size_t)j * HD + d], y);
-                store[(size_t)j * HD + d] = (uint8_t)f32_to_e4m3x4(y[0] * f, 0.f, 0.f, 0.f);
-            }
-        }
-        had = e;
+    for (int i = 0; i < KV8_STEP_ROWS; ++i) {
+        at[i] = to[i] >= 0 && to[i] >> c.block_log2 == block ? (int)(to[i] & (c.block - 1)) : -1;
+#pragma unroll
+        for (int j = i + 1; j < KV8_STEP_ROWS; ++j)
+            if (to[j] == to[i]) at[i] = -1;
+        if (at[i] < 0) continue;
+        x[i] = value(i, is_v ? (p.Hq + c.Hkv + h) * HD : (p.Hq + h) * HD, !is_v);
+        if (fabsf(x[i]) <= 3.402823466e38f) top = fmaxf(top, fabsf(x[i]));
+        written |= 1ull << at[i];
+        last = max(last, at[i]);
     }
-    if (d == 0) *scale = (uint8_t)(had + 127);
+    top = warp_max(top);
+    if ((d & 31) == 0) tops[d >> 5] = top;
+    __syncthreads();   // and every thread has read the old exponent
+    top = tops[0];
+#pragma unroll
+    for (int w = 1; w < HD / 32; ++w) top = fmaxf(top, tops[w]);
+    const unsigned long long held = ((1ull << last) - 1) & ~written;   // earlier positions in the block
+    int e = kv8_exponent(top);
+    if (held) e = max(e, had);
+    if (held && e > had) {
+        const float f = pow2i(max(had - e, -60));
+        for (unsigned long long m = held; m; m &= m - 1) {   // each thread its own dim: no other thread's bytes
+            uint8_t* y8 = store + (size_t)(__ffsll((long long)m) - 1) * HD + d;
+            float y[4];
+            e4m3x4_to_f32(*y8, y);
+            *y8 = (uint8_t)f32_to_e4m3x4(y[0] * f, 0.f, 0.f, 0.f);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < KV8_STEP_ROWS; ++i) {
+        if (at[i] < 0) continue;
+        float y = x[i] * pow2i(-min(e, 126));
+        if (!(fabsf(y) <= 448.f)) y = __int_as_float(0x7FFFFFFF);
+        store[(size_t)at[i] * HD + d] = (uint8_t)f32_to_e4m3x4(y, 0.f, 0.f, 0.f);
+    }
+    if (d == 0) *scale = (uint8_t)(e + 127);
     pdl_trigger();
 }
 
 }  // namespace
 
 cudaError_t kv8_step_launch(const Kv8Step& p, cudaStream_t s, bool pdl) {
+    if (p.R > KV8_STEP_ROWS || p.c.block > 64) return cudaErrorInvalidValue;   // a capture has neither
     cudaLaunchAttribute at[1];
     at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     at[0].val.programmaticStreamSerializationAllowed = 1;

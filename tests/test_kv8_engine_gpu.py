@@ -269,3 +269,49 @@ def test_faults_and_refusals():
     with pytest.raises(B.DecError, match="scales"):
         d.kv_scale(0, 0)
     d.close()
+
+
+@pytest.mark.parametrize("at", [[0, 1, 2, 3], [3, 2, 1, 0], [37, 32, 41, 34], [60, 5, 61, 4], [50, 50, 7, 50], [15, 16, 0, 31]], ids=str)
+@pytest.mark.parametrize("hd,page", [(64, 64), (128, 32), (64, 16)])
+def test_rows_that_share_blocks_in_any_order(at, hd, page):
+    """Rows of one sequence step at positions in any order, with values far apart: one scale a block, from all of them;
+    what the block held below the last of them is rounded again; of equal positions the last row's counts."""
+    heads, kv, cap, rows, block = 4, 2, 64, 4, page
+    w = weights(torch.float32, heads, kv, hd)
+    dec = decoder(w, rows, cap, True, page, "f32", heads, kv, hd)
+    pages = [2, 0, 3, 1][:cap // page]
+    dec.set_slot_map(np.array([pages] * rows, dtype=np.int32))
+    g = torch.Generator().manual_seed(3)
+    dec.step([0] * rows, at)   # the write map
+    stores = [(dec.kv(0, i), dec.kv_scale(0, i)) for i in (0, 1)]
+    for x, s in stores:
+        x.copy_((torch.randn(x.shape, generator=g) * 60).clamp(-448, 448).to(torch.float8_e4m3fn))
+        s.copy_(torch.randint(119, 122, s.shape, generator=g, dtype=torch.uint8))
+    before = [(x.float().cpu().double(), s.cpu().long() - 127) for x, s in stores]
+    qkv = torch.randn(rows, (heads + 2 * kv) * hd, generator=g) * (8.0 ** torch.arange(rows))[torch.randperm(rows, generator=g), None]
+    pos, out = torch.tensor(at, dtype=torch.int32), torch.empty(rows, heads * hd, device="cuda")
+    dec.attention(0, qkv.cuda(), pos.cuda(), out)
+    torch.cuda.synchronize()
+    counts = [r for r in range(rows) if at[r] not in at[r + 1:]]
+    for which in (0, 1):
+        x, e = (t.clone() for t in before[which])
+        new = qkv[:, (heads + which * kv) * hd:(heads + (which + 1) * kv) * hd].double().view(rows, kv, hd)
+        new = rope(new, pos) if which == 0 else new
+        for b in {at[r] // block for r in counts}:
+            here = [r for r in counts if at[r] // block == b]
+            pg, first = pages[b * block // page], b * block % page
+            for h in range(kv):
+                held = [j for j in range(max(at[r] for r in here) % block) if b * block + j not in at]
+                was, need = int(e[pg, h, first // block]), R.exponent(float(new[here, h].abs().max()))
+                e[pg, h, first // block] = now = max(was, need) if held else need
+                for j in held:
+                    x[pg, h, first + j] = R.e4m3(x[pg, h, first + j] * 2.0 ** (was - now))
+                for r in here:
+                    x[pg, h, first + at[r] % block] = R.e4m3(new[r, h] * 2.0 ** -now)
+        got, scale = stores[which][0].float().cpu().double(), stores[which][1].cpu().long() - 127
+        assert torch.equal(scale, e)
+        if which == 1:
+            assert torch.equal(got, x)
+        else:   # k after RoPE carries fp32 errors: a value next to a rounding border may be stored a step away
+            assert bool(((got - x).abs() <= x.abs() * 2.0 ** -3 + 2.0 ** -9).all()) and int((got != x).sum()) <= 3 * rows
+    dec.close()
