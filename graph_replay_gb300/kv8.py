@@ -6,8 +6,8 @@ for each block of positions and K/V head (graphdec.h, "The 8-bit K/V cache").
     out = cache.attend(q, kv_len, window=4096, sinks=4)
 
 Both calls launch on torch's current stream and return at once; nothing reads
-back to the host.  ``check`` does, and raises if a call met an entry of
-``kv_len``, ``q_start`` or the page table that is out of range.
+back to the host.  ``check`` does, and raises if a call on any stream met an
+entry of ``kv_len``, ``q_start``, the page table or the scales that is out of range.
 """
 from __future__ import annotations
 
@@ -53,6 +53,8 @@ class KV8Cache:
         self.device = k.device
         self._need, self._ws, self._lock = {}, {}, threading.Lock()
         self._err = torch.zeros(1, dtype=torch.int32, device=k.device)
+        if not torch.cuda.is_current_stream_capturing():
+            torch.cuda.current_stream(k.device).synchronize()   # zeroed before a call on any other stream adds to it
         self._c = B.dec_kv8_cache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                   None if page_table is None else page_table.data_ptr(), rows, per_row, page, pages,
                                   heads, dim, self.scale_block, k.device.index)
@@ -145,8 +147,11 @@ class KV8Cache:
         return out
 
     def check(self) -> None:
-        """Wait for the calls so far and raise DecError if one met an entry out of range since the last check."""
+        """Wait for all work on the device so far, on whatever stream and in whatever graph, and raise DecError if a call
+        met an entry out of range since the last check."""
+        torch.cuda.synchronize(self.device)
         bits = int(self._err.item())
         if bits:
             self._err.zero_()
+            torch.cuda.synchronize(self.device)   # a later call on another stream adds its bits after this
             raise B.DecError(B.DEC_E_DEVICE_FAULT, f"8-bit K/V cache: an entry out of range (error word 0x{bits:x})")
