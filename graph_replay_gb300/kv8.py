@@ -104,6 +104,8 @@ class KV8Cache:
             b = B.dec_kv8_batch(self._c.pages or self._c.k, self._c.k, self._c.k, tokens, max_new)   # addresses are not read
             a = B.dec_kv8_attn(self._c.k, self._c.k, n_heads * self.head_dim, n_heads * self.head_dim, _DT[dtype], n_heads,
                                window, sinks, 0.0, None, 0)
+            if len(self._need) >= 256:   # prompts come in any length
+                self._need.clear()
             need = self._need[key] = B.dec_kv8_workspace(self._c, b, a)
         return need
 

@@ -34,3 +34,10 @@ def test_check_sees_calls_on_other_streams(recorded):
         cache.check()
     cache.attend(q, lens)
     cache.check()
+
+
+def test_sizes_kept_are_bounded():
+    cache, _, _ = small()
+    sizes = [cache.workspace_bytes(n, 4, max_new=n) for n in range(1, 2000)]
+    assert len(cache._need) <= 256
+    assert sizes[0] == cache.workspace_bytes(1, 4) and sizes[-1] == cache.workspace_bytes(1999, 4, max_new=1999)
