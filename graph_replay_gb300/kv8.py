@@ -63,6 +63,8 @@ class KV8Cache:
     def empty(cls, rows: int, cap: int, n_kv_heads: int, head_dim: int, scale_block: int = 64,
               device="cuda") -> "KV8Cache":
         """An empty contiguous cache of `cap` positions (a multiple of scale_block) for each row."""
+        if scale_block < 1 or cap < 1 or cap % scale_block:
+            raise ValueError(f"KV8Cache.empty: cap {cap} is no multiple of scale_block {scale_block}")
         k = torch.zeros(rows, n_kv_heads, cap, head_dim, dtype=torch.uint8, device=device)
         s = torch.full((rows, n_kv_heads, cap // scale_block), 127, dtype=torch.uint8, device=device)
         return cls(k, torch.zeros_like(k), s, s.clone(), rows=rows)

@@ -141,3 +141,10 @@ def test_store_size(B):
         B.dec_workspace_size(config(), 8200, 1, B.DEC_KV_CONTIGUOUS)     # not a multiple of 16
     with pytest.raises(B.DecError):
         B.dec_workspace_size(config(), 64, 1, B.DEC_KV_PAGED, 8, 64)
+
+
+@pytest.mark.parametrize("cap,block", [(100, 64), (64, 0), (0, 64), (63, 64)])
+def test_empty_caches_of_odd_capacity(B, cap, block):
+    from graph_replay_gb300 import KV8Cache
+    with pytest.raises(ValueError, match="cap"):   # before anything is allocated: no device is needed
+        KV8Cache.empty(1, cap, 1, 64, scale_block=block)
