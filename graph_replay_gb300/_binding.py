@@ -275,7 +275,15 @@ def dec_set_kv_sweep(h, sweep: int) -> None:
     check(h, lib().dec_set_kv_sweep(h, sweep))
 
 
+def check_int32(**values) -> None:
+    """ctypes cuts an integer off to its field's 32 bits without a word: 2^32 + 5 would be 5."""
+    for name, v in values.items():
+        if not -0x80000000 <= v <= 0x7FFFFFFF:
+            raise ValueError(f"{name} = {v} does not fit 32 bits")
+
+
 def dec_set_window(h, window: int, sinks: int) -> None:
+    check_int32(window=window, sinks=sinks)
     check(h, lib().dec_set_window(h, window, sinks))
 
 

@@ -73,6 +73,8 @@ class KV8Cache:
         for t in (kv_len,) if q_start is None else (kv_len, q_start):
             if t.dtype != torch.int32 or t.device != self.device or not t.is_contiguous():
                 raise ValueError("KV8Cache: kv_len and q_start are contiguous int32 tensors on the cache's device")
+        if not -0x80000000 <= max_new <= 0x7FFFFFFF:
+            B.check_int32(max_new=max_new)
         if kv_len.numel() != self.rows or (q_start is not None and q_start.numel() != self.rows + 1):
             raise ValueError("KV8Cache: kv_len has rows entries, q_start rows + 1")
         return B.dec_kv8_batch(None if q_start is None else q_start.data_ptr(), kv_len.data_ptr(),
@@ -103,6 +105,7 @@ class KV8Cache:
         key = (tokens, n_heads, max_new, window, sinks, dtype)
         need = self._need.get(key)
         if need is None:
+            B.check_int32(tokens=tokens, n_heads=n_heads, max_new=max_new, window=window, sinks=sinks)
             b = B.dec_kv8_batch(self._c.pages or self._c.k, self._c.k, self._c.k, tokens, max_new)   # addresses are not read
             a = B.dec_kv8_attn(self._c.k, self._c.k, n_heads * self.head_dim, n_heads * self.head_dim, _DT[dtype], n_heads,
                                window, sinks, 0.0, None, 0)
@@ -131,6 +134,8 @@ class KV8Cache:
         (allocated like q if None); packed tokens that belong to no row are not written.  `workspace`: uint8, zeroed
         before its first use, of workspace_bytes(...); None: the cache keeps one for each stream, and a graph that
         records the call one of its own."""
+        if not (-0x80000000 <= window <= 0x7FFFFFFF and -0x80000000 <= sinks <= 0x7FFFFFFF):
+            B.check_int32(window=window, sinks=sinks)
         qs = self._tokens("q", q, 0)
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)

@@ -41,3 +41,19 @@ def test_sizes_kept_are_bounded():
     sizes = [cache.workspace_bytes(n, 4, max_new=n) for n in range(1, 2000)]
     assert len(cache._need) <= 256
     assert sizes[0] == cache.workspace_bytes(1, 4) and sizes[-1] == cache.workspace_bytes(1999, 4, max_new=1999)
+
+
+@pytest.mark.parametrize("value", [2 ** 31, 2 ** 32 + 5, -2 ** 32])
+@pytest.mark.parametrize("name", ["window", "sinks", "max_new"])
+def test_numbers_beyond_32_bits_are_refused(name, value):
+    cache, q, lens = small()
+    kw = dict(window=7) if name == "sinks" else {}
+    with pytest.raises(ValueError, match=name):
+        cache.attend(q, lens, **kw, **{name: value})
+    with pytest.raises(ValueError, match=name):
+        cache.workspace_bytes(2, 4, **{name: value})
+    if name == "max_new":
+        with pytest.raises(ValueError, match=name):
+            cache.append(q[:, :2], q[:, 2:], lens, max_new=value)
+    cache.attend(q, lens, window=2 ** 31 - 1, sinks=2 ** 31 - 1)   # the largest: no window
+    cache.check()

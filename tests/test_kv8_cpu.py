@@ -148,3 +148,9 @@ def test_empty_caches_of_odd_capacity(B, cap, block):
     from graph_replay_gb300 import KV8Cache
     with pytest.raises(ValueError, match="cap"):   # before anything is allocated: no device is needed
         KV8Cache.empty(1, cap, 1, 64, scale_block=block)
+
+
+def test_windows_beyond_32_bits(B):
+    for window, sinks in ((2 ** 32 + 5, 0), (5, 2 ** 31), (-2 ** 32, 0)):
+        with pytest.raises(ValueError, match="32 bits"):
+            B.dec_set_window(None, window, sinks)   # before the handle is looked at
