@@ -1329,7 +1329,7 @@ int dec_stats_get(const dec_handle* h, dec_stats* out) {
     out->kv_layout = h->layout;
     out->last_step_us = h->last_step_us;
     out->workspace_bytes = (int64_t)h->lay.total;
-    out->kv_bytes = (int64_t)(2 * (size_t)h->cfg.n_layers * h->lay.kv_layer);
+    out->kv_bytes = (int64_t)(2 * (size_t)h->cfg.n_layers * (h->lay.kv_layer + h->lay.kvs_layer));
     return DEC_OK;
 }
 

@@ -183,7 +183,7 @@ typedef struct dec_stats {
     int32_t reserved;
     double last_step_us;      /* host wall time of the last dec_step */
     int64_t workspace_bytes;  /* device bytes the capture uses (KV included) */
-    int64_t kv_bytes;         /* device bytes of K and V over all layers */
+    int64_t kv_bytes;         /* device bytes of K and V over all layers, an e4m3 store's scales included */
 } dec_stats;
 
 /* Create a handle for `cfg` on cfg->device ("Execution", executor contract:

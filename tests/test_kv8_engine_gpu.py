@@ -315,3 +315,12 @@ def test_rows_that_share_blocks_in_any_order(at, hd, page):
         else:   # k after RoPE carries fp32 errors: a value next to a rounding border may be stored a step away
             assert bool(((got - x).abs() <= x.abs() * 2.0 ** -3 + 2.0 ** -9).all()) and int((got != x).sum()) <= 3 * rows
     dec.close()
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_stats_count_the_scales(paged):
+    w = weights(torch.bfloat16)
+    dec = decoder(w, 2, 256, paged, 16)
+    parts = [t.numel() for l in range(LAYERS) for i in (0, 1) for t in (dec.kv(l, i), dec.kv_scale(l, i))]
+    assert sum(parts) <= dec.stats()["kv_bytes"] <= sum(parts) + 256 * len(parts)   # each part up to a multiple of 256
+    dec.close()
