@@ -154,3 +154,18 @@ def test_windows_beyond_32_bits(B):
     for window, sinks in ((2 ** 32 + 5, 0), (5, 2 ** 31), (-2 ** 32, 0)):
         with pytest.raises(ValueError, match="32 bits"):
             B.dec_set_window(None, window, sinks)   # before the handle is looked at
+
+
+def test_growing_a_block_gives_these_values():
+    """The exact values behind test_growing_a_block_rounds_its_earlier_tokens."""
+    s = R.Store(1, 1, 16, 64, 16)
+    one = torch.ones(1, 1, 64, dtype=torch.float64)
+    s.append([0], 0, one * 1.125)                    # 448 * 2^-8 >= 1.125: stored as 288 * 2^-8
+    assert int(s.e[0, 0, 0]) == -8 and bool((s.x[0, 0, 0] == 288).all())
+    s.append([0], 1, one * 1000.0)                   # 1000 * 2^-2 = 250: between 240 and 256, and 288 * 2^-10 between 0.28125
+    assert int(s.e[0, 0, 0]) == 2 and bool((s.x[0, 0, 1] == 256).all()) and bool((s.x[0, 0, 0] == 0.28125).all())
+    s.append([0], 2, one * 2.0 ** 18)                # 2^18 <= 448 * 2^10: 1.125 * 2^-10 is over half of the least step, 2^-9
+    assert int(s.e[0, 0, 0]) == 10 and bool((s.x[0, 0, 2] == 256).all())
+    assert bool((s.x[0, 0, 0] == 2.0 ** -9).all()) and bool((s.x[0, 0, 1] == 1.0).all())   # 1024 * 2^-10
+    s.append([0], 3, one * 2.0 ** 19)                # half of the least step, to the even one: 0
+    assert int(s.e[0, 0, 0]) == 11 and bool((s.x[0, 0, 0] == 0.0).all())

@@ -158,3 +158,45 @@ def test_scales_out_of_range(byte, which, new):
         scale[at] = was
     assert torch.equal(cache.attend(q.cuda(), kv_len.cuda(), **args), good)
     cache.check()
+
+
+# fp32 q over 32k positions: the error's norm over the result's.  Scores: the tensor core cuts each of its 8 (dim 128) or 4
+# sums off at half a step of 2^-23 on the average, relative to scores of some 4 bits: 4 * 8 * 2^-24 = 2e-6 at the largest
+# scores, half of it at the usual ones.  Exponential: 2^-22, its argument (up to 32) 2^-20 at the worst, a third on the
+# average: 4e-7 each.  P V: 3 parts x 4 sums x 6 tiles are cut off before a fold, half a step of 2^-23 each of a sum that
+# is half grown on the average: 72 * 2^-24 / 2 / 2 (a step is between 2^-24 and 2^-23 of the sum) = 1.1e-6.  Together
+# 1.6e-6 as independent errors, 3e-6 with a factor for what is not.  Without the folds it is 7e-6, with weights of one
+# part 1e-4
+@pytest.mark.parametrize("new,heads,kv_heads,dim", [(1, 4, 2, 128), (1, 8, 2, 64), (64, 4, 2, 64), (64, 4, 1, 128)])
+def test_fp32_error_over_long_contexts(new, heads, kv_heads, dim):
+    import _kv8 as R
+    rows = [(32767, new)]
+    K, V, table, q, kv_len, starts = build(rows, heads, kv_heads, dim, 64, 64, 41, F32, poison=False)
+    K.e[:], V.e[:] = -6, -6          # values of about 1, scores of about 1
+    cache = gpu_cache(K, V, table)
+    out = cache.attend(q.cuda(), kv_len.cuda(), starts.cuda(), max_new=new).double().cpu()
+    cache.check()
+    at = table[0].long()
+    want, _, _ = R.attend(q.double(), K.values(at), V.values(at), torch.arange(32767 - new, 32767))
+    assert float((out - want).norm() / want.norm()) <= 3e-6
+
+
+def test_nan_behind_a_thousand_tiles():
+    """CTAs of more than 1024 tiles of 64 positions, where the marks of tiles that hold a NaN come round again."""
+    from graph_replay_gb300 import KV8Cache
+    heads, length, new, window = 160, 64 * 1100, 60, 70000     # enough heads that no CTA shares its positions with another
+    cache = KV8Cache.empty(1, length, heads, 64, scale_block=64)
+    cache.v.fill_(0x38)                                         # 1.0 everywhere; K is zero, so every result is 1
+    first = length - new
+    early, late = first + 30 - window, 1029 * 64 + 5   # tile of `early` and tile 1029, whose marks are one
+    assert (early // 64) % 1024 == 1029 % 1024 and 0 <= early and late // 64 == 1029
+    cache.v[0, 0, early, 3] = 0x7F
+    cache.v[0, 1, late, 7] = 0xFF
+    cache.v[0, 2, first - window - 64, 9] = 0x7F                # nobody sees it
+    out = cache.attend(torch.ones(new, heads, 64, device="cuda", dtype=BF16), torch.tensor([length], dtype=torch.int32, device="cuda"),
+                       torch.tensor([0, new], dtype=torch.int32, device="cuda"), max_new=new, window=window)
+    cache.check()
+    nan = torch.zeros(new, heads, 64, dtype=torch.bool, device="cuda")
+    nan[:30, 0, 3] = True            # token t sees positions from first + t - window + 1 on: t < 30 see `early`
+    nan[:, 1, 7] = True
+    assert torch.equal(torch.isnan(out), nan) and bool((out[~nan] == 1).all())
