@@ -21,15 +21,14 @@
 //     P V where it is added to the result in fp32;
 //   * q enters as two f16 parts (22 bits; exact for bf16, whose second part is
 //     not multiplied), the weights as two f16 parts for either type;
-//   * the maximum is kept within a factor 2 of the true one (weights are scaled
-//     by 2^13, f16 holds 2^15), so a 16-key step needs a vote and almost never a
-//     reduction or a rescaling;
+//   * the maximum is kept within a factor 4 of the true one (weights are scaled
+//     by 2^13, f16 holds 2^15), so a 16-key step needs one vote and almost never
+//     a reduction or a rescaling;
 //   * two f16 parts hold only some 27 bits below the largest weight, and the
-//     largest may belong to a position whose V is 0 in a dim.  A second vote finds
-//     a step with smaller weights; it is taken relative to its own largest, and
-//     where its 16 weights lie further apart than that it is computed again for
-//     the rest, by an instance of its own (as a loop around the product alone,
-//     where its registers add to the others, 32 rows x 32k take 6 us more);
+//     largest may belong to a position whose V is 0 in a dim.  The same vote finds
+//     a step with smaller weights.  It is taken relative to its own largest, and
+//     where its 16 weights lie further apart than that, it is marked, and computed
+//     again for the rest when the loop is done;
 //   * work: the visible 16-key steps of each row and K/V head (windows make gaps
 //     that are never touched).  Where the places (two CTAs an SM) suffice, each
 //     (row, head) is cut into pieces of its own, of at least two steps a warp, so
@@ -39,15 +38,15 @@
 //     it last joins them, in the order of the pieces, and sets its counter back
 //     to 0: one launch.
 //
-// Measured (128 dims): 32 bf16 rows of up to 32k positions 237 us, 6.0 TB/s or
-// 88 % of the measured copy rate (222 with weights of one f16 part and nothing for
+// Measured (128 dims): 32 bf16 rows of up to 32k positions 227 us, 6.2 TB/s or
+// 92 % of the measured copy rate (222 with weights of one f16 part and nothing for
 // the small ones; with queries twice and four times as long, whose scores lie
-// further apart, 254 and 414); 8 fp32 rows x 8k 30.7 us and one row of 8191
-// 13.5 us, where the ends bind it: of the 7.3 us that one short row takes on the
+// further apart, 256 and 477); 8 fp32 rows x 8k 30.8 us and one row of 8191
+// 13.9 us, where the ends bind it: of the 7.4 us that one short row takes on the
 // device, the launch, the plan (a trip to the lengths), the first steps (page id,
-// then bytes) and the join's trip through memory are nearly all.  Two CTAs an SM hide one's ends
-// behind the other's stream: when it was changed, a single CTA of 12 warps took
-// 34.6 us for the 8 rows, three of 4 warps 31.
+// then bytes) and the join's trip through memory are nearly all.  Two CTAs an SM
+// hide one's ends behind the other's stream: when it was changed, a single CTA of
+// 12 warps took 34.6 us for the 8 rows, three of 4 warps 31.
 #include <limits.h>
 #include <type_traits>
 #include "kv8.cuh"
@@ -58,13 +57,18 @@ namespace gd {
 namespace {
 
 constexpr int KD_STEP = 16;           // positions of a step: the unit of work
-constexpr float KD_SLACK = 1.f;       // how far the maximum may lag (log2)
-constexpr float KD_SHIFT = 13.f;      // weights carry 2^13
-// Two f16 parts hold a weight 2^(x + KD_SHIFT) to 11 bits from x = -27 on; where the second carries KD_LOW, as with fp32 q,
-// to 20 bits from x = -30 on.  A step with smaller weights is taken relative to its own largest, and what is smaller than
-// that by as much takes a product of its own.  Weights below 2^-KD_LAST of the largest are 0 in fp32
+constexpr float KD_SLACK = 1.f;       // how far the maximum, rounded down, may lag (log2)
+constexpr float KD_SHIFT = 13.f;      // weights carry 2^13: M is the maximum less 13
+constexpr float KD_NONE = -3.402823466e38f;   // M before the first score: any is above it by more than the slack
+// Two f16 parts hold a weight of 2^(x - KD_SHIFT) of M's to 11 bits from x = -14 on; where the second carries KD_LOW, as
+// with fp32 q, to 20 bits from x = -17 on: KD_DEEP below the largest.  A step with smaller weights is taken relative to
+// its own largest, which gets another bit, and what lies more than KD_SPAN below that waits for a pass of its own.
+// Weights below 2^-KD_LAST of the largest are 0 in fp32.  (The hundredth: no rounding lets a step that is not taken
+// relative to its own largest hold a weight below KD_SPAN.)
 template <bool FINE>
-constexpr int KD_DEEP = FINE ? 30 : 27;
+constexpr int KD_SPAN = FINE ? 31 : 28;
+template <bool FINE>
+constexpr float KD_DEEP = KD_SPAN<FINE> - 1.01f;
 constexpr float KD_LOW = 0x1p12f, KD_LAST = 126.f;
 constexpr float KD_UNIT = 0x1p-14f;   // results are summed in this unit, so that no term is above V's own size
 
@@ -309,24 +313,27 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             ke = c.ks[at];   // not looked at before the step is computed: nothing waits for them here
             ve = c.vs[at];
         };
+        // the step of lane l of the 32 into a stage of the ring
+        auto copy_step = [&](int l, int stage) {
+            const int there = __shfl_sync(0xffffffffu, place, l);
+            if (there < 0) return;
+            const size_t at = (size_t)there * (16 * HD);
+            const uint32_t dst = ring + (uint32_t)(stage * KdShared<HD, MT>::STEP);
+#pragma unroll
+            for (int u = 0; u < HD / 32; ++u) {
+                const int x = lane + 32 * u;
+                const uint32_t d = dst + kd_at<HD>(x / (HD / 16), x % (HD / 16));
+                copy16(d, c.k + at + (size_t)x * 16);
+                copy16(d + 16 * HD, c.v + at + (size_t)x * 16);
+            }
+        };
         int ahead = 0;   // the next step to copy
         // one more step into the ring; one group a call, also for nothing
         auto copy_next = [&]() {
             const int i = ahead++;
             if (i < mine) {
                 if ((i & 31) == 0) next32(i);
-                const int there = __shfl_sync(0xffffffffu, place, i & 31);
-                if (there >= 0) {
-                    const size_t at = (size_t)there * (16 * HD);
-                    const uint32_t dst = ring + (uint32_t)((i % STAGES) * KdShared<HD, MT>::STEP);
-#pragma unroll
-                    for (int u = 0; u < HD / 32; ++u) {
-                        const int x = lane + 32 * u;
-                        const uint32_t d = dst + kd_at<HD>(x / (HD / 16), x % (HD / 16));
-                        copy16(d, c.k + at + (size_t)x * 16);
-                        copy16(d + 16 * HD, c.v + at + (size_t)x * 16);
-                    }
-                }
+                copy_step(i & 31, i % STAGES);
             }
             copy_commit();
         };
@@ -398,14 +405,14 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             for (int k = 0; k < NK; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[a][k][e] = 0.f;
-            M[a][0] = M[a][1] = -INFINITY;
+            M[a][0] = M[a][1] = KD_NONE;
             l[a][0] = l[a][1] = 0.f;
         }
 
-        auto compute = [&](auto is_first, int i, int e_k, int e_v, int level) -> bool {
+        auto compute = [&](auto is_first, int i, int stage, int e_k, int e_v, int level) -> bool {
             constexpr bool FIRST = decltype(is_first)::value;
             const int kb = key0(i);
-            const unsigned char* step = ring_p + (i % STAGES) * KdShared<HD, MT>::STEP;
+            const unsigned char* step = ring_p + stage * KdShared<HD, MT>::STEP;
             // S^T: rows keys g, g + 8; columns query rows 2t, 2t + 1
             float sc[MT][4], s1[MT][4];   // two chains of products are half as long as one
 #pragma unroll
@@ -441,66 +448,86 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             const float kf = pow2i(e_k);
             // positions every token of the row sees need no mask
             const bool all = kb + 15 <= p0 && (kb + 15 < p.sinks || kb > row.len - 1 - p.window);
-            bool grew = false;
-#pragma unroll
-            for (int a = 0; a < MT; ++a)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int b = e & 1, j = kb + g + (e >> 1) * 8;
-                    sc[a][e] = __fmul_rn(sc[a][e], __fmul_rn(fac[a][b], kf));
-                    if (!all && !(pos[a][b] >= 0 && kv8_sees(pos[a][b], j, p.window, p.sinks))) sc[a][e] = -INFINITY;
-                    grew |= sc[a][e] > M[a][b] + KD_SLACK;
-                }
-            if (FIRST && __any_sync(0xffffffffu, grew)) {
+            float by[MT][2], x[MT][4];   // x: log2 of the weights
+            auto weigh = [&]() {
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        float m = fmaxf(sc[a][b], sc[a][b + 2]);
-#pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                        m = fmaxf(m, M[a][b]);
-                        const float f = M[a][b] == m ? 1.f : kv8_exp2(M[a][b] - m);   // -inf: 0
-                        M[a][b] = m;
-                        l[a][b] *= f;
-#pragma unroll
-                        for (int k = 0; k < NK; ++k) {
-                            o[a][k][b] *= f;
-                            o[a][k][b + 2] *= f;
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const int b = e & 1, j = kb + g + (e >> 1) * 8;
+                        x[a][e] = __fadd_rn(__fmul_rn(sc[a][e], by[a][b]), -M[a][b]);   // not fused: M is of rounded scores
+                        if (!all && !(pos[a][b] >= 0 && kv8_sees(pos[a][b], j, p.window, p.sinks))) x[a][e] = -INFINITY;
                     }
+            };
+            float high = -INFINITY, low = INFINITY;
+#pragma unroll
+            for (int a = 0; a < MT; ++a) by[a][0] = __fmul_rn(fac[a][0], kf), by[a][1] = __fmul_rn(fac[a][1], kf);
+            weigh();
+#pragma unroll
+            for (int a = 0; a < MT; ++a)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) high = fmaxf(high, x[a][e]), low = fminf(low, x[a][e]);
+            float w[MT][4], unit[MT][2];   // weights, and what the product with them is worth for each query row
+            bool deep = !FIRST, rest = false;
+            if (FIRST && __any_sync(0xffffffffu, high > KD_SHIFT + KD_SLACK || low < KD_SHIFT - KD_DEEP<FINE>)) {
+                if (__any_sync(0xffffffffu, high > KD_SHIFT + KD_SLACK)) {
+#pragma unroll
+                    for (int a = 0; a < MT; ++a)
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            float m = -INFINITY;
+#pragma unroll
+                            for (int e = b; e < 4; e += 2)
+                                if (x[a][e] > -INFINITY) m = fmaxf(m, __fmul_rn(sc[a][e], by[a][b]));
+#pragma unroll
+                            for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+                            m = fmaxf(__fadd_ru(floorf(m), -KD_SHIFT), M[a][b]);   // up: no weight above f16, whatever the scores
+                            const float f = kv8_exp2(M[a][b] - m);
+                            M[a][b] = m;
+                            l[a][b] *= f;
+#pragma unroll
+                            for (int k = 0; k < NK; ++k) {
+                                o[a][k][b] *= f;
+                                o[a][k][b + 2] *= f;
+                            }
+                        }
+                    weigh();
+                }
+#pragma unroll
+                for (int a = 0; a < MT; ++a)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) deep |= x[a][e] < KD_SHIFT - KD_DEEP<FINE> && x[a][e] > KD_SHIFT - KD_LAST;
+                deep = __any_sync(0xffffffffu, deep);
             }
-            // weights, and what the product with them is worth for each query row
-            float w[MT][4], unit[MT][2];
-            bool deep = false, rest = false;
 #pragma unroll
             for (int a = 0; a < MT; ++a)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float m = M[a][e & 1];
-                    sc[a][e] = __fadd_rn(sc[a][e], m == -INFINITY ? 0.f : -m);   // log2 of the weight
-                    w[a][e] = kv8_exp2(sc[a][e] + KD_SHIFT);
+                    w[a][e] = kv8_exp2(x[a][e]);
                     if constexpr (FIRST) l[a][e & 1] += w[a][e];
-                    deep |= sc[a][e] < -(float)KD_DEEP<FINE> && sc[a][e] > -KD_LAST;
                     unit[a][e & 1] = pow2i(e_v) * KD_UNIT;
                 }
-            if (!FIRST || __any_sync(0xffffffffu, deep)) {
-                constexpr float SPAN = KD_DEEP<FINE>;
+            if (deep) {
+                // y, of the step's own largest: it does not depend on M, so that the passes agree on who is whose
+                constexpr int SPAN = KD_SPAN<FINE>;
 #pragma unroll
                 for (int a = 0; a < MT; ++a)
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
-                        float m = fmaxf(sc[a][b], sc[a][b + 2]);
+                        float s[2], m;
 #pragma unroll
-                        for (int x = 4; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-                        const float top = fmaxf(floorf(m), -KD_LAST), floor = -SPAN * (level + 1);
-                        unit[a][b] *= pow2i((int)top) * pow2i(-KD_DEEP<FINE> * level);
+                        for (int e = 0; e < 2; ++e) s[e] = x[a][b + 2 * e] == -INFINITY ? -INFINITY : __fmul_rn(sc[a][b + 2 * e], by[a][b]);
+                        m = fmaxf(s[0], s[1]);
 #pragma unroll
-                        for (int e = b; e < 4; e += 2) {
-                            const float x = __fadd_rn(sc[a][e], -top);
-                            w[a][e] = kv8_exp2(x + (KD_SHIFT + SPAN * level));
-                            if (x < floor || (!FIRST && x >= floor + SPAN)) w[a][e] = 0.f;
-                            rest |= x < floor && sc[a][e] > -KD_LAST;
+                        for (int i = 4; i < 32; i <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, i));
+                        const float top = m == -INFINITY ? 0.f : floorf(m), up = KD_SHIFT + 1.f + SPAN * level, floor = -SPAN * (level + 1.f);
+                        const float down = top - M[a][b] - up;   // M is a whole number: so is this
+                        unit[a][b] *= m == -INFINITY || down < -126.f ? 0.f : pow2i((int)down);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float y = __fadd_rn(s[e], -top);
+                            w[a][b + 2 * e] = y < floor || (!FIRST && y >= floor + SPAN) ? 0.f : kv8_exp2(y + up);
+                            rest |= y < floor && x[a][b + 2 * e] > KD_SHIFT - KD_LAST;
                         }
                     }
                 rest = __any_sync(0xffffffffu, rest);
@@ -525,13 +552,14 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
                     const int j = kb + 2 * t + (x & 1) + (x >> 1) * 8;
                     bool any = false;
                     for (int n = max(-p0, 0); n < row.n; ++n) any |= kv8_sees(p0 + n, j, p.window, p.sinks);
-                    if (!any)
+                    if (!any) {
 #pragma unroll
                         for (int d = 0; d < HD / 32; ++d) v[x][d] = 0u;
-                    else if (row.n > 1)
+                    } else if (row.n > 1) {
 #pragma unroll
                         for (int d = 0; d < HD / 32; ++d)
                             seen_nan[x] |= ((v[x][d] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                    }
                 }
             }
             if (__any_sync(0xffffffffu, seen_nan[0] | seen_nan[1] | seen_nan[2] | seen_nan[3])) {
@@ -613,6 +641,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             return rest;
         };
 
+        uint32_t far = 0;   // the steps with weights that wait: step i has bit i % 32 of lane i / 32 % 32
         for (int i = 0; i < mine; ++i) {
             copy_next();
             copy_wait<STAGES - 1>();   // step i's group is complete
@@ -621,12 +650,41 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
             const int there = __shfl_sync(0xffffffffu, now ? place : place_before, i & 31);
             const int e_k = __shfl_sync(0xffffffffu, now ? ke : ke_before, i & 31) - 127;
             const int e_v = __shfl_sync(0xffffffffu, now ? ve : ve_before, i & 31) - 127;
-            if (there >= 0 && compute(std::true_type{}, i, e_k, e_v, 0))
-                for (int level = 1; compute(std::false_type{}, i, e_k, e_v, level); ++level) {}
+            if (there >= 0 && compute(std::true_type{}, i, i % STAGES, e_k, e_v, 0) && lane == (i >> 5 & 31)) far |= 1u << (i & 31);
             __syncwarp();              // the stage may be overwritten
         }
         check_scales();
         copy_wait<0>();
+        // The weights that wait: their steps again, 32 at a time.  Within the loop above the code of this would cost every
+        // step (the compiler no longer overlaps them: 32 rows x 32k 235 us, so 225)
+        if (__any_sync(0xffffffffu, far))
+            for (int first = 0; first < mine; first += 32) {
+                const uint32_t marks = __shfl_sync(0xffffffffu, far, first >> 5 & 31);
+                if (!marks) continue;
+                next32(first);
+                uint32_t rest = marks;
+                int copied = 0, done = 0;
+                auto copy_marked = [&]() {
+                    if (rest) copy_step(__ffs(rest) - 1, copied++ % STAGES);
+                    rest &= rest - 1;
+                    copy_commit();
+                };
+#pragma unroll
+                for (int x = 0; x < STAGES - 1; ++x) copy_marked();
+                for (uint32_t m = marks; m; m &= m - 1) {
+                    const int l = __ffs(m) - 1;
+                    copy_marked();
+                    copy_wait<STAGES - 1>();
+                    __syncwarp();
+                    const int there = __shfl_sync(0xffffffffu, place, l);
+                    const int e_k = __shfl_sync(0xffffffffu, ke, l) - 127, e_v = __shfl_sync(0xffffffffu, ve, l) - 127;
+                    const int stage = done++ % STAGES;
+                    if (there >= 0)
+                        for (int level = 1; compute(std::false_type{}, first + l, stage, e_k, e_v, level); ++level) {}
+                    __syncwarp();   // the stage may be overwritten
+                }
+                copy_wait<0>();
+            }
         __syncthreads();   // every warp is done with its ring
 
         // join the warps: the largest maximum, then sums in warp order
@@ -637,7 +695,7 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[a][b] += __shfl_xor_sync(0xffffffffu, l[a][b], x);
                 if (g == 0) {
-                    m_s[warp][a * 8 + 2 * t + b] = M[a][b];
+                    m_s[warp][a * 8 + 2 * t + b] = M[a][b] == KD_NONE ? -INFINITY : M[a][b];
                     l_s[warp][a * 8 + 2 * t + b] = l[a][b];
                 }
             }
@@ -768,19 +826,23 @@ __global__ void __launch_bounds__(32 * KdShared<HD, MT>::W, KdShared<HD, MT>::CT
 }
 
 // Tokens of a row that a launch takes, and the launches.  A prompt kernel's CTA has 256 query rows, so drafts of a large
-// batch leave most of it idle: there the stream of K and V, read two or three times, is shorter (4 query heads a K/V
-// head; 8 rows x 8k: 8 tokens 75 us in two launches, 106 by the prompt kernel; 16 rows x 32k: 8 tokens 271 and 645, 12
-// tokens 397 in three and 645).  Where few heads let the prompt kernel split the positions over the SMs it is as fast as
-// one launch here (one row x 8k: 8 tokens 23 us, 4 tokens 23.5), and for short caches a launch is what counts
+// batch leave most of it idle: there the stream of K and V, read two or three times, may be shorter.  It is cut evenly
+// where the lengths differ, the prompt kernel's time is the longest row's.  Measured, here and by the prompt kernel, 4
+// query heads a K/V head, 8 tokens (two launches), rows of equal and of unequal lengths: 16 rows x 32k bf16 542 and 569,
+// 333 and 564, fp32 610 and 927, 373 and 906; 32 rows x 4k bf16 182 and 161, 124 and 143, fp32 202 and 259, 138 and 220;
+// 8 rows x 8k, where the prompt kernel splits the positions over the SMs, bf16 115 and 85, 74 and 81, fp32 128 and 133,
+// 82 and 131.  12 tokens (three), 16 rows x 32k: bf16 814 and 577, 494 and 573, fp32 916 and 930, 555 and 909.  With one
+// row x 8k it is as fast as one launch here (8 tokens 25 us, 4 tokens 26), and for short caches a launch is what counts
 int decode_tokens(const Kv8Attend& p) { return p.b.max_new * p.G <= 16 ? p.b.max_new : 16 / p.G; }
 int decode_launches(const Kv8Attend& p, int num_sms) {
     const int each = decode_tokens(p);
     if (each == p.b.max_new) return 1;
-    if (each == 0 || p.b.max_new > 3 * each) return 0;
+    const bool fine = p.dtype == W_F32;
+    if (each == 0 || p.b.max_new > (fine ? 3 : 2) * each) return 0;
     const long long cap = (long long)p.c.ppr * p.c.page, win = (long long)p.window + p.sinks + p.b.max_new;
     const long long heads = (long long)p.c.rows * p.c.Hkv;
     const int n = (p.b.max_new + each - 1) / each;
-    return (win < cap ? win : cap) >= 2048 && (n == 2 ? 3 : 2) * heads >= num_sms ? n : 0;
+    return (win < cap ? win : cap) >= 2048 && (fine && n == 2 ? 3 : 2) * heads >= num_sms ? n : 0;
 }
 int decode_sets(const Kv8Attend& p) { return (decode_tokens(p) * p.G + 7) / 8; }
 
