@@ -37,8 +37,8 @@
 // with one warp for both tiles those trips, not the products, filled its time
 // (8191 tokens: 602 -> 543 us; K's and V's waits as one: 539).
 //
-// Bound, measured: 8191 tokens 620 us, 46 % of the measured bf16 rate; 2 x 64 fp32
-// tokens over 32k 109 us.  The chain of a tile's steps binds it -- P to S of the
+// Bound, measured: 8191 tokens 623 us, 46 % of the measured bf16 rate; 2 x 64 fp32
+// tokens over 32k 108 us with 64 dims, 187 with 128.  The chain of a tile's steps binds it -- P to S of the
 // tile after the next to P again -- and the hand-overs in it.  With one f16 part a
 // weight (540 us) a K/V tile took about 2200 cycles, of which the tensor core needed
 // 1280 (now 1790) and a softmax warp 1700.  Leaving out half of the MMAs, the
@@ -745,19 +745,21 @@ __global__ void __launch_bounds__(KP_THREADS, 1) k_kv8_prompt(const Kv8Attend p,
                 }
             }
             const float sub = (M == -INFINITY ? 0.f : M) - KP_SHIFT;
-            const uint64_t minus2 = pair(-1.f, -1.f);
+            const uint64_t minus2 = pair(-1.f, -1.f), less2 = pair(-sub, -sub);
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
                 uint32_t hi[16], low[16], third[FINE ? 16 : 1];
 #pragma unroll
                 for (int b = 0; b < 2; ++b) {
-                    const float mu = mul[2 * q + b], plus = add[2 * q + b] - sub;
-                    const uint64_t mul2 = pair(mu, mu), plus2 = pair(plus, plus);
+                    const float mu = mul[2 * q + b], plus = add[2 * q + b];
+                    const uint64_t by = pair(mu, mu), plus2 = pair(plus, plus);
                     uint64_t sum0 = 0, sum1 = 0;
 #pragma unroll
                     for (int e = 0; e < 16; e += 2) {
                         float w0, w1;
-                        unpair(fma2(pair(__uint_as_float(v[q][16 * b + e]), __uint_as_float(v[q][16 * b + e + 1])), mul2, plus2), w0, w1);
+                        // rounded before M is subtracted: M is a rounded score, and past 2^24 an unrounded one may lie far from
+                        // it.  (mul.f32x2 and add.f32x2 would be fused by the assembler; a sum with what it does not know is not)
+                        unpair(add2(fma2(pair(__uint_as_float(v[q][16 * b + e]), __uint_as_float(v[q][16 * b + e + 1])), by, plus2), less2), w0, w1);
                         w0 = kv8_exp2(w0);
                         w1 = kv8_exp2(w1);
                         if (e == 0) sum0 = pair(w0, w1);

@@ -200,3 +200,27 @@ def test_nan_behind_a_thousand_tiles():
     nan[:30, 0, 3] = True            # token t sees positions from first + t - window + 1 on: t < 30 see `early`
     nan[:, 1, 7] = True
     assert torch.equal(torch.isnan(out), nan) and bool((out[~nan] == 1).all())
+
+
+@pytest.mark.parametrize("power", [10, 20, 24, 25, 27, 30, 40, 60])
+@pytest.mark.parametrize("rows,dim", SHAPES, ids=IDS)
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_one_score_far_above(power, rows, dim, dtype):
+    """Position 5 scores 1.25 * 2^power / sqrt(dim), the others 0: the results are its V, also where scores lie further
+    apart than 1 in fp32."""
+    K, V, table, q, kv_len, starts = build(rows, 4, 2, dim, 64, 16, 17, dtype)
+    q = torch.zeros_like(q)
+    q[..., 0] = 1.0
+    K.x.zero_()
+    K.e.zero_()
+    K.x[table[:, 0].long(), :, 5, 0] = 1.25
+    K.e[table[:, 0].long(), :, 0] = power
+    cache = gpu_cache(K, V, table)
+    out = cache.attend(q.cuda(), kv_len.cuda(), starts.cuda(), max_new=max(n for _, n in rows))
+    cache.check()
+    for r, (l, n) in enumerate(rows):
+        v = V.values(table[r].long())[:, 5].repeat_interleave(2, 0)
+        off = (out[starts[r]:starts[r + 1]].double().cpu() - v)[max(5 - (l - n), 0):].abs()
+        # the weight and the sum are one number; its inverse and the products are rounded: four half steps of fp32, then the
+        # result's own (a value of 4 bits, so bf16 has it)
+        assert bool((off <= v.abs() * 4 * 2.0 ** -24).all() if dtype == F32 else (off == 0).all())
