@@ -21,7 +21,8 @@
 // may lie far apart, so small weights have to keep their digits: f16 holds 20 bits
 // below the largest, bf16 what fp32 does.  It has 8 bits where f16 has 11, hence two
 // parts for a weight, and that is what bf16 prompts pay for it (8191 tokens: one
-// f16 part 540 us, two bf16 parts 620; the second product itself costs 15 of them).
+// f16 part 540 us, two bf16 parts 620; the second product itself costs 15 of them;
+// scores rounded before the maximum is subtracted 20 more).
 // 64 positions rather than 128: with 128 there is room for one S a query tile,
 // and product and softmax wait for one another (8191 tokens: 682 -> 633 us with
 // the change, although S = Q K^T of 64 columns reads Q from shared memory twice as
@@ -37,8 +38,8 @@
 // with one warp for both tiles those trips, not the products, filled its time
 // (8191 tokens: 602 -> 543 us; K's and V's waits as one: 539).
 //
-// Bound, measured: 8191 tokens 623 us, 46 % of the measured bf16 rate; 2 x 64 fp32
-// tokens over 32k 108 us with 64 dims, 187 with 128.  The chain of a tile's steps binds it -- P to S of the
+// Bound, measured: 8191 tokens 640 us, 45 % of the measured bf16 rate; 2 x 64 fp32
+// tokens over 32k 111 us with 64 dims, 195 with 128.  The chain of a tile's steps binds it -- P to S of the
 // tile after the next to P again -- and the hand-overs in it.  With one f16 part a
 // weight (540 us) a K/V tile took about 2200 cycles, of which the tensor core needed
 // 1280 (now 1790) and a softmax warp 1700.  Leaving out half of the MMAs, the
@@ -78,7 +79,7 @@ constexpr int KP_REGS_SOFTMAX = 120, KP_REGS_CONV = 88, KP_REGS_MMA = 64;
 constexpr int KP_QPANEL = KP_ROWS * 128, KP_PANEL = KP_KEYS * 128;   // bytes of 64 dims of a query tile, of a K or V tile
 constexpr float KP_SLACK = 8.f, KP_SHIFT = -8.f;   // log2: maximum may lag; weights carry 2^-8, so none is above 1
 // fp32 q: tiles between two folds of O into memory (64 tokens over 32k, relative error and time: 12 2.2e-6, 101 us; 8
-// 1.6e-6, 106; 6 1.2e-6, 109.  fp32 sums in the plain order: 2.9e-6, but 0.9e-6 over 2000 positions)
+// 1.6e-6, 106; 6 1.2e-6, 109, before scores were rounded first.  fp32 sums in the plain order: 2.9e-6, but 0.9e-6 over 2000 positions)
 constexpr int KP_FOLD = 6;
 constexpr int KP_META = 8;                // tiles whose scales are held
 constexpr int KP_GROUPS = KP_KEYS / 16, KP_BATCH = 32 / KP_GROUPS;   // 16-position groups of a tile; tiles that a warp's lanes know of
