@@ -157,7 +157,7 @@ class KV8Cache:
 
     def check(self) -> None:
         """Wait for all work on the device so far, on whatever stream and in whatever graph, and raise DecError if a call
-        met an entry out of range since the last check."""
+        met an entry out of range since the last check.  Not while any stream is being captured."""
         torch.cuda.synchronize(self.device)
         bits = int(self._err.item())
         if bits:

@@ -224,3 +224,28 @@ def test_one_score_far_above(power, rows, dim, dtype):
         # the weight and the sum are one number; its inverse and the products are rounded: four half steps of fp32, then the
         # result's own (a value of 4 bits, so bf16 has it)
         assert bool((off <= v.abs() * 4 * 2.0 ** -24).all() if dtype == F32 else (off == 0).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_steps_that_wait_in_long_pieces(dtype):
+    """640 heads of 131072 positions: a warp has more steps than it has marks.  One position of each head, at other places,
+    scores 30 nats above the others and holds no V; the 15 others of its step are a ten-thousandth of the result."""
+    from graph_replay_gb300 import KV8Cache
+    heads, length = 640, 1 << 17
+    cache = KV8Cache.empty(1, length, heads, 64)
+    cache.v.fill_(0x38)                                    # 1.0
+    h = torch.arange(heads, device="cuda")
+    at = (h * 7919 + 5) * 131 % length
+    cache.k[0, h, at, 0] = int(torch.tensor(120.0).to(torch.float8_e4m3fn).view(torch.uint8))
+    cache.k_scale[0, h, at // 64] = 125                    # 120 / 4
+    cache.v[0, h, at] = 0
+    q = torch.zeros(1, heads, 64, dtype=dtype, device="cuda")
+    q[..., 0] = 8.0                                        # 8 * 30 / sqrt(64)
+    out = cache.attend(q, torch.tensor([length], dtype=torch.int32, device="cuda"))
+    cache.check()
+    w = (length - 1) * math.exp(-30.0)
+    want = w / (1 + w)
+    # the exponential and its argument of 43 in fp32 (2^-21 + 43 * 2^-24), the sums (131072 equal terms, each rounding at
+    # most half a step of the sum: sqrt(n) * 2^-24), the type's half step; with fp32 a fifth of what the 15 weigh
+    tol = want * (2.0 ** -21 + 43 * 2.0 ** -24 + math.sqrt(length) * 2.0 ** -24 + torch.finfo(dtype).eps / 2)
+    assert float((out.double() - want).abs().max()) <= tol
