@@ -35,6 +35,9 @@ DEC_KV_CONTIGUOUS = 0
 DEC_KV_PAGED = 1
 DEC_STRATEGY_GRAPH = 0
 DEC_STRATEGY_PERSISTENT = 1
+DEC_ACT_SILU = 0
+DEC_ACT_GELU_TANH = 1
+DEC_W4_COUNTER_BYTES = 65536
 DEC_SWEEP_CAP = 0
 DEC_SWEEP_POS = 1
 
@@ -91,6 +94,20 @@ class dec_kv8_attn(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class dec_w4_weight(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("n", ctypes.c_int32), ("k", ctypes.c_int32),
+                ("group", ctypes.c_int32), ("device", ctypes.c_int32)]
+
+
+class dec_w4_call(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("gain", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("out", ctypes.c_void_p),
+                ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int32), ("x_dtype", ctypes.c_int32), ("gain_dtype", ctypes.c_int32),
+                ("out_dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("eps", ctypes.c_double), ("err", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
+
+
 # every symbol the header declares: (name, restype, argtypes)
 _P = ctypes.c_void_p
 _I32 = ctypes.c_int32
@@ -126,6 +143,13 @@ _SIG = [
                                       ctypes.POINTER(dec_kv8_attn), _P]),
     ("dec_kv8_workspace", ctypes.c_int, [ctypes.POINTER(dec_kv8_cache), ctypes.POINTER(dec_kv8_batch),
                                          ctypes.POINTER(dec_kv8_attn), ctypes.POINTER(ctypes.c_size_t)]),
+    ("dec_w4_quantize", ctypes.c_int, [ctypes.POINTER(dec_w4_weight), _P, _I64, _I32, _P]),
+    ("dec_w4_dequantize", ctypes.c_int, [ctypes.POINTER(dec_w4_weight), _P, _I64, _I32, _P]),
+    ("dec_w4_linear", ctypes.c_int, [ctypes.POINTER(dec_w4_weight), ctypes.POINTER(dec_w4_call), _P]),
+    ("dec_w4_glu", ctypes.c_int, [ctypes.POINTER(dec_w4_weight), ctypes.POINTER(dec_w4_weight), ctypes.POINTER(dec_w4_call),
+                                  _P]),
+    ("dec_w4_workspace", ctypes.c_int, [ctypes.POINTER(dec_w4_weight), ctypes.POINTER(dec_w4_weight),
+                                        ctypes.POINTER(dec_w4_call), ctypes.POINTER(ctypes.c_size_t)]),
     ("dec_logits_ptr", ctypes.c_int, [_P, ctypes.POINTER(_P)]),
     ("dec_stream", ctypes.c_int, [_P, ctypes.POINTER(_P)]),
     ("dec_stats_get", ctypes.c_int, [_P, ctypes.POINTER(dec_stats)]),
@@ -327,6 +351,28 @@ def dec_kv8_attend(cache: dec_kv8_cache, batch: dec_kv8_batch, attn: dec_kv8_att
 def dec_kv8_workspace(cache: dec_kv8_cache, batch: dec_kv8_batch, attn: dec_kv8_attn) -> int:
     n = ctypes.c_size_t()
     check(None, lib().dec_kv8_workspace(cache, batch, attn, ctypes.byref(n)))
+    return n.value
+
+
+def dec_w4_quantize(w: dec_w4_weight, src, stride: int, dtype: int, stream) -> None:
+    check(None, lib().dec_w4_quantize(w, src, stride, dtype, stream))
+
+
+def dec_w4_dequantize(w: dec_w4_weight, dst, stride: int, dtype: int, stream) -> None:
+    check(None, lib().dec_w4_dequantize(w, dst, stride, dtype, stream))
+
+
+def dec_w4_linear(w: dec_w4_weight, call: dec_w4_call, stream) -> None:
+    check(None, lib().dec_w4_linear(w, call, stream))
+
+
+def dec_w4_glu(gate: dec_w4_weight, up: dec_w4_weight, call: dec_w4_call, stream) -> None:
+    check(None, lib().dec_w4_glu(gate, up, call, stream))
+
+
+def dec_w4_workspace(w: dec_w4_weight, up, call: dec_w4_call) -> int:
+    n = ctypes.c_size_t()
+    check(None, lib().dec_w4_workspace(w, up, call, ctypes.byref(n)))
     return n.value
 
 

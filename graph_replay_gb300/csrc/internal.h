@@ -176,6 +176,56 @@ size_t kv8_decode_floats(const Kv8Attend& p, int num_sms);   // of workspace
 cudaError_t kv8_prompt_launch(const Kv8Attend& p, int num_sms, cudaStream_t s);
 size_t kv8_prompt_floats(const Kv8Attend& p, int num_sms);
 
+// ---------------- 4-bit weights (w4*.cu) ----------------
+struct W4Matrix {              // a dec_w4_weight that passed its checks
+    const void* codes;         // [n, k / 2]
+    const void* scales;        // [n, k / group] bf16
+    int n, k, group;
+};
+cudaError_t w4_quantize_launch(const W4Matrix& w, const void* src, long long stride, bool f32, int num_sms, cudaStream_t s);
+cudaError_t w4_values_launch(const W4Matrix& w, void* dst, long long stride, bool f32, int num_sms, cudaStream_t s);
+// out[t, n] = residual[t, n] + sum_k W[n, k] a[t, k] over up to three matrices of one k and group, stacked; with glu, over a
+// gate and an up matrix of one shape, out[t, n] = act(gate[t, n]) * up[t, n].  a = x, or RMSNorm(x) with a gain
+struct W4Call {
+    W4Matrix w[3];
+    int nw;
+    bool glu;
+    int act;                   // DEC_ACT_*
+    int tokens;
+    const void* x;             // [tokens, k]
+    const void* gain;          // [k] or null: no norm
+    const void* residual;      // [tokens, n] or null
+    void* out;                 // [tokens, n]
+    long long x_stride, residual_stride, out_stride;   // elements
+    bool x_f32, gain_f32, out_f32;                      // else bf16; the residual has out's type
+    float eps;
+    unsigned* err;
+    int n() const { return glu ? w[0].n : w[0].n + (nw > 1 ? w[1].n : 0) + (nw > 2 ? w[2].n : 0); }
+    int k() const { return w[0].k; }
+    int group() const { return w[0].group; }
+    int parts() const { return x_f32 || gain ? 2 : 1; }   // fp16 parts of an activation
+};
+struct W4Gemv {                // how w4_gemv.cu runs a call of few tokens
+    W4Call c;
+    int block;                 // tokens of a CTA
+    int wk;                    // warps along k
+    int ks;                    // CTAs along k
+    int grid, rows;            // CTAs along n, output rows of each (the last may have fewer)
+    int stages;                // ring stages
+    int bufs;                  // buffers of the cross-warp sums
+    size_t smem;
+    float* part;               // ks > 1: [ks][tokens][n or 2 n]
+    unsigned* count;           // ks > 1: [blocks of tokens][grid], zero between calls
+    unsigned long long* amax;  // logits of a decode step: [tokens] argmax keys, or null
+    unsigned* nonfinite;       // [tokens]
+    unsigned long long* trace;
+    int trace_id;
+};
+cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms);
+size_t w4_gemv_floats(const W4Gemv& g);      // of g.part
+size_t w4_gemv_counters(const W4Gemv& g);    // of g.count
+cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl);
+
 // ---------------- split-KV masked decode attention ----------------
 struct AttnParams {
     const float* qkv;      // [R, qkv_stride]: q [Hq*hd], k [Hkv*hd], v [Hkv*hd] (fp32, pre-RoPE)

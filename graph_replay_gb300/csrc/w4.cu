@@ -1,0 +1,237 @@
+// w4.cu -- the C ABI of the 4-bit weights: argument checks and launches on the
+// caller's stream.  No handle, no allocation, no wait: each call only launches
+// kernels, so it can be recorded into a graph.
+#include <limits.h>
+#include <stdarg.h>
+#include <stdio.h>
+
+#include <cmath>
+
+#include "graphdec.h"
+#include "internal.h"
+
+using namespace gd;
+
+namespace {
+
+int refuse(int code, const char* fmt, ...) {
+    char buf[256];
+    va_list ap;
+    va_start(ap, fmt);
+    vsnprintf(buf, sizeof buf, fmt, ap);
+    va_end(ap);
+    set_call_message(buf);
+    return code;
+}
+
+bool aligned(const void* p, unsigned to) { return ((uintptr_t)p & (to - 1)) == 0; }
+
+// the caller's current device is put back when the call ends
+struct OnDevice {
+    int prev = -1, dev;
+    cudaError_t e;
+    explicit OnDevice(int device) : dev(device) {
+        e = cudaGetDevice(&prev);
+        if (e == cudaSuccess && prev != dev) e = cudaSetDevice(dev);
+    }
+    ~OnDevice() {
+        if (prev >= 0 && prev != dev) cudaSetDevice(prev);
+    }
+};
+
+int launched(cudaError_t e, const char* what) {
+    if (e == cudaSuccess) return DEC_OK;
+    cudaGetLastError();
+    return refuse(DEC_E_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
+}
+
+int sms_of(int device, int* n) {
+    const cudaError_t e = cudaDeviceGetAttribute(n, cudaDevAttrMultiProcessorCount, device);
+    if (e == cudaSuccess) return DEC_OK;
+    cudaGetLastError();
+    return refuse(DEC_E_CUDA, "device %d: %s", device, cudaGetErrorString(e));
+}
+
+int check_weight(const char* what, const dec_w4_weight* w, W4Matrix* out) {
+    if (!w) return refuse(DEC_E_INVALID, "%s is NULL", what);
+    if (!w->codes || !w->scales) return refuse(DEC_E_INVALID, "%s: codes and scales are required", what);
+    if (!aligned(w->codes, 16) || !aligned(w->scales, 2))
+        return refuse(DEC_E_INVALID, "%s: codes must be 16-byte, scales 2-byte aligned", what);
+    if (w->n < 1 || w->k < 1) return refuse(DEC_E_INVALID, "%s: n and k must be >= 1", what);
+    if (w->group != 32 && w->group != 64 && w->group != 128)
+        return refuse(DEC_E_UNSUPPORTED, "%s: group %d unsupported (32, 64 or 128)", what, w->group);
+    if (w->k % w->group) return refuse(DEC_E_INVALID, "%s: k must be a multiple of group", what);
+    if (w->k > (1 << 20) || (int64_t)w->n * w->k > (1ll << 33))
+        return refuse(DEC_E_UNSUPPORTED, "%s: at most 2^20 columns and 2^33 weights", what);
+    if (w->device < 0) return refuse(DEC_E_INVALID, "%s: device must be >= 0", what);
+    *out = W4Matrix{w->codes, w->scales, w->n, w->k, w->group};
+    return DEC_OK;
+}
+
+int check_dtype(const char* what, int dtype, bool* f32) {
+    if (dtype != DEC_DTYPE_F32 && dtype != DEC_DTYPE_BF16)
+        return refuse(DEC_E_INVALID, "%s must be DEC_DTYPE_F32 or DEC_DTYPE_BF16", what);
+    *f32 = dtype == DEC_DTYPE_F32;
+    return DEC_OK;
+}
+
+// a matrix that is read or written in 16-byte pieces
+int check_rows(const char* what, const void* p, int64_t stride, int64_t cols, bool f32) {
+    if (!p) return refuse(DEC_E_INVALID, "%s is NULL", what);
+    if (!aligned(p, 16)) return refuse(DEC_E_INVALID, "%s must be 16-byte aligned", what);
+    if (stride < cols || stride > (1ll << 40) || (stride * (f32 ? 4 : 2)) % 16)
+        return refuse(DEC_E_INVALID, "%s: the stride must hold a row and be a multiple of 16 bytes", what);
+    return DEC_OK;
+}
+
+// a matrix that is read or written one value at a time
+int check_values(const char* what, const void* p, int64_t stride, int64_t cols, bool f32) {
+    if (!p) return refuse(DEC_E_INVALID, "%s is NULL", what);
+    if (!aligned(p, f32 ? 4 : 2)) return refuse(DEC_E_INVALID, "%s must be aligned to its type", what);
+    if (stride < cols || stride > (1ll << 40)) return refuse(DEC_E_INVALID, "%s: the stride must hold a row", what);
+    return DEC_OK;
+}
+
+int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* c, W4Call* p) {
+    int rc;
+    *p = W4Call{};
+    if ((rc = check_weight(glu ? "gate" : "w", w, &p->w[0])) != DEC_OK) return rc;
+    p->nw = 1;
+    p->glu = glu;
+    if (glu) {
+        if ((rc = check_weight("up", up, &p->w[1])) != DEC_OK) return rc;
+        if (up->n != w->n || up->k != w->k || up->group != w->group || up->device != w->device)
+            return refuse(DEC_E_INVALID, "gate and up must have one shape, group and device");
+        p->nw = 2;
+    }
+    if (!c) return refuse(DEC_E_INVALID, "call is NULL");
+    if (c->tokens < 0) return refuse(DEC_E_INVALID, "tokens must be >= 0");
+    if ((int64_t)c->tokens * w->n > INT_MAX) return refuse(DEC_E_UNSUPPORTED, "tokens * n: at most 2^31 - 1");
+    if ((int64_t)c->tokens * w->k > INT_MAX) return refuse(DEC_E_UNSUPPORTED, "tokens * k: at most 2^31 - 1");
+    if ((rc = check_dtype("x_dtype", c->x_dtype, &p->x_f32)) != DEC_OK) return rc;
+    if ((rc = check_dtype("out_dtype", c->out_dtype, &p->out_f32)) != DEC_OK) return rc;
+    if (c->gain) {
+        if ((rc = check_dtype("gain_dtype", c->gain_dtype, &p->gain_f32)) != DEC_OK) return rc;
+        if (!aligned(c->gain, 16)) return refuse(DEC_E_INVALID, "gain must be 16-byte aligned");
+        if (!(c->eps >= 0.0) || !std::isfinite((float)c->eps)) return refuse(DEC_E_INVALID, "eps must be finite and >= 0");
+    }
+    if (glu) {
+        if (c->act != DEC_ACT_SILU && c->act != DEC_ACT_GELU_TANH)
+            return refuse(DEC_E_INVALID, "act must be DEC_ACT_SILU or DEC_ACT_GELU_TANH");
+        if (c->residual) return refuse(DEC_E_INVALID, "dec_w4_glu takes no residual");
+    }
+    if (!c->err || !aligned(c->err, 4)) return refuse(DEC_E_INVALID, "err is required");
+    if (c->tokens > 0) {
+        if ((rc = check_rows("x", c->x, c->x_stride, w->k, p->x_f32)) != DEC_OK) return rc;
+        if ((rc = check_values("out", c->out, c->out_stride, w->n, p->out_f32)) != DEC_OK) return rc;
+        if (c->residual) {
+            if ((rc = check_values("residual", c->residual, c->residual_stride, w->n, p->out_f32)) != DEC_OK) return rc;
+            if (c->residual == c->out && c->residual_stride != c->out_stride)
+                return refuse(DEC_E_INVALID, "a residual that is out must have its stride");
+        }
+    }
+    p->act = c->act;
+    p->tokens = c->tokens;
+    p->x = c->x;
+    p->gain = c->gain;
+    p->residual = c->residual;
+    p->out = c->out;
+    p->x_stride = c->x_stride;
+    p->residual_stride = c->residual_stride;
+    p->out_stride = c->out_stride;
+    p->eps = (float)c->eps;
+    p->err = c->err;
+    return DEC_OK;
+}
+
+// the workspace is used by plans that split k over CTAs only
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+// how a call runs, and what of the workspace it uses behind the counters
+struct Plan {
+    W4Gemv gemv;
+    size_t bytes;
+};
+
+cudaError_t plan_of(const W4Call& c, int sms, Plan* p) {
+    p->gemv = W4Gemv{};
+    p->gemv.c = c;
+    const cudaError_t e = w4_gemv_plan(&p->gemv, sms);
+    const size_t floats = w4_gemv_floats(p->gemv);
+    p->bytes = floats ? DEC_W4_COUNTER_BYTES + round256(sizeof(float) * floats) : 0;
+    return e;
+}
+
+int run(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* call, void* stream) {
+    W4Call c;
+    int rc, sms;
+    if ((rc = check_call(w, up, glu, call, &c)) != DEC_OK) return rc;
+    if (c.tokens == 0) return DEC_OK;
+    const char* what = glu ? "dec_w4_glu" : "dec_w4_linear";
+    OnDevice on(w->device);
+    if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
+    if ((rc = sms_of(w->device, &sms)) != DEC_OK) return rc;
+    Plan p;
+    if ((rc = launched(plan_of(c, sms, &p), what)) != DEC_OK) return rc;
+    if (p.bytes && (!call->workspace || call->workspace_bytes < p.bytes))
+        return refuse(DEC_E_OOM, "workspace of %zu bytes is smaller than the %zu needed",
+                      call->workspace ? call->workspace_bytes : (size_t)0, p.bytes);
+    if (!aligned(call->workspace, 256)) return refuse(DEC_E_INVALID, "workspace must be 256-byte aligned");
+    p.gemv.count = (unsigned*)call->workspace;
+    p.gemv.part = (float*)((char*)call->workspace + DEC_W4_COUNTER_BYTES);
+    return launched(w4_gemv_launch(p.gemv, (cudaStream_t)stream, false), what);
+}
+
+}  // namespace
+
+extern "C" {
+
+int dec_w4_quantize(const dec_w4_weight* w, const void* src, int64_t src_stride, int32_t dtype, void* stream) {
+    W4Matrix m;
+    bool f32;
+    int rc, sms;
+    if ((rc = check_weight("w", w, &m)) != DEC_OK) return rc;
+    if ((rc = check_dtype("dtype", dtype, &f32)) != DEC_OK) return rc;
+    if ((rc = check_rows("src", src, src_stride, w->k, f32)) != DEC_OK) return rc;
+    OnDevice on(w->device);
+    if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
+    if ((rc = sms_of(w->device, &sms)) != DEC_OK) return rc;
+    return launched(w4_quantize_launch(m, src, src_stride, f32, sms, (cudaStream_t)stream), "dec_w4_quantize");
+}
+
+int dec_w4_dequantize(const dec_w4_weight* w, void* dst, int64_t dst_stride, int32_t dtype, void* stream) {
+    W4Matrix m;
+    bool f32;
+    int rc, sms;
+    if ((rc = check_weight("w", w, &m)) != DEC_OK) return rc;
+    if ((rc = check_dtype("dtype", dtype, &f32)) != DEC_OK) return rc;
+    if ((rc = check_rows("dst", dst, dst_stride, w->k, f32)) != DEC_OK) return rc;
+    OnDevice on(w->device);
+    if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
+    if ((rc = sms_of(w->device, &sms)) != DEC_OK) return rc;
+    return launched(w4_values_launch(m, dst, dst_stride, f32, sms, (cudaStream_t)stream), "dec_w4_dequantize");
+}
+
+int dec_w4_workspace(const dec_w4_weight* w, const dec_w4_weight* up, const dec_w4_call* call, size_t* bytes) {
+    if (!bytes) return refuse(DEC_E_INVALID, "bytes is NULL");
+    W4Call c;
+    int rc, sms;
+    if ((rc = check_call(w, up, up != nullptr, call, &c)) != DEC_OK) return rc;
+    *bytes = 0;
+    if (c.tokens == 0) return DEC_OK;
+    OnDevice on(w->device);
+    if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
+    if ((rc = sms_of(w->device, &sms)) != DEC_OK) return rc;
+    Plan p;
+    if ((rc = launched(plan_of(c, sms, &p), "dec_w4_workspace")) != DEC_OK) return rc;
+    *bytes = p.bytes;
+    return DEC_OK;
+}
+
+int dec_w4_linear(const dec_w4_weight* w, const dec_w4_call* call, void* stream) { return run(w, nullptr, false, call, stream); }
+
+int dec_w4_glu(const dec_w4_weight* gate, const dec_w4_weight* up, const dec_w4_call* call, void* stream) {
+    return run(gate, up, true, call, stream);
+}
+
+}  // extern "C"

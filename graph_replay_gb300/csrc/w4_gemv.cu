@@ -1,0 +1,120 @@
+// w4_gemv.cu -- planning and launch of the few-token products with 4-bit weights
+// (w4_gemv.cuh; instantiated in w4_gemv_g32.cu, w4_gemv_g64.cu, w4_gemv_g128.cu).
+#include "w4_gemv.cuh"
+
+namespace gd {
+
+const void* w4_gemv_kernel_32(int parts, int nb, bool glu);
+const void* w4_gemv_kernel_64(int parts, int nb, bool glu);
+const void* w4_gemv_kernel_128(int parts, int nb, bool glu);
+
+namespace {
+
+constexpr size_t SMEM_MOST = 220 * 1024;       // dynamic shared memory of a CTA
+
+int blocks_of(const W4Gemv& g) { return g.block * g.c.parts() <= 8 ? 1 : 2; }
+
+const void* kernel_of(const W4Gemv& g) {
+    const int nb = blocks_of(g), P = g.c.parts();
+    switch (g.c.group()) {
+        case 32: return w4_gemv_kernel_32(P, nb, g.c.glu);
+        case 64: return w4_gemv_kernel_64(P, nb, g.c.glu);
+        default: return w4_gemv_kernel_128(P, nb, g.c.glu);
+    }
+}
+
+size_t smem_of(const W4Gemv& g) {
+    const int P = g.c.parts(), chunks = (g.c.k() + 127) / 128, most = (chunks + g.ks - 1) / g.ks;
+    const size_t ring = (size_t)WG_WARPS * g.stages * WG_STEP, x = (size_t)most * g.block * P * 256;
+    const size_t f = ((size_t)most * g.block + 3) / 4 * 16;
+    return ring + x + f + sizeof(float) * g.bufs * WG_WARPS * wg_tokens(P, blocks_of(g)) * WG_PITCH;
+}
+
+}  // namespace
+
+cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
+    const W4Call& c = g->c;
+    const int P = c.parts(), N = c.n(), chunks = (c.k() + 127) / 128, most = WG_MAX_TOKENS / P;
+    g->block = c.tokens < most ? c.tokens : most;
+    while (c.tokens > g->block && g->block > 1 && (size_t)chunks * g->block * P * 256 > 64 * 1024) g->block /= 2;
+    // rows evenly over the SMs, at least 8 a CTA: a tile has 16, and a CTA of fewer saves nothing
+    const int gr = c.glu ? 16 : 32;
+    g->stages = 4;
+    for (g->ks = 1; g->ks <= chunks; ++g->ks) {
+        const int places = num_sms / g->ks < 1 ? 1 : num_sms / g->ks;
+        g->rows = (N + places - 1) / places;
+        if (g->rows < 8) g->rows = 8;
+        g->grid = (N + g->rows - 1) / g->rows;
+        const int groups = (g->rows + gr - 1) / gr;
+        const int own = (chunks + g->ks - 1) / g->ks;
+        // warps along k: as many as have a chunk, but no more than leave each set of warps a row group
+        g->wk = WG_WARPS;
+        while (g->wk > 1 && (own < g->wk || (groups >= 2 * (WG_WARPS / g->wk) && own < 4 * g->wk))) g->wk /= 2;
+        const int sets = WG_WARPS / g->wk, iters = (groups + sets - 1) / sets;
+        g->bufs = iters > 1 ? 2 : 1;
+        if (smem_of(*g) <= SMEM_MOST) break;
+    }
+    if (g->ks > chunks || w4_gemv_counters(*g) > DEC_W4_COUNTER_BYTES / sizeof(unsigned)) return cudaErrorInvalidValue;
+    g->smem = smem_of(*g);
+    // the cap once for each kernel and device
+    static OncePerDevice once[3][2][2][2];
+    const void* fn = kernel_of(*g);
+    return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][P - 1][blocks_of(*g) - 1][c.glu].run([&] { return raise_smem_cap(fn); });
+}
+
+size_t w4_gemv_floats(const W4Gemv& g) { return g.ks > 1 ? (size_t)g.ks * g.c.tokens * g.c.n() * (g.c.glu ? 2 : 1) : 0; }
+size_t w4_gemv_counters(const W4Gemv& g) { return g.ks > 1 ? (size_t)g.grid * ((g.c.tokens + g.block - 1) / g.block) : 0; }
+
+cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl) {
+    const W4Call& c = g.c;
+    W4GemvArgs a{};
+    int end = 0;
+    for (int i = 0; i < 3; ++i) {
+        const W4Matrix& w = c.w[i < c.nw ? i : c.nw - 1];
+        a.codes[i] = (const uint8_t*)w.codes;
+        a.scales[i] = (const __nv_bfloat16*)w.scales;
+        end += i < c.nw ? w.n : 0;
+        a.end[i] = end;
+    }
+    a.N = c.n();
+    a.K = c.k();
+    a.tokens = c.tokens;
+    a.block = g.block;
+    a.wk = g.wk;
+    a.ks = g.ks;
+    a.rows = g.rows;
+    a.stages = g.stages;
+    a.bufs = g.bufs;
+    a.act = c.act;
+    a.x_f32 = c.x_f32;
+    a.gain_f32 = c.gain_f32;
+    a.out_f32 = c.out_f32;
+    a.x = c.x;
+    a.gain = c.gain;
+    a.residual = c.residual;
+    a.out = c.out;
+    a.x_stride = c.x_stride;
+    a.residual_stride = c.residual_stride;
+    a.out_stride = c.out_stride;
+    a.eps = c.eps;
+    a.part = g.part;
+    a.count = g.count;
+    a.amax = g.amax;
+    a.nonfinite = g.nonfinite;
+    a.trace = g.trace;
+    a.trace_id = g.trace_id;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(g.grid * g.ks, (c.tokens + g.block - 1) / g.block);
+    cfg.blockDim = dim3(WG_THREADS);
+    cfg.dynamicSmemBytes = g.smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    void* args[] = {&a};
+    return cudaLaunchKernelExC(&cfg, kernel_of(g), args);
+}
+
+}  // namespace gd

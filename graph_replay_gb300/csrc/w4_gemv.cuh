@@ -1,0 +1,486 @@
+// w4_gemv.cuh -- the products of a few tokens with 4-bit weights (mma.sync, sm_103a).
+//
+// out[t, n] = sum_k W[n, k] a[t, k] reads each weight once for all tokens, so it is
+// bound by the bytes of the codes: at the card's rate an SM has to turn about 45
+// codes a clock into products.  One FMA and one conversion a weight and token would
+// already be too many for the CUDA cores; here a 16 x 16 tile of codes is the A
+// operand of mma.sync m16n8k16 (about one instruction a code to unpack, w4.cuh) and
+// the tokens are the 8 columns of B:
+//   * codes enter as exact fp16 integers; a group's products are summed in the
+//     tensor core over at most 128 columns and then multiplied by the group's scale
+//     and added to an fp32 sum, so scales cost 1/16 of an FMA a weight and no
+//     rounding of a scaled weight happens;
+//   * activations enter as one or two fp16 parts (w4.cuh) scaled for each block of
+//     128 columns, so bf16 and fp32 run the same path.  The columns of B are
+//     (token, part) pairs;
+//   * which of the 16 columns of an MMA step is which is free, as long as A and B
+//     agree: lane (g, t) takes the words that it finds in 16 consecutive bytes of
+//     its row, or, where a group is shorter, in two or four places of 64 bytes.
+// A CTA (one an SM, sixteen warps) owns a range of output rows; `wk` warps share
+// its columns, 128 at a time in turn, and 16 / wk sets of warps take row groups in
+// turn (32 rows; a gate/up pair: 16 of each).  Each warp copies its own tiles with
+// cp.async into a ring of its own, so the loop has no barriers; a row group ends
+// with one barrier and a sum over the warps in their order.
+// The activations of a CTA's columns stay in shared memory as B fragments.  Where
+// they do not fit, `ks` CTAs share the columns of a row range, leave their sums in
+// the workspace, and the last to arrive adds them in order.  Results do not depend
+// on scheduling.
+#pragma once
+#include "w4.cuh"
+
+namespace gd {
+
+constexpr int WG_WARPS = 16;
+constexpr int WG_THREADS = WG_WARPS * 32;
+constexpr int WG_STEP = 2048;                  // bytes of a step: two tiles of 16 rows x 128 columns
+constexpr int WG_PITCH = 33;                   // of 32 rows' sums of one token
+constexpr int WG_MAX_TOKENS = 16;
+
+// tokens of a CTA whose columns fill NB blocks of 8
+__host__ __device__ constexpr int wg_tokens(int P, int NB) { return NB * 8 / P; }
+
+struct W4GemvArgs {
+    const uint8_t* codes[3];
+    const __nv_bfloat16* scales[3];
+    int end[3];                // rows of segments 0, 0 + 1, all
+    int N, K, tokens, block, wk, ks, rows, stages, bufs, act, x_f32, gain_f32, out_f32;
+    const void* x;
+    const void* gain;
+    const void* residual;
+    void* out;
+    long long x_stride, residual_stride, out_stride;
+    float eps;
+    float* part;
+    unsigned* count;
+    unsigned long long* amax;
+    unsigned* nonfinite;
+    unsigned long long* trace;
+    int trace_id;
+};
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait(int left) {   // all but the newest `left` groups have landed
+    if (left >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
+    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+    else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
+// G: columns of a group; P: fp16 parts of an activation; NB: blocks of 8 B columns
+template <int G, int P, int NB, bool GLU>
+__global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant__ W4GemvArgs p) {
+    constexpr int NG = 128 / G;                // groups of a step
+    constexpr int MT = wg_tokens(P, NB);       // tokens that fit
+    constexpr int AC = P == 2 ? 2 : 4;         // sums of a lane, tile and column block
+    constexpr int GR = GLU ? 16 : 32;          // output rows of a row group
+    extern __shared__ __align__(128) unsigned char smem[];
+    __shared__ float ss_s[WG_WARPS][MT];
+    __shared__ float inv_s[MT];
+    __shared__ unsigned long long best_s[8];
+    __shared__ unsigned nonfinite_s[8];
+    __shared__ int last_s;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int tok0 = blockIdx.y * p.block, m = min(p.block, p.tokens - tok0);
+    const int cols = p.block * P;
+    const int q = blockIdx.x % p.ks, ri = blockIdx.x / p.ks;
+    const int row0 = ri * p.rows, row1 = min(p.N, row0 + p.rows);
+    const int chunks = (p.K + 127) >> 7;                        // 128 columns each
+    const int ch0 = (int)((long long)q * chunks / p.ks), ch1 = (int)((long long)(q + 1) * chunks / p.ks);
+    const int set = warp / p.wk, sets = WG_WARPS / p.wk, slice = warp % p.wk;
+    const int ngroups = (row1 - row0 + GR - 1) / GR;            // row groups of the CTA
+    const int iters = (ngroups + sets - 1) / sets;              // of each set
+    const int mine = (ch1 - ch0 - slice + p.wk - 1) / p.wk;     // this warp's chunks of a row group (>= 0)
+    const int S = p.stages;
+
+    unsigned char* ring = smem + (size_t)warp * S * WG_STEP;
+    unsigned char* xs = smem + (size_t)WG_WARPS * S * WG_STEP;               // [chunk][4][cols][64 bytes]
+    float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14)
+    float* red = fs + (((ch1 - ch0) * p.block + 3) & ~3);                    // [bufs][warp][MT][WG_PITCH]
+    const uint32_t ring_at = smem_u32(ring);
+
+    unsigned long long* tr = nullptr;
+    if (tid == 0) {
+        tr = trace_if_on(p.trace);
+        trace_mark(tr, p.trace_id, 0);
+    }
+    if (tid < 8) {
+        best_s[tid] = 0ull;
+        nonfinite_s[tid] = 0u;
+    }
+
+    // ---- the warp's steps: row groups set, set + sets, ...; in each its chunks; two tiles a step ----
+    // where this lane's 16 bytes of row g or g + 8 of a tile go, and where its words are
+    const int swz = G == 128 ? 0 : G == 64 ? ((g >> 1) & 1) << 1 : (g >> 1) & 3;
+    const uint32_t put = (uint32_t)(g * 64 + ((t ^ swz) << 4));
+    struct Rows {
+        const uint8_t* c[4];
+        const __nv_bfloat16* s[4];
+        bool on[4];
+    };
+    const size_t cpitch = (size_t)(p.K >> 1), spitch = (size_t)(p.K / G);
+    auto rows_of = [&](int it, Rows& r) {
+        const int base = row0 + (it * sets + set) * GR;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {          // tile i >> 1, row g or g + 8
+            const int n = base + (GLU ? 0 : 16 * (i >> 1)) + 8 * (i & 1) + g;
+            r.on[i] = n < row1;
+            int sg = GLU ? i >> 1 : 0, local = min(n, row1 - 1);
+            if (!GLU) {
+                if (local >= p.end[1]) { sg = 2; local -= p.end[1]; }
+                else if (local >= p.end[0]) { sg = 1; local -= p.end[0]; }
+            }
+            const uint8_t* cb = sg == 0 ? p.codes[0] : sg == 1 ? p.codes[1] : p.codes[2];
+            const __nv_bfloat16* sb = sg == 0 ? p.scales[0] : sg == 1 ? p.scales[1] : p.scales[2];
+            r.c[i] = cb + (size_t)local * cpitch;
+            r.s[i] = sb + (size_t)local * spitch;
+        }
+    };
+    const int steps = mine > 0 ? iters * mine : 0;
+    Rows ahead;                                // of the step that is copied next
+    int a_it = 0, a_i = 0, a_step = 0;
+    if (steps > 0) rows_of(0, ahead);
+    auto copy_next = [&]() {
+        if (a_step < steps) {
+            const int k0 = (ch0 + slice + a_i * p.wk) * 128;
+            const bool in = k0 + 32 * t < p.K;
+            const uint32_t dst = ring_at + (uint32_t)((a_step % S) * WG_STEP) + put;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                cp_async16(dst + (uint32_t)((i >> 1) * 1024 + (i & 1) * 512), in ? ahead.c[i] + (k0 >> 1) + 16 * t : ahead.c[i],
+                           in && ahead.on[i]);
+            ++a_step;
+            if (++a_i == mine) {
+                a_i = 0;
+                if (++a_it < iters) rows_of(a_it, ahead);
+            }
+        }
+        cp_commit();
+    };
+    for (int s = 0; s < S - 1; ++s) copy_next();   // the weights do not depend on the kernel before
+
+    pdl_wait();
+    if (tid == 0) trace_mark(tr, p.trace_id, 1);
+
+    // ---- activations: each warp makes the fragments of every sixteenth chunk, all warps' are used by all ----
+    {
+        const int nc = (ch1 - ch0 - warp + WG_WARPS - 1) / WG_WARPS;
+        const int total = nc > 0 ? nc * m : 0;
+        const int w = lane >> 1;               // word of the chunk that the lane's four columns lie in
+        const int bt = G == 128 ? w >> 2 : G == 64 ? (w >> 1) & 3 : w & 3;
+        const int bq = G == 128 ? w & 3 : G == 64 ? ((w >> 3) << 1) | (w & 1) : w >> 2;
+        float ss = 0.f;
+        constexpr int AHEAD = 8;
+        int r = 0, j = 0;                      // token and chunk of the next value to load
+        int cr = 0, cj = 0;                    // ... to convert
+        for (int b = 0; b < total; b += AHEAD) {
+            float4 v[AHEAD], gv[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                v[u] = gv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (b + u < total) {
+                    const int k = (ch0 + warp + j * WG_WARPS) * 128 + 4 * lane;
+                    if (k < p.K) {
+                        v[u] = w4_load4(p.x, p.x_f32, (size_t)(tok0 + r) * p.x_stride + k);
+                        if (p.gain) gv[u] = w4_load4(p.gain, p.gain_f32, k);
+                    }
+                    if (++j == nc) { j = 0; ++r; }
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) {
+                if (b + u >= total) break;
+                float4 x = v[u];
+                if (p.gain) {
+                    ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, ss))));
+                    x.x *= gv[u].x; x.y *= gv[u].y; x.z *= gv[u].z; x.w *= gv[u].w;
+                }
+                const uint32_t top = __reduce_max_sync(
+                    0xffffffffu, max(max(w4_finite_bits(x.x), w4_finite_bits(x.y)), max(w4_finite_bits(x.z), w4_finite_bits(x.w))));
+                const int e = w4_exponent(top);
+                const float up = w4_up(e);
+                x.x *= up; x.y *= up; x.z *= up; x.w *= up;
+                const int ci = warp + cj * WG_WARPS;
+                uint32_t h01 = w4_pack_half(x.x, x.y), h23 = w4_pack_half(x.z, x.w);
+                uint32_t l01 = 0, l23 = 0;
+                if (P == 2) {
+                    l01 = w4_rest(x.x, x.y, h01);
+                    l23 = w4_rest(x.z, x.w, h23);
+                }
+                const bool odd = lane & 1;
+#pragma unroll
+                for (int part = 0; part < P; ++part) {
+                    const uint32_t a01 = part ? l01 : h01, a23 = part ? l23 : h23;
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a01 : a23, 1);
+                    const uint32_t lo = odd ? got : a01, hi = odd ? a23 : got;     // columns j and j + 4 of the word
+                    const uint2 f = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+                    *reinterpret_cast<uint2*>(xs + ((size_t)(ci * 4 + bq) * cols + cr * P + part) * 64 + bt * 16 + (odd ? 8 : 0)) = f;
+                }
+                if (lane == 0) fs[ci * p.block + cr] = w4_down(e);
+                if (++cj == nc) {
+                    if (p.gain) {
+                        ss = warp_sum(ss);
+                        if (lane == 0) ss_s[warp][cr] = ss;
+                        ss = 0.f;
+                    }
+                    cj = 0;
+                    ++cr;
+                }
+            }
+        }
+        if (p.gain && nc <= 0 && lane < m) ss_s[warp][lane] = 0.f;
+        if (p.gain && p.ks > 1) {   // the other CTAs' columns, for the norm
+            __syncwarp();
+            for (int r2 = 0; r2 < m; ++r2) {
+                float s2 = 0.f;
+                for (int c = warp; c < chunks; c += WG_WARPS) {
+                    const int k = c * 128 + 4 * lane;
+                    if ((c < ch0 || c >= ch1) && k < p.K) {
+                        const float4 x = w4_load4(p.x, p.x_f32, (size_t)(tok0 + r2) * p.x_stride + k);
+                        s2 = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, s2))));
+                    }
+                }
+                s2 = warp_sum(s2);
+                if (lane == 0) ss_s[warp][r2] += s2;
+            }
+        }
+    }
+    __syncthreads();
+    pdl_trigger();
+    if (tid < m) {
+        float s = 0.f;
+        if (p.gain)
+            for (int w = 0; w < WG_WARPS; ++w) s += ss_s[w][tid];
+        inv_s[tid] = p.gain ? 1.0f / sqrtf(s / (float)p.K + p.eps) : 1.0f;   // read behind the next barrier
+    }
+
+    // one output: gate / value v and up u, unscaled by the norm
+    auto finish = [&](int r, int n, float v, float u) {
+        v *= inv_s[r];
+        if (GLU) {
+            v = w4_glu(p.act, v, u * inv_s[r]);
+        } else if (p.residual) {
+            v += w4_load1(p.residual, p.out_f32, (size_t)(tok0 + r) * p.residual_stride + n);
+        }
+        w4_store1(p.out, p.out_f32, (size_t)(tok0 + r) * p.out_stride + n, v);
+        if (!GLU && p.amax) {
+            atomicMax(&best_s[r], argmax_key(v, n));
+            if (!isfinite(v)) nonfinite_s[r] = 1u;
+        }
+    };
+
+    // ---- the products ----
+    // the scales of the step after this one: of row g in the low half, of row g + 8 in the high half, of group t (one of
+    // NG); raw bits
+    Rows cur, next;
+    uint32_t sc[2] = {0u, 0u};
+    auto scales_of = [&](const Rows& r, int i, uint32_t (&o)[2]) {
+        const int gr = (ch0 + slice + i * p.wk) * NG + (NG > 1 ? t % NG : 0);
+        const bool in = gr < (int)spitch;
+#pragma unroll
+        for (int tile = 0; tile < 2; ++tile) {
+            const uint32_t a = in ? __ldg(reinterpret_cast<const unsigned short*>(r.s[2 * tile]) + gr) : 0u;
+            const uint32_t b = in ? __ldg(reinterpret_cast<const unsigned short*>(r.s[2 * tile + 1]) + gr) : 0u;
+            o[tile] = a | (b << 16);
+        }
+    };
+    if (steps > 0) {
+        rows_of(0, cur);
+        scales_of(cur, 0, sc);
+    }
+    int step = 0;
+    for (int it = 0; it < iters; ++it) {
+        float acc[2][NB][AC];
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int c = 0; c < AC; ++c) acc[a][b][c] = 0.f;
+        const int base = row0 + (it * sets + set) * GR;
+        for (int i = 0; i < mine; ++i, ++step) {
+            uint32_t sn[2] = {0u, 0u};
+            if (i + 1 < mine) {
+                scales_of(cur, i + 1, sn);
+            } else if (it + 1 < iters) {
+                rows_of(it + 1, next);
+                scales_of(next, 0, sn);
+            }
+            cp_wait(S - 2);
+            __syncwarp();
+            copy_next();                       // into the slot that the step before read
+            const unsigned char* st = ring + (size_t)(step % S) * WG_STEP;
+            const int ci = slice + i * p.wk;
+            uint4 bf[NB][4];                   // [q]: the B words of MMA 2q and 2q + 1
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+                    bf[b][c] = b * 8 + g < cols ? *reinterpret_cast<const uint4*>(xs + ((size_t)(ci * 4 + c) * cols + b * 8 + g) * 64 + t * 16)
+                                                : make_uint4(0u, 0u, 0u, 0u);
+            float f[NB][P == 2 ? 1 : 2];       // 2^(e - 14) of the tokens of this lane's sums
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int c = 0; c < (P == 2 ? 1 : 2); ++c) {
+                    const int r = P == 2 ? b * 4 + t : b * 8 + 2 * t + c;
+                    f[b][c] = r < m ? fs[ci * p.block + r] : 0.f;
+                }
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                if (!GLU && tile == 1 && base + 16 >= row1) break;   // the same for the whole warp
+                const unsigned char* ta = st + tile * 1024 + g * 64;
+                uint32_t wa[4], wb[4];         // words of rows g and g + 8, word c for MMAs 2c and 2c + 1
+                if (G == 128) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(ta + t * 16), b = *reinterpret_cast<const uint4*>(ta + 512 + t * 16);
+                    wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
+                    wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
+                } else if (G == 64) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int at = ((2 * h + (t >> 1)) ^ swz) * 16 + (t & 1) * 8;
+                        const uint2 a = *reinterpret_cast<const uint2*>(ta + at), b = *reinterpret_cast<const uint2*>(ta + 512 + at);
+                        wa[2 * h] = a.x; wa[2 * h + 1] = a.y;
+                        wb[2 * h] = b.x; wb[2 * h + 1] = b.y;
+                    }
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int at = (c ^ swz) * 16 + t * 4;
+                        wa[c] = *reinterpret_cast<const uint32_t*>(ta + at);
+                        wb[c] = *reinterpret_cast<const uint32_t*>(ta + 512 + at);
+                    }
+                }
+#pragma unroll
+                for (int gi = 0; gi < NG; ++gi) {
+                    float d[NB][4];
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) d[b][0] = d[b][1] = d[b][2] = d[b][3] = 0.f;
+#pragma unroll
+                    for (int c = gi * (4 / NG); c < (gi + 1) * (4 / NG); ++c) {
+                        uint32_t pa[4], pb[4];
+                        w4_unpack(wa[c], pa);
+                        w4_unpack(wb[c], pb);
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            mma_f16(d[b], pa[0], pb[0], pa[1], pb[1], bf[b][c].x, bf[b][c].y);
+                            mma_f16(d[b], pa[2], pb[2], pa[3], pb[3], bf[b][c].z, bf[b][c].w);
+                        }
+                    }
+                    const uint32_t sw = NG > 1 ? __shfl_sync(0xffffffffu, sc[tile], (lane & 28) | gi) : sc[tile];
+                    const float s0 = bf16_lo(sw), s1 = bf16_hi(sw);
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        if (P == 2) {          // columns 2t and 2t + 1 are the two parts of one token
+                            acc[tile][b][0] = fmaf(d[b][0] + d[b][1], s0 * f[b][0], acc[tile][b][0]);
+                            acc[tile][b][1] = fmaf(d[b][2] + d[b][3], s1 * f[b][0], acc[tile][b][1]);
+                        } else {
+                            acc[tile][b][0] = fmaf(d[b][0], s0 * f[b][0], acc[tile][b][0]);
+                            acc[tile][b][AC > 2 ? 1 : 0] = fmaf(d[b][1], s0 * f[b][P == 2 ? 0 : 1], acc[tile][b][AC > 2 ? 1 : 0]);
+                            acc[tile][b][AC > 2 ? 2 : 0] = fmaf(d[b][2], s1 * f[b][0], acc[tile][b][AC > 2 ? 2 : 0]);
+                            acc[tile][b][AC > 2 ? 3 : 0] = fmaf(d[b][3], s1 * f[b][P == 2 ? 0 : 1], acc[tile][b][AC > 2 ? 3 : 0]);
+                        }
+                    }
+                }
+            }
+            sc[0] = sn[0];
+            sc[1] = sn[1];
+        }
+        if (it + 1 < iters && mine > 0) cur = next;
+
+        // the warps' sums of the row group: [warp][token][row]
+        float* rb = red + (size_t)(p.bufs > 1 ? it & 1 : 0) * WG_WARPS * MT * WG_PITCH;
+        float* rw = rb + (size_t)warp * MT * WG_PITCH;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int c = 0; c < AC; ++c) {
+                    const int r = P == 2 ? b * 4 + t : b * 8 + 2 * t + (c & 1);
+                    const int row = a * 16 + g + 8 * (P == 2 ? c : c >> 1);
+                    rw[r * WG_PITCH + row] = acc[a][b][c];
+                }
+        __syncthreads();
+        for (int i = tid; i < sets * m * 32; i += WG_THREADS) {
+            const int row = i & 31, r = (i >> 5) % m, st2 = (i >> 5) / m;
+            if (GLU && row >= 16) continue;
+            const int n = row0 + (it * sets + st2) * GR + row;
+            if (n >= row1) continue;
+            float v = 0.f, u = 0.f;
+            for (int w = 0; w < p.wk; ++w) {
+                const float* s = rb + ((size_t)(st2 * p.wk + w) * MT + r) * WG_PITCH + row;
+                v += s[0];
+                if (GLU) u += s[16];
+            }
+            if (p.ks == 1) {
+                finish(r, n, v, u);
+            } else {
+                float* o = p.part + ((size_t)q * p.tokens + tok0 + r) * p.N * (GLU ? 2 : 1) + n;
+                o[0] = v;
+                if (GLU) o[p.N] = u;
+            }
+        }
+        // one buffer: the next row group's sums wait for this one's readers
+        if (p.bufs == 1 && it + 1 < iters) __syncthreads();
+    }
+
+    if (p.ks > 1) {
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) {
+            unsigned* c = p.count + (size_t)blockIdx.y * (gridDim.x / p.ks) + ri;
+            const unsigned before = atomicAdd(c, 1u);
+            last_s = before == (unsigned)p.ks - 1u;
+            if (last_s) *c = 0u;               // ready for the next call
+        }
+        __syncthreads();
+        if (last_s) {
+            __threadfence();
+            const int nr = row1 - row0;
+            for (int i = tid; i < nr * m; i += WG_THREADS) {
+                const int r = i / nr, n = row0 + i - r * nr;
+                float v = 0.f, u = 0.f;
+                for (int w = 0; w < p.ks; ++w) {
+                    const float* o = p.part + ((size_t)w * p.tokens + tok0 + r) * p.N * (GLU ? 2 : 1) + n;
+                    v += __ldcg(o);
+                    if (GLU) u += __ldcg(o + p.N);
+                }
+                finish(r, n, v, u);
+            }
+        }
+    }
+    if (!GLU && p.amax) {
+        __syncthreads();
+        if (tid < m) {
+            if (best_s[tid]) atomicMax(p.amax + tok0 + tid, best_s[tid]);
+            if (nonfinite_s[tid]) atomicOr(p.nonfinite + tok0 + tid, 1u);
+        }
+    }
+    if (tid == 0) {
+        trace_mark(tr, p.trace_id, 2);
+        trace_mark(tr, p.trace_id, 3);
+    }
+}
+
+template <int G>
+const void* w4_gemv_kernel(int parts, int nb, bool glu) {
+    if (parts == 1) {
+        if (nb == 1) return glu ? (const void*)&k_w4_gemv<G, 1, 1, true> : (const void*)&k_w4_gemv<G, 1, 1, false>;
+        return glu ? (const void*)&k_w4_gemv<G, 1, 2, true> : (const void*)&k_w4_gemv<G, 1, 2, false>;
+    }
+    if (nb == 1) return glu ? (const void*)&k_w4_gemv<G, 2, 1, true> : (const void*)&k_w4_gemv<G, 2, 1, false>;
+    return glu ? (const void*)&k_w4_gemv<G, 2, 2, true> : (const void*)&k_w4_gemv<G, 2, 2, false>;
+}
+
+}  // namespace gd

@@ -18,7 +18,7 @@
  *     failure, dec_last_error() returns a NUL-terminated message owned by the
  *     handle (valid until the next call on that handle); dec_last_error(NULL)
  *     gives the message of the last failed call without a handle (dec_init,
- *     dec_kv8_*) on the calling thread.
+ *     dec_kv8_*, dec_w4_*) on the calling thread.
  *   - Pointers marked "device" are CUDA device addresses on the handle's GPU;
  *     "host" pointers are ordinary (pageable or pinned) host memory.  The
  *     library never frees memory it did not allocate.
@@ -565,6 +565,79 @@ int dec_kv8_attend(const dec_kv8_cache *cache, const dec_kv8_batch *batch, const
 /* Bytes of workspace that dec_kv8_attend needs for these arguments (*bytes,
  * host).  Reads sizes only: the same for every content. */
 int dec_kv8_workspace(const dec_kv8_cache *cache, const dec_kv8_batch *batch, const dec_kv8_attn *attn, size_t *bytes);
+
+/* ---- 4-bit weights ----
+ * A matrix [n, k] (nn.Linear layout) stored in 4 bits: codes -8 .. 7 in two's
+ * complement, two in a byte (column 2i in the low half of byte i, 2i + 1 in the
+ * high half; a row is k / 2 bytes, rows follow one another), and one bf16 scale
+ * for each `group` consecutive columns of a row.  It stands for code * scale:
+ * 4.125 bits a weight with groups of 128, a quarter of bf16's bytes to hold and,
+ * in a decode step, to read.
+ *
+ * Like dec_kv8_* these calls take no handle, only launch kernels on the caller's
+ * stream (NULL: the legacy default stream), neither wait nor allocate, and may be
+ * recorded into a graph.  The current device is put back before they return.
+ * Messages: dec_last_error(NULL).
+ *   group   32, 64 or 128; k a multiple of it, at most 2^20
+ *   n       >= 1, n * k <= 2^33 */
+typedef struct dec_w4_weight {
+    void *codes;                 /* device, 16-byte aligned: [n, k / 2] bytes */
+    void *scales;                /* device, 2-byte aligned: bf16 [n, k / group] */
+    int32_t n, k, group;
+    int32_t device;              /* CUDA device ordinal of all of it */
+} dec_w4_weight;
+
+/* Store src [n, k] (f32 or bf16, rows src_stride elements apart, 16-byte aligned
+ * like the stride) into w.  Over each group scale = bf16(max |x| / 7) and code =
+ * x / scale to the nearest whole number, ties to even.  A group whose scale would
+ * be below 2^-100 holds zeros at scale 0; a group with a NaN or an infinity has
+ * scale NaN (and so gives NaN wherever it is used). */
+int dec_w4_quantize(const dec_w4_weight *w, const void *src, int64_t src_stride, int32_t dtype, void *stream);
+
+/* The values that w stands for, [n, k] in f32 (exact) or bf16 (rounded once). */
+int dec_w4_dequantize(const dec_w4_weight *w, void *dst, int64_t dst_stride, int32_t dtype, void *stream);
+
+typedef enum dec_act { DEC_ACT_SILU = 0, DEC_ACT_GELU_TANH = 1 } dec_act;
+
+/* One call's activations.  With a gain a = x / sqrt(mean(x^2) + eps) * gain, else
+ * a = x.  out may be the residual itself (then with its stride); it overlaps
+ * nothing else of the call. */
+typedef struct dec_w4_call {
+    const void *x;               /* device [tokens, k], 16-byte aligned */
+    const void *gain;            /* device [k], 16-byte aligned, or NULL: no norm */
+    const void *residual;        /* dec_w4_linear: device [tokens, n] of out's type, or NULL */
+    void *out;                   /* device [tokens, n] */
+    int64_t x_stride;            /* elements between tokens, a multiple of 16 bytes */
+    int64_t residual_stride, out_stride;   /* at least n */
+    int32_t tokens;              /* >= 0; tokens * n <= 2^31 - 1 */
+    int32_t x_dtype, gain_dtype, out_dtype;   /* F32 or BF16 each */
+    int32_t act;                 /* dec_w4_glu: dec_act */
+    int32_t reserved;            /* 0 */
+    double eps;
+    uint32_t *err;               /* device: DEC_FAULT_WAIT is added if a copy or product never ended (the call's results are
+                                    not to be used); never cleared */
+    void *workspace;             /* device, 256-byte aligned, dec_w4_workspace bytes.  Its first DEC_W4_COUNTER_BYTES are
+                                    zero-filled by the caller before its first use; every call leaves it ready for the next
+                                    one of any shape that it holds.  Calls that may overlap on the GPU need one each */
+    size_t workspace_bytes;
+} dec_w4_call;
+#define DEC_W4_COUNTER_BYTES 65536
+
+/* out[t, n] = residual[t, n] + sum_k W[n, k] a[t, k].  Products with the codes are
+ * summed in fp32 at least; bf16 activations enter exactly, fp32 ones and normed
+ * ones to about 2^-22 of each (or 2^-39 of the largest near it), normed bf16 ones
+ * of more than a few tokens to 2^-12.  What a token gives does not depend on the
+ * others beside it, nor on scheduling. */
+int dec_w4_linear(const dec_w4_weight *w, const dec_w4_call *call, void *stream);
+
+/* The first half of a gated feed-forward block: out[t, n] = act(gate_n . a_t) *
+ * (up_n . a_t), gate and up of one shape and group.  silu(z) = z / (1 + e^-z);
+ * gelu_tanh(z) = z / 2 (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))). */
+int dec_w4_glu(const dec_w4_weight *gate, const dec_w4_weight *up, const dec_w4_call *call, void *stream);
+
+/* Bytes of workspace that dec_w4_linear (up = NULL) or dec_w4_glu needs for these
+ * arguments (*bytes, host); reads sizes, types and whether there is a gain only. */
+int dec_w4_workspace(const dec_w4_weight *w, const dec_w4_weight *up, const dec_w4_call *call, size_t *bytes);
 
 /* Device address of the logits [rows, vocab] fp32 of the last step. */
 int dec_logits_ptr(dec_handle *h, float **ptr);
