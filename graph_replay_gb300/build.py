@@ -15,7 +15,8 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libgraphdec.so")
 SOURCES = ["engine.cu", "gemv.cu", "gemv_bf16.cu", "gemv_f32.cu", "gemv_tc.cu", "gemv_tma.cu", "attn.cu", "attn_mma.cu", "misc.cu", "sample.cu", "noalloc.cu", "persist.cu", "prefill.cu",
            "kv8.cu", "kv8_append.cu", "kv8_decode.cu", "kv8_prompt.cu", "kv8_step.cu",
-           "w4.cu", "w4_store.cu", "w4_gemv.cu", "w4_gemv_g32.cu", "w4_gemv_g64.cu", "w4_gemv_g128.cu"]
+           "w4.cu", "w4_store.cu", "w4_gemv.cu", "w4_gemv_g32.cu", "w4_gemv_g64.cu", "w4_gemv_g128.cu",
+           "w4_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

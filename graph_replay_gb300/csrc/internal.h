@@ -225,6 +225,17 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms);
 size_t w4_gemv_floats(const W4Gemv& g);      // of g.part
 size_t w4_gemv_counters(const W4Gemv& g);    // of g.count
 cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl);
+struct W4Gemm {                // how w4_gemm.cu runs a call of many tokens
+    W4Call c;                  // nw == 1, or glu
+    int nt;                    // tokens of a tile
+    int ks;                    // CTAs along k
+    int kp, ksteps;            // columns rounded up to 64; steps of 64
+    void* ws;                  // w4_gemm_bytes()
+    unsigned* count;           // ks > 1: [tiles], zero between calls
+};
+cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms);
+size_t w4_gemm_bytes(const W4Gemm& g);
+cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s);
 
 // ---------------- split-KV masked decode attention ----------------
 struct AttnParams {

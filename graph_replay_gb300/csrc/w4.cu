@@ -144,16 +144,25 @@ int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const 
     return DEC_OK;
 }
 
-// the workspace is used by plans that split k over CTAs only
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // how a call runs, and what of the workspace it uses behind the counters
 struct Plan {
+    bool few;
     W4Gemv gemv;
+    W4Gemm gemm;
     size_t bytes;
 };
 
 cudaError_t plan_of(const W4Call& c, int sms, Plan* p) {
+    p->few = c.tokens * c.parts() <= 16;
+    if (!p->few) {
+        p->gemm = W4Gemm{};
+        p->gemm.c = c;
+        const cudaError_t e = w4_gemm_plan(&p->gemm, sms);
+        p->bytes = DEC_W4_COUNTER_BYTES + round256(w4_gemm_bytes(p->gemm));
+        return e;
+    }
     p->gemv = W4Gemv{};
     p->gemv.c = c;
     const cudaError_t e = w4_gemv_plan(&p->gemv, sms);
@@ -177,6 +186,11 @@ int run(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_
         return refuse(DEC_E_OOM, "workspace of %zu bytes is smaller than the %zu needed",
                       call->workspace ? call->workspace_bytes : (size_t)0, p.bytes);
     if (!aligned(call->workspace, 256)) return refuse(DEC_E_INVALID, "workspace must be 256-byte aligned");
+    if (!p.few) {
+        p.gemm.count = (unsigned*)call->workspace;
+        p.gemm.ws = (char*)call->workspace + DEC_W4_COUNTER_BYTES;
+        return launched(w4_gemm_launch(p.gemm, (cudaStream_t)stream), what);
+    }
     p.gemv.count = (unsigned*)call->workspace;
     p.gemv.part = (float*)((char*)call->workspace + DEC_W4_COUNTER_BYTES);
     return launched(w4_gemv_launch(p.gemv, (cudaStream_t)stream, false), what);

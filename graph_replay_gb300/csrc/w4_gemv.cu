@@ -36,7 +36,6 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     const W4Call& c = g->c;
     const int P = c.parts(), N = c.n(), chunks = (c.k() + 127) / 128, most = WG_MAX_TOKENS / P;
     g->block = c.tokens < most ? c.tokens : most;
-    while (c.tokens > g->block && g->block > 1 && (size_t)chunks * g->block * P * 256 > 64 * 1024) g->block /= 2;
     // rows evenly over the SMs, at least 8 a CTA: a tile has 16, and a CTA of fewer saves nothing
     const int gr = c.glu ? 16 : 32;
     g->stages = 4;

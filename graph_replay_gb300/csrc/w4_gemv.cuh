@@ -382,13 +382,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         if (P == 2) {          // columns 2t and 2t + 1 are the two parts of one token
-                            acc[tile][b][0] = fmaf(d[b][0] + d[b][1], s0 * f[b][0], acc[tile][b][0]);
-                            acc[tile][b][1] = fmaf(d[b][2] + d[b][3], s1 * f[b][0], acc[tile][b][1]);
+                            acc[tile][b][0] = fmaf((d[b][0] + d[b][1]) * f[b][0], s0, acc[tile][b][0]);
+                            acc[tile][b][1] = fmaf((d[b][2] + d[b][3]) * f[b][0], s1, acc[tile][b][1]);
                         } else {
-                            acc[tile][b][0] = fmaf(d[b][0], s0 * f[b][0], acc[tile][b][0]);
-                            acc[tile][b][AC > 2 ? 1 : 0] = fmaf(d[b][1], s0 * f[b][P == 2 ? 0 : 1], acc[tile][b][AC > 2 ? 1 : 0]);
-                            acc[tile][b][AC > 2 ? 2 : 0] = fmaf(d[b][2], s1 * f[b][0], acc[tile][b][AC > 2 ? 2 : 0]);
-                            acc[tile][b][AC > 2 ? 3 : 0] = fmaf(d[b][3], s1 * f[b][P == 2 ? 0 : 1], acc[tile][b][AC > 2 ? 3 : 0]);
+                            acc[tile][b][0] = fmaf(d[b][0] * f[b][0], s0, acc[tile][b][0]);
+                            acc[tile][b][AC > 2 ? 1 : 0] = fmaf(d[b][1] * f[b][P == 2 ? 0 : 1], s0, acc[tile][b][AC > 2 ? 1 : 0]);
+                            acc[tile][b][AC > 2 ? 2 : 0] = fmaf(d[b][2] * f[b][0], s1, acc[tile][b][AC > 2 ? 2 : 0]);
+                            acc[tile][b][AC > 2 ? 3 : 0] = fmaf(d[b][3] * f[b][P == 2 ? 0 : 1], s1, acc[tile][b][AC > 2 ? 3 : 0]);
                         }
                     }
                 }

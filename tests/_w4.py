@@ -70,11 +70,11 @@ def glu(act, g, u):
 
 def product_bound(a, w, part_bits, k):
     """How far a product sum_k w a may be off: each activation enters to 2^-part_bits of itself (or 2^-39 of the largest
-    beside it), and fp32 sums of k products lose at most 2^-23 a step (the tensor core cuts off), in chains of at most
-    256 steps of a sum that the absolute values bound."""
+    beside it), and fp32 sums lose at most 2^-23 of the absolute values' sum a step (the tensor core cuts off): a step for
+    each 16 columns and part, and a few to join warps and splits."""
     mag = a.abs() @ w.abs().T
     top = a.abs().amax(-1, keepdim=True) * w.abs().sum(-1)[None]
-    steps = min(256, k // 16 + 24)
+    steps = 2 * (k // 16) + 24
     return mag * (2.0 ** -part_bits + steps * 2.0 ** -23) + top * 2.0 ** -38
 
 
