@@ -229,7 +229,7 @@ struct W4Gemm {                // how w4_gemm.cu runs a call of many tokens
     W4Call c;                  // nw == 1, or glu
     int nt;                    // tokens of a tile
     int ks;                    // CTAs along k
-    int kp, ksteps;            // columns rounded up to 64; steps of 64
+    int kp, steps;             // columns rounded up to 64; steps of 128
     void* ws;                  // w4_gemm_bytes()
     unsigned* count;           // ks > 1: [tiles], zero between calls
 };

@@ -5,22 +5,26 @@
 // is exact in fp16: a code of 4 bits times a scale of 8 significant bits has 11, so
 // once the scales of a row are brought to fp16's range by one power of two (2^11 at
 // the row's largest) nothing is rounded (a scale more than 2^28 below the row's largest
-// loses bits, 2^-39 of that largest).  Activations are fp16 parts, scaled by a power of two a token:
-// one part for bf16 ones (8 bits fit), two for fp32.  So a bf16 call needs one MMA a
-// weight tile, with fp32 sums.
+// loses bits, 2^-39 of that largest).  Activations are fp16 parts, scaled by a power of
+// two a token: one part for bf16 ones (8 bits fit), two for fp32.
 //
 //   k_w4_split   one CTA a token: RMSNorm's sum, the token's power of two, its parts in
 //                the column order in which the words of codes come apart (w4.cuh).
-//   k_w4_gemm    A = a tile of 128 output rows (TMEM lanes), B = up to 256 tokens.
-//     warps 0-7  two warpgroups in turn take 64 columns of the tile: a thread has a row,
-//                reads 32 bytes of codes, makes 64 fp16 weights and stores them to TMEM
-//                (tcgen05.st), from where the MMA reads A: no shared memory is written,
+//   k_w4_gemm    A = two tiles of 128 output rows (TMEM lanes): 256 rows of one matrix, or
+//                128 rows each of gate and up; B = up to 128 tokens, read from shared memory
+//                once for both.  A step is 128 columns:
+//     warps 0-15 a warpgroup takes one tile and one half of the step's columns: a thread has
+//                a row, reads 32 bytes of codes, makes 64 fp16 weights and stores them to
+//                TMEM (tcgen05.st), from where the MMA reads A: no shared memory is written,
 //                and its reads are left to B
-//     warp 8     codes by TMA, 128 columns a stage
-//     warp 9     activations by TMA, 64 columns a stage (128-byte swizzle)
-//     warp 10    tcgen05.mma kind::f16, D in TMEM (gate/up: two accumulators)
-//   and warps 0-7 again for the epilogue: thread = output row, so a warp's stores of one
+//     warp 16    codes by TMA (64-byte swizzle)
+//     warp 17    activations by TMA (128-byte swizzle)
+//     warp 18    tcgen05.mma kind::f16, two accumulators in TMEM
+//   and warps 0-15 again for the epilogue: thread = output row, so a warp's stores of one
 //   token lie side by side.
+// The tensor core cuts its fp32 sums off instead of rounding them.  For fp32 activations
+// the accumulators are therefore folded into registers every WM_FOLD steps (with rounding),
+// while the MMAs go on in a second pair.
 // Few tokens leave few tiles: then `ks` CTAs share the columns of a tile, leave their
 // sums in the workspace, and the last to arrive adds them in order.
 // Every wait is bounded; one that gives up sets FAULT_WAIT, and the CTA ends.
@@ -32,12 +36,17 @@ namespace gd {
 
 namespace {
 
-constexpr int WM_DQ = 8;                       // warps that make weights, and write results
+constexpr int WM_DQ = 16;                      // warps that make weights, and write results: four warpgroups
 constexpr int WM_THREADS = (WM_DQ + 3) * 32;
-constexpr int WM_CODES = 128 * 64;             // bytes of a codes stage: 128 rows x 128 columns
-constexpr int WM_MAX_SC = 16, WM_MAX_SB = 12;
+constexpr int WM_CODES = 2 * 128 * 64;         // bytes of a codes stage: two tiles of 128 rows x 128 columns
+constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 3;
 constexpr int WM_SMEM = 200 * 1024;            // for both rings
-constexpr int WM_MAX_NT = 256;
+constexpr int WM_FOLD = 2;                     // fp32 activations: steps of an accumulator
+
+// fp32 activations: stages of 64 columns (two parts), and accumulators of half as many tokens, in two pairs
+constexpr int wm_tokens(int P) { return P == 2 ? 64 : 128; }
+constexpr int wm_halves(int P) { return P; }   // activation stages of a step
+constexpr int wm_stage(int P, int nt) { return nt * 256; }   // bytes: 128 columns of one part or 64 of two
 
 struct WmParams {
     CUtensorMap codes[2];      // [n, k / 2] bytes, box [64, 128], 64-byte swizzle
@@ -47,7 +56,7 @@ struct WmParams {
     const void* residual;
     void* out;
     long long residual_stride, out_stride;
-    int N, K, tokens, nt, ks, ksteps, sc, sb, na, act, out_f32;
+    int N, K, tokens, nt, ks, steps, sc, sx, sa, act, out_f32;
     bool wide;                 // scales can be read eight at a time
     float* part;
     unsigned* count;
@@ -64,6 +73,16 @@ __device__ __forceinline__ void tm_st32(uint32_t a, const uint32_t (&r)[32]) {
         "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
         : "memory");
 }
+__device__ __forceinline__ void tmem_ld32(uint32_t a, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+          "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(a));
+}
 __device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
@@ -73,17 +92,19 @@ __device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&r)[16]) {
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-// D (+)= A B over 64 columns by the warp's elected lane: A in TMEM (8 columns a step of 16), B K-major in shared memory
-// (128-byte swizzle, 32 bytes a step).  acc 0: D starts anew
+// D (+)= A B over 64 columns: A in TMEM (8 columns a step of 16), B K-major in shared memory (128-byte swizzle, 32 bytes a
+// step; `b` is the low word of its descriptor).  acc 0: D starts anew.  The whole warp comes here with the same operands and
+// its elected lane issues: 100 clocks for four MMAs, 300 from the code of a single lane
 constexpr uint32_t WM_DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t wm_desc(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | 1u << 16; }
 __device__ __forceinline__ void mma_64(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t acc) {
     asm volatile("{\n .reg .pred e, p, t;\n .reg .b64 y;\n .reg .b32 a;\n setp.ne.u32 p, %5, 0;\n setp.eq.u32 t, 0, 0;\n"
                  " mov.b32 a, %1;\n mov.b64 y, {%2, %3};\n elect.sync _|e, 0xffffffff;\n"
                  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, p;\n add.u32 a, a, 8;\n add.u64 y, y, 2;\n"
                  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n add.u32 a, a, 8;\n add.u64 y, y, 2;\n"
                  " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n add.u32 a, a, 8;\n add.u64 y, y, 2;\n"
-                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n}\n" ::"r"(d), "r"(a),
-                 "r"(((b & 0x3FFFFu) >> 4) | 1u << 16), "r"(WM_DESC_HI), "r"(idesc), "r"(acc)
+                 " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [a], y, %4, t;\n}\n" ::"r"(d), "r"(a), "r"(b), "r"(WM_DESC_HI),
+                 "r"(idesc), "r"(acc)
                  : "memory");
 }
 __device__ __forceinline__ void commit(uint64_t* bar) {
@@ -91,6 +112,18 @@ __device__ __forceinline__ void commit(uint64_t* bar) {
                  " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar))
                  : "memory");
 }
+
+// where a ring stands: a division by its length would take longer than a step
+struct Ring {
+    int slot = 0;
+    uint32_t odd = 0;          // parity of the rounds gone through
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) {
+            slot = 0;
+            odd ^= 1u;
+        }
+    }
+};
 
 // a row's scales are multiplied by 2^(11 - e), 2^e the power of two at or below the largest of them: weights below 2^15
 __device__ __forceinline__ float row_up(int e) { return __uint_as_float((uint32_t)(265 - e) << 23); }
@@ -108,28 +141,28 @@ __device__ __forceinline__ uint32_t pick16(const uint4& w, int i) {   // element
 // G: columns of a group; P: fp16 parts of an activation
 template <int G, int P, bool GLU>
 __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant__ WmParams p) {
-    constexpr int MATS = GLU ? 2 : 1;
+    constexpr int ROWS = GLU ? 128 : 256;      // output rows of a CTA
+    constexpr int XH = wm_halves(P);           // activation stages of a step
+    constexpr bool FOLD = P == 2;
+    constexpr int NS = G == 32 ? 2 : 1;        // scales of a thread's 64 columns
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
-    __shared__ __align__(8) uint64_t codes_full[WM_MAX_SC], codes_empty[WM_MAX_SC], x_full[WM_MAX_SB], x_empty[WM_MAX_SB];
-    __shared__ __align__(8) uint64_t a_full[8], a_empty[8], done;
+    __shared__ __align__(8) uint64_t codes_full[WM_MAX_SC], codes_empty[WM_MAX_SC], x_full[WM_MAX_SX], x_empty[WM_MAX_SX];
+    __shared__ __align__(8) uint64_t a_full[WM_MAX_SA], a_empty[WM_MAX_SA], d_full[2], d_empty[2];
     __shared__ uint32_t tmem;
     __shared__ int aborted, last_s;
-    __shared__ int row_e[MATS][128];
-    __shared__ float tok_f[WM_MAX_NT];
+    __shared__ int row_e[2][128];
+    __shared__ float tok_f[128];
     volatile int* ab = &aborted;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int tile = blockIdx.x, blk = blockIdx.y, split = blockIdx.z;
-    const int row0 = tile * 128, tok0 = blk * p.nt, m = min(p.nt, p.tokens - tok0);
-    // this split's steps of 64 columns, an even number but for the last split's
-    const int pairs = (p.ksteps + 1) >> 1;
-    const int s0 = 2 * (int)((long long)split * pairs / p.ks);
-    const int s1 = min(p.ksteps, 2 * (int)((long long)(split + 1) * pairs / p.ks));
-    const int n = s1 - s0;
-    const int xbytes = p.nt * P * 128, cbytes = WM_CODES * MATS;
+    const int row0 = tile * ROWS, tok0 = blk * p.nt, m = min(p.nt, p.tokens - tok0);
+    const int s0 = (int)((long long)split * p.steps / p.ks), s1 = (int)((long long)(split + 1) * p.steps / p.ks);
+    const int n = s1 - s0;                     // steps of this split, >= 1
+    const int xbytes = wm_stage(P, p.nt);
     unsigned char* codes_s = smem;
-    unsigned char* x_s = smem + (size_t)p.sc * cbytes;
+    unsigned char* x_s = smem + (size_t)p.sc * WM_CODES;
     const int spitch = p.K / G;
 
     if (warp == 0) {
@@ -141,22 +174,26 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             mbar_init(&codes_full[s], 1);
             mbar_init(&codes_empty[s], WM_DQ);
         }
-        for (int s = 0; s < p.sb; ++s) {
+        for (int s = 0; s < p.sx; ++s) {
             mbar_init(&x_full[s], 1);
             mbar_init(&x_empty[s], 1);
         }
-        for (int s = 0; s < p.na; ++s) {
-            mbar_init(&a_full[s], WM_DQ / 2);
+        for (int s = 0; s < p.sa; ++s) {
+            mbar_init(&a_full[s], WM_DQ);
             mbar_init(&a_empty[s], 1);
         }
-        mbar_init(&done, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&d_full[s], 1);
+            mbar_init(&d_empty[s], WM_DQ);
+        }
         aborted = 0;
         mbar_fence_init();
     }
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t dt = tmem, at0 = dt + (uint32_t)(p.nt * MATS);   // accumulators, then the ring of A
+    // TMEM columns: accumulators (tile i at i * nt, the second pair behind the first), then the ring of A
+    const uint32_t dt = tmem, at0 = dt + (uint32_t)(p.nt * (FOLD ? 4 : 2));
     auto give_up = [&]() {
         *ab = 1;
         atomicOr(p.err, FAULT_WAIT);
@@ -164,20 +201,19 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
 
     if (warp == WM_DQ) {
         // ---- codes ----
-        int issued = 0;
-        const int stages = (n + 1) >> 1;
         if (lane == 0) {
-            for (int s = 0; s < stages; ++s) {
-                const int slot = s % p.sc;
+            Ring r;
+            int issued = 0;
+            for (int s = 0; s < n; ++s, r.next(p.sc)) {
                 if (*ab) break;
-                if (s >= p.sc && !mbar_wait(&codes_empty[slot], (uint32_t)(s / p.sc - 1) & 1u)) {
+                if (s >= p.sc && !mbar_wait(&codes_empty[r.slot], r.odd ^ 1u)) {
                     give_up();
                     break;
                 }
-                mbar_arrive_expect_tx(&codes_full[slot], (uint32_t)cbytes);
-#pragma unroll
-                for (int i = 0; i < MATS; ++i)
-                    tma_load_2d(codes_s + (size_t)slot * cbytes + i * WM_CODES, &p.codes[i], (s0 + 2 * s) * 32, row0, &codes_full[slot]);
+                unsigned char* dst = codes_s + (size_t)r.slot * WM_CODES;
+                mbar_arrive_expect_tx(&codes_full[r.slot], WM_CODES);
+                tma_load_2d(dst, &p.codes[0], (s0 + s) * 64, row0, &codes_full[r.slot]);
+                tma_load_2d(dst + WM_CODES / 2, &p.codes[1], (s0 + s) * 64, GLU ? row0 : row0 + 128, &codes_full[r.slot]);
                 issued = s + 1;
             }
             // no copy may still be landing when the CTA exits
@@ -186,62 +222,95 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         }
         __syncwarp();
     } else if (warp == WM_DQ + 1) {
-        // ---- activations ----
-        int issued = 0;
+        // ---- activations: a step is one stage of 128 columns, or two of 64 with both parts ----
         if (lane == 0) {
             pdl_wait();   // k_w4_split has written them
-            for (int s = 0; s < n; ++s) {
-                const int slot = s % p.sb;
+            Ring r;
+            int issued = 0;
+            for (int s = 0; s < n * XH; ++s, r.next(p.sx)) {
                 if (*ab) break;
-                if (s >= p.sb && !mbar_wait(&x_empty[slot], (uint32_t)(s / p.sb - 1) & 1u)) {
+                if (s >= p.sx && !mbar_wait(&x_empty[r.slot], r.odd ^ 1u)) {
                     give_up();
                     break;
                 }
-                mbar_arrive_expect_tx(&x_full[slot], (uint32_t)xbytes);
+                unsigned char* dst = x_s + (size_t)r.slot * xbytes;
+                mbar_arrive_expect_tx(&x_full[r.slot], (uint32_t)xbytes);
 #pragma unroll
-                for (int i = 0; i < P; ++i)
-                    tma_load_2d(x_s + (size_t)slot * xbytes + i * p.nt * 128, &p.x, (s0 + s) * 64, i * p.tokens + tok0, &x_full[slot]);
+                for (int i = 0; i < 2; ++i)
+                    tma_load_2d(dst + i * p.nt * 128, &p.x, P == 2 ? (s0 * 2 + s) * 64 : (s0 + s) * 128 + i * 64,
+                                P == 2 ? i * p.tokens + tok0 : tok0, &x_full[r.slot]);
                 issued = s + 1;
             }
-            for (int s = max(0, issued - p.sb); s < issued; ++s)
-                if (!mbar_wait(&x_full[s % p.sb], (uint32_t)(s / p.sb) & 1u)) give_up();
+            for (int s = max(0, issued - p.sx); s < issued; ++s)
+                if (!mbar_wait(&x_full[s % p.sx], (uint32_t)(s / p.sx) & 1u)) give_up();
         }
         __syncwarp();
     } else if (warp == WM_DQ + 2) {
-        // ---- products ----
+        // ---- products: one warp, which lies on the tensor cores' path ----
         const uint32_t idesc = (1u << 4) | ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-        for (int s = 0; s < n; ++s) {
-            const int sa = s % p.na, sx = s % p.sb;
-            const bool ok = !*ab && mbar_wait(&a_full[sa], (uint32_t)(s / p.na) & 1u) && mbar_wait(&x_full[sx], (uint32_t)(s / p.sb) & 1u);
-            if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) give_up();
-                break;
-            }
+        const uint32_t xd = wm_desc(smem_u32(x_s)), half = (uint32_t)(p.nt * 128) >> 4;
+        Ring ra, rx;
+        int fold = 0, used = 0;                // steps in the accumulators; pairs of them handed over
+        bool ok = true;
+        for (int s = 0; s < n; ++s, ra.next(p.sa)) {
+            const uint32_t d = dt + (FOLD && (used & 1) ? (uint32_t)(2 * p.nt) : 0u);
+            if (FOLD && fold == 0 && used >= 2) ok = mbar_wait(&d_empty[used & 1], (uint32_t)((used >> 1) - 1) & 1u);
+            ok = ok && mbar_wait(&x_full[rx.slot], rx.odd) && mbar_wait(&a_full[ra.slot], ra.odd);
+            if (!__all_sync(0xffffffffu, ok)) break;
             fence_after();
-            const uint32_t xb = smem_u32(x_s + (size_t)sx * xbytes);
+            const uint32_t a = at0 + (uint32_t)(ra.slot * 128);
 #pragma unroll
-            for (int i = 0; i < MATS; ++i)
+            for (int h = 0; h < 2; ++h) {
+                if (P == 2 && h == 1) {
+                    ok = mbar_wait(&x_full[rx.slot], rx.odd);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    fence_after();
+                }
+                const uint32_t x = xd + (uint32_t)(rx.slot * (xbytes >> 4));
+                const uint32_t acc = fold > 0 || h > 0 ? 1u : 0u;
+                // B: P == 1: half h of the stage; P == 2: the second parts first, while the sums are small
 #pragma unroll
-                for (int q = 0; q < P; ++q)
-                    mma_64(dt + (uint32_t)(i * p.nt), at0 + (uint32_t)((sa * MATS + i) * 32), xb + (uint32_t)(q * p.nt * 128), idesc,
-                           s > 0 || q > 0 ? 1u : 0u);
-            commit(&a_empty[sa]);
-            commit(&x_empty[sx]);
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t ai = a + (uint32_t)(i * 64 + h * 32), di = d + (uint32_t)(i * p.nt);
+                    if (P == 1) {
+                        mma_64(di, ai, x + h * half, idesc, acc);
+                    } else {
+                        mma_64(di, ai, x + half, idesc, acc);
+                        mma_64(di, ai, x, idesc, 1u);
+                    }
+                }
+                if (P == 2 || h == 1) {
+                    commit(&x_empty[rx.slot]);
+                    rx.next(p.sx);
+                }
+            }
+            if (!ok) break;                    // the same for all lanes
+            commit(&a_empty[ra.slot]);
+            if (++fold == (FOLD ? WM_FOLD : n) || s + 1 == n) {
+                commit(&d_full[FOLD ? used & 1 : 0]);
+                ++used;
+                fold = 0;
+            }
         }
-        commit(&done);
+        if (!__all_sync(0xffffffffu, ok) && lane == 0) give_up();
+        __syncwarp();
     } else {
         // ---- weights ----
         const int wg = warp >> 2, r = (warp & 3) * 32 + lane;   // TMEM lane = tile row
-        // the rows' powers of two: a warp takes 16 rows of each matrix, its lanes the scales of a row
-        const int g0 = s0 * 64 / G, g1 = min(spitch, (s1 * 64 + G - 1) / G);
+        const int mat = wg >> 1, h = wg & 1;                    // tile, half of the step's columns
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        // the rows' powers of two: a warp takes 16 rows, its lanes the scales of a row
+        {
+            const int g0 = s0 * (128 / G), g1 = min(spitch, s1 * (128 / G));
+            const int i = warp >> 3, first = row0 + (GLU ? 0 : i * 128);
+            const unsigned short* base = reinterpret_cast<const unsigned short*>(p.scales[i]);
 #pragma unroll
-        for (int i = 0; i < MATS; ++i) {
-#pragma unroll 4
             for (int j = 0; j < 16; ++j) {
-                const int rr = warp * 16 + j;
+                const int rr = (warp & 7) * 16 + j;
                 uint32_t top = 0;
-                if (row0 + rr < p.N) {
-                    const unsigned short* s = reinterpret_cast<const unsigned short*>(p.scales[i]) + (size_t)(row0 + rr) * spitch;
+                if (first + rr < p.N) {
+                    const unsigned short* s = base + (size_t)(first + rr) * spitch;
                     for (int c = g0 + lane; c < g1; c += 32) {
                         const uint32_t b = __ldg(s + c) & 0x7fffu;
                         top = max(top, b < 0x7f80u ? b : 0u);
@@ -252,136 +321,217 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             }
         }
         named_sync(1, WM_DQ * 32);
-        const bool in = row0 + r < p.N;
-        float up[MATS];
-        const unsigned short* sp[MATS];
-#pragma unroll
-        for (int i = 0; i < MATS; ++i) {
-            up[i] = row_up(row_e[i][r]);
-            sp[i] = reinterpret_cast<const unsigned short*>(p.scales[i]) + (size_t)(in ? row0 + r : 0) * spitch;
-        }
+        const int nn = row0 + (GLU ? 0 : mat * 128) + r;        // this thread's row of its matrix
+        const bool in = nn < p.N;
+        const float up = row_up(row_e[mat][r]), down = row_down(row_e[mat][r]);
+        const unsigned short* sp = reinterpret_cast<const unsigned short*>(p.scales[mat]) + (size_t)(in ? nn : 0) * spitch;
         // eight scales of the row at a time, the next eight under way
-        constexpr int WIN = 8 * G / 64;   // steps of eight groups
-        uint4 sw[MATS], sn[MATS];
-        int win = -1;
-        auto load_win = [&](int i, int w) {
-            return w * 8 < spitch ? __ldg(reinterpret_cast<const uint4*>(sp[i]) + w) : make_uint4(0u, 0u, 0u, 0u);
+        constexpr int WIN = 8 * G / 128;       // steps of eight groups
+        uint4 sw = make_uint4(0u, 0u, 0u, 0u), sn = sw;
+        int left = 0;                          // steps that sw still serves
+        auto load_win = [&](int w) { return w * 8 < spitch ? __ldg(reinterpret_cast<const uint4*>(sp) + w) : make_uint4(0u, 0u, 0u, 0u); };
+        if (p.wide) {
+            sw = load_win(s0 / WIN);
+            sn = load_win(s0 / WIN + 1);
+            left = WIN - s0 % WIN;
+        }
+        // fp32 activations: the sums of 32 tokens of this thread's row; tokens 32 h .. 32 h + 31 of tile `mat`
+        float acc[FOLD ? 32 : 1];
+#pragma unroll
+        for (int e = 0; e < (FOLD ? 32 : 1); ++e) acc[e] = 0.f;
+        int folded = 0;                        // pairs of accumulators taken
+        auto fold_in = [&]() -> bool {
+            if (!mbar_wait(&d_full[folded & 1], (uint32_t)(folded >> 1) & 1u)) return false;
+            fence_after();
+            if (h * 32 < p.nt) {
+                uint32_t v[32];
+                tmem_ld32(dt + lanes + (uint32_t)((folded & 1) * 2 * p.nt + mat * p.nt + h * 32), v);
+                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                for (int e = 0; e < (FOLD ? 32 : 1); ++e) {
+                    asm volatile("" : "+r"(v[e]));
+                    acc[e] += __uint_as_float(v[e]);
+                }
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&d_empty[folded & 1]);
+            ++folded;
+            return true;
         };
         const int swz = (r >> 1) & 3;
-        for (int s = wg; s < n; s += 2) {
-            const int cs = s >> 1, slot = cs % p.sc, sa = s % p.na, step = s0 + s;
-            uint32_t sc[MATS][G == 32 ? 2 : 1];
+        const unsigned char* row = codes_s + mat * (WM_CODES / 2) + r * 64;
+        const int c0 = ((2 * h) ^ swz) << 4, c1 = ((2 * h + 1) ^ swz) << 4;
+        Ring rc, ra;
+        bool ok = true;
+        uint4 q0, q1;                          // a row's 32 bytes of codes
+        auto read_codes = [&]() {
+            ok = mbar_wait(&codes_full[rc.slot], rc.odd) && ok;
+            q0 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * WM_CODES + c0);
+            q1 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * WM_CODES + c1);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&codes_empty[rc.slot]);
+            rc.next(p.sc);
+        };
+        read_codes();
+        for (int s = 0; s < n; ++s, ra.next(p.sa)) {
+            const int step = s0 + s;
+            uint32_t sc[NS];
             if (p.wide) {
-                const int w = step / WIN;
-                if (w != win) {
-#pragma unroll
-                    for (int i = 0; i < MATS; ++i) {
-                        sw[i] = win < 0 ? load_win(i, w) : sn[i];
-                        sn[i] = load_win(i, w + 1);
-                    }
-                    win = w;
+                if (left == 0) {
+                    sw = sn;
+                    sn = load_win(step / WIN + 1);
+                    left = WIN;
                 }
+                --left;
 #pragma unroll
-                for (int i = 0; i < MATS; ++i)
-#pragma unroll
-                    for (int h = 0; h < (G == 32 ? 2 : 1); ++h)
-                        sc[i][h] = scale_pair(pick16(sw[i], (G == 32 ? step * 2 + h : step * 64 / G) & 7), up[i]);
+                for (int c = 0; c < NS; ++c)
+                    sc[c] = scale_pair(pick16(sw, (G == 128 ? step : G == 64 ? 2 * step + h : 4 * step + 2 * h + c) & 7), up);
             } else {
 #pragma unroll
-                for (int i = 0; i < MATS; ++i)
-#pragma unroll
-                    for (int h = 0; h < (G == 32 ? 2 : 1); ++h) {
-                        const int c = G == 32 ? step * 2 + h : step * 64 / G;
-                        sc[i][h] = c < spitch ? scale_pair(__ldg(sp[i] + c), up[i]) : 0u;
-                    }
-            }
-            bool ok = !*ab && mbar_wait(&codes_full[slot], (uint32_t)(cs / p.sc) & 1u);
-            uint4 q[MATS][2];
-#pragma unroll
-            for (int i = 0; i < MATS; ++i) {
-                const unsigned char* row = codes_s + (size_t)slot * cbytes + i * WM_CODES + r * 64;
-                q[i][0] = *reinterpret_cast<const uint4*>(row + (((2 * wg) ^ swz) << 4));
-                q[i][1] = *reinterpret_cast<const uint4*>(row + (((2 * wg + 1) ^ swz) << 4));
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&codes_empty[slot]);
-            if (s >= p.na) ok = ok && mbar_wait(&a_empty[sa], (uint32_t)(s / p.na - 1) & 1u);
-            if (!__all_sync(0xffffffffu, ok)) {
-                if (lane == 0) give_up();
-                break;
-            }
-            fence_after();
-#pragma unroll
-            for (int i = 0; i < MATS; ++i) {
-                uint32_t a[32];
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t w[4] = {q[i][h].x, q[i][h].y, q[i][h].z, q[i][h].w};
-                    const uint32_t f = sc[i][G == 32 ? h : 0];
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t pr[4];
-                        w4_unpack(w[c], pr);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) a[h * 16 + c * 4 + e] = w4_hmul(pr[e], f);
-                    }
+                for (int c = 0; c < NS; ++c) {
+                    const int g = G == 128 ? step : G == 64 ? 2 * step + h : 4 * step + 2 * h + c;
+                    sc[c] = g < spitch ? scale_pair(__ldg(sp + g), up) : 0u;
                 }
-                tm_st32(at0 + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)((sa * MATS + i) * 32), a);
             }
+            const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+            if (s + 1 < n) read_codes();       // the next step's, under this one's arithmetic
+            uint32_t a[32];
+            {
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t pr[4];
+                    w4_unpack(w[c], pr);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) a[c * 4 + e] = w4_hmul(pr[e], sc[NS == 2 ? c >> 2 : 0]);
+                }
+            }
+            if (s >= p.sa) ok = mbar_wait(&a_empty[ra.slot], ra.odd ^ 1u) && ok;
+            if (!__all_sync(0xffffffffu, ok)) break;
+            fence_after();
+            tm_st32(at0 + lanes + (uint32_t)(ra.slot * 128 + mat * 64 + h * 32), a);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&a_full[sa]);
+            if (lane == 0) mbar_arrive(&a_full[ra.slot]);
+            // a pair of accumulators is taken a step after its last weights were made: its products have had that long
+            if (FOLD && s >= WM_FOLD && s % WM_FOLD == 0) {
+                ok = fold_in();
+                if (!__all_sync(0xffffffffu, ok)) break;
+            }
         }
-        // an odd number of steps: the second warpgroup leaves its half of the last stage unread
-        if ((n & 1) && wg == 1 && lane == 0) mbar_arrive(&codes_empty[((n - 1) >> 1) % p.sc]);
+        if (!__all_sync(0xffffffffu, ok) && lane == 0) give_up();
 
         // ---- epilogue ----
         pdl_wait();
         for (int i = tid; i < m; i += WM_DQ * 32) tok_f[i] = __ldcg(p.factor + tok0 + i);
+        bool live = __all_sync(0xffffffffu, ok) && !*ab;
+        if (FOLD) {
+            const int pairs = (n + WM_FOLD - 1) / WM_FOLD;
+            while (live && folded < pairs) live = __all_sync(0xffffffffu, fold_in());
+        } else if (live) {
+            live = __all_sync(0xffffffffu, mbar_wait(&d_full[0], 0u));
+            fence_after();
+        }
+        if (!live && lane == 0) give_up();
         named_sync(1, WM_DQ * 32);
-        const bool okd = mbar_wait(&done, 0u);
-        if (!okd) give_up();
-        fence_after();
-        const bool live = okd && !*ab;
-        const int nn = row0 + r;
-        float down[MATS];
-#pragma unroll
-        for (int i = 0; i < MATS; ++i) down[i] = row_down(row_e[i][r]);
-        auto put = [&](int t, float v, float u) {   // token t of the block; sums in true size
-            if (GLU) v = w4_glu(p.act, v, u);
-            else if (p.residual) v += w4_load1(p.residual, p.out_f32, (size_t)(tok0 + t) * p.residual_stride + nn);
-            w4_store1(p.out, p.out_f32, (size_t)(tok0 + t) * p.out_stride + nn, v);
-        };
+        live = !*ab;
         // the smaller factor first: no step leaves fp32's range unless the result does
-        auto sized = [&](float v, float a, float b) { return v * fminf(a, b) * fmaxf(a, b); };
-        if (__all_sync(0xffffffffu, live)) {
-            for (int c = wg * 16; c < p.nt; c += 32) {
-                if (c >= m) break;
-                uint32_t d[MATS][16];
+        auto sized = [&](float v, float b) { return v * fminf(down, b) * fmaxf(down, b); };
+        // the results of up to 16 tokens from token c of the block for output row nn: sums v (of the gate; then u of up)
+        auto put16 = [&](int c, int count, float (&v)[16], float (&u)[16]) {
+            if (GLU) {
 #pragma unroll
-                for (int i = 0; i < MATS; ++i) tm_ld16(dt + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(i * p.nt + c), d[i]);
-                float res[16];
+                for (int e = 0; e < 16; ++e) v[e] = w4_glu(p.act, v[e], u[e]);
+            } else if (p.residual) {
+                const size_t at = (size_t)(tok0 + c) * p.residual_stride + nn;
+                if (p.out_f32) {
+                    const float* x = reinterpret_cast<const float*>(p.residual) + at;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] = e < count ? x[(size_t)e * p.residual_stride] : 0.f;
+                } else {
+                    const __nv_bfloat16* x = reinterpret_cast<const __nv_bfloat16*>(p.residual) + at;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) u[e] = e < count ? __bfloat162float(x[(size_t)e * p.residual_stride]) : 0.f;
+                }
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] += u[e];
+            }
+            const size_t at = (size_t)(tok0 + c) * p.out_stride + nn;
+            if (p.out_f32) {
+                float* o = reinterpret_cast<float*>(p.out) + at;
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
-                    res[e] = !GLU && p.ks == 1 && p.residual && in && c + e < m
-                                 ? w4_load1(p.residual, p.out_f32, (size_t)(tok0 + c + e) * p.residual_stride + nn) : 0.f;
+                    if (e < count) o[(size_t)e * p.out_stride] = v[e];
+            } else {
+                __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(p.out) + at;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (e < count) o[(size_t)e * p.out_stride] = __float2bfloat16_rn(v[e]);
+            }
+        };
+        // Sums of 16 tokens from token c for this thread's row of its matrix.  Plain and split results go out from here; a
+        // gate's meet the up's in shared memory (the codes' ring: all copies have landed, all weights are made)
+        constexpr int US = 129;                // of a token's 128 rows
+        float* meet = reinterpret_cast<float*>(smem);            // [nt][US]
+        const size_t pitch = (size_t)p.N * (GLU ? 2 : 1);
+        auto take16 = [&](int c, float (&v)[16]) {
+            const int count = min(16, m - c);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = e < count ? sized(v[e], tok_f[c + e]) : 0.f;
+            if (p.ks > 1) {
+                float* o = p.part + ((size_t)split * p.tokens + tok0 + c) * pitch + (GLU ? mat * p.N : 0) + nn;
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (in && e < count) o[e * pitch] = v[e];
+            } else if (GLU) {
+                if (mat == 1) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) meet[(c + e) * US + r] = v[e];
+                }
+            } else if (in) {
+                float u[16];
+                put16(c, count, v, u);
+            }
+        };
+        // P == 1: chunks of 16 tokens of a tile go to its two warpgroups in turn.  P == 2: they are in acc
+        auto chunk = [&](int c, float (&v)[16]) {
+            if (FOLD) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) v[e] = c & 16 ? acc[FOLD ? 16 + e : 0] : acc[FOLD ? e : 0];
+            } else {
+                uint32_t d[16];
+                tm_ld16(dt + lanes + (uint32_t)(mat * p.nt + c), d);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
+                    asm volatile("" : "+r"(d[e]));
+                    v[e] = __uint_as_float(d[e]);
+                }
+            }
+        };
+        const int cfirst = FOLD ? h * 32 : h * 16, cstep = FOLD ? 16 : 32, cend = FOLD ? min(m, h * 32 + 32) : m;
+        if (live) {
+            for (int c = cfirst; c < cend; c += cstep) {
+                float v[16];
+                if (GLU && p.ks == 1 && mat == 0) continue;      // up first
+                chunk(c, v);
+                take16(c, v);
+            }
+        }
+        if (GLU && p.ks == 1) {
+            named_sync(1, WM_DQ * 32);
+            if (live && mat == 0) {
+                for (int c = cfirst; c < cend; c += cstep) {
+                    float v[16], u[16];
+                    const int count = min(16, m - c);
+                    chunk(c, v);
 #pragma unroll
-                    for (int i = 0; i < MATS; ++i) asm volatile("" : "+r"(d[i][e]));
-                    if (!in || c + e >= m) continue;
-                    const float f = tok_f[c + e];
-                    const float v = sized(__uint_as_float(d[0][e]), down[0], f);
-                    const float u = GLU ? sized(__uint_as_float(d[MATS - 1][e]), down[MATS - 1], f) : 0.f;
-                    if (p.ks > 1) {
-                        float* o = p.part + ((size_t)split * p.tokens + tok0 + c + e) * p.N * MATS + nn;
-                        o[0] = v;
-                        if (GLU) o[p.N] = u;
-                    } else {
-                        w4_store1(p.out, p.out_f32, (size_t)(tok0 + c + e) * p.out_stride + nn, GLU ? w4_glu(p.act, v, u) : v + res[e]);
+                    for (int e = 0; e < 16; ++e) {
+                        v[e] = e < count ? sized(v[e], tok_f[c + e]) : 0.f;
+                        u[e] = meet[(c + e) * US + r];
                     }
+                    if (in) put16(c, count, v, u);
                 }
             }
         }
@@ -397,16 +547,27 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             named_sync(1, WM_DQ * 32);
             if (last_s) {
                 __threadfence();
-                if (in) {
-                    for (int t = wg; t < m; t += 2) {
-                        float v = 0.f, u = 0.f;
-                        for (int w = 0; w < p.ks; ++w) {
-                            const float* o = p.part + ((size_t)w * p.tokens + tok0 + t) * p.N * MATS + nn;
-                            v += __ldcg(o);
-                            if (GLU) u += __ldcg(o + p.N);
+                // rows as before; gate/up: all four warpgroups take rows of the one output
+                for (int c = (GLU ? wg : h) * 16; in && c < m; c += GLU ? 64 : 32) {
+                    const int count = min(16, m - c);
+                    float v[16], u[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) v[e] = u[e] = 0.f;
+                    for (int w = 0; w < p.ks; ++w) {
+                        const float* o = p.part + ((size_t)w * p.tokens + tok0 + c) * pitch + nn;
+                        float b[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) b[e] = e < count ? __ldcg(o + e * pitch) : 0.f;
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] += b[e];
+                        if (GLU) {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) b[e] = e < count ? __ldcg(o + e * pitch + p.N) : 0.f;
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) u[e] += b[e];
                         }
-                        put(t, v, u);
                     }
+                    put16(c, count, v, u);
                 }
             }
         }
@@ -534,21 +695,21 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
     const W4Call& c = g->c;
-    const int P = c.x_f32 ? 2 : 1, mats = c.glu ? 2 : 1;
-    const int tiles = (c.n() + 127) / 128, ksteps = (c.k() + 63) / 64, most = P * mats > 1 ? 128 : 256;
-    // Tokens of a tile and CTAs along k: the least time of the longest CTA, in clocks.  A step of 64 columns takes the
-    // tensor cores 2 clocks a token, part and matrix, its weights 150 a matrix to make; a CTA starts and ends in about
-    // 4000, and a split adds the writing and reading of its sums
+    const int P = c.x_f32 ? 2 : 1, rows = c.glu ? 128 : 256;
+    const int tiles = (c.n() + rows - 1) / rows, steps = (c.k() + 127) / 128;
+    // Tokens of a tile and CTAs along k: the least time of the longest CTA, in clocks.  A step takes the tensor cores 8
+    // clocks a token and part, or the making and handing over of its weights 650; a CTA starts and ends in about 7000,
+    // and a split adds the writing and reading of its sums
     double best = -1.0;
-    const int least = (c.tokens + most - 1) / most;
+    const int least = (c.tokens + wm_tokens(P) - 1) / wm_tokens(P);
     for (int blocks = least; blocks <= least + 8; ++blocks) {
         const int nt = round_up((c.tokens + blocks - 1) / blocks, 16), used = (c.tokens + nt - 1) / nt;
         for (int ks = 1; ks <= 16; ++ks) {
-            if (ks > 1 && (ksteps / ks < 8 || (long long)tiles * used > DEC_W4_COUNTER_BYTES / 4)) break;
+            if (ks > 1 && (steps / ks < 2 || (long long)tiles * used > DEC_W4_COUNTER_BYTES / 4)) break;
             const double waves = (double)(((long long)tiles * used * ks + num_sms - 1) / num_sms);
-            const double step = 2.0 * nt * P * mats > 150.0 * mats ? 2.0 * nt * P * mats : 150.0 * mats;
-            const double t = waves * ((double)((ksteps + ks - 1) / ks) * step + 4000.0 + 12.0 * nt * mats) +
-                             (ks > 1 ? 2500.0 + 10.0 * nt * mats * ks : 0.0);
+            const double step = 8.0 * nt * P > 650.0 ? 8.0 * nt * P : 650.0;
+            const double t = waves * ((double)((steps + ks - 1) / ks) * step + 7000.0 + 16.0 * nt) +
+                             (ks > 1 ? 2500.0 + 16.0 * nt * ks : 0.0);
             if (best < 0.0 || t < best) {
                 best = t;
                 g->nt = nt;
@@ -558,7 +719,7 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
         if (nt <= 16) break;
     }
     g->kp = round_up(c.k(), 64);
-    g->ksteps = ksteps;
+    g->steps = steps;
     const void* fn = kernel_of(*g);
     static OncePerDevice once[3][2][2];
     return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][P - 1][c.glu].run([&] { return raise_smem_cap(fn); });
@@ -596,22 +757,22 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     p.tokens = c.tokens;
     p.nt = g.nt;
     p.ks = g.ks;
-    p.ksteps = g.ksteps;
+    p.steps = g.steps;
     p.act = c.act;
     p.out_f32 = c.out_f32;
     p.wide = (c.k() / c.group()) % 8 == 0 && ((uintptr_t)p.scales[0] & 15) == 0 && ((uintptr_t)p.scales[1] & 15) == 0;
     p.part = (float*)((char*)factor + round256((size_t)c.tokens * 4));
     p.count = g.count;
     p.err = c.err;
-    // the rings: activations first, the rest for codes
-    const int xb = g.nt * P * 128, cb = WM_CODES * mats;
-    p.sb = (WM_SMEM - 4 * cb) / xb;
-    if (p.sb > WM_MAX_SB) p.sb = WM_MAX_SB;
-    p.sc = (WM_SMEM - p.sb * xb) / cb;
+    // the rings: four stages of codes at least (behind the last step they also hold a tile's up sums), then activations
+    const int xb = wm_stage(P, g.nt);
+    p.sx = (WM_SMEM - 5 * WM_CODES) / xb;
+    if (p.sx > WM_MAX_SX) p.sx = WM_MAX_SX;
+    p.sc = (WM_SMEM - p.sx * xb) / WM_CODES;
     if (p.sc > WM_MAX_SC) p.sc = WM_MAX_SC;
-    p.na = (512 - g.nt * mats) / (32 * mats);
-    if (p.na > 8) p.na = 8;
-    if (p.sb < 2 || p.sc < 2 || p.na < 2) return cudaErrorInvalidValue;
+    p.sa = (512 - g.nt * (P == 2 ? 4 : 2)) / 128;
+    if (p.sa > WM_MAX_SA) p.sa = WM_MAX_SA;
+    if (p.sx < 2 || p.sc < 5 || p.sa < 2) return cudaErrorInvalidValue;
 
     if (P == 1)
         k_w4_split<1><<<c.tokens, WS_THREADS, 0, s>>>(c.x, c.x_stride, c.x_f32, c.gain, c.gain_f32, c.eps, c.k(), g.kp, c.tokens, parts, factor);
@@ -620,9 +781,10 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((c.n() + 127) / 128, (c.tokens + g.nt - 1) / g.nt, g.ks);
+    const int rows = c.glu ? 128 : 256;
+    cfg.gridDim = dim3((c.n() + rows - 1) / rows, (c.tokens + g.nt - 1) / g.nt, g.ks);
     cfg.blockDim = dim3(WM_THREADS);
-    cfg.dynamicSmemBytes = (size_t)p.sb * xb + (size_t)p.sc * cb + 1024;
+    cfg.dynamicSmemBytes = (size_t)p.sx * xb + (size_t)p.sc * WM_CODES + 1024;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];   // starts while k_w4_split runs: codes and scales do not depend on it
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
