@@ -3,9 +3,9 @@
 //
 // out[t, n] = sum_k W[n, k] a[t, k].  The tensor cores take fp16, and a stored weight
 // is exact in fp16: a code of 4 bits times a scale of 8 significant bits has 11, so
-// once the scales of a row are brought to fp16's range by one power of two (2^11 at
-// the row's largest) nothing is rounded (a scale more than 2^28 below the row's largest
-// loses bits, 2^-39 of that largest).  Activations are fp16 parts, scaled by a power of
+// once the scales of a row are brought to fp16's range by one power of two (2^10 at
+// the row's largest) nothing is rounded (a scale more than 2^27 below the row's largest
+// loses bits, 2^-38 of that largest).  Activations are fp16 parts, scaled by a power of
 // two a token: one part for bf16 ones (8 bits fit), two for fp32.
 //
 //   k_w4_split   one CTA a token: RMSNorm's sum, the token's power of two, its parts in
@@ -19,7 +19,7 @@
 //                and its reads are left to B
 //     warp 16    codes by TMA (64-byte swizzle)
 //     warp 17    activations by TMA (128-byte swizzle)
-//     warp 18    tcgen05.mma kind::f16, two accumulators in TMEM
+//     warps 18-19 tcgen05.mma kind::f16, a tile each, accumulators in TMEM
 //   and warps 0-15 again for the epilogue: thread = output row, so a warp's stores of one
 //   token lie side by side.
 // The tensor core cuts its fp32 sums off instead of rounding them.  For fp32 activations
@@ -37,7 +37,7 @@ namespace gd {
 namespace {
 
 constexpr int WM_DQ = 16;                      // warps that make weights, and write results: four warpgroups
-constexpr int WM_THREADS = (WM_DQ + 3) * 32;
+constexpr int WM_THREADS = (WM_DQ + 4) * 32;
 constexpr int WM_CODES = 2 * 128 * 64;         // bytes of a codes stage: two tiles of 128 rows x 128 columns
 constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 3;
 constexpr int WM_SMEM = 200 * 1024;            // for both rings
@@ -125,13 +125,22 @@ struct Ring {
     }
 };
 
-// a row's scales are multiplied by 2^(11 - e), 2^e the power of two at or below the largest of them: weights below 2^15
-__device__ __forceinline__ float row_up(int e) { return __uint_as_float((uint32_t)(265 - e) << 23); }
-__device__ __forceinline__ float row_down(int e) { return __uint_as_float((uint32_t)(e - 11) << 23); }
+// a row's scales are multiplied by 2^(10 - e), 2^e the power of two at or below the largest of them: weights below 2^14
+__device__ __forceinline__ float row_up(int e) { return __uint_as_float((uint32_t)(264 - e) << 23); }
+__device__ __forceinline__ float row_down(int e) { return __uint_as_float((uint32_t)(e - 10) << 23); }
 // a scale's bf16 bits as the scaled fp16 in both halves
 __device__ __forceinline__ uint32_t scale_pair(uint32_t bits, float up) {
     const float s = __uint_as_float(bits << 16) * up;
     return w4_pack_half(s, s);
+}
+// The columns (j, j + 4) of a word times a scale s, f = (s, s) and f24 = (-24 s, -24 s), exact.  Two pairs as in w4_unpack,
+// then times s; the other two with the code moved to the top of the mantissa of 16, where (16 + (q + 8)) s - 24 s is one
+// fused step (24 s has 10 significant bits): so the half-precision and the integer pipe get as much each
+__device__ __forceinline__ void unpack_scaled(uint32_t w, uint32_t f, uint32_t f24, uint32_t* o) {
+    o[0] = w4_hmul(w4_hsub((w & 0x000f000fu) ^ 0x64086408u, 0x64086408u), f);
+    o[1] = w4_hmul(w4_hfma((w & 0x00f000f0u) ^ 0x64806480u, 0x2c002c00u, 0xd480d480u), f);
+    o[2] = w4_hfma(((w >> 2) & 0x03c003c0u) ^ 0x4e004e00u, f, f24);   // 0x4c00 is 16; 0x200 turns the code's sign bit over
+    o[3] = w4_hfma(((w >> 6) & 0x03c003c0u) ^ 0x4e004e00u, f, f24);
 }
 __device__ __forceinline__ uint32_t pick16(const uint4& w, int i) {   // element i (0 .. 7) of eight
     const uint32_t lo = i & 2 ? w.y : w.x, hi = i & 2 ? w.w : w.z, v = i & 4 ? hi : lo;
@@ -176,14 +185,14 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         }
         for (int s = 0; s < p.sx; ++s) {
             mbar_init(&x_full[s], 1);
-            mbar_init(&x_empty[s], 1);
+            mbar_init(&x_empty[s], 2);         // both issuing warps
         }
         for (int s = 0; s < p.sa; ++s) {
             mbar_init(&a_full[s], WM_DQ);
-            mbar_init(&a_empty[s], 1);
+            mbar_init(&a_empty[s], 2);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&d_full[s], 1);
+            mbar_init(&d_full[s], 2);
             mbar_init(&d_empty[s], WM_DQ);
         }
         aborted = 0;
@@ -245,20 +254,21 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 if (!mbar_wait(&x_full[s % p.sx], (uint32_t)(s / p.sx) & 1u)) give_up();
         }
         __syncwarp();
-    } else if (warp == WM_DQ + 2) {
-        // ---- products: one warp, which lies on the tensor cores' path ----
+    } else if (warp >= WM_DQ + 2) {
+        // ---- products: a warp for each tile, so that one's waits lie under the other's MMAs ----
+        const int i = warp - (WM_DQ + 2);
         const uint32_t idesc = (1u << 4) | ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
         const uint32_t xd = wm_desc(smem_u32(x_s)), half = (uint32_t)(p.nt * 128) >> 4;
         Ring ra, rx;
         int fold = 0, used = 0;                // steps in the accumulators; pairs of them handed over
         bool ok = true;
         for (int s = 0; s < n; ++s, ra.next(p.sa)) {
-            const uint32_t d = dt + (FOLD && (used & 1) ? (uint32_t)(2 * p.nt) : 0u);
+            const uint32_t d = dt + (uint32_t)(i * p.nt) + (FOLD && (used & 1) ? (uint32_t)(2 * p.nt) : 0u);
             if (FOLD && fold == 0 && used >= 2) ok = mbar_wait(&d_empty[used & 1], (uint32_t)((used >> 1) - 1) & 1u);
             ok = ok && mbar_wait(&x_full[rx.slot], rx.odd) && mbar_wait(&a_full[ra.slot], ra.odd);
             if (!__all_sync(0xffffffffu, ok)) break;
             fence_after();
-            const uint32_t a = at0 + (uint32_t)(ra.slot * 128);
+            const uint32_t a = at0 + (uint32_t)(ra.slot * 128 + i * 64);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (P == 2 && h == 1) {
@@ -270,15 +280,11 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 const uint32_t x = xd + (uint32_t)(rx.slot * (xbytes >> 4));
                 const uint32_t acc = fold > 0 || h > 0 ? 1u : 0u;
                 // B: P == 1: half h of the stage; P == 2: the second parts first, while the sums are small
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t ai = a + (uint32_t)(i * 64 + h * 32), di = d + (uint32_t)(i * p.nt);
-                    if (P == 1) {
-                        mma_64(di, ai, x + h * half, idesc, acc);
-                    } else {
-                        mma_64(di, ai, x + half, idesc, acc);
-                        mma_64(di, ai, x, idesc, 1u);
-                    }
+                if (P == 1) {
+                    mma_64(d, a + (uint32_t)(h * 32), x + h * half, idesc, acc);
+                } else {
+                    mma_64(d, a + (uint32_t)(h * 32), x + half, idesc, acc);
+                    mma_64(d, a + (uint32_t)(h * 32), x, idesc, 1u);
                 }
                 if (P == 2 || h == 1) {
                     commit(&x_empty[rx.slot]);
@@ -398,13 +404,11 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             if (s + 1 < n) read_codes();       // the next step's, under this one's arithmetic
             uint32_t a[32];
             {
+                uint32_t f24[NS];
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    uint32_t pr[4];
-                    w4_unpack(w[c], pr);
+                for (int c = 0; c < NS; ++c) f24[c] = w4_hmul(sc[c], 0xce00ce00u);   // -24
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) a[c * 4 + e] = w4_hmul(pr[e], sc[NS == 2 ? c >> 2 : 0]);
-                }
+                for (int c = 0; c < 8; ++c) unpack_scaled(w[c], sc[NS == 2 ? c >> 2 : 0], f24[NS == 2 ? c >> 2 : 0], a + c * 4);
             }
             if (s >= p.sa) ok = mbar_wait(&a_empty[ra.slot], ra.odd ^ 1u) && ok;
             if (!__all_sync(0xffffffffu, ok)) break;
