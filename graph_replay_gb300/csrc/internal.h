@@ -211,7 +211,6 @@ struct W4Gemv {                // how w4_gemv.cu runs a call of few tokens
     int wk;                    // warps along k
     int ks;                    // CTAs along k
     int grid, rows;            // CTAs along n, output rows of each (the last may have fewer)
-    int stages;                // ring stages
     int bufs;                  // buffers of the cross-warp sums
     size_t smem;
     float* part;               // ks > 1: [ks][tokens][n or 2 n]

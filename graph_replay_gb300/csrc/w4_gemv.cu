@@ -4,28 +4,29 @@
 
 namespace gd {
 
-const void* w4_gemv_kernel_32(int parts, int nb, bool glu);
-const void* w4_gemv_kernel_64(int parts, int nb, bool glu);
-const void* w4_gemv_kernel_128(int parts, int nb, bool glu);
+const void* w4_gemv_kernel_32(int parts, int nb, int kind);
+const void* w4_gemv_kernel_64(int parts, int nb, int kind);
+const void* w4_gemv_kernel_128(int parts, int nb, int kind);
 
 namespace {
 
 constexpr size_t SMEM_MOST = 220 * 1024;       // dynamic shared memory of a CTA
 
+int kind_of(const W4Call& c) { return c.glu ? W4_GLU : c.nw > 1 ? W4_STACK : W4_ONE; }
 int blocks_of(const W4Gemv& g) { return g.block * g.c.parts() <= 8 ? 1 : 2; }
 
 const void* kernel_of(const W4Gemv& g) {
-    const int nb = blocks_of(g), P = g.c.parts();
+    const int nb = blocks_of(g), P = g.c.parts(), kind = kind_of(g.c);
     switch (g.c.group()) {
-        case 32: return w4_gemv_kernel_32(P, nb, g.c.glu);
-        case 64: return w4_gemv_kernel_64(P, nb, g.c.glu);
-        default: return w4_gemv_kernel_128(P, nb, g.c.glu);
+        case 32: return w4_gemv_kernel_32(P, nb, kind);
+        case 64: return w4_gemv_kernel_64(P, nb, kind);
+        default: return w4_gemv_kernel_128(P, nb, kind);
     }
 }
 
 size_t smem_of(const W4Gemv& g) {
     const int P = g.c.parts(), chunks = (g.c.k() + 127) / 128, most = (chunks + g.ks - 1) / g.ks;
-    const size_t ring = (size_t)WG_WARPS * g.stages * WG_STEP, x = (size_t)most * g.block * P * 256;
+    const size_t ring = (size_t)WG_WARPS * WG_STAGES * WG_STEP, x = (size_t)most * g.block * P * 256;
     const size_t f = ((size_t)most * g.block + 3) / 4 * 16;
     return ring + x + f + sizeof(float) * g.bufs * WG_WARPS * wg_tokens(P, blocks_of(g)) * WG_PITCH;
 }
@@ -38,7 +39,6 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     g->block = c.tokens < most ? c.tokens : most;
     // rows evenly over the SMs, at least 8 a CTA: a tile has 16, and a CTA of fewer saves nothing
     const int gr = c.glu ? 16 : 32;
-    g->stages = 4;
     for (g->ks = 1; g->ks <= chunks; ++g->ks) {
         const int places = num_sms / g->ks < 1 ? 1 : num_sms / g->ks;
         g->rows = (N + places - 1) / places;
@@ -48,7 +48,7 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
         const int own = (chunks + g->ks - 1) / g->ks;
         // warps along k: as many as have a chunk, but no more than leave each set of warps a row group
         g->wk = WG_WARPS;
-        while (g->wk > 1 && (own < g->wk || (groups >= 2 * (WG_WARPS / g->wk) && own < 4 * g->wk))) g->wk /= 2;
+        while (g->wk > 1 && (own < g->wk || (groups >= 2 * (WG_WARPS / g->wk) && own < 8 * g->wk))) g->wk /= 2;
         const int sets = WG_WARPS / g->wk, iters = (groups + sets - 1) / sets;
         g->bufs = iters > 1 ? 2 : 1;
         if (smem_of(*g) <= SMEM_MOST) break;
@@ -56,9 +56,10 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     if (g->ks > chunks || w4_gemv_counters(*g) > DEC_W4_COUNTER_BYTES / sizeof(unsigned)) return cudaErrorInvalidValue;
     g->smem = smem_of(*g);
     // the cap once for each kernel and device
-    static OncePerDevice once[3][2][2][2];
+    static OncePerDevice once[3][2][2][3];
     const void* fn = kernel_of(*g);
-    return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][P - 1][blocks_of(*g) - 1][c.glu].run([&] { return raise_smem_cap(fn); });
+    if (!fn) return cudaErrorInvalidValue;
+    return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][P - 1][blocks_of(*g) - 1][kind_of(c)].run([&] { return raise_smem_cap(fn); });
 }
 
 size_t w4_gemv_floats(const W4Gemv& g) { return g.ks > 1 ? (size_t)g.ks * g.c.tokens * g.c.n() * (g.c.glu ? 2 : 1) : 0; }
@@ -82,7 +83,6 @@ cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl) {
     a.wk = g.wk;
     a.ks = g.ks;
     a.rows = g.rows;
-    a.stages = g.stages;
     a.bufs = g.bufs;
     a.act = c.act;
     a.x_f32 = c.x_f32;

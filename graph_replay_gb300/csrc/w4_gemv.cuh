@@ -35,6 +35,10 @@ constexpr int WG_THREADS = WG_WARPS * 32;
 constexpr int WG_STEP = 2048;                  // bytes of a step: two tiles of 16 rows x 128 columns
 constexpr int WG_PITCH = 33;                   // of 32 rows' sums of one token
 constexpr int WG_MAX_TOKENS = 16;
+constexpr int WG_STAGES = 4;                   // steps of a warp's ring
+
+// one matrix; a gate and an up matrix; two or three stacked
+enum { W4_ONE = 0, W4_GLU = 1, W4_STACK = 2 };
 
 // tokens of a CTA whose columns fill NB blocks of 8
 __host__ __device__ constexpr int wg_tokens(int P, int NB) { return NB * 8 / P; }
@@ -43,7 +47,7 @@ struct W4GemvArgs {
     const uint8_t* codes[3];
     const __nv_bfloat16* scales[3];
     int end[3];                // rows of segments 0, 0 + 1, all
-    int N, K, tokens, block, wk, ks, rows, stages, bufs, act, x_f32, gain_f32, out_f32;
+    int N, K, tokens, block, wk, ks, rows, bufs, act, x_f32, gain_f32, out_f32;
     const void* x;
     const void* gain;
     const void* residual;
@@ -77,8 +81,10 @@ __device__ __forceinline__ void cp_wait(int left) {   // all but the newest `lef
 }
 
 // G: columns of a group; P: fp16 parts of an activation; NB: blocks of 8 B columns
-template <int G, int P, int NB, bool GLU>
+template <int G, int P, int NB, int KIND>
 __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant__ W4GemvArgs p) {
+    constexpr bool GLU = KIND == W4_GLU;
+    constexpr int S = WG_STAGES;
     constexpr int NG = 128 / G;                // groups of a step
     constexpr int MT = wg_tokens(P, NB);       // tokens that fit
     constexpr int AC = P == 2 ? 2 : 4;         // sums of a lane, tile and column block
@@ -101,7 +107,6 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const int ngroups = (row1 - row0 + GR - 1) / GR;            // row groups of the CTA
     const int iters = (ngroups + sets - 1) / sets;              // of each set
     const int mine = (ch1 - ch0 - slice + p.wk - 1) / p.wk;     // this warp's chunks of a row group (>= 0)
-    const int S = p.stages;
 
     unsigned char* ring = smem + (size_t)warp * S * WG_STEP;
     unsigned char* xs = smem + (size_t)WG_WARPS * S * WG_STEP;               // [chunk][4][cols][64 bytes]
@@ -123,45 +128,65 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     // where this lane's 16 bytes of row g or g + 8 of a tile go, and where its words are
     const int swz = G == 128 ? 0 : G == 64 ? ((g >> 1) & 1) << 1 : (g >> 1) & 3;
     const uint32_t put = (uint32_t)(g * 64 + ((t ^ swz) << 4));
-    struct Rows {
+    const size_t cpitch = (size_t)(p.K >> 1), spitch = (size_t)(p.K / G);
+    struct Rows {                              // of a row group: rows g, g + 8 of tile 0, then of tile 1
         const uint8_t* c[4];
         const __nv_bfloat16* s[4];
-        bool on[4];
+        unsigned on;                           // bit i: row i is one of the CTA's
     };
-    const size_t cpitch = (size_t)(p.K >> 1), spitch = (size_t)(p.K / G);
     auto rows_of = [&](int it, Rows& r) {
-        const int base = row0 + (it * sets + set) * GR;
+        const int base = row0 + (it * sets + set) * GR + g;
+        r.on = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {          // tile i >> 1, row g or g + 8
-            const int n = base + (GLU ? 0 : 16 * (i >> 1)) + 8 * (i & 1) + g;
-            r.on[i] = n < row1;
-            int sg = GLU ? i >> 1 : 0, local = min(n, row1 - 1);
-            if (!GLU) {
-                if (local >= p.end[1]) { sg = 2; local -= p.end[1]; }
-                else if (local >= p.end[0]) { sg = 1; local -= p.end[0]; }
+        for (int i = 0; i < 4; ++i) r.on |= (base + (GLU ? 0 : 16 * (i >> 1)) + 8 * (i & 1) < row1 ? 1u : 0u) << i;
+        if (KIND == W4_STACK) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                int n = min(base + 8 * i, row1 - 1);
+                const bool z = n >= p.end[1], y = n >= p.end[0];
+                const uint8_t* cb = z ? p.codes[2] : y ? p.codes[1] : p.codes[0];
+                const __nv_bfloat16* sb = z ? p.scales[2] : y ? p.scales[1] : p.scales[0];
+                n -= z ? p.end[1] : y ? p.end[0] : 0;
+                r.c[i] = cb + (size_t)n * cpitch;
+                r.s[i] = sb + (size_t)n * spitch;
             }
-            const uint8_t* cb = sg == 0 ? p.codes[0] : sg == 1 ? p.codes[1] : p.codes[2];
-            const __nv_bfloat16* sb = sg == 0 ? p.scales[0] : sg == 1 ? p.scales[1] : p.scales[2];
-            r.c[i] = cb + (size_t)local * cpitch;
-            r.s[i] = sb + (size_t)local * spitch;
+        } else {
+            // rows behind the CTA's last are never read, so their addresses may lie anywhere
+#pragma unroll
+            for (int i = 0; i < (GLU ? 2 : 1); ++i) {
+                r.c[2 * i] = p.codes[i] + (size_t)base * cpitch;
+                r.s[2 * i] = p.scales[i] + (size_t)base * spitch;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (GLU ? !(i & 1) : i == 0) continue;
+                r.c[i] = r.c[i - 1] + 8 * cpitch;
+                r.s[i] = r.s[i - 1] + 8 * spitch;
+            }
         }
     };
     const int steps = mine > 0 ? iters * mine : 0;
+    const unsigned hop = (unsigned)p.wk * 64;  // bytes of a row from one of the warp's chunks to its next
+    const unsigned a_first = (unsigned)(ch0 + slice) * 64 + 16 * t;
     Rows ahead;                                // of the step that is copied next
-    int a_it = 0, a_i = 0, a_step = 0;
+    int a_it = 0, a_i = 0, a_left = steps;
+    unsigned a_at = a_first, a_slot = 0;       // byte of a row; slot of the ring, in bytes
     if (steps > 0) rows_of(0, ahead);
     auto copy_next = [&]() {
-        if (a_step < steps) {
-            const int k0 = (ch0 + slice + a_i * p.wk) * 128;
-            const bool in = k0 + 32 * t < p.K;
-            const uint32_t dst = ring_at + (uint32_t)((a_step % S) * WG_STEP) + put;
+        if (a_left > 0) {
+            const bool in = a_at < (unsigned)cpitch;
+            const uint32_t dst = ring_at + a_slot + put;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                cp_async16(dst + (uint32_t)((i >> 1) * 1024 + (i & 1) * 512), in ? ahead.c[i] + (k0 >> 1) + 16 * t : ahead.c[i],
-                           in && ahead.on[i]);
-            ++a_step;
+            for (int i = 0; i < 4; ++i) {
+                const bool live = in && (ahead.on >> i & 1u);
+                cp_async16(dst + (uint32_t)((i >> 1) * 1024 + (i & 1) * 512), live ? ahead.c[i] + a_at : p.codes[0], live);
+            }
+            --a_left;
+            a_slot = (a_slot + WG_STEP) & (S * WG_STEP - 1);
+            a_at += hop;
             if (++a_i == mine) {
                 a_i = 0;
+                a_at = a_first;
                 if (++a_it < iters) rows_of(a_it, ahead);
             }
         }
@@ -284,21 +309,21 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     // NG); raw bits
     Rows cur, next;
     uint32_t sc[2] = {0u, 0u};
-    auto scales_of = [&](const Rows& r, int i, uint32_t (&o)[2]) {
-        const int gr = (ch0 + slice + i * p.wk) * NG + (NG > 1 ? t % NG : 0);
+    const int g_first = (ch0 + slice) * NG + (NG > 1 ? t % NG : 0), g_hop = p.wk * NG;
+    auto scales_of = [&](const Rows& r, int gr, uint32_t (&o)[2]) {
         const bool in = gr < (int)spitch;
 #pragma unroll
         for (int tile = 0; tile < 2; ++tile) {
-            const uint32_t a = in ? __ldg(reinterpret_cast<const unsigned short*>(r.s[2 * tile]) + gr) : 0u;
-            const uint32_t b = in ? __ldg(reinterpret_cast<const unsigned short*>(r.s[2 * tile + 1]) + gr) : 0u;
+            const uint32_t a = in && (r.on >> (2 * tile) & 1u) ? __ldg(reinterpret_cast<const unsigned short*>(r.s[2 * tile]) + gr) : 0u;
+            const uint32_t b = in && (r.on >> (2 * tile + 1) & 1u) ? __ldg(reinterpret_cast<const unsigned short*>(r.s[2 * tile + 1]) + gr) : 0u;
             o[tile] = a | (b << 16);
         }
     };
     if (steps > 0) {
         rows_of(0, cur);
-        scales_of(cur, 0, sc);
+        scales_of(cur, g_first, sc);
     }
-    int step = 0;
+    unsigned slot = 0;                         // of this step, in bytes
     for (int it = 0; it < iters; ++it) {
         float acc[2][NB][AC];
 #pragma unroll
@@ -308,18 +333,19 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < AC; ++c) acc[a][b][c] = 0.f;
         const int base = row0 + (it * sets + set) * GR;
-        for (int i = 0; i < mine; ++i, ++step) {
+        for (int i = 0; i < mine; ++i) {
             uint32_t sn[2] = {0u, 0u};
             if (i + 1 < mine) {
-                scales_of(cur, i + 1, sn);
+                scales_of(cur, g_first + (i + 1) * g_hop, sn);
             } else if (it + 1 < iters) {
                 rows_of(it + 1, next);
-                scales_of(next, 0, sn);
+                scales_of(next, g_first, sn);
             }
             cp_wait(S - 2);
             __syncwarp();
             copy_next();                       // into the slot that the step before read
-            const unsigned char* st = ring + (size_t)(step % S) * WG_STEP;
+            const unsigned char* st = ring + slot;
+            slot = (slot + WG_STEP) & (S * WG_STEP - 1);
             const int ci = slice + i * p.wk;
             uint4 bf[NB][4];                   // [q]: the B words of MMA 2q and 2q + 1
 #pragma unroll
@@ -473,14 +499,18 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     }
 }
 
+// stacked matrices come from a decode step, whose activations are fp32
+template <int G, int P, int NB>
+const void* w4_gemv_pick(int kind) {
+    if (kind == W4_ONE) return (const void*)&k_w4_gemv<G, P, NB, W4_ONE>;
+    if (kind == W4_GLU) return (const void*)&k_w4_gemv<G, P, NB, W4_GLU>;
+    if constexpr (P == 2) return (const void*)&k_w4_gemv<G, P, NB, W4_STACK>;
+    else return nullptr;
+}
 template <int G>
-const void* w4_gemv_kernel(int parts, int nb, bool glu) {
-    if (parts == 1) {
-        if (nb == 1) return glu ? (const void*)&k_w4_gemv<G, 1, 1, true> : (const void*)&k_w4_gemv<G, 1, 1, false>;
-        return glu ? (const void*)&k_w4_gemv<G, 1, 2, true> : (const void*)&k_w4_gemv<G, 1, 2, false>;
-    }
-    if (nb == 1) return glu ? (const void*)&k_w4_gemv<G, 2, 1, true> : (const void*)&k_w4_gemv<G, 2, 1, false>;
-    return glu ? (const void*)&k_w4_gemv<G, 2, 2, true> : (const void*)&k_w4_gemv<G, 2, 2, false>;
+const void* w4_gemv_kernel(int parts, int nb, int kind) {
+    if (parts == 1) return nb == 1 ? w4_gemv_pick<G, 1, 1>(kind) : w4_gemv_pick<G, 1, 2>(kind);
+    return nb == 1 ? w4_gemv_pick<G, 2, 1>(kind) : w4_gemv_pick<G, 2, 2>(kind);
 }
 
 }  // namespace gd

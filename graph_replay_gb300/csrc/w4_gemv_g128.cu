@@ -2,5 +2,5 @@
 #include "w4_gemv.cuh"
 
 namespace gd {
-const void* w4_gemv_kernel_128(int parts, int nb, bool glu) { return w4_gemv_kernel<128>(parts, nb, glu); }
+const void* w4_gemv_kernel_128(int parts, int nb, int kind) { return w4_gemv_kernel<128>(parts, nb, kind); }
 }  // namespace gd

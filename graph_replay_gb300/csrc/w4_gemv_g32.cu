@@ -2,5 +2,5 @@
 #include "w4_gemv.cuh"
 
 namespace gd {
-const void* w4_gemv_kernel_32(int parts, int nb, bool glu) { return w4_gemv_kernel<32>(parts, nb, glu); }
+const void* w4_gemv_kernel_32(int parts, int nb, int kind) { return w4_gemv_kernel<32>(parts, nb, kind); }
 }  // namespace gd

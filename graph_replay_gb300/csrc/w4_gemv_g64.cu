@@ -2,5 +2,5 @@
 #include "w4_gemv.cuh"
 
 namespace gd {
-const void* w4_gemv_kernel_64(int parts, int nb, bool glu) { return w4_gemv_kernel<64>(parts, nb, glu); }
+const void* w4_gemv_kernel_64(int parts, int nb, int kind) { return w4_gemv_kernel<64>(parts, nb, kind); }
 }  // namespace gd
