@@ -151,17 +151,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 r.s[i] = sb + (size_t)n * spitch;
             }
         } else {
-            // rows behind the CTA's last are never read, so their addresses may lie anywhere
-#pragma unroll
-            for (int i = 0; i < (GLU ? 2 : 1); ++i) {
-                r.c[2 * i] = p.codes[i] + (size_t)base * cpitch;
-                r.s[2 * i] = p.scales[i] + (size_t)base * spitch;
-            }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (GLU ? !(i & 1) : i == 0) continue;
-                r.c[i] = r.c[i - 1] + 8 * cpitch;
-                r.s[i] = r.s[i - 1] + 8 * spitch;
+                const int n = min(base + (GLU ? 8 * (i & 1) : 8 * i), row1 - 1);   // scales are read of any row
+                r.c[i] = p.codes[GLU ? i >> 1 : 0] + (size_t)n * cpitch;
+                r.s[i] = p.scales[GLU ? i >> 1 : 0] + (size_t)n * spitch;
             }
         }
     };
@@ -178,8 +172,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             const uint32_t dst = ring_at + a_slot + put;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const bool live = in && (ahead.on >> i & 1u);
-                cp_async16(dst + (uint32_t)((i >> 1) * 1024 + (i & 1) * 512), live ? ahead.c[i] + a_at : p.codes[0], live);
+                // (of rows behind the CTA's last and columns behind the row's nothing is read: zeros)
+                cp_async16(dst + (uint32_t)((i >> 1) * 1024 + (i & 1) * 512), ahead.c[i] + a_at, in && (ahead.on >> i & 1u));
             }
             --a_left;
             a_slot = (a_slot + WG_STEP) & (S * WG_STEP - 1);
@@ -310,20 +304,21 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     Rows cur, next;
     uint32_t sc[2] = {0u, 0u};
     const int g_first = (ch0 + slice) * NG + (NG > 1 ? t % NG : 0), g_hop = p.wk * NG;
-    auto scales_of = [&](const Rows& r, int gr, uint32_t (&o)[2]) {
+    auto scales_of = [&](const Rows& r, int gr, uint32_t (&o)[2]) {   // no branches: the loop has few instructions to spare
         const bool in = gr < (int)spitch;
+        const int at = in ? gr : (int)spitch - 1;
+        uint32_t v[4];
 #pragma unroll
-        for (int tile = 0; tile < 2; ++tile) {
-            const uint32_t a = in && (r.on >> (2 * tile) & 1u) ? __ldg(reinterpret_cast<const unsigned short*>(r.s[2 * tile]) + gr) : 0u;
-            const uint32_t b = in && (r.on >> (2 * tile + 1) & 1u) ? __ldg(reinterpret_cast<const unsigned short*>(r.s[2 * tile + 1]) + gr) : 0u;
-            o[tile] = a | (b << 16);
-        }
+        for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const unsigned short*>(r.s[i]) + at);
+        o[0] = in ? v[0] | (v[1] << 16) : 0u;
+        o[1] = in ? v[2] | (v[3] << 16) : 0u;
     };
     if (steps > 0) {
         rows_of(0, cur);
         scales_of(cur, g_first, sc);
     }
     unsigned slot = 0;                         // of this step, in bytes
+    const unsigned b_hop = (unsigned)p.wk * 4 * cols * 64, f_hop = (unsigned)(p.wk * p.block);
     for (int it = 0; it < iters; ++it) {
         float acc[2][NB][AC];
 #pragma unroll
@@ -333,6 +328,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < AC; ++c) acc[a][b][c] = 0.f;
         const int base = row0 + (it * sets + set) * GR;
+        unsigned b_at[NB], f_at[NB][P == 2 ? 1 : 2];   // of the step's chunk
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            b_at[b] = (unsigned)slice * 4 * cols * 64 + (unsigned)min(b * 8 + g, cols - 1) * 64 + t * 16;
+#pragma unroll
+            for (int c = 0; c < (P == 2 ? 1 : 2); ++c)
+                f_at[b][c] = (unsigned)(slice * p.block + min(P == 2 ? b * 4 + t : b * 8 + 2 * t + c, p.block - 1));
+        }
         for (int i = 0; i < mine; ++i) {
             uint32_t sn[2] = {0u, 0u};
             if (i + 1 < mine) {
@@ -346,22 +349,20 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             copy_next();                       // into the slot that the step before read
             const unsigned char* st = ring + slot;
             slot = (slot + WG_STEP) & (S * WG_STEP - 1);
-            const int ci = slice + i * p.wk;
+            // columns of B and tokens that there are not repeat others: what they give is not used
             uint4 bf[NB][4];                   // [q]: the B words of MMA 2q and 2q + 1
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-                    bf[b][c] = b * 8 + g < cols ? *reinterpret_cast<const uint4*>(xs + ((size_t)(ci * 4 + c) * cols + b * 8 + g) * 64 + t * 16)
-                                                : make_uint4(0u, 0u, 0u, 0u);
             float f[NB][P == 2 ? 1 : 2];       // 2^(e - 14) of the tokens of this lane's sums
 #pragma unroll
-            for (int b = 0; b < NB; ++b)
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) bf[b][c] = *reinterpret_cast<const uint4*>(xs + b_at[b] + (unsigned)c * cols * 64);
+                b_at[b] += b_hop;
 #pragma unroll
                 for (int c = 0; c < (P == 2 ? 1 : 2); ++c) {
-                    const int r = P == 2 ? b * 4 + t : b * 8 + 2 * t + c;
-                    f[b][c] = r < m ? fs[ci * p.block + r] : 0.f;
+                    f[b][c] = fs[f_at[b][c]];
+                    f_at[b][c] += f_hop;
                 }
+            }
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
                 if (!GLU && tile == 1 && base + 16 >= row1) break;   // the same for the whole warp
