@@ -31,13 +31,30 @@ __device__ __forceinline__ uint32_t w4_hmul(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// (a & mask) ^ c in one instruction
+template <uint32_t MASK>
+__device__ __forceinline__ uint32_t w4_and_xor(uint32_t a, uint32_t c) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(a), "n"(MASK), "r"(c));
+    return r;
+}
+// constants that stay in registers: as immediates they would cost an instruction more at each use
+struct W4Const {
+    uint32_t low, high, part, less;            // 1032, the pattern of the next position, 1 / 16, -72, in both halves
+    __device__ __forceinline__ W4Const() {
+        asm volatile("mov.b32 %0, 0x64086408;" : "=r"(low));
+        asm volatile("mov.b32 %0, 0x64806480;" : "=r"(high));
+        asm volatile("mov.b32 %0, 0x2c002c00;" : "=r"(part));
+        asm volatile("mov.b32 %0, 0xd480d480;" : "=r"(less));
+    }
+};
 // the columns (j, j + 4), j = 0 .. 3, of a word as fp16 pairs
-__device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t (&pair)[4]) {
+__device__ __forceinline__ void w4_unpack(uint32_t w, const W4Const& k, uint32_t (&pair)[4]) {
     const uint32_t v = w >> 8;
-    pair[0] = w4_hsub((w & 0x000f000fu) ^ 0x64086408u, 0x64086408u);                 // - 1032
-    pair[1] = w4_hfma((w & 0x00f000f0u) ^ 0x64806480u, 0x2c002c00u, 0xd480d480u);    // / 16 - 72
-    pair[2] = w4_hsub((v & 0x000f000fu) ^ 0x64086408u, 0x64086408u);
-    pair[3] = w4_hfma((v & 0x00f000f0u) ^ 0x64806480u, 0x2c002c00u, 0xd480d480u);
+    pair[0] = w4_hsub(w4_and_xor<0x000f000fu>(w, k.low), k.low);                // - 1032
+    pair[1] = w4_hfma(w4_and_xor<0x00f000f0u>(w, k.high), k.part, k.less);      // / 16 - 72
+    pair[2] = w4_hsub(w4_and_xor<0x000f000fu>(v, k.low), k.low);
+    pair[3] = w4_hfma(w4_and_xor<0x00f000f0u>(v, k.high), k.part, k.less);
 }
 
 // two fp32 values to an fp16 pair, the first in the low half

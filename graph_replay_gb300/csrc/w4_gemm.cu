@@ -136,11 +136,11 @@ __device__ __forceinline__ uint32_t scale_pair(uint32_t bits, float up) {
 // The columns (j, j + 4) of a word times a scale s, f = (s, s) and f24 = (-24 s, -24 s), exact.  Two pairs as in w4_unpack,
 // then times s; the other two with the code moved to the top of the mantissa of 16, where (16 + (q + 8)) s - 24 s is one
 // fused step (24 s has 10 significant bits): so the half-precision and the integer pipe get as much each
-__device__ __forceinline__ void unpack_scaled(uint32_t w, uint32_t f, uint32_t f24, uint32_t* o) {
-    o[0] = w4_hmul(w4_hsub((w & 0x000f000fu) ^ 0x64086408u, 0x64086408u), f);
-    o[1] = w4_hmul(w4_hfma((w & 0x00f000f0u) ^ 0x64806480u, 0x2c002c00u, 0xd480d480u), f);
-    o[2] = w4_hfma(((w >> 2) & 0x03c003c0u) ^ 0x4e004e00u, f, f24);   // 0x4c00 is 16; 0x200 turns the code's sign bit over
-    o[3] = w4_hfma(((w >> 6) & 0x03c003c0u) ^ 0x4e004e00u, f, f24);
+__device__ __forceinline__ void unpack_scaled(uint32_t w, const W4Const& k, uint32_t sixteen, uint32_t f, uint32_t f24, uint32_t* o) {
+    o[0] = w4_hmul(w4_hsub(w4_and_xor<0x000f000fu>(w, k.low), k.low), f);
+    o[1] = w4_hmul(w4_hfma(w4_and_xor<0x00f000f0u>(w, k.high), k.part, k.less), f);
+    o[2] = w4_hfma(w4_and_xor<0x03c003c0u>(w >> 2, sixteen), f, f24);
+    o[3] = w4_hfma(w4_and_xor<0x03c003c0u>(w >> 6, sixteen), f, f24);
 }
 __device__ __forceinline__ uint32_t pick16(const uint4& w, int i) {   // element i (0 .. 7) of eight
     const uint32_t lo = i & 2 ? w.y : w.x, hi = i & 2 ? w.w : w.z, v = i & 4 ? hi : lo;
@@ -365,6 +365,9 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             ++folded;
             return true;
         };
+        const W4Const kc;
+        uint32_t sixteen;                      // 16 in both halves, the code's sign bit turned over
+        asm volatile("mov.b32 %0, 0x4e004e00;" : "=r"(sixteen));
         const int swz = (r >> 1) & 3;
         const unsigned char* row = codes_s + mat * (WM_CODES / 2) + r * 64;
         const int c0 = ((2 * h) ^ swz) << 4, c1 = ((2 * h + 1) ^ swz) << 4;
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < NS; ++c) f24[c] = w4_hmul(sc[c], 0xce00ce00u);   // -24
 #pragma unroll
-                for (int c = 0; c < 8; ++c) unpack_scaled(w[c], sc[NS == 2 ? c >> 2 : 0], f24[NS == 2 ? c >> 2 : 0], a + c * 4);
+                for (int c = 0; c < 8; ++c) unpack_scaled(w[c], kc, sixteen, sc[NS == 2 ? c >> 2 : 0], f24[NS == 2 ? c >> 2 : 0], a + c * 4);
             }
             if (s >= p.sa) ok = mbar_wait(&a_empty[ra.slot], ra.odd ^ 1u) && ok;
             if (!__all_sync(0xffffffffu, ok)) break;

@@ -317,6 +317,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         rows_of(0, cur);
         scales_of(cur, g_first, sc);
     }
+    const W4Const kc;
     unsigned slot = 0;                         // of this step, in bytes
     const unsigned b_hop = (unsigned)p.wk * 4 * cols * 64, f_hop = (unsigned)(p.wk * p.block);
     for (int it = 0; it < iters; ++it) {
@@ -396,8 +397,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
                     for (int c = gi * (4 / NG); c < (gi + 1) * (4 / NG); ++c) {
                         uint32_t pa[4], pb[4];
-                        w4_unpack(wa[c], pa);
-                        w4_unpack(wb[c], pb);
+                        w4_unpack(wa[c], kc, pa);
+                        w4_unpack(wb[c], kc, pb);
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
                             mma_f16(d[b], pa[0], pb[0], pa[1], pb[1], bf[b][c].x, bf[b][c].y);
