@@ -62,12 +62,38 @@ struct W4GemvArgs {
     int trace_id;
 };
 
+// d = a b + (c0, c1, c0, c1): the sum's start depends on the column only
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
+                                          float c0, float c1) {
+    asm(   // not volatile: chains of different groups and tiles may be mixed
+       
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The pairs (j, j + 4) of a word as fp16 subnormals: with its sign bit turned over a code is u = q + 8, 0 .. 15, and bits
+// 0-3 of a half stand for u 2^-24, bits 4-7 for u 2^-20.  Nothing has to be converted; the sums start at -8 times the
+// activations' sum, and the activations of the second and fourth pair are 2^-4 of the others
+struct W4Sign {
+    uint32_t low, high;        // in registers: as immediates they would cost an instruction more at each use
+    __device__ __forceinline__ W4Sign() {
+        asm volatile("mov.b32 %0, 0x00080008;" : "=r"(low));
+        asm volatile("mov.b32 %0, 0x00800080;" : "=r"(high));
+    }
+};
+__device__ __forceinline__ void w4_raw(uint32_t w, const W4Sign& k, uint32_t (&pair)[4]) {
+    const uint32_t v = w >> 8;
+    pair[0] = w4_and_xor<0x000f000fu>(w, k.low);
+    pair[1] = w4_and_xor<0x00f000f0u>(w, k.high);
+    pair[2] = w4_and_xor<0x000f000fu>(v, k.low);
+    pair[3] = w4_and_xor<0x00f000f0u>(v, k.high);
 }
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -110,8 +136,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 
     unsigned char* ring = smem + (size_t)warp * S * WG_STEP;
     unsigned char* xs = smem + (size_t)WG_WARPS * S * WG_STEP;               // [chunk][4][cols][64 bytes]
-    float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14)
-    float* red = fs + (((ch1 - ch0) * p.block + 3) & ~3);                    // [bufs][warp][MT][WG_PITCH]
+    float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14 + 12)
+    float* cs = fs + (((ch1 - ch0) * p.block + 3) & ~3);                     // [chunk][NG][cols]: where a group's sums start
+    float* red = cs + (ch1 - ch0) * NG * cols;                               // [bufs][warp][MT][WG_PITCH]
     const uint32_t ring_at = smem_u32(ring);
 
     unsigned long long* tr = nullptr;
@@ -198,63 +225,71 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         const int w = lane >> 1;               // word of the chunk that the lane's four columns lie in
         const int bt = G == 128 ? w >> 2 : G == 64 ? (w >> 1) & 3 : w & 3;
         const int bq = G == 128 ? w & 3 : G == 64 ? ((w >> 3) << 1) | (w & 1) : w >> 2;
+        const bool odd = lane & 1;
         float ss = 0.f;
-        constexpr int AHEAD = 8;
+        // four values of a token's chunk at a time, three more under way
         int r = 0, j = 0;                      // token and chunk of the next value to load
-        int cr = 0, cj = 0;                    // ... to convert
-        for (int b = 0; b < total; b += AHEAD) {
-            float4 v[AHEAD], gv[AHEAD];
-#pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                v[u] = gv[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (b + u < total) {
-                    const int k = (ch0 + warp + j * WG_WARPS) * 128 + 4 * lane;
-                    if (k < p.K) {
-                        v[u] = w4_load4(p.x, p.x_f32, (size_t)(tok0 + r) * p.x_stride + k);
-                        if (p.gain) gv[u] = w4_load4(p.gain, p.gain_f32, k);
-                    }
-                    if (++j == nc) { j = 0; ++r; }
-                }
+        auto load = [&](float4& v, float4& gv) {
+            const int k = (ch0 + warp + j * WG_WARPS) * 128 + 4 * lane;
+            v = gv = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (r < m && k < p.K) {
+                v = w4_load4(p.x, p.x_f32, (size_t)(tok0 + r) * p.x_stride + k);
+                if (p.gain) gv = w4_load4(p.gain, p.gain_f32, k);
             }
+            if (++j >= nc) { j = 0; ++r; }
+        };
+        float4 v0, v1, v2, v3, g0, g1, g2, g3;
+        if (total > 0) {
+            load(v0, g0);
+            load(v1, g1);
+            load(v2, g2);
+            load(v3, g3);
+        }
+        int cr = 0, cj = 0;                    // token and chunk at hand
+#pragma unroll 1
+        for (int b = 0; b < total; ++b) {
+            float4 x = v0;
+            if (p.gain) {
+                ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, ss))));
+                x.x *= g0.x; x.y *= g0.y; x.z *= g0.z; x.w *= g0.w;
+            }
+            v0 = v1; v1 = v2; v2 = v3;
+            g0 = g1; g1 = g2; g2 = g3;
+            load(v3, g3);
+            const uint32_t top = __reduce_max_sync(
+                0xffffffffu, max(max(w4_finite_bits(x.x), w4_finite_bits(x.y)), max(w4_finite_bits(x.z), w4_finite_bits(x.w))));
+            const int e = w4_exponent(top);
+            const float up = w4_up(e), up4 = up * 0.0625f;
+            x.x *= up; x.y *= up4; x.z *= up; x.w *= up4;      // columns j of a word meet codes times 2^-24, 2^-20, ...
+            const int ci = warp + cj * WG_WARPS;
 #pragma unroll
-            for (int u = 0; u < AHEAD; ++u) {
-                if (b + u >= total) break;
-                float4 x = v[u];
+            for (int part = 0; part < P; ++part) {
+                const uint32_t a01 = w4_pack_half(x.x, x.y), a23 = w4_pack_half(x.z, x.w);
+                const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&a01));
+                const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&a23));
+                float sum = (f01.x + f23.x) + 16.0f * (f01.y + f23.y);
+#pragma unroll
+                for (int o = 1; o < G / 4; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const int col = cr * P + part;
+                if (lane % (G / 4) == 0) cs[(ci * NG + lane / (G / 4)) * cols + col] = sum * -4.76837158203125e-07f;   // -8 2^-24
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a01 : a23, 1);
+                const uint32_t lo = odd ? got : a01, hi = odd ? a23 : got;     // columns j and j + 4 of the word
+                const uint2 f = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+                *reinterpret_cast<uint2*>(xs + ((size_t)(ci * 4 + bq) * cols + col) * 64 + bt * 16 + (odd ? 8 : 0)) = f;
+                // what the part leaves (nothing where it is not finite)
+                x.x -= f01.x; x.y -= f01.y; x.z -= f23.x; x.w -= f23.y;
+                x.x = isfinite(x.x) ? x.x : 0.f; x.y = isfinite(x.y) ? x.y : 0.f;
+                x.z = isfinite(x.z) ? x.z : 0.f; x.w = isfinite(x.w) ? x.w : 0.f;
+            }
+            if (lane == 0) fs[ci * p.block + cr] = w4_down(e) * 4096.0f;   // half of the codes' 2^-24; the rest with the norm
+            if (++cj == nc) {
                 if (p.gain) {
-                    ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, ss))));
-                    x.x *= gv[u].x; x.y *= gv[u].y; x.z *= gv[u].z; x.w *= gv[u].w;
+                    ss = warp_sum(ss);
+                    if (lane == 0) ss_s[warp][cr] = ss;
+                    ss = 0.f;
                 }
-                const uint32_t top = __reduce_max_sync(
-                    0xffffffffu, max(max(w4_finite_bits(x.x), w4_finite_bits(x.y)), max(w4_finite_bits(x.z), w4_finite_bits(x.w))));
-                const int e = w4_exponent(top);
-                const float up = w4_up(e);
-                x.x *= up; x.y *= up; x.z *= up; x.w *= up;
-                const int ci = warp + cj * WG_WARPS;
-                uint32_t h01 = w4_pack_half(x.x, x.y), h23 = w4_pack_half(x.z, x.w);
-                uint32_t l01 = 0, l23 = 0;
-                if (P == 2) {
-                    l01 = w4_rest(x.x, x.y, h01);
-                    l23 = w4_rest(x.z, x.w, h23);
-                }
-                const bool odd = lane & 1;
-#pragma unroll
-                for (int part = 0; part < P; ++part) {
-                    const uint32_t a01 = part ? l01 : h01, a23 = part ? l23 : h23;
-                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a01 : a23, 1);
-                    const uint32_t lo = odd ? got : a01, hi = odd ? a23 : got;     // columns j and j + 4 of the word
-                    const uint2 f = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
-                    *reinterpret_cast<uint2*>(xs + ((size_t)(ci * 4 + bq) * cols + cr * P + part) * 64 + bt * 16 + (odd ? 8 : 0)) = f;
-                }
-                if (lane == 0) fs[ci * p.block + cr] = w4_down(e);
-                if (++cj == nc) {
-                    if (p.gain) {
-                        ss = warp_sum(ss);
-                        if (lane == 0) ss_s[warp][cr] = ss;
-                        ss = 0.f;
-                    }
-                    cj = 0;
-                    ++cr;
-                }
+                cj = 0;
+                ++cr;
             }
         }
         if (p.gain && nc <= 0 && lane < m) ss_s[warp][lane] = 0.f;
@@ -280,22 +315,31 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         float s = 0.f;
         if (p.gain)
             for (int w = 0; w < WG_WARPS; ++w) s += ss_s[w][tid];
-        inv_s[tid] = p.gain ? 1.0f / sqrtf(s / (float)p.K + p.eps) : 1.0f;   // read behind the next barrier
+        inv_s[tid] = 4096.0f * (p.gain ? 1.0f / sqrtf(s / (float)p.K + p.eps) : 1.0f);   // read behind the next barrier
     }
 
-    // one output: gate / value v and up u, unscaled by the norm
-    auto finish = [&](int r, int n, float v, float u) {
+    // one output: gate / value v and up u, unscaled by the norm; its residual
+    auto finish = [&](int r, int n, float v, float u, float res) {
         v *= inv_s[r];
-        if (GLU) {
-            v = w4_glu(p.act, v, u * inv_s[r]);
-        } else if (p.residual) {
-            v += w4_load1(p.residual, p.out_f32, (size_t)(tok0 + r) * p.residual_stride + n);
-        }
+        v = GLU ? w4_glu(p.act, v, u * inv_s[r]) : v + res;
         w4_store1(p.out, p.out_f32, (size_t)(tok0 + r) * p.out_stride + n, v);
         if (!GLU && p.amax) {
             atomicMax(&best_s[r], argmax_key(v, n));
             if (!isfinite(v)) nonfinite_s[r] = 1u;
         }
+    };
+    auto residual_of = [&](int r, int n) -> float {
+        return !GLU && p.residual ? w4_load1(p.residual, p.out_f32, (size_t)(tok0 + r) * p.residual_stride + n) : 0.f;
+    };
+    // The joining of a row group's sums: four threads an output, item = ((set, token), row).  Each takes a part of the warps
+    constexpr int RG = GLU ? 16 : 32;          // rows of an item's row group
+    const int items = sets * m * RG;
+    auto item_of = [&](int it, int i, int& r, int& st2, int& row) -> int {   // the output row, or -1
+        row = i % RG;
+        st2 = i / RG / m;
+        r = i / RG - st2 * m;
+        const int n = row0 + (it * sets + st2) * GR + row;
+        return i < items && n < row1 ? n : -1;
     };
 
     // ---- the products ----
@@ -317,10 +361,18 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         rows_of(0, cur);
         scales_of(cur, g_first, sc);
     }
-    const W4Const kc;
+    const W4Sign kc;
     unsigned slot = 0;                         // of this step, in bytes
-    const unsigned b_hop = (unsigned)p.wk * 4 * cols * 64, f_hop = (unsigned)(p.wk * p.block);
+    const unsigned b_hop = (unsigned)p.wk * 4 * cols * 64, f_hop = (unsigned)(p.wk * p.block),
+                   c_hop = (unsigned)(p.wk * NG * cols);
     for (int it = 0; it < iters; ++it) {
+        // the residual of the thread's first output, under the products
+        float res = 0.f;
+        if (!GLU && p.residual && p.ks == 1) {
+            int r, st2, row;
+            const int n = item_of(it, tid >> 2, r, st2, row);
+            if (n >= 0) res = residual_of(r, n);
+        }
         float acc[2][NB][AC];
 #pragma unroll
         for (int a = 0; a < 2; ++a)
@@ -329,13 +381,15 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < AC; ++c) acc[a][b][c] = 0.f;
         const int base = row0 + (it * sets + set) * GR;
-        unsigned b_at[NB], f_at[NB][P == 2 ? 1 : 2];   // of the step's chunk
+        unsigned b_at[NB], f_at[NB][P == 2 ? 1 : 2], c_at[NB][2];   // of the step's chunk
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             b_at[b] = (unsigned)slice * 4 * cols * 64 + (unsigned)min(b * 8 + g, cols - 1) * 64 + t * 16;
 #pragma unroll
             for (int c = 0; c < (P == 2 ? 1 : 2); ++c)
                 f_at[b][c] = (unsigned)(slice * p.block + min(P == 2 ? b * 4 + t : b * 8 + 2 * t + c, p.block - 1));
+#pragma unroll
+            for (int c = 0; c < 2; ++c) c_at[b][c] = (unsigned)(slice * NG * cols + min(b * 8 + 2 * t + c, cols - 1));
         }
         for (int i = 0; i < mine; ++i) {
             uint32_t sn[2] = {0u, 0u};
@@ -352,7 +406,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             slot = (slot + WG_STEP) & (S * WG_STEP - 1);
             // columns of B and tokens that there are not repeat others: what they give is not used
             uint4 bf[NB][4];                   // [q]: the B words of MMA 2q and 2q + 1
-            float f[NB][P == 2 ? 1 : 2];       // 2^(e - 14) of the tokens of this lane's sums
+            float f[NB][P == 2 ? 1 : 2];       // the scales of the tokens of this lane's sums
+            float start[NB][NG][2];            // of its two columns
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
 #pragma unroll
@@ -362,6 +417,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 for (int c = 0; c < (P == 2 ? 1 : 2); ++c) {
                     f[b][c] = fs[f_at[b][c]];
                     f_at[b][c] += f_hop;
+                }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+#pragma unroll
+                    for (int gi = 0; gi < NG; ++gi) start[b][gi][c] = cs[c_at[b][c] + (unsigned)(gi * cols)];
+                    c_at[b][c] += c_hop;
                 }
             }
 #pragma unroll
@@ -391,32 +452,41 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 }
 #pragma unroll
                 for (int gi = 0; gi < NG; ++gi) {
-                    float d[NB][4];
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) d[b][0] = d[b][1] = d[b][2] = d[b][3] = 0.f;
+                    // a group of 128 columns is eight MMAs: two chains of four
+                    constexpr int CH = NG == 1 ? 2 : 1;
+                    float d[NB][CH][4];
 #pragma unroll
                     for (int c = gi * (4 / NG); c < (gi + 1) * (4 / NG); ++c) {
                         uint32_t pa[4], pb[4];
-                        w4_unpack(wa[c], kc, pa);
-                        w4_unpack(wb[c], kc, pb);
+                        w4_raw(wa[c], kc, pa);
+                        w4_raw(wb[c], kc, pb);
+                        constexpr int PER = 4 / NG;
+                        const int ch = CH == 2 ? (c - gi * PER) & 1 : 0;
+                        const bool first = c - gi * PER < CH;
 #pragma unroll
                         for (int b = 0; b < NB; ++b) {
-                            mma_f16(d[b], pa[0], pb[0], pa[1], pb[1], bf[b][c].x, bf[b][c].y);
-                            mma_f16(d[b], pa[2], pb[2], pa[3], pb[3], bf[b][c].z, bf[b][c].w);
+                            if (first) mma_first(d[b][ch], pa[0], pb[0], pa[1], pb[1], bf[b][c].x, bf[b][c].y,
+                                                 ch ? 0.f : start[b][gi][0], ch ? 0.f : start[b][gi][1]);
+                            else mma_f16(d[b][ch], pa[0], pb[0], pa[1], pb[1], bf[b][c].x, bf[b][c].y);
+                            mma_f16(d[b][ch], pa[2], pb[2], pa[3], pb[3], bf[b][c].z, bf[b][c].w);
                         }
                     }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) d[b][0][e] += CH == 2 ? d[b][CH - 1][e] : 0.f;
                     const uint32_t sw = NG > 1 ? __shfl_sync(0xffffffffu, sc[tile], (lane & 28) | gi) : sc[tile];
                     const float s0 = bf16_lo(sw), s1 = bf16_hi(sw);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
                         if (P == 2) {          // columns 2t and 2t + 1 are the two parts of one token
-                            acc[tile][b][0] = fmaf((d[b][0] + d[b][1]) * f[b][0], s0, acc[tile][b][0]);
-                            acc[tile][b][1] = fmaf((d[b][2] + d[b][3]) * f[b][0], s1, acc[tile][b][1]);
+                            acc[tile][b][0] = fmaf((d[b][0][0] + d[b][0][1]) * f[b][0], s0, acc[tile][b][0]);
+                            acc[tile][b][1] = fmaf((d[b][0][2] + d[b][0][3]) * f[b][0], s1, acc[tile][b][1]);
                         } else {
-                            acc[tile][b][0] = fmaf(d[b][0] * f[b][0], s0, acc[tile][b][0]);
-                            acc[tile][b][AC > 2 ? 1 : 0] = fmaf(d[b][1] * f[b][P == 2 ? 0 : 1], s0, acc[tile][b][AC > 2 ? 1 : 0]);
-                            acc[tile][b][AC > 2 ? 2 : 0] = fmaf(d[b][2] * f[b][0], s1, acc[tile][b][AC > 2 ? 2 : 0]);
-                            acc[tile][b][AC > 2 ? 3 : 0] = fmaf(d[b][3] * f[b][P == 2 ? 0 : 1], s1, acc[tile][b][AC > 2 ? 3 : 0]);
+                            acc[tile][b][0] = fmaf(d[b][0][0] * f[b][0], s0, acc[tile][b][0]);
+                            acc[tile][b][AC > 2 ? 1 : 0] = fmaf(d[b][0][1] * f[b][P == 2 ? 0 : 1], s0, acc[tile][b][AC > 2 ? 1 : 0]);
+                            acc[tile][b][AC > 2 ? 2 : 0] = fmaf(d[b][0][2] * f[b][0], s1, acc[tile][b][AC > 2 ? 2 : 0]);
+                            acc[tile][b][AC > 2 ? 3 : 0] = fmaf(d[b][0][3] * f[b][P == 2 ? 0 : 1], s1, acc[tile][b][AC > 2 ? 3 : 0]);
                         }
                     }
                 }
@@ -440,23 +510,32 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     rw[r * WG_PITCH + row] = acc[a][b][c];
                 }
         __syncthreads();
-        for (int i = tid; i < sets * m * 32; i += WG_THREADS) {
-            const int row = i & 31, r = (i >> 5) % m, st2 = (i >> 5) / m;
-            if (GLU && row >= 16) continue;
-            const int n = row0 + (it * sets + st2) * GR + row;
-            if (n >= row1) continue;
+        for (int i = tid >> 2; i - (int)(lane >> 2) < items; i += WG_THREADS / 4) {   // the same for the whole warp
+            int r, st2, row;
+            const int n = item_of(it, i, r, st2, row);
             float v = 0.f, u = 0.f;
-            for (int w = 0; w < p.wk; ++w) {
-                const float* s = rb + ((size_t)(st2 * p.wk + w) * MT + r) * WG_PITCH + row;
-                v += s[0];
-                if (GLU) u += s[16];
+            if (n >= 0) {
+                for (int w = tid & 3; w < p.wk; w += 4) {
+                    const float* s = rb + ((size_t)(st2 * p.wk + w) * MT + r) * WG_PITCH + row;
+                    v += s[0];
+                    if (GLU) u += s[16];
+                }
             }
-            if (p.ks == 1) {
-                finish(r, n, v, u);
-            } else {
-                float* o = p.part + ((size_t)q * p.tokens + tok0 + r) * p.N * (GLU ? 2 : 1) + n;
-                o[0] = v;
-                if (GLU) o[p.N] = u;
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            if (GLU) {
+                u += __shfl_xor_sync(0xffffffffu, u, 1);
+                u += __shfl_xor_sync(0xffffffffu, u, 2);
+            }
+            if (n >= 0 && (tid & 3) == 0) {
+                if (p.ks == 1) {
+                    if (i != tid >> 2) res = residual_of(r, n);
+                    finish(r, n, v, u, res);
+                } else {
+                    float* o = p.part + ((size_t)q * p.tokens + tok0 + r) * p.N * (GLU ? 2 : 1) + n;
+                    o[0] = v;
+                    if (GLU) o[p.N] = u;
+                }
             }
         }
         // one buffer: the next row group's sums wait for this one's readers
@@ -484,7 +563,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     v += __ldcg(o);
                     if (GLU) u += __ldcg(o + p.N);
                 }
-                finish(r, n, v, u);
+                finish(r, n, v, u, residual_of(r, n));
             }
         }
     }
