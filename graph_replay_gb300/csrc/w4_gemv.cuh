@@ -155,36 +155,40 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     // where this lane's 16 bytes of row g or g + 8 of a tile go, and where its words are
     const int swz = G == 128 ? 0 : G == 64 ? ((g >> 1) & 1) << 1 : (g >> 1) & 3;
     const uint32_t put = (uint32_t)(g * 64 + ((t ^ swz) << 4));
-    const size_t cpitch = (size_t)(p.K >> 1), spitch = (size_t)(p.K / G);
+    // bytes of a row's codes and scales; a matrix has less than 2^32 of either, so a row is a 32-bit offset
+    const unsigned cpitch = (unsigned)p.K >> 1, spitch = (unsigned)(p.K / G) * 2u;
     struct Rows {                              // of a row group: rows g, g + 8 of tile 0, then of tile 1
-        const uint8_t* c[4];
-        const __nv_bfloat16* s[4];
+        unsigned c[4], s[4];                   // offsets of their codes and scales
         unsigned on;                           // bit i: row i is one of the CTA's
+        unsigned seg;                          // W4_STACK: bits 2i, 2i + 1: the matrix that row i lies in
     };
     auto rows_of = [&](int it, Rows& r) {
         const int base = row0 + (it * sets + set) * GR + g;
-        r.on = 0;
+        r.on = r.seg = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) r.on |= (base + (GLU ? 0 : 16 * (i >> 1)) + 8 * (i & 1) < row1 ? 1u : 0u) << i;
-        if (KIND == W4_STACK) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                int n = min(base + 8 * i, row1 - 1);
-                const bool z = n >= p.end[1], y = n >= p.end[0];
-                const uint8_t* cb = z ? p.codes[2] : y ? p.codes[1] : p.codes[0];
-                const __nv_bfloat16* sb = z ? p.scales[2] : y ? p.scales[1] : p.scales[0];
-                n -= z ? p.end[1] : y ? p.end[0] : 0;
-                r.c[i] = cb + (size_t)n * cpitch;
-                r.s[i] = sb + (size_t)n * spitch;
+        for (int i = 0; i < 4; ++i) {
+            const int at = base + (GLU ? 8 * (i & 1) : 8 * i);
+            r.on |= (at < row1 ? 1u : 0u) << i;
+            int n = min(at, row1 - 1);         // scales are read of any row
+            if (KIND == W4_STACK) {
+                const int sg = (n >= p.end[0]) + (n >= p.end[1]);
+                n -= sg == 2 ? p.end[1] : sg == 1 ? p.end[0] : 0;
+                r.seg |= (unsigned)sg << (2 * i);
             }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int n = min(base + (GLU ? 8 * (i & 1) : 8 * i), row1 - 1);   // scales are read of any row
-                r.c[i] = p.codes[GLU ? i >> 1 : 0] + (size_t)n * cpitch;
-                r.s[i] = p.scales[GLU ? i >> 1 : 0] + (size_t)n * spitch;
-            }
+            r.c[i] = (unsigned)n * cpitch;
+            r.s[i] = (unsigned)n * spitch;
         }
+    };
+    // the matrix of row i
+    auto codes_of = [&](const Rows& r, int i) -> const uint8_t* {
+        if (KIND != W4_STACK) return p.codes[GLU ? i >> 1 : 0];
+        const unsigned sg = r.seg >> (2 * i) & 3u;
+        return sg == 2 ? p.codes[2] : sg == 1 ? p.codes[1] : p.codes[0];
+    };
+    auto scale_of = [&](const Rows& r, int i) -> const unsigned char* {
+        if (KIND != W4_STACK) return reinterpret_cast<const unsigned char*>(p.scales[GLU ? i >> 1 : 0]);
+        const unsigned sg = r.seg >> (2 * i) & 3u;
+        return reinterpret_cast<const unsigned char*>(sg == 2 ? p.scales[2] : sg == 1 ? p.scales[1] : p.scales[0]);
     };
     const int steps = mine > 0 ? iters * mine : 0;
     const unsigned hop = (unsigned)p.wk * 64;  // bytes of a row from one of the warp's chunks to its next
@@ -195,12 +199,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     if (steps > 0) rows_of(0, ahead);
     auto copy_next = [&]() {
         if (a_left > 0) {
-            const bool in = a_at < (unsigned)cpitch;
+            const bool in = a_at < cpitch;
             const uint32_t dst = ring_at + a_slot + put;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // (of rows behind the CTA's last and columns behind the row's nothing is read: zeros)
-                cp_async16(dst + (uint32_t)((i >> 1) * 1024 + (i & 1) * 512), ahead.c[i] + a_at, in && (ahead.on >> i & 1u));
+                cp_async16(dst + (uint32_t)((i >> 1) * 1024 + (i & 1) * 512), codes_of(ahead, i) + (size_t)(ahead.c[i] + a_at),
+                           in && (ahead.on >> i & 1u));
             }
             --a_left;
             a_slot = (a_slot + WG_STEP) & (S * WG_STEP - 1);
@@ -346,20 +351,17 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     // the scales of the step after this one: of row g in the low half, of row g + 8 in the high half, of group t (one of
     // NG); raw bits
     Rows cur, next;
-    uint32_t sc[2] = {0u, 0u};
-    const int g_first = (ch0 + slice) * NG + (NG > 1 ? t % NG : 0), g_hop = p.wk * NG;
-    auto scales_of = [&](const Rows& r, int gr, uint32_t (&o)[2]) {   // no branches: the loop has few instructions to spare
-        const bool in = gr < (int)spitch;
-        const int at = in ? gr : (int)spitch - 1;
-        uint32_t v[4];
+    // two sets in turn: moving one into the other would wait for the loads
+    uint32_t s_even[4] = {0u, 0u, 0u, 0u}, s_odd[4] = {0u, 0u, 0u, 0u};
+    const unsigned g_first = 2u * (unsigned)((ch0 + slice) * NG + (NG > 1 ? t % NG : 0)), g_hop = 2u * (unsigned)(p.wk * NG);
+    auto scales_of = [&](const Rows& r, unsigned at, uint32_t (&o)[4]) {
+        at = min(at, spitch - 2u);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __ldg(reinterpret_cast<const unsigned short*>(r.s[i]) + at);
-        o[0] = in ? v[0] | (v[1] << 16) : 0u;
-        o[1] = in ? v[2] | (v[3] << 16) : 0u;
+        for (int i = 0; i < 4; ++i) o[i] = __ldg(reinterpret_cast<const unsigned short*>(scale_of(r, i) + (size_t)(r.s[i] + at)));
     };
     if (steps > 0) {
         rows_of(0, cur);
-        scales_of(cur, g_first, sc);
+        scales_of(cur, g_first, s_even);
     }
     const W4Sign kc;
     unsigned slot = 0;                         // of this step, in bytes
@@ -391,13 +393,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
             for (int c = 0; c < 2; ++c) c_at[b][c] = (unsigned)(slice * NG * cols + min(b * 8 + 2 * t + c, cols - 1));
         }
-        for (int i = 0; i < mine; ++i) {
-            uint32_t sn[2] = {0u, 0u};
+        auto one_step = [&](int i, const uint32_t (&use)[4], uint32_t (&fill)[4]) {
             if (i + 1 < mine) {
-                scales_of(cur, g_first + (i + 1) * g_hop, sn);
+                scales_of(cur, g_first + (unsigned)(i + 1) * g_hop, fill);
             } else if (it + 1 < iters) {
                 rows_of(it + 1, next);
-                scales_of(next, g_first, sn);
+                scales_of(next, g_first, fill);
             }
             cp_wait(S - 2);
             __syncwarp();
@@ -425,6 +426,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     c_at[b][c] += c_hop;
                 }
             }
+            // the scales of rows g and g + 8 of each tile (none behind the last group)
+            const bool in = g_first + (unsigned)i * g_hop < spitch;
+            const uint32_t sc[2] = {in ? use[0] | (use[1] << 16) : 0u, in ? use[2] | (use[3] << 16) : 0u};
 #pragma unroll
             for (int tile = 0; tile < 2; ++tile) {
                 if (!GLU && tile == 1 && base + 16 >= row1) break;   // the same for the whole warp
@@ -491,8 +495,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     }
                 }
             }
-            sc[0] = sn[0];
-            sc[1] = sn[1];
+        };
+        for (int i = 0; i < mine; i += 2) {
+            one_step(i, s_even, s_odd);
+            if (i + 1 < mine) one_step(i + 1, s_odd, s_even);
+        }
+        if (mine & 1) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) s_even[i] = s_odd[i];
         }
         if (it + 1 < iters && mine > 0) cur = next;
 
