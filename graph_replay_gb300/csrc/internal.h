@@ -209,20 +209,17 @@ struct W4Gemv {                // how w4_gemv.cu runs a call of few tokens
     W4Call c;
     int block;                 // tokens of a CTA
     int wk;                    // warps along k
-    int ks;                    // CTAs along k
+    int ks;                    // CTAs along k, a cluster
     int grid, rows;            // CTAs along n, output rows of each (the last may have fewer)
+    int stages;                // ring steps
     int bufs;                  // buffers of the cross-warp sums
     size_t smem;
-    float* part;               // ks > 1: [ks][tokens][n or 2 n]
-    unsigned* count;           // ks > 1: [blocks of tokens][grid], zero between calls
     unsigned long long* amax;  // logits of a decode step: [tokens] argmax keys, or null
     unsigned* nonfinite;       // [tokens]
     unsigned long long* trace;
     int trace_id;
 };
 cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms);
-size_t w4_gemv_floats(const W4Gemv& g);      // of g.part
-size_t w4_gemv_counters(const W4Gemv& g);    // of g.count
 cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl);
 struct W4Gemm {                // how w4_gemm.cu runs a call of many tokens
     W4Call c;                  // nw == 1, or glu

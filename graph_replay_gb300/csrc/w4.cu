@@ -165,10 +165,8 @@ cudaError_t plan_of(const W4Call& c, int sms, Plan* p) {
     }
     p->gemv = W4Gemv{};
     p->gemv.c = c;
-    const cudaError_t e = w4_gemv_plan(&p->gemv, sms);
-    const size_t floats = w4_gemv_floats(p->gemv);
-    p->bytes = floats ? DEC_W4_COUNTER_BYTES + round256(sizeof(float) * floats) : 0;
-    return e;
+    p->bytes = 0;
+    return w4_gemv_plan(&p->gemv, sms);
 }
 
 int run(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* call, void* stream) {
@@ -191,8 +189,6 @@ int run(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_
         p.gemm.ws = (char*)call->workspace + DEC_W4_COUNTER_BYTES;
         return launched(w4_gemm_launch(p.gemm, (cudaStream_t)stream), what);
     }
-    p.gemv.count = (unsigned*)call->workspace;
-    p.gemv.part = (float*)((char*)call->workspace + DEC_W4_COUNTER_BYTES);
     return launched(w4_gemv_launch(p.gemv, (cudaStream_t)stream, false), what);
 }
 

@@ -26,9 +26,40 @@ const void* kernel_of(const W4Gemv& g) {
 
 size_t smem_of(const W4Gemv& g) {
     const int P = g.c.parts(), chunks = (g.c.k() + 127) / 128, most = (chunks + g.ks - 1) / g.ks;
-    const size_t ring = (size_t)WG_WARPS * WG_STAGES * WG_STEP, x = (size_t)most * g.block * P * 256;
+    const size_t ring = (size_t)WG_WARPS * g.stages * WG_STEP, x = (size_t)most * g.block * P * 256;
     const size_t f = ((size_t)most * g.block + 3) / 4 * 16 + (size_t)most * (128 / g.c.group()) * g.block * P * sizeof(float);
-    return ring + x + f + sizeof(float) * g.bufs * WG_WARPS * wg_tokens(P, blocks_of(g)) * WG_PITCH;
+    const size_t sums = g.ks > 1 ? sizeof(float) * (g.c.glu ? 2 : 1) * g.block * g.rows : 0;
+    return ring + x + f + sums + sizeof(float) * g.bufs * WG_WARPS * wg_tokens(P, blocks_of(g)) * WG_PITCH;
+}
+
+// how many clusters of ks CTAs, one an SM, run at a time: they do not cross the chip's SM groups, so it may be less than
+// the SMs hold (asked once for each size; devices of one process are alike)
+int clusters(int ks, int num_sms) {
+    if (ks == 1) return num_sms;
+    static std::atomic<int> known[4];
+    const int i = ks == 2 ? 1 : ks == 4 ? 2 : 3;
+    int n = known[i].load(std::memory_order_relaxed);
+    if (n == 0) {
+        const void* fn = w4_gemv_kernel_128(2, 1, W4_ONE);
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr;
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = (unsigned)ks;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3((unsigned)(num_sms / ks * ks));
+        cfg.blockDim = dim3(WG_THREADS);
+        cfg.dynamicSmemBytes = SMEM_MOST;
+        cfg.attrs = &attr;
+        cfg.numAttrs = 1;
+        if (raise_smem_cap(fn) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+            cudaGetLastError();
+            n = num_sms / ks;
+        }
+        if (n > num_sms / ks) n = num_sms / ks;
+        if (n < 1) n = 1;
+        known[i].store(n, std::memory_order_relaxed);
+    }
+    return n;
 }
 
 }  // namespace
@@ -39,8 +70,10 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     g->block = c.tokens < most ? c.tokens : most;
     // rows evenly over the SMs, at least 8 a CTA: a tile has 16, and a CTA of fewer saves nothing
     const int gr = c.glu ? 16 : 32;
-    for (g->ks = 1; g->ks <= chunks; ++g->ks) {
-        const int places = num_sms / g->ks < 1 ? 1 : num_sms / g->ks;
+    // CTAs along k: the fewest (a cluster: 1, 2, 4 or 8) whose shared memory holds the activations beside a ring of four,
+    // three or two steps
+    for (g->ks = 1; g->ks <= 8 && g->ks <= chunks; g->ks *= 2) {
+        const int places = clusters(g->ks, num_sms);
         g->rows = (N + places - 1) / places;
         if (g->rows < 8) g->rows = 8;
         g->grid = (N + g->rows - 1) / g->rows;
@@ -51,9 +84,10 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
         while (g->wk > 1 && (own < g->wk || (groups >= 2 * (WG_WARPS / g->wk) && own < 8 * g->wk))) g->wk /= 2;
         const int sets = WG_WARPS / g->wk, iters = (groups + sets - 1) / sets;
         g->bufs = iters > 1 ? 2 : 1;
+        for (g->stages = WG_STAGES; g->stages > 2 && smem_of(*g) > SMEM_MOST; --g->stages) {}
         if (smem_of(*g) <= SMEM_MOST) break;
     }
-    if (g->ks > chunks || w4_gemv_counters(*g) > DEC_W4_COUNTER_BYTES / sizeof(unsigned)) return cudaErrorInvalidValue;
+    if (g->ks > 8 || g->ks > chunks) return cudaErrorInvalidValue;
     g->smem = smem_of(*g);
     // the cap once for each kernel and device
     static OncePerDevice once[3][2][2][3];
@@ -61,9 +95,6 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     if (!fn) return cudaErrorInvalidValue;
     return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][P - 1][blocks_of(*g) - 1][kind_of(c)].run([&] { return raise_smem_cap(fn); });
 }
-
-size_t w4_gemv_floats(const W4Gemv& g) { return g.ks > 1 ? (size_t)g.ks * g.c.tokens * g.c.n() * (g.c.glu ? 2 : 1) : 0; }
-size_t w4_gemv_counters(const W4Gemv& g) { return g.ks > 1 ? (size_t)g.grid * ((g.c.tokens + g.block - 1) / g.block) : 0; }
 
 cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl) {
     const W4Call& c = g.c;
@@ -83,6 +114,7 @@ cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl) {
     a.wk = g.wk;
     a.ks = g.ks;
     a.rows = g.rows;
+    a.stages = g.stages;
     a.bufs = g.bufs;
     a.act = c.act;
     a.x_f32 = c.x_f32;
@@ -96,8 +128,6 @@ cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl) {
     a.residual_stride = c.residual_stride;
     a.out_stride = c.out_stride;
     a.eps = c.eps;
-    a.part = g.part;
-    a.count = g.count;
     a.amax = g.amax;
     a.nonfinite = g.nonfinite;
     a.trace = g.trace;
@@ -107,11 +137,18 @@ cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl) {
     cfg.blockDim = dim3(WG_THREADS);
     cfg.dynamicSmemBytes = g.smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchAttribute attr[2];
     cfg.attrs = attr;
-    cfg.numAttrs = pdl ? 1 : 0;
+    if (pdl) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    if (g.ks > 1) {
+        attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        attr[cfg.numAttrs].val.clusterDim.x = (unsigned)g.ks;
+        attr[cfg.numAttrs].val.clusterDim.y = attr[cfg.numAttrs].val.clusterDim.z = 1;
+        ++cfg.numAttrs;
+    }
     void* args[] = {&a};
     return cudaLaunchKernelExC(&cfg, kernel_of(g), args);
 }

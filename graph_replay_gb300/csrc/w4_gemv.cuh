@@ -22,9 +22,9 @@
 // cp.async into a ring of its own, so the loop has no barriers; a row group ends
 // with one barrier and a sum over the warps in their order.
 // The activations of a CTA's columns stay in shared memory as B fragments.  Where
-// they do not fit, `ks` CTAs share the columns of a row range, leave their sums in
-// the workspace, and the last to arrive adds them in order.  Results do not depend
-// on scheduling.
+// they do not fit, a cluster of `ks` CTAs shares the columns of a row range, and each
+// of them adds the sums of a part of the rows from the others' shared memory, in
+// order.  Results do not depend on scheduling.
 #pragma once
 #include "w4.cuh"
 
@@ -35,7 +35,7 @@ constexpr int WG_THREADS = WG_WARPS * 32;
 constexpr int WG_STEP = 2048;                  // bytes of a step: two tiles of 16 rows x 128 columns
 constexpr int WG_PITCH = 33;                   // of 32 rows' sums of one token
 constexpr int WG_MAX_TOKENS = 16;
-constexpr int WG_STAGES = 4;                   // steps of a warp's ring
+constexpr int WG_STAGES = 4;                   // steps of a warp's ring at most
 
 // one matrix; a gate and an up matrix; two or three stacked
 enum { W4_ONE = 0, W4_GLU = 1, W4_STACK = 2 };
@@ -47,15 +47,13 @@ struct W4GemvArgs {
     const uint8_t* codes[3];
     const __nv_bfloat16* scales[3];
     int end[3];                // rows of segments 0, 0 + 1, all
-    int N, K, tokens, block, wk, ks, rows, bufs, act, x_f32, gain_f32, out_f32;
+    int N, K, tokens, block, wk, ks, rows, stages, bufs, act, x_f32, gain_f32, out_f32;
     const void* x;
     const void* gain;
     const void* residual;
     void* out;
     long long x_stride, residual_stride, out_stride;
     float eps;
-    float* part;
-    unsigned* count;
     unsigned long long* amax;
     unsigned* nonfinite;
     unsigned long long* trace;
@@ -106,11 +104,23 @@ __device__ __forceinline__ void cp_wait(int left) {   // all but the newest `lef
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// all threads of the cluster's CTAs; what they wrote to shared memory is visible to all behind it
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the value at p's place in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
 // G: columns of a group; P: fp16 parts of an activation; NB: blocks of 8 B columns
 template <int G, int P, int NB, int KIND>
 __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant__ W4GemvArgs p) {
     constexpr bool GLU = KIND == W4_GLU;
-    constexpr int S = WG_STAGES;
     constexpr int NG = 128 / G;                // groups of a step
     constexpr int MT = wg_tokens(P, NB);       // tokens that fit
     constexpr int AC = P == 2 ? 2 : 4;         // sums of a lane, tile and column block
@@ -120,7 +130,6 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     __shared__ float inv_s[MT];
     __shared__ unsigned long long best_s[8];
     __shared__ unsigned nonfinite_s[8];
-    __shared__ int last_s;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
     const int tok0 = blockIdx.y * p.block, m = min(p.block, p.tokens - tok0);
@@ -134,11 +143,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const int iters = (ngroups + sets - 1) / sets;              // of each set
     const int mine = (ch1 - ch0 - slice + p.wk - 1) / p.wk;     // this warp's chunks of a row group (>= 0)
 
-    unsigned char* ring = smem + (size_t)warp * S * WG_STEP;
-    unsigned char* xs = smem + (size_t)WG_WARPS * S * WG_STEP;               // [chunk][4][cols][64 bytes]
+    const int S = p.stages;
+    const unsigned ring_bytes = (unsigned)S * WG_STEP;
+    unsigned char* ring = smem + (size_t)warp * ring_bytes;
+    unsigned char* xs = smem + (size_t)WG_WARPS * ring_bytes;                // [chunk][4][cols][64 bytes]
     float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14 + 12)
     float* cs = fs + (((ch1 - ch0) * p.block + 3) & ~3);                     // [chunk][NG][cols]: where a group's sums start
     float* red = cs + (ch1 - ch0) * NG * cols;                               // [bufs][warp][MT][WG_PITCH]
+    float* sums = red + p.bufs * WG_WARPS * MT * WG_PITCH;                   // ks > 1: [1 or 2][block][rows], read by the cluster
     const uint32_t ring_at = smem_u32(ring);
 
     unsigned long long* tr = nullptr;
@@ -208,7 +220,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                            in && (ahead.on >> i & 1u));
             }
             --a_left;
-            a_slot = (a_slot + WG_STEP) & (S * WG_STEP - 1);
+            a_slot = a_slot + WG_STEP == ring_bytes ? 0u : a_slot + WG_STEP;
             a_at += hop;
             if (++a_i == mine) {
                 a_i = 0;
@@ -298,19 +310,26 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             }
         }
         if (p.gain && nc <= 0 && lane < m) ss_s[warp][lane] = 0.f;
-        if (p.gain && p.ks > 1) {   // the other CTAs' columns, for the norm
+        if (p.gain && p.ks > 1) {   // the other CTAs' columns, for the norm: a load of every token at a time
             __syncwarp();
-            for (int r2 = 0; r2 < m; ++r2) {
-                float s2 = 0.f;
-                for (int c = warp; c < chunks; c += WG_WARPS) {
-                    const int k = c * 128 + 4 * lane;
-                    if ((c < ch0 || c >= ch1) && k < p.K) {
-                        const float4 x = w4_load4(p.x, p.x_f32, (size_t)(tok0 + r2) * p.x_stride + k);
-                        s2 = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, s2))));
-                    }
-                }
-                s2 = warp_sum(s2);
-                if (lane == 0) ss_s[warp][r2] += s2;
+            float s2[MT];
+#pragma unroll
+            for (int i = 0; i < MT; ++i) s2[i] = 0.f;
+            for (int c = warp; c < chunks; c += WG_WARPS) {
+                const int k = c * 128 + 4 * lane;
+                if ((c >= ch0 && c < ch1) || k >= p.K) continue;
+                float4 x[MT];
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    x[i] = i < m ? w4_load4(p.x, p.x_f32, (size_t)(tok0 + i) * p.x_stride + k) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int i = 0; i < MT; ++i)
+                    s2[i] = fmaf(x[i].x, x[i].x, fmaf(x[i].y, x[i].y, fmaf(x[i].z, x[i].z, fmaf(x[i].w, x[i].w, s2[i]))));
+            }
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                const float s = warp_sum(s2[i]);
+                if (lane == 0 && i < m) ss_s[warp][i] += s;
             }
         }
     }
@@ -404,96 +423,102 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             __syncwarp();
             copy_next();                       // into the slot that the step before read
             const unsigned char* st = ring + slot;
-            slot = (slot + WG_STEP) & (S * WG_STEP - 1);
+            slot = slot + WG_STEP == ring_bytes ? 0u : slot + WG_STEP;
             // columns of B and tokens that there are not repeat others: what they give is not used
-            uint4 bf[NB][4];                   // [q]: the B words of MMA 2q and 2q + 1
             float f[NB][P == 2 ? 1 : 2];       // the scales of the tokens of this lane's sums
-            float start[NB][NG][2];            // of its two columns
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) bf[b][c] = *reinterpret_cast<const uint4*>(xs + b_at[b] + (unsigned)c * cols * 64);
-                b_at[b] += b_hop;
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int c = 0; c < (P == 2 ? 1 : 2); ++c) {
                     f[b][c] = fs[f_at[b][c]];
                     f_at[b][c] += f_hop;
                 }
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-#pragma unroll
-                    for (int gi = 0; gi < NG; ++gi) start[b][gi][c] = cs[c_at[b][c] + (unsigned)(gi * cols)];
-                    c_at[b][c] += c_hop;
-                }
-            }
             // the scales of rows g and g + 8 of each tile (none behind the last group)
             const bool in = g_first + (unsigned)i * g_hop < spitch;
             const uint32_t sc[2] = {in ? use[0] | (use[1] << 16) : 0u, in ? use[2] | (use[3] << 16) : 0u};
+            const unsigned char* ta = st + g * 64;
+            uint32_t wa[2][4], wb[2][4];       // words of rows g and g + 8 of a tile, word c for MMAs 2c and 2c + 1
+            if (G == 128) {
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
-                if (!GLU && tile == 1 && base + 16 >= row1) break;   // the same for the whole warp
-                const unsigned char* ta = st + tile * 1024 + g * 64;
-                uint32_t wa[4], wb[4];         // words of rows g and g + 8, word c for MMAs 2c and 2c + 1
-                if (G == 128) {
-                    const uint4 a = *reinterpret_cast<const uint4*>(ta + t * 16), b = *reinterpret_cast<const uint4*>(ta + 512 + t * 16);
-                    wa[0] = a.x; wa[1] = a.y; wa[2] = a.z; wa[3] = a.w;
-                    wb[0] = b.x; wb[1] = b.y; wb[2] = b.z; wb[3] = b.w;
-                } else if (G == 64) {
+                for (int tile = 0; tile < 2; ++tile) {
+                    const uint4 a = *reinterpret_cast<const uint4*>(ta + tile * 1024 + t * 16);
+                    const uint4 b = *reinterpret_cast<const uint4*>(ta + tile * 1024 + 512 + t * 16);
+                    wa[tile][0] = a.x; wa[tile][1] = a.y; wa[tile][2] = a.z; wa[tile][3] = a.w;
+                    wb[tile][0] = b.x; wb[tile][1] = b.y; wb[tile][2] = b.z; wb[tile][3] = b.w;
+                }
+            }
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int at = ((2 * h + (t >> 1)) ^ swz) * 16 + (t & 1) * 8;
+            for (int gi = 0; gi < NG; ++gi) {
+                constexpr int PER = 4 / NG;    // words of a group
+                if (G == 64) {
+#pragma unroll
+                    for (int tile = 0; tile < 2; ++tile) {
+                        const int at = tile * 1024 + ((2 * gi + (t >> 1)) ^ swz) * 16 + (t & 1) * 8;
                         const uint2 a = *reinterpret_cast<const uint2*>(ta + at), b = *reinterpret_cast<const uint2*>(ta + 512 + at);
-                        wa[2 * h] = a.x; wa[2 * h + 1] = a.y;
-                        wb[2 * h] = b.x; wb[2 * h + 1] = b.y;
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int at = (c ^ swz) * 16 + t * 4;
-                        wa[c] = *reinterpret_cast<const uint32_t*>(ta + at);
-                        wb[c] = *reinterpret_cast<const uint32_t*>(ta + 512 + at);
+                        wa[tile][2 * gi] = a.x; wa[tile][2 * gi + 1] = a.y;
+                        wb[tile][2 * gi] = b.x; wb[tile][2 * gi + 1] = b.y;
                     }
                 }
+                float d[2][NB][4];
 #pragma unroll
-                for (int gi = 0; gi < NG; ++gi) {
-                    // a group of 128 columns is eight MMAs: two chains of four
-                    constexpr int CH = NG == 1 ? 2 : 1;
-                    float d[NB][CH][4];
+                for (int c = gi * PER; c < (gi + 1) * PER; ++c) {
+                    if (G == 32) {
 #pragma unroll
-                    for (int c = gi * (4 / NG); c < (gi + 1) * (4 / NG); ++c) {
-                        uint32_t pa[4], pb[4];
-                        w4_raw(wa[c], kc, pa);
-                        w4_raw(wb[c], kc, pb);
-                        constexpr int PER = 4 / NG;
-                        const int ch = CH == 2 ? (c - gi * PER) & 1 : 0;
-                        const bool first = c - gi * PER < CH;
-#pragma unroll
-                        for (int b = 0; b < NB; ++b) {
-                            if (first) mma_first(d[b][ch], pa[0], pb[0], pa[1], pb[1], bf[b][c].x, bf[b][c].y,
-                                                 ch ? 0.f : start[b][gi][0], ch ? 0.f : start[b][gi][1]);
-                            else mma_f16(d[b][ch], pa[0], pb[0], pa[1], pb[1], bf[b][c].x, bf[b][c].y);
-                            mma_f16(d[b][ch], pa[2], pb[2], pa[3], pb[3], bf[b][c].z, bf[b][c].w);
+                        for (int tile = 0; tile < 2; ++tile) {
+                            const int at = tile * 1024 + (c ^ swz) * 16 + t * 4;
+                            wa[tile][c] = *reinterpret_cast<const uint32_t*>(ta + at);
+                            wb[tile][c] = *reinterpret_cast<const uint32_t*>(ta + 512 + at);
                         }
+                    }
+                    uint4 bf[NB];              // the B words of MMAs 2c and 2c + 1
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) bf[b] = *reinterpret_cast<const uint4*>(xs + b_at[b] + (unsigned)c * cols * 64);
+                    // (a second tile without rows holds zeros: its products cost less than a branch around them)
+                    uint32_t pa[2][4], pb[2][4];
+#pragma unroll
+                    for (int tile = 0; tile < 2; ++tile) {
+                        w4_raw(wa[tile][c], kc, pa[tile]);
+                        w4_raw(wb[tile][c], kc, pb[tile]);
                     }
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) d[b][0][e] += CH == 2 ? d[b][CH - 1][e] : 0.f;
+                        for (int tile = 0; tile < 2; ++tile) {
+                            if (c == gi * PER) mma_first(d[tile][b], pa[tile][0], pb[tile][0], pa[tile][1], pb[tile][1], bf[b].x, bf[b].y,
+                                                         cs[c_at[b][0] + (unsigned)(gi * cols)], cs[c_at[b][1] + (unsigned)(gi * cols)]);
+                            else mma_f16(d[tile][b], pa[tile][0], pb[tile][0], pa[tile][1], pb[tile][1], bf[b].x, bf[b].y);
+                        }
+#pragma unroll
+                    for (int b = 0; b < NB; ++b)
+#pragma unroll
+                        for (int tile = 0; tile < 2; ++tile)
+                            mma_f16(d[tile][b], pa[tile][2], pb[tile][2], pa[tile][3], pb[tile][3], bf[b].z, bf[b].w);
+                }
+#pragma unroll
+                for (int tile = 0; tile < 2; ++tile) {
                     const uint32_t sw = NG > 1 ? __shfl_sync(0xffffffffu, sc[tile], (lane & 28) | gi) : sc[tile];
                     const float s0 = bf16_lo(sw), s1 = bf16_hi(sw);
 #pragma unroll
                     for (int b = 0; b < NB; ++b) {
+                        const float* e = d[tile][b];
+                        float* o = acc[tile][b];
                         if (P == 2) {          // columns 2t and 2t + 1 are the two parts of one token
-                            acc[tile][b][0] = fmaf((d[b][0][0] + d[b][0][1]) * f[b][0], s0, acc[tile][b][0]);
-                            acc[tile][b][1] = fmaf((d[b][0][2] + d[b][0][3]) * f[b][0], s1, acc[tile][b][1]);
+                            o[0] = fmaf((e[0] + e[1]) * f[b][0], s0, o[0]);
+                            o[1] = fmaf((e[2] + e[3]) * f[b][0], s1, o[1]);
                         } else {
-                            acc[tile][b][0] = fmaf(d[b][0][0] * f[b][0], s0, acc[tile][b][0]);
-                            acc[tile][b][AC > 2 ? 1 : 0] = fmaf(d[b][0][1] * f[b][P == 2 ? 0 : 1], s0, acc[tile][b][AC > 2 ? 1 : 0]);
-                            acc[tile][b][AC > 2 ? 2 : 0] = fmaf(d[b][0][2] * f[b][0], s1, acc[tile][b][AC > 2 ? 2 : 0]);
-                            acc[tile][b][AC > 2 ? 3 : 0] = fmaf(d[b][0][3] * f[b][P == 2 ? 0 : 1], s1, acc[tile][b][AC > 2 ? 3 : 0]);
+                            o[0] = fmaf(e[0] * f[b][0], s0, o[0]);
+                            o[AC == 4 ? 1 : 0] = fmaf(e[1] * f[b][P == 2 ? 0 : 1], s0, o[AC == 4 ? 1 : 0]);
+                            o[AC == 4 ? 2 : 0] = fmaf(e[2] * f[b][0], s1, o[AC == 4 ? 2 : 0]);
+                            o[AC == 4 ? 3 : 0] = fmaf(e[3] * f[b][P == 2 ? 0 : 1], s1, o[AC == 4 ? 3 : 0]);
                         }
                     }
                 }
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                b_at[b] += b_hop;
+                c_at[b][0] += c_hop;
+                c_at[b][1] += c_hop;
             }
         };
         for (int i = 0; i < mine; i += 2) {
@@ -542,9 +567,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     if (i != tid >> 2) res = residual_of(r, n);
                     finish(r, n, v, u, res);
                 } else {
-                    float* o = p.part + ((size_t)q * p.tokens + tok0 + r) * p.N * (GLU ? 2 : 1) + n;
-                    o[0] = v;
-                    if (GLU) o[p.N] = u;
+                    sums[r * p.rows + n - row0] = v;
+                    if (GLU) sums[(p.block + r) * p.rows + n - row0] = u;
                 }
             }
         }
@@ -553,29 +577,22 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     }
 
     if (p.ks > 1) {
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) {
-            unsigned* c = p.count + (size_t)blockIdx.y * (gridDim.x / p.ks) + ri;
-            const unsigned before = atomicAdd(c, 1u);
-            last_s = before == (unsigned)p.ks - 1u;
-            if (last_s) *c = 0u;               // ready for the next call
-        }
-        __syncthreads();
-        if (last_s) {
-            __threadfence();
-            const int nr = row1 - row0;
-            for (int i = tid; i < nr * m; i += WG_THREADS) {
-                const int r = i / nr, n = row0 + i - r * nr;
-                float v = 0.f, u = 0.f;
-                for (int w = 0; w < p.ks; ++w) {
-                    const float* o = p.part + ((size_t)w * p.tokens + tok0 + r) * p.N * (GLU ? 2 : 1) + n;
-                    v += __ldcg(o);
-                    if (GLU) u += __ldcg(o + p.N);
-                }
-                finish(r, n, v, u, residual_of(r, n));
+        // every CTA of the cluster finishes a part of the outputs: the sums of all, in their order
+        cluster_sync();
+        const int nr = row1 - row0, all = nr * m;
+        const int end = (int)((long long)(q + 1) * all / p.ks);
+        for (int i = (int)((long long)q * all / p.ks) + tid; i < end; i += WG_THREADS) {
+            const int r = i / nr, row = i - r * nr;
+            const float res = residual_of(r, row0 + row);
+            float v = 0.f, u = 0.f;
+            for (int w = 0; w < p.ks; ++w) {
+                const float* s = sums + r * p.rows + row;
+                v += ld_cluster(s, w);
+                if (GLU) u += ld_cluster(s + p.block * p.rows, w);
             }
+            finish(r, row0 + row, v, u, res);
         }
+        cluster_sync();                        // until the others have read this CTA's sums
     }
     if (!GLU && p.amax) {
         __syncthreads();
