@@ -99,6 +99,10 @@ class dec_w4_weight(ctypes.Structure):
                 ("group", ctypes.c_int32), ("device", ctypes.c_int32)]
 
 
+class dec_w4_binding(ctypes.Structure):
+    _fields_ = [("role", ctypes.c_int32), ("layer", ctypes.c_int32), ("w", dec_w4_weight)]
+
+
 class dec_w4_call(ctypes.Structure):
     _fields_ = [("x", ctypes.c_void_p), ("gain", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("out", ctypes.c_void_p),
                 ("x_stride", ctypes.c_int64), ("residual_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
@@ -115,6 +119,7 @@ _I64 = ctypes.c_int64
 _SIG = [
     ("dec_init", ctypes.c_int, [ctypes.POINTER(dec_config), ctypes.POINTER(_P)]),
     ("dec_load_weights", ctypes.c_int, [_P, ctypes.POINTER(dec_weight), ctypes.c_size_t]),
+    ("dec_load_w4", ctypes.c_int, [_P, ctypes.POINTER(dec_w4_binding), ctypes.c_size_t]),
     ("dec_workspace_size", ctypes.c_int, [ctypes.POINTER(dec_config), _I32, _I32, _I32, _I32, _I32,
                                           ctypes.POINTER(ctypes.c_size_t)]),
     ("dec_capture", ctypes.c_int, [_P, _I32, _I32, _I32, _I32, _I32, _P, ctypes.c_size_t, _P]),
@@ -227,6 +232,11 @@ def dec_init(cfg: dec_config) -> int:
 def dec_load_weights(h, bindings) -> None:
     arr = (dec_weight * len(bindings))(*bindings)
     check(h, lib().dec_load_weights(h, arr, len(bindings)))
+
+
+def dec_load_w4(h, bindings) -> None:
+    arr = (dec_w4_binding * len(bindings))(*bindings)
+    check(h, lib().dec_load_w4(h, arr, len(bindings)))
 
 
 def dec_workspace_size(cfg: dec_config, cap, rows, kv_layout, page_size=0, num_pages=0) -> int:

@@ -18,6 +18,7 @@
 #include <array>
 #include <chrono>
 #include <cmath>
+#include <memory>
 #include <string>
 #include <thread>
 #include <vector>
@@ -165,6 +166,9 @@ struct dec_handle {
     const void* embed = nullptr;
     const void* final_norm = nullptr;
     const void* lm_head = nullptr;
+    std::vector<std::array<W4Matrix, 9>> lw4;   // per layer, by role: bound by dec_load_w4 (codes null: not)
+    W4Matrix lm_head4{};
+    std::vector<std::unique_ptr<W4Gemv>> w4;    // the plans of projections in 4 bits
     std::vector<std::array<const void*, 9>> lw;   // roles DEC_W_ATTN_NORM .. DEC_W_DOWN
 
     // capture
@@ -365,6 +369,19 @@ Kv8Cache kv8_cache(const dec_handle* h, int l) {
                     kv8_log2(block), FastDiv((unsigned)page)};
 }
 
+bool any_w4(const dec_handle* h) {
+    if (h->lm_head4.codes) return true;
+    for (const auto& w : h->lw4)
+        if (w[1].codes) return true;
+    return false;
+}
+
+// bytes of a projection's matrices (es: of a value that is not in 4 bits)
+int64_t matrix_bytes(const GemvPlan& g, int64_t es) {
+    const int64_t n = (int64_t)g.p.N * g.p.K;
+    return g.w4 ? n / 2 + 2 * (n / g.w4->c.group()) : n * es;
+}
+
 // launch the whole step (the sequence the graph records)
 cudaError_t enqueue_step(dec_handle* h) {
     cudaError_t e;
@@ -487,6 +504,7 @@ int dec_init(const dec_config* cfg, dec_handle** out) {
     h->cfg = *cfg;
     if (h->cfg.wait_timeout_ms <= 0) h->cfg.wait_timeout_ms = 600000;
     h->lw.assign(cfg->n_layers, std::array<const void*, 9>{});
+    h->lw4.assign(cfg->n_layers, std::array<W4Matrix, 9>{});
     cudaError_t e = cudaSetDevice(cfg->device);
     if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->num_sms, cudaDevAttrMultiProcessorCount, cfg->device);
     if (e != cudaSuccess) {
@@ -523,8 +541,49 @@ int dec_load_weights(dec_handle* h, const dec_weight* w, size_t n) {
         switch (b.role) {
             case DEC_W_EMBED: h->embed = b.data; break;
             case DEC_W_FINAL_NORM: h->final_norm = b.data; break;
-            case DEC_W_LM_HEAD: h->lm_head = b.data; break;
-            default: h->lw[b.layer][b.role - DEC_W_ATTN_NORM] = b.data;
+            case DEC_W_LM_HEAD:
+                h->lm_head = b.data;
+                h->lm_head4 = W4Matrix{};
+                break;
+            default:
+                h->lw[b.layer][b.role - DEC_W_ATTN_NORM] = b.data;
+                h->lw4[b.layer][b.role - DEC_W_ATTN_NORM] = W4Matrix{};
+        }
+    }
+    return DEC_OK;
+}
+
+int dec_load_w4(dec_handle* h, const dec_w4_binding* w, size_t n) {
+    int rc = gate(h, false);
+    if (rc) return rc;
+    if (h->captured) return fail(h, DEC_E_STATE, "weights are bound before dec_capture");
+    if (!w && n) return fail(h, DEC_E_INVALID, "binding array is NULL");
+    for (size_t i = 0; i < n; ++i) {
+        const dec_w4_binding& b = w[i];
+        const dec_w4_weight& m = b.w;
+        const bool head = b.role == DEC_W_LM_HEAD;
+        if (!head && (b.role < DEC_W_Q || b.role > DEC_W_DOWN || b.role == DEC_W_FFN_NORM))
+            return fail(h, DEC_E_INVALID, "binding %zu: role %d (%s) has no 4-bit form", i, b.role, role_name(b.role));
+        if (head ? b.layer != -1 : (b.layer < 0 || b.layer >= h->cfg.n_layers))
+            return fail(h, DEC_E_INVALID, "binding %zu (%s): bad layer %d", i, role_name(b.role), b.layer);
+        if (!shape_ok(h->cfg, b.role, m.n, m.k))
+            return fail(h, DEC_E_INVALID, "binding %zu (%s, layer %d): shape [%d, %d] does not match the config", i,
+                        role_name(b.role), b.layer, m.n, m.k);
+        if (m.device != h->cfg.device)
+            return fail(h, DEC_E_INVALID, "binding %zu (%s): on device %d, the handle on %d", i, role_name(b.role), m.device,
+                        h->cfg.device);
+        W4Matrix checked;
+        if ((rc = w4_check(role_name(b.role), &m, &checked)) != DEC_OK) return fail(h, rc, "binding %zu: %s", i, call_message());
+    }
+    for (size_t i = 0; i < n; ++i) {
+        const dec_w4_binding& b = w[i];
+        const W4Matrix m{b.w.codes, b.w.scales, b.w.n, b.w.k, b.w.group};
+        if (b.role == DEC_W_LM_HEAD) {
+            h->lm_head = nullptr;
+            h->lm_head4 = m;
+        } else {
+            h->lw[b.layer][b.role - DEC_W_ATTN_NORM] = nullptr;
+            h->lw4[b.layer][b.role - DEC_W_ATTN_NORM] = m;
         }
     }
     return DEC_OK;
@@ -569,10 +628,21 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
     if (h->window && !kv8) return fail(h, DEC_E_UNSUPPORTED, "a window needs an e4m3 K/V store");
     if (!h->embed) return fail(h, DEC_E_INVALID, "weight EMBED is unbound");
     if (!h->final_norm) return fail(h, DEC_E_INVALID, "weight FINAL_NORM is unbound");
-    if (!h->lm_head) return fail(h, DEC_E_INVALID, "weight LM_HEAD is unbound");
+    if (!h->lm_head && !h->lm_head4.codes) return fail(h, DEC_E_INVALID, "weight LM_HEAD is unbound");
     for (int l = 0; l < c.n_layers; ++l)
         for (int k = 0; k < 9; ++k)
-            if (!h->lw[l][k]) return fail(h, DEC_E_INVALID, "weight %s of layer %d is unbound", role_name(k + 1), l);
+            if (!h->lw[l][k] && !h->lw4[l][k].codes)
+                return fail(h, DEC_E_INVALID, "weight %s of layer %d is unbound", role_name(k + 1), l);
+    for (int l = 0; l < c.n_layers; ++l) {
+        const auto& w = h->lw4[l];   // by role as in lw: 1 q, 2 k, 3 v, 4 o, 6 gate, 7 up, 8 down
+        const int count = !!w[1].codes + !!w[2].codes + !!w[3].codes + !!w[4].codes + !!w[6].codes + !!w[7].codes + !!w[8].codes;
+        if (count != 0 && count != 7)
+            return fail(h, DEC_E_UNSUPPORTED, "layer %d: all seven matrices in 4 bits or none, not %d", l, count);
+        if (count && (w[1].group != w[2].group || w[1].group != w[3].group || w[6].group != w[7].group))
+            return fail(h, DEC_E_UNSUPPORTED, "layer %d: Q, K and V have one group, and GATE and UP", l);
+    }
+    if (h->strategy == DEC_STRATEGY_PERSISTENT && any_w4(h))
+        return fail(h, DEC_E_UNSUPPORTED, "the persistent strategy has no matrices in 4 bits");
 
     cudaError_t e = cudaSetDevice(c.device);
     if (e != cudaSuccess) return cuda_fail(h, e, "cudaSetDevice");
@@ -712,8 +782,50 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
         p.tc_cnt = (unsigned*)(h->ws + h->lay.gcnt);
         return pl;
     };
+    // a projection whose matrices are in 4 bits: the shape as mk gives it, and the plan that runs
+    auto mk4 = [&](int pro, int epi, const W4Matrix* w, int nw, const float* act, int act_stride, const void* gain, float* out,
+                   int out_stride) {
+        const bool glu = epi == EPI_SWIGLU;
+        GemvPlan pl = mk(pro, epi, nullptr, w[0].n, nullptr, nw > 1 ? w[1].n : 0, nullptr, nw > 2 ? w[2].n : 0, w[0].k, act,
+                         act_stride, gain, out, out_stride);
+        h->w4.emplace_back(new W4Gemv{});
+        W4Gemv& g = *h->w4.back();
+        W4Call& q = g.c;
+        for (int i = 0; i < nw; ++i) q.w[i] = w[i];
+        q.nw = nw;
+        q.glu = glu;
+        q.act = DEC_ACT_SILU;
+        q.tokens = rows;
+        q.x = act;
+        q.x_stride = act_stride;
+        q.x_f32 = true;
+        q.gain = gain;
+        q.gain_f32 = wt == W_F32;
+        q.eps = (float)c.rms_eps;
+        q.out = out;
+        q.out_stride = out_stride;
+        q.out_f32 = true;
+        q.residual = epi == EPI_ADD ? out : nullptr;
+        q.residual_stride = out_stride;
+        q.err = &h->d_status->err;
+        if (epi == EPI_LOGITS) {
+            g.amax = h->d_status->amax;
+            g.nonfinite = h->d_status->nonfinite;
+        }
+        g.trace = h->d_trace;
+        pl.w4 = &g;
+        return pl;
+    };
+    h->w4.clear();
     for (int l = 0; l < c.n_layers; ++l) {
         const auto& w = h->lw[l];   // attn_norm, q, k, v, o, ffn_norm, gate, up, down
+        const auto& w4 = h->lw4[l];
+        if (w4[1].codes) {
+            h->gemv.push_back(mk4(PRO_RMSNORM, EPI_STORE, &w4[1], 3, h->d_x, d, w[0], h->d_qkv, qkv_stride));
+            h->gemv.push_back(mk4(PRO_PLAIN, EPI_ADD, &w4[4], 1, h->d_attn, Hq * hd, nullptr, h->d_x, d));
+            h->gemv.push_back(mk4(PRO_RMSNORM, EPI_SWIGLU, &w4[6], 2, h->d_x, d, w[5], h->d_gu, 2 * F));
+            h->gemv.push_back(mk4(PRO_PLAIN, EPI_ADD, &w4[8], 1, h->d_gu, 2 * F, nullptr, h->d_x, d));
+        } else {
         h->gemv.push_back(mk(PRO_RMSNORM, EPI_STORE, w[1], Hq * hd, w[2], Hkv * hd, w[3], Hkv * hd, d, h->d_x, d, w[0],
                              h->d_qkv, qkv_stride));
         h->gemv.push_back(mk(PRO_PLAIN, EPI_ADD, w[4], d, nullptr, 0, nullptr, 0, Hq * hd, h->d_attn, Hq * hd, nullptr,
@@ -728,6 +840,7 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
                                  2 * F));
             h->gemv.push_back(mk(PRO_SWIGLU, EPI_ADD, w[8], d, nullptr, 0, nullptr, 0, F, h->d_gu, 2 * F, nullptr,
                                  h->d_x, d));
+        }
         }
         AttnPlan ap{};
         ap.kvtype = c.kv_dtype == DEC_DTYPE_BF16 ? W_BF16 : W_F32;
@@ -758,8 +871,11 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
         p.trace_id = 2 + 5 * l;
         h->attn.push_back(ap);
     }
-    h->gemv.push_back(mk(PRO_RMSNORM, EPI_LOGITS, h->lm_head, c.vocab, nullptr, 0, nullptr, 0, d, h->d_x, d,
-                         h->final_norm, h->d_logits, c.vocab));
+    if (h->lm_head4.codes)
+        h->gemv.push_back(mk4(PRO_RMSNORM, EPI_LOGITS, &h->lm_head4, 1, h->d_x, d, h->final_norm, h->d_logits, c.vocab));
+    else
+        h->gemv.push_back(mk(PRO_RMSNORM, EPI_LOGITS, h->lm_head, c.vocab, nullptr, 0, nullptr, 0, d, h->d_x, d,
+                             h->final_norm, h->d_logits, c.vocab));
     for (int l = 0; l < c.n_layers; ++l) {
         h->gemv[4 * l + 0].p.trace_id = 1 + 5 * l;
         h->gemv[4 * l + 1].p.trace_id = 3 + 5 * l;
@@ -768,6 +884,14 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
     }
     h->gemv.back().p.trace_id = 5 * c.n_layers + 1;
     for (auto& pl : h->gemv) {
+        if (pl.w4) {
+            W4Gemv* g = const_cast<W4Gemv*>(pl.w4);   // the engine's own
+            g->trace_id = pl.p.trace_id;
+            if ((e = w4_gemv_plan(g, h->num_sms)) != cudaSuccess)
+                return fail(h, DEC_E_UNSUPPORTED, "no 4-bit kernel for rows=%d K=%d N=%d (%s)", rows, pl.p.K, pl.p.N,
+                            cudaGetErrorString(e));
+            continue;
+        }
         if ((e = gemv_plan(&pl, h->num_sms)) != cudaSuccess)
             return fail(h, DEC_E_UNSUPPORTED, "no GEMV kernel for rows=%d K=%d N=%d (%s)", rows, pl.p.K, pl.p.N,
                         cudaGetErrorString(e));
@@ -1100,6 +1224,9 @@ int dec_prefill_block(dec_handle* h, int32_t row, const int32_t* pages, const in
     const dec_config& c = h->cfg;
     if (c.weight_dtype != DEC_DTYPE_BF16 || c.kv_dtype == DEC_DTYPE_F32)
         return fail(h, DEC_E_UNSUPPORTED, "the block prefill needs bf16 weights and bf16 or e4m3 K/V");
+    for (int l = 0; l < c.n_layers; ++l)
+        if (h->lw4[l][1].codes)
+            return fail(h, DEC_E_UNSUPPORTED, "the block prefill needs layers in bf16, not in 4 bits (dec_prefill takes them)");
     PrefillArgs a{};
     a.L = c.n_layers; a.d = c.d_model; a.Hq = c.n_heads; a.Hkv = c.n_kv_heads; a.hd = c.head_dim;
     a.F = c.ffn_hidden; a.cap = h->cap; a.eps = (float)c.rms_eps;
@@ -1384,7 +1511,7 @@ int dec_launch_kernel(dec_handle* h, int32_t index, int32_t pdl, int64_t* bytes)
     } else if (index == 5 * L + 1) {
         const GemvPlan& g = h->gemv.back();
         e = gemv_launch(g, h->stream, pdl != 0);
-        b = (int64_t)g.p.N * g.p.K * wes + R * g.p.K * 4 + R * (int64_t)g.p.N * 4;
+        b = matrix_bytes(g, wes) + R * g.p.K * 4 + R * (int64_t)g.p.N * 4;
     } else {
         const int l = (index - 1) / 5, k = (index - 1) % 5;
         if (k == 1) {
@@ -1398,7 +1525,7 @@ int dec_launch_kernel(dec_handle* h, int32_t index, int32_t pdl, int64_t* bytes)
             const int64_t act_in = g.pro == PRO_SWIGLU ? 2 * g.p.K : g.p.K;
             const int64_t out_rw = g.epi == EPI_ADD ? 8 : 4;
             const int64_t n_out = g.epi == EPI_SWIGLU ? g.p.N / 2 : g.p.N;
-            b = (int64_t)g.p.N * g.p.K * wes + R * act_in * 4 + R * n_out * out_rw +
+            b = matrix_bytes(g, wes) + R * act_in * 4 + R * n_out * out_rw +
                 (g.pro == PRO_RMSNORM ? g.p.K * wes : 0);
         }
     }
@@ -1484,6 +1611,7 @@ int engine_fail(dec_handle* h, int code, const char* msg) {
 }
 int engine_device(const dec_handle* h) { return h->cfg.device; }
 void set_call_message(const char* msg) { g_init_msg = msg; }
+const char* call_message() { return g_init_msg.c_str(); }
 
 }  // namespace gd
 

@@ -100,6 +100,7 @@ cudaError_t gemv_plan(GemvPlan* plan, int num_sms) {
 }
 
 cudaError_t gemv_launch(const GemvPlan& plan, cudaStream_t s, bool pdl) {
+    if (plan.w4) return w4_gemv_launch(*plan.w4, s, pdl);
     if (plan.tc == 2) return gemv_box_launch(plan, s, pdl);
     const void* fn = pick(plan);
     if (!fn) return cudaErrorInvalidValue;

@@ -66,7 +66,10 @@ struct GemvParams {
     int trace_id;
 };
 
+struct W4Gemv;
 struct GemvPlan {
+    const W4Gemv* w4 = nullptr;   // matrices in 4 bits: the plan that runs (w4_gemv.cu), owned by the engine; p still says
+                                  // the shape, and nothing else below is used
     int wtype, pro, epi, nr, cpl;
     int tc;                // 1: tensor-core GEMV (gemv_tc.cu), 2: box-streamed tensor-core GEMV (gemv_tma.cu)
     alignas(64) unsigned char tma_maps[3 * 128];   // tc == 2: one TMA tensor map per weight segment
@@ -182,6 +185,8 @@ struct W4Matrix {              // a dec_w4_weight that passed its checks
     const void* scales;        // [n, k / group] bf16
     int n, k, group;
 };
+// a weight's checks: DEC_OK, or a status and the calling thread's message
+int w4_check(const char* what, const dec_w4_weight* w, W4Matrix* out);
 cudaError_t w4_quantize_launch(const W4Matrix& w, const void* src, long long stride, bool f32, int num_sms, cudaStream_t s);
 cudaError_t w4_values_launch(const W4Matrix& w, void* dst, long long stride, bool f32, int num_sms, cudaStream_t s);
 // out[t, n] = residual[t, n] + sum_k W[n, k] a[t, k] over up to three matrices of one k and group, stacked; with glu, over a
@@ -443,5 +448,6 @@ int engine_fail(dec_handle* h, int code, const char* msg);
 int engine_device(const dec_handle* h);
 // the message that dec_last_error(NULL) gives on this thread
 void set_call_message(const char* msg);
+const char* call_message();
 
 }  // namespace gd

@@ -52,7 +52,10 @@ int sms_of(int device, int* n) {
     return refuse(DEC_E_CUDA, "device %d: %s", device, cudaGetErrorString(e));
 }
 
-int check_weight(const char* what, const dec_w4_weight* w, W4Matrix* out) {
+}  // namespace
+
+namespace gd {
+int w4_check(const char* what, const dec_w4_weight* w, W4Matrix* out) {
     if (!w) return refuse(DEC_E_INVALID, "%s is NULL", what);
     if (!w->codes || !w->scales) return refuse(DEC_E_INVALID, "%s: codes and scales are required", what);
     if (!aligned(w->codes, 16) || !aligned(w->scales, 2))
@@ -67,6 +70,9 @@ int check_weight(const char* what, const dec_w4_weight* w, W4Matrix* out) {
     *out = W4Matrix{w->codes, w->scales, w->n, w->k, w->group};
     return DEC_OK;
 }
+}  // namespace gd
+
+namespace {
 
 int check_dtype(const char* what, int dtype, bool* f32) {
     if (dtype != DEC_DTYPE_F32 && dtype != DEC_DTYPE_BF16)
@@ -95,11 +101,11 @@ int check_values(const char* what, const void* p, int64_t stride, int64_t cols, 
 int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* c, W4Call* p) {
     int rc;
     *p = W4Call{};
-    if ((rc = check_weight(glu ? "gate" : "w", w, &p->w[0])) != DEC_OK) return rc;
+    if ((rc = w4_check(glu ? "gate" : "w", w, &p->w[0])) != DEC_OK) return rc;
     p->nw = 1;
     p->glu = glu;
     if (glu) {
-        if ((rc = check_weight("up", up, &p->w[1])) != DEC_OK) return rc;
+        if ((rc = w4_check("up", up, &p->w[1])) != DEC_OK) return rc;
         if (up->n != w->n || up->k != w->k || up->group != w->group || up->device != w->device)
             return refuse(DEC_E_INVALID, "gate and up must have one shape, group and device");
         p->nw = 2;
@@ -200,7 +206,7 @@ int dec_w4_quantize(const dec_w4_weight* w, const void* src, int64_t src_stride,
     W4Matrix m;
     bool f32;
     int rc, sms;
-    if ((rc = check_weight("w", w, &m)) != DEC_OK) return rc;
+    if ((rc = w4_check("w", w, &m)) != DEC_OK) return rc;
     if ((rc = check_dtype("dtype", dtype, &f32)) != DEC_OK) return rc;
     if ((rc = check_rows("src", src, src_stride, w->k, f32)) != DEC_OK) return rc;
     OnDevice on(w->device);
@@ -213,7 +219,7 @@ int dec_w4_dequantize(const dec_w4_weight* w, void* dst, int64_t dst_stride, int
     W4Matrix m;
     bool f32;
     int rc, sms;
-    if ((rc = check_weight("w", w, &m)) != DEC_OK) return rc;
+    if ((rc = w4_check("w", w, &m)) != DEC_OK) return rc;
     if ((rc = check_dtype("dtype", dtype, &f32)) != DEC_OK) return rc;
     if ((rc = check_rows("dst", dst, dst_stride, w->k, f32)) != DEC_OK) return rc;
     OnDevice on(w->device);

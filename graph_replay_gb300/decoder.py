@@ -15,6 +15,7 @@ import numpy as np
 import torch
 
 from . import _binding as B
+from .w4 import W4Weight
 
 _ROLE = {"attn_norm": B.DEC_W_ATTN_NORM, "wq": B.DEC_W_Q, "wk": B.DEC_W_K, "wv": B.DEC_W_V, "wo": B.DEC_W_O,
          "ffn_norm": B.DEC_W_FFN_NORM, "wg": B.DEC_W_GATE, "wu": B.DEC_W_UP, "wd": B.DEC_W_DOWN}
@@ -71,7 +72,10 @@ class Decoder:
         self.h = B.dec_init(cfg)
         self._weights = weights   # borrowed device memory must outlive the handle
         try:
-            B.dec_load_weights(self.h, self._bindings(weights))
+            plain, w4 = self._bindings(weights)
+            B.dec_load_weights(self.h, plain)
+            if w4:
+                B.dec_load_w4(self.h, w4)
             B.dec_set_strategy(self.h, B.DEC_STRATEGY_PERSISTENT if strategy == "persistent" else B.DEC_STRATEGY_GRAPH)
             # "cap": the constant-shape sweep of [0, cap); "pos": stop at the tile holding pos (same results)
             B.dec_set_kv_sweep(self.h, B.DEC_SWEEP_POS if kv_sweep == "pos" else B.DEC_SWEEP_CAP)
@@ -100,9 +104,13 @@ class Decoder:
         self._nf = np.empty(rows, dtype=np.uint8)
 
     def _bindings(self, w: dict):
-        out = []
+        """The weights by role: tensors, and matrices in 4 bits (W4Weight)."""
+        out, w4 = [], []
 
-        def add(role, layer, t: torch.Tensor):
+        def add(role, layer, t):
+            if isinstance(t, W4Weight):
+                w4.append(B.dec_w4_binding(role, layer, t._c))
+                return
             if not t.is_cuda or not t.is_contiguous():
                 raise ValueError("weights must be contiguous CUDA tensors")
             rows = t.shape[0]
@@ -115,7 +123,7 @@ class Decoder:
         for l, lw in enumerate(w["layers"]):
             for name, role in _ROLE.items():
                 add(role, l, lw[name])
-        return out
+        return out, w4
 
     def _after_torch(self) -> None:
         """Order the handle's stream after work torch queued on its current stream

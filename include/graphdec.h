@@ -202,6 +202,17 @@ int dec_init(const dec_config *cfg, dec_handle **out);
  * place: nothing is copied. */
 int dec_load_weights(dec_handle *h, const dec_weight *w, size_t n);
 
+struct dec_w4_binding;
+
+/* Bind `n` matrices in 4 bits by role (the format is at dec_w4_weight below):
+ * Q, K, V, O, GATE, UP and DOWN of a layer, all seven or none, and LM_HEAD (layer
+ * -1).  A later binding of a role replaces an earlier one of either kind.  Norm
+ * gains and embeddings stay in weight_dtype.  Q, K and V of a layer have one group,
+ * and so have GATE and UP.  Read in place like the others; the step's products are
+ * dec_w4_linear's and dec_w4_glu's.  DEC_STRATEGY_GRAPH only, and no
+ * dec_prefill_block (DEC_E_UNSUPPORTED there; dec_prefill takes them). */
+int dec_load_w4(dec_handle *h, const struct dec_w4_binding *w, size_t n);
+
 /* Device bytes that dec_capture needs for this shape (KV store, slots,
  * activations, attention partials, RoPE table): the preallocated Storage::State
  * buffers of capacity cap per layer plus the step's intermediates ("Execution",
@@ -577,7 +588,8 @@ int dec_kv8_workspace(const dec_kv8_cache *cache, const dec_kv8_batch *batch, co
  * Like dec_kv8_* these calls take no handle, only launch kernels on the caller's
  * stream (NULL: the legacy default stream), neither wait nor allocate, and may be
  * recorded into a graph.  The current device is put back before they return.
- * Messages: dec_last_error(NULL).
+ * Messages: dec_last_error(NULL).  A capture takes such matrices through
+ * dec_load_w4.
  *   group   32, 64 or 128; k a multiple of it, at most 2^20
  *   n       >= 1, n * k <= 2^33 */
 typedef struct dec_w4_weight {
@@ -586,6 +598,13 @@ typedef struct dec_w4_weight {
     int32_t n, k, group;
     int32_t device;              /* CUDA device ordinal of all of it */
 } dec_w4_weight;
+
+/* A matrix of a capture (dec_load_w4). */
+typedef struct dec_w4_binding {
+    int32_t role;                /* dec_role */
+    int32_t layer;               /* 0 .. n_layers-1; -1 for LM_HEAD */
+    dec_w4_weight w;             /* must outlive the handle */
+} dec_w4_binding;
 
 /* Store src [n, k] (f32 or bf16, rows src_stride elements apart, 16-byte aligned
  * like the stride) into w.  Over each group scale = bf16(max |x| / 7) and code =
