@@ -27,7 +27,7 @@ const void* kernel_of(const W4Gemv& g) {
 size_t smem_of(const W4Gemv& g) {
     const int P = g.c.parts(), chunks = (g.c.k() + 127) / 128, most = (chunks + g.ks - 1) / g.ks;
     const size_t ring = (size_t)WG_WARPS * g.stages * WG_STEP, x = (size_t)most * g.block * P * 256;
-    const size_t f = ((size_t)most * g.block + 3) / 4 * 16 + (size_t)most * (128 / g.c.group()) * g.block * P * sizeof(float);
+    const size_t f = ((size_t)most * g.block + 3) / 4 * 16 + (size_t)most * (128 / g.c.group()) * g.block * sizeof(float);
     const size_t sums = g.ks > 1 ? sizeof(float) * (g.c.glu ? 2 : 1) * g.block * g.rows : 0;
     return ring + x + f + sums + sizeof(float) * g.bufs * WG_WARPS * wg_tokens(P, blocks_of(g)) * WG_PITCH;
 }
@@ -70,8 +70,8 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     g->block = c.tokens < most ? c.tokens : most;
     // rows evenly over the SMs, at least 8 a CTA: a tile has 16, and a CTA of fewer saves nothing
     const int gr = c.glu ? 16 : 32;
-    // CTAs along k: the fewest (a cluster: 1, 2, 4 or 8) whose shared memory holds the activations beside a ring of four,
-    // three or two steps
+    // CTAs along k: the fewest (a cluster: 1, 2, 4 or 8) whose shared memory holds the activations beside a ring of four
+    // steps or two
     for (g->ks = 1; g->ks <= 8 && g->ks <= chunks; g->ks *= 2) {
         const int places = clusters(g->ks, num_sms);
         g->rows = (N + places - 1) / places;
@@ -84,7 +84,8 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
         while (g->wk > 1 && (own < g->wk || (groups >= 2 * (WG_WARPS / g->wk) && own < 8 * g->wk))) g->wk /= 2;
         const int sets = WG_WARPS / g->wk, iters = (groups + sets - 1) / sets;
         g->bufs = iters > 1 ? 2 : 1;
-        for (g->stages = WG_STAGES; g->stages > 2 && smem_of(*g) > SMEM_MOST; --g->stages) {}
+        g->stages = WG_STAGES;
+        if (smem_of(*g) > SMEM_MOST) g->stages = 2;
         if (smem_of(*g) <= SMEM_MOST) break;
     }
     if (g->ks > 8 || g->ks > chunks) return cudaErrorInvalidValue;

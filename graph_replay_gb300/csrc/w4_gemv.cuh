@@ -60,15 +60,13 @@ struct W4GemvArgs {
     int trace_id;
 };
 
-// d = a b + (c0, c1, c0, c1): the sum's start depends on the column only
-__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1,
-                                          float c0, float c1) {
-    asm(   // not volatile: chains of different groups and tiles may be mixed
-       
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%11,%10,%11};\n"
+// d = a b
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
+// d += a b
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
     asm(
@@ -77,8 +75,8 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 // The pairs (j, j + 4) of a word as fp16 subnormals: with its sign bit turned over a code is u = q + 8, 0 .. 15, and bits
-// 0-3 of a half stand for u 2^-24, bits 4-7 for u 2^-20.  Nothing has to be converted; the sums start at -8 times the
-// activations' sum, and the activations of the second and fourth pair are 2^-4 of the others
+// 0-3 of a half stand for u 2^-24, bits 4-7 for u 2^-20.  Nothing has to be converted; 8 times the activations' sum is taken
+// off behind a group's products, and the activations of the second and fourth pair are 2^-4 of the others
 struct W4Sign {
     uint32_t low, high;        // in registers: as immediates they would cost an instruction more at each use
     __device__ __forceinline__ W4Sign() {
@@ -93,17 +91,14 @@ __device__ __forceinline__ void w4_raw(uint32_t w, const W4Sign& k, uint32_t (&p
     pair[2] = w4_and_xor<0x000f000fu>(v, k.low);
     pair[3] = w4_and_xor<0x00f000f0u>(v, k.high);
 }
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, unsigned bytes) {   // the rest of 16 bytes is zero
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-__device__ __forceinline__ void cp_wait(int left) {   // all but the newest `left` groups have landed
-    if (left >= 3) asm volatile("cp.async.wait_group 3;" ::: "memory");
-    else if (left == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
-    else if (left == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+__device__ __forceinline__ void cp_wait(bool four) {   // with a ring of four steps (or two) the oldest group has landed
+    if (four) asm volatile("cp.async.wait_group 2;" ::: "memory");
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-
 // all threads of the cluster's CTAs; what they wrote to shared memory is visible to all behind it
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -148,8 +143,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     unsigned char* ring = smem + (size_t)warp * ring_bytes;
     unsigned char* xs = smem + (size_t)WG_WARPS * ring_bytes;                // [chunk][4][cols][64 bytes]
     float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14 + 12)
-    float* cs = fs + (((ch1 - ch0) * p.block + 3) & ~3);                     // [chunk][NG][cols]: where a group's sums start
-    float* red = cs + (ch1 - ch0) * NG * cols;                               // [bufs][warp][MT][WG_PITCH]
+    float* cs = fs + (((ch1 - ch0) * p.block + 3) & ~3);                     // [chunk][NG][block]: what a group's sums are off
+    float* red = cs + (ch1 - ch0) * NG * p.block;                             // [bufs][warp][MT][WG_PITCH]
     float* sums = red + p.bufs * WG_WARPS * MT * WG_PITCH;                   // ks > 1: [1 or 2][block][rows], read by the cluster
     const uint32_t ring_at = smem_u32(ring);
 
@@ -171,16 +166,16 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const unsigned cpitch = (unsigned)p.K >> 1, spitch = (unsigned)(p.K / G) * 2u;
     struct Rows {                              // of a row group: rows g, g + 8 of tile 0, then of tile 1
         unsigned c[4], s[4];                   // offsets of their codes and scales
-        unsigned on;                           // bit i: row i is one of the CTA's
+        unsigned live[4];                      // 16 where row i is one of the CTA's, else 0
         unsigned seg;                          // W4_STACK: bits 2i, 2i + 1: the matrix that row i lies in
     };
     auto rows_of = [&](int it, Rows& r) {
         const int base = row0 + (it * sets + set) * GR + g;
-        r.on = r.seg = 0;
+        r.seg = 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int at = base + (GLU ? 8 * (i & 1) : 8 * i);
-            r.on |= (at < row1 ? 1u : 0u) << i;
+            r.live[i] = at < row1 ? 16u : 0u;
             int n = min(at, row1 - 1);         // scales are read of any row
             if (KIND == W4_STACK) {
                 const int sg = (n >= p.end[0]) + (n >= p.end[1]);
@@ -211,13 +206,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     if (steps > 0) rows_of(0, ahead);
     auto copy_next = [&]() {
         if (a_left > 0) {
-            const bool in = a_at < cpitch;
+            const unsigned in = a_at < cpitch ? ~0u : 0u;
             const uint32_t dst = ring_at + a_slot + put;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 // (of rows behind the CTA's last and columns behind the row's nothing is read: zeros)
                 cp_async16(dst + (uint32_t)((i >> 1) * 1024 + (i & 1) * 512), codes_of(ahead, i) + (size_t)(ahead.c[i] + a_at),
-                           in && (ahead.on >> i & 1u));
+                           in & ahead.live[i]);
             }
             --a_left;
             a_slot = a_slot + WG_STEP == ring_bytes ? 0u : a_slot + WG_STEP;
@@ -279,16 +274,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             const float up = w4_up(e), up4 = up * 0.0625f;
             x.x *= up; x.y *= up4; x.z *= up; x.w *= up4;      // columns j of a word meet codes times 2^-24, 2^-20, ...
             const int ci = warp + cj * WG_WARPS;
+            float sum = 0.f;                   // of all parts
 #pragma unroll
             for (int part = 0; part < P; ++part) {
                 const uint32_t a01 = w4_pack_half(x.x, x.y), a23 = w4_pack_half(x.z, x.w);
                 const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&a01));
                 const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&a23));
-                float sum = (f01.x + f23.x) + 16.0f * (f01.y + f23.y);
-#pragma unroll
-                for (int o = 1; o < G / 4; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                sum += (f01.x + f23.x) + 16.0f * (f01.y + f23.y);
                 const int col = cr * P + part;
-                if (lane % (G / 4) == 0) cs[(ci * NG + lane / (G / 4)) * cols + col] = sum * -4.76837158203125e-07f;   // -8 2^-24
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a01 : a23, 1);
                 const uint32_t lo = odd ? got : a01, hi = odd ? a23 : got;     // columns j and j + 4 of the word
                 const uint2 f = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
@@ -298,6 +291,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 x.x = isfinite(x.x) ? x.x : 0.f; x.y = isfinite(x.y) ? x.y : 0.f;
                 x.z = isfinite(x.z) ? x.z : 0.f; x.w = isfinite(x.w) ? x.w : 0.f;
             }
+#pragma unroll
+            for (int o = 1; o < G / 4; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (lane % (G / 4) == 0) cs[(ci * NG + lane / (G / 4)) * p.block + cr] = sum * -4.76837158203125e-07f;   // -8 2^-24
             if (lane == 0) fs[ci * p.block + cr] = w4_down(e) * 4096.0f;   // half of the codes' 2^-24; the rest with the norm
             if (++cj == nc) {
                 if (p.gain) {
@@ -385,7 +381,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const W4Sign kc;
     unsigned slot = 0;                         // of this step, in bytes
     const unsigned b_hop = (unsigned)p.wk * 4 * cols * 64, f_hop = (unsigned)(p.wk * p.block),
-                   c_hop = (unsigned)(p.wk * NG * cols);
+                   c_hop = (unsigned)(p.wk * NG * p.block);
     for (int it = 0; it < iters; ++it) {
         // the residual of the thread's first output, under the products
         float res = 0.f;
@@ -402,15 +398,16 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < AC; ++c) acc[a][b][c] = 0.f;
         const int base = row0 + (it * sets + set) * GR;
-        unsigned b_at[NB], f_at[NB][P == 2 ? 1 : 2], c_at[NB][2];   // of the step's chunk
+        unsigned b_at[NB], f_at[NB][P == 2 ? 1 : 2], c_at[NB][P == 2 ? 1 : 2];   // of the step's chunk
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             b_at[b] = (unsigned)slice * 4 * cols * 64 + (unsigned)min(b * 8 + g, cols - 1) * 64 + t * 16;
 #pragma unroll
-            for (int c = 0; c < (P == 2 ? 1 : 2); ++c)
-                f_at[b][c] = (unsigned)(slice * p.block + min(P == 2 ? b * 4 + t : b * 8 + 2 * t + c, p.block - 1));
-#pragma unroll
-            for (int c = 0; c < 2; ++c) c_at[b][c] = (unsigned)(slice * NG * cols + min(b * 8 + 2 * t + c, cols - 1));
+            for (int c = 0; c < (P == 2 ? 1 : 2); ++c) {
+                const int r = min(P == 2 ? b * 4 + t : b * 8 + 2 * t + c, p.block - 1);
+                f_at[b][c] = (unsigned)(slice * p.block + r);
+                c_at[b][c] = (unsigned)(slice * NG * p.block + r);
+            }
         }
         auto one_step = [&](int i, const uint32_t (&use)[4], uint32_t (&fill)[4]) {
             if (i + 1 < mine) {
@@ -419,7 +416,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 rows_of(it + 1, next);
                 scales_of(next, g_first, fill);
             }
-            cp_wait(S - 2);
+            cp_wait(S == 4);
             __syncwarp();
             copy_next();                       // into the slot that the step before read
             const unsigned char* st = ring + slot;
@@ -484,8 +481,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     for (int b = 0; b < NB; ++b)
 #pragma unroll
                         for (int tile = 0; tile < 2; ++tile) {
-                            if (c == gi * PER) mma_first(d[tile][b], pa[tile][0], pb[tile][0], pa[tile][1], pb[tile][1], bf[b].x, bf[b].y,
-                                                         cs[c_at[b][0] + (unsigned)(gi * cols)], cs[c_at[b][1] + (unsigned)(gi * cols)]);
+                            if (c == gi * PER) mma_first(d[tile][b], pa[tile][0], pb[tile][0], pa[tile][1], pb[tile][1], bf[b].x, bf[b].y);
                             else mma_f16(d[tile][b], pa[tile][0], pb[tile][0], pa[tile][1], pb[tile][1], bf[b].x, bf[b].y);
                         }
 #pragma unroll
@@ -494,6 +490,11 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                         for (int tile = 0; tile < 2; ++tile)
                             mma_f16(d[tile][b], pa[tile][2], pb[tile][2], pa[tile][3], pb[tile][3], bf[b].z, bf[b].w);
                 }
+                float off[NB][P == 2 ? 1 : 2];
+#pragma unroll
+                for (int b = 0; b < NB; ++b)
+#pragma unroll
+                    for (int c = 0; c < (P == 2 ? 1 : 2); ++c) off[b][c] = cs[c_at[b][c] + (unsigned)(gi * p.block)];
 #pragma unroll
                 for (int tile = 0; tile < 2; ++tile) {
                     const uint32_t sw = NG > 1 ? __shfl_sync(0xffffffffu, sc[tile], (lane & 28) | gi) : sc[tile];
@@ -502,14 +503,15 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     for (int b = 0; b < NB; ++b) {
                         const float* e = d[tile][b];
                         float* o = acc[tile][b];
+                        constexpr int L = P == 2 ? 0 : 1;
                         if (P == 2) {          // columns 2t and 2t + 1 are the two parts of one token
-                            o[0] = fmaf((e[0] + e[1]) * f[b][0], s0, o[0]);
-                            o[1] = fmaf((e[2] + e[3]) * f[b][0], s1, o[1]);
+                            o[0] = fmaf((e[0] + e[1] + off[b][0]) * f[b][0], s0, o[0]);
+                            o[1] = fmaf((e[2] + e[3] + off[b][0]) * f[b][0], s1, o[1]);
                         } else {
-                            o[0] = fmaf(e[0] * f[b][0], s0, o[0]);
-                            o[AC == 4 ? 1 : 0] = fmaf(e[1] * f[b][P == 2 ? 0 : 1], s0, o[AC == 4 ? 1 : 0]);
-                            o[AC == 4 ? 2 : 0] = fmaf(e[2] * f[b][0], s1, o[AC == 4 ? 2 : 0]);
-                            o[AC == 4 ? 3 : 0] = fmaf(e[3] * f[b][P == 2 ? 0 : 1], s1, o[AC == 4 ? 3 : 0]);
+                            o[0] = fmaf((e[0] + off[b][0]) * f[b][0], s0, o[0]);
+                            o[AC == 4 ? 1 : 0] = fmaf((e[1] + off[b][L]) * f[b][L], s0, o[AC == 4 ? 1 : 0]);
+                            o[AC == 4 ? 2 : 0] = fmaf((e[2] + off[b][0]) * f[b][0], s1, o[AC == 4 ? 2 : 0]);
+                            o[AC == 4 ? 3 : 0] = fmaf((e[3] + off[b][L]) * f[b][L], s1, o[AC == 4 ? 3 : 0]);
                         }
                     }
                 }
@@ -517,8 +519,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 b_at[b] += b_hop;
-                c_at[b][0] += c_hop;
-                c_at[b][1] += c_hop;
+#pragma unroll
+                for (int c = 0; c < (P == 2 ? 1 : 2); ++c) c_at[b][c] += c_hop;
             }
         };
         for (int i = 0; i < mine; i += 2) {
