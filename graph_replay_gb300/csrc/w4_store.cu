@@ -3,10 +3,11 @@
 // quantize: over each group of 32, 64 or 128 columns of a row
 //   s = bf16(max |w| / 7),  q = w / s to the nearest whole number (ties to even),
 // so |q| <= 7; s < 2^-100: s = 0 and q = 0; a NaN or an infinity in the group:
-// s = NaN.  A lane holds 8 columns, so a group is 4, 8 or 16 lanes of a warp and
+// s = NaN.  A lane holds 16 columns, so a group is 2, 4 or 8 lanes of a warp and
 // its largest value needs no shared memory.  The quotient is found without a
-// division: q0 = rint(w * (1 / s)) is at most one off, and w - q0 s is exact in one
-// fused multiply-add, so comparing it with s / 2 decides every case, ties too.
+// division: w * (1 / s) to the nearest whole number is at most one off, and w - q s is
+// exact in one fused multiply-add, so comparing it with s / 2 decides every case, ties
+// too.
 // Bound by memory: 2 or 4 bytes a weight read, 0.5 + 2 / group written.
 #include "w4.cuh"
 
@@ -28,51 +29,52 @@ __device__ __forceinline__ void load8(const void* p, size_t i, float (&v)[8]) {
     }
 }
 
+// 1.5 * 2^23: a sum with it is a whole number in fp32 (to the nearest, ties to even), whose low bits are the number's in
+// two's complement.  So no conversion between integers and floats is needed, which run at a quarter of the rate
+constexpr float MAGIC = 12582912.0f;
+
 __device__ __forceinline__ uint32_t code8(const float (&v)[8], float s, float inv) {
+    const float half = 0.5f * s;
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        float q = rintf(v[i] * inv);
-        const float r = fmaf(-q, s, v[i]);           // exact: |r| < s
-        const float d = 2.0f * fabsf(r) - s;         // exact in sign: both are multiples of one power of two
-        const float to = r > 0.0f ? 1.0f : -1.0f;
-        const bool odd = (int)q & 1;
-        if (d > 0.0f || (d == 0.0f && odd)) q += to;
-        w |= ((uint32_t)(int)q & 15u) << (4 * i);
+        float m = fmaf(v[i], inv, MAGIC);            // of w * (1 / s): right, or one off next to a border
+        const float r = fmaf(MAGIC - m, s, v[i]);    // w - q s, exact
+        // beyond half a step, or on the border at an odd code: one further
+        const bool odd = __float_as_uint(m) & 1u;
+        if (fabsf(r) > half || (fabsf(r) == half && odd)) m += copysignf(1.0f, r);
+        w |= (__float_as_uint(m) & 15u) << (4 * i);
     }
     return w;
 }
 
-// one item: 8 columns; n * k / 8 items in all, items of a row side by side
+// one item: 16 columns (so that a group's scale is found by few lanes); n * k / 16 items in all, items of a row side by side
 template <bool F32>
-__global__ void __launch_bounds__(QT) k_w4_quantize(const void* __restrict__ src, long long stride, uint32_t* __restrict__ codes,
-                                                    __nv_bfloat16* __restrict__ scales, int items, FastDiv k8, int lanes) {
+__global__ void __launch_bounds__(QT) k_w4_quantize(const void* __restrict__ src, long long stride, uint2* __restrict__ codes,
+                                                    __nv_bfloat16* __restrict__ scales, int items, FastDiv k16, int lanes) {
     const unsigned step = gridDim.x * QT;   // items < 2^31: no sum below wraps
     const int lane = threadIdx.x & 31;
-    for (unsigned i0 = blockIdx.x * QT + threadIdx.x; i0 - lane < (unsigned)items; i0 += step) {
-        const bool live = i0 < (unsigned)items;
-        const int i = live ? (int)i0 : items - 1;
-        const int row = k8.of(i);
-        const int c = i - row * (int)k8.d;
-        float v[8];
-        load8<F32>(src, (size_t)row * stride + (size_t)c * 8, v);
+    for (unsigned first = blockIdx.x * QT + threadIdx.x; first - lane < (unsigned)items; first += step) {
+        const int i = (int)min(first, (unsigned)items - 1u);
+        const int row = k16.of(i);
+        const size_t at = (size_t)row * stride + (size_t)(i - row * (int)k16.d) * 16;
+        float a[8], b[8];
+        load8<F32>(src, at, a);
+        load8<F32>(src, at + 8, b);
         uint32_t top = 0;   // the bits of |x| order like the values, with infinity and NaN above them
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+        for (int e = 0; e < 8; ++e) top = max(top, max(__float_as_uint(a[e]) & 0x7fffffffu, __float_as_uint(b[e]) & 0x7fffffffu));
         for (int o = 1; o < lanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
         const bool bad = top >= 0x7f800000u;
         __nv_bfloat16 sb = __float2bfloat16_rn(__fdiv_rn(__uint_as_float(top), 7.0f));
-        float s = __bfloat162float(sb);
+        const float s = __bfloat162float(sb);
         const bool none = bad || s < 7.8886090522101181e-31f;   // 2^-100
-        if (none) {
-            sb = __ushort_as_bfloat16(bad ? 0x7fc0 : 0);
-            s = 1.0f;
-        }
-        uint32_t w = 0;
-        if (!none) w = code8(v, s, __frcp_rn(s));
-        if (live) {
-            codes[i] = w;
-            if (lane % lanes == 0) scales[i / lanes] = sb;   // groups of all rows follow one another
+        const float inv = __frcp_rn(none ? 1.0f : s);
+        const uint32_t wa = code8(a, none ? 1.0f : s, inv), wb = code8(b, none ? 1.0f : s, inv);
+        if (first < (unsigned)items) {
+            codes[i] = none ? make_uint2(0u, 0u) : make_uint2(wa, wb);
+            // groups of all rows follow one another
+            if ((lane & (lanes - 1)) == 0) scales[(unsigned)i / (unsigned)lanes] = none ? __ushort_as_bfloat16(bad ? 0x7fc0 : 0) : sb;
         }
     }
 }
@@ -86,10 +88,11 @@ __global__ void __launch_bounds__(QT) k_w4_values(const uint32_t* __restrict__ c
         const int row = k8.of((int)i);
         const int c = (int)i - row * (int)k8.d;
         const uint32_t w = codes[i];
-        const float s = __bfloat162float(scales[i / lanes]);
+        const float s = __bfloat162float(scales[i / (unsigned)lanes]);
         float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (float)((int)(w << (28 - 4 * e)) >> 28) * s;
+        for (int e = 0; e < 8; ++e)   // 2^23 + (q + 8), less 2^23 + 8
+            v[e] = (__uint_as_float(((w >> (4 * e) & 15u) ^ 0x4b000008u)) - 8388616.0f) * s;
         const size_t at = (size_t)row * stride + (size_t)c * 8;
         if (F32) {
             float4* o = reinterpret_cast<float4*>(reinterpret_cast<float*>(dst) + at);
@@ -116,12 +119,12 @@ int grid_for(int items, int num_sms) {
 }  // namespace
 
 cudaError_t w4_quantize_launch(const W4Matrix& w, const void* src, long long stride, bool f32, int num_sms, cudaStream_t s) {
-    const int items = w.n * (w.k / 8);
-    const int grid = grid_for(items, num_sms);
-    uint32_t* codes = reinterpret_cast<uint32_t*>(const_cast<void*>(w.codes));
+    const int items = w.n * (w.k / 16), grid = grid_for(items, num_sms), lanes = w.group / 16;
+    const FastDiv k16((unsigned)(w.k / 16));
+    uint2* codes = reinterpret_cast<uint2*>(const_cast<void*>(w.codes));
     __nv_bfloat16* scales = reinterpret_cast<__nv_bfloat16*>(const_cast<void*>(w.scales));
-    if (f32) k_w4_quantize<true><<<grid, QT, 0, s>>>(src, stride, codes, scales, items, FastDiv((unsigned)(w.k / 8)), w.group / 8);
-    else k_w4_quantize<false><<<grid, QT, 0, s>>>(src, stride, codes, scales, items, FastDiv((unsigned)(w.k / 8)), w.group / 8);
+    if (f32) k_w4_quantize<true><<<grid, QT, 0, s>>>(src, stride, codes, scales, items, k16, lanes);
+    else k_w4_quantize<false><<<grid, QT, 0, s>>>(src, stride, codes, scales, items, k16, lanes);
     return cudaGetLastError();
 }
 
