@@ -37,7 +37,6 @@ DEC_STRATEGY_GRAPH = 0
 DEC_STRATEGY_PERSISTENT = 1
 DEC_ACT_SILU = 0
 DEC_ACT_GELU_TANH = 1
-DEC_W4_COUNTER_BYTES = 65536
 DEC_SWEEP_CAP = 0
 DEC_SWEEP_POS = 1
 

@@ -224,15 +224,15 @@ struct W4Gemv {                // how w4_gemv.cu runs a call of few tokens
     unsigned long long* trace;
     int trace_id;
 };
+int w4_clusters(int ks, int num_sms);   // clusters of ks CTAs, one CTA an SM, that run at a time
 cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms);
 cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl);
 struct W4Gemm {                // how w4_gemm.cu runs a call of many tokens
     W4Call c;                  // nw == 1, or glu
     int nt;                    // tokens of a tile
-    int ks;                    // CTAs along k
+    int ks;                    // CTAs along k, a cluster
     int kp, steps;             // columns rounded up to 64; steps of 128
     void* ws;                  // w4_gemm_bytes()
-    unsigned* count;           // ks > 1: [tiles], zero between calls
 };
 cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms);
 size_t w4_gemm_bytes(const W4Gemm& g);

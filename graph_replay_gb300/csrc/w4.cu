@@ -150,9 +150,7 @@ int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const 
     return DEC_OK;
 }
 
-size_t round256(size_t n) { return (n + 255) / 256 * 256; }
-
-// how a call runs, and what of the workspace it uses behind the counters
+// how a call runs, and what it needs of workspace
 struct Plan {
     bool few;
     W4Gemv gemv;
@@ -166,7 +164,7 @@ cudaError_t plan_of(const W4Call& c, int sms, Plan* p) {
         p->gemm = W4Gemm{};
         p->gemm.c = c;
         const cudaError_t e = w4_gemm_plan(&p->gemm, sms);
-        p->bytes = DEC_W4_COUNTER_BYTES + round256(w4_gemm_bytes(p->gemm));
+        p->bytes = w4_gemm_bytes(p->gemm);
         return e;
     }
     p->gemv = W4Gemv{};
@@ -191,8 +189,7 @@ int run(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_
                       call->workspace ? call->workspace_bytes : (size_t)0, p.bytes);
     if (!aligned(call->workspace, 256)) return refuse(DEC_E_INVALID, "workspace must be 256-byte aligned");
     if (!p.few) {
-        p.gemm.count = (unsigned*)call->workspace;
-        p.gemm.ws = (char*)call->workspace + DEC_W4_COUNTER_BYTES;
+        p.gemm.ws = call->workspace;
         return launched(w4_gemm_launch(p.gemm, (cudaStream_t)stream), what);
     }
     return launched(w4_gemv_launch(p.gemv, (cudaStream_t)stream, false), what);

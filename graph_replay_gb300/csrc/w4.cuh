@@ -64,6 +64,19 @@ __device__ __forceinline__ uint32_t w4_pack_half(float lo, float hi) {
     return r;
 }
 
+// all threads of the cluster's CTAs; what they wrote to shared memory is visible to all behind it
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// the value at p's place in the shared memory of the cluster's CTA `rank`
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+    uint32_t at;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+    return v;
+}
+
 // act(g) * u
 __device__ __forceinline__ float w4_glu(int act, float g, float u) {
     if (act == DEC_ACT_GELU_TANH) {

@@ -25,8 +25,9 @@
 // The tensor core cuts its fp32 sums off instead of rounding them.  For fp32 activations
 // the accumulators are therefore folded into registers every WM_FOLD steps (with rounding),
 // while the MMAs go on in a second pair.
-// Few tokens leave few tiles: then `ks` CTAs share the columns of a tile, leave their
-// sums in the workspace, and the last to arrive adds them in order.
+// Few tokens leave few tiles: then a cluster of `ks` CTAs shares the columns of a tile,
+// and each of them adds the sums of a part of the tokens from the others' shared memory,
+// in order.
 // Every wait is bounded; one that gives up sets FAULT_WAIT, and the CTA ends.
 #include <cuda.h>
 #include "w4.cuh"
@@ -41,6 +42,7 @@ constexpr int WM_THREADS = (WM_DQ + 4) * 32;
 constexpr int WM_CODES = 2 * 128 * 64;         // bytes of a codes stage: two tiles of 128 rows x 128 columns
 constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 3;
 constexpr int WM_SMEM = 200 * 1024;            // for both rings
+constexpr int WM_ROWS = 257;                   // of a split's sums of one token: 256, and one against bank conflicts
 constexpr int WM_FOLD = 2;                     // fp32 activations: steps of an accumulator
 
 // fp32 activations: stages of 64 columns (two parts), and accumulators of half as many tokens, in two pairs
@@ -58,8 +60,6 @@ struct WmParams {
     long long residual_stride, out_stride;
     int N, K, tokens, nt, ks, steps, sc, sx, sa, act, out_f32;
     bool wide;                 // scales can be read eight at a time
-    float* part;
-    unsigned* count;
     unsigned* err;
 };
 
@@ -159,13 +159,13 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     __shared__ __align__(8) uint64_t codes_full[WM_MAX_SC], codes_empty[WM_MAX_SC], x_full[WM_MAX_SX], x_empty[WM_MAX_SX];
     __shared__ __align__(8) uint64_t a_full[WM_MAX_SA], a_empty[WM_MAX_SA], d_full[2], d_empty[2];
     __shared__ uint32_t tmem;
-    __shared__ int aborted, last_s;
+    __shared__ int aborted;
     __shared__ int row_e[2][128];
     __shared__ float tok_f[128];
     volatile int* ab = &aborted;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int tile = blockIdx.x, blk = blockIdx.y, split = blockIdx.z;
+    const int split = blockIdx.x % p.ks, tile = blockIdx.x / p.ks, blk = blockIdx.y;
     const int row0 = tile * ROWS, tok0 = blk * p.nt, m = min(p.nt, p.tokens - tok0);
     const int s0 = (int)((long long)split * p.steps / p.ks), s1 = (int)((long long)(split + 1) * p.steps / p.ks);
     const int n = s1 - s0;                     // steps of this split, >= 1
@@ -477,20 +477,18 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                     if (e < count) o[(size_t)e * p.out_stride] = __float2bfloat16_rn(v[e]);
             }
         };
-        // Sums of 16 tokens from token c for this thread's row of its matrix.  Plain and split results go out from here; a
-        // gate's meet the up's in shared memory (the codes' ring: all copies have landed, all weights are made)
+        // Sums of 16 tokens from token c for this thread's row of its matrix.  Plain results go out from here; a gate's meet
+        // the up's in shared memory, and a split's those of the other CTAs (in the rings: all copies have landed, all
+        // weights are made, all products are done)
         constexpr int US = 129;                // of a token's 128 rows
         float* meet = reinterpret_cast<float*>(smem);            // [nt][US]
-        const size_t pitch = (size_t)p.N * (GLU ? 2 : 1);
         auto take16 = [&](int c, float (&v)[16]) {
             const int count = min(16, m - c);
 #pragma unroll
             for (int e = 0; e < 16; ++e) v[e] = e < count ? sized(v[e], tok_f[c + e]) : 0.f;
             if (p.ks > 1) {
-                float* o = p.part + ((size_t)split * p.tokens + tok0 + c) * pitch + (GLU ? mat * p.N : 0) + nn;
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (in && e < count) o[e * pitch] = v[e];
+                for (int e = 0; e < 16; ++e) meet[(c + e) * WM_ROWS + mat * 128 + r] = v[e];
             } else if (GLU) {
                 if (mat == 1) {
 #pragma unroll
@@ -542,42 +540,26 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 }
             }
         }
-        if (p.ks > 1) {
-            __threadfence();
-            named_sync(1, WM_DQ * 32);
-            if (tid == 0) {
-                unsigned* cnt = p.count + (size_t)blk * gridDim.x + tile;
-                const unsigned before = atomicAdd(cnt, 1u);
-                last_s = before == (unsigned)p.ks - 1u;
-                if (last_s) *cnt = 0u;         // ready for the next call
-            }
-            named_sync(1, WM_DQ * 32);
-            if (last_s) {
-                __threadfence();
-                // rows as before; gate/up: all four warpgroups take rows of the one output
-                for (int c = (GLU ? wg : h) * 16; in && c < m; c += GLU ? 64 : 32) {
-                    const int count = min(16, m - c);
-                    float v[16], u[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) v[e] = u[e] = 0.f;
-                    for (int w = 0; w < p.ks; ++w) {
-                        const float* o = p.part + ((size_t)w * p.tokens + tok0 + c) * pitch + nn;
-                        float b[16];
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) b[e] = e < count ? __ldcg(o + e * pitch) : 0.f;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] += b[e];
-                        if (GLU) {
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) b[e] = e < count ? __ldcg(o + e * pitch + p.N) : 0.f;
-#pragma unroll
-                            for (int e = 0; e < 16; ++e) u[e] += b[e];
-                        }
-                    }
-                    put16(c, count, v, u);
+    }
+    if (p.ks > 1) {
+        cluster_sync();
+        // the tokens of this CTA's part, a row a thread: the sums of all CTAs of the cluster, in their order
+        const float* sums = reinterpret_cast<const float*>(smem);
+        constexpr int OUT = GLU ? 128 : 256;   // output rows
+        const int r = tid % OUT, nn = row0 + r, t1 = (split + 1) * m / p.ks;
+        if (tid < WM_DQ * 32 && nn < p.N) {
+            for (int t = split * m / p.ks + tid / OUT; t < t1; t += WM_DQ * 32 / OUT) {
+                float res = 0.f;
+                if (!GLU && p.residual) res = w4_load1(p.residual, p.out_f32, (size_t)(tok0 + t) * p.residual_stride + nn);
+                float v = 0.f, u = 0.f;
+                for (int w = 0; w < p.ks; ++w) {
+                    v += ld_cluster(sums + t * WM_ROWS + r, w);
+                    if (GLU) u += ld_cluster(sums + t * WM_ROWS + 128 + r, w);
                 }
+                w4_store1(p.out, p.out_f32, (size_t)(tok0 + t) * p.out_stride + nn, GLU ? w4_glu(p.act, v, u) : v + res);
             }
         }
+        cluster_sync();                        // until the others have read this CTA's sums
     }
     fence_before();
     __syncthreads();
@@ -705,18 +687,18 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
     const int P = c.x_f32 ? 2 : 1, rows = c.glu ? 128 : 256;
     const int tiles = (c.n() + rows - 1) / rows, steps = (c.k() + 127) / 128;
     // Tokens of a tile and CTAs along k: the least time of the longest CTA, in clocks.  A step takes the tensor cores 8
-    // clocks a token and part, or the making and handing over of its weights 650; a CTA starts and ends in about 7000,
-    // and a split adds the writing and reading of its sums
+    // clocks a token and part, or the making and handing over of its weights 900; a CTA starts and ends in about 7000,
+    // and a split adds the joining of its sums
     double best = -1.0;
     const int least = (c.tokens + wm_tokens(P) - 1) / wm_tokens(P);
     for (int blocks = least; blocks <= least + 8; ++blocks) {
         const int nt = round_up((c.tokens + blocks - 1) / blocks, 16), used = (c.tokens + nt - 1) / nt;
-        for (int ks = 1; ks <= 16; ++ks) {
-            if (ks > 1 && (steps / ks < 2 || (long long)tiles * used > DEC_W4_COUNTER_BYTES / 4)) break;
-            const double waves = (double)(((long long)tiles * used * ks + num_sms - 1) / num_sms);
-            const double step = 8.0 * nt * P > 650.0 ? 8.0 * nt * P : 650.0;
-            const double t = waves * ((double)((steps + ks - 1) / ks) * step + 7000.0 + 16.0 * nt) +
-                             (ks > 1 ? 2500.0 + 16.0 * nt * ks : 0.0);
+        for (int ks = 1; ks <= 8; ks *= 2) {
+            if (ks > 1 && steps / ks < 2) break;
+            const long long places = ks == 1 ? num_sms : w4_clusters(ks, num_sms);
+            const double waves = (double)(((long long)tiles * used + places - 1) / places);
+            const double step = 8.0 * nt * P > 900.0 ? 8.0 * nt * P : 900.0;
+            const double t = waves * ((double)((steps + ks - 1) / ks) * step + 7000.0 + 16.0 * nt) + (ks > 1 ? 2000.0 + 8.0 * nt : 0.0);
             if (best < 0.0 || t < best) {
                 best = t;
                 g->nt = nt;
@@ -735,8 +717,7 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
 size_t w4_gemm_bytes(const W4Gemm& g) {
     const W4Call& c = g.c;
     const int P = c.x_f32 ? 2 : 1;
-    return round256((size_t)P * c.tokens * g.kp * 2) + round256((size_t)c.tokens * 4) +
-           (g.ks > 1 ? (size_t)g.ks * c.tokens * c.n() * (c.glu ? 2 : 1) * 4 : 0);
+    return round256((size_t)P * c.tokens * g.kp * 2) + round256((size_t)c.tokens * 4);
 }
 
 cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
@@ -768,8 +749,6 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     p.act = c.act;
     p.out_f32 = c.out_f32;
     p.wide = (c.k() / c.group()) % 8 == 0 && ((uintptr_t)p.scales[0] & 15) == 0 && ((uintptr_t)p.scales[1] & 15) == 0;
-    p.part = (float*)((char*)factor + round256((size_t)c.tokens * 4));
-    p.count = g.count;
     p.err = c.err;
     // the rings: four stages of codes at least (behind the last step they also hold a tile's up sums), then activations
     const int xb = wm_stage(P, g.nt);
@@ -789,15 +768,18 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     const int rows = c.glu ? 128 : 256;
-    cfg.gridDim = dim3((c.n() + rows - 1) / rows, (c.tokens + g.nt - 1) / g.nt, g.ks);
+    cfg.gridDim = dim3((c.n() + rows - 1) / rows * g.ks, (c.tokens + g.nt - 1) / g.nt);
     cfg.blockDim = dim3(WM_THREADS);
     cfg.dynamicSmemBytes = (size_t)p.sx * xb + (size_t)p.sc * WM_CODES + 1024;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];   // starts while k_w4_split runs: codes and scales do not depend on it
+    cudaLaunchAttribute attr[2];   // starts while k_w4_split runs: codes and scales do not depend on it
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)g.ks;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.numAttrs = g.ks > 1 ? 2 : 1;
     void* args[] = {&p};
     return cudaLaunchKernelExC(&cfg, kernel_of(g), args);
 }

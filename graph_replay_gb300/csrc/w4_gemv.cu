@@ -34,7 +34,9 @@ size_t smem_of(const W4Gemv& g) {
 
 // how many clusters of ks CTAs, one an SM, run at a time: they do not cross the chip's SM groups, so it may be less than
 // the SMs hold (asked once for each size; devices of one process are alike)
-int clusters(int ks, int num_sms) {
+}  // namespace
+
+int w4_clusters(int ks, int num_sms) {
     if (ks == 1) return num_sms;
     static std::atomic<int> known[4];
     const int i = ks == 2 ? 1 : ks == 4 ? 2 : 3;
@@ -62,8 +64,6 @@ int clusters(int ks, int num_sms) {
     return n;
 }
 
-}  // namespace
-
 cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     const W4Call& c = g->c;
     const int P = c.parts(), N = c.n(), chunks = (c.k() + 127) / 128, most = WG_MAX_TOKENS / P;
@@ -73,7 +73,7 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     // CTAs along k: the fewest (a cluster: 1, 2, 4 or 8) whose shared memory holds the activations beside a ring of four
     // steps or two
     for (g->ks = 1; g->ks <= 8 && g->ks <= chunks; g->ks *= 2) {
-        const int places = clusters(g->ks, num_sms);
+        const int places = w4_clusters(g->ks, num_sms);
         g->rows = (N + places - 1) / places;
         if (g->rows < 8) g->rows = 8;
         g->grid = (N + g->rows - 1) / g->rows;

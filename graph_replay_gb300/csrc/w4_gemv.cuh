@@ -99,19 +99,6 @@ __device__ __forceinline__ void cp_wait(bool four) {   // with a ring of four st
     if (four) asm volatile("cp.async.wait_group 2;" ::: "memory");
     else asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
-// all threads of the cluster's CTAs; what they wrote to shared memory is visible to all behind it
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// the value at p's place in the shared memory of the cluster's CTA `rank`
-__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
-    uint32_t at;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
-    return v;
-}
-
 // G: columns of a group; P: fp16 parts of an activation; NB: blocks of 8 B columns
 template <int G, int P, int NB, int KIND>
 __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant__ W4GemvArgs p) {

@@ -24,14 +24,14 @@ _ACT = {"silu": B.DEC_ACT_SILU, "gelu_tanh": B.DEC_ACT_GELU_TANH}
 
 
 class _Device:
-    """What the calls on one device share: the error word, and a workspace for each stream."""
+    """What the calls on one device share: the error word."""
 
     _all, _guard = {}, threading.Lock()
 
     def __init__(self, index: int):
         if _capturing():
             raise RuntimeError("W4Weight: the first one on a device is made before a stream is captured")
-        self.index, self.lock, self.ws = index, threading.Lock(), {}
+        self.index = index
         self.err = torch.zeros(1, dtype=torch.int32, device=f"cuda:{index}")
         self.err_ptr = self.err.data_ptr()
         torch.cuda.current_stream(self.err.device).synchronize()   # zeroed before a call on any other stream adds to it
@@ -43,20 +43,6 @@ class _Device:
             if d is None:
                 d = cls._all[index] = cls(index)
             return d
-
-    def workspace(self, stream: int, need: int) -> torch.Tensor:
-        # One for each stream, its counters zeroed once: calls on a stream follow one another, and each leaves them as it
-        # found them.  A recorded graph gets its own, from its pool, and zeroes the counters when it runs
-        if _capturing():
-            ws = torch.empty(need, dtype=torch.uint8, device=self.err.device)
-            ws[:B.DEC_W4_COUNTER_BYTES].zero_()
-            return ws
-        ws = self.ws.get(stream)
-        if ws is None or ws.numel() < need:
-            ws = torch.empty(need, dtype=torch.uint8, device=self.err.device)
-            ws[:B.DEC_W4_COUNTER_BYTES].zero_()
-            self.ws[stream] = ws
-        return ws
 
 
 class W4Weight:
@@ -74,7 +60,7 @@ class W4Weight:
         self.codes, self.scales = codes, scales
         self.shape, self.group, self.device = (n, k), k // scales.shape[1], codes.device
         self._dev = _Device.of(codes.device.index)
-        self._calls = {}
+        self._calls, self._lock = {}, threading.Lock()
         self._c = B.dec_w4_weight(codes.data_ptr(), scales.data_ptr(), n, k, self.group, codes.device.index)
 
     @classmethod
@@ -158,7 +144,7 @@ class W4Weight:
                None if up is None else (up.shape, up.group, up.device),
                None if residual is None else (residual.shape, residual.stride(), residual.dtype, residual.device),
                None if norm is None else (norm.shape, norm.stride(), norm.dtype, norm.device))
-        with dev.lock:   # the call record and the workspace are this thread's until the launch
+        with self._lock:   # the call record is this thread's until the launch
             got = self._calls.get(key)
             if got is None:
                 got = self._calls[key] = self._prepare(up, x, act, residual, norm, eps, out)
@@ -169,9 +155,9 @@ class W4Weight:
             if residual is not None:
                 c.residual = residual.data_ptr()
             stream = _raw_stream(dev.index)
-            if need:
-                ws = dev.workspace(stream, need)
-                c.workspace, c.workspace_bytes = ws.data_ptr(), ws.numel()
+            if need:   # from torch's allocator, which hands it on in the stream's order
+                ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+                c.workspace, c.workspace_bytes = ws.data_ptr(), need
             if up is None:
                 B.dec_w4_linear(self._c, c, stream)
             else:

@@ -635,12 +635,10 @@ typedef struct dec_w4_call {
     double eps;
     uint32_t *err;               /* device: DEC_FAULT_WAIT is added if a copy or product never ended (the call's results are
                                     not to be used); never cleared */
-    void *workspace;             /* device, 256-byte aligned, dec_w4_workspace bytes.  Its first DEC_W4_COUNTER_BYTES are
-                                    zero-filled by the caller before its first use; every call leaves it ready for the next
-                                    one of any shape that it holds.  Calls that may overlap on the GPU need one each */
+    void *workspace;             /* device, 256-byte aligned, dec_w4_workspace bytes (NULL where that is 0), of any content.
+                                    Calls that may overlap on the GPU need one each */
     size_t workspace_bytes;
 } dec_w4_call;
-#define DEC_W4_COUNTER_BYTES 65536
 
 /* out[t, n] = residual[t, n] + sum_k W[n, k] a[t, k].  Products with the codes are
  * summed in fp32 at least; bf16 activations enter exactly, fp32 ones and normed
