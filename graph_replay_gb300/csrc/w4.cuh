@@ -66,6 +66,7 @@ __device__ __forceinline__ uint32_t w4_pack_half(float lo, float hi) {
 
 // all threads of the cluster's CTAs; what they wrote to shared memory is visible to all behind it
 __device__ __forceinline__ void cluster_sync() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // the value at p's place in the shared memory of the cluster's CTA `rank`

@@ -22,9 +22,11 @@
 //     warps 18-19 tcgen05.mma kind::f16, a tile each, accumulators in TMEM
 //   and warps 0-15 again for the epilogue: thread = output row, so a warp's stores of one
 //   token lie side by side.
-// The tensor core cuts its fp32 sums off instead of rounding them.  For fp32 activations
-// the accumulators are therefore folded into registers every WM_FOLD steps (with rounding),
-// while the MMAs go on in a second pair.
+// The two parts of fp32 activations are twice as many columns of one MMA (an MMA of 64
+// columns takes as long as one of 128 when A lies in TMEM).  The tensor core cuts its fp32
+// sums off instead of rounding them, so these accumulators are folded into registers every
+// WM_FOLD steps, with rounding; the two tiles' turns lie half of that apart, and one tile's
+// MMAs run while the other's sums are taken.
 // Few tokens leave few tiles: then a cluster of `ks` CTAs shares the columns of a tile,
 // and each of them adds the sums of a part of the tokens from the others' shared memory,
 // in order.
@@ -43,9 +45,9 @@ constexpr int WM_CODES = 2 * 128 * 64;         // bytes of a codes stage: two ti
 constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 3;
 constexpr int WM_SMEM = 200 * 1024;            // for both rings
 constexpr int WM_ROWS = 257;                   // of a split's sums of one token: 256, and one against bank conflicts
-constexpr int WM_FOLD = 2;                     // fp32 activations: steps of an accumulator
+constexpr int WM_FOLD = 4;                     // fp32 activations: steps of an accumulator
 
-// fp32 activations: stages of 64 columns (two parts), and accumulators of half as many tokens, in two pairs
+// fp32 activations: stages of 64 columns (two parts), and half as many tokens
 constexpr int wm_tokens(int P) { return P == 2 ? 64 : 128; }
 constexpr int wm_halves(int P) { return P; }   // activation stages of a step
 constexpr int wm_stage(int P, int nt) { return nt * 256; }   // bytes: 128 columns of one part or 64 of two
@@ -192,8 +194,8 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             mbar_init(&a_empty[s], 2);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&d_full[s], 2);
-            mbar_init(&d_empty[s], WM_DQ);
+            mbar_init(&d_full[s], 1);          // of a tile
+            mbar_init(&d_empty[s], WM_DQ / 2);
         }
         aborted = 0;
         mbar_fence_init();
@@ -201,8 +203,10 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     fence_before();
     __syncthreads();
     fence_after();
-    // TMEM columns: accumulators (tile i at i * nt, the second pair behind the first), then the ring of A
-    const uint32_t dt = tmem, at0 = dt + (uint32_t)(p.nt * (FOLD ? 4 : 2));
+    // TMEM columns: accumulators (of a tile: its tokens' sums, of the second parts behind those of the first), then the
+    // ring of A
+    const int dcols = p.nt * P;
+    const uint32_t dt = tmem, at0 = dt + (uint32_t)(2 * dcols);
     auto give_up = [&]() {
         *ab = 1;
         atomicOr(p.err, FAULT_WAIT);
@@ -257,14 +261,15 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     } else if (warp >= WM_DQ + 2) {
         // ---- products: a warp for each tile, so that one's waits lie under the other's MMAs ----
         const int i = warp - (WM_DQ + 2);
-        const uint32_t idesc = (1u << 4) | ((uint32_t)(p.nt >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+        const uint32_t idesc = (1u << 4) | ((uint32_t)(dcols >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
         const uint32_t xd = wm_desc(smem_u32(x_s)), half = (uint32_t)(p.nt * 128) >> 4;
         Ring ra, rx;
-        int fold = 0, used = 0;                // steps in the accumulators; pairs of them handed over
+        int fold = FOLD ? i * WM_FOLD / 2 : 0, used = 0;   // steps in the accumulator (the tiles in turn); times it was handed over
+        bool fresh = true;                     // it starts anew
         bool ok = true;
         for (int s = 0; s < n; ++s, ra.next(p.sa)) {
-            const uint32_t d = dt + (uint32_t)(i * p.nt) + (FOLD && (used & 1) ? (uint32_t)(2 * p.nt) : 0u);
-            if (FOLD && fold == 0 && used >= 2) ok = mbar_wait(&d_empty[used & 1], (uint32_t)((used >> 1) - 1) & 1u);
+            const uint32_t d = dt + (uint32_t)(i * dcols);
+            if (FOLD && fresh && used > 0) ok = mbar_wait(&d_empty[i], (uint32_t)(used - 1) & 1u);
             ok = ok && mbar_wait(&x_full[rx.slot], rx.odd) && mbar_wait(&a_full[ra.slot], ra.odd);
             if (!__all_sync(0xffffffffu, ok)) break;
             fence_after();
@@ -278,14 +283,8 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                     fence_after();
                 }
                 const uint32_t x = xd + (uint32_t)(rx.slot * (xbytes >> 4));
-                const uint32_t acc = fold > 0 || h > 0 ? 1u : 0u;
-                // B: P == 1: half h of the stage; P == 2: the second parts first, while the sums are small
-                if (P == 1) {
-                    mma_64(d, a + (uint32_t)(h * 32), x + h * half, idesc, acc);
-                } else {
-                    mma_64(d, a + (uint32_t)(h * 32), x + half, idesc, acc);
-                    mma_64(d, a + (uint32_t)(h * 32), x, idesc, 1u);
-                }
+                // B: half h of the stage, or (P == 2) a stage of 64 columns, both parts
+                mma_64(d, a + (uint32_t)(h * 32), x + (P == 1 ? h * half : 0u), idesc, fresh && h == 0 ? 0u : 1u);
                 if (P == 2 || h == 1) {
                     commit(&x_empty[rx.slot]);
                     rx.next(p.sx);
@@ -293,8 +292,9 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             }
             if (!ok) break;                    // the same for all lanes
             commit(&a_empty[ra.slot]);
-            if (++fold == (FOLD ? WM_FOLD : n) || s + 1 == n) {
-                commit(&d_full[FOLD ? used & 1 : 0]);
+            fresh = (FOLD && ++fold == WM_FOLD) || s + 1 == n;
+            if (fresh) {
+                commit(&d_full[i]);
                 ++used;
                 fold = 0;
             }
@@ -345,23 +345,26 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         float acc[FOLD ? 32 : 1];
 #pragma unroll
         for (int e = 0; e < (FOLD ? 32 : 1); ++e) acc[e] = 0.f;
-        int folded = 0;                        // pairs of accumulators taken
+        int folded = 0;                        // times the tile's accumulator was taken
         auto fold_in = [&]() -> bool {
-            if (!mbar_wait(&d_full[folded & 1], (uint32_t)(folded >> 1) & 1u)) return false;
+            if (!mbar_wait(&d_full[mat], (uint32_t)folded & 1u)) return false;
             fence_after();
             if (h * 32 < p.nt) {
-                uint32_t v[32];
-                tmem_ld32(dt + lanes + (uint32_t)((folded & 1) * 2 * p.nt + mat * p.nt + h * 32), v);
-                asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-                for (int e = 0; e < (FOLD ? 32 : 1); ++e) {
-                    asm volatile("" : "+r"(v[e]));
-                    acc[e] += __uint_as_float(v[e]);
+                for (int part = 0; part < P; ++part) {
+                    uint32_t v[32];
+                    tmem_ld32(dt + lanes + (uint32_t)(mat * dcols + part * p.nt + h * 32), v);
+                    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+                    for (int e = 0; e < (FOLD ? 32 : 1); ++e) {
+                        asm volatile("" : "+r"(v[e]));
+                        acc[e] += __uint_as_float(v[e]);
+                    }
                 }
             }
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&d_empty[folded & 1]);
+            if (lane == 0) mbar_arrive(&d_empty[mat]);
             ++folded;
             return true;
         };
@@ -378,10 +381,9 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             ok = mbar_wait(&codes_full[rc.slot], rc.odd) && ok;
             q0 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * WM_CODES + c0);
             q1 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * WM_CODES + c1);
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&codes_empty[rc.slot]);
             rc.next(p.sc);
         };
+        int now = 0;                           // the slot that they came from
         read_codes();
         for (int s = 0; s < n; ++s, ra.next(p.sa)) {
             const int step = s0 + s;
@@ -403,6 +405,8 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                     sc[c] = g < spitch ? scale_pair(__ldg(sp + g), up) : 0u;
                 }
             }
+            const int codes_slot = now;
+            now = rc.slot;
             const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
             if (s + 1 < n) read_codes();       // the next step's, under this one's arithmetic
             uint32_t a[32];
@@ -420,9 +424,14 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&a_full[ra.slot]);
-            // a pair of accumulators is taken a step after its last weights were made: its products have had that long
-            if (FOLD && s >= WM_FOLD && s % WM_FOLD == 0) {
+            if (lane == 0) {
+                mbar_arrive(&a_full[ra.slot]);
+                // the codes have become weights, so they are read: at their load they were only asked for, and the next copy
+                // could have come first
+                mbar_arrive(&codes_empty[codes_slot]);
+            }
+            // the accumulator is taken when the weights of the step behind its last are made: its products have had that long
+            if (FOLD && s > 0 && (s + mat * (WM_FOLD / 2)) % WM_FOLD == 0) {
                 ok = fold_in();
                 if (!__all_sync(0xffffffffu, ok)) break;
             }
@@ -434,10 +443,10 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         for (int i = tid; i < m; i += WM_DQ * 32) tok_f[i] = __ldcg(p.factor + tok0 + i);
         bool live = __all_sync(0xffffffffu, ok) && !*ab;
         if (FOLD) {
-            const int pairs = (n + WM_FOLD - 1) / WM_FOLD;
-            while (live && folded < pairs) live = __all_sync(0xffffffffu, fold_in());
+            const int times = (n - 1 + mat * (WM_FOLD / 2)) / WM_FOLD + 1;
+            while (live && folded < times) live = __all_sync(0xffffffffu, fold_in());
         } else if (live) {
-            live = __all_sync(0xffffffffu, mbar_wait(&d_full[0], 0u));
+            live = __all_sync(0xffffffffu, mbar_wait(&d_full[mat], 0u));
             fence_after();
         }
         if (!live && lane == 0) give_up();
@@ -506,7 +515,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 for (int e = 0; e < 16; ++e) v[e] = c & 16 ? acc[FOLD ? 16 + e : 0] : acc[FOLD ? e : 0];
             } else {
                 uint32_t d[16];
-                tm_ld16(dt + lanes + (uint32_t)(mat * p.nt + c), d);
+                tm_ld16(dt + lanes + (uint32_t)(mat * dcols + c), d);
                 asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -756,7 +765,7 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     if (p.sx > WM_MAX_SX) p.sx = WM_MAX_SX;
     p.sc = (WM_SMEM - p.sx * xb) / WM_CODES;
     if (p.sc > WM_MAX_SC) p.sc = WM_MAX_SC;
-    p.sa = (512 - g.nt * (P == 2 ? 4 : 2)) / 128;
+    p.sa = (512 - 2 * g.nt * P) / 128;
     if (p.sa > WM_MAX_SA) p.sa = WM_MAX_SA;
     if (p.sx < 2 || p.sc < 5 || p.sa < 2) return cudaErrorInvalidValue;
 

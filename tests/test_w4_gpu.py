@@ -162,3 +162,21 @@ def run_glu(W, m, n, k, group, dtype, norm, act, seed=0):
 def test_glu(W, dtype, act, m, n, k, group):
     run_glu(W, m, n, k, group, dtype, True, act, seed=m)
     run_glu(W, m, n, k, group, dtype, False, act, seed=m + 1)
+
+
+@pytest.mark.parametrize("m, n, k, group, dtype", [(40, 6144, 4096, 128, "bf16"), (64, 4096, 14336, 64, "f32"), (9, 513, 4096, 32, "f32"),
+                                                   (300, 2000, 2048, 128, "f32"), (8, 4096, 14336, 128, "f32"), (3, 1001, 1120, 32, "bf16"),
+                                                   (1000, 1536, 1152, 64, "bf16")])
+def test_repeats_bit_for_bit(W, m, n, k, group, dtype):
+    """Results do not depend on when copies land: 40 calls in a row, with other work between, give the same bits."""
+    a, b = W(*R.random_matrix(n, k, group, 1)), W(*R.random_matrix(n, k, group, 2))
+    x = normal(m, k, seed=3, dtype=DT[dtype])
+    first, both = a.linear(x), a.glu(b, x)
+    run = R.activation(x, None, 0.0) @ R.values(a.codes, a.scales).T
+    R.close(first, run, R.product_bound(x.double(), R.values(a.codes, a.scales), 21 if dtype == "f32" else 40, k), "linear")
+    other = torch.empty(1 << 26, dtype=torch.uint8, device="cuda")
+    for i in range(40):
+        if i % 4 == 0:
+            other.fill_(i)     # the weights leave the cache
+        assert torch.equal(a.linear(x), first) and torch.equal(a.glu(b, x), both), i
+    a.check()
