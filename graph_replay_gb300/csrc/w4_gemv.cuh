@@ -74,23 +74,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// The pairs (j, j + 4) of a word as fp16 subnormals: with its sign bit turned over a code is u = q + 8, 0 .. 15, and bits
-// 0-3 of a half stand for u 2^-24, bits 4-7 for u 2^-20.  Nothing has to be converted; 8 times the activations' sum is taken
-// off behind a group's products, and the activations of the second and fourth pair are 2^-4 of the others
-struct W4Sign {
-    uint32_t low, high;        // in registers: as immediates they would cost an instruction more at each use
-    __device__ __forceinline__ W4Sign() {
-        asm volatile("mov.b32 %0, 0x00080008;" : "=r"(low));
-        asm volatile("mov.b32 %0, 0x00800080;" : "=r"(high));
-    }
-};
-__device__ __forceinline__ void w4_raw(uint32_t w, const W4Sign& k, uint32_t (&pair)[4]) {
-    const uint32_t v = w >> 8;
-    pair[0] = w4_and_xor<0x000f000fu>(w, k.low);
-    pair[1] = w4_and_xor<0x00f000f0u>(w, k.high);
-    pair[2] = w4_and_xor<0x000f000fu>(v, k.low);
-    pair[3] = w4_and_xor<0x00f000f0u>(v, k.high);
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, unsigned bytes) {   // the rest of 16 bytes is zero
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
@@ -129,9 +112,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const unsigned ring_bytes = (unsigned)S * WG_STEP;
     unsigned char* ring = smem + (size_t)warp * ring_bytes;
     unsigned char* xs = smem + (size_t)WG_WARPS * ring_bytes;                // [chunk][4][cols][64 bytes]
-    float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14 + 12)
-    float* cs = fs + (((ch1 - ch0) * p.block + 3) & ~3);                     // [chunk][NG][block]: what a group's sums are off
-    float* red = cs + (ch1 - ch0) * NG * p.block;                             // [bufs][warp][MT][WG_PITCH]
+    float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14)
+    float* red = fs + (((ch1 - ch0) * p.block + 3) & ~3);                             // [bufs][warp][MT][WG_PITCH]
     float* sums = red + p.bufs * WG_WARPS * MT * WG_PITCH;                   // ks > 1: [1 or 2][block][rows], read by the cluster
     const uint32_t ring_at = smem_u32(ring);
 
@@ -258,16 +240,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             const uint32_t top = __reduce_max_sync(
                 0xffffffffu, max(max(w4_finite_bits(x.x), w4_finite_bits(x.y)), max(w4_finite_bits(x.z), w4_finite_bits(x.w))));
             const int e = w4_exponent(top);
-            const float up = w4_up(e), up4 = up * 0.0625f;
-            x.x *= up; x.y *= up4; x.z *= up; x.w *= up4;      // columns j of a word meet codes times 2^-24, 2^-20, ...
+            const float up = w4_up(e);
+            x.x *= up; x.y *= up; x.z *= up; x.w *= up;
             const int ci = warp + cj * WG_WARPS;
-            float sum = 0.f;                   // of all parts
 #pragma unroll
             for (int part = 0; part < P; ++part) {
                 const uint32_t a01 = w4_pack_half(x.x, x.y), a23 = w4_pack_half(x.z, x.w);
                 const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&a01));
                 const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&a23));
-                sum += (f01.x + f23.x) + 16.0f * (f01.y + f23.y);
                 const int col = cr * P + part;
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a01 : a23, 1);
                 const uint32_t lo = odd ? got : a01, hi = odd ? a23 : got;     // columns j and j + 4 of the word
@@ -278,10 +258,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 x.x = isfinite(x.x) ? x.x : 0.f; x.y = isfinite(x.y) ? x.y : 0.f;
                 x.z = isfinite(x.z) ? x.z : 0.f; x.w = isfinite(x.w) ? x.w : 0.f;
             }
-#pragma unroll
-            for (int o = 1; o < G / 4; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (lane % (G / 4) == 0) cs[(ci * NG + lane / (G / 4)) * p.block + cr] = sum * -4.76837158203125e-07f;   // -8 2^-24
-            if (lane == 0) fs[ci * p.block + cr] = w4_down(e) * 4096.0f;   // half of the codes' 2^-24; the rest with the norm
+            if (lane == 0) fs[ci * p.block + cr] = w4_down(e);
             if (++cj == nc) {
                 if (p.gain) {
                     ss = warp_sum(ss);
@@ -322,7 +299,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         float s = 0.f;
         if (p.gain)
             for (int w = 0; w < WG_WARPS; ++w) s += ss_s[w][tid];
-        inv_s[tid] = 4096.0f * (p.gain ? 1.0f / sqrtf(s / (float)p.K + p.eps) : 1.0f);   // read behind the next barrier
+        inv_s[tid] = p.gain ? 1.0f / sqrtf(s / (float)p.K + p.eps) : 1.0f;   // read behind the next barrier
     }
 
     // one output: gate / value v and up u, unscaled by the norm; its residual
@@ -365,10 +342,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         rows_of(0, cur);
         scales_of(cur, g_first, s_even);
     }
-    const W4Sign kc;
+    const W4Const kc;
     unsigned slot = 0;                         // of this step, in bytes
-    const unsigned b_hop = (unsigned)p.wk * 4 * cols * 64, f_hop = (unsigned)(p.wk * p.block),
-                   c_hop = (unsigned)(p.wk * NG * p.block);
+    const unsigned b_hop = (unsigned)p.wk * 4 * cols * 64, f_hop = (unsigned)(p.wk * p.block);
     for (int it = 0; it < iters; ++it) {
         // the residual of the thread's first output, under the products
         float res = 0.f;
@@ -385,7 +361,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < AC; ++c) acc[a][b][c] = 0.f;
         const int base = row0 + (it * sets + set) * GR;
-        unsigned b_at[NB], f_at[NB][P == 2 ? 1 : 2], c_at[NB][P == 2 ? 1 : 2];   // of the step's chunk
+        unsigned b_at[NB], f_at[NB][P == 2 ? 1 : 2];   // of the step's chunk
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             b_at[b] = (unsigned)slice * 4 * cols * 64 + (unsigned)min(b * 8 + g, cols - 1) * 64 + t * 16;
@@ -393,7 +369,6 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             for (int c = 0; c < (P == 2 ? 1 : 2); ++c) {
                 const int r = min(P == 2 ? b * 4 + t : b * 8 + 2 * t + c, p.block - 1);
                 f_at[b][c] = (unsigned)(slice * p.block + r);
-                c_at[b][c] = (unsigned)(slice * NG * p.block + r);
             }
         }
         auto one_step = [&](int i, const uint32_t (&use)[4], uint32_t (&fill)[4]) {
@@ -461,8 +436,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     uint32_t pa[2][4], pb[2][4];
 #pragma unroll
                     for (int tile = 0; tile < 2; ++tile) {
-                        w4_raw(wa[tile][c], kc, pa[tile]);
-                        w4_raw(wb[tile][c], kc, pb[tile]);
+                        w4_unpack(wa[tile][c], kc, pa[tile]);
+                        w4_unpack(wb[tile][c], kc, pb[tile]);
                     }
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
@@ -477,11 +452,6 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                         for (int tile = 0; tile < 2; ++tile)
                             mma_f16(d[tile][b], pa[tile][2], pb[tile][2], pa[tile][3], pb[tile][3], bf[b].z, bf[b].w);
                 }
-                float off[NB][P == 2 ? 1 : 2];
-#pragma unroll
-                for (int b = 0; b < NB; ++b)
-#pragma unroll
-                    for (int c = 0; c < (P == 2 ? 1 : 2); ++c) off[b][c] = cs[c_at[b][c] + (unsigned)(gi * p.block)];
 #pragma unroll
                 for (int tile = 0; tile < 2; ++tile) {
                     const uint32_t sw = NG > 1 ? __shfl_sync(0xffffffffu, sc[tile], (lane & 28) | gi) : sc[tile];
@@ -492,23 +462,19 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                         float* o = acc[tile][b];
                         constexpr int L = P == 2 ? 0 : 1;
                         if (P == 2) {          // columns 2t and 2t + 1 are the two parts of one token
-                            o[0] = fmaf((e[0] + e[1] + off[b][0]) * f[b][0], s0, o[0]);
-                            o[1] = fmaf((e[2] + e[3] + off[b][0]) * f[b][0], s1, o[1]);
+                            o[0] = fmaf((e[0] + e[1]) * f[b][0], s0, o[0]);
+                            o[1] = fmaf((e[2] + e[3]) * f[b][0], s1, o[1]);
                         } else {
-                            o[0] = fmaf((e[0] + off[b][0]) * f[b][0], s0, o[0]);
-                            o[AC == 4 ? 1 : 0] = fmaf((e[1] + off[b][L]) * f[b][L], s0, o[AC == 4 ? 1 : 0]);
-                            o[AC == 4 ? 2 : 0] = fmaf((e[2] + off[b][0]) * f[b][0], s1, o[AC == 4 ? 2 : 0]);
-                            o[AC == 4 ? 3 : 0] = fmaf((e[3] + off[b][L]) * f[b][L], s1, o[AC == 4 ? 3 : 0]);
+                            o[0] = fmaf(e[0] * f[b][0], s0, o[0]);
+                            o[AC == 4 ? 1 : 0] = fmaf(e[1] * f[b][L], s0, o[AC == 4 ? 1 : 0]);
+                            o[AC == 4 ? 2 : 0] = fmaf(e[2] * f[b][0], s1, o[AC == 4 ? 2 : 0]);
+                            o[AC == 4 ? 3 : 0] = fmaf(e[3] * f[b][L], s1, o[AC == 4 ? 3 : 0]);
                         }
                     }
                 }
             }
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                b_at[b] += b_hop;
-#pragma unroll
-                for (int c = 0; c < (P == 2 ? 1 : 2); ++c) c_at[b][c] += c_hop;
-            }
+            for (int b = 0; b < NB; ++b) b_at[b] += b_hop;
         };
         for (int i = 0; i < mine; i += 2) {
             one_step(i, s_even, s_odd);
