@@ -826,21 +826,21 @@ int dec_capture(dec_handle* h, int32_t cap, int32_t rows, int32_t kv_layout, int
             h->gemv.push_back(mk4(PRO_RMSNORM, EPI_SWIGLU, &w4[6], 2, h->d_x, d, w[5], h->d_gu, 2 * F));
             h->gemv.push_back(mk4(PRO_PLAIN, EPI_ADD, &w4[8], 1, h->d_gu, 2 * F, nullptr, h->d_x, d));
         } else {
-        h->gemv.push_back(mk(PRO_RMSNORM, EPI_STORE, w[1], Hq * hd, w[2], Hkv * hd, w[3], Hkv * hd, d, h->d_x, d, w[0],
-                             h->d_qkv, qkv_stride));
-        h->gemv.push_back(mk(PRO_PLAIN, EPI_ADD, w[4], d, nullptr, 0, nullptr, 0, Hq * hd, h->d_attn, Hq * hd, nullptr,
-                             h->d_x, d));
-        if (tc) {
-            h->gemv.push_back(mk(PRO_RMSNORM, EPI_SWIGLU, w[6], F, w[7], F, nullptr, 0, d, h->d_x, d, w[5], h->d_gu,
-                                 2 * F));
-            h->gemv.push_back(mk(PRO_PLAIN, EPI_ADD, w[8], d, nullptr, 0, nullptr, 0, F, h->d_gu, 2 * F, nullptr,
+            h->gemv.push_back(mk(PRO_RMSNORM, EPI_STORE, w[1], Hq * hd, w[2], Hkv * hd, w[3], Hkv * hd, d, h->d_x, d, w[0],
+                                 h->d_qkv, qkv_stride));
+            h->gemv.push_back(mk(PRO_PLAIN, EPI_ADD, w[4], d, nullptr, 0, nullptr, 0, Hq * hd, h->d_attn, Hq * hd, nullptr,
                                  h->d_x, d));
-        } else {
-            h->gemv.push_back(mk(PRO_RMSNORM, EPI_STORE, w[6], F, w[7], F, nullptr, 0, d, h->d_x, d, w[5], h->d_gu,
-                                 2 * F));
-            h->gemv.push_back(mk(PRO_SWIGLU, EPI_ADD, w[8], d, nullptr, 0, nullptr, 0, F, h->d_gu, 2 * F, nullptr,
-                                 h->d_x, d));
-        }
+            if (tc) {
+                h->gemv.push_back(mk(PRO_RMSNORM, EPI_SWIGLU, w[6], F, w[7], F, nullptr, 0, d, h->d_x, d, w[5], h->d_gu,
+                                     2 * F));
+                h->gemv.push_back(mk(PRO_PLAIN, EPI_ADD, w[8], d, nullptr, 0, nullptr, 0, F, h->d_gu, 2 * F, nullptr,
+                                     h->d_x, d));
+            } else {
+                h->gemv.push_back(mk(PRO_RMSNORM, EPI_STORE, w[6], F, w[7], F, nullptr, 0, d, h->d_x, d, w[5], h->d_gu,
+                                     2 * F));
+                h->gemv.push_back(mk(PRO_SWIGLU, EPI_ADD, w[8], d, nullptr, 0, nullptr, 0, F, h->d_gu, 2 * F, nullptr,
+                                     h->d_x, d));
+            }
         }
         AttnPlan ap{};
         ap.kvtype = c.kv_dtype == DEC_DTYPE_BF16 ? W_BF16 : W_F32;

@@ -98,6 +98,16 @@ int check_values(const char* what, const void* p, int64_t stride, int64_t cols, 
     return DEC_OK;
 }
 
+// whether rows of two matrices with as many rows meet: x and out may be columns of one wider matrix
+bool meet(const void* a, int64_t a_stride, int64_t a_bytes, const void* b, int64_t b_stride, int64_t b_bytes, int64_t rows) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    if (x + (uint64_t)((rows - 1) * a_stride + a_bytes) <= y || y + (uint64_t)((rows - 1) * b_stride + b_bytes) <= x) return false;
+    if (rows == 1 || a_stride != b_stride) return true;
+    const int64_t off = (int64_t)((y - x) % (uint64_t)a_stride);   // y's column in a's rows
+    const int64_t at = y >= x ? off : (int64_t)(a_stride - (int64_t)((x - y) % (uint64_t)a_stride)) % a_stride;
+    return at < a_bytes || at + b_bytes > a_stride;
+}
+
 int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* c, W4Call* p) {
     int rc;
     *p = W4Call{};
@@ -113,6 +123,7 @@ int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const 
     if (!c) return refuse(DEC_E_INVALID, "call is NULL");
     if (c->tokens < 0) return refuse(DEC_E_INVALID, "tokens must be >= 0");
     if ((int64_t)c->tokens * w->n > INT_MAX) return refuse(DEC_E_UNSUPPORTED, "tokens * n: at most 2^31 - 1");
+    if (c->tokens > (1 << 21)) return refuse(DEC_E_UNSUPPORTED, "tokens = %d: at most 2^21", c->tokens);
     if ((int64_t)c->tokens * w->k > INT_MAX) return refuse(DEC_E_UNSUPPORTED, "tokens * k: at most 2^31 - 1");
     if ((rc = check_dtype("x_dtype", c->x_dtype, &p->x_f32)) != DEC_OK) return rc;
     if ((rc = check_dtype("out_dtype", c->out_dtype, &p->out_f32)) != DEC_OK) return rc;
@@ -135,6 +146,13 @@ int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const 
             if (c->residual == c->out && c->residual_stride != c->out_stride)
                 return refuse(DEC_E_INVALID, "a residual that is out must have its stride");
         }
+        const int64_t xs = p->x_f32 ? 4 : 2, os = p->out_f32 ? 4 : 2, n = w->n, k = w->k;
+        if (meet(c->x, c->x_stride * xs, k * xs, c->out, c->out_stride * os, n * os, c->tokens) ||
+            (c->gain && meet(c->gain, k * 4, k * (p->gain_f32 ? 4 : 2), c->out, c->out_stride * os,
+                             ((int64_t)c->tokens - 1) * c->out_stride * os + n * os, 1)) ||
+            (c->residual && c->residual != c->out &&
+             meet(c->residual, c->residual_stride * os, n * os, c->out, c->out_stride * os, n * os, c->tokens)))
+            return refuse(DEC_E_INVALID, "out overlaps x, the gain or the residual (it may be the residual itself)");
     }
     p->act = c->act;
     p->tokens = c->tokens;
@@ -158,19 +176,23 @@ struct Plan {
     size_t bytes;
 };
 
+// Few tokens (at most 16 columns of activation parts) go to w4_gemv.cu: 8 fp32 tokens, 14336 -> 4096, take 22 us there and
+// 40 in w4_gemm.cu; 9 bf16 ones as long in both, 16 longer.  Columns too many for its shared memory go there too
 cudaError_t plan_of(const W4Call& c, int sms, Plan* p) {
     p->few = c.tokens * c.parts() <= 16;
-    if (!p->few) {
-        p->gemm = W4Gemm{};
-        p->gemm.c = c;
-        const cudaError_t e = w4_gemm_plan(&p->gemm, sms);
-        p->bytes = w4_gemm_bytes(p->gemm);
-        return e;
-    }
-    p->gemv = W4Gemv{};
-    p->gemv.c = c;
     p->bytes = 0;
-    return w4_gemv_plan(&p->gemv, sms);
+    if (p->few) {
+        p->gemv = W4Gemv{};
+        p->gemv.c = c;
+        if (w4_gemv_plan(&p->gemv, sms) == cudaSuccess) return cudaSuccess;
+        cudaGetLastError();
+        p->few = false;
+    }
+    p->gemm = W4Gemm{};
+    p->gemm.c = c;
+    const cudaError_t e = w4_gemm_plan(&p->gemm, sms);
+    p->bytes = w4_gemm_bytes(p->gemm);
+    return e;
 }
 
 int run(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* call, void* stream) {

@@ -67,28 +67,31 @@ int w4_clusters(int ks, int num_sms) {
 cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     const W4Call& c = g->c;
     const int P = c.parts(), N = c.n(), chunks = (c.k() + 127) / 128, most = WG_MAX_TOKENS / P;
-    g->block = c.tokens < most ? c.tokens : most;
+    // as many tokens a CTA as its shared memory holds; the rest in further rows of the grid
+    for (g->block = c.tokens < most ? c.tokens : most;; g->block = (g->block + 1) / 2) {
     // rows evenly over the SMs, at least 8 a CTA: a tile has 16, and a CTA of fewer saves nothing
     const int gr = c.glu ? 16 : 32;
-    // CTAs along k: the fewest (a cluster: 1, 2, 4 or 8) whose shared memory holds the activations beside a ring of four
-    // steps or two
-    for (g->ks = 1; g->ks <= 8 && g->ks <= chunks; g->ks *= 2) {
-        const int places = w4_clusters(g->ks, num_sms);
-        g->rows = (N + places - 1) / places;
-        if (g->rows < 8) g->rows = 8;
-        g->grid = (N + g->rows - 1) / g->rows;
-        const int groups = (g->rows + gr - 1) / gr;
-        const int own = (chunks + g->ks - 1) / g->ks;
-        // warps along k: as many as have a chunk, but no more than leave each set of warps a row group
-        g->wk = WG_WARPS;
-        while (g->wk > 1 && (own < g->wk || (groups >= 2 * (WG_WARPS / g->wk) && own < 8 * g->wk))) g->wk /= 2;
-        const int sets = WG_WARPS / g->wk, iters = (groups + sets - 1) / sets;
-        g->bufs = iters > 1 ? 2 : 1;
-        g->stages = WG_STAGES;
-        if (smem_of(*g) > SMEM_MOST) g->stages = 2;
-        if (smem_of(*g) <= SMEM_MOST) break;
+        // CTAs along k: the fewest (a cluster: 1, 2, 4 or 8) whose shared memory holds the activations beside a ring of four
+        // steps or two
+        for (g->ks = 1; g->ks <= 8 && g->ks <= chunks; g->ks *= 2) {
+            const int places = w4_clusters(g->ks, num_sms);
+            g->rows = (N + places - 1) / places;
+            if (g->rows < 8) g->rows = 8;
+            g->grid = (N + g->rows - 1) / g->rows;
+            const int groups = (g->rows + gr - 1) / gr;
+            const int own = (chunks + g->ks - 1) / g->ks;
+            // warps along k: as many as have a chunk, but no more than leave each set of warps a row group
+            g->wk = WG_WARPS;
+            while (g->wk > 1 && (own < g->wk || (groups >= 2 * (WG_WARPS / g->wk) && own < 8 * g->wk))) g->wk /= 2;
+            const int sets = WG_WARPS / g->wk, iters = (groups + sets - 1) / sets;
+            g->bufs = iters > 1 ? 2 : 1;
+            g->stages = WG_STAGES;
+            if (smem_of(*g) > SMEM_MOST) g->stages = 2;
+            if (smem_of(*g) <= SMEM_MOST) break;
+        }
+        if (g->ks <= 8 && g->ks <= chunks) break;
+        if (g->block == 1) return cudaErrorInvalidValue;
     }
-    if (g->ks > 8 || g->ks > chunks) return cudaErrorInvalidValue;
     g->smem = smem_of(*g);
     // the cap once for each kernel and device
     static OncePerDevice once[3][2][2][3];

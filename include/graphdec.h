@@ -628,7 +628,7 @@ typedef struct dec_w4_call {
     void *out;                   /* device [tokens, n] */
     int64_t x_stride;            /* elements between tokens, a multiple of 16 bytes */
     int64_t residual_stride, out_stride;   /* at least n */
-    int32_t tokens;              /* >= 0; tokens * n <= 2^31 - 1 */
+    int32_t tokens;              /* 0 .. 2^21; tokens * n and tokens * k <= 2^31 - 1 */
     int32_t x_dtype, gain_dtype, out_dtype;   /* F32 or BF16 each */
     int32_t act;                 /* dec_w4_glu: dec_act */
     int32_t reserved;            /* 0 */
@@ -641,10 +641,13 @@ typedef struct dec_w4_call {
 } dec_w4_call;
 
 /* out[t, n] = residual[t, n] + sum_k W[n, k] a[t, k].  Products with the codes are
- * summed in fp32 at least; bf16 activations enter exactly, fp32 ones and normed
- * ones to about 2^-22 of each (or 2^-39 of the largest near it), normed bf16 ones
- * of more than a few tokens to 2^-12.  What a token gives does not depend on the
- * others beside it, nor on scheduling. */
+ * summed in fp32; bf16 activations enter exactly, fp32 ones and normed ones to
+ * about 2^-22 of each, normed bf16 ones of more than a few tokens to 2^-12 (and
+ * all to no less than 2^-39 of the token's largest; weights of more than a few
+ * tokens to no less than 2^-38 of the row's largest scale).  Results do not depend
+ * on scheduling nor on the values of other tokens, but their last digits do on how
+ * many tokens a call has.  A token with a NaN or an infinity gives NaN or
+ * infinities. */
 int dec_w4_linear(const dec_w4_weight *w, const dec_w4_call *call, void *stream);
 
 /* The first half of a gated feed-forward block: out[t, n] = act(gate_n . a_t) *

@@ -201,3 +201,27 @@ def test_one_layer_of_a_program_with_its_own_cache(W):
     assert torch.isfinite(prompt).all()
     wq.check()
     cache.check()
+
+
+@pytest.mark.parametrize("m, n, k, dt", [(8, 40, 32768, torch.float32), (8, 3000, 28672, torch.float32), (16, 100, 65536, torch.bfloat16),
+                                         (1, 9, 1 << 19, torch.float32), (2, 16, 1 << 20, torch.bfloat16)])
+def test_many_columns(W, m, n, k, dt):
+    """More than the activations' shared memory holds at once."""
+    c, s = R.random_matrix(n, k, 128, 5)
+    x = normal(m, k, seed=1, dtype=dt)
+    w, v = W(c, s), R.values(c, s)
+    R.close(w.linear(x), x.double() @ v.T, R.product_bound(x.double(), v, 21 if dt == torch.float32 else 40, k))
+    w.check()
+
+
+def test_out_beside_x_and_over_it(W):
+    from graph_replay_gb300 import _binding as B
+    w = W(*R.random_matrix(128, 128, 128, 5))
+    wide = normal(6, 512, seed=1)
+    x = wide[:, :128].clone()
+    want = w.linear(x)
+    assert torch.equal(w.linear(wide[:, :128], out=wide[:, 128:256]), want)
+    assert torch.equal(wide[:, :128], x)
+    for out in (wide[:, :128], wide[:, 64:192], wide[1:].view(-1)[:6 * 128].view(6, 128)[:6]):
+        with pytest.raises(B.DecError, match="overlaps"):
+            w.linear(wide[:, :128], out=out)

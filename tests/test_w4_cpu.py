@@ -25,7 +25,7 @@ def weight(B, **kw):
 
 
 def call(B, **kw):
-    c = dict(x=PTR, gain=None, residual=None, out=PTR, x_stride=256, residual_stride=0, out_stride=64, tokens=3, x_dtype=0,
+    c = dict(x=PTR, gain=None, residual=None, out=PTR + (1 << 18), x_stride=256, residual_stride=0, out_stride=64, tokens=3, x_dtype=0,
              gain_dtype=0, out_dtype=0, act=0, reserved=0, eps=1e-5, err=PTR, workspace=None, workspace_bytes=0)
     c.update(kw)
     return B.dec_w4_call(**c)
@@ -53,7 +53,9 @@ def test_bad_weights(B, what, code, word):
     (dict(out_stride=63), 1, "out"), (dict(x_dtype=2), 1, "x_dtype"), (dict(out_dtype=7), 1, "out_dtype"),
     (dict(gain=PTR, gain_dtype=2), 1, "gain"), (dict(gain=PTR + 8), 1, "gain"), (dict(gain=PTR, eps=-1.0), 1, "eps"),
     (dict(gain=PTR, eps=math.nan), 1, "eps"), (dict(gain=PTR, eps=1e300), 1, "eps"), (dict(err=None), 1, "err"),
-    (dict(err=PTR + 2), 1, "err"), (dict(tokens=1 << 26), 2, "tokens")])
+    (dict(err=PTR + 2), 1, "err"), (dict(tokens=1 << 26), 2, "tokens"), (dict(tokens=(1 << 21) + 1), 2, "tokens"),
+    (dict(out=PTR), 1, "overlaps"), (dict(out=PTR + 1024), 1, "overlaps"), (dict(out=PTR + 4 * 255, out_stride=256), 1, "overlaps"),
+    (dict(out=PTR - 4 * 62, out_stride=256), 1, "overlaps"), (dict(gain=PTR + (1 << 16), out=PTR + (1 << 16) + 64), 1, "overlaps")])
 def test_bad_calls(B, what, code, word):
     lib = B.lib()
     for rc in (lib.dec_w4_linear(weight(B), call(B, **what), None), lib.dec_w4_glu(weight(B), weight(B), call(B, **what), None)):
@@ -63,7 +65,8 @@ def test_bad_calls(B, what, code, word):
 def test_bad_residuals_activations_and_pairs(B):
     lib = B.lib()
     for what, word in ((dict(residual=PTR + 1, residual_stride=64), "residual"), (dict(residual=PTR, residual_stride=60), "residual"),
-                       (dict(residual=PTR, residual_stride=128), "stride")):
+                       (dict(residual=PTR + (1 << 18), residual_stride=128), "stride"),
+                       (dict(residual=PTR + (1 << 18) + 4, residual_stride=64), "overlaps")):
         assert lib.dec_w4_linear(weight(B), call(B, **what), None) == 1 and word in B.last_error(None)
     assert lib.dec_w4_glu(weight(B), weight(B), call(B, residual=PTR + 4096, residual_stride=64), None) == 1
     assert "residual" in B.last_error(None)
@@ -81,6 +84,15 @@ def test_bad_storing(B):
                lib.dec_w4_quantize(weight(B), PTR, 255, 0, None), lib.dec_w4_quantize(weight(B), PTR, 256, 2, None),
                lib.dec_w4_dequantize(weight(B), None, 256, 1, None), lib.dec_w4_dequantize(weight(B), PTR, 260, 1, None)):
         assert rc == 1
+
+
+def test_columns_of_one_wider_matrix_do_not_overlap(B):
+    """x and out side by side in rows of 1024 floats, either way round: refused for nothing but the device that is not there."""
+    lib = B.lib()
+    for x, out in ((PTR, PTR + 1024), (PTR + 1024, PTR + 256), (PTR + 4096 * 2, PTR + 1024)):
+        c = call(B, x=x, x_stride=1024, out=out, out_stride=1024, eps=0.0)
+        if not torch.cuda.is_available():
+            assert lib.dec_w4_linear(weight(B), c, None) == 5   # DEC_E_CUDA: every check before it passed
 
 
 def test_no_tokens_is_nothing_to_do(B):
