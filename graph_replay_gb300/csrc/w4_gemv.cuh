@@ -77,6 +77,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, unsigned bytes) {   // the rest of 16 bytes is zero
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
+// shared memory by its 32-bit address; in order with the copies' waits
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_wait(bool four) {   // with a ring of four steps (or two) the oldest group has landed
     if (four) asm volatile("cp.async.wait_group 2;" ::: "memory");
@@ -111,7 +127,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const int S = p.stages;
     const unsigned ring_bytes = (unsigned)S * WG_STEP;
     unsigned char* ring = smem + (size_t)warp * ring_bytes;
-    unsigned char* xs = smem + (size_t)WG_WARPS * ring_bytes;                // [chunk][4][cols][64 bytes]
+    unsigned char* xs = smem + (size_t)WG_WARPS * ring_bytes;                // [chunk][cols][4][64 bytes], an odd column's words in pairs exchanged: no bank conflicts
     float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14)
     float* red = fs + (((ch1 - ch0) * p.block + 3) & ~3);                             // [bufs][warp][MT][WG_PITCH]
     float* sums = red + p.bufs * WG_WARPS * MT * WG_PITCH;                   // ks > 1: [1 or 2][block][rows], read by the cluster
@@ -175,7 +191,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     if (steps > 0) rows_of(0, ahead);
     auto copy_next = [&]() {
         if (a_left > 0) {
-            const unsigned in = a_at < cpitch ? ~0u : 0u;
+            const unsigned in = G == 128 || a_at < cpitch ? ~0u : 0u;   // (k is a multiple of G)
             const uint32_t dst = ring_at + a_slot + put;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -184,7 +200,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                            in & ahead.live[i]);
             }
             --a_left;
-            a_slot = a_slot + WG_STEP == ring_bytes ? 0u : a_slot + WG_STEP;
+            a_slot = (a_slot + WG_STEP) & (ring_bytes - 1u);   // four steps or two
             a_at += hop;
             if (++a_i == mine) {
                 a_i = 0;
@@ -252,7 +268,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a01 : a23, 1);
                 const uint32_t lo = odd ? got : a01, hi = odd ? a23 : got;     // columns j and j + 4 of the word
                 const uint2 f = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
-                *reinterpret_cast<uint2*>(xs + ((size_t)(ci * 4 + bq) * cols + col) * 64 + bt * 16 + (odd ? 8 : 0)) = f;
+                *reinterpret_cast<uint2*>(xs + ((size_t)(ci * cols + col) * 4 + (bq ^ (col & 1))) * 64 + bt * 16 + (odd ? 8 : 0)) = f;
                 // what the part leaves (nothing where it is not finite)
                 x.x -= f01.x; x.y -= f01.y; x.z -= f23.x; x.w -= f23.y;
                 x.x = isfinite(x.x) ? x.x : 0.f; x.y = isfinite(x.y) ? x.y : 0.f;
@@ -344,7 +360,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     }
     const W4Const kc;
     unsigned slot = 0;                         // of this step, in bytes
-    const unsigned b_hop = (unsigned)p.wk * 4 * cols * 64, f_hop = (unsigned)(p.wk * p.block);
+    const unsigned b_hop = (unsigned)p.wk * cols * 256, f_hop = (unsigned)(p.wk * p.block);
     for (int it = 0; it < iters; ++it) {
         // the residual of the thread's first output, under the products
         float res = 0.f;
@@ -361,10 +377,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < AC; ++c) acc[a][b][c] = 0.f;
         const int base = row0 + (it * sets + set) * GR;
-        unsigned b_at[NB], f_at[NB][P == 2 ? 1 : 2];   // of the step's chunk
+        unsigned b_at[NB], b_odd[NB], f_at[NB][P == 2 ? 1 : 2];   // of the step's chunk
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-            b_at[b] = (unsigned)slice * 4 * cols * 64 + (unsigned)min(b * 8 + g, cols - 1) * 64 + t * 16;
+            const int col = min(b * 8 + g, cols - 1);
+            b_at[b] = smem_u32(xs) + (unsigned)(slice * cols + col) * 256 + t * 16;
+            b_odd[b] = (col & 1) ? 64u : 0u;
 #pragma unroll
             for (int c = 0; c < (P == 2 ? 1 : 2); ++c) {
                 const int r = min(P == 2 ? b * 4 + t : b * 8 + 2 * t + c, p.block - 1);
@@ -381,8 +399,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             cp_wait(S == 4);
             __syncwarp();
             copy_next();                       // into the slot that the step before read
-            const unsigned char* st = ring + slot;
-            slot = slot + WG_STEP == ring_bytes ? 0u : slot + WG_STEP;
+            const uint32_t ta = ring_at + slot + g * 64;
+            slot = (slot + WG_STEP) & (ring_bytes - 1u);
             // columns of B and tokens that there are not repeat others: what they give is not used
             float f[NB][P == 2 ? 1 : 2];       // the scales of the tokens of this lane's sums
 #pragma unroll
@@ -394,14 +412,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 }
             // the scales of rows g and g + 8 of each tile (none behind the last group)
             const bool in = g_first + (unsigned)i * g_hop < spitch;
-            const uint32_t sc[2] = {in ? use[0] | (use[1] << 16) : 0u, in ? use[2] | (use[3] << 16) : 0u};
-            const unsigned char* ta = st + g * 64;
+            const uint32_t sc[2] = {G == 128 || in ? __byte_perm(use[0], use[1], 0x5410) : 0u,
+                                    G == 128 || in ? __byte_perm(use[2], use[3], 0x5410) : 0u};
             uint32_t wa[2][4], wb[2][4];       // words of rows g and g + 8 of a tile, word c for MMAs 2c and 2c + 1
             if (G == 128) {
 #pragma unroll
                 for (int tile = 0; tile < 2; ++tile) {
-                    const uint4 a = *reinterpret_cast<const uint4*>(ta + tile * 1024 + t * 16);
-                    const uint4 b = *reinterpret_cast<const uint4*>(ta + tile * 1024 + 512 + t * 16);
+                    const uint4 a = lds16(ta + t * 16 + tile * 1024), b = lds16(ta + t * 16 + tile * 1024 + 512);
                     wa[tile][0] = a.x; wa[tile][1] = a.y; wa[tile][2] = a.z; wa[tile][3] = a.w;
                     wb[tile][0] = b.x; wb[tile][1] = b.y; wb[tile][2] = b.z; wb[tile][3] = b.w;
                 }
@@ -412,8 +429,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 if (G == 64) {
 #pragma unroll
                     for (int tile = 0; tile < 2; ++tile) {
-                        const int at = tile * 1024 + ((2 * gi + (t >> 1)) ^ swz) * 16 + (t & 1) * 8;
-                        const uint2 a = *reinterpret_cast<const uint2*>(ta + at), b = *reinterpret_cast<const uint2*>(ta + 512 + at);
+                        const uint32_t at = ta + ((2 * gi + (t >> 1)) ^ swz) * 16 + (t & 1) * 8 + tile * 1024;
+                        const uint2 a = lds8(at), b = lds8(at + 512);
                         wa[tile][2 * gi] = a.x; wa[tile][2 * gi + 1] = a.y;
                         wb[tile][2 * gi] = b.x; wb[tile][2 * gi + 1] = b.y;
                     }
@@ -424,14 +441,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     if (G == 32) {
 #pragma unroll
                         for (int tile = 0; tile < 2; ++tile) {
-                            const int at = tile * 1024 + (c ^ swz) * 16 + t * 4;
-                            wa[tile][c] = *reinterpret_cast<const uint32_t*>(ta + at);
-                            wb[tile][c] = *reinterpret_cast<const uint32_t*>(ta + 512 + at);
+                            const uint32_t at = ta + (c ^ swz) * 16 + t * 4 + tile * 1024;
+                            wa[tile][c] = lds4(at);
+                            wb[tile][c] = lds4(at + 512);
                         }
                     }
                     uint4 bf[NB];              // the B words of MMAs 2c and 2c + 1
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) bf[b] = *reinterpret_cast<const uint4*>(xs + b_at[b] + (unsigned)c * cols * 64);
+                    for (int b = 0; b < NB; ++b) bf[b] = lds16(b_at[b] + (c & 1 ? -b_odd[b] : b_odd[b]) + c * 64);
                     // (a second tile without rows holds zeros: its products cost less than a branch around them)
                     uint32_t pa[2][4], pb[2][4];
 #pragma unroll
