@@ -331,16 +331,10 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     auto residual_of = [&](int r, int n) -> float {
         return !GLU && p.residual ? w4_load1(p.residual, p.out_f32, (size_t)(tok0 + r) * p.residual_stride + n) : 0.f;
     };
-    // The joining of a row group's sums: four threads an output, item = ((set, token), row).  Each takes a part of the warps
-    constexpr int RG = GLU ? 16 : 32;          // rows of an item's row group
-    const int items = sets * m * RG;
-    auto item_of = [&](int it, int i, int& r, int& st2, int& row) -> int {   // the output row, or -1
-        row = i % RG;
-        st2 = i / RG / m;
-        r = i / RG - st2 * m;
-        const int n = row0 + (it * sets + st2) * GR + row;
-        return i < items && n < row1 ? n : -1;
-    };
+    // The joining of a row group's sums: four threads an output, each takes a part of the warps.  A thread's first output is
+    // row j_row of set j_set's row group, token j_tok; its next ones are J_NEXT (set, token) pairs further
+    constexpr int RG = GLU ? 16 : 32, J_NEXT = WG_THREADS / 4 / RG;
+    const int j_row = (tid >> 2) % RG, j_set = (tid >> 2) / RG / m, j_tok = (tid >> 2) / RG - j_set * m;
 
     // ---- the products ----
     // the scales of the step after this one: of row g in the low half, of row g + 8 in the high half, of group t (one of
@@ -365,9 +359,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         // the residual of the thread's first output, under the products
         float res = 0.f;
         if (!GLU && p.residual && p.ks == 1) {
-            int r, st2, row;
-            const int n = item_of(it, tid >> 2, r, st2, row);
-            if (n >= 0) res = residual_of(r, n);
+            const int n = row0 + (it * sets + j_set) * GR + j_row;
+            if (j_set < sets && n < row1) res = residual_of(j_tok, n);
         }
         float acc[2][NB][AC];
 #pragma unroll
@@ -517,13 +510,14 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                     rw[r * WG_PITCH + row] = acc[a][b][c];
                 }
         __syncthreads();
-        for (int i = tid >> 2; i - (int)(lane >> 2) < items; i += WG_THREADS / 4) {   // the same for the whole warp
-            int r, st2, row;
-            const int n = item_of(it, i, r, st2, row);
+        int r = j_tok, st2 = j_set;
+        for (bool first = true; __any_sync(0xffffffffu, st2 < sets); first = false) {
+            const int n = row0 + (it * sets + st2) * GR + j_row;
+            const bool live = st2 < sets && n < row1;
             float v = 0.f, u = 0.f;
-            if (n >= 0) {
+            if (live) {
                 for (int w = tid & 3; w < p.wk; w += 4) {
-                    const float* s = rb + ((size_t)(st2 * p.wk + w) * MT + r) * WG_PITCH + row;
+                    const float* s = rb + ((size_t)(st2 * p.wk + w) * MT + r) * WG_PITCH + j_row;
                     v += s[0];
                     if (GLU) u += s[16];
                 }
@@ -534,15 +528,16 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 u += __shfl_xor_sync(0xffffffffu, u, 1);
                 u += __shfl_xor_sync(0xffffffffu, u, 2);
             }
-            if (n >= 0 && (tid & 3) == 0) {
+            if (live && (tid & 3) == 0) {
                 if (p.ks == 1) {
-                    if (i != tid >> 2) res = residual_of(r, n);
+                    if (!first) res = residual_of(r, n);
                     finish(r, n, v, u, res);
                 } else {
                     sums[r * p.rows + n - row0] = v;
                     if (GLU) sums[(p.block + r) * p.rows + n - row0] = u;
                 }
             }
+            for (r += J_NEXT; r >= m; r -= m) ++st2;
         }
         // one buffer: the next row group's sums wait for this one's readers
         if (p.bufs == 1 && it + 1 < iters) __syncthreads();
