@@ -132,6 +132,7 @@ cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl) {
     a.residual_stride = c.residual_stride;
     a.out_stride = c.out_stride;
     a.eps = c.eps;
+    a.pdl = pdl;
     a.amax = g.amax;
     a.nonfinite = g.nonfinite;
     a.trace = g.trace;

@@ -47,7 +47,7 @@ struct W4GemvArgs {
     const uint8_t* codes[3];
     const __nv_bfloat16* scales[3];
     int end[3];                // rows of segments 0, 0 + 1, all
-    int N, K, tokens, block, wk, ks, rows, stages, bufs, act, x_f32, gain_f32, out_f32;
+    int N, K, tokens, block, wk, ks, rows, stages, bufs, act, x_f32, gain_f32, out_f32, pdl;
     const void* x;
     const void* gain;
     const void* residual;
@@ -108,7 +108,6 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     constexpr int GR = GLU ? 16 : 32;          // output rows of a row group
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ float ss_s[WG_WARPS][MT];
-    __shared__ float inv_s[MT];
     __shared__ unsigned long long best_s[8];
     __shared__ unsigned nonfinite_s[8];
 
@@ -210,82 +209,97 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         }
         cp_commit();
     };
-    for (int s = 0; s < S - 1; ++s) copy_next();   // the weights do not depend on the kernel before
-
-    pdl_wait();
+    // Activations are copied as they are to where their fragments will lie: a token's 128 values take no more room than
+    // their parts.  All copies are under way at once
+    const int nc = (ch1 - ch0 - warp + WG_WARPS - 1) / WG_WARPS;   // chunks that this warp makes fragments of
+    auto copy_x = [&]() {
+        const unsigned size = p.x_f32 ? 4u : 2u, row = (unsigned)p.K * size, first = (unsigned)(ch0 + warp) * 128u * size + 16u * lane;
+        const unsigned char* src = reinterpret_cast<const unsigned char*>(p.x) + (size_t)tok0 * p.x_stride * size;
+        const bool on = p.x_f32 || lane < 16;
+        for (int r = 0; r < m; ++r, src += (size_t)p.x_stride * size) {
+            uint32_t dst = smem_u32(xs) + (unsigned)(warp * cols + r * P) * 256u + 16u * lane;
+            unsigned at = first;
+            for (int j = 0; j < nc; ++j, at += WG_WARPS * 128u * size, dst += (unsigned)(WG_WARPS * cols) * 256u)
+                if (on) cp_async16(dst, src + at, at < row ? 16u : 0u);
+        }
+        cp_commit();
+    };
+    if (!p.pdl) {
+        copy_x();
+        for (int s = 0; s < S - 1; ++s) copy_next();
+    } else {
+        for (int s = 0; s < S - 1; ++s) copy_next();   // the weights do not depend on the kernel before
+        pdl_wait();
+        copy_x();
+    }
     if (tid == 0) trace_mark(tr, p.trace_id, 1);
 
     // ---- activations: each warp makes the fragments of every sixteenth chunk, all warps' are used by all ----
     {
-        const int nc = (ch1 - ch0 - warp + WG_WARPS - 1) / WG_WARPS;
-        const int total = nc > 0 ? nc * m : 0;
         const int w = lane >> 1;               // word of the chunk that the lane's four columns lie in
         const int bt = G == 128 ? w >> 2 : G == 64 ? (w >> 1) & 3 : w & 3;
         const int bq = G == 128 ? w & 3 : G == 64 ? ((w >> 3) << 1) | (w & 1) : w >> 2;
         const bool odd = lane & 1;
         float ss = 0.f;
-        // four values of a token's chunk at a time, three more under way
-        int r = 0, j = 0;                      // token and chunk of the next value to load
-        auto load = [&](float4& v, float4& gv) {
-            const int k = (ch0 + warp + j * WG_WARPS) * 128 + 4 * lane;
-            v = gv = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (r < m && k < p.K) {
-                v = w4_load4(p.x, p.x_f32, (size_t)(tok0 + r) * p.x_stride + k);
-                if (p.gain) gv = w4_load4(p.gain, p.gain_f32, k);
-            }
-            if (++j >= nc) { j = 0; ++r; }
+        if (p.pdl) asm volatile("cp.async.wait_group 0;" ::: "memory");
+        else if (S == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else asm volatile("cp.async.wait_group 1;" ::: "memory");
+        __syncwarp();
+        const int k0 = (ch0 + warp) * 128 + 4 * lane;
+        auto gain_of = [&](int j) {
+            const int k = k0 + j * WG_WARPS * 128;
+            return p.gain && j < nc && k < p.K ? w4_load4(p.gain, p.gain_f32, k) : make_float4(0.f, 0.f, 0.f, 0.f);
         };
-        float4 v0, v1, v2, v3, g0, g1, g2, g3;
-        if (total > 0) {
-            load(v0, g0);
-            load(v1, g1);
-            load(v2, g2);
-            load(v3, g3);
-        }
-        int cr = 0, cj = 0;                    // token and chunk at hand
+        for (int r = 0; r < m; ++r) {
+            float4 g0 = gain_of(0), g1 = gain_of(1);
+            unsigned char* o = xs + (size_t)(warp * cols + r * P) * 256;
+            float* fo = fs + warp * p.block + r;
 #pragma unroll 1
-        for (int b = 0; b < total; ++b) {
-            float4 x = v0;
-            if (p.gain) {
-                ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, ss))));
-                x.x *= g0.x; x.y *= g0.y; x.z *= g0.z; x.w *= g0.w;
-            }
-            v0 = v1; v1 = v2; v2 = v3;
-            g0 = g1; g1 = g2; g2 = g3;
-            load(v3, g3);
-            const uint32_t top = __reduce_max_sync(
-                0xffffffffu, max(max(w4_finite_bits(x.x), w4_finite_bits(x.y)), max(w4_finite_bits(x.z), w4_finite_bits(x.w))));
-            const int e = w4_exponent(top);
-            const float up = w4_up(e);
-            x.x *= up; x.y *= up; x.z *= up; x.w *= up;
-            const int ci = warp + cj * WG_WARPS;
-#pragma unroll
-            for (int part = 0; part < P; ++part) {
-                const uint32_t a01 = w4_pack_half(x.x, x.y), a23 = w4_pack_half(x.z, x.w);
-                const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&a01));
-                const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&a23));
-                const int col = cr * P + part;
-                const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a01 : a23, 1);
-                const uint32_t lo = odd ? got : a01, hi = odd ? a23 : got;     // columns j and j + 4 of the word
-                const uint2 f = make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
-                *reinterpret_cast<uint2*>(xs + ((size_t)(ci * cols + col) * 4 + (bq ^ (col & 1))) * 64 + bt * 16 + (odd ? 8 : 0)) = f;
-                // what the part leaves (nothing where it is not finite)
-                x.x -= f01.x; x.y -= f01.y; x.z -= f23.x; x.w -= f23.y;
-                x.x = isfinite(x.x) ? x.x : 0.f; x.y = isfinite(x.y) ? x.y : 0.f;
-                x.z = isfinite(x.z) ? x.z : 0.f; x.w = isfinite(x.w) ? x.w : 0.f;
-            }
-            if (lane == 0) fs[ci * p.block + cr] = w4_down(e);
-            if (++cj == nc) {
-                if (p.gain) {
-                    ss = warp_sum(ss);
-                    if (lane == 0) ss_s[warp][cr] = ss;
-                    ss = 0.f;
+            for (int j = 0; j < nc; ++j, o += (size_t)WG_WARPS * cols * 256, fo += WG_WARPS * p.block) {
+                float4 x;
+                if (p.x_f32) {
+                    x = *reinterpret_cast<const float4*>(o + 16 * lane);
+                } else {
+                    const uint2 b = *reinterpret_cast<const uint2*>(o + 8 * lane);
+                    x = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
                 }
-                cj = 0;
-                ++cr;
+                if (p.gain) {
+                    ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, ss))));
+                    x.x *= g0.x; x.y *= g0.y; x.z *= g0.z; x.w *= g0.w;
+                    g0 = g1;
+                    g1 = gain_of(j + 2);
+                }
+                // (the vote also has every lane's values read before any lane writes over them)
+                const uint32_t top = __reduce_max_sync(0xffffffffu, max(max(w4_finite_bits(x.x), w4_finite_bits(x.y)),
+                                                                        max(w4_finite_bits(x.z), w4_finite_bits(x.w))));
+                __syncwarp();
+                const int e = w4_exponent(top);
+                const float up = w4_up(e);
+                x.x *= up; x.y *= up; x.z *= up; x.w *= up;
+#pragma unroll
+                for (int part = 0; part < P; ++part) {
+                    const uint32_t a01 = w4_pack_half(x.x, x.y), a23 = w4_pack_half(x.z, x.w);
+                    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? a01 : a23, 1);
+                    const uint32_t lo = odd ? got : a01, hi = odd ? a23 : got;     // columns j and j + 4 of the word
+                    const int swap = (r * P + part) & 1;   // of an odd column
+                    *reinterpret_cast<uint2*>(o + part * 256 + (bq ^ swap) * 64 + bt * 16 + (odd ? 8 : 0)) =
+                        make_uint2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+                    if (part + 1 < P) {        // what the part leaves (nothing where it is not finite)
+                        const float2 f01 = __half22float2(*reinterpret_cast<const __half2*>(&a01));
+                        const float2 f23 = __half22float2(*reinterpret_cast<const __half2*>(&a23));
+                        x.x -= f01.x; x.y -= f01.y; x.z -= f23.x; x.w -= f23.y;
+                        x.x = isfinite(x.x) ? x.x : 0.f; x.y = isfinite(x.y) ? x.y : 0.f;
+                        x.z = isfinite(x.z) ? x.z : 0.f; x.w = isfinite(x.w) ? x.w : 0.f;
+                    }
+                }
+                if (lane == 0) *fo = w4_down(e);
+            }
+            if (p.gain) {
+                ss = warp_sum(ss);
+                if (lane == 0) ss_s[warp][r] = ss;
+                ss = 0.f;
             }
         }
-        if (p.gain && nc <= 0 && lane < m) ss_s[warp][lane] = 0.f;
         if (p.gain && p.ks > 1) {   // the other CTAs' columns, for the norm: a load of every token at a time
             __syncwarp();
             float s2[MT];
@@ -309,19 +323,27 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             }
         }
     }
-    __syncthreads();
+    // where all warps share the columns, a warp's chunks are those that it made itself
+    if (p.wk < WG_WARPS) __syncthreads();
+    else __syncwarp();
     pdl_trigger();
-    if (tid < m) {
-        float s = 0.f;
-        if (p.gain)
-            for (int w = 0; w < WG_WARPS; ++w) s += ss_s[w][tid];
-        inv_s[tid] = p.gain ? 1.0f / sqrtf(s / (float)p.K + p.eps) : 1.0f;   // read behind the next barrier
-    }
 
     // one output: gate / value v and up u, unscaled by the norm; its residual
+    float inv = 1.0f;                          // of the norm of token inv_of
+    int inv_of = -1;
     auto finish = [&](int r, int n, float v, float u, float res) {
-        v *= inv_s[r];
-        v = GLU ? w4_glu(p.act, v, u * inv_s[r]) : v + res;
+        if (p.gain) {                          // (behind a row group's barrier)
+            if (r != inv_of) {
+                float s = 0.f;
+#pragma unroll
+                for (int w = 0; w < WG_WARPS; ++w) s += ss_s[w][r];
+                inv = 1.0f / sqrtf(s / (float)p.K + p.eps);
+                inv_of = r;
+            }
+            v *= inv;
+            u *= inv;
+        }
+        v = GLU ? w4_glu(p.act, v, u) : v + res;
         w4_store1(p.out, p.out_f32, (size_t)(tok0 + r) * p.out_stride + n, v);
         if (!GLU && p.amax) {
             atomicMax(&best_s[r], argmax_key(v, n));
