@@ -27,7 +27,7 @@ const void* kernel_of(const W4Gemv& g) {
 size_t smem_of(const W4Gemv& g) {
     const int P = g.c.parts(), chunks = (g.c.k() + 127) / 128, most = (chunks + g.ks - 1) / g.ks;
     const size_t ring = (size_t)WG_WARPS * g.stages * WG_STEP, x = (size_t)most * g.block * P * 256;
-    const size_t f = ((size_t)most * g.block + 3) / 4 * 16;
+    const size_t f = ((size_t)most * g.block + 3) / 4 * 16 + (g.c.gain ? (size_t)most * 512 : 0);
     const size_t sums = g.ks > 1 ? sizeof(float) * (g.c.glu ? 2 : 1) * g.block * g.rows : 0;
     return ring + x + f + sums + sizeof(float) * g.bufs * WG_WARPS * wg_tokens(P, blocks_of(g)) * WG_PITCH;
 }

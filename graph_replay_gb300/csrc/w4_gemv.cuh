@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     unsigned char* ring = smem + (size_t)warp * ring_bytes;
     unsigned char* xs = smem + (size_t)WG_WARPS * ring_bytes;                // [chunk][cols][4][64 bytes], an odd column's words in pairs exchanged: no bank conflicts
     float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14)
-    float* red = fs + (((ch1 - ch0) * p.block + 3) & ~3);                             // [bufs][warp][MT][WG_PITCH]
+    unsigned char* gs = reinterpret_cast<unsigned char*>(fs + (((ch1 - ch0) * p.block + 3) & ~3));   // [chunk][512]: the gain
+    float* red = reinterpret_cast<float*>(gs + (p.gain ? (ch1 - ch0) * 512 : 0));   // [bufs][warp][MT][WG_PITCH]
     float* sums = red + p.bufs * WG_WARPS * MT * WG_PITCH;                   // ks > 1: [1 or 2][block][rows], read by the cluster
     const uint32_t ring_at = smem_u32(ring);
 
@@ -222,6 +223,13 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
             for (int j = 0; j < nc; ++j, at += WG_WARPS * 128u * size, dst += (unsigned)(WG_WARPS * cols) * 256u)
                 if (on) cp_async16(dst, src + at, at < row ? 16u : 0u);
         }
+        if (p.gain) {
+            const unsigned gsize = p.gain_f32 ? 4u : 2u, grow = (unsigned)p.K * gsize;
+            unsigned at = (unsigned)(ch0 + warp) * 128u * gsize + 16u * lane;
+            uint32_t dst = smem_u32(gs) + (unsigned)warp * 512u + 16u * lane;
+            for (int j = 0; j < nc; ++j, at += WG_WARPS * 128u * gsize, dst += WG_WARPS * 512u)
+                if (p.gain_f32 || lane < 16) cp_async16(dst, reinterpret_cast<const unsigned char*>(p.gain) + at, at < grow ? 16u : 0u);
+        }
         cp_commit();
     };
     if (!p.pdl) {
@@ -245,29 +253,22 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
         else if (S == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
         else asm volatile("cp.async.wait_group 1;" ::: "memory");
         __syncwarp();
-        const int k0 = (ch0 + warp) * 128 + 4 * lane;
-        auto gain_of = [&](int j) {
-            const int k = k0 + j * WG_WARPS * 128;
-            return p.gain && j < nc && k < p.K ? w4_load4(p.gain, p.gain_f32, k) : make_float4(0.f, 0.f, 0.f, 0.f);
+        auto four = [&](const unsigned char* at, bool f32) {   // this lane's four of 128 values
+            if (f32) return *reinterpret_cast<const float4*>(at + 16 * lane);
+            const uint2 b = *reinterpret_cast<const uint2*>(at + 8 * lane);
+            return make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
         };
         for (int r = 0; r < m; ++r) {
-            float4 g0 = gain_of(0), g1 = gain_of(1);
+            const unsigned char* go = gs + warp * 512;
             unsigned char* o = xs + (size_t)(warp * cols + r * P) * 256;
             float* fo = fs + warp * p.block + r;
 #pragma unroll 1
-            for (int j = 0; j < nc; ++j, o += (size_t)WG_WARPS * cols * 256, fo += WG_WARPS * p.block) {
-                float4 x;
-                if (p.x_f32) {
-                    x = *reinterpret_cast<const float4*>(o + 16 * lane);
-                } else {
-                    const uint2 b = *reinterpret_cast<const uint2*>(o + 8 * lane);
-                    x = make_float4(bf16_lo(b.x), bf16_hi(b.x), bf16_lo(b.y), bf16_hi(b.y));
-                }
+            for (int j = 0; j < nc; ++j, o += (size_t)WG_WARPS * cols * 256, fo += WG_WARPS * p.block, go += WG_WARPS * 512) {
+                float4 x = four(o, p.x_f32);
                 if (p.gain) {
+                    const float4 gv = four(go, p.gain_f32);
                     ss = fmaf(x.x, x.x, fmaf(x.y, x.y, fmaf(x.z, x.z, fmaf(x.w, x.w, ss))));
-                    x.x *= g0.x; x.y *= g0.y; x.z *= g0.z; x.w *= g0.w;
-                    g0 = g1;
-                    g1 = gain_of(j + 2);
+                    x.x *= gv.x; x.y *= gv.y; x.z *= gv.z; x.w *= gv.w;
                 }
                 // (the vote also has every lane's values read before any lane writes over them)
                 const uint32_t top = __reduce_max_sync(0xffffffffu, max(max(w4_finite_bits(x.x), w4_finite_bits(x.y)),
