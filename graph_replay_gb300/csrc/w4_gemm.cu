@@ -31,6 +31,16 @@
 // and each of them adds the sums of a part of the tokens from the others' shared memory,
 // in order.
 // Every wait is bounded; one that gives up sets FAULT_WAIT, and the CTA ends.
+//
+// Measured, in captures: 4095 bf16 tokens, 14336 -> 4096: 442 us, 1088 TFLOP/s (a library
+// product of 16-bit weights: 1927).  1000 fp32 tokens, gate and up 14336 x 4096: 577 us, 407
+// TFLOP/s of result, twice that in the tensor cores.  64 bf16 tokens, 4096 x 4096: 20.4 us.
+// Bound by making the weights: about 1300 clocks a step, 720 of them arithmetic (four warps a
+// scheduler) and 100 to 250 for each wait even when there is nothing to wait for, where the
+// MMAs of 128 tokens take 1024; the tensor pipe is active 42 % of a launch of 1024 tokens.
+// One row tile with 256 tokens would make half the weights for as many products, but reads its
+// activations twice as fast as one SM's share of L2 gives them; two such CTAs would have to
+// share each copy (not done).
 #include <cuda.h>
 #include "w4.cuh"
 #include "mma_helpers.cuh"
