@@ -229,7 +229,8 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms);
 cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl);
 struct W4Gemm {                // how w4_gemm.cu runs a call of many tokens
     W4Call c;                  // nw == 1, or glu
-    int nt;                    // tokens of a tile
+    int nt;                    // tokens of an accumulator
+    bool wide;                 // one row tile and two blocks of nt tokens a CTA, or two row tiles and one block
     int ks;                    // CTAs along k, a cluster
     int kp, steps;             // columns rounded up to 64; steps of 128
     void* ws;                  // w4_gemm_bytes()

@@ -51,16 +51,19 @@ namespace {
 
 constexpr int WM_DQ = 16;                      // warps that make weights, and write results: four warpgroups
 constexpr int WM_THREADS = (WM_DQ + 4) * 32;
-constexpr int WM_CODES = 2 * 128 * 64;         // bytes of a codes stage: two tiles of 128 rows x 128 columns
-constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 3;
+constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 4;
 constexpr int WM_SMEM = 200 * 1024;            // for both rings
 constexpr int WM_ROWS = 257;                   // of a split's sums of one token: 256, and one against bank conflicts
+constexpr double WIDE_MAKE = 600.0;
 constexpr int WM_FOLD = 4;                     // fp32 activations: steps of an accumulator
 
 // fp32 activations: stages of 64 columns (two parts), and half as many tokens
 constexpr int wm_tokens(int P) { return P == 2 ? 64 : 128; }
-constexpr int wm_halves(int P) { return P; }   // activation stages of a step
-constexpr int wm_stage(int P, int nt) { return nt * 256; }   // bytes: 128 columns of one part or 64 of two
+// WIDE: one tile and twice the tokens
+constexpr int wm_codes(bool wide) { return (wide ? 1 : 2) * 128 * 64; }         // bytes of a codes stage: 128 rows x 128 columns a tile
+constexpr int wm_halves(int P, bool wide) { return wide ? 2 : P; }              // activation stages of a step
+constexpr int wm_stage(int P, bool wide, int nt) { return nt * (wide && P == 2 ? 512 : 256); }   // bytes
+constexpr int wm_rows(bool glu, bool wide) { return (glu ? 128 : 256) >> (wide ? 1 : 0); }   // output rows of a CTA
 
 struct WmParams {
     CUtensorMap codes[2];      // [n, k / 2] bytes, box [64, 128], 64-byte swizzle
@@ -160,10 +163,14 @@ __device__ __forceinline__ uint32_t pick16(const uint4& w, int i) {   // element
 }
 
 // G: columns of a group; P: fp16 parts of an activation
-template <int G, int P, bool GLU>
+template <int G, int P, bool GLU, bool WIDE>
 __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant__ WmParams p) {
-    constexpr int ROWS = GLU ? 128 : 256;      // output rows of a CTA
-    constexpr int XH = wm_halves(P);           // activation stages of a step
+    constexpr int ROWS = wm_rows(GLU, WIDE), CODES = wm_codes(WIDE);
+    constexpr int XH = wm_halves(P, WIDE);     // activation stages of a step
+    constexpr int MAKERS = WIDE ? WM_DQ / 2 : WM_DQ;   // warps that make a step's weights
+    constexpr int EACH = WIDE ? 2 : 1;         // a warpgroup's steps lie so far apart
+    constexpr int AC = WIDE ? 64 : 128;        // TMEM columns of a step's weights
+    constexpr int APART = WIDE ? 1 : WM_FOLD / 2;   // steps between the two accumulators' turns to be folded
     constexpr bool FOLD = P == 2;
     constexpr int NS = G == 32 ? 2 : 1;        // scales of a thread's 64 columns
     extern __shared__ __align__(1024) unsigned char raw[];
@@ -172,18 +179,18 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     __shared__ __align__(8) uint64_t a_full[WM_MAX_SA], a_empty[WM_MAX_SA], d_full[2], d_empty[2];
     __shared__ uint32_t tmem;
     __shared__ int aborted;
-    __shared__ int row_e[2][128];
-    __shared__ float tok_f[128];
+    __shared__ int row_e[WIDE ? 1 : 2][128];
+    __shared__ float tok_f[WIDE ? 256 : 128];
     volatile int* ab = &aborted;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int split = blockIdx.x % p.ks, tile = blockIdx.x / p.ks, blk = blockIdx.y;
-    const int row0 = tile * ROWS, tok0 = blk * p.nt, m = min(p.nt, p.tokens - tok0);
+    const int row0 = tile * ROWS, nblk = WIDE ? 2 * p.nt : p.nt, tok0 = blk * nblk, m = min(nblk, p.tokens - tok0);
     const int s0 = (int)((long long)split * p.steps / p.ks), s1 = (int)((long long)(split + 1) * p.steps / p.ks);
     const int n = s1 - s0;                     // steps of this split, >= 1
-    const int xbytes = wm_stage(P, p.nt);
+    const int xbytes = wm_stage(P, WIDE, p.nt);
     unsigned char* codes_s = smem;
-    unsigned char* x_s = smem + (size_t)p.sc * WM_CODES;
+    unsigned char* x_s = smem + (size_t)p.sc * CODES;
     const int spitch = p.K / G;
 
     if (warp == 0) {
@@ -193,18 +200,18 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     if (tid == 32) {
         for (int s = 0; s < p.sc; ++s) {
             mbar_init(&codes_full[s], 1);
-            mbar_init(&codes_empty[s], WM_DQ);
+            mbar_init(&codes_empty[s], MAKERS);
         }
         for (int s = 0; s < p.sx; ++s) {
             mbar_init(&x_full[s], 1);
             mbar_init(&x_empty[s], 2);         // both issuing warps
         }
         for (int s = 0; s < p.sa; ++s) {
-            mbar_init(&a_full[s], WM_DQ);
+            mbar_init(&a_full[s], MAKERS);
             mbar_init(&a_empty[s], 2);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&d_full[s], 1);          // of a tile
+            mbar_init(&d_full[s], 1);          // of a tile, or of a half of the tokens
             mbar_init(&d_empty[s], WM_DQ / 2);
         }
         aborted = 0;
@@ -233,10 +240,11 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                     give_up();
                     break;
                 }
-                unsigned char* dst = codes_s + (size_t)r.slot * WM_CODES;
-                mbar_arrive_expect_tx(&codes_full[r.slot], WM_CODES);
+                unsigned char* dst = codes_s + (size_t)r.slot * CODES;
+                mbar_arrive_expect_tx(&codes_full[r.slot], CODES);
                 tma_load_2d(dst, &p.codes[0], (s0 + s) * 64, row0, &codes_full[r.slot]);
-                tma_load_2d(dst + WM_CODES / 2, &p.codes[1], (s0 + s) * 64, GLU ? row0 : row0 + 128, &codes_full[r.slot]);
+                if (GLU || !WIDE)
+                    tma_load_2d(dst + CODES / 2, &p.codes[1], (s0 + s) * 64, GLU ? row0 : row0 + 128, &codes_full[r.slot]);
                 issued = s + 1;
             }
             // no copy may still be landing when the CTA exits
@@ -259,9 +267,11 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 unsigned char* dst = x_s + (size_t)r.slot * xbytes;
                 mbar_arrive_expect_tx(&x_full[r.slot], (uint32_t)xbytes);
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    tma_load_2d(dst + i * p.nt * 128, &p.x, P == 2 ? (s0 * 2 + s) * 64 : (s0 + s) * 128 + i * 64,
-                                P == 2 ? i * p.tokens + tok0 : tok0, &x_full[r.slot]);
+                for (int i = 0; i < (WIDE ? 2 * P : 2); ++i) {
+                    const int part = P == 2 ? i & 1 : 0;   // WIDE: the halves of the tokens, of each its parts
+                    const int col = XH == 2 ? (s0 * 2 + s) * 64 : (s0 + s) * 128 + i * 64;
+                    tma_load_2d(dst + i * p.nt * 128, &p.x, col, part * p.tokens + tok0 + (WIDE ? i / P * p.nt : 0), &x_full[r.slot]);
+                }
                 issued = s + 1;
             }
             for (int s = max(0, issued - p.sx); s < issued; ++s)
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         const uint32_t idesc = (1u << 4) | ((uint32_t)(dcols >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
         const uint32_t xd = wm_desc(smem_u32(x_s)), half = (uint32_t)(p.nt * 128) >> 4;
         Ring ra, rx;
-        int fold = FOLD ? i * WM_FOLD / 2 : 0, used = 0;   // steps in the accumulator (the tiles in turn); times it was handed over
+        int fold = FOLD ? i * APART : 0, used = 0;   // steps in the accumulator (the tiles in turn); times it was handed over
         bool fresh = true;                     // it starts anew
         bool ok = true;
         for (int s = 0; s < n; ++s, ra.next(p.sa)) {
@@ -283,19 +293,19 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             ok = ok && mbar_wait(&x_full[rx.slot], rx.odd) && mbar_wait(&a_full[ra.slot], ra.odd);
             if (!__all_sync(0xffffffffu, ok)) break;
             fence_after();
-            const uint32_t a = at0 + (uint32_t)(ra.slot * 128 + i * 64);
+            const uint32_t a = at0 + (uint32_t)(ra.slot * AC + (WIDE ? 0 : i * 64));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (P == 2 && h == 1) {
+                if (XH == 2 && h == 1) {
                     ok = mbar_wait(&x_full[rx.slot], rx.odd);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     fence_after();
                 }
                 const uint32_t x = xd + (uint32_t)(rx.slot * (xbytes >> 4));
-                // B: half h of the stage, or (P == 2) a stage of 64 columns, both parts
-                mma_64(d, a + (uint32_t)(h * 32), x + (P == 1 ? h * half : 0u), idesc, fresh && h == 0 ? 0u : 1u);
-                if (P == 2 || h == 1) {
+                // B: half h of the stage, or a stage of 64 columns: both parts, or (WIDE) a half of the tokens
+                mma_64(d, a + (uint32_t)(h * 32), x + (XH == 1 ? h * half : WIDE ? i * P * half : 0u), idesc, fresh && h == 0 ? 0u : 1u);
+                if (XH == 2 || h == 1) {
                     commit(&x_empty[rx.slot]);
                     rx.next(p.sx);
                 }
@@ -314,16 +324,23 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     } else {
         // ---- weights ----
         const int wg = warp >> 2, r = (warp & 3) * 32 + lane;   // TMEM lane = tile row
-        const int mat = wg >> 1, h = wg & 1;                    // tile, half of the step's columns
+        // the accumulator that the warpgroup takes: its tile, or (WIDE) a half of the tokens, and then it makes the weights
+        // of every other step; half of the step's columns
+        const int mat = wg >> 1, h = wg & 1;
+        const bool second = WIDE ? r >= 64 : mat == 1;          // GLU: the row is of the up matrix
+        const int own = WIDE ? mat : 0;                         // its first step
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         // the rows' powers of two: a warp takes 16 rows, its lanes the scales of a row
         {
             const int g0 = s0 * (128 / G), g1 = min(spitch, s1 * (128 / G));
-            const int i = warp >> 3, first = row0 + (GLU ? 0 : i * 128);
-            const unsigned short* base = reinterpret_cast<const unsigned short*>(p.scales[i]);
+            constexpr int EACH_WARP = WIDE ? 8 : 16;            // rows of a warp
+            const int i = WIDE ? 0 : warp >> 3;
+            const bool up_rows = GLU && (WIDE ? warp >= 8 : i == 1);
+            const int first = row0 + (GLU ? (WIDE && up_rows ? -64 : 0) : i * 128);
+            const unsigned short* base = reinterpret_cast<const unsigned short*>(p.scales[GLU ? up_rows : i]);
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                const int rr = (warp & 7) * 16 + j;
+            for (int j = 0; j < EACH_WARP; ++j) {
+                const int rr = (WIDE ? warp : warp & 7) * EACH_WARP + j;
                 uint32_t top = 0;
                 if (first + rr < p.N) {
                     const unsigned short* s = base + (size_t)(first + rr) * spitch;
@@ -337,19 +354,19 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             }
         }
         named_sync(1, WM_DQ * 32);
-        const int nn = row0 + (GLU ? 0 : mat * 128) + r;        // this thread's row of its matrix
+        const int nn = row0 + (WIDE ? (GLU ? r & 63 : r) : (GLU ? 0 : mat * 128) + r);   // this thread's row of its matrix
         const bool in = nn < p.N;
-        const float up = row_up(row_e[mat][r]), down = row_down(row_e[mat][r]);
-        const unsigned short* sp = reinterpret_cast<const unsigned short*>(p.scales[mat]) + (size_t)(in ? nn : 0) * spitch;
+        const float up = row_up(row_e[WIDE ? 0 : mat][r]), down = row_down(row_e[WIDE ? 0 : mat][r]);
+        const unsigned short* sp = reinterpret_cast<const unsigned short*>(p.scales[GLU ? second : WIDE ? 0 : mat]) + (size_t)(in ? nn : 0) * spitch;
         // eight scales of the row at a time, the next eight under way
         constexpr int WIN = 8 * G / 128;       // steps of eight groups
         uint4 sw = make_uint4(0u, 0u, 0u, 0u), sn = sw;
         int left = 0;                          // steps that sw still serves
         auto load_win = [&](int w) { return w * 8 < spitch ? __ldg(reinterpret_cast<const uint4*>(sp) + w) : make_uint4(0u, 0u, 0u, 0u); };
         if (p.wide) {
-            sw = load_win(s0 / WIN);
-            sn = load_win(s0 / WIN + 1);
-            left = WIN - s0 % WIN;
+            sw = load_win((s0 + own) / WIN);
+            sn = load_win((s0 + own) / WIN + 1);
+            left = WIN - (s0 + own) % WIN;
         }
         // fp32 activations: the sums of 32 tokens of this thread's row; tokens 32 h .. 32 h + 31 of tile `mat`
         float acc[FOLD ? 32 : 1];
@@ -382,29 +399,34 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         uint32_t sixteen;                      // 16 in both halves, the code's sign bit turned over
         asm volatile("mov.b32 %0, 0x4e004e00;" : "=r"(sixteen));
         const int swz = (r >> 1) & 3;
-        const unsigned char* row = codes_s + mat * (WM_CODES / 2) + r * 64;
+        const unsigned char* row = codes_s + (WIDE ? 0 : mat * (CODES / 2)) + r * 64;
         const int c0 = ((2 * h) ^ swz) << 4, c1 = ((2 * h + 1) ^ swz) << 4;
         Ring rc, ra;
         bool ok = true;
         uint4 q0, q1;                          // a row's 32 bytes of codes
         auto read_codes = [&]() {
             ok = mbar_wait(&codes_full[rc.slot], rc.odd) && ok;
-            q0 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * WM_CODES + c0);
-            q1 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * WM_CODES + c1);
-            rc.next(p.sc);
+            q0 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * CODES + c0);
+            q1 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * CODES + c1);
+            // (WIDE: the rings' lengths are even, so a slot is always the same warpgroups')
+            for (int e = 0; e < EACH; ++e) rc.next(p.sc);
         };
-        int now = 0;                           // the slot that they came from
-        read_codes();
-        for (int s = 0; s < n; ++s, ra.next(p.sa)) {
+        if (own) {
+            rc.next(p.sc);
+            ra.next(p.sa);
+        }
+        int now = rc.slot;                     // the slot that they came from
+        if (own < n) read_codes();
+        for (int s = own; s < n; s += EACH) {
             const int step = s0 + s;
             uint32_t sc[NS];
             if (p.wide) {
-                if (left == 0) {
+                if (left <= 0) {
                     sw = sn;
                     sn = load_win(step / WIN + 1);
-                    left = WIN;
+                    left += WIN;
                 }
-                --left;
+                left -= EACH;
 #pragma unroll
                 for (int c = 0; c < NS; ++c)
                     sc[c] = scale_pair(pick16(sw, (G == 128 ? step : G == 64 ? 2 * step + h : 4 * step + 2 * h + c) & 7), up);
@@ -418,7 +440,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             const int codes_slot = now;
             now = rc.slot;
             const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-            if (s + 1 < n) read_codes();       // the next step's, under this one's arithmetic
+            if (s + EACH < n) read_codes();       // the next step's, under this one's arithmetic
             uint32_t a[32];
             {
                 uint32_t f24[NS];
@@ -430,7 +452,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             if (s >= p.sa) ok = mbar_wait(&a_empty[ra.slot], ra.odd ^ 1u) && ok;
             if (!__all_sync(0xffffffffu, ok)) break;
             fence_after();
-            tm_st32(at0 + lanes + (uint32_t)(ra.slot * 128 + mat * 64 + h * 32), a);
+            tm_st32(at0 + lanes + (uint32_t)(ra.slot * AC + (WIDE ? 0 : mat * 64) + h * 32), a);
             asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
             fence_before();
             __syncwarp();
@@ -440,8 +462,9 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 // could have come first
                 mbar_arrive(&codes_empty[codes_slot]);
             }
+            for (int e = 0; e < EACH; ++e) ra.next(p.sa);
             // the accumulator is taken when the weights of the step behind its last are made: its products have had that long
-            if (FOLD && s > 0 && (s + mat * (WM_FOLD / 2)) % WM_FOLD == 0) {
+            if (FOLD && s > 0 && (s + mat * APART) % WM_FOLD == 0) {
                 ok = fold_in();
                 if (!__all_sync(0xffffffffu, ok)) break;
             }
@@ -453,7 +476,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         for (int i = tid; i < m; i += WM_DQ * 32) tok_f[i] = __ldcg(p.factor + tok0 + i);
         bool live = __all_sync(0xffffffffu, ok) && !*ab;
         if (FOLD) {
-            const int times = (n - 1 + mat * (WM_FOLD / 2)) / WM_FOLD + 1;
+            const int times = (n - 1 + mat * APART) / WM_FOLD + 1;
             while (live && folded < times) live = __all_sync(0xffffffffu, fold_in());
         } else if (live) {
             live = __all_sync(0xffffffffu, mbar_wait(&d_full[mat], 0u));
@@ -462,15 +485,16 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         if (!live && lane == 0) give_up();
         named_sync(1, WM_DQ * 32);
         live = !*ab;
+        const int tb = WIDE ? mat * p.nt : 0, mh = WIDE ? min(p.nt, m - tb) : m;   // the accumulator's first token; its tokens
         // the smaller factor first: no step leaves fp32's range unless the result does
         auto sized = [&](float v, float b) { return v * fminf(down, b) * fmaxf(down, b); };
-        // the results of up to 16 tokens from token c of the block for output row nn: sums v (of the gate; then u of up)
+        // the results of up to 16 tokens from token c of the accumulator for output row nn: sums v (of the gate; then u of up)
         auto put16 = [&](int c, int count, float (&v)[16], float (&u)[16]) {
             if (GLU) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = w4_glu(p.act, v[e], u[e]);
             } else if (p.residual) {
-                const size_t at = (size_t)(tok0 + c) * p.residual_stride + nn;
+                const size_t at = (size_t)(tok0 + tb + c) * p.residual_stride + nn;
                 if (p.out_f32) {
                     const float* x = reinterpret_cast<const float*>(p.residual) + at;
 #pragma unroll
@@ -483,7 +507,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] += u[e];
             }
-            const size_t at = (size_t)(tok0 + c) * p.out_stride + nn;
+            const size_t at = (size_t)(tok0 + tb + c) * p.out_stride + nn;
             if (p.out_f32) {
                 float* o = reinterpret_cast<float*>(p.out) + at;
 #pragma unroll
@@ -499,19 +523,19 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         // Sums of 16 tokens from token c for this thread's row of its matrix.  Plain results go out from here; a gate's meet
         // the up's in shared memory, and a split's those of the other CTAs (in the rings: all copies have landed, all
         // weights are made, all products are done)
-        constexpr int US = 129;                // of a token's 128 rows
-        float* meet = reinterpret_cast<float*>(smem);            // [nt][US]
+        constexpr int US = ROWS + 1;           // GLU: of a token's rows
+        float* meet = reinterpret_cast<float*>(smem);            // [tokens][US]
         auto take16 = [&](int c, float (&v)[16]) {
-            const int count = min(16, m - c);
+            const int count = min(16, mh - c);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] = e < count ? sized(v[e], tok_f[c + e]) : 0.f;
-            if (p.ks > 1) {
+            for (int e = 0; e < 16; ++e) v[e] = e < count ? sized(v[e], tok_f[tb + c + e]) : 0.f;
+            if (!WIDE && p.ks > 1) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) meet[(c + e) * WM_ROWS + mat * 128 + r] = v[e];
             } else if (GLU) {
-                if (mat == 1) {
+                if (second) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) meet[(c + e) * US + r] = v[e];
+                    for (int e = 0; e < 16; ++e) meet[(tb + c + e) * US + r % ROWS] = v[e];
                 }
             } else if (in) {
                 float u[16];
@@ -534,33 +558,33 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 }
             }
         };
-        const int cfirst = FOLD ? h * 32 : h * 16, cstep = FOLD ? 16 : 32, cend = FOLD ? min(m, h * 32 + 32) : m;
+        const int cfirst = FOLD ? h * 32 : h * 16, cstep = FOLD ? 16 : 32, cend = FOLD ? min(mh, h * 32 + 32) : mh;
         if (live) {
             for (int c = cfirst; c < cend; c += cstep) {
                 float v[16];
-                if (GLU && p.ks == 1 && mat == 0) continue;      // up first
+                if (GLU && p.ks == 1 && !second) continue;       // up first
                 chunk(c, v);
                 take16(c, v);
             }
         }
         if (GLU && p.ks == 1) {
             named_sync(1, WM_DQ * 32);
-            if (live && mat == 0) {
+            if (live && !second) {
                 for (int c = cfirst; c < cend; c += cstep) {
                     float v[16], u[16];
-                    const int count = min(16, m - c);
+                    const int count = min(16, mh - c);
                     chunk(c, v);
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
-                        v[e] = e < count ? sized(v[e], tok_f[c + e]) : 0.f;
-                        u[e] = meet[(c + e) * US + r];
+                        v[e] = e < count ? sized(v[e], tok_f[tb + c + e]) : 0.f;
+                        u[e] = meet[(tb + c + e) * US + r];
                     }
                     if (in) put16(c, count, v, u);
                 }
             }
         }
     }
-    if (p.ks > 1) {
+    if (!WIDE && p.ks > 1) {
         cluster_sync();
         // the tokens of this CTA's part, a row a thread: the sums of all CTAs of the cluster, in their order
         const float* sums = reinterpret_cast<const float*>(smem);
@@ -681,18 +705,22 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, long lon
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int G, int P>
+const void* gemm_kernel(bool glu, bool wide) {
+    if (wide) return glu ? (const void*)&k_w4_gemm<G, P, true, true> : (const void*)&k_w4_gemm<G, P, false, true>;
+    return glu ? (const void*)&k_w4_gemm<G, P, true, false> : (const void*)&k_w4_gemm<G, P, false, false>;
+}
 template <int G>
-const void* gemm_kernel(int P, bool glu) {
-    if (P == 1) return glu ? (const void*)&k_w4_gemm<G, 1, true> : (const void*)&k_w4_gemm<G, 1, false>;
-    return glu ? (const void*)&k_w4_gemm<G, 2, true> : (const void*)&k_w4_gemm<G, 2, false>;
+const void* gemm_kernel(int P, bool glu, bool wide) {
+    return P == 1 ? gemm_kernel<G, 1>(glu, wide) : gemm_kernel<G, 2>(glu, wide);
 }
 
 const void* kernel_of(const W4Gemm& g) {
     const int P = g.c.x_f32 ? 2 : 1;
     switch (g.c.group()) {
-        case 32: return gemm_kernel<32>(P, g.c.glu);
-        case 64: return gemm_kernel<64>(P, g.c.glu);
-        default: return gemm_kernel<128>(P, g.c.glu);
+        case 32: return gemm_kernel<32>(P, g.c.glu, g.wide);
+        case 64: return gemm_kernel<64>(P, g.c.glu, g.wide);
+        default: return gemm_kernel<128>(P, g.c.glu, g.wide);
     }
 }
 
@@ -703,7 +731,7 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
     const W4Call& c = g->c;
-    const int P = c.x_f32 ? 2 : 1, rows = c.glu ? 128 : 256;
+    const int P = c.x_f32 ? 2 : 1, rows = wm_rows(c.glu, false);
     const int tiles = (c.n() + rows - 1) / rows, steps = (c.k() + 127) / 128;
     // Tokens of a tile and CTAs along k: the least time of the longest CTA, in clocks.  A step takes the tensor cores 8
     // clocks a token and part, or the making and handing over of its weights 900; a CTA starts and ends in about 7000,
@@ -716,21 +744,40 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
             if (ks > 1 && steps / ks < 2) break;
             const long long places = ks == 1 ? num_sms : w4_clusters(ks, num_sms);
             const double waves = (double)(((long long)tiles * used + places - 1) / places);
-            const double step = 8.0 * nt * P > 900.0 ? 8.0 * nt * P : 900.0;
+            const double step = 8.0 * nt * P > 900.0 ? 8.0 * nt * P * 1.4 : 900.0;
             const double t = waves * ((double)((steps + ks - 1) / ks) * step + 7000.0 + 16.0 * nt) + (ks > 1 ? 2000.0 + 8.0 * nt : 0.0);
             if (best < 0.0 || t < best) {
                 best = t;
                 g->nt = nt;
                 g->ks = ks;
+                g->wide = false;
             }
         }
         if (nt <= 16) break;
     }
+    // the same with one tile and twice the tokens: half the weights to make
+    if (c.tokens > wm_tokens(P)) {
+        const int wrows = wm_rows(c.glu, true), wtiles = (c.n() + wrows - 1) / wrows, two = 2 * wm_tokens(P);
+        const int wleast = (c.tokens + two - 1) / two;
+        for (int blocks = wleast; blocks <= wleast + 8; ++blocks) {
+            const int nt = round_up((c.tokens + 2 * blocks - 1) / (2 * blocks), 16), used = (c.tokens + 2 * nt - 1) / (2 * nt);
+            const double waves = (double)(((long long)wtiles * used + num_sms - 1) / num_sms);
+            const double step = 8.0 * nt * P > WIDE_MAKE ? 8.0 * nt * P : WIDE_MAKE;
+            const double t = waves * ((double)steps * step + 7000.0 + 32.0 * nt);
+            if (t < best) {
+                best = t;
+                g->nt = nt;
+                g->ks = 1;
+                g->wide = true;
+            }
+            if (nt <= 16) break;
+        }
+    }
     g->kp = round_up(c.k(), 64);
     g->steps = steps;
     const void* fn = kernel_of(*g);
-    static OncePerDevice once[3][2][2];
-    return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][P - 1][c.glu].run([&] { return raise_smem_cap(fn); });
+    static OncePerDevice once[3][2][2][2];
+    return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][P - 1][c.glu][g->wide].run([&] { return raise_smem_cap(fn); });
 }
 
 size_t w4_gemm_bytes(const W4Gemm& g) {
@@ -747,7 +794,7 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     WmParams p{};
     for (int i = 0; i < 2; ++i) {
         const W4Matrix& w = c.w[i < mats ? i : 0];
-        if (!encode(&p.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.n, w.k / 2, w.k / 2, 64, 128, CU_TENSOR_MAP_SWIZZLE_64B))
+        if (!encode(&p.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.n, w.k / 2, w.k / 2, 64, g.wide && c.glu ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
         p.scales[i] = (const __nv_bfloat16*)w.scales;
     }
@@ -770,14 +817,18 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     p.wide = (c.k() / c.group()) % 8 == 0 && ((uintptr_t)p.scales[0] & 15) == 0 && ((uintptr_t)p.scales[1] & 15) == 0;
     p.err = c.err;
     // the rings: four stages of codes at least (behind the last step they also hold a tile's up sums), then activations
-    const int xb = wm_stage(P, g.nt);
-    p.sx = (WM_SMEM - 5 * WM_CODES) / xb;
+    const int xb = wm_stage(P, g.wide, g.nt), cb = wm_codes(g.wide);
+    p.sx = (WM_SMEM - 5 * cb) / xb;
     if (p.sx > WM_MAX_SX) p.sx = WM_MAX_SX;
-    p.sc = (WM_SMEM - p.sx * xb) / WM_CODES;
+    p.sc = (WM_SMEM - p.sx * xb) / cb;
     if (p.sc > WM_MAX_SC) p.sc = WM_MAX_SC;
-    p.sa = (512 - 2 * g.nt * P) / 128;
+    p.sa = (512 - 2 * g.nt * P) / (g.wide ? 64 : 128);
     if (p.sa > WM_MAX_SA) p.sa = WM_MAX_SA;
-    if (p.sx < 2 || p.sc < 5 || p.sa < 2) return cudaErrorInvalidValue;
+    if (g.wide) {                              // even
+        p.sc &= ~1;
+        p.sa &= ~1;
+    }
+    if (p.sx < 2 || p.sc < 4 || p.sa < 2) return cudaErrorInvalidValue;
 
     if (P == 1)
         k_w4_split<1><<<c.tokens, WS_THREADS, 0, s>>>(c.x, c.x_stride, c.x_f32, c.gain, c.gain_f32, c.eps, c.k(), g.kp, c.tokens, parts, factor);
@@ -786,10 +837,10 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    const int rows = c.glu ? 128 : 256;
-    cfg.gridDim = dim3((c.n() + rows - 1) / rows * g.ks, (c.tokens + g.nt - 1) / g.nt);
+    const int rows = wm_rows(c.glu, g.wide), block = g.wide ? 2 * g.nt : g.nt;
+    cfg.gridDim = dim3((c.n() + rows - 1) / rows * g.ks, (c.tokens + block - 1) / block);
     cfg.blockDim = dim3(WM_THREADS);
-    cfg.dynamicSmemBytes = (size_t)p.sx * xb + (size_t)p.sc * WM_CODES + 1024;
+    cfg.dynamicSmemBytes = (size_t)p.sx * xb + (size_t)p.sc * cb + 1024;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];   // starts while k_w4_split runs: codes and scales do not depend on it
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
