@@ -10,7 +10,7 @@
 //
 //   k_w4_split   one CTA a token: RMSNorm's sum, the token's power of two, its parts in
 //                the column order in which the words of codes come apart (w4.cuh).
-//   k_w4_gemm    A = two tiles of 128 output rows (TMEM lanes): 256 rows of one matrix, or
+//   k_w4_gemm    A = two tiles (WIDE: one) of 128 output rows (TMEM lanes): 256 rows of one matrix, or
 //                128 rows each of gate and up; B = up to 128 tokens, read from shared memory
 //                once for both.  A step is 128 columns:
 //     warps 0-15 a warpgroup takes one tile and one half of the step's columns: a thread has
@@ -33,14 +33,13 @@
 // Every wait is bounded; one that gives up sets FAULT_WAIT, and the CTA ends.
 //
 // Measured, in captures: 4095 bf16 tokens, 14336 -> 4096: 442 us, 1088 TFLOP/s (a library
-// product of 16-bit weights: 1927).  1000 fp32 tokens, gate and up 14336 x 4096: 577 us, 407
+// product of 16-bit weights: 1918).  1000 fp32 tokens, gate and up 14336 x 4096: 500 us, 470
 // TFLOP/s of result, twice that in the tensor cores.  64 bf16 tokens, 4096 x 4096: 20.4 us.
-// Bound by making the weights: about 1300 clocks a step, 720 of them arithmetic (four warps a
-// scheduler) and 100 to 250 for each wait even when there is nothing to wait for, where the
-// MMAs of 128 tokens take 1024; the tensor pipe is active 42 % of a launch of 1024 tokens.
-// One row tile with 256 tokens would make half the weights for as many products, but reads its
-// activations twice as fast as one SM's share of L2 gives them; two such CTAs would have to
-// share each copy (not done).
+// A step takes about 1700 clocks, the MMAs of 128 tokens 1024 of them; making the weights takes
+// 1300 (720 of them arithmetic, four warps a scheduler, and 100 to 250 for each wait even when
+// there is nothing to wait for).  The tensor pipe is active 42 % of a launch of 1024 tokens.
+// Many fp32 tokens (WIDE): one row tile and two blocks of tokens a CTA, 64 gate and 64 up rows;
+// two of the warpgroups make a step's weights, the other two the next step's.
 #include <cuda.h>
 #include "w4.cuh"
 #include "mma_helpers.cuh"
@@ -54,19 +53,17 @@ constexpr int WM_THREADS = (WM_DQ + 4) * 32;
 constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 4;
 constexpr int WM_SMEM = 200 * 1024;            // for both rings
 constexpr int WM_ROWS = 257;                   // of a split's sums of one token: 256, and one against bank conflicts
-constexpr double WIDE_MAKE = 600.0;
 constexpr int WM_FOLD = 4;                     // fp32 activations: steps of an accumulator
 
 // fp32 activations: stages of 64 columns (two parts), and half as many tokens
 constexpr int wm_tokens(int P) { return P == 2 ? 64 : 128; }
-// WIDE: one tile and twice the tokens
-constexpr int wm_codes(bool wide) { return (wide ? 1 : 2) * 128 * 64; }         // bytes of a codes stage: 128 rows x 128 columns a tile
-constexpr int wm_halves(int P, bool wide) { return wide ? 2 : P; }              // activation stages of a step
-constexpr int wm_stage(int P, bool wide, int nt) { return nt * (wide && P == 2 ? 512 : 256); }   // bytes
+// wide (fp32 activations): one row tile and two blocks of tokens
+constexpr int wm_codes(bool wide) { return (wide ? 1 : 2) * 128 * 64; }   // bytes of a codes stage: 128 rows x 128 columns a tile
+constexpr int wm_stage(bool wide, int nt) { return nt * (wide ? 512 : 256); }   // bytes: 128 columns of one part or 64 of two
 constexpr int wm_rows(bool glu, bool wide) { return (glu ? 128 : 256) >> (wide ? 1 : 0); }   // output rows of a CTA
 
 struct WmParams {
-    CUtensorMap codes[2];      // [n, k / 2] bytes, box [64, 128], 64-byte swizzle
+    CUtensorMap codes[2];      // [n, k / 2] bytes, box [64, 128] (WIDE and GLU: [64, 64]), 64-byte swizzle
     CUtensorMap x;             // [parts * tokens, kp] fp16, box [64, nt], 128-byte swizzle
     const __nv_bfloat16* scales[2];
     const float* factor;       // [tokens]
@@ -162,11 +159,12 @@ __device__ __forceinline__ uint32_t pick16(const uint4& w, int i) {   // element
     return i & 1 ? v >> 16 : v & 0xffffu;
 }
 
-// G: columns of a group; P: fp16 parts of an activation
+// G: columns of a group; P: fp16 parts of an activation; WIDE: one row tile and two blocks of tokens
 template <int G, int P, bool GLU, bool WIDE>
 __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant__ WmParams p) {
     constexpr int ROWS = wm_rows(GLU, WIDE), CODES = wm_codes(WIDE);
-    constexpr int XH = wm_halves(P, WIDE);     // activation stages of a step
+    static_assert(P == 2 || !WIDE, "");
+    constexpr int XH = P;                      // activation stages of a step
     constexpr int MAKERS = WIDE ? WM_DQ / 2 : WM_DQ;   // warps that make a step's weights
     constexpr int EACH = WIDE ? 2 : 1;         // a warpgroup's steps lie so far apart
     constexpr int AC = WIDE ? 64 : 128;        // TMEM columns of a step's weights
@@ -188,7 +186,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     const int row0 = tile * ROWS, nblk = WIDE ? 2 * p.nt : p.nt, tok0 = blk * nblk, m = min(nblk, p.tokens - tok0);
     const int s0 = (int)((long long)split * p.steps / p.ks), s1 = (int)((long long)(split + 1) * p.steps / p.ks);
     const int n = s1 - s0;                     // steps of this split, >= 1
-    const int xbytes = wm_stage(P, WIDE, p.nt);
+    const int xbytes = wm_stage(WIDE, p.nt);
     unsigned char* codes_s = smem;
     unsigned char* x_s = smem + (size_t)p.sc * CODES;
     const int spitch = p.K / G;
@@ -211,7 +209,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             mbar_init(&a_empty[s], 2);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(&d_full[s], 1);          // of a tile, or of a half of the tokens
+            mbar_init(&d_full[s], 1);          // of a tile, or (WIDE) of a block of tokens
             mbar_init(&d_empty[s], WM_DQ / 2);
         }
         aborted = 0;
@@ -267,11 +265,9 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 unsigned char* dst = x_s + (size_t)r.slot * xbytes;
                 mbar_arrive_expect_tx(&x_full[r.slot], (uint32_t)xbytes);
 #pragma unroll
-                for (int i = 0; i < (WIDE ? 2 * P : 2); ++i) {
-                    const int part = P == 2 ? i & 1 : 0;   // WIDE: the halves of the tokens, of each its parts
-                    const int col = XH == 2 ? (s0 * 2 + s) * 64 : (s0 + s) * 128 + i * 64;
-                    tma_load_2d(dst + i * p.nt * 128, &p.x, col, part * p.tokens + tok0 + (WIDE ? i / P * p.nt : 0), &x_full[r.slot]);
-                }
+                for (int i = 0; i < (WIDE ? 4 : 2); ++i)   // WIDE: of each block of tokens both parts
+                    tma_load_2d(dst + i * p.nt * 128, &p.x, P == 2 ? (s0 * 2 + s) * 64 : (s0 + s) * 128 + i * 64,
+                                P == 2 ? (i & 1) * p.tokens + tok0 + (i >> 1) * p.nt : tok0, &x_full[r.slot]);
                 issued = s + 1;
             }
             for (int s = max(0, issued - p.sx); s < issued; ++s)
@@ -296,16 +292,16 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             const uint32_t a = at0 + (uint32_t)(ra.slot * AC + (WIDE ? 0 : i * 64));
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (XH == 2 && h == 1) {
+                if (P == 2 && h == 1) {
                     ok = mbar_wait(&x_full[rx.slot], rx.odd);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
                     fence_after();
                 }
                 const uint32_t x = xd + (uint32_t)(rx.slot * (xbytes >> 4));
-                // B: half h of the stage, or a stage of 64 columns: both parts, or (WIDE) a half of the tokens
-                mma_64(d, a + (uint32_t)(h * 32), x + (XH == 1 ? h * half : WIDE ? i * P * half : 0u), idesc, fresh && h == 0 ? 0u : 1u);
-                if (XH == 2 || h == 1) {
+                // B: half h of the stage, or (P == 2) a stage of 64 columns, both parts, WIDE: of a block of tokens
+                mma_64(d, a + (uint32_t)(h * 32), x + (P == 1 ? h * half : WIDE ? i * P * half : 0u), idesc, fresh && h == 0 ? 0u : 1u);
+                if (P == 2 || h == 1) {
                     commit(&x_empty[rx.slot]);
                     rx.next(p.sx);
                 }
@@ -324,7 +320,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     } else {
         // ---- weights ----
         const int wg = warp >> 2, r = (warp & 3) * 32 + lane;   // TMEM lane = tile row
-        // the accumulator that the warpgroup takes: its tile, or (WIDE) a half of the tokens, and then it makes the weights
+        // the accumulator that the warpgroup takes: of its tile, or (WIDE) of a block of tokens, and then it makes the weights
         // of every other step; half of the step's columns
         const int mat = wg >> 1, h = wg & 1;
         const bool second = WIDE ? r >= 64 : mat == 1;          // GLU: the row is of the up matrix
@@ -705,14 +701,11 @@ bool encode(CUtensorMap* m, CUtensorMapDataType type, const void* base, long lon
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int G, int P>
-const void* gemm_kernel(bool glu, bool wide) {
-    if (wide) return glu ? (const void*)&k_w4_gemm<G, P, true, true> : (const void*)&k_w4_gemm<G, P, false, true>;
-    return glu ? (const void*)&k_w4_gemm<G, P, true, false> : (const void*)&k_w4_gemm<G, P, false, false>;
-}
 template <int G>
 const void* gemm_kernel(int P, bool glu, bool wide) {
-    return P == 1 ? gemm_kernel<G, 1>(glu, wide) : gemm_kernel<G, 2>(glu, wide);
+    if (wide) return glu ? (const void*)&k_w4_gemm<G, 2, true, true> : (const void*)&k_w4_gemm<G, 2, false, true>;
+    if (P == 1) return glu ? (const void*)&k_w4_gemm<G, 1, true, false> : (const void*)&k_w4_gemm<G, 1, false, false>;
+    return glu ? (const void*)&k_w4_gemm<G, 2, true, false> : (const void*)&k_w4_gemm<G, 2, false, false>;
 }
 
 const void* kernel_of(const W4Gemm& g) {
@@ -744,40 +737,34 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
             if (ks > 1 && steps / ks < 2) break;
             const long long places = ks == 1 ? num_sms : w4_clusters(ks, num_sms);
             const double waves = (double)(((long long)tiles * used + places - 1) / places);
-            const double step = 8.0 * nt * P > 900.0 ? 8.0 * nt * P * 1.4 : 900.0;
+            const double step = 8.0 * nt * P > 900.0 ? 8.0 * nt * P : 900.0;
             const double t = waves * ((double)((steps + ks - 1) / ks) * step + 7000.0 + 16.0 * nt) + (ks > 1 ? 2000.0 + 8.0 * nt : 0.0);
             if (best < 0.0 || t < best) {
                 best = t;
                 g->nt = nt;
                 g->ks = ks;
-                g->wide = false;
             }
         }
         if (nt <= 16) break;
     }
-    // the same with one tile and twice the tokens: half the weights to make
-    if (c.tokens > wm_tokens(P)) {
-        const int wrows = wm_rows(c.glu, true), wtiles = (c.n() + wrows - 1) / wrows, two = 2 * wm_tokens(P);
-        const int wleast = (c.tokens + two - 1) / two;
-        for (int blocks = wleast; blocks <= wleast + 8; ++blocks) {
-            const int nt = round_up((c.tokens + 2 * blocks - 1) / (2 * blocks), 16), used = (c.tokens + 2 * nt - 1) / (2 * nt);
-            const double waves = (double)(((long long)wtiles * used + num_sms - 1) / num_sms);
-            const double step = 8.0 * nt * P > WIDE_MAKE ? 8.0 * nt * P : WIDE_MAKE;
-            const double t = waves * ((double)steps * step + 7000.0 + 32.0 * nt);
-            if (t < best) {
-                best = t;
-                g->nt = nt;
-                g->ks = 1;
-                g->wide = true;
-            }
-            if (nt <= 16) break;
+    // fp32 activations: with one row tile and two blocks of tokens a CTA makes half the weights for as many products. It has
+    // no split along k, so it is for calls whose tiles fill most of the card: 1000 tokens, gate and up 14336 x 4096, take 500 us
+    // against 577, 1024 tokens 4096 x 4096 81 against 97. With bf16 ones it gains nothing: 4095 tokens 14336 -> 4096 take 453
+    // against 442
+    if (P == 2 && c.tokens > wm_tokens(P)) {
+        const int two = 2 * wm_tokens(P), blocks = (c.tokens + two - 1) / two;
+        const int wide = (c.n() + wm_rows(c.glu, true) - 1) / wm_rows(c.glu, true);
+        if ((long long)wide * blocks * 4 >= 3ll * num_sms) {
+            g->nt = round_up((c.tokens + 2 * blocks - 1) / (2 * blocks), 16);
+            g->ks = 1;
+            g->wide = true;
         }
     }
     g->kp = round_up(c.k(), 64);
     g->steps = steps;
     const void* fn = kernel_of(*g);
-    static OncePerDevice once[3][2][2][2];
-    return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][P - 1][c.glu][g->wide].run([&] { return raise_smem_cap(fn); });
+    static OncePerDevice once[3][3][2];
+    return once[c.group() == 32 ? 0 : c.group() == 64 ? 1 : 2][g->wide ? 2 : P - 1][c.glu].run([&] { return raise_smem_cap(fn); });
 }
 
 size_t w4_gemm_bytes(const W4Gemm& g) {
@@ -794,7 +781,8 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     WmParams p{};
     for (int i = 0; i < 2; ++i) {
         const W4Matrix& w = c.w[i < mats ? i : 0];
-        if (!encode(&p.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.n, w.k / 2, w.k / 2, 64, g.wide && c.glu ? 64 : 128, CU_TENSOR_MAP_SWIZZLE_64B))
+        if (!encode(&p.codes[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, w.codes, w.n, w.k / 2, w.k / 2, 64, g.wide && c.glu ? 64 : 128,
+                    CU_TENSOR_MAP_SWIZZLE_64B))
             return cudaErrorInvalidValue;
         p.scales[i] = (const __nv_bfloat16*)w.scales;
     }
@@ -817,14 +805,14 @@ cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     p.wide = (c.k() / c.group()) % 8 == 0 && ((uintptr_t)p.scales[0] & 15) == 0 && ((uintptr_t)p.scales[1] & 15) == 0;
     p.err = c.err;
     // the rings: four stages of codes at least (behind the last step they also hold a tile's up sums), then activations
-    const int xb = wm_stage(P, g.wide, g.nt), cb = wm_codes(g.wide);
+    const int xb = wm_stage(g.wide, g.nt), cb = wm_codes(g.wide);
     p.sx = (WM_SMEM - 5 * cb) / xb;
     if (p.sx > WM_MAX_SX) p.sx = WM_MAX_SX;
     p.sc = (WM_SMEM - p.sx * xb) / cb;
     if (p.sc > WM_MAX_SC) p.sc = WM_MAX_SC;
     p.sa = (512 - 2 * g.nt * P) / (g.wide ? 64 : 128);
     if (p.sa > WM_MAX_SA) p.sa = WM_MAX_SA;
-    if (g.wide) {                              // even
+    if (g.wide) {                              // even: a warpgroup makes every other step's weights
         p.sc &= ~1;
         p.sa &= ~1;
     }
