@@ -404,23 +404,23 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             ok = mbar_wait(&codes_full[rc.slot], rc.odd) && ok;
             q0 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * CODES + c0);
             q1 = *reinterpret_cast<const uint4*>(row + (size_t)rc.slot * CODES + c1);
-            // (WIDE: the rings' lengths are even, so a slot is always the same warpgroups')
-            for (int e = 0; e < EACH; ++e) rc.next(p.sc);
+            rc.next(p.sc);
+            if (WIDE) rc.next(p.sc);           // the rings' lengths are even, so a slot is always the same warpgroups'
         };
-        if (own) {
+        if (WIDE && own) {
             rc.next(p.sc);
             ra.next(p.sa);
         }
-        int now = rc.slot;                     // the slot that they came from
-        if (own < n) read_codes();
-        for (int s = own; s < n; s += EACH) {
+        int now = WIDE ? rc.slot : 0;          // the slot that they came from
+        if (!WIDE || own < n) read_codes();
+        for (int s = own; s < n; s += EACH, ra.next(p.sa)) {
             const int step = s0 + s;
             uint32_t sc[NS];
             if (p.wide) {
-                if (left <= 0) {
+                if (WIDE ? left <= 0 : left == 0) {
                     sw = sn;
                     sn = load_win(step / WIN + 1);
-                    left += WIN;
+                    left = WIDE ? left + WIN : WIN;
                 }
                 left -= EACH;
 #pragma unroll
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             const int codes_slot = now;
             now = rc.slot;
             const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-            if (s + EACH < n) read_codes();       // the next step's, under this one's arithmetic
+            if (s + EACH < n) read_codes();    // its next step's, under this one's arithmetic
             uint32_t a[32];
             {
                 uint32_t f24[NS];
@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 // could have come first
                 mbar_arrive(&codes_empty[codes_slot]);
             }
-            for (int e = 0; e < EACH; ++e) ra.next(p.sa);
+            if (WIDE) ra.next(p.sa);
             // the accumulator is taken when the weights of the step behind its last are made: its products have had that long
             if (FOLD && s > 0 && (s + mat * APART) % WM_FOLD == 0) {
                 ok = fold_in();
