@@ -747,17 +747,25 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
         }
         if (nt <= 16) break;
     }
-    // fp32 activations: with one row tile and two blocks of tokens a CTA makes half the weights for as many products. It has
-    // no split along k, so it is for calls whose tiles fill most of the card: 1000 tokens, gate and up 14336 x 4096, take 500 us
-    // against 577, 1024 tokens 4096 x 4096 81 against 97. With bf16 ones it gains nothing: 4095 tokens 14336 -> 4096 take 453
-    // against 442
+    // fp32 activations: with one row tile and two blocks of tokens a CTA makes half the weights for as many products, and a
+    // step takes 0.8 of the time; but it has no split along k, and the tiles have to fill the card. 1000 tokens, gate and up
+    // 14336 x 4096, take 500 us against 577, 1024 tokens 4096 x 4096 81 against 97; 520 tokens 14336 -> 4096, two waves half
+    // full, 248 against 160. With bf16 ones it gains nothing: 4095 tokens 14336 -> 4096 take 453 against 442
     if (P == 2 && c.tokens > wm_tokens(P)) {
-        const int two = 2 * wm_tokens(P), blocks = (c.tokens + two - 1) / two;
+        const int two = 2 * wm_tokens(P), few = (c.tokens + two - 1) / two;
         const int wide = (c.n() + wm_rows(c.glu, true) - 1) / wm_rows(c.glu, true);
-        if ((long long)wide * blocks * 4 >= 3ll * num_sms) {
-            g->nt = round_up((c.tokens + 2 * blocks - 1) / (2 * blocks), 16);
-            g->ks = 1;
-            g->wide = true;
+        for (int blocks = few; blocks <= few + 8; ++blocks) {
+            const int nt = round_up((c.tokens + 2 * blocks - 1) / (2 * blocks), 16), used = (c.tokens + 2 * nt - 1) / (2 * nt);
+            const double waves = (double)(((long long)wide * used + num_sms - 1) / num_sms);
+            const double step = 16.0 * nt > 900.0 ? 16.0 * nt : 900.0;
+            const double t = waves * (0.8 * (double)steps * step + 7000.0 + 32.0 * nt);
+            if (t < best) {
+                best = t;
+                g->nt = nt;
+                g->ks = 1;
+                g->wide = true;
+            }
+            if (nt <= 16) break;
         }
     }
     g->kp = round_up(c.k(), 64);
