@@ -33,7 +33,7 @@
 // Every wait is bounded; one that gives up sets FAULT_WAIT, and the CTA ends.
 //
 // Measured, in captures: 4095 bf16 tokens, 14336 -> 4096: 442 us, 1088 TFLOP/s (a library
-// product of 16-bit weights: 1918).  1000 fp32 tokens, gate and up 14336 x 4096: 500 us, 470
+// product of 16-bit weights: 1918).  1000 fp32 tokens, gate and up 14336 x 4096: 510 us, 460
 // TFLOP/s of result, twice that in the tensor cores.  64 bf16 tokens, 4096 x 4096: 20.4 us.
 // A step takes about 1700 clocks, the MMAs of 128 tokens 1024 of them; making the weights takes
 // 1300 (720 of them arithmetic, four warps a scheduler, and 100 to 250 for each wait even when
@@ -53,7 +53,8 @@ constexpr int WM_THREADS = (WM_DQ + 4) * 32;
 constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 4;
 constexpr int WM_SMEM = 200 * 1024;            // for both rings
 constexpr int WM_ROWS = 257;                   // of a split's sums of one token: 256, and one against bank conflicts
-constexpr int WM_FOLD = 4;                     // fp32 activations: steps of an accumulator
+// fp32 activations: steps of an accumulator. 2: errors as of a plain fp32 product, 4: up to 4 times that; 1 % slower than 4
+constexpr int WM_FOLD = 2;
 
 // fp32 activations: stages of 64 columns (two parts), and half as many tokens
 constexpr int wm_tokens(int P) { return P == 2 ? 64 : 128; }
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     constexpr int MAKERS = WIDE ? WM_DQ / 2 : WM_DQ;   // warps that make a step's weights
     constexpr int EACH = WIDE ? 2 : 1;         // a warpgroup's steps lie so far apart
     constexpr int AC = WIDE ? 64 : 128;        // TMEM columns of a step's weights
-    constexpr int APART = WIDE ? 1 : WM_FOLD / 2;   // steps between the two accumulators' turns to be folded
+    constexpr int APART = WM_FOLD / 2;         // steps between the two accumulators' turns (WIDE: as the makers' steps)
     constexpr bool FOLD = P == 2;
     constexpr int NS = G == 32 ? 2 : 1;        // scales of a thread's 64 columns
     extern __shared__ __align__(1024) unsigned char raw[];

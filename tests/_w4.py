@@ -71,8 +71,8 @@ def glu(act, g, u):
 def product_bound(a, w, part_bits, k):
     """How far a product sum_k w a may be off: each activation enters to 2^-part_bits of itself (or 2^-39 of the largest
     beside it), and fp32 sums lose at most 2^-23 of the absolute values' sum a step (the tensor core cuts off).  Steps: one
-    for each 16 columns where activations are one part; with two, 32 before the sums of both are taken over and rounded, each
-    512 columns.  A few more join warps and splits."""
+    for each 16 columns where activations are one part; with two, 16 before the sums of both are taken over and rounded, each
+    256 columns.  A few more join warps and splits."""
     mag = a.abs() @ w.abs().T
     top = a.abs().amax(-1, keepdim=True) * w.abs().sum(-1)[None]
     steps = 64 + k // 256 if part_bits == 21 else k // 16 + 24
