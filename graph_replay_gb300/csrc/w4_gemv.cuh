@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const int row0 = ri * p.rows, row1 = min(p.N, row0 + p.rows);
     const int chunks = (p.K + 127) >> 7;                        // 128 columns each
     const int ch0 = (int)((long long)q * chunks / p.ks), ch1 = (int)((long long)(q + 1) * chunks / p.ks);
+    const int room = (chunks + p.ks - 1) / p.ks;                // chunks of a CTA at most: a cluster's CTAs lay out memory alike
     const int set = warp / p.wk, sets = WG_WARPS / p.wk, slice = warp % p.wk;
     const int ngroups = (row1 - row0 + GR - 1) / GR;            // row groups of the CTA
     const int iters = (ngroups + sets - 1) / sets;              // of each set
@@ -140,9 +141,9 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const int S = p.stages;
     const unsigned ring_bytes = (unsigned)S * WG_STEP;
     unsigned char* xs = smem + (size_t)WG_WARPS * ring_bytes;                // [chunk][cols][4][64 bytes], an odd column's words in pairs exchanged: no bank conflicts
-    float* fs = reinterpret_cast<float*>(xs + (size_t)(ch1 - ch0) * cols * 256);   // [chunk][block]: 2^(e - 14)
-    unsigned char* gs = reinterpret_cast<unsigned char*>(fs + (((ch1 - ch0) * p.block + 3) & ~3));   // [chunk][512]: the gain
-    float* red = reinterpret_cast<float*>(gs + (p.gain ? (ch1 - ch0) * 512 : 0));   // [bufs][warp][MT][WG_PITCH]
+    float* fs = reinterpret_cast<float*>(xs + (size_t)room * cols * 256);   // [chunk][block]: 2^(e - 14)
+    unsigned char* gs = reinterpret_cast<unsigned char*>(fs + ((room * p.block + 3) & ~3));   // [chunk][512]: the gain
+    float* red = reinterpret_cast<float*>(gs + (p.gain ? room * 512 : 0));   // [bufs][warp][MT][WG_PITCH]
     float* sums = red + p.bufs * WG_WARPS * MT * WG_PITCH;                   // ks > 1: [1 or 2][block][rows], read by the cluster
     const uint32_t ring_at = smem_u32(smem) + (unsigned)warp * ring_bytes;
 
