@@ -208,7 +208,10 @@ struct W4Call {
     int n() const { return glu ? w[0].n : w[0].n + (nw > 1 ? w[1].n : 0) + (nw > 2 ? w[2].n : 0); }
     int k() const { return w[0].k; }
     int group() const { return w[0].group; }
-    int parts() const { return x_f32 || gain ? 2 : 1; }   // fp16 parts of an activation
+    // fp16 parts of an activation, for few tokens and many alike.  A normed bf16 one is a product with a gain, of more than
+    // the 11 bits of one part: with one, results are off by 2e-4 of the whole, and a tenth of bf16 results are a step off.
+    // Two cost 28 us in place of 22 (40 tokens, 6144 x 4096) and 2020 in place of 899 (4095 tokens, gate and up 14336 x 4096)
+    int parts() const { return x_f32 || gain ? 2 : 1; }
 };
 struct W4Gemv {                // how w4_gemv.cu runs a call of few tokens
     W4Call c;

@@ -6,7 +6,8 @@
 // once the scales of a row are brought to fp16's range by one power of two (2^10 at
 // the row's largest) nothing is rounded (a scale more than 2^27 below the row's largest
 // loses bits, 2^-38 of that largest).  Activations are fp16 parts, scaled by a power of
-// two a token: one part for bf16 ones (8 bits fit), two for fp32.
+// two a token: one part for bf16 ones (8 bits fit), two for fp32 ones and for normed ones
+// (the product with a gain has up to 24 bits whatever the types).
 //
 //   k_w4_split   one CTA a token: RMSNorm's sum, the token's power of two, its parts in
 //                the column order in which the words of codes come apart (w4.cuh).
@@ -22,7 +23,7 @@
 //     warps 18-19 tcgen05.mma kind::f16, a tile each, accumulators in TMEM
 //   and warps 0-15 again for the epilogue: thread = output row, so a warp's stores of one
 //   token lie side by side.
-// The two parts of fp32 activations are twice as many columns of one MMA (an MMA of 64
+// Two parts are twice as many columns of one MMA (an MMA of 64
 // columns takes as long as one of 128 when A lies in TMEM).  The tensor core cuts its fp32
 // sums off instead of rounding them, so these accumulators are folded into registers every
 // WM_FOLD steps, with rounding; the two tiles' turns lie half of that apart, and one tile's
@@ -38,7 +39,7 @@
 // A step takes about 1700 clocks, the MMAs of 128 tokens 1024 of them; making the weights takes
 // 1300 (720 of them arithmetic, four warps a scheduler, and 100 to 250 for each wait even when
 // there is nothing to wait for).  The tensor pipe is active 42 % of a launch of 1024 tokens.
-// Many fp32 tokens (WIDE): one row tile and two blocks of tokens a CTA, 64 gate and 64 up rows;
+// Many tokens of two parts (WIDE): one row tile and two blocks of tokens a CTA, 64 gate and 64 up rows;
 // two of the warpgroups make a step's weights, the other two the next step's.
 #include <cuda.h>
 #include "w4.cuh"
@@ -53,12 +54,12 @@ constexpr int WM_THREADS = (WM_DQ + 4) * 32;
 constexpr int WM_MAX_SC = 12, WM_MAX_SX = 12, WM_MAX_SA = 4;
 constexpr int WM_SMEM = 200 * 1024;            // for both rings
 constexpr int WM_ROWS = 257;                   // of a split's sums of one token: 256, and one against bank conflicts
-// fp32 activations: steps of an accumulator. 2: errors as of a plain fp32 product, 4: up to 4 times that; 1 % slower than 4
+// two parts: steps of an accumulator. 2: errors as of a plain fp32 product, 4: up to 4 times that; 1 % slower than 4
 constexpr int WM_FOLD = 2;
 
-// fp32 activations: stages of 64 columns (two parts), and half as many tokens
+// two parts: stages of 64 columns, and half as many tokens
 constexpr int wm_tokens(int P) { return P == 2 ? 64 : 128; }
-// wide (fp32 activations): one row tile and two blocks of tokens
+// wide (two parts): one row tile and two blocks of tokens
 constexpr int wm_codes(bool wide) { return (wide ? 1 : 2) * 128 * 64; }   // bytes of a codes stage: 128 rows x 128 columns a tile
 constexpr int wm_stage(bool wide, int nt) { return nt * (wide ? 512 : 256); }   // bytes: 128 columns of one part or 64 of two
 constexpr int wm_rows(bool glu, bool wide) { return (glu ? 128 : 256) >> (wide ? 1 : 0); }   // output rows of a CTA
@@ -365,7 +366,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             sn = load_win((s0 + own) / WIN + 1);
             left = WIN - (s0 + own) % WIN;
         }
-        // fp32 activations: the sums of 32 tokens of this thread's row; tokens 32 h .. 32 h + 31 of tile `mat`
+        // two parts: the sums of 32 tokens of this thread's row; tokens 32 h .. 32 h + 31 of tile `mat`
         float acc[FOLD ? 32 : 1];
 #pragma unroll
         for (int e = 0; e < (FOLD ? 32 : 1); ++e) acc[e] = 0.f;
@@ -710,7 +711,7 @@ const void* gemm_kernel(int P, bool glu, bool wide) {
 }
 
 const void* kernel_of(const W4Gemm& g) {
-    const int P = g.c.x_f32 ? 2 : 1;
+    const int P = g.c.parts();
     switch (g.c.group()) {
         case 32: return gemm_kernel<32>(P, g.c.glu, g.wide);
         case 64: return gemm_kernel<64>(P, g.c.glu, g.wide);
@@ -725,7 +726,7 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
     const W4Call& c = g->c;
-    const int P = c.x_f32 ? 2 : 1, rows = wm_rows(c.glu, false);
+    const int P = c.parts(), rows = wm_rows(c.glu, false);
     const int tiles = (c.n() + rows - 1) / rows, steps = (c.k() + 127) / 128;
     // Tokens of a tile and CTAs along k: the least time of the longest CTA, in clocks.  A step takes the tensor cores 8
     // clocks a token and part, or the making and handing over of its weights 900; a CTA starts and ends in about 7000,
@@ -748,10 +749,10 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
         }
         if (nt <= 16) break;
     }
-    // fp32 activations: with one row tile and two blocks of tokens a CTA makes half the weights for as many products, and a
+    // Two parts: with one row tile and two blocks of tokens a CTA makes half the weights for as many products, and a
     // step takes 0.8 of the time; but it has no split along k, and the tiles have to fill the card. 1000 tokens, gate and up
     // 14336 x 4096, take 500 us against 577, 1024 tokens 4096 x 4096 81 against 97; 520 tokens 14336 -> 4096, two waves half
-    // full, 248 against 160. With bf16 ones it gains nothing: 4095 tokens 14336 -> 4096 take 453 against 442
+    // full, 248 against 160. With one part it gains nothing: 4095 tokens 14336 -> 4096 take 453 against 442
     if (P == 2 && c.tokens > wm_tokens(P)) {
         const int two = 2 * wm_tokens(P), few = (c.tokens + two - 1) / two;
         const int wide = (c.n() + wm_rows(c.glu, true) - 1) / wm_rows(c.glu, true);
@@ -778,13 +779,13 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
 
 size_t w4_gemm_bytes(const W4Gemm& g) {
     const W4Call& c = g.c;
-    const int P = c.x_f32 ? 2 : 1;
+    const int P = c.parts();
     return round256((size_t)P * c.tokens * g.kp * 2) + round256((size_t)c.tokens * 4);
 }
 
 cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     const W4Call& c = g.c;
-    const int P = c.x_f32 ? 2 : 1, mats = c.glu ? 2 : 1;
+    const int P = c.parts(), mats = c.glu ? 2 : 1;
     __half* parts = (__half*)g.ws;
     float* factor = (float*)((char*)g.ws + round256((size_t)P * c.tokens * g.kp * 2));
     WmParams p{};

@@ -642,9 +642,10 @@ typedef struct dec_w4_call {
 
 /* out[t, n] = residual[t, n] + sum_k W[n, k] a[t, k].  Products with the codes are
  * summed in fp32; bf16 activations enter exactly, fp32 ones and normed ones to
- * about 2^-22 of each, normed bf16 ones of more than a few tokens to 2^-12 (and
- * all to no less than 2^-39 of the token's largest; weights of more than a few
- * tokens to no less than 2^-38 of the row's largest scale).  Results do not depend
+ * about 2^-22 of each (and all to no less than 2^-39 of the token's largest;
+ * weights of more than a few tokens to no less than 2^-38 of the row's largest
+ * scale).  For many bf16 tokens a gain doubles the products: activations that were
+ * normed to bf16 before the call are faster, and have 8 bits.  Results do not depend
  * on scheduling nor on the values of other tokens, but their last digits do on how
  * many tokens a call has.  A token with a NaN or an infinity gives NaN or
  * infinities. */
