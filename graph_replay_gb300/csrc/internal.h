@@ -232,6 +232,7 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms);
 cudaError_t w4_gemv_launch(const W4Gemv& g, cudaStream_t s, bool pdl);
 struct W4Gemm {                // how w4_gemm.cu runs a call of many tokens
     W4Call c;                  // nw == 1, or glu
+    int parts;                 // fp16 parts of an activation: c.parts(), or two because the sums are to be folded
     int nt;                    // tokens of an accumulator
     bool wide;                 // one row tile and two blocks of nt tokens a CTA, or two row tiles and one block
     int ks;                    // CTAs along k, a cluster

@@ -7,7 +7,7 @@
 // the row's largest) nothing is rounded (a scale more than 2^27 below the row's largest
 // loses bits, 2^-38 of that largest).  Activations are fp16 parts, scaled by a power of
 // two a token: one part for bf16 ones (8 bits fit), two for fp32 ones and for normed ones
-// (the product with a gain has up to 24 bits whatever the types).
+// (the product with a gain has up to 24 bits whatever the types), and for fp32 results.
 //
 //   k_w4_split   one CTA a token: RMSNorm's sum, the token's power of two, its parts in
 //                the column order in which the words of codes come apart (w4.cuh).
@@ -56,6 +56,8 @@ constexpr int WM_SMEM = 200 * 1024;            // for both rings
 constexpr int WM_ROWS = 257;                   // of a split's sums of one token: 256, and one against bank conflicts
 // two parts: steps of an accumulator. 2: errors as of a plain fp32 product, 4: up to 4 times that; 1 % slower than 4
 constexpr int WM_FOLD = 2;
+// one part: columns of an accumulator at most
+constexpr int WM_UNFOLDED = 32768;
 
 // two parts: stages of 64 columns, and half as many tokens
 constexpr int wm_tokens(int P) { return P == 2 ? 64 : 128; }
@@ -711,7 +713,7 @@ const void* gemm_kernel(int P, bool glu, bool wide) {
 }
 
 const void* kernel_of(const W4Gemm& g) {
-    const int P = g.c.parts();
+    const int P = g.parts;
     switch (g.c.group()) {
         case 32: return gemm_kernel<32>(P, g.c.glu, g.wide);
         case 64: return gemm_kernel<64>(P, g.c.glu, g.wide);
@@ -726,8 +728,14 @@ size_t round256(size_t v) { return (v + 255) / 256 * 256; }
 
 cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
     const W4Call& c = g->c;
-    const int P = c.parts(), rows = wm_rows(c.glu, false);
+    const int rows = wm_rows(c.glu, false);
     const int tiles = (c.n() + rows - 1) / rows, steps = (c.k() + 127) / 128;
+    // One part is not folded: 128 tokens' sums are twice the registers that a thread has for them.  What the tensor cores cut off
+    // adds up over an accumulator's columns, at most 2^-23 of the sums for each 16.  Up to WM_UNFOLDED of them that is 2^-12, an
+    // eighth of a bf16 result's half step (measured: 4e-5 of the whole); clusters keep to it where there are more columns.  An fp32
+    // result shows it, so there bf16 activations take two parts, the second of zeros, and are folded: 893 us in place of 424 (4095
+    // tokens, 14336 -> 4096), 50 in place of 36 (40 tokens)
+    const int P = g->parts = c.parts() == 2 || c.out_f32 || steps > 8 * WM_UNFOLDED / 128 ? 2 : 1;
     // Tokens of a tile and CTAs along k: the least time of the longest CTA, in clocks.  A step takes the tensor cores 8
     // clocks a token and part, or the making and handing over of its weights 900; a CTA starts and ends in about 7000,
     // and a split adds the joining of its sums
@@ -737,6 +745,7 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
         const int nt = round_up((c.tokens + blocks - 1) / blocks, 16), used = (c.tokens + nt - 1) / nt;
         for (int ks = 1; ks <= 8; ks *= 2) {
             if (ks > 1 && steps / ks < 2) break;
+            if (P == 1 && (steps + ks - 1) / ks > WM_UNFOLDED / 128) continue;
             const long long places = ks == 1 ? num_sms : w4_clusters(ks, num_sms);
             const double waves = (double)(((long long)tiles * used + places - 1) / places);
             const double step = 8.0 * nt * P > 900.0 ? 8.0 * nt * P : 900.0;
@@ -779,13 +788,13 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
 
 size_t w4_gemm_bytes(const W4Gemm& g) {
     const W4Call& c = g.c;
-    const int P = c.parts();
+    const int P = g.parts;
     return round256((size_t)P * c.tokens * g.kp * 2) + round256((size_t)c.tokens * 4);
 }
 
 cudaError_t w4_gemm_launch(const W4Gemm& g, cudaStream_t s) {
     const W4Call& c = g.c;
-    const int P = c.parts(), mats = c.glu ? 2 : 1;
+    const int P = g.parts, mats = c.glu ? 2 : 1;
     __half* parts = (__half*)g.ws;
     float* factor = (float*)((char*)g.ws + round256((size_t)P * c.tokens * g.kp * 2));
     WmParams p{};

@@ -644,8 +644,11 @@ typedef struct dec_w4_call {
  * summed in fp32; bf16 activations enter exactly, fp32 ones and normed ones to
  * about 2^-22 of each (and all to no less than 2^-39 of the token's largest;
  * weights of more than a few tokens to no less than 2^-38 of the row's largest
- * scale).  For many bf16 tokens a gain doubles the products: activations that were
- * normed to bf16 before the call are faster, and have 8 bits.  Results do not depend
+ * scale).  For many bf16 tokens a gain or an fp32 result doubles the products:
+ * activations that were normed to bf16 before the call are faster, and have 8 bits.
+ * bf16 results of many bf16 tokens without a gain come from sums of up to 32768
+ * columns that the tensor cores cut off (2^-12 of the absolute values' sum at most,
+ * seen 4e-5 of the result's size); all others keep 2^-18 of the result's size.  Results do not depend
  * on scheduling nor on the values of other tokens, but their last digits do on how
  * many tokens a call has.  A token with a NaN or an infinity gives NaN or
  * infinities. */

@@ -44,3 +44,23 @@ def test_normed_bf16_tokens(W, m, n, k, group, out, gain_dtype):   # noqa: F811
     check(w.linear(x, norm=gain, dtype=DT[out]), y, "linear")
     check(w.glu(u, x, norm=gain, dtype=DT[out]), R.glu("silu", y, z), "glu")
     w.check()
+
+
+@pytest.mark.parametrize("m, n, k, group", [(16, 300, 14336, 128), (17, 300, 14336, 128), (64, 513, 14336, 64), (300, 256, 14336, 32),
+                                            (1000, 640, 4096, 128), (4095, 1100, 14336, 128), (40, 64, 1 << 18, 128)])
+def test_fp32_results_of_bf16_tokens(W, m, n, k, group):   # noqa: F811
+    """What the tensor cores cut off does not add up over the columns."""
+    a, b, x = inputs(m, n, k, group, torch.bfloat16, m)
+    w, u = W(*a), W(*b)
+    y, z = x.double() @ R.values(*a).T, x.double() @ R.values(*b).T
+    check(w.linear(x, dtype=torch.float32), y, "linear")
+    check(w.glu(u, x, dtype=torch.float32), R.glu("silu", y, z), "glu")
+    w.check()
+
+
+@pytest.mark.parametrize("m, n, k", [(20, 200, 1 << 16), (40, 64, 1 << 18), (200, 30, 1 << 20)])
+def test_bf16_results_over_many_columns(W, m, n, k):   # noqa: F811
+    a, _, x = inputs(m, n, k, 128, torch.bfloat16, m)
+    w = W(*a)
+    check(w.linear(x), x.double() @ R.values(*a).T, "linear")
+    w.check()
