@@ -50,6 +50,10 @@ constexpr int WG_STEP = 2048;                  // bytes of a step: two tiles of 
 constexpr int WG_PITCH = 33;                   // of 32 rows' sums of one token
 constexpr int WG_MAX_TOKENS = 16;
 constexpr int WG_STAGES = 4;                   // steps of a warp's ring at most
+// A group's sum is multiplied by its token's factor, up to 2^113, before the scale that may bring it back into fp32's range.  The
+// sum is at most 2^25 (128 columns, codes of 8, parts up to 2^15), so with factors 2^11 smaller (exact: a power of two down to
+// 2^-137) no product leaves that range unless the result does; the sums are made 2^11 larger behind the products
+constexpr float WG_LESS = 0x1p-11f, WG_MORE = 0x1p11f;
 
 // one matrix; a gate and an up matrix; two or three stacked
 enum { W4_ONE = 0, W4_GLU = 1, W4_STACK = 2 };
@@ -141,7 +145,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     const int S = p.stages;
     const unsigned ring_bytes = (unsigned)S * WG_STEP;
     unsigned char* xs = smem + (size_t)WG_WARPS * ring_bytes;                // [chunk][cols][4][64 bytes], an odd column's words in pairs exchanged: no bank conflicts
-    float* fs = reinterpret_cast<float*>(xs + (size_t)room * cols * 256);   // [chunk][block]: 2^(e - 14)
+    float* fs = reinterpret_cast<float*>(xs + (size_t)room * cols * 256);   // [chunk][block]: 2^(e - 14 - 11)
     unsigned char* gs = reinterpret_cast<unsigned char*>(fs + ((room * p.block + 3) & ~3));   // [chunk][512]: the gain
     float* red = reinterpret_cast<float*>(gs + (p.gain ? room * 512 : 0));   // [bufs][warp][MT][WG_PITCH]
     float* sums = red + p.bufs * WG_WARPS * MT * WG_PITCH;                   // ks > 1: [1 or 2][block][rows], read by the cluster
@@ -307,7 +311,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                         x.z = isfinite(x.z) ? x.z : 0.f; x.w = isfinite(x.w) ? x.w : 0.f;
                     }
                 }
-                if (lane == 0) *fo = w4_down(e);
+                if (lane == 0) *fo = w4_down(e) * WG_LESS;
             }
             if (p.gain) {
                 ss = warp_sum(ss);
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 for (int c = 0; c < AC; ++c) {
                     const int r = P == 2 ? b * 4 + t : b * 8 + 2 * t + (c & 1);
                     const int row = a * 16 + g + 8 * (P == 2 ? c : c >> 1);
-                    rw[r * WG_PITCH + row] = acc[a][b][c];
+                    rw[r * WG_PITCH + row] = acc[a][b][c] * WG_MORE;
                 }
         __syncthreads();
         int r = j_tok, st2 = j_set;

@@ -64,3 +64,59 @@ def test_bf16_results_over_many_columns(W, m, n, k):   # noqa: F811
     w = W(*a)
     check(w.linear(x), x.double() @ R.values(*a).T, "linear")
     w.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m", [1, 3, 8, 11, 24, 300])
+def test_sizes_at_both_ends(W, m, group, dtype):   # noqa: F811
+    """Activations from 2^-110 to 2^123 and scales that bring their products back: no step leaves fp32's range where the result
+    does not."""
+    n, k = 70, 2176
+    codes, _ = R.random_matrix(n, k, group, 5)
+    row = torch.arange(n, device="cuda")[:, None]
+    x = normal(m, k, seed=1)
+    tok = torch.arange(m, device="cuda")[:, None]
+    for up, down in ((120, -40), (123, -110), (-100, 40), (-90, 110), (60, -100)):
+        s = (torch.rand(n, k // group, device="cuda") + 0.5) * torch.exp2(down + (row % 3).float())
+        far = (x * torch.exp2(torch.where(tok % 2 == 0, float(up), float(-down)))).to(DT[dtype])
+        w = W(codes, s.bfloat16())
+        want = far.double() @ R.values(codes, w.scales).T
+        got = w.linear(far, dtype=torch.float32)
+        for t in range(m):
+            err = (got[t].double() - want[t]).norm()
+            assert err <= KEPT * want[t].norm(), f"2^{up}, 2^{down}, token {t}: {err / want[t].norm():.3g}"
+    w.check()
+
+
+def test_one_large_block_of_columns(W):   # noqa: F811
+    """A token whose large values lie in one block of columns, and tokens beside it that have none: theirs stay as they are."""
+    n, k = 300, 4096
+    a = R.random_matrix(n, k, 64, 5)
+    w = W(a[0], (a[1].float() * 2.0 ** -30).bfloat16())
+    x = normal(6, k, seed=2)
+    alone = w.linear(x)
+    x[2, 1500:1510] = 1e38
+    x[4, 100] = -3e38
+    got = w.linear(x)
+    want = x.double() @ R.values(w.codes, w.scales).T
+    keep = [0, 1, 3, 5]
+    assert torch.equal(got[keep], alone[keep])
+    for t in range(6):
+        assert (got[t].double() - want[t]).norm() <= KEPT * want[t].norm()
+    w.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [1, 8, 20])
+def test_largest_sums(W, m, dtype):   # noqa: F811
+    """The largest activations and codes, all of one sign: 128 columns make 2^138."""
+    n, k = 40, 1024
+    codes = torch.full((n, k // 2), 0x88, dtype=torch.uint8, device="cuda")
+    for group in (32, 64, 128):
+        w = W(codes, torch.full((n, k // group), 2.0 ** -20, dtype=torch.bfloat16, device="cuda"))
+        x = torch.full((m, k), torch.finfo(DT[dtype]).max, device="cuda", dtype=DT[dtype])
+        got = w.linear(x, dtype=torch.float32)
+        want = x[0, 0].double() * -8.0 * k * 2.0 ** -20
+        assert ((got.double() - want).abs() <= KEPT * want.abs()).all()
+    w.check()
