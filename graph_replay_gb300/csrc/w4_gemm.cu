@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         for (int e = 0; e < (FOLD ? 32 : 1); ++e) acc[e] = 0.f;
         int folded = 0;                        // times the tile's accumulator was taken
         auto fold_in = [&]() -> bool {
-            if (!mbar_wait(&d_full[mat], (uint32_t)folded & 1u)) return false;
+            // a lane's wait may run out by itself: all of the warp read TMEM, or none
+            if (!__all_sync(0xffffffffu, mbar_wait(&d_full[mat], (uint32_t)folded & 1u))) return false;
             fence_after();
             if (h * 32 < p.nt) {
 #pragma unroll
@@ -466,7 +467,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
             // the accumulator is taken when the weights of the step behind its last are made: its products have had that long
             if (FOLD && s > 0 && (s + mat * APART) % WM_FOLD == 0) {
                 ok = fold_in();
-                if (!__all_sync(0xffffffffu, ok)) break;
+                if (!ok) break;                // the same for all lanes
             }
         }
         if (!__all_sync(0xffffffffu, ok) && lane == 0) give_up();
@@ -474,17 +475,17 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         // ---- epilogue ----
         pdl_wait();
         for (int i = tid; i < m; i += WM_DQ * 32) tok_f[i] = __ldcg(p.factor + tok0 + i);
-        bool live = __all_sync(0xffffffffu, ok) && !*ab;
+        bool live = __all_sync(0xffffffffu, ok && !*ab);   // (another warp may set it between two lanes' reads)
         if (FOLD) {
             const int times = (n - 1 + mat * APART) / WM_FOLD + 1;
-            while (live && folded < times) live = __all_sync(0xffffffffu, fold_in());
+            while (live && folded < times) live = fold_in();
         } else if (live) {
             live = __all_sync(0xffffffffu, mbar_wait(&d_full[mat], 0u));
             fence_after();
         }
         if (!live && lane == 0) give_up();
         named_sync(1, WM_DQ * 32);
-        live = !*ab;
+        live = __all_sync(0xffffffffu, !*ab);
         const int tb = WIDE ? mat * p.nt : 0, mh = WIDE ? min(p.nt, m - tb) : m;   // the accumulator's first token; its tokens
         // the smaller factor first: no step leaves fp32's range unless the result does
         auto sized = [&](float v, float b) { return v * fminf(down, b) * fmaxf(down, b); };
@@ -544,6 +545,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         };
         // P == 1: chunks of 16 tokens of a tile go to its two warpgroups in turn.  P == 2: they are in acc
         auto chunk = [&](int c, float (&v)[16]) {
+            __syncwarp();                      // lanes without a row wrote nothing: all of the warp read TMEM together
             if (FOLD) {
 #pragma unroll
                 for (int e = 0; e < 16; ++e) v[e] = c & 16 ? acc[FOLD ? 16 + e : 0] : acc[FOLD ? e : 0];
