@@ -108,7 +108,8 @@ bool meet(const void* a, int64_t a_stride, int64_t a_bytes, const void* b, int64
     return at < a_bytes || at + b_bytes > a_stride;
 }
 
-int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* c, W4Call* p) {
+// sizes, types and whether there is a gain: what a plan follows from
+int check_sizes(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* c, W4Call* p) {
     int rc;
     *p = W4Call{};
     if ((rc = w4_check(glu ? "gate" : "w", w, &p->w[0])) != DEC_OK) return rc;
@@ -129,7 +130,6 @@ int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const 
     if ((rc = check_dtype("out_dtype", c->out_dtype, &p->out_f32)) != DEC_OK) return rc;
     if (c->gain) {
         if ((rc = check_dtype("gain_dtype", c->gain_dtype, &p->gain_f32)) != DEC_OK) return rc;
-        if (!aligned(c->gain, 16)) return refuse(DEC_E_INVALID, "gain must be 16-byte aligned");
         if (!(c->eps >= 0.0) || !std::isfinite((float)c->eps)) return refuse(DEC_E_INVALID, "eps must be finite and >= 0");
     }
     if (glu) {
@@ -137,6 +137,17 @@ int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const 
             return refuse(DEC_E_INVALID, "act must be DEC_ACT_SILU or DEC_ACT_GELU_TANH");
         if (c->residual) return refuse(DEC_E_INVALID, "dec_w4_glu takes no residual");
     }
+    p->act = c->act;
+    p->tokens = c->tokens;
+    p->gain = c->gain;
+    p->eps = (float)c->eps;
+    return DEC_OK;
+}
+
+// the pointers, strides and overlaps of a call whose sizes are checked
+int check_tensors(const dec_w4_weight* w, const dec_w4_call* c, W4Call* p) {
+    int rc;
+    if (!aligned(c->gain, 16)) return refuse(DEC_E_INVALID, "gain must be 16-byte aligned");
     if (!c->err || !aligned(c->err, 4)) return refuse(DEC_E_INVALID, "err is required");
     if (c->tokens > 0) {
         if ((rc = check_rows("x", c->x, c->x_stride, w->k, p->x_f32)) != DEC_OK) return rc;
@@ -154,16 +165,12 @@ int check_call(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const 
              meet(c->residual, c->residual_stride * os, n * os, c->out, c->out_stride * os, n * os, c->tokens)))
             return refuse(DEC_E_INVALID, "out overlaps x, the gain or the residual (it may be the residual itself)");
     }
-    p->act = c->act;
-    p->tokens = c->tokens;
     p->x = c->x;
-    p->gain = c->gain;
     p->residual = c->residual;
     p->out = c->out;
     p->x_stride = c->x_stride;
     p->residual_stride = c->residual_stride;
     p->out_stride = c->out_stride;
-    p->eps = (float)c->eps;
     p->err = c->err;
     return DEC_OK;
 }
@@ -198,7 +205,7 @@ cudaError_t plan_of(const W4Call& c, int sms, Plan* p) {
 int run(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* call, void* stream) {
     W4Call c;
     int rc, sms;
-    if ((rc = check_call(w, up, glu, call, &c)) != DEC_OK) return rc;
+    if ((rc = check_sizes(w, up, glu, call, &c)) != DEC_OK || (rc = check_tensors(w, call, &c)) != DEC_OK) return rc;
     if (c.tokens == 0) return DEC_OK;
     const char* what = glu ? "dec_w4_glu" : "dec_w4_linear";
     OnDevice on(w->device);
@@ -251,7 +258,7 @@ int dec_w4_workspace(const dec_w4_weight* w, const dec_w4_weight* up, const dec_
     if (!bytes) return refuse(DEC_E_INVALID, "bytes is NULL");
     W4Call c;
     int rc, sms;
-    if ((rc = check_call(w, up, up != nullptr, call, &c)) != DEC_OK) return rc;
+    if ((rc = check_sizes(w, up, up != nullptr, call, &c)) != DEC_OK) return rc;
     *bytes = 0;
     if (c.tokens == 0) return DEC_OK;
     OnDevice on(w->device);

@@ -660,7 +660,8 @@ int dec_w4_linear(const dec_w4_weight *w, const dec_w4_call *call, void *stream)
 int dec_w4_glu(const dec_w4_weight *gate, const dec_w4_weight *up, const dec_w4_call *call, void *stream);
 
 /* Bytes of workspace that dec_w4_linear (up = NULL) or dec_w4_glu needs for these
- * arguments (*bytes, host); reads sizes, types and whether there is a gain only. */
+ * arguments (*bytes, host).  Reads sizes, types and whether there is a gain: of the
+ * call's pointers and strides none is checked, and all but the gain may be NULL. */
 int dec_w4_workspace(const dec_w4_weight *w, const dec_w4_weight *up, const dec_w4_call *call, size_t *bytes);
 
 /* Device address of the logits [rows, vocab] fp32 of the last step. */
