@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
     extern __shared__ __align__(1024) unsigned char raw[];
     unsigned char* smem = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     __shared__ __align__(8) uint64_t codes_full[WM_MAX_SC], codes_empty[WM_MAX_SC], x_full[WM_MAX_SX], x_empty[WM_MAX_SX];
-    __shared__ __align__(8) uint64_t a_full[WM_MAX_SA], a_empty[WM_MAX_SA], d_full[2], d_empty[2];
+    __shared__ __align__(8) uint64_t a_full[WM_MAX_SA], a_empty[WM_MAX_SA], d_full[2], d_empty[2], done[2];
     __shared__ uint32_t tmem;
     __shared__ int aborted;
     __shared__ int row_e[WIDE ? 1 : 2][128];
@@ -215,6 +215,7 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
         for (int s = 0; s < 2; ++s) {
             mbar_init(&d_full[s], 1);          // of a tile, or (WIDE) of a block of tokens
             mbar_init(&d_empty[s], WM_DQ / 2);
+            mbar_init(&done[s], 1);
         }
         aborted = 0;
         mbar_fence_init();
@@ -319,6 +320,9 @@ __global__ void __launch_bounds__(WM_THREADS, 1) k_w4_gemm(const __grid_constant
                 fold = 0;
             }
         }
+        // no product may still read shared memory or TMEM when the CTA frees them, also where a wait gave up before its end
+        commit(&done[i]);
+        ok = mbar_wait(&done[i], 0u) && ok;
         if (!__all_sync(0xffffffffu, ok) && lane == 0) give_up();
         __syncwarp();
     } else {
