@@ -6,7 +6,8 @@
     a = gate.glu(up, x, act="silu", norm=gain)            # silu(gate x) * (up x)
 
 The calls launch on torch's current stream and return at once; nothing reads back to the host.  ``check`` does, and
-raises if a call on any stream gave up waiting for a copy or a product.
+raises if a call on any stream gave up waiting for a copy or a product.  There is no backward pass: where gradients are
+recorded, tensors that require one are refused.
 """
 from __future__ import annotations
 
@@ -135,6 +136,11 @@ class W4Weight:
         return c, need
 
     def _run(self, up, x, act, residual, norm, eps, out, dtype):
+        if torch.is_grad_enabled() and (x.requires_grad or norm is not None and norm.requires_grad
+                                        or residual is not None and residual.requires_grad
+                                        or out is not None and out.requires_grad):
+            raise ValueError("W4Weight: no backward pass, and x, norm, residual or out requires a gradient (call it under "
+                             "torch.no_grad, or detach them)")
         if out is None:
             out = torch.empty(x.shape[0], self.shape[0], dtype=x.dtype if dtype is None else dtype, device=x.device)
         elif dtype is not None and out.dtype != dtype:
