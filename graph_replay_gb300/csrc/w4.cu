@@ -108,6 +108,23 @@ bool meet(const void* a, int64_t a_stride, int64_t a_bytes, const void* b, int64
     return at < a_bytes || at + b_bytes > a_stride;
 }
 
+// whether one of `rows` rows, `bytes` each and `stride` bytes apart, has a byte of [q, q + qbytes)
+bool rows_touch(const void* p, int64_t stride, int64_t bytes, int64_t rows, const void* q, int64_t qbytes) {
+    const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
+    if (b + (uint64_t)qbytes <= a) return false;
+    const uint64_t i = b > a ? (b - a) / (uint64_t)stride : 0;   // the last row that starts at or before q, or the first
+    if (i < (uint64_t)rows && a + i * stride + bytes > b) return true;
+    return i + 1 < (uint64_t)rows && a + (i + 1) * stride < b + (uint64_t)qbytes;
+}
+
+int check_apart(const char* what, const dec_w4_weight* w, const void* p, int64_t stride, bool f32) {
+    const int64_t size = f32 ? 4 : 2, codes = (int64_t)w->n * w->k / 2, scales = (int64_t)w->n * (w->k / w->group) * 2;
+    if (rows_touch(p, stride * size, w->k * size, w->n, w->codes, codes) || rows_touch(p, stride * size, w->k * size, w->n, w->scales, scales) ||
+        rows_touch(w->codes, codes, codes, 1, w->scales, scales))
+        return refuse(DEC_E_INVALID, "%s, codes and scales overlap", what);
+    return DEC_OK;
+}
+
 // sizes, types and whether there is a gain: what a plan follows from
 int check_sizes(const dec_w4_weight* w, const dec_w4_weight* up, bool glu, const dec_w4_call* c, W4Call* p) {
     int rc;
@@ -235,6 +252,7 @@ int dec_w4_quantize(const dec_w4_weight* w, const void* src, int64_t src_stride,
     if ((rc = w4_check("w", w, &m)) != DEC_OK) return rc;
     if ((rc = check_dtype("dtype", dtype, &f32)) != DEC_OK) return rc;
     if ((rc = check_rows("src", src, src_stride, w->k, f32)) != DEC_OK) return rc;
+    if ((rc = check_apart("src", w, src, src_stride, f32)) != DEC_OK) return rc;
     OnDevice on(w->device);
     if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
     if ((rc = sms_of(w->device, &sms)) != DEC_OK) return rc;
@@ -248,6 +266,7 @@ int dec_w4_dequantize(const dec_w4_weight* w, void* dst, int64_t dst_stride, int
     if ((rc = w4_check("w", w, &m)) != DEC_OK) return rc;
     if ((rc = check_dtype("dtype", dtype, &f32)) != DEC_OK) return rc;
     if ((rc = check_rows("dst", dst, dst_stride, w->k, f32)) != DEC_OK) return rc;
+    if ((rc = check_apart("dst", w, dst, dst_stride, f32)) != DEC_OK) return rc;
     OnDevice on(w->device);
     if ((rc = launched(on.e, "cudaSetDevice")) != DEC_OK) return rc;
     if ((rc = sms_of(w->device, &sms)) != DEC_OK) return rc;

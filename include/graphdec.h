@@ -610,10 +610,13 @@ typedef struct dec_w4_binding {
  * like the stride) into w.  Over each group scale = bf16(max |x| / 7) and code =
  * x / scale to the nearest whole number, ties to even.  A group whose scale would
  * be below 2^-100 holds zeros at scale 0; a group with a NaN or an infinity has
- * scale NaN (and so gives NaN wherever it is used). */
+ * scale NaN (and so gives NaN wherever it is used).  src, codes and scales do not
+ * overlap. */
 int dec_w4_quantize(const dec_w4_weight *w, const void *src, int64_t src_stride, int32_t dtype, void *stream);
 
-/* The values that w stands for, [n, k] in f32 (exact) or bf16 (rounded once). */
+/* The values that w stands for, [n, k] in f32 (exact) or bf16 (rounded once); rows
+ * dst_stride elements apart, 16-byte aligned like the stride, and not over w's own
+ * memory. */
 int dec_w4_dequantize(const dec_w4_weight *w, void *dst, int64_t dst_stride, int32_t dtype, void *stream);
 
 typedef enum dec_act { DEC_ACT_SILU = 0, DEC_ACT_GELU_TANH = 1 } dec_act;
