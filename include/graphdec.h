@@ -209,8 +209,8 @@ struct dec_w4_binding;
  * -1).  A later binding of a role replaces an earlier one of either kind.  Norm
  * gains and embeddings stay in weight_dtype.  Q, K and V of a layer have one group,
  * and so have GATE and UP.  Read in place like the others; the step's products are
- * dec_w4_linear's and dec_w4_glu's.  DEC_STRATEGY_GRAPH only, and no
- * dec_prefill_block (DEC_E_UNSUPPORTED there; dec_prefill takes them). */
+ * dec_w4_linear's and dec_w4_glu's.  DEC_STRATEGY_GRAPH only, and with layers in 4
+ * bits no dec_prefill_block (DEC_E_UNSUPPORTED there; dec_prefill takes them). */
 int dec_load_w4(dec_handle *h, const struct dec_w4_binding *w, size_t n);
 
 /* Device bytes that dec_capture needs for this shape (KV store, slots,
