@@ -52,7 +52,7 @@ constexpr int WG_MAX_TOKENS = 16;
 constexpr int WG_STAGES = 4;                   // steps of a warp's ring at most
 // A group's sum is multiplied by its token's factor, up to 2^113, before the scale that may bring it back into fp32's range.  The
 // sum is at most 2^25 (128 columns, codes of 8, parts up to 2^15), so with factors 2^11 smaller (exact: a power of two down to
-// 2^-137) no product leaves that range unless the result does; the sums are made 2^11 larger behind the products
+// 2^-137) no product leaves that range unless the result does; the outputs are made 2^11 larger (with the norm's factor)
 constexpr float WG_LESS = 0x1p-11f, WG_MORE = 0x1p11f;
 
 // one matrix; a gate and an up matrix; two or three stacked
@@ -347,8 +347,8 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
     else __syncwarp();
     pdl_trigger();
 
-    // one output: gate / value v and up u, unscaled by the norm; its residual
-    float inv = 1.0f;                          // of the norm of token inv_of
+    // one output: gate / value v and up u, 2^11 too small and unscaled by the norm; its residual
+    float inv = WG_MORE;                       // with that of the norm of token inv_of
     int inv_of = -1;
     auto finish = [&](int r, int n, float v, float u, float res) {
         if (p.gain) {                          // (behind a row group's barrier)
@@ -356,12 +356,12 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 float s = 0.f;
 #pragma unroll
                 for (int w = 0; w < WG_WARPS; ++w) s += ss_s[w][r];
-                inv = 1.0f / sqrtf(s / (float)p.K + p.eps);
+                inv = WG_MORE / sqrtf(s / (float)p.K + p.eps);
                 inv_of = r;
             }
-            v *= inv;
-            u *= inv;
         }
+        v *= inv;
+        u *= inv;
         v = GLU ? w4_glu(p.act, v, u) : v + res;
         w4_store1(p.out, p.out_f32, (size_t)(tok0 + r) * p.out_stride + n, v);
         if (!GLU && p.amax) {
@@ -548,7 +548,7 @@ __global__ void __launch_bounds__(WG_THREADS, 1) k_w4_gemv(const __grid_constant
                 for (int c = 0; c < AC; ++c) {
                     const int r = P == 2 ? b * 4 + t : b * 8 + 2 * t + (c & 1);
                     const int row = a * 16 + g + 8 * (P == 2 ? c : c >> 1);
-                    rw[r * WG_PITCH + row] = acc[a][b][c] * WG_MORE;
+                    rw[r * WG_PITCH + row] = acc[a][b][c];
                 }
         __syncthreads();
         int r = j_tok, st2 = j_set;
