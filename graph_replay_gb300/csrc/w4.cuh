@@ -106,6 +106,10 @@ __device__ __forceinline__ void w4_store1(void* p, bool f32, size_t i, float v) 
 // two at or below the largest finite |v| of their block: the scaled values lie
 // below 2^15, one part keeps 11 bits of each and two keep 22 (or 2^-39 of the
 // block's largest, where that is coarser).  `top` is the largest |v|'s bits.
+// fp32 activations have 24 bits: a third part would be half as many products again for
+// errors that are below an fp32 product's already (of the whole, against 64 bits, and
+// in parentheses the plain fp32 form's: one token 6144 x 4096 1.1e-7 (1.9e-7), eight
+// tokens 14336 -> 4096 1.0e-7 (4.2e-7), 1000 tokens gate/up 14336 x 4096 5.6e-7 (1.3e-6)).
 __device__ __forceinline__ int w4_exponent(uint32_t top) { return min(max((int)(top >> 23), 15), 254); }
 __device__ __forceinline__ float w4_up(int e) { return __uint_as_float((uint32_t)(268 - e) << 23); }     // 2^(14 - (e - 127))
 __device__ __forceinline__ float w4_down(int e) { return __uint_as_float((uint32_t)(e - 14) << 23); }    // its reciprocal

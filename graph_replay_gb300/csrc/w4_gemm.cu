@@ -33,9 +33,10 @@
 // in order.
 // Every wait is bounded; one that gives up sets FAULT_WAIT, and the CTA ends.
 //
-// Measured, in captures: 4095 bf16 tokens, 14336 -> 4096: 442 us, 1088 TFLOP/s (a library
-// product of 16-bit weights: 1918).  1000 fp32 tokens, gate and up 14336 x 4096: 510 us, 460
-// TFLOP/s of result, twice that in the tensor cores.  64 bf16 tokens, 4096 x 4096: 20.4 us.
+// Measured, in captures: 4095 bf16 tokens, 14336 -> 4096: 437 us, 1100 TFLOP/s (a library
+// product of 16-bit weights: 1918).  1000 fp32 tokens, gate and up 14336 x 4096: 513 us, 458
+// TFLOP/s of result, twice that in the tensor cores.  64 bf16 tokens, 4096 x 4096: 21.3 us; 40
+// with a norm (two parts), 6144 x 4096: 26.9 us, 96 CTAs of clusters of four.
 // A step takes about 1700 clocks, the MMAs of 128 tokens 1024 of them; making the weights takes
 // 1300 (720 of them arithmetic, four warps a scheduler, and 100 to 250 for each wait even when
 // there is nothing to wait for).  The tensor pipe is active 42 % of a launch of 1024 tokens.
@@ -766,8 +767,8 @@ cudaError_t w4_gemm_plan(W4Gemm* g, int num_sms) {
     }
     // Two parts: with one row tile and two blocks of tokens a CTA makes half the weights for as many products, and a
     // step takes 0.8 of the time; but it has no split along k, and the tiles have to fill the card. 1000 tokens, gate and up
-    // 14336 x 4096, take 500 us against 577, 1024 tokens 4096 x 4096 81 against 97; 520 tokens 14336 -> 4096, two waves half
-    // full, 248 against 160. With one part it gains nothing: 4095 tokens 14336 -> 4096 take 453 against 442
+    // 14336 x 4096, take 513 us against 607, 1024 tokens 4096 x 4096 82 against 102, 330 45 against 62; 520 tokens 14336 -> 4096
+    // would be two waves half full, 250 against 170. With one part it gains nothing: 4095 tokens 14336 -> 4096 took 453 against 442
     if (P == 2 && c.tokens > wm_tokens(P)) {
         const int two = 2 * wm_tokens(P), few = (c.tokens + two - 1) / two;
         const int wide = (c.n() + wm_rows(c.glu, true) - 1) / wm_rows(c.glu, true);

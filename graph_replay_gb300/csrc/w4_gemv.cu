@@ -32,10 +32,10 @@ size_t smem_of(const W4Gemv& g) {
     return ring + x + f + sums + sizeof(float) * g.bufs * WG_WARPS * wg_tokens(P, blocks_of(g)) * WG_PITCH;
 }
 
-// how many clusters of ks CTAs, one an SM, run at a time: they do not cross the chip's SM groups, so it may be less than
-// the SMs hold (asked once for each size; devices of one process are alike)
 }  // namespace
 
+// how many clusters of ks CTAs, one an SM, run at a time: they do not cross the chip's SM groups, so it may be less than
+// the SMs hold (asked once for each size; devices of one process are alike)
 int w4_clusters(int ks, int num_sms) {
     if (ks == 1) return num_sms;
     static std::atomic<int> known[4];
@@ -69,8 +69,8 @@ cudaError_t w4_gemv_plan(W4Gemv* g, int num_sms) {
     const int P = c.parts(), N = c.n(), chunks = (c.k() + 127) / 128, most = WG_MAX_TOKENS / P;
     // as many tokens a CTA as its shared memory holds; the rest in further rows of the grid
     for (g->block = c.tokens < most ? c.tokens : most;; g->block = (g->block + 1) / 2) {
-    // rows evenly over the SMs, at least 8 a CTA: a tile has 16, and a CTA of fewer saves nothing
-    const int gr = c.glu ? 16 : 32;
+        // rows evenly over the SMs, at least 8 a CTA: a tile has 16, and a CTA of fewer saves nothing
+        const int gr = c.glu ? 16 : 32;
         // CTAs along k: the fewest (a cluster: 1, 2, 4 or 8) whose shared memory holds the activations beside a ring of four
         // steps or two
         for (g->ks = 1; g->ks <= 8 && g->ks <= chunks; g->ks *= 2) {

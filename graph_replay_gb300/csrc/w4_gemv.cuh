@@ -28,17 +28,19 @@
 // a last CTA that adds them).  Results do not depend on scheduling.
 //
 // Measured in captures, fp32 activations, copies of the weights larger than L2 in turn:
-//   one token     128256 x 4096, groups of 64, norm   66.6 us   4.2 TB/s (a copy: 6.8)
-//                 gate and up 14336 x 4096            20.3 us   3.0 TB/s
-//                 14336 -> 4096                       12.9 us   2.3 TB/s
-//                 4096 x 4096                          6.4 us   1.4 TB/s
-//   eight tokens  14336 -> 4096, residual             21.1 us
-//                 gate and up 14336 x 4096, groups of 32, norm   38.6 us
+//   one token     128256 x 4096, groups of 64, norm   65.8 us   4.2 TB/s (a copy: 6.8)
+//                 gate and up 14336 x 4096, norm      20.6 us   2.9 TB/s
+//                 14336 -> 4096, residual             13.5 us   2.2 TB/s
+//                 4096 x 4096, residual                6.8 us   1.3 TB/s
+//   eight tokens  14336 -> 4096, residual             21.2 us
+//                 gate and up 14336 x 4096, groups of 32, norm   38.7 us
 // The largest is bound by instructions, not by bytes: about 360 for a step of 4096
 // codes and warp, 64 % of the issue slots; the integer and the half-precision pipe, each
 // of which takes an instruction every other clock, are busy in turn, and the tensor pipe
-// at 23 %.  The small ones are bound by their ends: launch, the copy and conversion of
-// the activations (1 to 6 thousand clocks) and the join.
+// at 23 %.  Eight tokens issue in 54 % (14336 -> 4096) and 61 % (groups of 32) of the slots,
+// and wait for results and at the row groups' barriers besides.  The small ones are bound by
+// their ends: launch, the copy and conversion of the activations (1 to 6 thousand clocks) and
+// the join.
 #pragma once
 #include "w4.cuh"
 

@@ -11,7 +11,10 @@
 // Bound by memory, 2 or 4 bytes a weight read, 0.5 + 2 / group written, where the weights
 // are fp32: 14336 x 4096 in 47.6 us, 5.6 TB/s (a copy: 6.8).  bf16 ones take 42.5 us, 3.5
 // TB/s: there the border of each code, about a dozen instructions a weight, takes as long
-// as the bytes.  Reading back: 28.9 us to bf16 (5.1 TB/s), 63.7 to fp32 (4.2).
+// as the bytes (two would do where the weight has 8 bits: w / s is never nearer to a border
+// than 2^-10 without being on it).  Reading back: 28.9 us to bf16 (5.1 TB/s), 64 to fp32 (4.1),
+// where a lane's two stores are 32 bytes side by side, so each of a warp's covers half of the
+// sectors that it touches.
 // With conversions between integers and floats and 8 columns a lane, storing and reading
 // back in bf16 took 110 us together; 71 now.
 #include "w4.cuh"

@@ -67,8 +67,9 @@ class W4Weight:
     @classmethod
     def quantize(cls, w: torch.Tensor, group: int = 128, codes: Optional[torch.Tensor] = None,
                  scales: Optional[torch.Tensor] = None) -> "W4Weight":
-        """w [n, k] (f32 or bf16, rows any stride) in 4 bits: over each group scale = bf16(max |w| / 7), code = w / scale to
-        the nearest whole number.  Into `codes` and `scales`, or new tensors."""
+        """w [n, k] (f32 or bf16; its rows may be parts of longer ones, and start at multiples of 16 bytes) in 4 bits: over each
+        group scale = bf16(max |w| / 7), code = w / scale to the nearest whole number.  Into `codes` and `scales`, or new
+        tensors; neither lies over w."""
         if w.dim() != 2 or not w.is_cuda or w.dtype not in _DT or w.stride(1) != 1:
             raise ValueError("W4Weight.quantize: w is an f32 or bf16 CUDA matrix, its columns side by side")
         n, k = w.shape
@@ -85,7 +86,8 @@ class W4Weight:
         return q
 
     def dequantize(self, dtype: torch.dtype = torch.float32, out: Optional[torch.Tensor] = None) -> torch.Tensor:
-        """The matrix that the codes and scales stand for, [n, k], as dtype (or into out, as its type)."""
+        """The matrix that the codes and scales stand for, [n, k], as dtype (or into out, as its type; out's rows start at
+        multiples of 16 bytes)."""
         if out is None:
             if dtype not in _DT:
                 raise ValueError("W4Weight.dequantize: f32 or bf16")
@@ -98,8 +100,9 @@ class W4Weight:
 
     def linear(self, x: torch.Tensor, residual: Optional[torch.Tensor] = None, norm: Optional[torch.Tensor] = None,
                eps: float = 1e-5, out: Optional[torch.Tensor] = None, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
-        """residual + W a for x [tokens, k] (f32 or bf16): a = x, or with a gain `norm` [k] its RMSNorm.  The result
-        [tokens, n] has dtype, by default x's; `out` may be the residual itself."""
+        """residual + W a for x [tokens, k] (f32 or bf16, its rows at multiples of 16 bytes): a = x, or with a gain `norm` [k]
+        its RMSNorm.  The result [tokens, n] has dtype, by default x's; `out` may be the residual itself.  For many bf16 tokens
+        a norm or an fp32 result doubles the products (both keep more than bf16's bits)."""
         return self._run(None, x, 0, residual, norm, eps, out, dtype)
 
     def glu(self, up: "W4Weight", x: torch.Tensor, act: str = "silu", norm: Optional[torch.Tensor] = None,

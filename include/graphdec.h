@@ -643,18 +643,21 @@ typedef struct dec_w4_call {
     size_t workspace_bytes;
 } dec_w4_call;
 
-/* out[t, n] = residual[t, n] + sum_k W[n, k] a[t, k].  Products with the codes are
- * summed in fp32; bf16 activations enter exactly, fp32 ones and normed ones to
- * about 2^-22 of each (and all to no less than 2^-39 of the token's largest;
- * weights of more than a few tokens to no less than 2^-38 of the row's largest
- * scale).  For many bf16 tokens a gain or an fp32 result doubles the products:
- * activations that were normed to bf16 before the call are faster, and have 8 bits.
- * bf16 results of many bf16 tokens without a gain come from sums of up to 32768
- * columns that the tensor cores cut off (2^-12 of the absolute values' sum at most,
- * seen 4e-5 of the result's size); all others keep 2^-18 of the result's size.  Results do not depend
- * on scheduling nor on the values of other tokens, but their last digits do on how
- * many tokens a call has.  A token with a NaN or an infinity gives NaN or
- * infinities. */
+/* out[t, n] = residual[t, n] + sum_k W[n, k] a[t, k].
+ *   Activations: bf16 ones enter exactly, fp32 ones and normed ones to about 2^-22
+ * of each (and all to no less than 2^-39 of the token's largest; weights of more
+ * than a few tokens to no less than 2^-38 of the row's largest scale).
+ *   Sums: in fp32, off by less than 2^-18 of the result's size.  bf16 results of many
+ * bf16 tokens without a gain come from sums of up to 32768 columns that the tensor
+ * cores cut off: 2^-12 of the absolute values' sum at most, seen 4e-5 of the result's
+ * size.
+ *   For many bf16 tokens a gain or an fp32 result doubles the products: activations
+ * that were normed to bf16 before the call are faster, and have 8 bits.
+ *   Range: x * gain, x^2 and the sum of x^2 are fp32 values, so a normed token's
+ * largest is below 2^63 / sqrt(k); without a gain, all finite values are taken.
+ *   Results do not depend on scheduling nor on the values of other tokens, but their
+ * last digits do on how many tokens a call has.  A token with a NaN or an infinity
+ * gives NaN or infinities. */
 int dec_w4_linear(const dec_w4_weight *w, const dec_w4_call *call, void *stream);
 
 /* The first half of a gated feed-forward block: out[t, n] = act(gate_n . a_t) *
