@@ -133,3 +133,20 @@ def test_rows_that_do_not_fill_a_warp(W, n, dtype):   # noqa: F811
         check(w.linear(x, residual=h), y + h.double(), "linear")
         check(w.glu(u, x, act="gelu_tanh"), R.glu("gelu_tanh", y, z), "glu")
     w.check()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("m", [1, 3, 8, 20, 130])
+def test_normed_tokens_of_far_sizes(W, m, dtype):   # noqa: F811
+    """From 2^-58 to 2^55, the sum of squares within fp32; with no eps the sizes go out again."""
+    n, k = 70, 2176
+    a, _, x = inputs(m, n, k, 64, torch.float32, 3)
+    size = torch.tensor([55.0, 0.0, -58.0], device="cuda")[torch.arange(m, device="cuda") % 3]
+    x = (x * torch.exp2(size)[:, None]).to(DT[dtype])
+    gain = (1.0 + 0.3 * normal(k, seed=9)).to(DT[dtype])
+    w = W(*a)
+    for eps in (0.0, 1e-5):
+        want = R.activation(x, gain, eps) @ R.values(*a).T
+        got = w.linear(x, norm=gain, eps=eps, dtype=torch.float32)
+        assert ((got.double() - want).norm(dim=1) <= KEPT * want.norm(dim=1)).all(), eps
+    w.check()
